@@ -268,6 +268,94 @@ int mesa_forward_chunked_noalloc(int B, int H, int T, int dk, int dv, int dtype,
                                  void *out, int32_t *iters_used, cudaStream_t stream);
 
 /*
+ * Gated delta rule: the first-order relative of the Mesa layer ("Declaracao do Problema" and "A
+ * Camada Mesa" contrast the layer with DeltaNet-style updates), with the same forget gates.  Per
+ * (batch, head) unit, with the state S [dv, dk] (zero, or S0, before token 0):
+ *     e_t = v_t - gamma_t S_{t-1} k_t,            u_t = beta_t e_t,
+ *     S_t = gamma_t S_{t-1} + u_t k_t^T,          o_t = scale S_t q_t,
+ * i.e. S_t = gamma_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T.  The caller normalises q
+ * and k (mesa_qk_preprocess); beta in [0, 2] with unit keys keeps the recurrence bounded.
+ *   q, k [B, Hk, T, dk] dtype; v, out [B, H, T, dv] dtype; gamma, beta [B, H, T] fp32.
+ *   Hk divides H: value head h reads query / key head h / (H / Hk).
+ *   S0, S_final: NULL or [B, H, dv, dk] fp32 (each may be given without the other).
+ *   gamma_t = 0 forgets everything before token t (a packed document's first token); beta_t = 0
+ *   leaves a token unwritten (padding).  gamma below e^-80 counts as 0 on the tensor-core path.
+ * dk, dv in {16, 32, 64, 128}, not necessarily equal; T >= 0; B * H <= 65535.  q, k, v, out, S0
+ * and S_final 16-byte aligned (MESA_ERR_INVALID_ARG otherwise).
+ * workspace: at least mesa_delta_workspace_size() bytes, 256-byte aligned; its first word is the
+ * status word read by mesa_forward_status.  Any chunk length gives the same result up to
+ * rounding; the library picks its own.
+ */
+size_t mesa_delta_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
+int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,
+                               const void *k, const void *v, const float *gamma, const float *beta,
+                               float scale, void *out, const float *S0, float *S_final,
+                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Gradients of mesa_delta_forward_chunked for dout = dL/dout and, optionally, dS_final =
+ * dL/dS_final.  With A_t the adjoint of S_t from the tokens after t and g_t = dout_t:
+ *     dS_t = A_t + scale g_t q_t^T,      du_t = dS_t k_t,       N_t = dS_t - beta_t du_t k_t^T,
+ *     A_{t-1} = gamma_t N_t,             dq_t = scale S_t^T g_t,
+ *     dk_t = dS_t^T u_t - beta_t gamma_t S_{t-1}^T du_t,        dv_t = beta_t du_t,
+ *     dbeta_t = du_t . e_t,              dgamma_t = <N_t, S_{t-1}>   (also where gamma_t = 0).
+ * dq, dk_out [B, Hk, T, dk] (summed over the value heads of a key head), dv_out [B, H, T, dv],
+ * dgamma, dbeta [B, H, T]: all of dtype -- the gates' gradients come from the same products as
+ * the others and carry no more digits.  dS0: NULL or [B, H, dv, dk] fp32, dL/dS0.  The states
+ * are recomputed; every sum has a fixed order.  S0 as given to the forward.
+ * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward.
+ */
+size_t mesa_delta_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
+int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,
+                                const void *k, const void *v, const float *gamma, const float *beta,
+                                float scale, const void *dout, const float *S0, const float *dS_final,
+                                void *dq, void *dk_out, void *dv_out, void *dgamma, void *dbeta,
+                                float *dS0, void *workspace, size_t workspace_bytes,
+                                cudaStream_t stream);
+
+/*
+ * One recurrent step of the gated delta rule for N sequences x H heads, in place on the caller's
+ * fp32 states S_state [N, H, dv, dk] (16-byte aligned).  q, k [N, Hk, dk], v, out [N, H, dv]
+ * dtype (q, k 16-byte aligned); gamma, beta [N, H] fp32.  Sizes and errors as the forward, with
+ * any N * H.
+ */
+int mesa_delta_step(int N, int H, int Hk, int dk, int dv, int dtype, float *S_state, const void *q,
+                    const void *k, const void *v, const float *gamma, const float *beta, float scale,
+                    void *out, cudaStream_t stream);
+
+/*
+ * The norms before and after a block, fused with its output gate and residual scale ("Arquitetura
+ * (MesaNet)": residual blocks of a Llama-like decoder).  Per row of D channels:
+ *     z = y rsqrt(mean(y^2) + eps) w_post,   x' = x + res_scale silu(gate) z,
+ *     h = x' rsqrt(mean(x'^2) + eps) w_pre.
+ * Each of x, gate, w_post, res_scale, w_pre may be NULL: x = 0, silu(gate) = 1, z = y (no norm),
+ * res_scale = 1, no h.  x = NULL with rows of one head's channels is the gated per-head norm of
+ * a layer's output.
+ *   x, y, gate, x_out, h_out [N, D] dtype; w_post, res_scale, w_pre [D] fp32.  1 <= D <= 8192.
+ *   x_out may be NULL when h is asked for; h_out is required with w_pre and ignored without.
+ *   x_out may be x or y, h_out may be y or gate (a row is read before it is written).
+ * Arithmetic is fp32; h is computed from x' before its rounding.  eps >= 0.
+ */
+int mesa_block_norm(int N, int D, int dtype, const void *x, const void *y, const void *gate,
+                    const float *w_post, const float *res_scale, const float *w_pre, float eps,
+                    void *x_out, void *h_out, cudaStream_t stream);
+
+/*
+ * Gradients of mesa_block_norm for dx_out = dL/dx' (NULL: zero) and dh = dL/dh (NULL: zero;
+ * ignored without w_pre).  x, y, gate and the weights as given to the forward (x may be NULL
+ * when it was).  dx, dgate NULL or [N, D] dtype; dy [N, D] dtype; dw_post, dres_scale, dw_pre
+ * NULL or [D] fp32, overwritten with the sums over the rows in a fixed order.
+ * workspace: at least mesa_block_norm_backward_workspace_size() bytes (256-byte aligned), for
+ * the column sums; may be NULL when no weight gradient is asked for.
+ */
+size_t mesa_block_norm_backward_workspace_size(int N, int D);
+int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void *y, const void *gate,
+                             const float *w_post, const float *res_scale, const float *w_pre,
+                             float eps, const void *dx_out, const void *dh, void *dx, void *dy,
+                             void *dgate, float *dw_post, float *dres_scale, float *dw_pre,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Device status word of the last mesa_forward_chunked (or _save, or mesa_backward_chunked)
  * call that used `workspace`: copies the word to *flags (host) on `stream` and synchronises
  * it.  Bits: 0 (1) a tensor-core kernel's bounded wait for its matrix multiplies gave up --

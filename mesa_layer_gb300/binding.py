@@ -15,6 +15,7 @@ import torch
 from . import build as _build
 
 MESA_F32, MESA_BF16 = 0, 1
+_DTYPE_CODES = {torch.float32: MESA_F32, torch.bfloat16: MESA_BF16}
 MESA_OK, MESA_ERR_TIMEOUT, MESA_ERR_NONFINITE = 0, 5, 6
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported size or option",
            3: "workspace missing or too small", 4: "CUDA launch failed",
@@ -82,6 +83,24 @@ def load(build_if_missing: bool = True):
         _fp, _fp, _ip, _ip, _vp, _sz, _vp]
     lib.mesa_forward_chunked_save.restype = _i
     lib.mesa_forward_chunked_save.argtypes = [_i] * 6 + [_vp] * 5 + [_i, _f, _i, _vp, _ip, _fp, _vp, _sz, _vp]
+    lib.mesa_delta_workspace_size.restype = _sz
+    lib.mesa_delta_workspace_size.argtypes = [_i] * 7
+    lib.mesa_delta_forward_chunked.restype = _i
+    lib.mesa_delta_forward_chunked.argtypes = [_i] * 7 + [_vp] * 3 + [_fp, _fp, _f, _vp, _fp, _fp, _vp, _sz, _vp]
+    lib.mesa_delta_backward_workspace_size.restype = _sz
+    lib.mesa_delta_backward_workspace_size.argtypes = [_i] * 7
+    lib.mesa_delta_backward_chunked.restype = _i
+    lib.mesa_delta_backward_chunked.argtypes = [_i] * 7 + [_vp] * 3 + [_fp, _fp, _f, _vp, _fp, _fp] + [_vp] * 5 + [
+        _fp, _vp, _sz, _vp]
+    lib.mesa_delta_step.restype = _i
+    lib.mesa_delta_step.argtypes = [_i] * 6 + [_fp, _vp, _vp, _vp, _fp, _fp, _f, _vp, _vp]
+    lib.mesa_block_norm.restype = _i
+    lib.mesa_block_norm.argtypes = [_i] * 3 + [_vp] * 3 + [_fp] * 3 + [_f, _vp, _vp, _vp]
+    lib.mesa_block_norm_backward_workspace_size.restype = _sz
+    lib.mesa_block_norm_backward_workspace_size.argtypes = [_i] * 2
+    lib.mesa_block_norm_backward.restype = _i
+    lib.mesa_block_norm_backward.argtypes = [_i] * 3 + [_vp] * 3 + [_fp] * 3 + [_f] + [_vp] * 5 + [_fp] * 3 + [
+        _vp, _sz, _vp]
     _lib = lib
     return lib
 
@@ -362,6 +381,185 @@ def mesa_decode_step_warm(H_state, G_state, X_state, q, k, v, gamma, lambda_diag
                                    _ptr(out), _ptr(iters_used), _stream(stream))
     _check(st, "mesa_decode_step_warm")
     return out, iters_used
+
+
+def _require_shape(t, name, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise MesaError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _require_all(device, *specs):
+    """Check (tensor or None, name, dtype, shape) on one device."""
+    for t, name, dtype, shape in specs:
+        if t is None:
+            continue
+        _require(t, name, dtype)
+        _require_shape(t, name, shape)
+        if t.device != device:
+            raise MesaError(f"{name} must be on {device}, got {t.device}")
+
+
+def _new(shape, dtype, device, stream):
+    """An output or scratch tensor for work on `stream`: when that is not the current stream, the
+    allocator is told, so that the memory is not handed out again before that work is done."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.numel():
+        t.record_stream(stream)
+    return t
+
+
+def _workspace(workspace, nbytes, device, stream):
+    if workspace is None:
+        return _new(max(nbytes, 256), torch.uint8, device, stream)
+    _require_all(device, (workspace, "workspace", torch.uint8, workspace.shape))
+    return workspace
+
+
+def _delta_dims(q, k, v, gamma, beta):
+    """(B, H, Hk, T, dk, dv) of the gated delta rule's sequence forms, every shape checked."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise MesaError("q, k must be [B, Hk, T, dk] and v [B, H, T, dv]")
+    B, Hk, T, dk = q.shape
+    H, dv = v.shape[1], v.shape[3]
+    _require_all(q.device, (q, "q", None, q.shape), (k, "k", q.dtype, q.shape), (v, "v", q.dtype, (B, H, T, dv)),
+                 (gamma, "gamma", torch.float32, (B, H, T)), (beta, "beta", torch.float32, (B, H, T)))
+    return B, H, Hk, T, dk, dv
+
+
+def mesa_delta_workspace_size(B, H, Hk, T, dk, dv, dtype) -> int:
+    """Bytes of workspace of mesa_delta_forward_chunked (dtype: torch.float32 or torch.bfloat16)."""
+    return int(load().mesa_delta_workspace_size(B, H, Hk, T, dk, dv, _DTYPE_CODES[dtype]))
+
+
+def mesa_delta_forward_chunked(q, k, v, gamma, beta, scale=1.0, out=None, S0=None, S_final=None, workspace=None,
+                               stream=None):
+    """Gated delta rule over whole sequences.  q, k [B, Hk, T, dk], v [B, H, T, dv] (fp32 or
+    bf16; Hk divides H), gamma, beta [B, H, T] fp32; S0 [B, H, dv, dk] fp32 or None (zero);
+    S_final [B, H, dv, dk] fp32 or None, written.  Returns out [B, H, T, dv]."""
+    lib = load()
+    code = _dtype_code(q)
+    B, H, Hk, T, dk, dv = _delta_dims(q, k, v, gamma, beta)
+    out = _new((B, H, T, dv), q.dtype, q.device, stream) if out is None else out
+    _require_all(q.device, (out, "out", q.dtype, (B, H, T, dv)), (S0, "S0", torch.float32, (B, H, dv, dk)),
+                 (S_final, "S_final", torch.float32, (B, H, dv, dk)))
+    workspace = _workspace(workspace, int(lib.mesa_delta_workspace_size(B, H, Hk, T, dk, dv, code)), q.device, stream)
+    _check(lib.mesa_delta_forward_chunked(B, H, Hk, T, dk, dv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
+                                          _ptr(beta), float(scale), _ptr(out), _ptr(S0), _ptr(S_final),
+                                          _ptr(workspace), workspace.numel(), _stream(stream)),
+           "mesa_delta_forward_chunked")
+    return out
+
+
+def mesa_delta_backward_workspace_size(B, H, Hk, T, dk, dv, dtype) -> int:
+    """Bytes of workspace of mesa_delta_backward_chunked."""
+    return int(load().mesa_delta_backward_workspace_size(B, H, Hk, T, dk, dv, _DTYPE_CODES[dtype]))
+
+
+def mesa_delta_backward_chunked(q, k, v, gamma, beta, dout, scale=1.0, S0=None, dS_final=None, dq=None, dk=None,
+                                dv=None, dgamma=None, dbeta=None, dS0=None, workspace=None, stream=None):
+    """Gradients of mesa_delta_forward_chunked given dout = dL/dout (and dS_final = dL/dS_final):
+    returns (dq, dk, dv, dgamma, dbeta), all of q's dtype; dS0 [B, H, dv, dk] fp32, when given,
+    receives dL/dS0."""
+    lib = load()
+    code = _dtype_code(q)
+    B, H, Hk, T, dkk, dvv = _delta_dims(q, k, v, gamma, beta)
+    dev = q.device
+    dq = _new(q.shape, q.dtype, dev, stream) if dq is None else dq
+    dk = _new(q.shape, q.dtype, dev, stream) if dk is None else dk
+    dv = _new(v.shape, q.dtype, dev, stream) if dv is None else dv
+    dgamma = _new((B, H, T), q.dtype, dev, stream) if dgamma is None else dgamma
+    dbeta = _new((B, H, T), q.dtype, dev, stream) if dbeta is None else dbeta
+    state = (B, H, dvv, dkk)
+    _require_all(dev, (dout, "dout", q.dtype, v.shape), (dq, "dq", q.dtype, q.shape), (dk, "dk", q.dtype, q.shape),
+                 (dv, "dv", q.dtype, v.shape), (dgamma, "dgamma", q.dtype, (B, H, T)),
+                 (dbeta, "dbeta", q.dtype, (B, H, T)), (S0, "S0", torch.float32, state),
+                 (dS_final, "dS_final", torch.float32, state), (dS0, "dS0", torch.float32, state))
+    workspace = _workspace(workspace, int(lib.mesa_delta_backward_workspace_size(B, H, Hk, T, dkk, dvv, code)), dev,
+                           stream)
+    _check(lib.mesa_delta_backward_chunked(B, H, Hk, T, dkk, dvv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
+                                           _ptr(beta), float(scale), _ptr(dout), _ptr(S0), _ptr(dS_final), _ptr(dq),
+                                           _ptr(dk), _ptr(dv), _ptr(dgamma), _ptr(dbeta), _ptr(dS0),
+                                           _ptr(workspace), workspace.numel(), _stream(stream)),
+           "mesa_delta_backward_chunked")
+    return dq, dk, dv, dgamma, dbeta
+
+
+def mesa_delta_step(S_state, q, k, v, gamma, beta, scale=1.0, out=None, stream=None):
+    """One step of the gated delta rule in place on S_state [N, H, dv, dk] (fp32).  q, k
+    [N, Hk, dk], v [N, H, dv] (fp32 or bf16), gamma, beta [N, H] fp32.  Returns out [N, H, dv]."""
+    lib = load()
+    code = _dtype_code(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise MesaError("q, k must be [N, Hk, dk] and v [N, H, dv]")
+    N, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    out = _new((N, H, dv), q.dtype, q.device, stream) if out is None else out
+    _require_all(q.device, (q, "q", None, q.shape), (k, "k", q.dtype, q.shape), (v, "v", q.dtype, (N, H, dv)),
+                 (gamma, "gamma", torch.float32, (N, H)), (beta, "beta", torch.float32, (N, H)),
+                 (S_state, "S_state", torch.float32, (N, H, dv, dk)), (out, "out", q.dtype, (N, H, dv)))
+    _check(lib.mesa_delta_step(N, H, Hk, dk, dv, code, _ptr(S_state), _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
+                               _ptr(beta), float(scale), _ptr(out), _stream(stream)), "mesa_delta_step")
+    return out
+
+
+def _norm_check(x, y, gate, w_post, res_scale, w_pre):
+    if y.dim() < 1 or y.shape[-1] < 1:
+        raise MesaError("y must be [..., D] with D >= 1")
+    D = y.shape[-1]
+    _require_all(y.device, (y, "y", None, y.shape), (x, "x", y.dtype, y.shape), (gate, "gate", y.dtype, y.shape),
+                 (w_post, "w_post", torch.float32, (D,)), (res_scale, "res_scale", torch.float32, (D,)),
+                 (w_pre, "w_pre", torch.float32, (D,)))
+    return y.numel() // D, D
+
+
+def mesa_block_norm(x, y, gate=None, w_post=None, res_scale=None, w_pre=None, eps=1e-6, x_out=None, h_out=None,
+                    stream=None):
+    """The norms around a block: x_out = x + res_scale * silu(gate) * rmsnorm(y) * w_post and
+    h_out = rmsnorm(x_out) * w_pre over the last axis.  x, y, gate [..., D] (fp32 or bf16; x and
+    gate may be None), w_post, res_scale, w_pre [D] fp32 or None.  Returns (x_out, h_out), h_out
+    None without w_pre."""
+    lib = load()
+    code = _dtype_code(y)
+    N, D = _norm_check(x, y, gate, w_post, res_scale, w_pre)
+    x_out = _new(y.shape, y.dtype, y.device, stream) if x_out is None else x_out
+    if w_pre is not None and h_out is None:
+        h_out = _new(y.shape, y.dtype, y.device, stream)
+    _require_all(y.device, (x_out, "x_out", y.dtype, y.shape), (h_out, "h_out", y.dtype, y.shape))
+    _check(lib.mesa_block_norm(N, D, code, _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(res_scale), _ptr(w_pre),
+                               float(eps), _ptr(x_out), _ptr(h_out), _stream(stream)), "mesa_block_norm")
+    return x_out, (h_out if w_pre is not None else None)
+
+
+def mesa_block_norm_backward_workspace_size(N, D) -> int:
+    return int(load().mesa_block_norm_backward_workspace_size(N, D))
+
+
+def mesa_block_norm_backward(x, y, dx_out, dh=None, gate=None, w_post=None, res_scale=None, w_pre=None, eps=1e-6,
+                             dx=None, dy=None, dgate=None, dw_post=None, dres_scale=None, dw_pre=None, workspace=None,
+                             stream=None):
+    """Gradients of mesa_block_norm given dx_out = dL/dx_out and dh = dL/dh_out (each may be
+    None: zero).  Returns (dx, dy, dgate, dw_post, dres_scale, dw_pre), None for what the forward
+    did not have; the weights' gradients are fp32 sums over the rows."""
+    lib = load()
+    code = _dtype_code(y)
+    N, D = _norm_check(x, y, gate, w_post, res_scale, w_pre)
+    dev = y.device
+
+    def out(t, like, dtype):
+        return _new(like.shape, dtype, dev, stream) if t is None and like is not None else t
+
+    dx, dy, dgate = out(dx, x, y.dtype), out(dy, y, y.dtype), out(dgate, gate, y.dtype)
+    dw_post, dres_scale, dw_pre = (out(t, w, torch.float32) for t, w in (
+        (dw_post, w_post), (dres_scale, res_scale), (dw_pre, w_pre)))
+    _require_all(dev, *[(t, n, y.dtype, y.shape) for t, n in (
+        (dx_out, "dx_out"), (dh, "dh"), (dx, "dx"), (dy, "dy"), (dgate, "dgate"))],
+        *[(t, n, torch.float32, (D,)) for t, n in ((dw_post, "dw_post"), (dres_scale, "dres_scale"), (dw_pre, "dw_pre"))])
+    workspace = _workspace(workspace, int(lib.mesa_block_norm_backward_workspace_size(N, D)), dev, stream)
+    _check(lib.mesa_block_norm_backward(N, D, code, _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(res_scale),
+                                        _ptr(w_pre), float(eps), _ptr(dx_out), _ptr(dh), _ptr(dx), _ptr(dy),
+                                        _ptr(dgate), _ptr(dw_post), _ptr(dres_scale), _ptr(dw_pre), _ptr(workspace),
+                                        workspace.numel(), _stream(stream)), "mesa_block_norm_backward")
+    return dx, dy, dgate, dw_post, dres_scale, dw_pre
 
 
 def mesa_forward_status(workspace, stream=None) -> int:

@@ -1,0 +1,568 @@
+// gated_delta.cu -- the gated delta rule on the CUDA cores: token recurrence for whole
+// sequences (forward, and the two sweeps of the backward pass), the backward's per-chunk
+// gradients, and the decode step.
+//
+// Per (batch, head) unit, with the state S [dv, dk]:
+//     e_t = v_t - gamma_t S_{t-1} k_t,  u_t = beta_t e_t,  S_t = gamma_t S_{t-1} + u_t k_t^T,
+//     o_t = scale S_t q_t.
+// Every row of S evolves on its own given k, q and the gates, so rows are split over lanes,
+// warps and CTAs without any exchange but the sum over dk.  The adjoint A_t of S_t (from the
+// tokens after t) runs the same way in reverse: with g_t = dL/do_t
+//     A <- A + scale g_t q_t^T,  du_t = A k_t,  N_t = A - beta_t du_t k_t^T,  A_{t-1} = gamma_t N_t,
+// and the gradients are dv_t = beta_t du_t, dbeta_t = du_t . e_t, dgamma_t = <N_t, S_{t-1}>,
+// dq_t = scale S_t^T g_t, dk_t = (A + scale g q^T)^T u_t - beta_t gamma_t S_{t-1}^T du_t.
+#include "common.cuh"
+#include "gated_delta.h"
+#include "launch.h"
+
+namespace mesa {
+
+namespace {
+
+using u64 = unsigned long long;
+// Two fp32 lanes in one 64-bit register (each lane rounds like the scalar instruction).
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 pack2(float x, float y) {
+  u64 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ float sum2(u64 a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+__device__ __forceinline__ void cp16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+enum ScanMode { kForward = 0, kStates = 1, kAdjoint = 2 };
+constexpr int TB = 16;    // tokens staged at a time
+constexpr int ROWS = 32;  // state rows per CTA, four lanes each
+
+// One CTA: 32 rows of one unit's state through all tokens.  The recurrence is a dependent
+// chain per token (sum over dk, two shuffles, rank-one update); four lanes a row keep the
+// in-lane sums short and leave enough CTAs for small batches.  k, q and v (or dout) of the
+// next 16 tokens arrive by cp.async while a block of 16 is worked on; bf16 is widened once per
+// block.  Bound by the chain's latency when units are few, by FMA issue when they are many
+// (packed fp32 pairs halve the issue slots).
+//   kForward: out, S_final.  kStates: e and the state before each 32-token chunk.
+//   kAdjoint: tokens descending; du and the adjoint after each chunk, dS0.
+template <int DK, typename TIO, int MODE>
+__global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwdWorkspace ws) {
+  constexpr int VPL = DK / 4, NG = VPL / 4;  // values and 16-byte groups per lane
+  constexpr bool WIDE = sizeof(TIO) == 4;
+  constexpr bool USEQ = MODE != kStates;
+  __shared__ __align__(16) TIO kraw[2][TB * DK], qraw[2][USEQ ? TB * DK : 8], xraw[2][TB * ROWS];
+  __shared__ __align__(16) float kwide[WIDE ? 4 : TB * DK], qwide[WIDE || !USEQ ? 4 : TB * DK];
+  __shared__ float os[TB * ROWS], gs[2][TB], bs[2][TB];
+  const int u = blockIdx.y, r0 = blockIdx.x * ROWS, tid = threadIdx.x;
+  const int r = tid >> 2, j = tid & 3, nr = min(ROWS, a.dv - r0);
+  const int T = a.T, nblk = (T + TB - 1) / TB;
+  const size_t qk0 = (size_t)a.qk_unit(u) * T, tu = (size_t)u * T;
+  const TIO *kp = (const TIO *)a.k + qk0 * DK, *qp = (const TIO *)a.q + qk0 * DK;
+  const TIO *xp = (const TIO *)(MODE == kAdjoint ? a.dout : a.v) + tu * a.dv + r0;
+  const bool rin = r < nr;
+
+  auto fetch = [&](int blk, int buf) {
+    const int t0 = blk * TB, n = min(TB, T - t0);
+    constexpr int E = 16 / sizeof(TIO);
+    for (int i = tid; i < n * DK / E; i += 128) {
+      cp16(&kraw[buf][i * E], kp + (size_t)t0 * DK + i * E);
+      if (USEQ) cp16(&qraw[buf][i * E], qp + (size_t)t0 * DK + i * E);
+    }
+    const int per = nr / E;
+    for (int i = tid; i < n * per; i += 128) {
+      const int t = i / per, c = i % per;
+      cp16(&xraw[buf][t * ROWS + c * E], xp + (size_t)(t0 + t) * a.dv + c * E);
+    }
+    if (tid < n) {
+      gs[buf][tid] = a.gamma[tu + t0 + tid];
+      bs[buf][tid] = a.beta[tu + t0 + tid];
+    }
+    cp_commit();
+  };
+
+  u64 s[2 * NG];
+  {
+    const float *init = MODE == kAdjoint ? a.dS_final : a.S0;
+    const float *src = init ? init + ((size_t)u * a.dv + r0 + r) * DK : nullptr;
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      const float4 x = (src && rin) ? *reinterpret_cast<const float4 *>(src + 4 * (j + 4 * g)) : make_float4(0, 0, 0, 0);
+      s[2 * g] = pack2(x.x, x.y);
+      s[2 * g + 1] = pack2(x.z, x.w);
+    }
+  }
+  auto store_state = [&](float *dst) {  // this lane's part of row r (dst: the unit's matrix)
+    if (!rin) return;
+#pragma unroll
+    for (int g = 0; g < NG; g++)
+      *reinterpret_cast<ulonglong2 *>(dst + (size_t)(r0 + r) * DK + 4 * (j + 4 * g)) =
+          make_ulonglong2(s[2 * g], s[2 * g + 1]);
+  };
+
+  const int NC = (T + kRuleChunk - 1) / kRuleChunk;
+  constexpr int BPC = kRuleChunk / TB;  // blocks per chunk
+  fetch(MODE == kAdjoint ? nblk - 1 : 0, 0);
+  for (int it = 0; it < nblk; it++) {
+    const int blk = MODE == kAdjoint ? nblk - 1 - it : it, buf = it & 1;
+    const int t0 = blk * TB, n = min(TB, T - t0);
+    if (it + 1 < nblk) {
+      fetch(MODE == kAdjoint ? blk - 1 : blk + 1, buf ^ 1);
+      cp_wait<1>();
+    } else {
+      cp_wait<0>();
+    }
+    __syncthreads();
+    const float *kf, *qf;
+    if constexpr (WIDE) {
+      kf = kraw[buf];
+      qf = qraw[buf];
+    } else {
+      for (int i = tid; i < TB * DK / 4; i += 128) {
+        *reinterpret_cast<float4 *>(&kwide[4 * i]) = load4(kraw[buf], 4 * i);
+        if (USEQ) *reinterpret_cast<float4 *>(&qwide[4 * i]) = load4(qraw[buf], 4 * i);
+      }
+      kf = kwide;
+      qf = qwide;
+      __syncthreads();
+    }
+    if (MODE == kStates && blk % BPC == 0) store_state(ws.S + ((size_t)u * NC + blk / BPC) * a.dv * DK);
+    if (MODE == kAdjoint && (blk % BPC == BPC - 1 || blk == nblk - 1))
+      store_state(ws.dS + ((size_t)u * NC + blk / BPC) * a.dv * DK);
+    for (int tt = 0; tt < n; tt++) {
+      const int t = MODE == kAdjoint ? n - 1 - tt : tt;
+      const float g = gs[buf][t], b = bs[buf][t];
+      const float x = ld(xraw[buf], t * ROWS + r);
+      const ulonglong2 *kv = reinterpret_cast<const ulonglong2 *>(kf + t * DK);
+      const ulonglong2 *qv = reinterpret_cast<const ulonglong2 *>(qf + t * DK);
+      if constexpr (MODE == kAdjoint) {
+        const u64 gx = pack2(a.scale * x, a.scale * x);
+        u64 d0 = 0, d1 = 0;
+        ulonglong2 kk[NG];
+#pragma unroll
+        for (int i = 0; i < NG; i++) {
+          const ulonglong2 qq = qv[j + 4 * i];
+          kk[i] = kv[j + 4 * i];
+          s[2 * i] = fma2(gx, qq.x, s[2 * i]);
+          s[2 * i + 1] = fma2(gx, qq.y, s[2 * i + 1]);
+          d0 = fma2(s[2 * i], kk[i].x, d0);
+          d1 = fma2(s[2 * i + 1], kk[i].y, d1);
+        }
+        float du = sum2(d0) + sum2(d1);
+        du += __shfl_xor_sync(0xffffffffu, du, 1);
+        du += __shfl_xor_sync(0xffffffffu, du, 2);
+        const u64 w = pack2(-b * du, -b * du), g2 = pack2(g, g);
+#pragma unroll
+        for (int i = 0; i < NG; i++) {
+          s[2 * i] = mul2(g2, fma2(w, kk[i].x, s[2 * i]));
+          s[2 * i + 1] = mul2(g2, fma2(w, kk[i].y, s[2 * i + 1]));
+        }
+        if (j == 0) os[t * ROWS + r] = du;
+      } else {
+        u64 d0 = 0, d1 = 0;
+        ulonglong2 kk[NG];
+#pragma unroll
+        for (int i = 0; i < NG; i++) {
+          kk[i] = kv[j + 4 * i];
+          d0 = fma2(s[2 * i], kk[i].x, d0);
+          d1 = fma2(s[2 * i + 1], kk[i].y, d1);
+        }
+        float d = sum2(d0) + sum2(d1);
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        d += __shfl_xor_sync(0xffffffffu, d, 2);
+        const float e = fmaf(-g, d, x), uu = b * e;
+        const u64 u2 = pack2(uu, uu), g2 = pack2(g, g);
+        u64 o0 = 0, o1 = 0;
+#pragma unroll
+        for (int i = 0; i < NG; i++) {
+          s[2 * i] = fma2(u2, kk[i].x, mul2(g2, s[2 * i]));
+          s[2 * i + 1] = fma2(u2, kk[i].y, mul2(g2, s[2 * i + 1]));
+          if constexpr (MODE == kForward) {
+            const ulonglong2 qq = qv[j + 4 * i];
+            o0 = fma2(s[2 * i], qq.x, o0);
+            o1 = fma2(s[2 * i + 1], qq.y, o1);
+          }
+        }
+        if constexpr (MODE == kForward) {
+          float o = sum2(o0) + sum2(o1);
+          o += __shfl_xor_sync(0xffffffffu, o, 1);
+          o += __shfl_xor_sync(0xffffffffu, o, 2);
+          if (j == 0) os[t * ROWS + r] = a.scale * o;
+        } else {
+          if (j == 0) os[t * ROWS + r] = e;
+        }
+      }
+    }
+    __syncthreads();
+    bool bad = false;
+    for (int i = tid; i < n * ROWS; i += 128) {
+      const int t = i / ROWS, rr = i % ROWS;
+      if (rr >= nr) continue;
+      const size_t at = (tu + t0 + t) * a.dv + r0 + rr;
+      const float y = os[i];
+      if (MODE == kForward) {
+        st((TIO *)a.out, at, y);
+        bad |= !isfinite(y);
+      } else {
+        (MODE == kStates ? ws.e : ws.du)[at] = y;
+      }
+    }
+    if (MODE == kForward && bad) atomicOr(a.status, tc_err_nonfinite());
+  }
+  if (MODE == kForward && a.S_final) store_state(a.S_final + (size_t)u * a.dv * DK);
+  if (MODE == kAdjoint && a.dS0) store_state(a.dS0 + (size_t)u * a.dv * DK);
+}
+
+// The gradients of one 32-token chunk of one unit, from the state before it, the adjoint after
+// it, e and du.  With the decay D_ij from token j to token i (a product of gates: exact for
+// closed ones), w = scale (g u^T) o D and x = (db u^T) o D (strictly lower), db = beta du:
+//     dq = scale D_i0 (g S0) + w K,
+//     dk = w^T Q + D_Cj (u dS) - D_i0 (db S0) - (x + x^T) K,
+//     dgamma_t = sum over every pair (i >= t > j) that the gate separates, i the state's reader
+//                (or dS), j its writer (or S0), each with its decay without gamma_t.
+// 256 threads: column groups of four over dk, token groups of four.
+template <int DK, typename TIO>
+__global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBwdWorkspace ws) {
+  constexpr int C = kRuleChunk, CG = DK / 4, P = C + 1;
+  extern __shared__ __align__(16) float sm[];
+  const int dv = a.dv, vp = dv + 4, kp = DK + 4;
+  float *K = sm, *Q = K + C * kp, *G = Q + C * kp, *Uu = G + C * vp, *Db = Uu + C * vp;
+  float *W = Db + C * vp, *V = W + C * P, *X = V + C * P, *D = X + C * P;  // [C][P]
+  float *gam = D + C * P, *bet = gam + C, *from0 = bet + C, *xin = from0 + C, *xout = xin + C, *red = xout + C;
+  const int u = blockIdx.y, c = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.T, t0 = c * C, n = min(C, T - t0), NC = gridDim.x;
+  const size_t qk0 = ((size_t)a.qk_unit(u) * T + t0) * DK, v0 = ((size_t)u * T + t0) * dv, tu = (size_t)u * T + t0;
+  if (tid < C) {
+    gam[tid] = tid < n ? a.gamma[tu + tid] : 1.0f;
+    bet[tid] = tid < n ? a.beta[tu + tid] : 0.0f;
+    xin[tid] = 0.0f;
+    xout[tid] = 0.0f;
+  }
+  __syncthreads();
+  for (int i = 4 * tid; i < C * DK; i += 1024) {
+    const int t = i / DK, d = i % DK;
+    const bool in = t < n;
+    *reinterpret_cast<float4 *>(K + t * kp + d) = in ? load4((const TIO *)a.k, qk0 + i) : make_float4(0, 0, 0, 0);
+    *reinterpret_cast<float4 *>(Q + t * kp + d) = in ? load4((const TIO *)a.q, qk0 + i) : make_float4(0, 0, 0, 0);
+  }
+  // tokens' rows; dv and dbeta on the way (a warp per token)
+  for (int t = warp; t < C; t += 8) {
+    float db_sum = 0.0f;
+    for (int d = lane; d < dv; d += 32) {
+      float g = 0, e = 0, du = 0;
+      if (t < n) {
+        const size_t at = v0 + (size_t)t * dv + d;
+        g = ld((const TIO *)a.dout, at);
+        e = ws.e[at];
+        du = ws.du[at];
+        st((TIO *)a.dv_out, at, bet[t] * du);
+      }
+      db_sum = fmaf(du, e, db_sum);
+      G[t * vp + d] = a.scale * g;
+      Uu[t * vp + d] = bet[t] * e;
+      Db[t * vp + d] = bet[t] * du;
+    }
+    db_sum = warp_sum(db_sum);
+    if (lane == 0 && t < n) st((TIO *)a.dbeta, tu + t, db_sum);
+  }
+  // decays: D[i][j] = gamma_{j+1} .. gamma_i (j <= i), from0[i] = gamma_0 .. gamma_i
+  if (warp == 0) {
+    float p = 1.0f, f = 1.0f;
+    for (int i = 0; i < C; i++) {
+      if (i > lane) p *= gam[i];
+      D[i * P + lane] = i >= lane ? p : 0.0f;
+      f *= gam[i];
+      if (lane == 0) from0[i] = f;
+    }
+  }
+  __syncthreads();
+  // token x token products
+  {
+    const int i0 = tid >> 4, j0 = tid & 15;  // rows i0, i0 + 16; columns j0, j0 + 16
+    float gu[2][2] = {}, bu[2][2] = {}, kk[2][2] = {}, qk[2][2] = {};
+    for (int d = 0; d < dv; d++) {
+      const float ua = Uu[j0 * vp + d], ub = Uu[(j0 + 16) * vp + d];
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        const float g = G[(i0 + 16 * x) * vp + d], b = Db[(i0 + 16 * x) * vp + d];
+        gu[x][0] = fmaf(g, ua, gu[x][0]);
+        gu[x][1] = fmaf(g, ub, gu[x][1]);
+        bu[x][0] = fmaf(b, ua, bu[x][0]);
+        bu[x][1] = fmaf(b, ub, bu[x][1]);
+      }
+    }
+    for (int d = 0; d < DK; d++) {
+      const float ka = K[j0 * kp + d], kb = K[(j0 + 16) * kp + d];
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        const float k = K[(i0 + 16 * x) * kp + d], q = Q[(i0 + 16 * x) * kp + d];
+        kk[x][0] = fmaf(k, ka, kk[x][0]);
+        kk[x][1] = fmaf(k, kb, kk[x][1]);
+        qk[x][0] = fmaf(q, ka, qk[x][0]);
+        qk[x][1] = fmaf(q, kb, qk[x][1]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; x++)
+#pragma unroll
+      for (int y = 0; y < 2; y++) {
+        const int i = i0 + 16 * x, j = j0 + 16 * y;
+        const float dec = D[i * P + j];
+        W[i * P + j] = j <= i ? gu[x][y] * dec : 0.0f;
+        V[i * P + j] = j < i ? bu[x][y] * dec : 0.0f;
+        X[i * P + j] = gu[x][y] * qk[x][y] - bu[x][y] * kk[x][y];
+      }
+  }
+  __syncthreads();
+  // token x state products, then dq and dk: tokens 4 tg .. 4 tg + 3, columns 4 cg .. 4 cg + 3
+  const float *S0 = ws.S + ((size_t)u * NC + c) * dv * DK, *dS = ws.dS + ((size_t)u * NC + c) * dv * DK;
+  const int cg = tid % CG, tg = tid / CG;
+  float cross = 0.0f;  // <dS, S0>
+  if (tg < C / 4) {  // (whole warps: 8 CG threads)
+    float4 gS[4] = {}, bS[4] = {}, uS[4] = {};
+    auto axpy = [](float f, const float4 &x, float4 &y) {
+      y.x = fmaf(f, x.x, y.x);
+      y.y = fmaf(f, x.y, y.y);
+      y.z = fmaf(f, x.z, y.z);
+      y.w = fmaf(f, x.w, y.w);
+    };
+    for (int v = 0; v < dv; v++) {
+      const float4 s0 = *reinterpret_cast<const float4 *>(S0 + (size_t)v * DK + 4 * cg);
+      const float4 ds = *reinterpret_cast<const float4 *>(dS + (size_t)v * DK + 4 * cg);
+      if (tg == 0) cross = fmaf(s0.x, ds.x, fmaf(s0.y, ds.y, fmaf(s0.z, ds.z, fmaf(s0.w, ds.w, cross))));
+#pragma unroll
+      for (int m = 0; m < 4; m++) {
+        axpy(G[(4 * tg + m) * vp + v], s0, gS[m]);
+        axpy(Db[(4 * tg + m) * vp + v], s0, bS[m]);
+        axpy(Uu[(4 * tg + m) * vp + v], ds, uS[m]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+      const int t = 4 * tg + m;
+      const float f0 = from0[t], fC = D[(C - 1) * P + t];
+      const float4 q = *reinterpret_cast<const float4 *>(Q + t * kp + 4 * cg);
+      const float4 k = *reinterpret_cast<const float4 *>(K + t * kp + 4 * cg);
+      float xi = gS[m].x * q.x + gS[m].y * q.y + gS[m].z * q.z + gS[m].w * q.w -
+                 (bS[m].x * k.x + bS[m].y * k.y + bS[m].z * k.z + bS[m].w * k.w);
+      float xo = uS[m].x * k.x + uS[m].y * k.y + uS[m].z * k.z + uS[m].w * k.w;
+#pragma unroll
+      for (int o = (CG < 32 ? CG : 32) / 2; o > 0; o >>= 1) {
+        xi += __shfl_xor_sync(0xffffffffu, xi, o);
+        xo += __shfl_xor_sync(0xffffffffu, xo, o);
+      }
+      if (cg == 0) {
+        xin[t] = xi;
+        xout[t] = xo;
+      }
+      float4 dq = make_float4(f0 * gS[m].x, f0 * gS[m].y, f0 * gS[m].z, f0 * gS[m].w);
+      float4 dk = make_float4(fC * uS[m].x - f0 * bS[m].x, fC * uS[m].y - f0 * bS[m].y, fC * uS[m].z - f0 * bS[m].z,
+                              fC * uS[m].w - f0 * bS[m].w);
+      for (int s = 0; s < C; s++) {
+        const float4 ks = *reinterpret_cast<const float4 *>(K + s * kp + 4 * cg);
+        const float4 qs = *reinterpret_cast<const float4 *>(Q + s * kp + 4 * cg);
+        axpy(W[t * P + s], ks, dq);
+        axpy(W[s * P + t], qs, dk);
+        axpy(-(V[t * P + s] + V[s * P + t]), ks, dk);
+      }
+      if (t < n) {
+        if (ws.dqp) {
+          const size_t at = (tu + t) * DK + 4 * cg;
+          *reinterpret_cast<float4 *>(ws.dqp + at) = dq;
+          *reinterpret_cast<float4 *>(ws.dkp + at) = dk;
+        } else {
+          const size_t at = qk0 + (size_t)t * DK + 4 * cg;
+          TIO *dqo = (TIO *)a.dq, *dko = (TIO *)a.dk_out;
+          st(dqo, at, dq.x);
+          st(dqo, at + 1, dq.y);
+          st(dqo, at + 2, dq.z);
+          st(dqo, at + 3, dq.w);
+          st(dko, at, dk.x);
+          st(dko, at + 1, dk.y);
+          st(dko, at + 2, dk.z);
+          st(dko, at + 3, dk.w);
+        }
+      }
+    }
+  }
+  cross = warp_sum(cross);
+  if (lane == 0) red[warp] = cross;
+  __syncthreads();
+  cross = 0.0f;
+  for (int w = 0; w < 8; w++) cross += red[w];
+  // dgamma: a warp per token, lanes over i (readers) or j (writers)
+  for (int t = warp; t < n; t += 8) {
+    const float prev0 = t > 0 ? from0[t - 1] : 1.0f, toC = D[(C - 1) * P + t];
+    const float dprev = lane < t ? D[(t - 1) * P + lane] : 0.0f;
+    float col = 0.0f;  // sum over i >= t of D[i][t] X[i][lane]
+    for (int i = t; i < C; i++) col = fmaf(D[i * P + t], X[i * P + lane], col);
+    float s = (lane < t ? dprev * (col + toC * xout[lane]) : 0.0f) + prev0 * (D[lane * P + t] * xin[lane]);
+    s = warp_sum(s);
+    if (lane == 0) st((TIO *)a.dgamma, tu + t, fmaf(toC * prev0, cross, s));
+  }
+}
+
+template <typename TIO>
+__global__ void __launch_bounds__(256) mesa_rule_group_sum_kernel(RuleArgs a, const float *dqp, const float *dkp) {
+  const size_t per = (size_t)a.T * a.dk, total = (size_t)a.B * a.Hk * per;
+  const int group = a.H / a.Hk;
+  for (size_t i = 4 * ((size_t)blockIdx.x * 256 + threadIdx.x); i < total; i += (size_t)gridDim.x * 1024) {
+    const size_t uk = i / per, at = i % per, b = uk / a.Hk, hk = uk % a.Hk;
+    float4 q = make_float4(0, 0, 0, 0), k = q;
+    for (int g = 0; g < group; g++) {
+      const size_t src = (b * a.H + hk * group + g) * per + at;
+      const float4 x = *reinterpret_cast<const float4 *>(dqp + src), y = *reinterpret_cast<const float4 *>(dkp + src);
+      q = make_float4(q.x + x.x, q.y + x.y, q.z + x.z, q.w + x.w);
+      k = make_float4(k.x + y.x, k.y + y.y, k.z + y.z, k.w + y.w);
+    }
+    TIO *dq = (TIO *)a.dq + i, *dk = (TIO *)a.dk_out + i;
+    st(dq, 0, q.x);
+    st(dq, 1, q.y);
+    st(dq, 2, q.z);
+    st(dq, 3, q.w);
+    st(dk, 0, k.x);
+    st(dk, 1, k.y);
+    st(dk, 2, k.z);
+    st(dk, 3, k.w);
+  }
+}
+
+// One decode step.  A lane holds 16 values of a row (float4 groups DK/16 lanes apart, so that
+// a group of lanes reads whole 128-byte lines for dk = 128), a warp four rows at a time for
+// dk = 128; the state is read and written once and its traffic is the bound.  A CTA takes 32
+// rows and more of one unit: small batches spread over many SMs.
+template <int DK, typename TIO>
+__global__ void __launch_bounds__(128) mesa_rule_step_kernel(RuleStepArgs a) {
+  constexpr int LPR = DK / 16, RPW = 32 / LPR, PASS = DK == 128 ? 2 : 1;
+  const int u = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = lane % LPR, rs = lane / LPR;
+  const int row0 = (blockIdx.y * 4 + warp) * RPW * PASS;
+  const int uk = (u / a.H) * a.Hk + (u % a.H) / (a.H / a.Hk);
+  float4 s[PASS][4];
+#pragma unroll
+  for (int p = 0; p < PASS; p++) {
+    const int row = row0 + p * RPW + rs;
+    const float4 *src = reinterpret_cast<const float4 *>(a.S + ((size_t)u * a.dv + row) * DK);
+#pragma unroll
+    for (int i = 0; i < 4; i++) s[p][i] = row < a.dv ? src[j + LPR * i] : make_float4(0, 0, 0, 0);
+  }
+  float4 k[4], q[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    k[i] = load4((const TIO *)a.k, (size_t)uk * DK + 4 * (j + LPR * i));
+    q[i] = load4((const TIO *)a.q, (size_t)uk * DK + 4 * (j + LPR * i));
+  }
+  const float g = a.gamma[u], b = a.beta[u];
+  auto dot = [&](const float4 (&x)[4], const float4 (&y)[4]) {
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) t[i] = fmaf(x[i].x, y[i].x, fmaf(x[i].y, y[i].y, fmaf(x[i].z, y[i].z, x[i].w * y[i].w)));
+    float d = (t[0] + t[1]) + (t[2] + t[3]);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    return d;
+  };
+#pragma unroll
+  for (int p = 0; p < PASS; p++) {
+    const int row = row0 + p * RPW + rs;
+    const float v = row < a.dv ? ld((const TIO *)a.v, (size_t)u * a.dv + row) : 0.0f;
+    const float uu = b * fmaf(-g, dot(s[p], k), v);
+    float4 *dst = reinterpret_cast<float4 *>(a.S + ((size_t)u * a.dv + row) * DK);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      s[p][i].x = fmaf(g, s[p][i].x, uu * k[i].x);
+      s[p][i].y = fmaf(g, s[p][i].y, uu * k[i].y);
+      s[p][i].z = fmaf(g, s[p][i].z, uu * k[i].z);
+      s[p][i].w = fmaf(g, s[p][i].w, uu * k[i].w);
+      if (row < a.dv) dst[j + LPR * i] = s[p][i];
+    }
+    const float o = dot(s[p], q);
+    if (row < a.dv && j == 0) st((TIO *)a.out, (size_t)u * a.dv + row, a.scale * o);
+  }
+}
+
+template <int DK, typename TIO, int MODE>
+int launch_scan(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st) {
+  timing_mark_begin(K_RULE_SCAN, st);
+  mesa_rule_scan_kernel<DK, TIO, MODE><<<dim3((a.dv + ROWS - 1) / ROWS, a.units()), 128, 0, st>>>(a, ws);
+  timing_mark_end(K_RULE_SCAN, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int DK, typename TIO>
+int launch_bwd_t(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st) {
+  if (launch_scan<DK, TIO, kStates>(a, ws, st) != 0 || launch_scan<DK, TIO, kAdjoint>(a, ws, st) != 0) return -1;
+  const int smem = (2 * kRuleChunk * (DK + 4) + 3 * kRuleChunk * (a.dv + 4) + 4 * kRuleChunk * (kRuleChunk + 1) +
+                    5 * kRuleChunk + 8) * (int)sizeof(float);
+  auto kfn = mesa_rule_grads_kernel<DK, TIO>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+  timing_mark_begin(K_RULE_GRADS, st);
+  kfn<<<dim3((a.T + kRuleChunk - 1) / kRuleChunk, a.units()), 256, smem, st>>>(a, ws);
+  timing_mark_end(K_RULE_GRADS, st);
+  if (cudaPeekAtLastError() != cudaSuccess) return -1;
+  return ws.dqp ? launch_rule_group_sum(a, ws.dqp, ws.dkp, st) : 0;
+}
+
+template <int DK, typename TIO>
+int launch_step_t(const RuleStepArgs &a, cudaStream_t st) {
+  constexpr int rows = 4 * (32 / (DK / 16)) * (DK == 128 ? 2 : 1);
+  timing_mark_begin(K_RULE_STEP, st);
+  mesa_rule_step_kernel<DK, TIO><<<dim3(a.N * a.H, (a.dv + rows - 1) / rows), 128, 0, st>>>(a);
+  timing_mark_end(K_RULE_STEP, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+// F<DK, TIO>(...) for the supported key sizes and element types.
+#define MESA_RULE_DISPATCH(F, a, ...)                                                          \
+  switch (a.dk) {                                                                              \
+    case 16: return a.dtype == 1 ? F<16, __nv_bfloat16>(__VA_ARGS__) : F<16, float>(__VA_ARGS__);   \
+    case 32: return a.dtype == 1 ? F<32, __nv_bfloat16>(__VA_ARGS__) : F<32, float>(__VA_ARGS__);   \
+    case 64: return a.dtype == 1 ? F<64, __nv_bfloat16>(__VA_ARGS__) : F<64, float>(__VA_ARGS__);   \
+    case 128: return a.dtype == 1 ? F<128, __nv_bfloat16>(__VA_ARGS__) : F<128, float>(__VA_ARGS__); \
+  }                                                                                            \
+  return -1
+
+template <int DK, typename TIO>
+int launch_fwd_t(const RuleArgs &a, cudaStream_t st) {
+  return launch_scan<DK, TIO, kForward>(a, RuleBwdWorkspace{}, st);
+}
+
+}  // namespace
+
+int launch_rule_forward(const RuleArgs &a, cudaStream_t st) { MESA_RULE_DISPATCH(launch_fwd_t, a, a, st); }
+int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st) {
+  MESA_RULE_DISPATCH(launch_bwd_t, a, a, ws, st);
+}
+int launch_rule_step(const RuleStepArgs &a, cudaStream_t st) { MESA_RULE_DISPATCH(launch_step_t, a, a, st); }
+
+int launch_rule_group_sum(const RuleArgs &a, const float *dqp, const float *dkp, cudaStream_t st) {
+  const size_t total = (size_t)a.B * a.Hk * a.T * a.dk / 4;
+  const size_t want = (total + 255) / 256;
+  const int grid = (int)(want < 4096 ? want : 4096);
+  timing_mark_begin(K_RULE_GROUP, st);
+  if (a.dtype == 1)
+    mesa_rule_group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, dqp, dkp);
+  else
+    mesa_rule_group_sum_kernel<float><<<grid, 256, 0, st>>>(a, dqp, dkp);
+  timing_mark_end(K_RULE_GROUP, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace mesa

@@ -1,0 +1,55 @@
+// gated_delta.h -- argument bundle and launchers of the gated delta rule (internal).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mesa {
+
+// One bundle for the sequence forms.  Units u = b H + h; unit u reads the query / key head
+// b Hk + h / (H / Hk).
+struct RuleArgs {
+  int B, H, Hk, T, dk, dv, dtype;
+  const void *q, *k, *v;               // [B, Hk, T, dk] x 2, [B, H, T, dv]
+  const float *gamma, *beta;           // [B, H, T]
+  float scale;
+  void *out = nullptr;                 // [B, H, T, dv] (forward)
+  const float *S0 = nullptr;           // [B, H, dv, dk] or nullptr
+  float *S_final = nullptr;
+  // backward
+  const void *dout = nullptr;          // [B, H, T, dv]
+  const float *dS_final = nullptr;     // [B, H, dv, dk] or nullptr
+  void *dq = nullptr, *dk_out = nullptr, *dv_out = nullptr, *dgamma = nullptr, *dbeta = nullptr;
+  float *dS0 = nullptr;
+  unsigned *status = nullptr;
+  unsigned wait_limit = 0;
+  __host__ __device__ int units() const { return B * H; }
+  __host__ __device__ int qk_unit(int u) const { return (u / H) * Hk + (u % H) / (H / Hk); }
+};
+
+// CUDA-core path: chunks of kRuleChunk tokens in the backward pass.
+constexpr int kRuleChunk = 32;
+struct RuleBwdWorkspace {
+  float *S, *dS;       // [U, NC, dv, dk] states before / adjoints after each chunk
+  float *e, *du;       // [U, T, dv]
+  float *dqp, *dkp;    // [U, T, dk] per-unit dq, dk (nullptr when every head has its own q, k)
+};
+
+struct RuleStepArgs {
+  int N, H, Hk, dk, dv, dtype;
+  float *S;
+  const void *q, *k, *v;
+  const float *gamma, *beta;
+  float scale;
+  void *out;
+};
+
+// Each returns 0 when every launch was enqueued, -1 otherwise.
+int launch_rule_forward(const RuleArgs &a, cudaStream_t st);
+int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st);
+int launch_rule_step(const RuleStepArgs &a, cudaStream_t st);
+// dq, dk [B, Hk, T, dk] = sums of the per-unit fp32 parts over the value heads of a key head.
+int launch_rule_group_sum(const RuleArgs &a, const float *dqp, const float *dkp, cudaStream_t st);
+
+}  // namespace mesa
