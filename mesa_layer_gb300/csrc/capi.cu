@@ -213,6 +213,8 @@ const char *mesa_kernel_name(int kind) {
     case mesa::K_RULE_STEP: return "mesa_rule_step_kernel";
     case mesa::K_NORM: return "mesa_block_norm_kernel";
     case mesa::K_NORM_BWD: return "mesa_block_norm_bwd_kernel";
+    case mesa::K_RULE_PREP: return "mesa_rule_prep_kernel";
+    case mesa::K_RULE_CHAIN: return "mesa_rule_chain_kernel";
     case mesa::K_NORM_COLS: return "mesa_block_norm_cols_kernel";
   }
   return nullptr;

@@ -1,0 +1,34 @@
+// packed.cuh -- pairs of fp32 values in one 64-bit register: each instruction rounds both lanes
+// like the scalar one and takes one issue slot.
+#pragma once
+
+#include <stdint.h>
+
+namespace mesa {
+
+using u64 = unsigned long long;
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ u64 pack2(float x, float y) {
+  u64 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void unpack2(u64 a, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+__device__ __forceinline__ float sum2(u64 a) {
+  float x, y;
+  unpack2(a, x, y);
+  return x + y;
+}
+
+}  // namespace mesa

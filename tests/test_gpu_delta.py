@@ -283,3 +283,33 @@ def test_bad_shapes_are_refused():
     with pytest.raises(binding.MesaError):  # not contiguous
         binding.mesa_delta_forward_chunked(q.transpose(1, 2).contiguous().transpose(1, 2), q, q, g[:, :2].contiguous(),
                                            g[:, :2].contiguous())
+
+
+def test_wait_give_up_reports_timeout_and_the_next_call_is_clean():
+    """The tensor-core kernels' bounded waits made to give up at once: a status, no hang."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    s = ref.rule_inputs(19, "bf16", 1, 2, 2, 300, 128, 128, "open")
+    t = upload(s, "bf16")
+    args = [t[n] for n in ("q", "k", "v", "gamma", "beta")]
+    sizes = (1, 2, 2, 300, 128, 128, torch.bfloat16)
+    wf = torch.empty(binding.mesa_delta_workspace_size(*sizes), dtype=torch.uint8, device="cuda")
+    wb = torch.empty(binding.mesa_delta_backward_workspace_size(*sizes), dtype=torch.uint8, device="cuda")
+
+    def run():
+        out = binding.mesa_delta_forward_chunked(*args, workspace=wf)
+        grads = binding.mesa_delta_backward_chunked(*args, t["dout"], workspace=wb)
+        return [out, *grads], [binding.mesa_forward_status_code(w) for w in (wf, wb)]
+
+    want, codes = run()
+    assert codes == [(binding.MESA_OK, 0)] * 2
+    binding.mesa_debug_set_wait_limit(0)
+    try:
+        _, codes = run()
+    finally:
+        binding.mesa_debug_set_wait_limit(-1)
+    assert codes[0][0] == binding.MESA_ERR_TIMEOUT and codes[0][1] & 1 and not codes[0][1] & 4, codes
+    got, codes = run()
+    assert codes == [(binding.MESA_OK, 0)] * 2
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
