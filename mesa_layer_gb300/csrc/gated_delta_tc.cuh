@@ -28,11 +28,6 @@ constexpr int C = 64, D = 128;               // tokens per chunk; dk = dv
 constexpr uint32_t TILE = 2 * C * D * 2;     // fp16 [128 x 128] operand: K rows, then Q rows
 constexpr uint32_t SQ = C * C * 2;           // fp16 [64 x 64] operand
 constexpr uint32_t ROWS64 = C * D * 2;       // 64 bf16 rows
-// A chunk's record in the workspace: the factor T or T diag(beta) and P = (Q K^T o D), both as
-// swizzled K-major operands, then f and c.
-constexpr uint32_t REC_P = SQ, REC_F = 2 * SQ, REC_C = REC_F + 4 * C, REC = REC_C + 4 * C;
-static_assert(REC % 128 == 0, "records are bulk copied");
-
 // Operand scale of a tile with largest element m: a power of two with m s in (0.5, 1], limited
 // so that its square stays finite.
 __device__ __forceinline__ float tile_scale(float m) {
@@ -124,11 +119,190 @@ __device__ __forceinline__ GatePair gate_scan(const float *gamma, int n, int lan
   return GatePair{l - b, l, z - (int)sb, z};
 }
 
-// Workspace of the tensor-core forward: records and operand scales {s_k, s_q} of every chunk.
-struct TcWorkspace {
-  uint8_t *rec;     // [U, NC] records
-  float2 *scales;   // [U, NC]
+// 2^x (a PTX instruction; 2^-22 relative error).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D += A B of one 16 x 8 x 16 product (fp16 operands, fp32 sums): the blocks of the triangular
+// inverse, too small and too sequential for the 128-row products.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ---- the factors of a chunk, by 128 threads ------------------------------------------------------
+struct Factor {
+  __half Ah[C][72];      // A, fp16 (the blocks below the diagonal are used)
+  float Ad[C][20];       // its diagonal 16 x 16 blocks: row i, columns of block i / 16
+  __half Tb[4][16][24];  // inverses of the diagonal blocks of I + A, and their transposes
+  __half Yb[4][16][24];
+  float l[C], beta[C];
+  int z[C];
 };
+// Decays from the gates of one warp's scan: l, z, and f (chunk start to token), c (token to end).
+__device__ __forceinline__ void factor_gates(Factor &s, const GatePair &g, float *f, float *c, int lane) {
+  const float end = __shfl_sync(0xffffffffu, g.l1, 31);
+  const int zend = __shfl_sync(0xffffffffu, g.z1, 31);
+  *reinterpret_cast<float2 *>(&s.l[2 * lane]) = make_float2(g.l0, g.l1);
+  *reinterpret_cast<int2 *>(&s.z[2 * lane]) = make_int2(g.z0, g.z1);
+  *reinterpret_cast<float2 *>(f + 2 * lane) = make_float2(g.z0 == 0 ? ex2(g.l0) : 0.0f, g.z1 == 0 ? ex2(g.l1) : 0.0f);
+  *reinterpret_cast<float2 *>(c + 2 * lane) =
+      make_float2(g.z0 == zend ? ex2(end - g.l0) : 0.0f, g.z1 == zend ? ex2(end - g.l1) : 0.0f);
+}
+// Thread `tid` (warp w reads tensor-memory lanes 32 w ..): row tid of [K K^T; Q K^T] at tensor
+// memory `t`, in operand units.  Rows of A go to s, rows of P to the swizzled operand P.
+// after_load() runs once the accumulator has been read.
+template <typename AfterLoad>
+__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float sk, uint8_t *P, int tid, AfterLoad after_load) {
+  const int warp = tid >> 5, lane = tid & 31, i = tid & 63;
+  const bool isA = tid < C;
+  const float li = s.l[i], mul = isA ? s.beta[i] / (sk * sk) : 1.0f;
+  const int zi = s.z[i], last = isA ? i - 1 : i;
+  const bool cut = s.z[C - 1] != 0;  // a closed gate in the chunk
+  float v[C];
+  {
+    float x[32];
+    tc::tmem_ld32(t + ((uint32_t)(32 * warp) << 16), x);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; k++) v[k] = x[k];
+    tc::tmem_ld32(t + ((uint32_t)(32 * warp) << 16) + 32, x);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; k++) v[32 + k] = x[k];
+  }
+  after_load();
+#pragma unroll
+  for (int k = 0; k < C; k += 4) {
+    const float4 l4 = *reinterpret_cast<const float4 *>(&s.l[k]);
+    const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[k + e] = k + e <= last ? v[k + e] * (mul * ex2(li - lj[e])) : 0.0f;
+  }
+  if (cut) {
+#pragma unroll
+    for (int k = 0; k < C; k += 4) {
+      const int4 z4 = *reinterpret_cast<const int4 *>(&s.z[k]);
+      if (z4.x != zi) v[k] = 0.0f;
+      if (z4.y != zi) v[k + 1] = 0.0f;
+      if (z4.z != zi) v[k + 2] = 0.0f;
+      if (z4.w != zi) v[k + 3] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    float4 o;
+    o.x = half2_bits(v[8 * k], v[8 * k + 1]);
+    o.y = half2_bits(v[8 * k + 2], v[8 * k + 3]);
+    o.z = half2_bits(v[8 * k + 4], v[8 * k + 5]);
+    o.w = half2_bits(v[8 * k + 6], v[8 * k + 7]);
+    if (isA)
+      *reinterpret_cast<float4 *>(&s.Ah[i][8 * k]) = o;
+    else
+      *reinterpret_cast<float4 *>(P + tile_off(i, k, C)) = o;
+  }
+  if (isA) {  // the row's part of its diagonal block, in fp32
+    float d[16];
+#pragma unroll
+    for (int k = 0; k < 16; k++) {
+      const float lo = lane < 16 ? v[k] : v[16 + k], hi = lane < 16 ? v[32 + k] : v[48 + k];
+      d[k] = warp == 0 ? lo : hi;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+      *reinterpret_cast<float4 *>(&s.Ad[i][4 * k]) = make_float4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
+  }
+}
+// Warp w < 4: the inverse of diagonal block w by substitution in fp32 (lane = column, twice), to
+// s and to the swizzled operand M, columns times b (1 or beta).
+template <bool WITH_BETA>
+__device__ __forceinline__ void factor_diagonal(Factor &s, uint8_t *M, int w, int lane) {
+  const int col = lane & 15;
+  const float b = WITH_BETA ? s.beta[16 * w + col] : 1.0f;
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    float x[2] = {i == col ? 1.0f : 0.0f, 0.0f};
+#pragma unroll
+    for (int j4 = 0; j4 < i; j4 += 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(&s.Ad[16 * w + i][j4]);
+      x[0] = fmaf(-a.x, t[j4], x[0]);
+      if (j4 + 1 < i) x[1] = fmaf(-a.y, t[j4 + 1], x[1]);
+      if (j4 + 2 < i) x[0] = fmaf(-a.z, t[j4 + 2], x[0]);
+      if (j4 + 3 < i) x[1] = fmaf(-a.w, t[j4 + 3], x[1]);
+    }
+    t[i] = x[0] + x[1];
+  }
+  if (lane < 16) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      s.Tb[w][i][col] = __float2half_rn(t[i]);
+      *reinterpret_cast<__half *>(M + tc::sw128_offset(16 * w + i, 16 * w + col, C)) = __float2half_rn(t[i] * b);
+    }
+  } else {
+    __align__(16) float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) y[k] = half2_bits(t[2 * k], t[2 * k + 1]);
+    *reinterpret_cast<float4 *>(&s.Yb[w][col][0]) = *reinterpret_cast<const float4 *>(y);
+    *reinterpret_cast<float4 *>(&s.Yb[w][col][8]) = *reinterpret_cast<const float4 *>(y + 4);
+  }
+}
+// Warp c < 4: the blocks of column block c below the diagonal, downwards,
+//     T_bc = -T_bb sum_{k = c .. b-1} A_bk T_kc,
+// in transposed form Y_cb = T_bc^T: a product's sums are then the next one's operand as they lie in
+// the registers.
+template <bool WITH_BETA>
+__device__ __forceinline__ void factor_columns(Factor &s, uint8_t *M, int c, int lane) {
+  const int g = lane >> 2, q = 2 * (lane & 3);
+  const float be0 = WITH_BETA ? s.beta[16 * c + g] : 1.0f, be1 = WITH_BETA ? s.beta[16 * c + g + 8] : 1.0f;
+  uint32_t y[4][4];
+  auto word = [](const __half *p) { return *reinterpret_cast<const uint32_t *>(p); };
+  auto pack = [](float a, float b) { return __float_as_uint(half2_bits(a, b)); };
+#pragma unroll
+  for (int b = 0; b < 4; b++) {
+    if (b == c) {
+      y[b][0] = word(&s.Yb[b][g][q]);
+      y[b][1] = word(&s.Yb[b][g + 8][q]);
+      y[b][2] = word(&s.Yb[b][g][q + 8]);
+      y[b][3] = word(&s.Yb[b][g + 8][q + 8]);
+    } else if (b > c) {
+      float z0[4] = {}, z1[4] = {};
+#pragma unroll
+      for (int k = 0; k < b; k++) {
+        if (k < c) continue;
+        mma_16816(z0, y[k], word(&s.Ah[16 * b + g][16 * k + q]), word(&s.Ah[16 * b + g][16 * k + q + 8]));
+        mma_16816(z1, y[k], word(&s.Ah[16 * b + g + 8][16 * k + q]), word(&s.Ah[16 * b + g + 8][16 * k + q + 8]));
+      }
+      const uint32_t za[4] = {pack(-z0[0], -z0[1]), pack(-z0[2], -z0[3]), pack(-z1[0], -z1[1]), pack(-z1[2], -z1[3])};
+      float w0[4] = {}, w1[4] = {};
+      mma_16816(w0, za, word(&s.Tb[b][g][q]), word(&s.Tb[b][g][q + 8]));
+      mma_16816(w1, za, word(&s.Tb[b][g + 8][q]), word(&s.Tb[b][g + 8][q + 8]));
+      y[b][0] = pack(w0[0], w0[1]);
+      y[b][1] = pack(w0[2], w0[3]);
+      y[b][2] = pack(w1[0], w1[1]);
+      y[b][3] = pack(w1[2], w1[3]);
+      auto put = [&](int row, int col, float t) {
+        *reinterpret_cast<__half *>(M + tc::sw128_offset(16 * b + row, 16 * c + col, C)) = __float2half_rn(t);
+      };
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        put(q + e, g, w0[e] * be0);
+        put(q + e, g + 8, w0[2 + e] * be1);
+        put(q + 8 + e, g, w1[e] * be0);
+        put(q + 8 + e, g + 8, w1[2 + e] * be1);
+      }
+    }
+  }
+}
+// The blocks above the diagonal of M are never written: cleared once by 128 threads.
+__device__ __forceinline__ void factor_clear(uint8_t *M, int tid) {
+  for (int i = tid; i < (int)(SQ / 16); i += 128) reinterpret_cast<uint4 *>(M)[i] = make_uint4(0, 0, 0, 0);
+}
 
 }  // namespace rule
 }  // namespace mesa
