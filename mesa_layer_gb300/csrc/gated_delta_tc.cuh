@@ -8,11 +8,14 @@
 // (I + A) is unit lower triangular: its inverse comes from substitution, which keeps the
 // accuracy of the recurrence (powers of A would cancel).
 //
-// Operands of the matrix products are fp16 with power-of-two scales, accumulated in fp32: q
-// and k are bf16, exact in fp16 but for elements 2^14 below their tile's largest; states, u and
-// the triangular factors are rounded to 2^-12 relative to their row's largest element, well
-// inside the 2^-9 of the bf16 outputs.  The states themselves stay fp32 in registers, so
-// the operand rounding of one chunk is not carried on but as an input error.
+// Operands of the matrix products are fp16 with power-of-two scales, sums are fp32: q and k are
+// bf16, exact in fp16 but for elements 2^16 below their tile's largest; the state, R, U and the
+// factors are rounded to 2^-12, well inside the 2^-9 of the bf16 outputs (bf16 operands would
+// double the output's error).  Row scales come from bounds rather than from the largest
+// element: fp16 covers 2^29 in full precision, so a bound 2^15 above the values costs nothing.
+// The state itself stays fp32 in registers, so a chunk's operand rounding enters the next
+// one only through u.  The inverse is formed in fp32 (diagonal blocks) and from fp16 blocks with
+// fp32 sums (the rest).
 #pragma once
 
 #include "common.cuh"
@@ -25,43 +28,54 @@ namespace mesa {
 namespace rule {
 
 constexpr int C = 64, D = 128;               // tokens per chunk; dk = dv
-constexpr uint32_t TILE = 2 * C * D * 2;     // fp16 [128 x 128] operand: K rows, then Q rows
-constexpr uint32_t SQ = C * C * 2;           // fp16 [64 x 64] operand
-constexpr uint32_t ROWS64 = C * D * 2;       // 64 bf16 rows
-// Operand scale of a tile with largest element m: a power of two with m s in (0.5, 1], limited
-// so that its square stays finite.
-__device__ __forceinline__ float tile_scale(float m) {
-  return fminf(fmaxf(tc::rcp_pow2_ceil(m), 8.6736174e-19f), 1.1529215e18f);  // 2^-60 .. 2^60
-}
-
-// Eight bf16 values times s as fp16.
-__device__ __forceinline__ uint4 to_half8(uint4 raw, u64 s2) {
-  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const u64 x = mul2(pack2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), s2);
-    float a, b;
-    unpack2(x, a, b);
-    const __half2 h = __floats2half2_rn(a, b);
-    out[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  return make_uint4(out[0], out[1], out[2], out[3]);
-}
-__device__ __forceinline__ float absmax8(uint4 raw) {  // largest |x| of eight bf16 values
-  const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(in[i] << 16)), fabsf(__uint_as_float(in[i] & 0xffff0000u))));
-  return m;
-}
+constexpr uint32_t TILE = 2 * C * D * 2;     // [128 x 128] operand: K rows, then Q rows
+constexpr uint32_t SQ = C * C * 2;           // [64 x 64] operand
+constexpr uint32_t ROWS64 = C * D * 2;       // 64 rows of bf16
 __device__ __forceinline__ float half2_bits(float a, float b) {  // two fp16 values as a 32-bit register
   const __half2 h = __floats2half2_rn(a, b);
   return __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
 }
+__device__ __forceinline__ float half2_bits(u64 x) {
+  float a, b;
+  unpack2(x, a, b);
+  return half2_bits(a, b);
+}
+// The power of two s with 2^(top-1) < bound s < 2^top (bound taken as at least 2^-63 and at most
+// 2^63), and 1 / s.
+__device__ __forceinline__ float bound_scale(float bound, int top, float &inv) {
+  const int e = min(max((int)(__float_as_uint(bound) >> 23), 64), 190);
+  inv = __uint_as_float((uint32_t)(e + 1 - top) << 23);
+  return __uint_as_float((uint32_t)(253 + top - e) << 23);
+}
+constexpr int kTopRow = 15;   // state rows, R and U rows: bound to 2^15
+constexpr int kTopTile = 3;   // K and Q tiles: 128 products of two stay below 2^13
+// Largest |x| of 2 x 16-bit bf16 words, as an integer (the order of positive floats is theirs).
+__device__ __forceinline__ uint32_t absmax_words(uint32_t m, uint4 x) {
+  constexpr uint32_t k = 0x7fff7fffu;
+  return __vimax3_u16x2(__vimax3_u16x2(m, x.x & k, x.y & k), x.z & k, x.w & k);
+}
+__device__ __forceinline__ uint32_t absmax_fold(uint32_t m) {  // over the two halves and the warp
+  m = max(m & 0xffffu, m >> 16);
+  return __reduce_max_sync(0xffffffffu, m);
+}
+// Eight bf16 values times s as fp16.
+__device__ __forceinline__ uint4 to_half8(uint4 raw, u64 s2) {
+  auto two = [s2](uint32_t w) {
+    return __float_as_uint(half2_bits(mul2(pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), s2)));
+  };
+  return make_uint4(two(raw.x), two(raw.y), two(raw.z), two(raw.w));
+}
+// Tiled load of a box of a 3-D tensor map (channel x, token y, unit z); tokens past the end
+// read as zero.
+__device__ __forceinline__ void tensor_g2s_3d(uint32_t dst, const void *map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 
-// Offset in a swizzled K-major [rows x 128] fp16 tile of the 16 bytes holding columns
+// Offset in a swizzled K-major [rows x 128] 16-bit tile of the 16 bytes holding columns
 // 8 c8 .. 8 c8 + 7 of row r.
 __device__ __forceinline__ uint32_t tile_off(int r, int c8, int rows) { return tc::sw128_offset(r, 8 * c8, rows); }
 
@@ -144,78 +158,84 @@ struct Factor {
   float l[C], beta[C];
   int z[C];
 };
-// Decays from the gates of one warp's scan: l, z, and f (chunk start to token), c (token to end).
-__device__ __forceinline__ void factor_gates(Factor &s, const GatePair &g, float *f, float *c, int lane) {
+// Decays from the gates of one warp's scan: l, z, minus f (chunk start to token) and c (token to
+// end).
+__device__ __forceinline__ void factor_gates(Factor &s, const GatePair &g, float *nf, float *c, int lane) {
   const float end = __shfl_sync(0xffffffffu, g.l1, 31);
   const int zend = __shfl_sync(0xffffffffu, g.z1, 31);
   *reinterpret_cast<float2 *>(&s.l[2 * lane]) = make_float2(g.l0, g.l1);
   *reinterpret_cast<int2 *>(&s.z[2 * lane]) = make_int2(g.z0, g.z1);
-  *reinterpret_cast<float2 *>(f + 2 * lane) = make_float2(g.z0 == 0 ? ex2(g.l0) : 0.0f, g.z1 == 0 ? ex2(g.l1) : 0.0f);
+  *reinterpret_cast<float2 *>(nf + 2 * lane) = make_float2(g.z0 == 0 ? -ex2(g.l0) : 0.0f, g.z1 == 0 ? -ex2(g.l1) : 0.0f);
   *reinterpret_cast<float2 *>(c + 2 * lane) =
       make_float2(g.z0 == zend ? ex2(end - g.l0) : 0.0f, g.z1 == zend ? ex2(end - g.l1) : 0.0f);
 }
 // Thread `tid` (warp w reads tensor-memory lanes 32 w ..): row tid of [K K^T; Q K^T] at tensor
-// memory `t`, in operand units.  Rows of A go to s, rows of P to the swizzled operand P.
-// after_load() runs once the accumulator has been read.
+// memory `t`, in operand units (inv_kk: 1 / scale of K, squared).  Rows of A go to s, rows of P,
+// still in operand units, to the swizzled operand P.  Column
+// halves above the diagonal are skipped.  after_load() runs once the accumulator has been read.
 template <typename AfterLoad>
-__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float sk, uint8_t *P, int tid, AfterLoad after_load) {
+__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, uint8_t *P, int tid, AfterLoad after_load) {
   const int warp = tid >> 5, lane = tid & 31, i = tid & 63;
-  const bool isA = tid < C;
-  const float li = s.l[i], mul = isA ? s.beta[i] / (sk * sk) : 1.0f;
-  const int zi = s.z[i], last = isA ? i - 1 : i;
-  const bool cut = s.z[C - 1] != 0;  // a closed gate in the chunk
-  float v[C];
-  {
-    float x[32];
-    tc::tmem_ld32(t + ((uint32_t)(32 * warp) << 16), x);
+  const bool isA = tid < C, low = i >= 32;  // (uniform in a warp)
+  const float li = s.l[i], mul = isA ? s.beta[i] * inv_kk : 1.0f;
+  const int zi = s.z[i], last = (isA ? lane - 1 : lane);  // last column kept of the diagonal half
+  const bool cut = s.z[C - 1] != 0;                       // a closed gate in the chunk
+  const uint32_t tl = t + ((uint32_t)(32 * warp) << 16);
+  const u64 li2 = pack2(li, li), mul2x = pack2(mul, mul);
+  auto half = [&](int h, bool diagonal) {  // columns 32 h ..
+    float v[32];
+    tc::tmem_ld32(tl + 32 * h, v);
     tc::tmem_ld_wait();
-#pragma unroll
-    for (int k = 0; k < 32; k++) v[k] = x[k];
-    tc::tmem_ld32(t + ((uint32_t)(32 * warp) << 16) + 32, x);
-    tc::tmem_ld_wait();
-#pragma unroll
-    for (int k = 0; k < 32; k++) v[32 + k] = x[k];
-  }
-  after_load();
-#pragma unroll
-  for (int k = 0; k < C; k += 4) {
-    const float4 l4 = *reinterpret_cast<const float4 *>(&s.l[k]);
-    const float lj[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-    for (int e = 0; e < 4; e++) v[k + e] = k + e <= last ? v[k + e] * (mul * ex2(li - lj[e])) : 0.0f;
-  }
-  if (cut) {
-#pragma unroll
-    for (int k = 0; k < C; k += 4) {
-      const int4 z4 = *reinterpret_cast<const int4 *>(&s.z[k]);
-      if (z4.x != zi) v[k] = 0.0f;
-      if (z4.y != zi) v[k + 1] = 0.0f;
-      if (z4.z != zi) v[k + 2] = 0.0f;
-      if (z4.w != zi) v[k + 3] = 0.0f;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 8; k++) {
-    float4 o;
-    o.x = half2_bits(v[8 * k], v[8 * k + 1]);
-    o.y = half2_bits(v[8 * k + 2], v[8 * k + 3]);
-    o.z = half2_bits(v[8 * k + 4], v[8 * k + 5]);
-    o.w = half2_bits(v[8 * k + 6], v[8 * k + 7]);
-    if (isA)
-      *reinterpret_cast<float4 *>(&s.Ah[i][8 * k]) = o;
-    else
-      *reinterpret_cast<float4 *>(P + tile_off(i, k, C)) = o;
-  }
-  if (isA) {  // the row's part of its diagonal block, in fp32
+    if (diagonal) after_load();
+    uint32_t out[16];
     float d[16];
 #pragma unroll
-    for (int k = 0; k < 16; k++) {
-      const float lo = lane < 16 ? v[k] : v[16 + k], hi = lane < 16 ? v[32 + k] : v[48 + k];
-      d[k] = warp == 0 ? lo : hi;
+    for (int k = 0; k < 32; k += 4) {
+      const ulonglong2 lj = *reinterpret_cast<const ulonglong2 *>(&s.l[32 * h + k]);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float x, y;
+        unpack2(sub2(li2, e ? lj.y : lj.x), x, y);
+        unpack2(mul2(mul2(pack2(v[k + e], v[k + e + 1]), mul2x), pack2(ex2(x), ex2(y))), v[k + e], v[k + e + 1]);
+      }
+    }
+    if (diagonal) {
+#pragma unroll
+      for (int k = 0; k < 32; k++)
+        if (k > last) v[k] = 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < 4; k++)
-      *reinterpret_cast<float4 *>(&s.Ad[i][4 * k]) = make_float4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
+    for (int k = 0; k < 16; k++)
+      out[k] = __float_as_uint(half2_bits(v[2 * k], v[2 * k + 1]));
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      uint4 o = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+      if (isA)
+        *reinterpret_cast<uint4 *>(&s.Ah[i][32 * h + 8 * k]) = o;
+      else
+        *reinterpret_cast<uint4 *>(P + tile_off(i, 4 * h + k, C)) = o;
+    }
+    if (diagonal && isA) {  // the row's part of its diagonal block, in fp32
+#pragma unroll
+      for (int k = 0; k < 16; k++) d[k] = lane < 16 ? v[k] : v[16 + k];
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        *reinterpret_cast<float4 *>(&s.Ad[i][4 * k]) = make_float4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
+    }
+  };
+  if (low) half(0, false);
+  half(low ? 1 : 0, true);
+  if (cut) {  // rare: the entries across a closed gate, in the stored rows
+#pragma unroll 1
+    for (int j = 0; j < i; j++) {
+      if (s.z[j] == zi) continue;
+      if (isA) {
+        s.Ah[i][j] = __float2half_rn(0.0f);
+        if (j >> 4 == i >> 4) s.Ad[i][j & 15] = 0.0f;
+      } else {
+        *reinterpret_cast<uint16_t *>(P + tc::sw128_offset(i, j, C)) = 0;
+      }
+    }
   }
 }
 // Warp w < 4: the inverse of diagonal block w by substitution in fp32 (lane = column, twice), to
@@ -299,7 +319,8 @@ __device__ __forceinline__ void factor_columns(Factor &s, uint8_t *M, int c, int
     }
   }
 }
-// The blocks above the diagonal of M are never written: cleared once by 128 threads.
+// What lies above the diagonal blocks of M (and above the 32-column halves of P) is never written:
+// cleared once by 128 threads.
 __device__ __forceinline__ void factor_clear(uint8_t *M, int tid) {
   for (int i = tid; i < (int)(SQ / 16); i += 128) reinterpret_cast<uint4 *>(M)[i] = make_uint4(0, 0, 0, 0);
 }

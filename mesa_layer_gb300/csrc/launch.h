@@ -132,6 +132,9 @@ int launch_states_tc(const FwdArgs &a, const FwdWorkspace &ws, unsigned *status,
 // 32 columns x 128 rows and the 128-byte swizzle; false if the driver offers no encoder or
 // it rejects the map.
 bool tmap_rows128_f32(CUtensorMap *map, float *base, size_t rows);
+// Tensor map of a [units, T, 128] bf16 array (16-byte aligned) with boxes of 64 channels x 64
+// tokens of one unit and the 128-byte swizzle; tokens past T read as zero.
+bool tmap_units128_bf16(CUtensorMap *map, const void *base, int units, int T);
 // The backward pass's 32-token chunk states (bwd = false) or state adjoints (bwd = true) on
 // the tensor cores, d = 128 (sweep_tc.cu).
 int launch_sweep_tc(const BwdArgs &a, const FwdWorkspace &ws, bool bwd, cudaStream_t st);
