@@ -110,15 +110,14 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned lim
 
 // Decays of a chunk's tokens in log2, with closed gates counted apart: the decay from token j
 // to token i >= j is 2^(l_i - l_j) if z_i = z_j, else 0.  Lane l of a whole warp handles
-// tokens 2l and 2l + 1; gates past the end are 1.  Gates below e^-80 count as closed.
+// tokens 2l and 2l + 1 (gates past the end: 1).  Gates below e^-80 count as closed.
 struct GatePair {
   float l0, l1;
   int z0, z1;
 };
-__device__ __forceinline__ GatePair gate_scan(const float *gamma, int n, int lane) {
-  const float ga = 2 * lane < n ? gamma[2 * lane] : 1.0f, gb = 2 * lane + 1 < n ? gamma[2 * lane + 1] : 1.0f;
-  const bool sa = ga < 1.8048514e-35f, sb = gb < 1.8048514e-35f;
-  const float a = sa ? 0.0f : log2f(ga), b = sb ? 0.0f : log2f(gb);
+__device__ __forceinline__ GatePair gate_scan(float2 gamma, int lane) {
+  const bool sa = gamma.x < 1.8048514e-35f, sb = gamma.y < 1.8048514e-35f;
+  const float a = sa ? 0.0f : log2f(gamma.x), b = sb ? 0.0f : log2f(gamma.y);
   float l = a + b;
   int z = (int)sa + (int)sb;
 #pragma unroll
@@ -171,60 +170,55 @@ __device__ __forceinline__ void factor_gates(Factor &s, const GatePair &g, float
 }
 // Thread `tid` (warp w reads tensor-memory lanes 32 w ..): row tid of [K K^T; Q K^T] at tensor
 // memory `t`, in operand units (inv_kk: 1 / scale of K, squared).  Rows of A go to s, rows of P,
-// still in operand units, to the swizzled operand P.  Column
-// halves above the diagonal are skipped.  after_load() runs once the accumulator has been read.
+// still in operand units, to the swizzled operand P.  Columns
+// right of the diagonal's 32 are skipped.  after_load() runs once the accumulator has been read.
 template <typename AfterLoad>
 __device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, uint8_t *P, int tid, AfterLoad after_load) {
-  const int warp = tid >> 5, lane = tid & 31, i = tid & 63;
+  const int warp = tid >> 5, i = tid & 63;
   const bool isA = tid < C, low = i >= 32;  // (uniform in a warp)
   const float li = s.l[i], mul = isA ? s.beta[i] * inv_kk : 1.0f;
-  const int zi = s.z[i], last = (isA ? lane - 1 : lane);  // last column kept of the diagonal half
+  const int zi = s.z[i], last = isA ? i - 1 : i;  // last column kept
   const bool cut = s.z[C - 1] != 0;                       // a closed gate in the chunk
   const uint32_t tl = t + ((uint32_t)(32 * warp) << 16);
   const u64 li2 = pack2(li, li), mul2x = pack2(mul, mul);
-  auto half = [&](int h, bool diagonal) {  // columns 32 h ..
-    float v[32];
-    tc::tmem_ld32(tl + 32 * h, v);
+  const int diag = i >> 4;  // the row's diagonal block
+#pragma unroll 1
+  for (int h = 0; h < (low ? 4 : 2); h++) {  // columns 16 h ..
+    float v[16];
+    tc::tmem_ld16(tl + 16 * h, v);
+    ulonglong2 lj[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) lj[k] = *reinterpret_cast<const ulonglong2 *>(&s.l[16 * h + 4 * k]);
     tc::tmem_ld_wait();
-    if (diagonal) after_load();
-    uint32_t out[16];
-    float d[16];
 #pragma unroll
-    for (int k = 0; k < 32; k += 4) {
-      const ulonglong2 lj = *reinterpret_cast<const ulonglong2 *>(&s.l[32 * h + k]);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float x, y;
-        unpack2(sub2(li2, e ? lj.y : lj.x), x, y);
-        unpack2(mul2(mul2(pack2(v[k + e], v[k + e + 1]), mul2x), pack2(ex2(x), ex2(y))), v[k + e], v[k + e + 1]);
-      }
+    for (int k = 0; k < 16; k += 2) {
+      float x, y;
+      unpack2(sub2(li2, k & 2 ? lj[k / 4].y : lj[k / 4].x), x, y);
+      unpack2(mul2(mul2(pack2(v[k], v[k + 1]), mul2x), pack2(ex2(x), ex2(y))), v[k], v[k + 1]);
     }
-    if (diagonal) {
+    const int keep = last - 16 * h;
+    if (h >= (low ? 2 : 0)) {
 #pragma unroll
-      for (int k = 0; k < 32; k++)
-        if (k > last) v[k] = 0.0f;
+      for (int k = 0; k < 16; k++)
+        if (k > keep) v[k] = 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < 16; k++)
-      out[k] = __float_as_uint(half2_bits(v[2 * k], v[2 * k + 1]));
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      uint4 o = make_uint4(out[4 * k], out[4 * k + 1], out[4 * k + 2], out[4 * k + 3]);
+    for (int k = 0; k < 2; k++) {
+      const float4 o = make_float4(half2_bits(v[8 * k], v[8 * k + 1]), half2_bits(v[8 * k + 2], v[8 * k + 3]),
+                                   half2_bits(v[8 * k + 4], v[8 * k + 5]), half2_bits(v[8 * k + 6], v[8 * k + 7]));
       if (isA)
-        *reinterpret_cast<uint4 *>(&s.Ah[i][32 * h + 8 * k]) = o;
+        *reinterpret_cast<float4 *>(&s.Ah[i][16 * h + 8 * k]) = o;
       else
-        *reinterpret_cast<uint4 *>(P + tile_off(i, 4 * h + k, C)) = o;
+        *reinterpret_cast<float4 *>(P + tile_off(i, 2 * h + k, C)) = o;
     }
-    if (diagonal && isA) {  // the row's part of its diagonal block, in fp32
-#pragma unroll
-      for (int k = 0; k < 16; k++) d[k] = lane < 16 ? v[k] : v[16 + k];
+    if (isA && h == diag) {  // its part of the diagonal block, in fp32
 #pragma unroll
       for (int k = 0; k < 4; k++)
-        *reinterpret_cast<float4 *>(&s.Ad[i][4 * k]) = make_float4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
+        *reinterpret_cast<float4 *>(&s.Ad[i][4 * k]) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     }
-  };
-  if (low) half(0, false);
-  half(low ? 1 : 0, true);
+  }
+  tc::fence_before_sync();
+  after_load();
   if (cut) {  // rare: the entries across a closed gate, in the stored rows
 #pragma unroll 1
     for (int j = 0; j < i; j++) {
