@@ -171,9 +171,8 @@ __device__ __forceinline__ void factor_gates(Factor &s, const GatePair &g, float
 // Thread `tid` (warp w reads tensor-memory lanes 32 w ..): row tid of [K K^T; Q K^T] at tensor
 // memory `t`, in operand units (inv_kk: 1 / scale of K, squared).  Rows of A go to s, rows of P,
 // still in operand units, to the swizzled operand P.  Columns
-// right of the diagonal's 32 are skipped.  after_load() runs once the accumulator has been read.
-template <typename AfterLoad>
-__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, uint8_t *P, int tid, AfterLoad after_load) {
+// right of the diagonal's 32 are skipped.
+__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, uint8_t *P, int tid) {
   const int warp = tid >> 5, i = tid & 63;
   const bool isA = tid < C, low = i >= 32;  // (uniform in a warp)
   const float li = s.l[i], mul = isA ? s.beta[i] * inv_kk : 1.0f;
@@ -182,20 +181,26 @@ __device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk,
   const uint32_t tl = t + ((uint32_t)(32 * warp) << 16);
   const u64 li2 = pack2(li, li), mul2x = pack2(mul, mul);
   const int diag = i >> 4;  // the row's diagonal block
-#pragma unroll 1
-  for (int h = 0; h < (low ? 4 : 2); h++) {  // columns 16 h ..
-    float v[16];
-    tc::tmem_ld16(tl + 16 * h, v);
+  float w[2][16];
+  tc::tmem_ld16(tl, w[0]);
+#pragma unroll
+  for (int h = 0; h < 4; h++) {  // columns 16 h .., the next ones on their way
+    if (h >= 2 && !low) break;
+    float *v = w[h & 1];
     ulonglong2 lj[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) lj[k] = *reinterpret_cast<const ulonglong2 *>(&s.l[16 * h + 4 * k]);
-    tc::tmem_ld_wait();
+    u64 dec[8];
 #pragma unroll
-    for (int k = 0; k < 16; k += 2) {
+    for (int k = 0; k < 8; k++) {
       float x, y;
-      unpack2(sub2(li2, k & 2 ? lj[k / 4].y : lj[k / 4].x), x, y);
-      unpack2(mul2(mul2(pack2(v[k], v[k + 1]), mul2x), pack2(ex2(x), ex2(y))), v[k], v[k + 1]);
+      unpack2(sub2(li2, k & 1 ? lj[k / 2].y : lj[k / 2].x), x, y);
+      dec[k] = mul2(pack2(ex2(x), ex2(y)), mul2x);
     }
+    tc::tmem_ld_wait();
+    if (h < 1 || (h < 3 && low)) tc::tmem_ld16(tl + 16 * (h + 1), w[(h + 1) & 1]);
+#pragma unroll
+    for (int k = 0; k < 8; k++) unpack2(mul2(pack2(v[2 * k], v[2 * k + 1]), dec[k]), v[2 * k], v[2 * k + 1]);
     const int keep = last - 16 * h;
     if (h >= (low ? 2 : 0)) {
 #pragma unroll
@@ -217,8 +222,6 @@ __device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk,
         *reinterpret_cast<float4 *>(&s.Ad[i][4 * k]) = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
     }
   }
-  tc::fence_before_sync();
-  after_load();
   if (cut) {  // rare: the entries across a closed gate, in the stored rows
 #pragma unroll 1
     for (int j = 0; j < i; j++) {
