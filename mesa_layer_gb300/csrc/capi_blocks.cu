@@ -53,7 +53,7 @@ extern "C" {
 
 size_t mesa_delta_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   if (check_sizes(B, H, Hk, T, dk, dv, dtype, 1.0f) != MESA_OK) return 0;
-  return kStatusBytes;
+  return kStatusBytes + (rule_tc(dtype, dk, dv) ? mesa::rule_tc_workspace(B * H, T) : 0);
 }
 
 int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,
@@ -83,7 +83,7 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
   a.status = (unsigned *)workspace;
   a.wait_limit = mesa::wait_limit();
   if (cudaMemsetAsync(a.status, 0, sizeof(unsigned), stream) != cudaSuccess) return MESA_ERR_CUDA;
-  const int rc = rule_tc(dtype, dk, dv) ? mesa::launch_rule_forward_tc(a, stream)
+  const int rc = rule_tc(dtype, dk, dv) ? mesa::launch_rule_forward_tc(a, (char *)workspace + kStatusBytes, stream)
                                         : mesa::launch_rule_forward(a, stream);
   return rc == 0 ? MESA_OK : MESA_ERR_CUDA;
 }

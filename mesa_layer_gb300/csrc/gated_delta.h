@@ -49,8 +49,11 @@ struct RuleStepArgs {
 int launch_rule_forward(const RuleArgs &a, cudaStream_t st);
 int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st);
 int launch_rule_step(const RuleStepArgs &a, cudaStream_t st);
-// The forward on the tensor cores (bf16, dk = dv = 128).
-int launch_rule_forward_tc(const RuleArgs &a, cudaStream_t st);
+// The tensor-core path (bf16, dk = dv = 128): workspace bytes, the chunks' records (with_beta: the
+// forward's), the forward.
+size_t rule_tc_workspace(int U, int T);
+int launch_rule_prep(const RuleArgs &a, void *records, bool with_beta, cudaStream_t st);
+int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st);
 // dq, dk [B, Hk, T, dk] = sums of the per-unit fp32 parts over the value heads of a key head.
 int launch_rule_group_sum(const RuleArgs &a, const float *dqp, const float *dkp, cudaStream_t st);
 

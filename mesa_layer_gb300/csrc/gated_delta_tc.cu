@@ -1,9 +1,11 @@
 // gated_delta_tc.cu -- the gated delta rule's chunked forward on the tensor cores (bf16,
 // dk = dv = 128; the chunk algebra and the operand formats are in gated_delta_tc.cuh).
 //
-// One CTA per unit walks the unit's chunks with the state in registers (thread r of the chain
-// holds row r, 128 values) and everything laid out by state row, so that a chunk's chain of
-// dependent products never crosses threads:
+// Two kernels.  mesa_rule_prep_kernel, one CTA per chunk: K K^T and Q K^T in one product, decays,
+// masks and the triangular inverse, written as a record.  mesa_rule_chain_kernel, one CTA per
+// unit, walks the unit's chunks with the state in registers (thread r of the chain holds row r,
+// 128 values) and everything laid out by state row, so that a chunk's chain of dependent
+// products never crosses threads:
 //     D1 = S0 K^T          -> R = V^T - f D1      (row r of the accumulator is thread r's)
 //     D2 = R (T beta)^T    -> U
 //     dS = (c U) K         -> S = f_last S0 + dS
@@ -12,10 +14,10 @@
 // bounds the kernel, so all else runs beside it, in warp groups of their own:
 //     chain    the three epilogues above;
 //     helper   transposes V one chunk ahead, writes the readout of the chunk before;
-//     factor   decays, masks and the triangular inverse, one chunk ahead;
 //     convert  K and Q as fp16 operands, up to three chunks ahead.
-// Each group's first thread issues the products that the group itself waits for.
-// The inputs are read once and the output written once; nothing else goes to memory.
+// (With the preparation in the same kernel, as a fourth group, nothing but the inputs and the output
+// went to memory, but the groups' code no longer fitted the instruction caches and every
+// group slowed down: 268 us at 8 x 16 x 4096 against the two kernels' time below.)
 #include "gated_delta_tc.cuh"
 
 namespace mesa {
@@ -24,41 +26,145 @@ using namespace rule;
 
 namespace {
 
-// shared memory: three K, Q operand tiles | two slots of factors M, P | V^T in fp32 | V | output |
-// factor scratch | misc
-constexpr uint32_t CH_TILE = 0, CH_FAC = CH_TILE + 3 * TILE, CH_VT = CH_FAC + 4 * SQ, CH_V = CH_VT + 2 * ROWS64;
-constexpr uint32_t CH_OUT = CH_V + ROWS64, CH_SCR = CH_OUT + ROWS64;
-constexpr uint32_t CH_MISC = CH_SCR + ((sizeof(Factor) + 127) & ~127u);
+// ---- per-chunk preparation --------------------------------------------------------------------
+// shared memory: the operand tile, and once its products are done record | scratch in its place
+// (39 KB: five CTAs on an SM hide each other's substitution) | misc
+constexpr uint32_t PR_REC = 0, PR_SCR = REC_PAD;
+constexpr uint32_t PR_MISC = (PR_SCR + sizeof(Factor) > TILE ? PR_SCR + sizeof(Factor) : TILE);
+static_assert(PR_MISC % 16 == 0, "misc alignment");
+struct PrepMisc {
+  alignas(16) uint32_t red[8];
+  uint64_t mbar, drain;
+  uint32_t tmem;
+};
+constexpr uint32_t PR_SMEM = PR_MISC + sizeof(PrepMisc) + 1024;
+
+// grid (NC, U), 128 threads.  WITH_BETA: the record's factor is T diag(beta), else T.
+// Measured (8 x 16 x 4096, 8192 chunks): see the table at the launch.
+template <bool WITH_BETA>
+__global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint8_t *records) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  PrepMisc *m = reinterpret_cast<PrepMisc *>(sm + PR_MISC);
+  Factor &s = *reinterpret_cast<Factor *>(sm + PR_SCR);
+  uint8_t *rec = sm + PR_REC;
+  float *nf = reinterpret_cast<float *>(rec + REC_F), *cc = nf + C, *inv = cc + C;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int c = blockIdx.x, u = blockIdx.y, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
+  const size_t row0 = (size_t)a.qk_unit(u) * a.T + t0, tok0 = (size_t)u * a.T + t0;
+
+  // rows of K and Q: 16 threads a row, 8 rows a pass
+  const int r0 = tid >> 4, c8 = tid & 15;
+  uint4 x[8], y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+    if (8 * i + r0 < n) {
+      x[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + (row0 + r0 + 8 * i) * D + 8 * c8);
+      y[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + (row0 + r0 + 8 * i) * D + 8 * c8);
+    }
+  }
+  if (warp == 0) tc::tmem_alloc(tc::smem_u32(&m->tmem), 64);
+  if (tid == 32) {
+    tc::mbar_init(tc::smem_u32(&m->mbar), 1);
+    tc::mbar_init(tc::smem_u32(&m->drain), 1);
+  }
+  const float be = tid < n && tid < C ? a.beta[tok0 + tid] : 0.0f;
+  GatePair g;
+  if (warp == 3) {
+    const float *gp = a.gamma + tok0;
+    g = gate_scan(make_float2(2 * lane < n ? gp[2 * lane] : 1.0f, 2 * lane + 1 < n ? gp[2 * lane + 1] : 1.0f), lane);
+  }
+  uint32_t mk = 0, mq = 0;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    mk = absmax_words(mk, x[k]);
+    mq = absmax_words(mq, y[k]);
+  }
+  mk = absmax_fold(mk);
+  mq = absmax_fold(mq);
+  if (lane == 0) {
+    m->red[warp] = mk;
+    m->red[4 + warp] = mq;
+  }
+  __syncthreads();
+  const uint4 k4 = *reinterpret_cast<const uint4 *>(m->red), q4 = *reinterpret_cast<const uint4 *>(m->red + 4);
+  float ik, iq;
+  const float sk = bound_scale(__uint_as_float(max(max(k4.x, k4.y), max(k4.z, k4.w)) << 16), kTopTile, ik);
+  const float sq = bound_scale(__uint_as_float(max(max(q4.x, q4.y), max(q4.z, q4.w)) << 16), kTopTile, iq);
+  const u64 sk2 = pack2(sk, sk), sq2 = pack2(sq, sq);
+  uint8_t *dst = sm + tile_off(r0, c8, 128);
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    *reinterpret_cast<uint4 *>(dst + 1024 * k) = to_half8(x[k], sk2);
+    *reinterpret_cast<uint4 *>(dst + C * 128 + 1024 * k) = to_half8(y[k], sq2);
+  }
+  tc::fence_smem_to_async();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, m->tmem, 0), bar = tc::smem_u32(&m->mbar);
+  if (warp == 0 && elect_one()) {  // rows 0..63: K K^T, rows 64..127: Q K^T
+    const uint32_t id = tc::idesc_f16(128, C, false, false);
+    const uint64_t t = tc::kmajor_desc(tc::smem_u32(sm), 128, 0);
+#pragma unroll
+    for (int k = 0; k < 8; k++) tc::mma_f16(tbase, t + step128(k), t + step128(k), id, k > 0);
+    tc::mma_commit(bar);
+  }
+  const bool done = tc::mbar_wait(bar, 0, a.wait_limit);
+  tc::fence_after_sync();
+  if (__syncthreads_or(!done)) {
+    if (tid == 0) atomicOr(a.status, tc::kErrMmaTimeout);
+    const bool issuer = warp == 0 && elect_one();
+    tc::drain_mmas(tc::smem_u32(&m->drain), issuer, a.status);
+  } else {
+    if (tid == 0) *reinterpret_cast<float4 *>(inv) = make_float4(ik, iq, sk, sq);
+    if (tid < C) s.beta[tid] = be;
+    if (warp == 3) factor_gates(s, g, nf, cc, lane);
+    factor_clear(rec, tid);
+    factor_clear(rec + SQ, tid);
+    __syncthreads();
+    factor_rows(s, tbase, ik * ik, rec + SQ, tid);
+    tc::fence_before_sync();
+    __syncthreads();
+    factor_diagonal<WITH_BETA>(s, rec, warp, lane);
+    __syncthreads();
+    if (warp < 3) factor_columns<WITH_BETA>(s, rec, warp, lane);
+    tc::fence_smem_to_async();
+    __syncthreads();
+    if (tid == 0) {
+      bulk_s2g(records + ((size_t)u * NC + c) * REC, tc::smem_u32(rec), REC);
+      tc::bulk_commit();
+      tc::bulk_wait_all();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_free(tbase, 64);
+}
+
+// ---- the chain ----------------------------------------------------------------------------------
+// shared memory: three K, Q operand tiles | three records | V^T in fp32 | V | output | misc
+constexpr uint32_t CH_TILE = 0, CH_REC = CH_TILE + 3 * TILE, CH_VT = CH_REC + 3 * REC_PAD, CH_V = CH_VT + 2 * ROWS64;
+constexpr uint32_t CH_OUT = CH_V + ROWS64, CH_MISC = CH_OUT + ROWS64;
 struct ChainMisc {
   float o1[2][D], o2[2][D];     // units of the readout's accumulators, by state row
-  float nf[4][C], c[4][C];    // minus the decays from the chunk's start; those to its end
-  float inv_k[3], inv_q[3];   // 1 / operand scales, by tile
   float vmax[4];              // largest |v| of 32 channels
-  alignas(16) uint32_t red[16];
-  uint64_t tile_full[3], tile_free[3], v_full, vt_full, d0_full, fac_full[2], r_ready, u_ready, o_free;
-  uint64_t mma1, mma2, mma3, mma4[2], drain;
+  uint64_t tile_full[3], tile_free[3], rec_full[3], v_full, vt_full, r_ready, u_ready, o_free;
+  uint64_t mma1, mma2, mma3, mma4, drain;
   uint32_t tmem;
   int gave_up;
 };
 constexpr uint32_t CH_SMEM = CH_MISC + sizeof(ChainMisc) + 1024;
 static_assert(CH_SMEM <= 232448, "shared memory per block");
-// tensor memory columns: dS | S0 operand | D1 (then R, c U and U), O from S0 | D2 | O from U |
-// [K K^T; Q K^T]
-constexpr uint32_t T_DS = 0, T_S = 128, T_D1 = 192, T_O1 = 256, T_D2 = 320, T_O2 = 384, T_D0 = 448;
+// tensor memory columns: dS | S0 operand | D1 (then R, c U and U), O from S0 | D2 | O from U
+constexpr uint32_t T_DS = 0, T_S = 128, T_D1 = 192, T_O1 = 256, T_D2 = 320, T_O2 = 384;
 constexpr uint32_t T_R = T_D1, T_CU = T_D1, T_U = T_D1 + 32;  // two values a column, each over what has been read
 
 // Offset of tokens 4 ch .. 4 ch + 3 of channel r in the transposed fp32 values (256 bytes a
 // channel; permuted so that neither the writes nor a warp's reads of 32 channels meet in a bank).
 __device__ __forceinline__ uint32_t vt_off(int r, int ch) { return (uint32_t)(r * 256 + ((ch ^ (r & 7)) << 4)); }
 
-// One lane of a converged warp.  The products' operands are warp-uniform registers: behind a plain
-// thread test (not this, under a warp-uniform condition) each product took 130 cycles to issue,
-// whatever its size; so, 56 (N = 64) to 74 (N = 128).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}\n" : "=r"(p));
-  return p != 0;
-}
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -66,9 +172,9 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "memory");
 }
 
-// Register shares of the four warp groups; the block is launched with 128 a thread.
-constexpr int kRegChain = 208, kRegHelper = 104, kRegFactor = 104, kRegConvert = 96;
-static_assert(kRegChain + kRegHelper + kRegFactor + kRegConvert <= 4 * 128, "register file");
+// Register shares of the three warp groups; the block is launched with 168 a thread.
+constexpr int kRegChain = 240, kRegHelper = 136, kRegConvert = 120;
+static_assert(kRegChain + kRegHelper + kRegConvert <= 3 * 168, "register file");
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -78,14 +184,9 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
-// K-step s of 16 added to a K-major descriptor of a 128-row tile, of a 64-row tile with 64 columns, and
-// to an MN-major one, in the descriptor's 16-byte units.
-__device__ __forceinline__ uint64_t step128(int s) { return (uint64_t)((s >> 2) * 1024 + (s & 3) * 2); }
-__device__ __forceinline__ uint64_t step64(int s) { return (uint64_t)(2 * s); }
-__device__ __forceinline__ uint64_t step_mn(int s) { return (uint64_t)(128 * s); }
-
-// grid U, 512 threads: warps 0-3 chain, 4-7 helper, 8-11 factor, 12-15 convert.
-__global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, const __grid_constant__ CUtensorMap mapV) {
+// grid U, 384 threads: warps 0-3 chain, 4-7 helper, 8-11 convert.
+__global__ void __launch_bounds__(384, 1)
+    mesa_rule_chain_kernel(RuleArgs a, const uint8_t *records, const __grid_constant__ CUtensorMap mapV) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   ChainMisc *m = reinterpret_cast<ChainMisc *>(sm + CH_MISC);
@@ -101,17 +202,22 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
 #pragma unroll
     for (int h = 0; h < 2; h++) tensor_g2s_3d(dst + h * C * 128, &mapV, 64 * h, c * C, u, b);
   };
+  auto fetch_rec = [&](int c) {
+    const uint32_t b = bar(m->rec_full[c % 3]);
+    tc::mbar_arrive_expect_tx(b, REC);
+    tc::bulk_g2s(tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD), records + ((size_t)u * NC + c) * REC, REC, b);
+  };
   if (warp == 0) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
   if (tid == 128) {
-    for (uint64_t *b : {&m->vt_full, &m->fac_full[0], &m->fac_full[1], &m->r_ready, &m->u_ready, &m->o_free,
-                        &m->tile_full[0], &m->tile_full[1], &m->tile_full[2]})
+    for (uint64_t *b : {&m->vt_full, &m->r_ready, &m->u_ready, &m->o_free, &m->tile_full[0], &m->tile_full[1], &m->tile_full[2]})
       tc::mbar_init(bar(*b), 4);
-    for (uint64_t *b : {&m->tile_free[0], &m->tile_free[1], &m->tile_free[2], &m->v_full, &m->d0_full, &m->mma1, &m->mma2,
-                        &m->mma3, &m->mma4[0], &m->mma4[1]})
+    for (uint64_t *b : {&m->tile_free[0], &m->tile_free[1], &m->tile_free[2], &m->rec_full[0], &m->rec_full[1],
+                        &m->rec_full[2], &m->v_full, &m->mma1, &m->mma2, &m->mma3, &m->mma4})
       tc::mbar_init(bar(*b), 1);
-    tc::mbar_init(bar(m->drain), 3);  // the three threads that issue products
+    tc::mbar_init(bar(m->drain), 2);  // the two threads that issue products
     m->gave_up = 0;
     fetch_v(0);
+    for (int c = 0; c < min(NC, 3); c++) fetch_rec(c);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -123,7 +229,7 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
     if (lane == 0) mbar_arrive(bar(b));
   };
   bool ok = true;
-  int v_sent = 1;  // fetches issued (thread 128)
+  int v_sent = 1, rec_sent = min(NC, 3);  // fetches issued (thread 128)
 
   if (warp < 4) {
     // ---- the chain: thread r holds row r of the state ----
@@ -177,8 +283,8 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
     };
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1, tile = tc::smem_u32(sm + CH_TILE + (c % 3) * TILE),
-                     fac = tc::smem_u32(sm + CH_FAC + 2 * SQ * ph);
-      const float *nf = m->nf[c & 3], *cc = m->c[c & 3];
+                     rec = tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD);
+      const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F), *cc = nf + C, *inv = cc + C;
       ok &= wait(bar(m->tile_full[c % 3]), (c / 3) & 1, limit, gave_up);
       if (c > 0) ok &= wait(bar(m->o_free), (c - 1) & 1, limit, gave_up);  // (the last readout is read)
       if (meet()) break;
@@ -189,10 +295,10 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
           tc::mma_f16_ts(tbase + T_D1, tbase + T_S + 8 * s, kq + step128(s), id128, s > 0);
         tc::mma_commit(bar(m->mma1));
       }
-      ok &= wait(bar(m->fac_full[ph]), (c >> 1) & 1, limit, gave_up);
+      ok &= wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
       ok &= wait(bar(m->vt_full), ph, limit, gave_up);
-      const float iK = m->inv_k[c % 3], kmax = (float)(1 << kTopTile) * iK;
-      m->o1[ph][r] = -a.scale * iS * m->inv_q[c % 3];
+      const float iK = inv[0], kmax = (float)(1 << kTopTile) * iK, all = -nf[C - 1];  // all: the chunk's decay
+      m->o1[ph][r] = -a.scale * iS * inv[1];
       const float w1 = iS * iK;  // units of D1
       float iR;
       const float sR = bound_scale(fmaf((float)D * kmax, bS, m->vmax[warp]), kTopRow, iR);
@@ -227,7 +333,7 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
       tc::tmem_st_wait();
       if (meet()) break;
       if (warp == 0 && elect_one()) {
-        const uint64_t fm = tc::kmajor_desc(fac, C, 0);
+        const uint64_t fm = tc::kmajor_desc(rec, C, 0);
 #pragma unroll
         for (int s = 0; s < 4; s++) tc::mma_f16_ts(tbase + T_D2, tbase + T_R + 8 * s, fm + step64(s), id64, s > 0);
         tc::mma_commit(bar(m->mma2));
@@ -270,7 +376,7 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
         tc::tmem_st_wait();
       }
       const float w3 = iU * iR * iK;  // units of dS
-      m->o2[ph][r] = a.scale * w3 * m->inv_q[c % 3];
+      m->o2[ph][r] = a.scale * w3 * inv[1];
       if (meet()) break;
       if (warp == 0 && elect_one()) {
         const uint64_t kt = tc::mnmajor_desc(tile, 128, 0);
@@ -278,14 +384,14 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
         for (int s = 0; s < 4; s++) tc::mma_f16_ts(tbase + T_DS, tbase + T_CU + 8 * s, kt + step_mn(s), idKN, s > 0);
         tc::mma_commit(bar(m->mma3));
       }
-      warp_arrive(m->u_ready);
+      warp_arrive(m->u_ready);  // (and the record has been read)
       // the state after the chunk
       const u64 w3_2 = pack2(w3, w3);
       // 64 products of |c u| <= |u| and |k| bound what is added
-      bS = fmaf(-nf[C - 1], bS, (float)C * uU * iR * kmax);
+      bS = fmaf(all, bS, (float)C * uU * iR * kmax);
       const float sS = bound_scale(bS, kTopRow, iS);
       const u64 sS2 = pack2(sS, sS);
-      const u64 dec = pack2(-nf[C - 1], -nf[C - 1]);
+      const u64 dec = pack2(all, all);
       ok &= wait(bar(m->mma3), ph, limit, gave_up);
       tc::fence_after_sync();
       if (r == 0) mbar_arrive(bar(m->tile_free[c % 3]));
@@ -360,23 +466,24 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
           break;
         }
       }
-      bool got = wait(bar(m->u_ready), c & 1, limit, gave_up);
+      bool got = wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
+      got &= wait(bar(m->u_ready), c & 1, limit, gave_up);
       got = __all_sync(0xffffffffu, got);
       tc::fence_after_sync();
       if (warp == 4 && got && elect_one()) {  // U P^T
-        const uint64_t pd = tc::kmajor_desc(tc::smem_u32(sm + CH_FAC + 2 * SQ * (c & 1) + SQ), C, 0);
+        const uint64_t pd = tc::kmajor_desc(tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD + REC_P), C, 0);
 #pragma unroll
         for (int s = 0; s < 4; s++) tc::mma_f16_ts(tbase + T_O2, tbase + T_U + 8 * s, pd + step64(s), id64, s > 0);
-        tc::mma_commit(bar(m->mma4[c & 1]));
+        tc::mma_commit(bar(m->mma4));
       }
-      got &= wait(bar(m->mma4[c & 1]), (c >> 1) & 1, limit, gave_up);
+      got &= wait(bar(m->mma4), c & 1, limit, gave_up);
       if (h == 0) tc::bulk_wait_read();  // the last chunk's output has left its buffer
       if (group_or(2, 128, !got)) {
         ok = false;
         break;
       }
       tc::fence_after_sync();
-      const float *nf = m->nf[c & 3];
+      const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F);
       const float o1 = m->o1[c & 1][h], o2 = m->o2[c & 1][h];
       const u64 w1 = pack2(o1, o1), w2 = pack2(o2, o2);
       __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(sm + CH_OUT) + h;
@@ -413,75 +520,16 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
         bulk_s2g((__nv_bfloat16 *)a.out + ((size_t)u * T + (size_t)c * C) * D, tc::smem_u32(sm + CH_OUT),
                  (uint32_t)min(C, T - c * C) * D * 2);
         tc::bulk_commit();
+        if (c + 3 < NC) fetch_rec(c + 3);  // (the chain is past this record, and so is the group)
       }
+      if (c + 3 < NC) rec_sent++;
     }
     if (!(sum2(nonfinite) == 0.0f)) atomicOr(a.status, tc::kErrNonFinite);
     if (h == 0) tc::bulk_wait_all();
-  } else if (warp < 12) {
-    // ---- the factors, one chunk ahead of the chain ----
-    regs_down<kRegFactor>();
-    const int h = tid - 256, w = warp - 8;
-    Factor &s = *reinterpret_cast<Factor *>(sm + CH_SCR);
-    for (int b = 0; b < 4; b++) factor_clear(sm + CH_FAC + SQ * b, h);
-    const size_t g0 = (size_t)u * T;
-    // the next chunk's gates: gamma in warp 3, beta in warps 0 and 1
-    float2 ga;
-    float be = 0.0f;
-    auto load_gates = [&](int c) {
-      const int n = T - c * C;
-      const float *gp = a.gamma + g0 + (size_t)c * C, *bp = a.beta + g0 + (size_t)c * C;
-      if (w == 3) ga = make_float2(2 * lane < n ? gp[2 * lane] : 1.0f, 2 * lane + 1 < n ? gp[2 * lane + 1] : 1.0f);
-      if (w < 2) be = h < n ? bp[h] : 0.0f;
-    };
-    const uint32_t id64 = tc::idesc_f16(128, C, false, false);
-    auto begin = [&](int c) {  // warp 3: [K K^T; Q K^T] of chunk c, and its decays while that runs
-      const bool got = wait(bar(m->tile_full[c % 3]), (c / 3) & 1, limit, gave_up);
-      tc::fence_after_sync();
-      if (__all_sync(0xffffffffu, got) && elect_one()) {
-        const uint64_t t = tc::kmajor_desc(tc::smem_u32(sm + CH_TILE + (c % 3) * TILE), 128, 0);
-#pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_D0, t + step128(s), t + step128(s), id64, s > 0);
-        tc::mma_commit(bar(m->d0_full));
-      }
-      __syncwarp();
-      factor_gates(s, gate_scan(ga, lane), m->nf[c & 3], m->c[c & 3], lane);
-    };
-    load_gates(0);
-    if (w == 3) begin(0);
-    for (int c = 0; c < NC; c++) {
-      const int b = c & 1;
-      uint8_t *M = sm + CH_FAC + 2 * SQ * b, *P = M + SQ;
-      const float be_now = be;
-      if (c + 1 < NC) load_gates(c + 1);
-      // slot b of M and P is free once the readout product of chunk c - 2 is done (and slot c % 4
-      // of the decays: that product came after the readout of chunk c - 4)
-      bool got = c < 2 || wait(bar(m->mma4[b]), ((c >> 1) - 1) & 1, limit, gave_up);
-      got &= wait(bar(m->tile_full[c % 3]), (c / 3) & 1, limit, gave_up);
-      got &= wait(bar(m->d0_full), c & 1, limit, gave_up);
-      if (group_or(3, 128, !got)) {
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
-      if (w < 2) s.beta[h] = be_now;
-      factor_rows(s, tbase + T_D0, m->inv_k[c % 3] * m->inv_k[c % 3], P, h);
-      tc::fence_before_sync();
-      group_or(3, 128, false);
-      factor_diagonal<true>(s, M, w, lane);
-      group_or(3, 128, false);
-      tc::fence_after_sync();
-      if (w < 3) {
-        factor_columns<true>(s, M, w, lane);
-      } else if (c + 1 < NC) {  // (the last column block has nothing below its diagonal block)
-        begin(c + 1);
-      }
-      tc::fence_smem_to_async();
-      warp_arrive(m->fac_full[b]);
-    }
   } else {
     // ---- K and Q as operands, up to three chunks in flight ----
     regs_down<kRegConvert>();
-    const int h = tid - 384, r0 = h >> 4, c8 = h & 15, uk = a.qk_unit(u);  // rows r0, r0 + 8 ..; 8 channels
+    const int h = tid - 256, r0 = h >> 4, c8 = h & 15, uk = a.qk_unit(u);  // rows r0, r0 + 8 ..; 8 channels
     const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + ((size_t)uk * T + r0) * D + 8 * c8;
     const __nv_bfloat16 *qp = (const __nv_bfloat16 *)a.q + ((size_t)uk * T + r0) * D + 8 * c8;
     uint4 x[8], y[8];  // the next chunk's rows, on their way while this one's are converted
@@ -498,34 +546,14 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
     };
     load(0);
     for (int c = 0; c < NC; c++) {
-      uint32_t mk = 0, mq = 0;
-#pragma unroll
-      for (int k = 0; k < 8; k++) {
-        mk = absmax_words(mk, x[k]);
-        mq = absmax_words(mq, y[k]);
-      }
-      mk = absmax_fold(mk);
-      mq = absmax_fold(mq);
-      uint32_t *red = m->red + 8 * (c & 1);
-      if (lane == 0) {
-        red[warp - 12] = mk;
-        red[warp - 8] = mq;
-      }
-      bool got = true;
-      if (c >= 3) got = wait(bar(m->tile_free[c % 3]), (c / 3 - 1) & 1, limit, gave_up);
-      if (group_or(4, 128, !got)) {
+      bool got = wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
+      if (c >= 3) got &= wait(bar(m->tile_free[c % 3]), (c / 3 - 1) & 1, limit, gave_up);
+      if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
       }
-      const uint4 k4 = *reinterpret_cast<const uint4 *>(red), q4 = *reinterpret_cast<const uint4 *>(red + 4);
-      float ik, iq;
-      const float sk = bound_scale(__uint_as_float(max(max(k4.x, k4.y), max(k4.z, k4.w)) << 16), kTopTile, ik);
-      const float sq = bound_scale(__uint_as_float(max(max(q4.x, q4.y), max(q4.z, q4.w)) << 16), kTopTile, iq);
-      if (h == 0) {
-        m->inv_k[c % 3] = ik;
-        m->inv_q[c % 3] = iq;
-      }
-      const u64 sk2 = pack2(sk, sk), sq2 = pack2(sq, sq);
+      const float4 inv = *reinterpret_cast<const float4 *>(sm + CH_REC + (c % 3) * REC_PAD + REC_C + 4 * C);
+      const u64 sk2 = pack2(inv.z, inv.z), sq2 = pack2(inv.w, inv.w);
       uint8_t *dst = sm + CH_TILE + (c % 3) * TILE + tile_off(r0, c8, 128);
 #pragma unroll
       for (int k = 0; k < 8; k++) {
@@ -542,14 +570,18 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
   // a wait gave up: products and copies still in flight finish before the memory is released
   if (*gave_up) {
     // (a product's commit counts for the thread that issued it: the same elected lane)
-    if ((warp == 0 || warp == 4 || warp == 8) && elect_one()) tc::mma_commit(bar(m->drain));
+    if ((warp == 0 || warp == 4) && elect_one()) tc::mma_commit(bar(m->drain));
     if (tid == 0) {
       unsigned bits = tc::kErrMmaTimeout;
       if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
       atomicOr(a.status, bits);
     }
-    if (tid == 128 && !tc::mbar_wait(bar(m->v_full), (v_sent - 1) & 1, tc::kWaitLimit))
-      atomicOr(a.status, tc::kErrDrainTimeout);
+    if (tid == 128) {
+      bool in = tc::mbar_wait(bar(m->v_full), (v_sent - 1) & 1, tc::kWaitLimit);
+      for (int c = max(0, rec_sent - 3); c < rec_sent; c++)
+        in &= tc::mbar_wait(bar(m->rec_full[c % 3]), (c / 3) & 1, tc::kWaitLimit);
+      if (!in) atomicOr(a.status, tc::kErrDrainTimeout);
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -558,14 +590,28 @@ __global__ void __launch_bounds__(512, 1) mesa_rule_chain_kernel(RuleArgs a, con
 
 }  // namespace
 
-int launch_rule_forward_tc(const RuleArgs &a, cudaStream_t st) {
+size_t rule_tc_workspace(int U, int T) {
+  return (size_t)U * (((size_t)T + C - 1) / C) * REC;
+}
+
+int launch_rule_prep(const RuleArgs &a, void *records, bool with_beta, cudaStream_t st) {
+  auto kfn = with_beta ? mesa_rule_prep_kernel<true> : mesa_rule_prep_kernel<false>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PR_SMEM) != cudaSuccess) return -1;
+  timing_mark_begin(K_RULE_PREP, st);
+  kfn<<<dim3((a.T + C - 1) / C, a.units()), 128, PR_SMEM, st>>>(a, (uint8_t *)records);
+  timing_mark_end(K_RULE_PREP, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st) {
   CUtensorMap mapV{};
   if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T)) return -1;
   if (cudaFuncSetAttribute(mesa_rule_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CH_SMEM) !=
       cudaSuccess)
     return -1;
+  if (launch_rule_prep(a, workspace, true, st) != 0) return -1;
   timing_mark_begin(K_RULE_CHAIN, st);
-  mesa_rule_chain_kernel<<<a.units(), 512, CH_SMEM, st>>>(a, mapV);
+  mesa_rule_chain_kernel<<<a.units(), 384, CH_SMEM, st>>>(a, (const uint8_t *)workspace, mapV);
   timing_mark_end(K_RULE_CHAIN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

@@ -31,6 +31,10 @@ constexpr int C = 64, D = 128;               // tokens per chunk; dk = dv
 constexpr uint32_t TILE = 2 * C * D * 2;     // [128 x 128] operand: K rows, then Q rows
 constexpr uint32_t SQ = C * C * 2;           // [64 x 64] operand
 constexpr uint32_t ROWS64 = C * D * 2;       // 64 rows of bf16
+// A chunk's record: the factor T or T diag(beta) and P = Q K^T o D, swizzled K-major operands, then
+// minus f, c, and {1 / scale of K, of Q, scale of K, of Q}.  REC_PAD: its place in shared memory.
+constexpr uint32_t REC_P = SQ, REC_F = 2 * SQ, REC_C = REC_F + 4 * C, REC = REC_C + 4 * C + 128, REC_PAD = 17 * 1024;
+static_assert(REC % 16 == 0 && REC <= REC_PAD, "records are bulk copied");
 __device__ __forceinline__ float half2_bits(float a, float b) {  // two fp16 values as a 32-bit register
   const __half2 h = __floats2half2_rn(a, b);
   return __uint_as_float(*reinterpret_cast<const uint32_t *>(&h));
@@ -147,6 +151,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// One lane of a converged warp.  The products' operands are warp-uniform registers: behind a plain
+// thread test (not this, under a warp-uniform condition) each product took 130 cycles to issue,
+// whatever its size; so, 56 (N = 64) to 74 (N = 128).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+// K-step s of 16 added to a K-major descriptor of a 128-row tile, of a 64-row tile with 64 columns, and
+// to an MN-major one, in the descriptor's 16-byte units.
+__device__ __forceinline__ uint64_t step128(int s) { return (uint64_t)((s >> 2) * 1024 + (s & 3) * 2); }
+__device__ __forceinline__ uint64_t step64(int s) { return (uint64_t)(2 * s); }
+__device__ __forceinline__ uint64_t step_mn(int s) { return (uint64_t)(128 * s); }
 
 // ---- the factors of a chunk, by 128 threads ------------------------------------------------------
 struct Factor {
