@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint
   PrepMisc *m = reinterpret_cast<PrepMisc *>(sm + PR_MISC);
   Factor &s = *reinterpret_cast<Factor *>(sm + PR_SCR);
   uint8_t *rec = sm + PR_REC;
-  float *nf = reinterpret_cast<float *>(rec + REC_F), *cc = nf + C, *inv = cc + C;
+  float *nf = reinterpret_cast<float *>(rec + REC_F), *cc = nf + C, *inv = reinterpret_cast<float *>(rec + REC_S);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int c = blockIdx.x, u = blockIdx.y, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
   const size_t row0 = (size_t)a.qk_unit(u) * a.T + t0, tok0 = (size_t)u * a.T + t0;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint
     tc::drain_mmas(tc::smem_u32(&m->drain), issuer, a.status);
   } else {
     if (tid == 0) *reinterpret_cast<float4 *>(inv) = make_float4(ik, iq, sk, sq);
-    if (tid < C) s.beta[tid] = be;
+    if (tid < C) s.beta[tid] = reinterpret_cast<float *>(rec + REC_B)[tid] = be;
     if (warp == 3) factor_gates(s, g, nf, cc, lane);
     factor_clear(rec, tid);
     factor_clear(rec + SQ, tid);
@@ -165,6 +165,12 @@ constexpr uint32_t T_R = T_D1, T_CU = T_D1, T_U = T_D1 + 32;  // two values a co
 // channel; permuted so that neither the writes nor a warp's reads of 32 channels meet in a bank).
 __device__ __forceinline__ uint32_t vt_off(int r, int ch) { return (uint32_t)(r * 256 + ((ch ^ (r & 7)) << 4)); }
 
+__device__ __forceinline__ uint32_t bf2_bits(u64 x) {  // two bf16 values
+  float a, b;
+  unpack2(x, a, b);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -186,7 +192,8 @@ __device__ __forceinline__ void regs_down() {
 
 // grid U, 384 threads: warps 0-3 chain, 4-7 helper, 8-11 convert.
 __global__ void __launch_bounds__(384, 1)
-    mesa_rule_chain_kernel(RuleArgs a, const uint8_t *records, const __grid_constant__ CUtensorMap mapV) {
+    mesa_rule_chain_kernel(RuleArgs a, const uint8_t *records, const __grid_constant__ CUtensorMap mapV,
+                           const __grid_constant__ CUtensorMap mapO) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   ChainMisc *m = reinterpret_cast<ChainMisc *>(sm + CH_MISC);
@@ -284,7 +291,8 @@ __global__ void __launch_bounds__(384, 1)
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1, tile = tc::smem_u32(sm + CH_TILE + (c % 3) * TILE),
                      rec = tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD);
-      const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F), *cc = nf + C, *inv = cc + C;
+      const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F), *cc = nf + C,
+                  *inv = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_S);
       ok &= wait(bar(m->tile_full[c % 3]), (c / 3) & 1, limit, gave_up);
       if (c > 0) ok &= wait(bar(m->o_free), (c - 1) & 1, limit, gave_up);  // (the last readout is read)
       if (meet()) break;
@@ -484,41 +492,49 @@ __global__ void __launch_bounds__(384, 1)
       }
       tc::fence_after_sync();
       const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F);
-      const float o1 = m->o1[c & 1][h], o2 = m->o2[c & 1][h];
-      const u64 w1 = pack2(o1, o1), w2 = pack2(o2, o2);
-      __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(sm + CH_OUT) + h;
-      float x[64];  // from S0: all at once, the chain's next product writes there
-      tc::tmem_ld32(tl + T_O1, *reinterpret_cast<float(*)[32]>(x));
-      tc::tmem_ld32(tl + T_O1 + 32, *reinterpret_cast<float(*)[32]>(x + 32));
+      // 16 channels at a time in fragments of 8 tokens (this thread: channels T / 4 and T / 4 + 8, tokens
+      // 2 (T % 4) and the next of each 8), transposed into the swizzled output tile
+      float x[2][32];  // from S0: all at once, the chain's next product writes there
+      tmem_ld_frag64(tl + T_O1, x[0]);
+      tmem_ld_frag64(tl + (16u << 16) + T_O1, x[1]);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       warp_arrive(m->o_free);
+      const int w = warp - 4, q = 2 * (lane & 3);
 #pragma unroll
-      for (int g = 0; g < 4; g++) {
-        float y[16];
-        tc::tmem_ld16(tl + T_O2 + 16 * g, y);
-        ulonglong2 ff[4];
-#pragma unroll
-        for (int k = 0; k < 4; k++) ff[k] = *reinterpret_cast<const ulonglong2 *>(nf + 16 * g + 4 * k);
+      for (int hf = 0; hf < 2; hf++) {
+        float y[32];
+        tmem_ld_frag64(tl + ((uint32_t)(16 * hf) << 16) + T_O2, y);
+        const int ch = 32 * w + 16 * hf + (lane >> 2);
+        const u64 a1 = pack2(m->o1[c & 1][ch], m->o1[c & 1][ch]), a2 = pack2(m->o2[c & 1][ch], m->o2[c & 1][ch]);
+        const u64 b1 = pack2(m->o1[c & 1][ch + 8], m->o1[c & 1][ch + 8]),
+                  b2 = pack2(m->o2[c & 1][ch + 8], m->o2[c & 1][ch + 8]);
+        // rows of the four blocks of a store: tokens 16 p + 8 (lane / 16) + lane % 8, channels + 8 ((lane / 8) % 2)
+        const int tk = 8 * (lane >> 4) + (lane & 7), c8 = 4 * w + 2 * hf + ((lane >> 3) & 1);
         tc::tmem_ld_wait();
+        const float *z = x[hf];
 #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const u64 o = fma2(pack2(x[16 * g + k], x[16 * g + k + 1]), mul2(k & 2 ? ff[k / 4].y : ff[k / 4].x, w1),
-                             mul2(pack2(y[k], y[k + 1]), w2));
-          nonfinite = fma2(o, 0ull, nonfinite);
-          float p, q;
-          unpack2(o, p, q);
-          const __nv_bfloat162 b = __floats2bfloat162_rn(p, q);
-          dst[(16 * g + k) * D] = b.x;
-          dst[(16 * g + k + 1) * D] = b.y;
+        for (int p = 0; p < 4; p++) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const int j = 8 * p + 4 * e;
+            const u64 ff = *reinterpret_cast<const u64 *>(nf + 16 * p + 8 * e + q);
+            const u64 oa = fma2(pack2(z[j], z[j + 1]), mul2(ff, a1), mul2(pack2(y[j], y[j + 1]), a2));
+            const u64 ob = fma2(pack2(z[j + 2], z[j + 3]), mul2(ff, b1), mul2(pack2(y[j + 2], y[j + 3]), b2));
+            nonfinite = fma2(oa, 0ull, fma2(ob, 0ull, nonfinite));
+            o[2 * e] = bf2_bits(oa);
+            o[2 * e + 1] = bf2_bits(ob);
+          }
+          stmatrix_x4_trans(tc::smem_u32(sm + CH_OUT + tile_off(16 * p + tk, c8, C)), o[0], o[1], o[2], o[3]);
         }
       }
       tc::fence_before_sync();
       tc::fence_smem_to_async();
       group_or(2, 128, false);
       if (h == 0) {
-        bulk_s2g((__nv_bfloat16 *)a.out + ((size_t)u * T + (size_t)c * C) * D, tc::smem_u32(sm + CH_OUT),
-                 (uint32_t)min(C, T - c * C) * D * 2);
+#pragma unroll
+        for (int b = 0; b < 2; b++) tensor_s2g_3d(&mapO, tc::smem_u32(sm + CH_OUT + b * C * 128), 64 * b, c * C, u);
         tc::bulk_commit();
         if (c + 3 < NC) fetch_rec(c + 3);  // (the chain is past this record, and so is the group)
       }
@@ -552,7 +568,7 @@ __global__ void __launch_bounds__(384, 1)
         ok = false;
         break;
       }
-      const float4 inv = *reinterpret_cast<const float4 *>(sm + CH_REC + (c % 3) * REC_PAD + REC_C + 4 * C);
+      const float4 inv = *reinterpret_cast<const float4 *>(sm + CH_REC + (c % 3) * REC_PAD + REC_S);
       const u64 sk2 = pack2(inv.z, inv.z), sq2 = pack2(inv.w, inv.w);
       uint8_t *dst = sm + CH_TILE + (c % 3) * TILE + tile_off(r0, c8, 128);
 #pragma unroll
@@ -604,14 +620,14 @@ int launch_rule_prep(const RuleArgs &a, void *records, bool with_beta, cudaStrea
 }
 
 int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st) {
-  CUtensorMap mapV{};
-  if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T)) return -1;
+  CUtensorMap mapV{}, mapO{};
+  if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T) || !tmap_units128_bf16(&mapO, a.out, a.units(), a.T)) return -1;
   if (cudaFuncSetAttribute(mesa_rule_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CH_SMEM) !=
       cudaSuccess)
     return -1;
   if (launch_rule_prep(a, workspace, true, st) != 0) return -1;
   timing_mark_begin(K_RULE_CHAIN, st);
-  mesa_rule_chain_kernel<<<a.units(), 384, CH_SMEM, st>>>(a, (const uint8_t *)workspace, mapV);
+  mesa_rule_chain_kernel<<<a.units(), 384, CH_SMEM, st>>>(a, (const uint8_t *)workspace, mapV, mapO);
   timing_mark_end(K_RULE_CHAIN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

@@ -32,8 +32,9 @@ constexpr uint32_t TILE = 2 * C * D * 2;     // [128 x 128] operand: K rows, the
 constexpr uint32_t SQ = C * C * 2;           // [64 x 64] operand
 constexpr uint32_t ROWS64 = C * D * 2;       // 64 rows of bf16
 // A chunk's record: the factor T or T diag(beta) and P = Q K^T o D, swizzled K-major operands, then
-// minus f, c, and {1 / scale of K, of Q, scale of K, of Q}.  REC_PAD: its place in shared memory.
-constexpr uint32_t REC_P = SQ, REC_F = 2 * SQ, REC_C = REC_F + 4 * C, REC = REC_C + 4 * C + 128, REC_PAD = 17 * 1024;
+// minus f, c, beta, and {1 / scale of K, of Q, scale of K, of Q}.  REC_PAD: its place in shared memory.
+constexpr uint32_t REC_P = SQ, REC_F = 2 * SQ, REC_C = REC_F + 4 * C, REC_B = REC_C + 4 * C, REC_S = REC_B + 4 * C,
+                   REC = REC_S + 128, REC_PAD = 18 * 1024;
 static_assert(REC % 16 == 0 && REC <= REC_PAD, "records are bulk copied");
 __device__ __forceinline__ float half2_bits(float a, float b) {  // two fp16 values as a 32-bit register
   const __half2 h = __floats2half2_rn(a, b);
@@ -165,6 +166,35 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint64_t step128(int s) { return (uint64_t)((s >> 2) * 1024 + (s & 3) * 2); }
 __device__ __forceinline__ uint64_t step64(int s) { return (uint64_t)(2 * s); }
 __device__ __forceinline__ uint64_t step_mn(int s) { return (uint64_t)(128 * s); }
+
+// 64 columns of 16 tensor-memory lanes as 8-column fragments: for columns 8 j .. 8 j + 7 this thread gets
+// lane T / 4, columns 2 (T % 4) and the next, in r[4 j], r[4 j + 1]; lane T / 4 + 8 in the next two.
+__device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
+}
+// Four 8 x 8 blocks of 16-bit fragments to shared memory, transposed: lane l gives the address of row
+// l % 8 (the fragments' column) of block l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+// Tiled store of a box of a 3-D tensor map; tokens past the end are not written.
+__device__ __forceinline__ void tensor_s2g_3d(const void *map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(map), "r"(src),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 
 // ---- the factors of a chunk, by 128 threads ------------------------------------------------------
 struct Factor {
