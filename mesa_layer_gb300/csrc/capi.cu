@@ -208,13 +208,14 @@ const char *mesa_kernel_name(int kind) {
     case mesa::K_CARRY_TC: return "mesa_carry_tc_kernel";
     case mesa::K_BWD_SPROD: return "mesa_bwd_sprod_tc_kernel";
     case mesa::K_RULE_SCAN: return "mesa_rule_scan_kernel";
-    case mesa::K_RULE_GRADS: return "mesa_rule_grads_kernel";
+    case mesa::K_RULE_GRADS: return "mesa_rule_grads_kernel|mesa_rule_grads_tc_kernel";
     case mesa::K_RULE_GROUP: return "mesa_rule_group_sum_kernel";
     case mesa::K_RULE_STEP: return "mesa_rule_step_kernel";
     case mesa::K_NORM: return "mesa_block_norm_kernel";
     case mesa::K_NORM_BWD: return "mesa_block_norm_bwd_kernel";
     case mesa::K_RULE_PREP: return "mesa_rule_prep_kernel";
     case mesa::K_RULE_CHAIN: return "mesa_rule_chain_kernel";
+    case mesa::K_RULE_ADJOINT: return "mesa_rule_adjoint_kernel";
     case mesa::K_NORM_COLS: return "mesa_block_norm_cols_kernel";
   }
   return nullptr;

@@ -47,6 +47,22 @@ size_t backward_parts(int B, int H, int Hk, int T, int dk, int dv, size_t *off) 
   return at;
 }
 
+// Backward workspace of the tensor-core path: [status | records | S | A | u | du | their scales (4) |
+// per-head dq, dk].
+constexpr int kTcParts = 10;
+size_t backward_tc_parts(int B, int H, int Hk, int T, size_t *off) {
+  const size_t U = (size_t)B * H, n = U * (((size_t)T + 63) / 64);
+  const size_t part = Hk != H ? U * T * 128 * sizeof(float) : 0;
+  const size_t sizes[kTcParts + 1] = {mesa::rule_tc_workspace(B * H, T), n * 32768, n * 32768, n * 16384, n * 16384,
+                                      n * 4, n * 4, n * 4, n * 4, part, part};
+  size_t at = kStatusBytes;
+  for (int i = 0; i <= kTcParts; i++) {
+    off[i] = at;
+    at += align256(sizes[i]);
+  }
+  return at;
+}
+
 }  // namespace
 
 extern "C" {
@@ -90,8 +106,8 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
 
 size_t mesa_delta_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   if (check_sizes(B, H, Hk, T, dk, dv, dtype, 1.0f) != MESA_OK) return 0;
-  size_t off[kBwdParts];
-  return backward_parts(B, H, Hk, T, dk, dv, off);
+  size_t off[kTcParts + 1];
+  return rule_tc(dtype, dk, dv) ? backward_tc_parts(B, H, Hk, T, off) : backward_parts(B, H, Hk, T, dk, dv, off);
 }
 
 int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,
@@ -114,9 +130,10 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
   }
   if (!q || !k || !v || !gamma || !beta || !dout || !dq || !dk_out || !dv_out || !dgamma || !dbeta)
     return MESA_ERR_INVALID_ARG;
-  size_t off[kBwdParts];
-  if (!workspace || workspace_bytes < backward_parts(B, H, Hk, T, dk, dv, off) || ((uintptr_t)workspace & 255))
-    return MESA_ERR_WORKSPACE;
+  size_t off[kTcParts + 1];
+  const bool tc = rule_tc(dtype, dk, dv);
+  const size_t need = tc ? backward_tc_parts(B, H, Hk, T, off) : backward_parts(B, H, Hk, T, dk, dv, off);
+  if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255)) return MESA_ERR_WORKSPACE;
   char *w = (char *)workspace;
   mesa::RuleArgs a{B, H, Hk, T, dk, dv, dtype, q, k, v, gamma, beta, scale};
   a.S0 = S0;
@@ -130,10 +147,21 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
   a.dS0 = dS0;
   a.status = (unsigned *)workspace;
   a.wait_limit = mesa::wait_limit();
+  if (cudaMemsetAsync(a.status, 0, sizeof(unsigned), stream) != cudaSuccess) return MESA_ERR_CUDA;
+  if (tc) {
+    auto f = [&](int i) { return (float *)(w + off[i]); };
+    auto b8 = [&](int i) { return (uint8_t *)(w + off[i]); };
+    const mesa::RuleOperands so{b8(1), b8(3), f(5), f(6)}, ao{b8(2), b8(4), f(7), f(8)};
+    const bool ok = mesa::launch_rule_prep(a, b8(0), false, stream) == 0 &&
+                    mesa::launch_rule_states_tc(a, b8(0), so, stream) == 0 &&
+                    mesa::launch_rule_adjoint_tc(a, b8(0), ao, stream) == 0 &&
+                    mesa::launch_rule_grads_tc(a, b8(0), so, ao, Hk != H ? f(9) : nullptr, Hk != H ? f(10) : nullptr,
+                                               stream) == 0;
+    return ok ? MESA_OK : MESA_ERR_CUDA;
+  }
   mesa::RuleBwdWorkspace ws{(float *)(w + off[0]), (float *)(w + off[1]), (float *)(w + off[2]),
                             (float *)(w + off[3]), Hk != H ? (float *)(w + off[4]) : nullptr,
                             Hk != H ? (float *)(w + off[5]) : nullptr};
-  if (cudaMemsetAsync(a.status, 0, sizeof(unsigned), stream) != cudaSuccess) return MESA_ERR_CUDA;
   return mesa::launch_rule_backward(a, ws, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
 }
 

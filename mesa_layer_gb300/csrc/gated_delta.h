@@ -51,9 +51,21 @@ int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStre
 int launch_rule_step(const RuleStepArgs &a, cudaStream_t st);
 // The tensor-core path (bf16, dk = dv = 128): workspace bytes, the chunks' records (with_beta: the
 // forward's), the forward.
+// What the two chains of the backward pass keep, as fp16 operands of 64-token chunks, each with 1 /
+// its scale: states (or their adjoints) S [U, NC][128 x 128] and u (or du) U [U, NC][64 x 128].
+struct RuleOperands {
+  uint8_t *S = nullptr, *U = nullptr;
+  float *iS = nullptr, *iU = nullptr;
+};
 size_t rule_tc_workspace(int U, int T);
 int launch_rule_prep(const RuleArgs &a, void *records, bool with_beta, cudaStream_t st);
 int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st);
+// The backward on the tensor cores, from the records (without beta): the states and u before the
+// adjoint chain, the adjoint chain, the gradients.
+int launch_rule_states_tc(const RuleArgs &a, const void *records, const RuleOperands &so, cudaStream_t st);
+int launch_rule_adjoint_tc(const RuleArgs &a, const void *records, const RuleOperands &ao, cudaStream_t st);
+int launch_rule_grads_tc(const RuleArgs &a, const void *records, const RuleOperands &so, const RuleOperands &ao,
+                         float *dqp, float *dkp, cudaStream_t st);
 // dq, dk [B, Hk, T, dk] = sums of the per-unit fp32 parts over the value heads of a key head.
 int launch_rule_group_sum(const RuleArgs &a, const float *dqp, const float *dkp, cudaStream_t st);
 

@@ -1,0 +1,840 @@
+// gated_delta_bwd_tc.cu -- the gated delta rule's backward on the tensor cores (bf16, dk = dv = 128;
+// the chunk algebra, the records and the operand formats are in gated_delta_tc.cuh).
+//
+// After the records (T without beta) and a pass over the states (mesa_rule_chain_kernel<false>, which
+// keeps the state S0 before each chunk and the chunk's u), two kernels:
+//  - mesa_rule_adjoint_kernel, one CTA per unit, walks the chunks backwards with the adjoint A of the
+//    state after the chunk in registers, like the forward's chain (g = dL/do, scale in P and Q):
+//        R' = (c A K^T + g^T P),   du = R' T,   A <- f_last A + g^T (f Q) - (beta f du)^T K;
+//  - mesa_rule_grads_tc_kernel, one CTA per chunk, takes every gradient from S0, A, u, du and the
+//    chunk's rows:
+//        W = g u^T o D, V = beta du u^T o D (strictly lower),
+//        dq = f (g S0) + W K,   dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0),
+//        dv = beta du,          dbeta = du . (v - f S0 k - sum_j D_ij (k_i . k_j) u_j),
+//        dgamma_t: every pair (reader i >= t or the state after, writer j < t or the state before)
+//        that the gate separates, with the decay between them but for gamma_t's own.
+// States, adjoints, u and du go through memory as fp16 operands with one scale a chunk: what
+// bounds the path is that traffic and the two chains' latency.
+#include "gated_delta_tc.cuh"
+
+namespace mesa {
+
+using namespace rule;
+
+namespace {
+
+constexpr int kRegChain = 240, kRegHelper = 112, kRegConvert = 144;
+static_assert(kRegChain + kRegHelper + kRegConvert <= 3 * 168, "register file");
+
+// ---- the adjoint chain ----------------------------------------------------------------------------
+// shared memory: three records | two operand tiles (K, f Q) | two g tiles | kept adjoint | du | misc
+constexpr uint32_t AD_REC = 0, AD_TILE = 3 * REC_PAD, AD_G = AD_TILE + 2 * TILE, AD_STAGE = AD_G + 2 * ROWS64;
+constexpr uint32_t AD_OUT = AD_STAGE + TILE, AD_MISC = AD_OUT + ROWS64;
+struct AdjointMisc {
+  float iR[2][D];             // units of D2, by row
+  float bmax[4], umax[2][4];  // by chain warp: bounds of the adjoint, of |du|
+  alignas(16) uint32_t red[8];
+  float ig[2];                // 1 / scale of the g tiles
+  uint64_t tile_full[2], tile_free[2], rec_full[3], r_ready, u_ready, o_free, upd, dp_full, dq_full;
+  uint64_t mma1, mma2, mma3, drain;
+  uint32_t tmem;
+  int gave_up;
+};
+constexpr uint32_t AD_SMEM = AD_MISC + sizeof(AdjointMisc) + 1024;
+static_assert(AD_SMEM <= 232448, "shared memory per block");
+// tensor memory columns: (beta f du) K | g^T (f Q) | A operand | D1 (then R', then -beta f du) | g^T P | D2
+constexpr uint32_t T_DS = 0, T_DQ = 128, T_S = 256, T_D1 = 320, T_DP = 384, T_D2 = 448;
+constexpr uint32_t T_R = T_D1, T_CU = T_D1;
+
+// grid U, 384 threads: warps 0-3 chain (thread r: row r of A), 4-7 write du, 8-11 convert.
+__global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, const uint8_t *records, RuleOperands ao) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  AdjointMisc *m = reinterpret_cast<AdjointMisc *>(sm + AD_MISC);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // (warp: uniform)
+  const int u = blockIdx.x, T = a.T, NC = (T + C - 1) / C;
+  auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
+  volatile int *gave_up = &m->gave_up;
+  const unsigned limit = a.wait_limit;
+  // step it works on chunk NC - 1 - it
+  auto fetch_rec = [&](int it) {
+    const uint32_t b = bar(m->rec_full[it % 3]);
+    tc::mbar_arrive_expect_tx(b, REC);
+    tc::bulk_g2s(tc::smem_u32(sm + AD_REC + (it % 3) * REC_PAD), records + ((size_t)u * NC + NC - 1 - it) * REC, REC, b);
+  };
+  if (warp == 0) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
+  if (tid == 128) {
+    for (uint64_t *b : {&m->tile_full[0], &m->tile_full[1], &m->r_ready, &m->u_ready, &m->o_free, &m->upd})
+      tc::mbar_init(bar(*b), 4);
+    for (uint64_t *b : {&m->tile_free[0], &m->tile_free[1], &m->rec_full[0], &m->rec_full[1], &m->rec_full[2], &m->dp_full,
+                        &m->dq_full, &m->mma1, &m->mma2, &m->mma3})
+      tc::mbar_init(bar(*b), 1);
+    tc::mbar_init(bar(m->drain), 2);  // the threads that issue products
+    m->gave_up = 0;
+    for (int it = 0; it < min(NC, 3); it++) fetch_rec(it);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, m->tmem, 0);
+  auto warp_arrive = [&](uint64_t &b) {  // one arrival per warp, after what its lanes did
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
+  bool ok = true;
+  int rec_sent = min(NC, 3);  // fetches issued (thread 128)
+
+  if (warp < 4) {
+    regs_up<kRegChain>();
+    const int r = tid;
+    const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
+    u64 S[D / 2];
+    {
+      const float4 *src = a.dS_final ? reinterpret_cast<const float4 *>(a.dS_final + ((size_t)u * D + r) * D) : nullptr;
+#pragma unroll
+      for (int g = 0; g < D / 4; g++) {
+        const float4 x = src ? src[g] : make_float4(0, 0, 0, 0);
+        S[2 * g] = pack2(x.x, x.y);
+        S[2 * g + 1] = pack2(x.z, x.w);
+      }
+    }
+    float bS, iS;  // a bound of the row's elements; 1 / scale of the operand (the same for all rows)
+    auto row_max = [&]() {
+      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < D / 2; i++) {
+        float p, q;
+        unpack2(S[i], p, q);
+        x[i & 3] = fmaxf(x[i & 3], fmaxf(fabsf(p), fabsf(q)));
+      }
+      bS = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    };
+    auto all_rows = [&]() -> float {  // after a barrier that follows put_rows
+      const float4 x = *reinterpret_cast<const float4 *>(m->bmax);
+      return fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+    };
+    auto put_rows = [&](float b) {
+      const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(b));
+      if (lane == 0) m->bmax[warp] = __uint_as_float(w);
+    };
+    auto keep_words = [&](int k, const float (&v)[8]) {  // columns 16 k .. of this row
+      tc::tmem_st8(tl + T_S + 8 * k, v);
+      *reinterpret_cast<float4 *>(sm + AD_STAGE + tile_off(r, 2 * k, 128)) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(sm + AD_STAGE + tile_off(r, 2 * k + 1, 128)) = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    row_max();
+    put_rows(bS);
+    group_or(1, 128, false);
+    {
+      const float sS = bound_scale(all_rows(), kTopRow, iS);
+      const u64 s2 = pack2(sS, sS);
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = half2_bits(mul2(S[8 * k + i], s2));
+        keep_words(k, v);
+      }
+      tc::tmem_st_wait();
+    }
+    const uint32_t id64 = tc::idesc_f16(128, C, false, false);    // N = 64, B K-major
+    const uint32_t id64n = tc::idesc_f16(128, C, false, true);    // N = 64, B MN-major
+    const uint32_t idKN = tc::idesc_f16(128, D, false, true);     // N = 128, B MN-major
+    auto meet = [&]() -> bool {  // barrier of the chain; true when a wait gave up
+      tc::fence_before_sync();
+      const bool stop = group_or(1, 128, !ok);
+      tc::fence_after_sync();
+      ok &= !stop;
+      return stop;
+    };
+    const float ascale = fabsf(a.scale);
+    for (int it = 0; it < NC; it++) {
+      const uint32_t ph = it & 1, tile = tc::smem_u32(sm + AD_TILE + ph * TILE), rec = tc::smem_u32(sm + AD_REC + (it % 3) * REC_PAD);
+      const float *nf = reinterpret_cast<const float *>(sm + AD_REC + (it % 3) * REC_PAD + REC_F), *cc = nf + C, *be = cc + C;
+      ok &= wait(bar(m->tile_full[ph]), (it >> 1) & 1, limit, gave_up);
+      tc::fence_smem_to_async();
+      if (meet()) break;
+      if (warp == 0 && elect_one()) {
+        const uint64_t kd = tc::kmajor_desc(tile, 128, 0);
+#pragma unroll
+        for (int s = 0; s < 8; s++)  // A K^T
+          tc::mma_f16_ts(tbase + T_D1, tbase + T_S + 8 * s, kd + step128(s), id64, s > 0);
+        tc::mma_commit(bar(m->mma1));
+      }
+      if (r == 32) {  // the adjoint after the chunk
+        const size_t at = (size_t)u * NC + NC - 1 - it;
+        bulk_s2g(ao.S + at * TILE, tc::smem_u32(sm + AD_STAGE), TILE);
+        tc::bulk_commit();
+        ao.iS[at] = iS;
+      }
+      ok &= wait(bar(m->rec_full[it % 3]), (it / 3) & 1, limit, gave_up);
+      const float4 inv = *reinterpret_cast<const float4 *>(sm + AD_REC + (it % 3) * REC_PAD + REC_S);
+      const float iK = inv.x, iQ = inv.y, ig = m->ig[ph], top = (float)(1 << kTopTile);
+      const float kmax = top * iK, qmax = top * iQ, gmax = top * ig, all = -nf[C - 1];  // all: the chunk's decay
+      const float w1 = iS * iK, w2 = a.scale * ig * iK * iQ;  // units of D1 and of g^T P
+      float iR;
+      const float sR = bound_scale((float)D * kmax * fmaf((float)C * gmax * ascale, qmax, bS), kTopRow, iR);
+      m->iR[ph][r] = iR;
+      const u64 w1_2 = pack2(w1 * sR, w1 * sR), w2_2 = pack2(w2 * sR, w2 * sR);
+      ok &= wait(bar(m->dp_full), ph, limit, gave_up);
+      ok &= wait(bar(m->mma1), ph, limit, gave_up);
+      tc::fence_after_sync();
+      // R' = c D1 + g^T P
+#pragma unroll
+      for (int h = 0; h < 4; h++) {
+        float z[16], y[16], v[8];
+        tc::tmem_ld16(tl + T_D1 + 16 * h, z);
+        tc::tmem_ld16(tl + T_DP + 16 * h, y);
+        ulonglong2 ff[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) ff[k] = *reinterpret_cast<const ulonglong2 *>(cc + 16 * h + 4 * k);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          v[2 * k] = half2_bits(fma2(pack2(z[4 * k], z[4 * k + 1]), mul2(ff[k].x, w1_2),
+                                     mul2(pack2(y[4 * k], y[4 * k + 1]), w2_2)));
+          v[2 * k + 1] = half2_bits(fma2(pack2(z[4 * k + 2], z[4 * k + 3]), mul2(ff[k].y, w1_2),
+                                         mul2(pack2(y[4 * k + 2], y[4 * k + 3]), w2_2)));
+        }
+        tc::tmem_st8(tl + T_R + 8 * h, v);  // (columns 8 h ..: read by now)
+      }
+      tc::tmem_st_wait();
+      if (it > 0) ok &= wait(bar(m->o_free), (it - 1) & 1, limit, gave_up);  // (the last du is read)
+      if (meet()) break;
+      if (warp == 0 && elect_one()) {
+        const uint64_t td = tc::mnmajor_desc(rec, C, 0);
+#pragma unroll
+        for (int s = 0; s < 4; s++) tc::mma_f16_ts(tbase + T_D2, tbase + T_R + 8 * s, td + step_mn(s), id64n, s > 0);
+        tc::mma_commit(bar(m->mma2));
+      }
+      warp_arrive(m->r_ready);  // (g^T P has been read)
+      ok &= wait(bar(m->mma2), ph, limit, gave_up);
+      tc::fence_after_sync();
+      // -beta f du as the next operand (headroom for beta < 4)
+      float uU = 0.0f, iU;
+      {
+        float mx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          float x[32];
+          tc::tmem_ld32(tl + T_D2 + 32 * h, x);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
+        }
+        uU = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float sU = bound_scale(uU, kTopRow - 2, iU);
+        const u64 sU2 = pack2(sU, sU);
+#pragma unroll
+        for (int h = 0; h < 4; h++) {
+          float x[16], w[8];
+          tc::tmem_ld16(tl + T_D2 + 16 * h, x);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const ulonglong2 ff = *reinterpret_cast<const ulonglong2 *>(nf + 16 * h + 4 * k);
+            const ulonglong2 bb = *reinterpret_cast<const ulonglong2 *>(be + 16 * h + 4 * k);
+            w[2 * k] = half2_bits(mul2(mul2(pack2(x[4 * k], x[4 * k + 1]), sU2), mul2(ff.x, bb.x)));
+            w[2 * k + 1] = half2_bits(mul2(mul2(pack2(x[4 * k + 2], x[4 * k + 3]), sU2), mul2(ff.y, bb.y)));
+          }
+          tc::tmem_st8(tl + T_CU + 8 * h, w);
+        }
+        tc::tmem_st_wait();
+      }
+      const float w3 = iU * iR * iK, w4 = a.scale * ig * iQ;  // units of the two sums into A
+      bS = fmaf(all, bS, (float)C * fmaf(4.0f * uU * iR, kmax, gmax * qmax * ascale));
+      put_rows(bS);
+      {
+        const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(uU * iR));
+        if (lane == 0) m->umax[ph][warp] = __uint_as_float(w);
+      }
+      if (r == 32) tc::bulk_wait_read();  // the kept adjoint has left its tile
+      if (meet()) break;
+      if (warp == 0 && elect_one()) {
+        const uint64_t kt = tc::mnmajor_desc(tile, 128, 0);
+#pragma unroll
+        for (int s = 0; s < 4; s++) tc::mma_f16_ts(tbase + T_DS, tbase + T_CU + 8 * s, kt + step_mn(s), idKN, s > 0);
+        tc::mma_commit(bar(m->mma3));
+      }
+      warp_arrive(m->u_ready);  // (and the record has been read)
+      const float sS = bound_scale(all_rows(), kTopRow, iS);
+      const u64 w3_2 = pack2(w3, w3), w4_2 = pack2(w4, w4), sS2 = pack2(sS, sS), dec = pack2(all, all);
+      ok &= wait(bar(m->dq_full), ph, limit, gave_up);
+      ok &= wait(bar(m->mma3), ph, limit, gave_up);
+      tc::fence_after_sync();
+      if (r == 0) mbar_arrive(bar(m->tile_free[ph]));
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        float z[16], y[16], v[8];
+        tc::tmem_ld16(tl + T_DS + 16 * k, z);
+        tc::tmem_ld16(tl + T_DQ + 16 * k, y);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          S[8 * k + i] = fma2(pack2(z[2 * i], z[2 * i + 1]), w3_2,
+                              fma2(pack2(y[2 * i], y[2 * i + 1]), w4_2, mul2(S[8 * k + i], dec)));
+          v[i] = half2_bits(mul2(S[8 * k + i], sS2));
+        }
+        keep_words(k, v);  // the next chunk's operand
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      warp_arrive(m->upd);
+      if ((it & 7) == 7) row_max();  // (before the bound is loose)
+    }
+    if (r == 32) tc::bulk_wait_all();
+    if (!group_or(1, 128, !ok) && a.dS0) {
+      float4 *dst = reinterpret_cast<float4 *>(a.dS0 + ((size_t)u * D + r) * D);
+#pragma unroll
+      for (int g = 0; g < D / 4; g++) {
+        float4 x;
+        unpack2(S[2 * g], x.x, x.y);
+        unpack2(S[2 * g + 1], x.z, x.w);
+        dst[g] = x;
+      }
+    }
+  } else if (warp < 8) {
+    // ---- du as an operand: fragments, transposed into a token-major tile ----
+    regs_down<kRegHelper>();
+    const int h = tid - 128, w = warp - 4;
+    const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
+    for (int it = 0; it < NC; it++) {
+      const bool got = wait(bar(m->u_ready), it & 1, limit, gave_up);
+      if (h == 0) tc::bulk_wait_read();  // the last chunk's du has left its buffer
+      if (group_or(2, 128, !got)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      float x[2][32];
+      tmem_ld_frag64(tl + T_D2, x[0]);
+      tmem_ld_frag64(tl + (16u << 16) + T_D2, x[1]);
+      tc::tmem_ld_wait();
+      tc::fence_before_sync();
+      warp_arrive(m->o_free);
+      const float4 b = *reinterpret_cast<const float4 *>(m->umax[it & 1]);
+      float iu;
+      const float su = bound_scale(fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)), kTopRow, iu);
+      const int tk = 8 * (lane >> 4) + (lane & 7);
+#pragma unroll
+      for (int hf = 0; hf < 2; hf++) {
+        const int ch = 32 * w + 16 * hf + (lane >> 2), c8 = 4 * w + 2 * hf + ((lane >> 3) & 1);
+        const float r1 = m->iR[it & 1][ch] * su, r2 = m->iR[it & 1][ch + 8] * su;
+        const u64 a1 = pack2(r1, r1), b1 = pack2(r2, r2);
+        const float *z = x[hf];
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const int j = 8 * p + 4 * e;
+            o[2 * e] = __float_as_uint(half2_bits(mul2(pack2(z[j], z[j + 1]), a1)));
+            o[2 * e + 1] = __float_as_uint(half2_bits(mul2(pack2(z[j + 2], z[j + 3]), b1)));
+          }
+          stmatrix_x4_trans(tc::smem_u32(sm + AD_OUT + tile_off(16 * p + tk, c8, C)), o[0], o[1], o[2], o[3]);
+        }
+      }
+      tc::fence_smem_to_async();
+      group_or(2, 128, false);
+      if (h == 0) {
+        const size_t at = (size_t)u * NC + NC - 1 - it;
+        bulk_s2g(ao.U + at * ROWS64, tc::smem_u32(sm + AD_OUT), ROWS64);
+        tc::bulk_commit();
+        ao.iU[at] = iu;
+        if (it + 3 < NC) fetch_rec(it + 3);  // (the other groups are past this record)
+      }
+      if (it + 3 < NC) rec_sent++;
+    }
+    if (h == 0) tc::bulk_wait_all();
+  } else {
+    // ---- K, f Q and g as operands; the products of g ----
+    regs_down<kRegConvert>();
+    const int h = tid - 256, r0 = h >> 4, c8 = h & 15, uk = a.qk_unit(u);  // rows r0, r0 + 8 ..; 8 channels
+    const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + ((size_t)uk * T + r0) * D + 8 * c8;
+    const __nv_bfloat16 *qp = (const __nv_bfloat16 *)a.q + ((size_t)uk * T + r0) * D + 8 * c8;
+    const __nv_bfloat16 *gp = (const __nv_bfloat16 *)a.dout + ((size_t)u * T + r0) * D + 8 * c8;
+    uint4 x[8], y[8], z[8];
+    auto load = [&](int c) {
+      const int n = T - c * C - r0;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        x[i] = y[i] = z[i] = make_uint4(0, 0, 0, 0);
+        if (8 * i < n) {
+          const size_t at = ((size_t)c * C + 8 * i) * D;
+          x[i] = *reinterpret_cast<const uint4 *>(kp + at);
+          y[i] = *reinterpret_cast<const uint4 *>(qp + at);
+          z[i] = *reinterpret_cast<const uint4 *>(gp + at);
+        }
+      }
+    };
+    const uint32_t idP = tc::idesc_f16(128, C, true, true), idQ = tc::idesc_f16(128, D, true, true);
+    load(NC - 1);
+    for (int it = 0; it < NC; it++) {
+      const int b = it & 1;
+      uint32_t mg = 0;
+#pragma unroll
+      for (int k = 0; k < 8; k++) mg = absmax_words(mg, z[k]);
+      mg = absmax_fold(mg);
+      if (lane == 0) m->red[4 * b + warp - 8] = mg;
+      bool got = wait(bar(m->rec_full[it % 3]), (it / 3) & 1, limit, gave_up);
+      if (it >= 2) got &= wait(bar(m->tile_free[b]), ((it >> 1) - 1) & 1, limit, gave_up);
+      if (group_or(4, 128, !got)) {
+        ok = false;
+        break;
+      }
+      const uint4 g4 = *reinterpret_cast<const uint4 *>(m->red + 4 * b);
+      float ig;
+      const float sg = bound_scale(__uint_as_float(max(max(g4.x, g4.y), max(g4.z, g4.w)) << 16), kTopTile, ig);
+      if (h == 0) m->ig[b] = ig;
+      const float *nf = reinterpret_cast<const float *>(sm + AD_REC + (it % 3) * REC_PAD + REC_F);
+      const float4 inv = *reinterpret_cast<const float4 *>(sm + AD_REC + (it % 3) * REC_PAD + REC_S);
+      const u64 sk2 = pack2(inv.z, inv.z), sg2 = pack2(sg, sg);
+      uint8_t *dst = sm + AD_TILE + b * TILE + tile_off(r0, c8, 128), *dg = sm + AD_G + b * ROWS64 + tile_off(r0, c8, C);
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float fq = -nf[r0 + 8 * k] * inv.w;
+        *reinterpret_cast<uint4 *>(dst + 1024 * k) = to_half8(x[k], sk2);
+        *reinterpret_cast<uint4 *>(dst + C * 128 + 1024 * k) = to_half8(y[k], pack2(fq, fq));
+        *reinterpret_cast<uint4 *>(dg + 1024 * k) = to_half8(z[k], sg2);
+      }
+      tc::fence_smem_to_async();
+      warp_arrive(m->tile_full[b]);
+      if (it + 1 < NC) load(NC - 2 - it);
+      if (warp == 8) {
+        const uint64_t gd = tc::mnmajor_desc(tc::smem_u32(sm + AD_G + b * ROWS64), C, 0);
+        const uint64_t pd = tc::mnmajor_desc(tc::smem_u32(sm + AD_REC + (it % 3) * REC_PAD + REC_P), C, 0);
+        const uint64_t qd = tc::mnmajor_desc(tc::smem_u32(sm + AD_TILE + b * TILE + C * 128), 128, 0);
+        got = wait(bar(m->tile_full[b]), (it >> 1) & 1, limit, gave_up);
+        if (it > 0) got &= wait(bar(m->r_ready), (it - 1) & 1, limit, gave_up);
+        tc::fence_after_sync();
+        if (__all_sync(0xffffffffu, got) && elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 4; s++) tc::mma_f16(tbase + T_DP, gd + step_mn(s), pd + step_mn(s), idP, s > 0);
+          tc::mma_commit(bar(m->dp_full));
+        }
+        __syncwarp();
+        if (it > 0) got &= wait(bar(m->upd), (it - 1) & 1, limit, gave_up);
+        tc::fence_after_sync();
+        if (__all_sync(0xffffffffu, got) && elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 4; s++) tc::mma_f16(tbase + T_DQ, gd + step_mn(s), qd + step_mn(s), idQ, s > 0);
+          tc::mma_commit(bar(m->dq_full));
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (!ok) *gave_up = 1;
+  __syncthreads();
+  // a wait gave up: products and copies still in flight finish before the memory is released
+  if (*gave_up) {
+    if ((warp == 0 || warp == 8) && elect_one()) tc::mma_commit(bar(m->drain));
+    if (tid == 0) {
+      unsigned bits = tc::kErrMmaTimeout;
+      if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
+      atomicOr(a.status, bits);
+    }
+    if (tid == 128) {
+      bool in = true;
+      for (int c = max(0, rec_sent - 3); c < rec_sent; c++)
+        in &= tc::mbar_wait(bar(m->rec_full[c % 3]), (c / 3) & 1, tc::kWaitLimit);
+      if (!in) atomicOr(a.status, tc::kErrDrainTimeout);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_free(tbase, 512);
+}
+
+// ---- the gradients of a chunk ---------------------------------------------------------------------
+// shared memory: [g; du] | u | [Q; K] | S0 | A | products' operand | X | misc.  (u as rows 64 .. 127 of a
+// 128-row operand: its descriptor starts 8 KB before it.)  dq and dk leave through [g; du]'s place.
+constexpr uint32_t GR_A1 = 0, GR_U = TILE, GR_QK = GR_U + ROWS64, GR_S = GR_QK + TILE, GR_DS = GR_S + TILE, GR_A5 = GR_DS + TILE;
+constexpr int X_LD = 65;
+constexpr uint32_t GR_X = GR_A5 + TILE, GR_MISC = GR_X + ((C * X_LD * 4 + 127) & ~127);
+struct GradsMisc {
+  float l[C], gam[C], nf[C], c[C], beta[C];
+  int z[C];
+  float duv[C], dbeta[2][C], xin[2][2][C], xout[2][C];
+  uint32_t red[8];
+  float cross[8];
+  uint64_t load, mma_a, mma_b, mma_c, drain;
+  uint32_t tmem;
+};
+constexpr uint32_t GR_SMEM = GR_MISC + sizeof(GradsMisc) + 1024;
+static_assert(GR_SMEM <= 232448, "shared memory per block");
+// tensor memory columns: [g; du] S0 | [.; u] A | [g; du] u^T | [Q; K] K^T | [0 W; W^T -(V + V^T)] [Q; K]
+constexpr uint32_t T_G1 = 0, T_G2 = 128, T_G3 = 256, T_G4 = 320, T_G5 = 384;
+
+__device__ __forceinline__ float2 half2_at(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+// grid (NC, U), 256 threads: warps w and w + 4 share tensor-memory lanes 32 w .., each half the columns.
+__global__ void __launch_bounds__(256, 1)
+    mesa_rule_grads_tc_kernel(RuleArgs a, const uint8_t *records, RuleOperands so, RuleOperands ao, float *dqp, float *dkp,
+                              const __grid_constant__ CUtensorMap mapDq, const __grid_constant__ CUtensorMap mapDk) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  GradsMisc *m = reinterpret_cast<GradsMisc *>(sm + GR_MISC);
+  float *X = reinterpret_cast<float *>(sm + GR_X);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int c = blockIdx.x, u = blockIdx.y, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
+  const size_t at = (size_t)u * NC + c, tok0 = (size_t)u * a.T + t0, row0 = (size_t)a.qk_unit(u) * a.T + t0;
+  const uint32_t bl = tc::smem_u32(&m->load), ba = tc::smem_u32(&m->mma_a), bb = tc::smem_u32(&m->mma_b),
+                 bc = tc::smem_u32(&m->mma_c);
+
+  if (warp == 0) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
+  if (tid == 32) {
+    for (uint32_t b : {bl, ba, bb, bc, tc::smem_u32(&m->drain)}) tc::mbar_init(b, 1);
+    tc::mbar_arrive_expect_tx(bl, 2 * TILE + 2 * ROWS64);
+    tc::bulk_g2s(tc::smem_u32(sm + GR_U), so.U + at * ROWS64, ROWS64, bl);
+#pragma unroll
+    for (int h = 0; h < 2; h++)  // du: rows 64 .. of both column halves
+      tc::bulk_g2s(tc::smem_u32(sm + GR_A1 + h * ROWS64 + C * 128), ao.U + at * ROWS64 + h * C * 128, C * 128, bl);
+    tc::bulk_g2s(tc::smem_u32(sm + GR_S), so.S + at * TILE, TILE, bl);
+    tc::bulk_g2s(tc::smem_u32(sm + GR_DS), ao.S + at * TILE, TILE, bl);
+  }
+  const uint8_t *rec = records + at * REC;
+  const float4 inv = *reinterpret_cast<const float4 *>(rec + REC_S);
+  const float iS = so.iS[at], iu = so.iU[at], iA = ao.iS[at], idu = ao.iU[at];
+  if (tid < C) {
+    m->nf[tid] = reinterpret_cast<const float *>(rec + REC_F)[tid];
+    m->c[tid] = reinterpret_cast<const float *>(rec + REC_C)[tid];
+    m->beta[tid] = reinterpret_cast<const float *>(rec + REC_B)[tid];
+    m->gam[tid] = tid < n ? a.gamma[tok0 + tid] : 1.0f;
+  }
+  if (warp == 7) {
+    const float *gp = a.gamma + tok0;
+    const GatePair g =
+        gate_scan(make_float2(2 * lane < n ? gp[2 * lane] : 1.0f, 2 * lane + 1 < n ? gp[2 * lane + 1] : 1.0f), lane);
+    *reinterpret_cast<float2 *>(&m->l[2 * lane]) = make_float2(g.l0, g.l1);
+    *reinterpret_cast<int2 *>(&m->z[2 * lane]) = make_int2(g.z0, g.z1);
+  }
+  // rows of Q, K and g: 16 threads a row, 16 rows a pass
+  const int r0 = tid >> 4, c8 = tid & 15;
+  uint4 g4[4];
+  uint32_t mg = 0;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int r = r0 + 16 * i;
+    uint4 k4 = make_uint4(0, 0, 0, 0), q4 = k4;
+    g4[i] = k4;
+    if (r < n) {
+      q4 = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + (row0 + r) * D + 8 * c8);
+      k4 = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + (row0 + r) * D + 8 * c8);
+      g4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.dout + (tok0 + r) * D + 8 * c8);
+    }
+    *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(r, c8, 128)) = to_half8(q4, pack2(inv.w, inv.w));
+    *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(C + r, c8, 128)) = to_half8(k4, pack2(inv.z, inv.z));
+    mg = absmax_words(mg, g4[i]);
+  }
+  mg = absmax_fold(mg);
+  if (lane == 0) m->red[warp] = mg;
+  // the products' operand: its block of Q columns for dq is zero
+  for (int i = tid; i < C * 8; i += 256)
+    *reinterpret_cast<uint4 *>(sm + GR_A5 + tile_off(i >> 3, i & 7, 128)) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  mg = 0;
+#pragma unroll
+  for (int w = 0; w < 8; w++) mg = max(mg, m->red[w]);
+  float ig;
+  const float sg = bound_scale(__uint_as_float(mg << 16), kTopTile, ig);
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    *reinterpret_cast<uint4 *>(sm + GR_A1 + tile_off(r0 + 16 * i, c8, 128)) = to_half8(g4[i], pack2(sg, sg));
+  tc::fence_smem_to_async();
+  tc::fence_before_sync();
+  const bool loaded = tc::mbar_wait(bl, 0, a.wait_limit);
+  bool stop = __syncthreads_or(!loaded);
+  tc::fence_after_sync();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, m->tmem, 0);
+  const uint64_t dA1 = tc::kmajor_desc(tc::smem_u32(sm + GR_A1), 128, 0), dQK = tc::kmajor_desc(tc::smem_u32(sm + GR_QK), 128, 0);
+  if (!stop && warp == 0 && elect_one()) {
+    const uint32_t id64 = tc::idesc_f16(128, C, false, false), idN = tc::idesc_f16(128, D, false, true);
+    const uint64_t dU = tc::kmajor_desc(tc::smem_u32(sm + GR_U), C, 0), dUhi = tc::kmajor_desc(tc::smem_u32(sm + GR_U) - C * 128, C, 0);
+    const uint64_t dK = tc::kmajor_desc(tc::smem_u32(sm + GR_QK) + C * 128, 128, 0);
+    const uint64_t nS = tc::mnmajor_desc(tc::smem_u32(sm + GR_S), 128, 0), nA = tc::mnmajor_desc(tc::smem_u32(sm + GR_DS), 128, 0);
+    // (a 64-row tile's second column half is 8 KB on)
+    auto step64x128 = [](int s) { return (uint64_t)((s >> 2) * 512 + (s & 3) * 2); };
+#pragma unroll
+    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G3, dA1 + step128(s), dU + step64x128(s), id64, s > 0);
+#pragma unroll
+    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G4, dQK + step128(s), dK + step128(s), id64, s > 0);
+    tc::mma_commit(ba);
+#pragma unroll
+    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G1, dA1 + step128(s), nS + step_mn(s), idN, s > 0);
+#pragma unroll
+    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G2, dUhi + step64x128(s), nA + step_mn(s), idN, s > 0);
+    tc::mma_commit(bb);
+  }
+  __syncwarp();
+  float bad = 0.0f;  // NaN once a gradient was not finite
+  if (!stop) {
+    // dv = beta du, du . v, and <A, S0>, while the products run
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int r = r0 + 16 * i;
+      const uint4 d4 = *reinterpret_cast<const uint4 *>(sm + GR_A1 + tile_off(C + r, c8, 128));
+      const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
+      uint4 v4 = make_uint4(0, 0, 0, 0);
+      if (r < n) v4 = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + (tok0 + r) * D + 8 * c8);
+      const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
+      const float b = m->beta[r] * idu;
+      float s = 0.0f;
+      __align__(16) __nv_bfloat162 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float2 d = half2_at(dw[k]);
+        s = fmaf(d.x, __uint_as_float(vw[k] << 16), fmaf(d.y, __uint_as_float(vw[k] & 0xffff0000u), s));
+        o[k] = __floats2bfloat162_rn(b * d.x, b * d.y);
+      }
+      if (r < n) *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.dv_out + (tok0 + r) * D + 8 * c8) = *reinterpret_cast<uint4 *>(o);
+      s = group_sum<16>(s);
+      bad = fmaf(s, 0.0f, bad);
+      if (c8 == 0) m->duv[r] = s * idu;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < (int)(TILE / 16 / 256); i++) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(sm + GR_S + 16 * (tid + 256 * i));
+      const uint4 y = *reinterpret_cast<const uint4 *>(sm + GR_DS + 16 * (tid + 256 * i));
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float2 p = half2_at(xw[k]), q = half2_at(yw[k]);
+        s = fmaf(p.x, q.x, fmaf(p.y, q.y, s));
+      }
+    }
+    s = warp_sum(s);
+    if (lane == 0) m->cross[warp] = s * iS * iA;
+  }
+  // rows of the token x token products: row < 64: g_i and q_i, else du_i and k_i; columns 32 half ..
+  const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane, i = row & 63;
+  const bool upper = row < C;
+  const uint32_t tl = tbase + ((uint32_t)(32 * quad) << 16);
+  const float mul = upper ? a.scale * ig * iu : idu * iu, be = upper ? 1.0f : m->beta[i];
+  // the operand's units: W alpha, V alpha sq / sk, both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
+  // 128 products, beta < 4, V + V^T)
+  float ialpha;
+  const float vq = inv.w * inv.x;  // sq / sk
+  const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * iu * 33554432.0f, 8.0f * idu * iu * vq * 137438953472.0f),
+                                  kTopRow, ialpha);
+  if (!stop) stop = !tc::mbar_wait(ba, 0, a.wait_limit);
+  tc::fence_after_sync();
+  stop = __syncthreads_or(stop);
+  if (!stop) {
+    float x[32], y[32];
+    tc::tmem_ld32(tl + T_G3 + 32 * half, x);
+    tc::tmem_ld32(tl + T_G4 + 32 * half, y);
+    tc::tmem_ld_wait();
+    const float li = m->l[i];
+    const int zi = m->z[i];
+    const float qk = upper ? inv.x * inv.y : inv.x * inv.x;  // real q . k, k . k
+    const float op = upper ? alpha : -alpha * vq * be;
+    float db = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; k++) {
+      const int j = 32 * half + k;
+      const float w = x[k] * mul, pair = w * (y[k] * qk);
+      const float dec = m->z[j] == zi ? ex2(li - m->l[j]) : 0.0f;
+      const bool keep = upper ? j <= i : j < i;
+      y[k] = pair * be;                   // X's part, without the decay
+      x[k] = keep ? w * dec * op : 0.0f;  // the operand
+      if (j < i) db = fmaf(dec, pair, db);  // du_i against sum_j D_ij (k_i . k_j) u_j (no beta: it may be 0)
+    }
+    if (upper) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) {  // W: row i of dq's, K columns
+        const float4 o = make_float4(half2_bits(x[8 * k], x[8 * k + 1]), half2_bits(x[8 * k + 2], x[8 * k + 3]),
+                                     half2_bits(x[8 * k + 4], x[8 * k + 5]), half2_bits(x[8 * k + 6], x[8 * k + 7]));
+        *reinterpret_cast<float4 *>(sm + GR_A5 + tile_off(i, 8 + 4 * half + k, 128)) = o;
+      }
+#pragma unroll
+      for (int k = 0; k < 32; k++) {
+        const int j = 32 * half + k;
+        *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, i, 128)) = __float2half_rn(x[k]);  // W^T
+        if (j < C - 1) X[i * X_LD + j + 1] = y[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; k++) {
+        const int j = 32 * half + k;
+        if (j > i) continue;
+        const __half v = __float2half_rn(x[k]);  // -V (zero on the diagonal), both triangles
+        *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + i, C + j, 128)) = v;
+        *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, C + i, 128)) = v;
+      }
+    }
+    tc::fence_smem_to_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0 && elect_one()) {
+      const uint32_t idN = tc::idesc_f16(128, D, false, true);
+      const uint64_t dA5 = tc::kmajor_desc(tc::smem_u32(sm + GR_A5), 128, 0), nQK = tc::mnmajor_desc(tc::smem_u32(sm + GR_QK), 128, 0);
+#pragma unroll
+      for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G5, dA5 + step128(s), nQK + step_mn(s), idN, s > 0);
+      tc::mma_commit(bc);
+    }
+    __syncwarp();
+    if (!upper) {
+#pragma unroll
+      for (int k = 0; k < 32; k++) {
+        const int j = 32 * half + k;
+        if (j < C - 1) X[i * X_LD + j + 1] -= y[k];
+      }
+      m->dbeta[half][i] = db;
+    }
+  }
+  if (!stop) stop = !tc::mbar_wait(bb, 0, a.wait_limit);
+  tc::fence_after_sync();
+  stop = __syncthreads_or(stop);
+  // rows against q_i or k_i: what the gates and betas need of the state products; columns 64 half ..
+  if (!stop) {
+    float d1 = 0.0f, d2 = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+      float x[16], y[16];
+      tc::tmem_ld16(tl + T_G1 + 64 * half + 16 * h, x);
+      if (!upper) tc::tmem_ld16(tl + T_G2 + 64 * half + 16 * h, y);
+      const uint4 p = *reinterpret_cast<const uint4 *>(sm + GR_QK + tile_off(row, 8 * half + 2 * h, 128));
+      const uint4 q = *reinterpret_cast<const uint4 *>(sm + GR_QK + tile_off(row, 8 * half + 2 * h + 1, 128));
+      const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float2 f = half2_at(w[k]);
+        d1 = fmaf(x[2 * k], f.x, fmaf(x[2 * k + 1], f.y, d1));
+        if (!upper) d2 = fmaf(y[2 * k], f.x, fmaf(y[2 * k + 1], f.y, d2));
+      }
+    }
+    if (upper) {
+      m->xin[half][0][i] = d1 * (a.scale * ig * iS * inv.y);
+    } else {
+      m->xin[half][1][i] = d1 * (idu * iS * inv.x);  // (times beta below)
+      m->xout[half][i] = d2 * (iu * iA * inv.x);
+    }
+    __syncthreads();
+    if (tid < C) {
+      const float kS = m->xin[0][1][tid] + m->xin[1][1][tid];
+      X[tid * X_LD] = m->xin[0][0][tid] + m->xin[1][0][tid] - m->beta[tid] * kS;
+      m->duv[tid] += m->nf[tid] * kS;
+    }
+    __syncthreads();
+    // columns of X, upwards from the last token: Z_t = X_t + gamma_{t+1} Z_{t+1}, times the decay from the
+    // writer to t - 1; column 0: the state before the chunk
+    if (tid <= C - 1) {
+      const int j = tid - 1;
+      float Z;
+      if (j < 0) {
+        Z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; w++) Z += m->cross[w];
+      } else {
+        Z = m->xout[0][j] + m->xout[1][j];
+      }
+      const float lj = j < 0 ? 0.0f : m->l[j];
+      const int zj = j < 0 ? 0 : m->z[j];
+      for (int t = C - 1; t > j; t--) {
+        Z = fmaf(t == C - 1 ? 1.0f : m->gam[t + 1], Z, X[t * X_LD + tid]);
+        const float lp = t > 0 ? m->l[t - 1] : 0.0f;
+        const int zp = t > 0 ? m->z[t - 1] : 0;
+        X[t * X_LD + tid] = zp == zj ? Z * ex2(lp - lj) : 0.0f;
+      }
+    }
+    __syncthreads();
+    {  // four threads a token: its gate's gradient
+      const int t = tid >> 2, part = tid & 3;
+      float s = 0.0f;
+      for (int k = part; k <= t; k += 4) s += X[t * X_LD + k];
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      bad = fmaf(s, 0.0f, bad);
+      if (part == 0 && t < n) st((__nv_bfloat16 *)a.dgamma, tok0 + t, s);
+    }
+    if (tid < n) st((__nv_bfloat16 *)a.dbeta, tok0 + tid, m->duv[tid] - (m->dbeta[0][tid] + m->dbeta[1][tid]));
+  }
+  if (!stop) stop = !tc::mbar_wait(bc, 0, a.wait_limit);
+  tc::fence_after_sync();
+  stop = __syncthreads_or(stop);
+  if (!stop) {
+    // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 64 half ..
+    const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;
+    const float f2 = m->c[i] * iu * iA, f5 = ialpha * (upper ? inv.x : inv.y);
+    uint8_t *out = sm + GR_A1 + (upper ? 0 : ROWS64);
+    float *part = upper ? dqp : dkp;
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+      float x[16], y[16], z[16];
+      tc::tmem_ld16(tl + T_G1 + 64 * half + 16 * h, x);
+      tc::tmem_ld16(tl + T_G5 + 64 * half + 16 * h, z);
+      if (!upper) tc::tmem_ld16(tl + T_G2 + 64 * half + 16 * h, y);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; k++) {
+        x[k] = fmaf(x[k], f1, z[k] * f5);
+        if (!upper) x[k] = fmaf(y[k], f2, x[k]);
+        bad = fmaf(x[k], 0.0f, bad);
+      }
+      if (part) {
+        if (i < n) {
+          float4 *dst = reinterpret_cast<float4 *>(part + (tok0 + i) * D + 64 * half + 16 * h);
+#pragma unroll
+          for (int k = 0; k < 4; k++) dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        }
+      } else {
+        __align__(16) __nv_bfloat162 o[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) o[k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        *reinterpret_cast<uint4 *>(out + tile_off(i, 8 * half + 2 * h, C)) = *reinterpret_cast<const uint4 *>(o);
+        *reinterpret_cast<uint4 *>(out + tile_off(i, 8 * half + 2 * h + 1, C)) = *reinterpret_cast<const uint4 *>(o + 4);
+      }
+    }
+    if (!(bad == 0.0f)) atomicOr(a.status, tc::kErrNonFinite);
+    tc::fence_smem_to_async();
+    __syncthreads();
+    if (!part && tid == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        tensor_s2g_3d(&mapDq, tc::smem_u32(sm + GR_A1 + h * C * 128), 64 * h, t0, u);
+        tensor_s2g_3d(&mapDk, tc::smem_u32(sm + GR_A1 + ROWS64 + h * C * 128), 64 * h, t0, u);
+      }
+      tc::bulk_commit();
+      tc::bulk_wait_all();
+    }
+  } else {  // a wait gave up: what is in flight finishes before the memory is released
+    if (tid == 0) atomicOr(a.status, tc::kErrMmaTimeout);
+    const bool issuer = warp == 0 && elect_one();
+    tc::drain_mmas(tc::smem_u32(&m->drain), issuer, a.status);
+    if (tid == 0 && !tc::mbar_wait(bl, 0, tc::kWaitLimit)) atomicOr(a.status, tc::kErrDrainTimeout);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_free(tbase, 512);
+}
+
+}  // namespace
+
+int launch_rule_adjoint_tc(const RuleArgs &a, const void *records, const RuleOperands &ao, cudaStream_t st) {
+  if (cudaFuncSetAttribute(mesa_rule_adjoint_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AD_SMEM) != cudaSuccess)
+    return -1;
+  timing_mark_begin(K_RULE_ADJOINT, st);
+  mesa_rule_adjoint_kernel<<<a.units(), 384, AD_SMEM, st>>>(a, (const uint8_t *)records, ao);
+  timing_mark_end(K_RULE_ADJOINT, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_rule_grads_tc(const RuleArgs &a, const void *records, const RuleOperands &so, const RuleOperands &ao,
+                         float *dqp, float *dkp, cudaStream_t st) {
+  CUtensorMap mapDq{}, mapDk{};
+  if (!tmap_units128_bf16(&mapDq, a.dq, a.B * a.Hk, a.T) || !tmap_units128_bf16(&mapDk, a.dk_out, a.B * a.Hk, a.T)) return -1;
+  if (cudaFuncSetAttribute(mesa_rule_grads_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GR_SMEM) != cudaSuccess)
+    return -1;
+  timing_mark_begin(K_RULE_GRADS, st);
+  mesa_rule_grads_tc_kernel<<<dim3((a.T + C - 1) / C, a.units()), 256, GR_SMEM, st>>>(a, (const uint8_t *)records, so, ao, dqp,
+                                                                                      dkp, mapDq, mapDk);
+  timing_mark_end(K_RULE_GRADS, st);
+  if (cudaPeekAtLastError() != cudaSuccess) return -1;
+  return dqp ? launch_rule_group_sum(a, dqp, dkp, st) : 0;
+}
+
+}  // namespace mesa

@@ -144,12 +144,14 @@ __global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint
 }
 
 // ---- the chain ----------------------------------------------------------------------------------
-// shared memory: three K, Q operand tiles | three records | V^T in fp32 | V | output | misc
-constexpr uint32_t CH_TILE = 0, CH_REC = CH_TILE + 3 * TILE, CH_VT = CH_REC + 3 * REC_PAD, CH_V = CH_VT + 2 * ROWS64;
-constexpr uint32_t CH_OUT = CH_V + ROWS64, CH_MISC = CH_OUT + ROWS64;
+// shared memory: three records | V^T in fp32 | V | output | K, Q operand tiles (three; two when the states
+// are kept, and a tile for their way out) | misc
+constexpr uint32_t CH_REC = 0, CH_VT = CH_REC + 3 * REC_PAD, CH_V = CH_VT + 2 * ROWS64;
+constexpr uint32_t CH_OUT = CH_V + ROWS64, CH_TILE = CH_OUT + ROWS64, CH_STAGE = CH_TILE + 2 * TILE, CH_MISC = CH_TILE + 3 * TILE;
 struct ChainMisc {
   float o1[2][D], o2[2][D];     // units of the readout's accumulators, by state row
   float vmax[4];              // largest |v| of 32 channels
+  float bmax[4], umax[2][4];  // by chain warp: bounds of the state, of |u|
   uint64_t tile_full[3], tile_free[3], rec_full[3], v_full, vt_full, r_ready, u_ready, o_free;
   uint64_t mma1, mma2, mma3, mma4, drain;
   uint32_t tmem;
@@ -181,19 +183,16 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
 // Register shares of the three warp groups; the block is launched with 168 a thread.
 constexpr int kRegChain = 240, kRegHelper = 136, kRegConvert = 120;
 static_assert(kRegChain + kRegHelper + kRegConvert <= 3 * 168, "register file");
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
 
 // grid U, 384 threads: warps 0-3 chain, 4-7 helper, 8-11 convert.
+// FWD: the forward; the records hold T diag(beta).  Otherwise the backward's pass over the states: the
+// records hold T, nothing is read out, and the state before each chunk and the chunk's u are kept as
+// operands with one scale each (so.S, so.U).
+template <bool FWD>
 __global__ void __launch_bounds__(384, 1)
-    mesa_rule_chain_kernel(RuleArgs a, const uint8_t *records, const __grid_constant__ CUtensorMap mapV,
+    mesa_rule_chain_kernel(RuleArgs a, const uint8_t *records, RuleOperands so, const __grid_constant__ CUtensorMap mapV,
                            const __grid_constant__ CUtensorMap mapO) {
+  constexpr int NT = FWD ? 3 : 2;  // operand tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   ChainMisc *m = reinterpret_cast<ChainMisc *>(sm + CH_MISC);
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(384, 1)
     for (uint64_t *b : {&m->tile_free[0], &m->tile_free[1], &m->tile_free[2], &m->rec_full[0], &m->rec_full[1],
                         &m->rec_full[2], &m->v_full, &m->mma1, &m->mma2, &m->mma3, &m->mma4})
       tc::mbar_init(bar(*b), 1);
-    tc::mbar_init(bar(m->drain), 2);  // the two threads that issue products
+    tc::mbar_init(bar(m->drain), FWD ? 2 : 1);  // the threads that issue products
     m->gave_up = 0;
     fetch_v(0);
     for (int c = 0; c < min(NC, 3); c++) fetch_rec(c);
@@ -265,8 +264,25 @@ __global__ void __launch_bounds__(384, 1)
       bS = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
     };
     row_max();
+    // the bound that scales the operand: the row's, or that of all rows where the operand is kept
+    auto all_rows = [&](float b) -> float {  // after a barrier that follows put_rows
+      const float4 x = *reinterpret_cast<const float4 *>(m->bmax);
+      return FWD ? b : fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+    };
+    auto put_rows = [&](float b) {
+      const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(b));
+      if (lane == 0) m->bmax[warp] = __uint_as_float(w);
+    };
+    auto keep_words = [&](int k, const float (&v)[8]) {  // columns 16 k .. of this row, on their way out
+      *reinterpret_cast<float4 *>(sm + CH_STAGE + tile_off(r, 2 * k, 128)) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(sm + CH_STAGE + tile_off(r, 2 * k + 1, 128)) = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    if constexpr (!FWD) {
+      put_rows(bS);
+      group_or(1, 128, false);
+    }
     {
-      const float sS = bound_scale(bS, kTopRow, iS);
+      const float sS = bound_scale(all_rows(bS), kTopRow, iS);
       const u64 s2 = pack2(sS, sS);
 #pragma unroll
       for (int k = 0; k < 8; k++) {
@@ -274,6 +290,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = half2_bits(mul2(S[8 * k + i], s2));
         tc::tmem_st8(tl + T_S + 8 * k, v);
+        if constexpr (!FWD) keep_words(k, v);
       }
       tc::tmem_st_wait();
     }
@@ -289,28 +306,38 @@ __global__ void __launch_bounds__(384, 1)
       return stop;
     };
     for (int c = 0; c < NC; c++) {
-      const uint32_t ph = c & 1, tile = tc::smem_u32(sm + CH_TILE + (c % 3) * TILE),
+      const uint32_t ph = c & 1, tile = tc::smem_u32(sm + CH_TILE + (c % NT) * TILE),
                      rec = tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD);
       const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F), *cc = nf + C,
                   *inv = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_S);
-      ok &= wait(bar(m->tile_full[c % 3]), (c / 3) & 1, limit, gave_up);
+      ok &= wait(bar(m->tile_full[c % NT]), (c / NT) & 1, limit, gave_up);
       if (c > 0) ok &= wait(bar(m->o_free), (c - 1) & 1, limit, gave_up);  // (the last readout is read)
+      if constexpr (!FWD) tc::fence_smem_to_async();
       if (meet()) break;
       if (warp == 0 && elect_one()) {
         const uint64_t kq = tc::kmajor_desc(tile, 128, 0);
 #pragma unroll
-        for (int s = 0; s < 8; s++)  // S0 K^T and S0 Q^T
-          tc::mma_f16_ts(tbase + T_D1, tbase + T_S + 8 * s, kq + step128(s), id128, s > 0);
+        for (int s = 0; s < 8; s++)  // S0 K^T and S0 Q^T (one product), or the first alone
+          tc::mma_f16_ts(tbase + T_D1, tbase + T_S + 8 * s, kq + step128(s), FWD ? id128 : id64, s > 0);
         tc::mma_commit(bar(m->mma1));
+      }
+      if constexpr (!FWD) {
+        if (r == 32) {
+          bulk_s2g(so.S + ((size_t)u * NC + c) * TILE, tc::smem_u32(sm + CH_STAGE), TILE);
+          tc::bulk_commit();
+          so.iS[(size_t)u * NC + c] = iS;
+        }
       }
       ok &= wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
       ok &= wait(bar(m->vt_full), ph, limit, gave_up);
       const float iK = inv[0], kmax = (float)(1 << kTopTile) * iK, all = -nf[C - 1];  // all: the chunk's decay
-      m->o1[ph][r] = -a.scale * iS * inv[1];
+      if constexpr (FWD) m->o1[ph][r] = -a.scale * iS * inv[1];
       const float w1 = iS * iK;  // units of D1
       float iR;
-      const float sR = bound_scale(fmaf((float)D * kmax, bS, m->vmax[warp]), kTopRow, iR);
+      const float sR = bound_scale(fmaf((float)D * kmax, bS, m->vmax[warp]), FWD ? kTopRow : kTopRow - 2, iR);  // (beta < 4)
       const u64 w1_2 = pack2(w1, w1), sR2 = pack2(sR, sR);
+      const float *be = cc + C;
+      if constexpr (!FWD) m->o1[ph][r] = iR;
       ok &= wait(bar(m->mma1), ph, limit, gave_up);
       tc::fence_after_sync();
       // R = V^T - f D1, 16 tokens at a time (few registers beside the state's 128: what spills
@@ -331,8 +358,13 @@ __global__ void __launch_bounds__(384, 1)
           float v[8];
 #pragma unroll
           for (int k = 0; k < 4; k++) {
-            v[2 * k] = half2_bits(mul2(fma2(pack2(z[4 * k], z[4 * k + 1]), mul2(ff[k].x, w1_2), vv[k].x), sR2));
-            v[2 * k + 1] = half2_bits(mul2(fma2(pack2(z[4 * k + 2], z[4 * k + 3]), mul2(ff[k].y, w1_2), vv[k].y), sR2));
+            ulonglong2 bb = make_ulonglong2(sR2, sR2);
+            if constexpr (!FWD) {
+              bb = *reinterpret_cast<const ulonglong2 *>(be + 16 * h + 4 * k);
+              bb = make_ulonglong2(mul2(bb.x, sR2), mul2(bb.y, sR2));
+            }
+            v[2 * k] = half2_bits(mul2(fma2(pack2(z[4 * k], z[4 * k + 1]), mul2(ff[k].x, w1_2), vv[k].x), bb.x));
+            v[2 * k + 1] = half2_bits(mul2(fma2(pack2(z[4 * k + 2], z[4 * k + 3]), mul2(ff[k].y, w1_2), vv[k].y), bb.y));
           }
           // (columns 8 h .. 8 h + 7: read by now)
           tc::tmem_st8(tl + T_R + 8 * h, v);
@@ -379,12 +411,21 @@ __global__ void __launch_bounds__(384, 1)
             v[2 * k + 1] = half2_bits(q);
           }
           tc::tmem_st8(tl + T_CU + 8 * h, w);
-          tc::tmem_st8(tl + T_U + 8 * h, v);
+          if constexpr (FWD) tc::tmem_st8(tl + T_U + 8 * h, v);
         }
         tc::tmem_st_wait();
       }
       const float w3 = iU * iR * iK;  // units of dS
-      m->o2[ph][r] = a.scale * w3 * inv[1];
+      // 64 products of |c u| <= |u| and |k| bound what is added to the state
+      bS = fmaf(all, bS, (float)C * uU * iR * kmax);
+      if constexpr (FWD) {
+        m->o2[ph][r] = a.scale * w3 * inv[1];
+      } else {
+        put_rows(bS);
+        const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(uU * iR));
+        if (lane == 0) m->umax[ph][warp] = __uint_as_float(w);
+        if (r == 32) tc::bulk_wait_read();  // the kept state has left its tile
+      }
       if (meet()) break;
       if (warp == 0 && elect_one()) {
         const uint64_t kt = tc::mnmajor_desc(tile, 128, 0);
@@ -395,14 +436,12 @@ __global__ void __launch_bounds__(384, 1)
       warp_arrive(m->u_ready);  // (and the record has been read)
       // the state after the chunk
       const u64 w3_2 = pack2(w3, w3);
-      // 64 products of |c u| <= |u| and |k| bound what is added
-      bS = fmaf(all, bS, (float)C * uU * iR * kmax);
-      const float sS = bound_scale(bS, kTopRow, iS);
+      const float sS = bound_scale(all_rows(bS), kTopRow, iS);
       const u64 sS2 = pack2(sS, sS);
       const u64 dec = pack2(all, all);
       ok &= wait(bar(m->mma3), ph, limit, gave_up);
       tc::fence_after_sync();
-      if (r == 0) mbar_arrive(bar(m->tile_free[c % 3]));
+      if (r == 0) mbar_arrive(bar(m->tile_free[c % NT]));
       {
 #pragma unroll
         for (int k = 0; k < 8; k++) {
@@ -415,12 +454,16 @@ __global__ void __launch_bounds__(384, 1)
             v[i] = half2_bits(mul2(S[8 * k + i], sS2));
           }
           tc::tmem_st8(tl + T_S + 8 * k, v);  // the next chunk's operand
+          if constexpr (!FWD) keep_words(k, v);
         }
         tc::tmem_st_wait();
       }
       if ((c & 7) == 7) row_max();  // (before the bound is loose)
     }
-    if (!group_or(1, 128, !ok) && a.S_final) {
+    if constexpr (!FWD) {
+      if (r == 32) tc::bulk_wait_all();
+    }
+    if (!group_or(1, 128, !ok) && FWD && a.S_final) {
       float4 *dst = reinterpret_cast<float4 *>(a.S_final + ((size_t)u * D + r) * D);
 #pragma unroll
       for (int g = 0; g < D / 4; g++) {
@@ -478,13 +521,13 @@ __global__ void __launch_bounds__(384, 1)
       got &= wait(bar(m->u_ready), c & 1, limit, gave_up);
       got = __all_sync(0xffffffffu, got);
       tc::fence_after_sync();
-      if (warp == 4 && got && elect_one()) {  // U P^T
+      if (FWD && warp == 4 && got && elect_one()) {  // U P^T
         const uint64_t pd = tc::kmajor_desc(tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD + REC_P), C, 0);
 #pragma unroll
         for (int s = 0; s < 4; s++) tc::mma_f16_ts(tbase + T_O2, tbase + T_U + 8 * s, pd + step64(s), id64, s > 0);
         tc::mma_commit(bar(m->mma4));
       }
-      got &= wait(bar(m->mma4), c & 1, limit, gave_up);
+      if constexpr (FWD) got &= wait(bar(m->mma4), c & 1, limit, gave_up);
       if (h == 0) tc::bulk_wait_read();  // the last chunk's output has left its buffer
       if (group_or(2, 128, !got)) {
         ok = false;
@@ -494,21 +537,27 @@ __global__ void __launch_bounds__(384, 1)
       const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F);
       // 16 channels at a time in fragments of 8 tokens (this thread: channels T / 4 and T / 4 + 8, tokens
       // 2 (T % 4) and the next of each 8), transposed into the swizzled output tile
+      constexpr uint32_t first = FWD ? T_O1 : T_D2;
       float x[2][32];  // from S0: all at once, the chain's next product writes there
-      tmem_ld_frag64(tl + T_O1, x[0]);
-      tmem_ld_frag64(tl + (16u << 16) + T_O1, x[1]);
+      tmem_ld_frag64(tl + first, x[0]);
+      tmem_ld_frag64(tl + (16u << 16) + first, x[1]);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       warp_arrive(m->o_free);
       const int w = warp - 4, q = 2 * (lane & 3);
+      float su = 1.0f, iu = 1.0f;
+      if constexpr (!FWD) {
+        const float4 b = *reinterpret_cast<const float4 *>(m->umax[c & 1]);
+        su = bound_scale(fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)), kTopRow, iu);
+      }
 #pragma unroll
       for (int hf = 0; hf < 2; hf++) {
         float y[32];
-        tmem_ld_frag64(tl + ((uint32_t)(16 * hf) << 16) + T_O2, y);
+        if constexpr (FWD) tmem_ld_frag64(tl + ((uint32_t)(16 * hf) << 16) + T_O2, y);
         const int ch = 32 * w + 16 * hf + (lane >> 2);
-        const u64 a1 = pack2(m->o1[c & 1][ch], m->o1[c & 1][ch]), a2 = pack2(m->o2[c & 1][ch], m->o2[c & 1][ch]);
-        const u64 b1 = pack2(m->o1[c & 1][ch + 8], m->o1[c & 1][ch + 8]),
-                  b2 = pack2(m->o2[c & 1][ch + 8], m->o2[c & 1][ch + 8]);
+        const float r1 = m->o1[c & 1][ch] * su, r2 = m->o1[c & 1][ch + 8] * su;
+        const u64 a1 = pack2(r1, r1), b1 = pack2(r2, r2), a2 = pack2(m->o2[c & 1][ch], m->o2[c & 1][ch]);
+        const u64 b2 = pack2(m->o2[c & 1][ch + 8], m->o2[c & 1][ch + 8]);
         // rows of the four blocks of a store: tokens 16 p + 8 (lane / 16) + lane % 8, channels + 8 ((lane / 8) % 2)
         const int tk = 8 * (lane >> 4) + (lane & 7), c8 = 4 * w + 2 * hf + ((lane >> 3) & 1);
         tc::tmem_ld_wait();
@@ -519,6 +568,11 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
             const int j = 8 * p + 4 * e;
+            if constexpr (!FWD) {
+              o[2 * e] = __float_as_uint(half2_bits(mul2(pack2(z[j], z[j + 1]), a1)));
+              o[2 * e + 1] = __float_as_uint(half2_bits(mul2(pack2(z[j + 2], z[j + 3]), b1)));
+              continue;
+            }
             const u64 ff = *reinterpret_cast<const u64 *>(nf + 16 * p + 8 * e + q);
             const u64 oa = fma2(pack2(z[j], z[j + 1]), mul2(ff, a1), mul2(pack2(y[j], y[j + 1]), a2));
             const u64 ob = fma2(pack2(z[j + 2], z[j + 3]), mul2(ff, b1), mul2(pack2(y[j + 2], y[j + 3]), b2));
@@ -533,8 +587,13 @@ __global__ void __launch_bounds__(384, 1)
       tc::fence_smem_to_async();
       group_or(2, 128, false);
       if (h == 0) {
+        if constexpr (FWD) {
 #pragma unroll
-        for (int b = 0; b < 2; b++) tensor_s2g_3d(&mapO, tc::smem_u32(sm + CH_OUT + b * C * 128), 64 * b, c * C, u);
+          for (int b = 0; b < 2; b++) tensor_s2g_3d(&mapO, tc::smem_u32(sm + CH_OUT + b * C * 128), 64 * b, c * C, u);
+        } else {
+          bulk_s2g(so.U + ((size_t)u * NC + c) * ROWS64, tc::smem_u32(sm + CH_OUT), ROWS64);
+          so.iU[(size_t)u * NC + c] = iu;
+        }
         tc::bulk_commit();
         if (c + 3 < NC) fetch_rec(c + 3);  // (the chain is past this record, and so is the group)
       }
@@ -556,28 +615,28 @@ __global__ void __launch_bounds__(384, 1)
         x[i] = y[i] = make_uint4(0, 0, 0, 0);
         if (8 * i < n) {
           x[i] = *reinterpret_cast<const uint4 *>(kp + ((size_t)c * C + 8 * i) * D);
-          y[i] = *reinterpret_cast<const uint4 *>(qp + ((size_t)c * C + 8 * i) * D);
+          if (FWD) y[i] = *reinterpret_cast<const uint4 *>(qp + ((size_t)c * C + 8 * i) * D);
         }
       }
     };
     load(0);
     for (int c = 0; c < NC; c++) {
       bool got = wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
-      if (c >= 3) got &= wait(bar(m->tile_free[c % 3]), (c / 3 - 1) & 1, limit, gave_up);
+      if (c >= NT) got &= wait(bar(m->tile_free[c % NT]), (c / NT - 1) & 1, limit, gave_up);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
       }
       const float4 inv = *reinterpret_cast<const float4 *>(sm + CH_REC + (c % 3) * REC_PAD + REC_S);
       const u64 sk2 = pack2(inv.z, inv.z), sq2 = pack2(inv.w, inv.w);
-      uint8_t *dst = sm + CH_TILE + (c % 3) * TILE + tile_off(r0, c8, 128);
+      uint8_t *dst = sm + CH_TILE + (c % NT) * TILE + tile_off(r0, c8, 128);
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         *reinterpret_cast<uint4 *>(dst + 1024 * k) = to_half8(x[k], sk2);
-        *reinterpret_cast<uint4 *>(dst + C * 128 + 1024 * k) = to_half8(y[k], sq2);
+        if (FWD) *reinterpret_cast<uint4 *>(dst + C * 128 + 1024 * k) = to_half8(y[k], sq2);
       }
       tc::fence_smem_to_async();
-      warp_arrive(m->tile_full[c % 3]);
+      warp_arrive(m->tile_full[c % NT]);
       if (c + 1 < NC) load(c + 1);
     }
   }
@@ -586,7 +645,7 @@ __global__ void __launch_bounds__(384, 1)
   // a wait gave up: products and copies still in flight finish before the memory is released
   if (*gave_up) {
     // (a product's commit counts for the thread that issued it: the same elected lane)
-    if ((warp == 0 || warp == 4) && elect_one()) tc::mma_commit(bar(m->drain));
+    if ((warp == 0 || (FWD && warp == 4)) && elect_one()) tc::mma_commit(bar(m->drain));
     if (tid == 0) {
       unsigned bits = tc::kErrMmaTimeout;
       if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
@@ -602,6 +661,17 @@ __global__ void __launch_bounds__(384, 1)
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0) tc::tmem_free(tbase, 512);
+}
+
+template <bool FWD>
+int launch_chain(const RuleArgs &a, const uint8_t *records, const RuleOperands &so, const CUtensorMap &mapV,
+                 const CUtensorMap &mapO, cudaStream_t st) {
+  auto kfn = mesa_rule_chain_kernel<FWD>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CH_SMEM) != cudaSuccess) return -1;
+  timing_mark_begin(K_RULE_CHAIN, st);
+  kfn<<<a.units(), 384, CH_SMEM, st>>>(a, records, so, mapV, mapO);
+  timing_mark_end(K_RULE_CHAIN, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace
@@ -622,14 +692,14 @@ int launch_rule_prep(const RuleArgs &a, void *records, bool with_beta, cudaStrea
 int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st) {
   CUtensorMap mapV{}, mapO{};
   if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T) || !tmap_units128_bf16(&mapO, a.out, a.units(), a.T)) return -1;
-  if (cudaFuncSetAttribute(mesa_rule_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CH_SMEM) !=
-      cudaSuccess)
-    return -1;
   if (launch_rule_prep(a, workspace, true, st) != 0) return -1;
-  timing_mark_begin(K_RULE_CHAIN, st);
-  mesa_rule_chain_kernel<<<a.units(), 384, CH_SMEM, st>>>(a, (const uint8_t *)workspace, mapV, mapO);
-  timing_mark_end(K_RULE_CHAIN, st);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return launch_chain<true>(a, (const uint8_t *)workspace, RuleOperands{}, mapV, mapO, st);
+}
+
+int launch_rule_states_tc(const RuleArgs &a, const void *records, const RuleOperands &so, cudaStream_t st) {
+  CUtensorMap mapV{};
+  if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T)) return -1;
+  return launch_chain<false>(a, (const uint8_t *)records, so, mapV, mapV, st);
 }
 
 }  // namespace mesa

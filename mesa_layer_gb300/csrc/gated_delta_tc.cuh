@@ -167,6 +167,15 @@ __device__ __forceinline__ uint64_t step128(int s) { return (uint64_t)((s >> 2) 
 __device__ __forceinline__ uint64_t step64(int s) { return (uint64_t)(2 * s); }
 __device__ __forceinline__ uint64_t step_mn(int s) { return (uint64_t)(128 * s); }
 
+// Register shares of warp groups (setmaxnreg; a whole group of four warps).
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
 // 64 columns of 16 tensor-memory lanes as 8-column fragments: for columns 8 j .. 8 j + 7 this thread gets
 // lane T / 4, columns 2 (T % 4) and the next, in r[4 j], r[4 j + 1]; lane T / 4 + 8 in the next two.
 __device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, float (&v)[32]) {
