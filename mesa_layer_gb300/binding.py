@@ -389,14 +389,30 @@ def _require_shape(t, name, shape):
 
 
 def _require_all(device, *specs):
-    """Check (tensor or None, name, dtype, shape) on one device."""
+    """Check (tensor or None, name, dtype, shape) on one device.  (One pass with few attribute
+    reads; the message is put together only when something is wrong.)"""
+    index = device.index
     for t, name, dtype, shape in specs:
-        if t is None:
-            continue
-        _require(t, name, dtype)
-        _require_shape(t, name, shape)
-        if t.device != device:
+        if t is not None and (t.get_device() != index or t.dtype is not dtype or t.shape != shape
+                              or not t.is_contiguous()):
+            _require(t, name, dtype)
+            _require_shape(t, name, shape)
             raise MesaError(f"{name} must be on {device}, got {t.device}")
+
+
+def _require_cuda(t, name):
+    if not t.is_cuda:
+        raise MesaError(f"{name} must be a CUDA tensor")
+
+
+def _at(t):
+    """Address of a tensor, or None."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    """The given stream, or the device's current one, as an address."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _new(shape, dtype, device, stream):
@@ -419,10 +435,12 @@ def _delta_dims(q, k, v, gamma, beta):
     """(B, H, Hk, T, dk, dv) of the gated delta rule's sequence forms, every shape checked."""
     if q.dim() != 4 or v.dim() != 4:
         raise MesaError("q, k must be [B, Hk, T, dk] and v [B, H, T, dv]")
-    B, Hk, T, dk = q.shape
-    H, dv = v.shape[1], v.shape[3]
-    _require_all(q.device, (q, "q", None, q.shape), (k, "k", q.dtype, q.shape), (v, "v", q.dtype, (B, H, T, dv)),
-                 (gamma, "gamma", torch.float32, (B, H, T)), (beta, "beta", torch.float32, (B, H, T)))
+    _require_cuda(q, "q")
+    B, Hk, T, dk = shape = q.shape
+    _, H, _, dv = v.shape
+    dtype, gates = q.dtype, (B, H, T)
+    _require_all(q.device, (q, "q", dtype, shape), (k, "k", dtype, shape), (v, "v", dtype, (B, H, T, dv)),
+                 (gamma, "gamma", torch.float32, gates), (beta, "beta", torch.float32, gates))
     return B, H, Hk, T, dk, dv
 
 
@@ -443,10 +461,9 @@ def mesa_delta_forward_chunked(q, k, v, gamma, beta, scale=1.0, out=None, S0=Non
     _require_all(q.device, (out, "out", q.dtype, (B, H, T, dv)), (S0, "S0", torch.float32, (B, H, dv, dk)),
                  (S_final, "S_final", torch.float32, (B, H, dv, dk)))
     workspace = _workspace(workspace, int(lib.mesa_delta_workspace_size(B, H, Hk, T, dk, dv, code)), q.device, stream)
-    _check(lib.mesa_delta_forward_chunked(B, H, Hk, T, dk, dv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
-                                          _ptr(beta), float(scale), _ptr(out), _ptr(S0), _ptr(S_final),
-                                          _ptr(workspace), workspace.numel(), _stream(stream)),
-           "mesa_delta_forward_chunked")
+    _check(lib.mesa_delta_forward_chunked(B, H, Hk, T, dk, dv, code, _at(q), _at(k), _at(v), _at(gamma), _at(beta),
+                                          scale, _at(out), _at(S0), _at(S_final), _at(workspace), workspace.numel(),
+                                          _raw_stream(stream, q.device)), "mesa_delta_forward_chunked")
     return out
 
 
@@ -476,11 +493,10 @@ def mesa_delta_backward_chunked(q, k, v, gamma, beta, dout, scale=1.0, S0=None, 
                  (dS_final, "dS_final", torch.float32, state), (dS0, "dS0", torch.float32, state))
     workspace = _workspace(workspace, int(lib.mesa_delta_backward_workspace_size(B, H, Hk, T, dkk, dvv, code)), dev,
                            stream)
-    _check(lib.mesa_delta_backward_chunked(B, H, Hk, T, dkk, dvv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
-                                           _ptr(beta), float(scale), _ptr(dout), _ptr(S0), _ptr(dS_final), _ptr(dq),
-                                           _ptr(dk), _ptr(dv), _ptr(dgamma), _ptr(dbeta), _ptr(dS0),
-                                           _ptr(workspace), workspace.numel(), _stream(stream)),
-           "mesa_delta_backward_chunked")
+    _check(lib.mesa_delta_backward_chunked(B, H, Hk, T, dkk, dvv, code, _at(q), _at(k), _at(v), _at(gamma), _at(beta),
+                                           scale, _at(dout), _at(S0), _at(dS_final), _at(dq), _at(dk), _at(dv),
+                                           _at(dgamma), _at(dbeta), _at(dS0), _at(workspace), workspace.numel(),
+                                           _raw_stream(stream, dev)), "mesa_delta_backward_chunked")
     return dq, dk, dv, dgamma, dbeta
 
 
@@ -491,24 +507,29 @@ def mesa_delta_step(S_state, q, k, v, gamma, beta, scale=1.0, out=None, stream=N
     code = _dtype_code(q)
     if q.dim() != 3 or v.dim() != 3:
         raise MesaError("q, k must be [N, Hk, dk] and v [N, H, dv]")
-    N, Hk, dk = q.shape
-    H, dv = v.shape[1], v.shape[2]
-    out = _new((N, H, dv), q.dtype, q.device, stream) if out is None else out
-    _require_all(q.device, (q, "q", None, q.shape), (k, "k", q.dtype, q.shape), (v, "v", q.dtype, (N, H, dv)),
-                 (gamma, "gamma", torch.float32, (N, H)), (beta, "beta", torch.float32, (N, H)),
-                 (S_state, "S_state", torch.float32, (N, H, dv, dk)), (out, "out", q.dtype, (N, H, dv)))
-    _check(lib.mesa_delta_step(N, H, Hk, dk, dv, code, _ptr(S_state), _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
-                               _ptr(beta), float(scale), _ptr(out), _stream(stream)), "mesa_delta_step")
+    _require_cuda(q, "q")
+    N, Hk, dk = shape = q.shape
+    _, H, dv = v.shape
+    dev, dtype, vshape, gates = q.device, q.dtype, (N, H, dv), (N, H)
+    out = _new(vshape, dtype, dev, stream) if out is None else out
+    _require_all(dev, (q, "q", dtype, shape), (k, "k", dtype, shape), (v, "v", dtype, vshape),
+                 (gamma, "gamma", torch.float32, gates), (beta, "beta", torch.float32, gates),
+                 (S_state, "S_state", torch.float32, (N, H, dv, dk)), (out, "out", dtype, vshape))
+    _check(lib.mesa_delta_step(N, H, Hk, dk, dv, code, _at(S_state), _at(q), _at(k), _at(v), _at(gamma), _at(beta),
+                               scale, _at(out), _raw_stream(stream, dev)), "mesa_delta_step")
     return out
 
 
 def _norm_check(x, y, gate, w_post, res_scale, w_pre):
     if y.dim() < 1 or y.shape[-1] < 1:
         raise MesaError("y must be [..., D] with D >= 1")
-    D = y.shape[-1]
-    _require_all(y.device, (y, "y", None, y.shape), (x, "x", y.dtype, y.shape), (gate, "gate", y.dtype, y.shape),
-                 (w_post, "w_post", torch.float32, (D,)), (res_scale, "res_scale", torch.float32, (D,)),
-                 (w_pre, "w_pre", torch.float32, (D,)))
+    _require_cuda(y, "y")
+    shape, dtype = y.shape, y.dtype
+    D = shape[-1]
+    weight = (D,)
+    _require_all(y.device, (y, "y", dtype, shape), (x, "x", dtype, shape), (gate, "gate", dtype, shape),
+                 (w_post, "w_post", torch.float32, weight), (res_scale, "res_scale", torch.float32, weight),
+                 (w_pre, "w_pre", torch.float32, weight))
     return y.numel() // D, D
 
 
@@ -525,8 +546,8 @@ def mesa_block_norm(x, y, gate=None, w_post=None, res_scale=None, w_pre=None, ep
     if w_pre is not None and h_out is None:
         h_out = _new(y.shape, y.dtype, y.device, stream)
     _require_all(y.device, (x_out, "x_out", y.dtype, y.shape), (h_out, "h_out", y.dtype, y.shape))
-    _check(lib.mesa_block_norm(N, D, code, _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(res_scale), _ptr(w_pre),
-                               float(eps), _ptr(x_out), _ptr(h_out), _stream(stream)), "mesa_block_norm")
+    _check(lib.mesa_block_norm(N, D, code, _at(x), _at(y), _at(gate), _at(w_post), _at(res_scale), _at(w_pre), eps,
+                               _at(x_out), _at(h_out), _raw_stream(stream, y.device)), "mesa_block_norm")
     return x_out, (h_out if w_pre is not None else None)
 
 
@@ -555,10 +576,10 @@ def mesa_block_norm_backward(x, y, dx_out, dh=None, gate=None, w_post=None, res_
         (dx_out, "dx_out"), (dh, "dh"), (dx, "dx"), (dy, "dy"), (dgate, "dgate"))],
         *[(t, n, torch.float32, (D,)) for t, n in ((dw_post, "dw_post"), (dres_scale, "dres_scale"), (dw_pre, "dw_pre"))])
     workspace = _workspace(workspace, int(lib.mesa_block_norm_backward_workspace_size(N, D)), dev, stream)
-    _check(lib.mesa_block_norm_backward(N, D, code, _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(res_scale),
-                                        _ptr(w_pre), float(eps), _ptr(dx_out), _ptr(dh), _ptr(dx), _ptr(dy),
-                                        _ptr(dgate), _ptr(dw_post), _ptr(dres_scale), _ptr(dw_pre), _ptr(workspace),
-                                        workspace.numel(), _stream(stream)), "mesa_block_norm_backward")
+    _check(lib.mesa_block_norm_backward(N, D, code, _at(x), _at(y), _at(gate), _at(w_post), _at(res_scale), _at(w_pre),
+                                        eps, _at(dx_out), _at(dh), _at(dx), _at(dy), _at(dgate), _at(dw_post),
+                                        _at(dres_scale), _at(dw_pre), _at(workspace), workspace.numel(),
+                                        _raw_stream(stream, dev)), "mesa_block_norm_backward")
     return dx, dy, dgate, dw_post, dres_scale, dw_pre
 
 

@@ -10,35 +10,6 @@ namespace norm {
 
 constexpr int EPT = 8;  // channels per thread
 
-// VEC consecutive elements (the address aligned to VEC elements) as fp32, and back.
-template <int VEC>
-__device__ __forceinline__ void load_vec(const float *p, float *x) {
-  if constexpr (VEC == 4) {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-  } else if constexpr (VEC == 2) {
-    const float2 v = *reinterpret_cast<const float2 *>(p);
-    x[0] = v.x, x[1] = v.y;
-  } else {
-    x[0] = *p;
-  }
-}
-template <int VEC>
-__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float *x) {
-  if constexpr (VEC == 1) {
-    x[0] = __bfloat162float(*p);
-  } else {
-    __align__(16) __nv_bfloat162 b[VEC / 2];
-    if constexpr (VEC == 8) *reinterpret_cast<uint4 *>(b) = *reinterpret_cast<const uint4 *>(p);
-    if constexpr (VEC == 4) *reinterpret_cast<uint2 *>(b) = *reinterpret_cast<const uint2 *>(p);
-    if constexpr (VEC == 2) b[0] = *reinterpret_cast<const __nv_bfloat162 *>(p);
-#pragma unroll
-    for (int i = 0; i < VEC / 2; i++) {
-      const float2 f = __bfloat1622float2(b[i]);
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-  }
-}
 template <int VEC>
 __device__ __forceinline__ void store_vec(float *p, const float *x) {
   if constexpr (VEC == 4)
@@ -62,20 +33,48 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float *x) {
   }
 }
 
-// A thread's eight channels: vector i of them starts at channel (lane + i G) VEC of the row.
-template <int VEC, int G, typename T>
-__device__ __forceinline__ void load_row(const T *row, int lane, int D, bool in, float (&x)[EPT]) {
+// A thread's eight channels as they lie in memory, so that the next row's can be on their way in few
+// registers: vector i of VEC elements (the address aligned to it) starts at channel (lane + i G) VEC.
+template <typename T, int VEC>
+struct Raw {
+  static constexpr int kBytes = VEC * (int)sizeof(T), kWords = kBytes >= 4 ? kBytes / 4 : 1;
+  uint32_t w[EPT / VEC * kWords];
+  template <int G>
+  __device__ __forceinline__ void load(const T *row, int lane, int D, bool in) {
 #pragma unroll
-  for (int i = 0; i < EPT / VEC; i++) {
-    const int c = (lane + i * G) * VEC;
-    if (in && c < D) {
-      load_vec<VEC>(row + c, x + i * VEC);
-    } else {
+    for (int i = 0; i < EPT / VEC; i++) {
+      const int c = (lane + i * G) * VEC;
+      uint32_t *x = w + i * kWords;
 #pragma unroll
-      for (int k = 0; k < VEC; k++) x[i * VEC + k] = 0.0f;
+      for (int k = 0; k < kWords; k++) x[k] = 0;
+      if (in && c < D) {
+        if constexpr (kBytes == 16) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(row + c);
+          x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else if constexpr (kBytes == 8) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(row + c);
+          x[0] = v.x, x[1] = v.y;
+        } else if constexpr (kBytes == 4) {
+          x[0] = *reinterpret_cast<const uint32_t *>(row + c);
+        } else {
+          x[0] = *reinterpret_cast<const uint16_t *>(row + c);
+        }
+      }
     }
   }
-}
+  __device__ __forceinline__ void widen(float (&x)[EPT]) const {
+    if constexpr (sizeof(T) == 4 || kBytes == 2) {
+#pragma unroll
+      for (int i = 0; i < EPT; i++) x[i] = __uint_as_float(sizeof(T) == 4 ? w[i] : w[i] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPT / 2; i++) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+};
 template <int VEC, int G, typename T>
 __device__ __forceinline__ void store_row(T *row, int lane, int D, bool in, const float (&x)[EPT]) {
 #pragma unroll
@@ -94,6 +93,15 @@ __device__ __forceinline__ void load_weights(const float *w, int lane, int D, fl
       const int c = (lane + i * G) * VEC + k;
       x[i * VEC + k] = w && c < D ? w[c] : fill;
     }
+}
+
+// 1 / (1 + e^-g).  For bf16 rows by the approximate exponential and division (each within 2^-20 for
+// |g| < 10, far below the outputs' 2^-9): with the exact ones the arithmetic, not memory, set the
+// backward's pace.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+  if constexpr (sizeof(T) == 2) return __fdividef(1.0f, 1.0f + __expf(-g));
+  return 1.0f / (1.0f + expf(-g));
 }
 
 // Sums over a row's G threads, every thread getting them.  Rows wider than a warp go through

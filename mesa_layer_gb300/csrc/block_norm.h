@@ -32,12 +32,12 @@ inline int norm_rows(int D) {
   const int g = norm_group(D);
   return g < 128 ? 128 / g : 1;
 }
-// CTAs of the backward kernel: its column sums are kept per CTA.  A fixed count (four for each
-// of a GB300's 152 SMs), so that the workspace size needs no device.
-constexpr int kNormBwdCtas = 608;
+// CTAs of the backward kernel: its column sums are kept per CTA.  A fixed count (as many as are resident
+// on a GB300's 152 SMs), so that the workspace size needs no device.
 inline int norm_bwd_ctas(int N, int D) {
-  const int want = (int)(((size_t)N + norm_rows(D) - 1) / norm_rows(D));
-  return want < kNormBwdCtas ? want : kNormBwdCtas;
+  const int g = norm_group(D), most = 152 * (g <= 128 ? 4 : g == 256 ? 2 : 1);
+  const size_t want = ((size_t)N + norm_rows(D) - 1) / norm_rows(D);
+  return want < (size_t)most ? (int)want : most;
 }
 
 int launch_block_norm(const NormArgs &a, cudaStream_t st);
