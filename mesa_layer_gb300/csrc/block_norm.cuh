@@ -4,6 +4,7 @@
 
 #include "block_norm.h"
 #include "common.cuh"
+#include "packed.cuh"
 
 namespace mesa {
 namespace norm {
@@ -62,6 +63,12 @@ struct Raw {
       }
     }
   }
+  __device__ __forceinline__ void pairs(u64 (&x)[EPT / 2]) const {
+    float v[EPT];
+    widen(v);
+#pragma unroll
+    for (int i = 0; i < EPT / 2; i++) x[i] = pack2(v[2 * i], v[2 * i + 1]);
+  }
   __device__ __forceinline__ void widen(float (&x)[EPT]) const {
     if constexpr (sizeof(T) == 4 || kBytes == 2) {
 #pragma unroll
@@ -82,6 +89,13 @@ __device__ __forceinline__ void store_row(T *row, int lane, int D, bool in, cons
     const int c = (lane + i * G) * VEC;
     if (in && c < D) store_vec<VEC>(row + c, x + i * VEC);
   }
+}
+template <int VEC, int G, typename T>
+__device__ __forceinline__ void store_pairs(T *row, int lane, int D, bool in, const u64 (&x)[EPT / 2]) {
+  float v[EPT];
+#pragma unroll
+  for (int i = 0; i < EPT / 2; i++) unpack2(x[i], v[2 * i], v[2 * i + 1]);
+  store_row<VEC, G>(row, lane, D, in, v);
 }
 // A [D] fp32 vector's channels of this thread (fill where it is not given).
 template <int VEC, int G>

@@ -20,35 +20,35 @@ namespace mesa {
 namespace {
 
 template <typename T, int VEC, int G>
-__global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 ? 4 : G == 256 ? 2 : 1) mesa_block_norm_bwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 ? (sizeof(T) == 4 ? 3 : 4) : G == 256 ? 2 : 1) mesa_block_norm_bwd_kernel(NormArgs a) {
   using namespace norm;
   constexpr int RPC = G < 128 ? 128 / G : 1;
   __shared__ float red[2][1][32], red2[2][2][32];
-  constexpr int BLOCK = G < 128 ? 128 : G;
+  constexpr int BLOCK = G < 128 ? 128 : G, P = EPT / 2;
   extern __shared__ __align__(16) float wsm[];  // three weights of a row's channels, as the threads hold them
   const int lane = threadIdx.x % G, sub = threadIdx.x / G, D = a.D;
   const float inv_d = 1.0f / (float)D;
-  // weight k's channels of a thread: wsm[(k EPT + i) G + lane]
+  // weight k's channels of a thread, two at a time: the pair at wsm + 2 ((k EPT / 2 + i) G + lane)
   for (int t = threadIdx.x; t < 3 * G; t += BLOCK) {
     const int k = t / G, l = t % G;
     float v[EPT];
     load_weights<VEC, G>(k == 0 ? a.w_post : k == 1 ? a.res_scale : a.w_pre, l, D, k == 2 ? 0.0f : 1.0f, v);
 #pragma unroll
-    for (int i = 0; i < EPT; i++) wsm[(k * EPT + i) * G + l] = v[i];
+    for (int i = 0; i < EPT; i++) wsm[2 * ((k * (EPT / 2) + i / 2) * G + l) + (i & 1)] = v[i];
   }
   __syncthreads();
-  const float *wp = wsm + lane, *rs = wp + EPT * G, *wn = rs + EPT * G;
+  const u64 *wp = reinterpret_cast<const u64 *>(wsm) + lane, *rs = wp + P * G, *wn = rs + P * G;
   const T *x = (const T *)a.x, *y = (const T *)a.y, *gate = (const T *)a.gate;
   const T *dxo = (const T *)a.dx_out, *dh = (const T *)a.dh;
   const bool pre = a.w_pre && dh;
   // d - xh mean(d xh), the part of a norm's gradient across the row.  A row of one channel has
   // xh^2 = 1 - eps r^2: the difference, d eps r^2, is taken as such (in fp32 it would cancel).
   const bool one = D == 1;
-  const float eps = a.eps;
-  auto along = [one, eps](float d, float xh, float m, float r) {
-    return one ? d * (eps * r * r) : fmaf(-xh, m, d);
+  auto along = [&](u64 d, u64 xh, float m, float r) -> u64 {
+    const float e = a.eps * r * r;
+    return one ? mul2(d, pack2(e, e)) : fma2(xh, pack2(-m, -m), d);
   };
-  float cpost[EPT] = {}, cscale[EPT] = {}, cpre[EPT] = {};
+  u64 cpost[P] = {}, cscale[P] = {}, cpre[P] = {};
   int buf = 0, buf2 = 0;
   const size_t N = (size_t)a.N, step = (size_t)gridDim.x * RPC;
   Raw<T, VEC> ry, rg, rx, rd, rh;
@@ -64,73 +64,80 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 ? 4 : G == 256 ? 2
   for (size_t base = (size_t)blockIdx.x * RPC; base < N; base += step) {
     const size_t row = base + sub, at = row * D;
     const bool in = row < N;
-    float yv[EPT], gv[EPT], X[EPT], dX[EPT], dhv[EPT];
-    ry.widen(yv);
-    rg.widen(gv);
-    rx.widen(X);
-    rd.widen(dX);
-    rh.widen(dhv);
+    u64 yv[P], gv[P], X[P], dX[P], dhv[P];
+    ry.pairs(yv);
+    rg.pairs(gv);
+    rx.pairs(X);
+    rd.pairs(dX);
+    rh.pairs(dhv);
     fetch(row + step);
     float r = 1.0f;
     if (a.w_post) {
-      float ss[1] = {0.0f};
+      u64 t = 0;
 #pragma unroll
-      for (int i = 0; i < EPT; i++) ss[0] = fmaf(yv[i], yv[i], ss[0]);
+      for (int i = 0; i < P; i++) t = fma2(yv[i], yv[i], t);
+      float ss[1] = {sum2(t)};
       row_sums<G>(ss, red, buf);
       r = rsqrtf(fmaf(ss[0], inv_d, a.eps));
-    }
-    float act[EPT], dact[EPT];
 #pragma unroll
-    for (int i = 0; i < EPT; i++) {
-      yv[i] *= r;  // y normalised
+      for (int i = 0; i < P; i++) yv[i] = mul2(yv[i], pack2(r, r));  // y normalised
+    }
+    u64 act[P], dact[P];
+#pragma unroll
+    for (int i = 0; i < P; i++) {
+      act[i] = pack2(1.0f, 1.0f);
+      dact[i] = 0;
       if (gate) {
-        const float s = sigmoid<T>(gv[i]);
-        act[i] = gv[i] * s;
-        dact[i] = s * fmaf(gv[i], 1.0f - s, 1.0f);
-      } else {
-        act[i] = 1.0f;
-        dact[i] = 0.0f;
+        float g0, g1;
+        unpack2(gv[i], g0, g1);
+        const u64 s = pack2(sigmoid<T>(g0), sigmoid<T>(g1));
+        dact[i] = mul2(s, fma2(gv[i], sub2(act[i], s), act[i]));
+        act[i] = mul2(gv[i], s);
       }
     }
-    if (pre) {
-      float ss[2] = {0.0f, 0.0f};
+    u64 az[P];  // act z
 #pragma unroll
-      for (int i = 0; i < EPT; i++) {
-        X[i] = fmaf(rs[i * G], yv[i] * wp[i * G] * act[i], X[i]);
-        ss[0] = fmaf(X[i], X[i], ss[0]);
-        ss[1] = fmaf(dhv[i] * wn[i * G], X[i], ss[1]);
+    for (int i = 0; i < P; i++) az[i] = mul2(act[i], mul2(yv[i], wp[i * G]));
+    if (pre) {
+      u64 t0 = 0, t1 = 0;
+#pragma unroll
+      for (int i = 0; i < P; i++) {
+        X[i] = fma2(rs[i * G], az[i], X[i]);
+        t0 = fma2(X[i], X[i], t0);
+        t1 = fma2(mul2(dhv[i], wn[i * G]), X[i], t1);
       }
+      float ss[2] = {sum2(t0), sum2(t1)};
       row_sums<G>(ss, red2, buf2);
       const float rn = rsqrtf(fmaf(ss[0], inv_d, a.eps));
       const float m = ss[1] * rn * inv_d;  // mean(w_pre dh xh)
+      const u64 rn2 = pack2(rn, rn);
 #pragma unroll
-      for (int i = 0; i < EPT; i++) {
-        const float xh = X[i] * rn;
-        cpre[i] = fmaf(dhv[i], xh, cpre[i]);
-        dX[i] = fmaf(rn, along(dhv[i] * wn[i * G], xh, m, rn), dX[i]);
+      for (int i = 0; i < P; i++) {
+        const u64 xh = mul2(X[i], rn2);
+        cpre[i] = fma2(dhv[i], xh, cpre[i]);
+        dX[i] = fma2(rn2, along(mul2(dhv[i], wn[i * G]), xh, m, rn), dX[i]);
       }
     }
-    if (a.dx) store_row<VEC, G>((T *)a.dx + at, lane, D, in, dX);
-    float ss[1] = {0.0f};
+    if (a.dx) store_pairs<VEC, G>((T *)a.dx + at, lane, D, in, dX);
+    u64 t = 0;
 #pragma unroll
-    for (int i = 0; i < EPT; i++) {
-      const float z = yv[i] * wp[i * G];
-      cscale[i] = fmaf(dX[i], act[i] * z, cscale[i]);
-      const float d = dX[i] * rs[i * G];
-      gv[i] = d * z * dact[i];  // dgate
-      const float dz = d * act[i];
-      cpost[i] = fmaf(dz, yv[i], cpost[i]);
-      dX[i] = dz * wp[i * G];
-      ss[0] = fmaf(dX[i], yv[i], ss[0]);
+    for (int i = 0; i < P; i++) {
+      cscale[i] = fma2(dX[i], az[i], cscale[i]);
+      const u64 d = mul2(dX[i], rs[i * G]), dz = mul2(d, act[i]), w = wp[i * G];
+      gv[i] = mul2(mul2(d, dact[i]), mul2(yv[i], w));  // dgate
+      cpost[i] = fma2(dz, yv[i], cpost[i]);
+      dX[i] = mul2(dz, w);
+      t = fma2(dX[i], yv[i], t);
     }
-    if (a.dgate) store_row<VEC, G>((T *)a.dgate + at, lane, D, in, gv);
+    if (a.dgate) store_pairs<VEC, G>((T *)a.dgate + at, lane, D, in, gv);
     if (a.w_post) {
+      float ss[1] = {sum2(t)};
       row_sums<G>(ss, red, buf);
       const float m = ss[0] * inv_d;
 #pragma unroll
-      for (int i = 0; i < EPT; i++) dX[i] = r * along(dX[i], yv[i], m, r);
+      for (int i = 0; i < P; i++) dX[i] = mul2(along(dX[i], yv[i], m, r), pack2(r, r));
     }
-    store_row<VEC, G>((T *)a.dy + at, lane, D, in, dX);
+    store_pairs<VEC, G>((T *)a.dy + at, lane, D, in, dX);
   }
   if (!a.partial) return;
   float *out = a.partial + (size_t)blockIdx.x * 3 * D;
@@ -143,14 +150,21 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 ? 4 : G == 256 ? 2
         if (c < D) f(c, i * VEC + k);
       }
   };
+  float cp[EPT], cs[EPT], cn[EPT];
+#pragma unroll
+  for (int i = 0; i < P; i++) {
+    unpack2(cpost[i], cp[2 * i], cp[2 * i + 1]);
+    unpack2(cscale[i], cs[2 * i], cs[2 * i + 1]);
+    unpack2(cpre[i], cn[2 * i], cn[2 * i + 1]);
+  }
   if constexpr (G < 32) {  // the rows of a warp
 #pragma unroll
     for (int i = 0; i < EPT; i++)
 #pragma unroll
       for (int o = G; o < 32; o *= 2) {
-        cpost[i] += __shfl_xor_sync(0xffffffffu, cpost[i], o);
-        cscale[i] += __shfl_xor_sync(0xffffffffu, cscale[i], o);
-        cpre[i] += __shfl_xor_sync(0xffffffffu, cpre[i], o);
+        cp[i] += __shfl_xor_sync(0xffffffffu, cp[i], o);
+        cs[i] += __shfl_xor_sync(0xffffffffu, cs[i], o);
+        cn[i] += __shfl_xor_sync(0xffffffffu, cn[i], o);
       }
   }
   constexpr int W = G < 32 ? 32 : G, PARTS = BLOCK / W;  // threads that hold one sum; sums left in the CTA
@@ -164,13 +178,13 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 ? 4 : G == 256 ? 2
         for (int i = 0; i < EPT; i++) {
           float *c = cols + i * G + lane;
           if (p < PARTS - 1) {
-            cpost[i] += c[0];
-            cscale[i] += c[EPT * G];
-            cpre[i] += c[2 * EPT * G];
+            cp[i] += c[0];
+            cs[i] += c[EPT * G];
+            cn[i] += c[2 * EPT * G];
           }
-          c[0] = cpost[i];
-          c[EPT * G] = cscale[i];
-          c[2 * EPT * G] = cpre[i];
+          c[0] = cp[i];
+          c[EPT * G] = cs[i];
+          c[2 * EPT * G] = cn[i];
         }
       }
     }
@@ -178,9 +192,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 ? 4 : G == 256 ? 2
   }
   if (threadIdx.x % W < G)
     each([&](int c, int i) {
-      out[c] = cpost[i];
-      out[D + c] = cscale[i];
-      out[2 * D + c] = cpre[i];
+      out[c] = cp[i];
+      out[D + c] = cs[i];
+      out[2 * D + c] = cn[i];
     });
 }
 
