@@ -152,8 +152,9 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
     auto f = [&](int i) { return (float *)(w + off[i]); };
     auto b8 = [&](int i) { return (uint8_t *)(w + off[i]); };
     const mesa::RuleOperands so{b8(1), b8(3), f(5), f(6)}, ao{b8(2), b8(4), f(7), f(8)};
-    const bool ok = mesa::launch_rule_prep(a, b8(0), false, stream) == 0 &&
-                    mesa::launch_rule_states_tc(a, b8(0), so, stream) == 0 &&
+    const mesa::RuleSegments sg = mesa::rule_tc_segments(a.units(), T, b8(0));
+    const bool ok = mesa::launch_rule_prep(a, b8(0), sg, false, stream) == 0 &&
+                    mesa::launch_rule_states_tc(a, b8(0), sg, so, stream) == 0 &&
                     mesa::launch_rule_adjoint_tc(a, b8(0), ao, stream) == 0 &&
                     mesa::launch_rule_grads_tc(a, b8(0), so, ao, Hk != H ? f(9) : nullptr, Hk != H ? f(10) : nullptr,
                                                stream) == 0;

@@ -57,12 +57,21 @@ struct RuleOperands {
   uint8_t *S = nullptr, *U = nullptr;
   float *iS = nullptr, *iU = nullptr;
 };
+// Segments of long sequences with few units: n segments of `per` chunks.
+struct RuleSegments {
+  int n = 1, per = 0;
+  float2 *bounds = nullptr;  // [U, NC] log2 of what a chunk leaves of a state; what it adds to a row (bounds)
+  float *S = nullptr, *loc = nullptr, *Tr = nullptr;  // [U, n][128 x 128] the state before; what it leaves
+  int *whole = nullptr;  // [U, n] whether what went before counts (Tr is there and to be applied)
+};
 size_t rule_tc_workspace(int U, int T);
-int launch_rule_prep(const RuleArgs &a, void *records, bool with_beta, cudaStream_t st);
+RuleSegments rule_tc_segments(int U, int T, void *workspace);
+int launch_rule_prep(const RuleArgs &a, void *records, const RuleSegments &sg, bool with_beta, cudaStream_t st);
 int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st);
 // The backward on the tensor cores, from the records (without beta): the states and u before the
 // adjoint chain, the adjoint chain, the gradients.
-int launch_rule_states_tc(const RuleArgs &a, const void *records, const RuleOperands &so, cudaStream_t st);
+int launch_rule_states_tc(const RuleArgs &a, const void *records, const RuleSegments &sg, const RuleOperands &so,
+                          cudaStream_t st);
 int launch_rule_adjoint_tc(const RuleArgs &a, const void *records, const RuleOperands &ao, cudaStream_t st);
 int launch_rule_grads_tc(const RuleArgs &a, const void *records, const RuleOperands &so, const RuleOperands &ao,
                          float *dqp, float *dkp, cudaStream_t st);

@@ -34,15 +34,20 @@ constexpr uint32_t PR_MISC = (PR_SCR + sizeof(Factor) > TILE ? PR_SCR + sizeof(F
 static_assert(PR_MISC % 16 == 0, "misc alignment");
 struct PrepMisc {
   alignas(16) uint32_t red[8];
+  float grow[C], give[C];
+  uint32_t vmax[4];
   uint64_t mbar, drain;
   uint32_t tmem;
 };
 constexpr uint32_t PR_SMEM = PR_MISC + sizeof(PrepMisc) + 1024;
 
-// grid (NC, U), 128 threads.  WITH_BETA: the record's factor is T diag(beta), else T.
-// Measured (8 x 16 x 4096, 8192 chunks): see the table at the launch.
+// grid (NC, U), 128 threads.  WITH_BETA: the record's factor is T diag(beta), else T.  bounds [U, NC]
+// (or nullptr): log2 of how much of a state the chunk leaves, at most, the product over its tokens of
+// gamma max(1, |1 - beta k.k|) (the norm of gamma (I - beta k k^T)); and a bound of the norm of what it adds
+// to a row of the state, the largest |v| times the sum of beta |k|.  Numbers that are none (or
+// that could end in an overflow) bound nothing: infinity or NaN.
 template <bool WITH_BETA>
-__global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint8_t *records) {
+__global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint8_t *records, float2 *bounds) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   PrepMisc *m = reinterpret_cast<PrepMisc *>(sm + PR_MISC);
@@ -104,6 +109,11 @@ __global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = __shfl_sync(0xffffffffu, m->tmem, 0), bar = tc::smem_u32(&m->mbar);
+  if (bounds) {  // the values, on their way during the products
+    const uint4 *vp = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + tok0 * D);
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = 128 * i + tid < n * (D / 8) ? vp[128 * i + tid] : make_uint4(0, 0, 0, 0);
+  }
   if (warp == 0 && elect_one()) {  // rows 0..63: K K^T, rows 64..127: Q K^T
     const uint32_t id = tc::idesc_f16(128, C, false, false);
     const uint64_t t = tc::kmajor_desc(tc::smem_u32(sm), 128, 0);
@@ -113,6 +123,13 @@ __global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint
   }
   const bool done = tc::mbar_wait(bar, 0, a.wait_limit);
   tc::fence_after_sync();
+  if (bounds) {
+    uint32_t mv = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) mv = absmax_words(mv, x[i]);
+    mv = absmax_fold(mv);
+    if (lane == 0) m->vmax[warp] = mv;
+  }
   if (__syncthreads_or(!done)) {
     if (tid == 0) atomicOr(a.status, tc::kErrMmaTimeout);
     const bool issuer = warp == 0 && elect_one();
@@ -124,9 +141,32 @@ __global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint
     factor_clear(rec, tid);
     factor_clear(rec + SQ, tid);
     __syncthreads();
+    if (bounds && tid < C) {  // (the diagonal of K K^T: column i of row i)
+      float kk = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float x[16];
+        tc::tmem_ld16(tbase + ((uint32_t)(32 * warp) << 16) + 32 * warp + 16 * h, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; k++)
+          if (16 * h + k == lane) kk = x[k];
+      }
+      kk *= ik * ik;
+      const float grow = fabsf(1.0f - be * kk);  // (0.003: k's rounding to fp16)
+      m->grow[tid] = grow <= 1.0f ? 0.0f : grow < INFINITY ? log2f(grow) + 0.003f : INFINITY;
+      m->give[tid] = fabsf(be) * sqrtf(kk) * 1.002f;
+    }
     factor_rows(s, tbase, ik * ik, rec + SQ, tid);
     tc::fence_before_sync();
     __syncthreads();
+    if (bounds && warp == 3) {
+      const float grow = warp_sum(m->grow[lane] + m->grow[lane + 32]), give = warp_sum(m->give[lane] + m->give[lane + 32]);
+      const float vmax = __uint_as_float(max(max(m->vmax[0], m->vmax[1]), max(m->vmax[2], m->vmax[3])) << 16);
+      const float adds = vmax * give * exp2f(grow);
+      if (lane == 0)
+        bounds[(size_t)u * NC + c] = make_float2((s.z[C - 1] != 0 ? -1e30f : s.l[C - 1]) + grow, adds < 1e30f ? adds : INFINITY);
+    }
     factor_diagonal<WITH_BETA>(s, rec, warp, lane);
     __syncthreads();
     if (warp < 3) factor_columns<WITH_BETA>(s, rec, warp, lane);
@@ -156,6 +196,7 @@ struct ChainMisc {
   uint64_t mma1, mma2, mma3, mma4, drain;
   uint32_t tmem;
   int gave_up;
+  float rest, rest0;  // a bound of what the chunks before can have left, of the part of S0 that can be left
 };
 constexpr uint32_t CH_SMEM = CH_MISC + sizeof(ChainMisc) + 1024;
 static_assert(CH_SMEM <= 232448, "shared memory per block");
@@ -185,19 +226,81 @@ constexpr int kRegChain = 240, kRegHelper = 136, kRegConvert = 120;
 static_assert(kRegChain + kRegHelper + kRegConvert <= 3 * 168, "register file");
 
 // grid U, 384 threads: warps 0-3 chain, 4-7 helper, 8-11 convert.
-// FWD: the forward; the records hold T diag(beta).  Otherwise the backward's pass over the states: the
-// records hold T, nothing is read out, and the state before each chunk and the chunk's u are kept as
-// operands with one scale each (so.S, so.U).
-template <bool FWD>
+// kFwd: the forward.  kKeep: the backward's pass over the states: the records hold T without beta, nothing
+// is read out, and the state before each chunk and the chunk's u are kept as operands with one scale
+// each (so.S, so.U).  Grid (U, segments): a segment's CTA starts from the state in sg.
+// kSegment: what the segments start from: the state that segment y leaves when it starts from zero (the
+// first: from S0), and, where that is not all, the matrix that takes the state before it to its part
+// of the state after it (the rows of the identity without values).  First, grid (U, segments - 1): only
+// the chunks at the segment's end of which 2^-40 of a state is left, from zero; that is all when the
+// bounds of all that went before say that it adds less than 2^-26 of each row's largest element (the
+// operands carry 2^-12).  Then, grid (U, segments - 1, 2), the segments where it was not: all their chunks
+// (z = 0), the matrix (z = 1).
+// kSegmentT: the same from records without beta.
+constexpr float kLittle = -40.0f;  // log2
+enum ChainMode { kFwd = 0, kKeep = 1, kSegment = 2, kSegmentT = 3 };
+template <int MODE>
 __global__ void __launch_bounds__(384, 1)
-    mesa_rule_chain_kernel(RuleArgs a, const uint8_t *records, RuleOperands so, const __grid_constant__ CUtensorMap mapV,
-                           const __grid_constant__ CUtensorMap mapO) {
-  constexpr int NT = FWD ? 3 : 2;  // operand tiles
+    mesa_rule_chain_kernel(RuleArgs a, const uint8_t *records, RuleOperands so, RuleSegments sg,
+                           const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO) {
+  constexpr bool FWD = MODE == kFwd, KEEP = MODE == kKeep, SEG = MODE >= kSegment, BETA = KEEP || MODE == kSegmentT;
+  constexpr int NT = KEEP ? 2 : 3;  // operand tiles
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   ChainMisc *m = reinterpret_cast<ChainMisc *>(sm + CH_MISC);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // (warp: uniform)
-  const int u = blockIdx.x, T = a.T, NC = (T + C - 1) / C;
+  const int u = blockIdx.x, seg = blockIdx.y, T = a.T, NCT = (T + C - 1) / C;
+  const bool identity = SEG && blockIdx.z == 1, tail = SEG && gridDim.z == 1;
+  // this CTA's chunks: NC of them from c0 on (the loops count them from 0)
+  int c0 = sg.n > 1 ? seg * sg.per : 0, NC = sg.n > 1 ? min(NCT - c0, sg.per) : NCT;
+  const float *start = seg == 0 ? a.S0 : sg.S + ((size_t)u * sg.n + seg) * D * D;  // (nullptr: zero)
+  if constexpr (SEG) {
+    int *whole = sg.whole + (size_t)u * sg.n + seg;
+    if (seg > 0 || tail) start = nullptr;
+    if (tail) {
+      const int end = c0 + NC, lo = c0;
+      float left = 0.0f;
+      c0 = end;
+      while (c0 > lo && !(left <= kLittle)) left += sg.bounds[(size_t)u * NCT + --c0].x;
+      NC = end - c0;
+      if (!(left <= kLittle)) {
+        if (tid == 0) *whole = 1;
+        return;
+      }
+      if (warp == 11) {  // what the chunks before c0 can have left: four a lane, backwards
+        float rest = 0.0f;
+        for (int j0 = c0; j0 > 0; j0 -= 128) {
+          const int j = j0 - 1 - 4 * lane;
+          float2 b[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) b[i] = j - i >= 0 ? sg.bounds[(size_t)u * NCT + j - i] : make_float2(0, 0);
+          const float mine = b[0].x + b[1].x + b[2].x + b[3].x;
+          float run = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += x;
+          }
+          const float total = __shfl_sync(0xffffffffu, run, 31);
+          float after = left + __shfl_up_sync(0xffffffffu, run, 1);
+          if (lane == 0) after = left;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            rest = fmaf(b[i].y, exp2f(after), rest);
+            after += b[i].x;
+          }
+          left += total;
+        }
+        rest = warp_sum(rest);
+        if (lane == 0) {
+          m->rest = rest;
+          m->rest0 = exp2f(left);  // of S0
+        }
+      }
+    } else if (!*whole || (identity && seg == 0)) {
+      return;
+    }
+  }
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
@@ -206,12 +309,12 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t b = bar(m->v_full), dst = tc::smem_u32(sm + CH_V);
     tc::mbar_arrive_expect_tx(b, ROWS64);
 #pragma unroll
-    for (int h = 0; h < 2; h++) tensor_g2s_3d(dst + h * C * 128, &mapV, 64 * h, c * C, u, b);
+    for (int h = 0; h < 2; h++) tensor_g2s_3d(dst + h * C * 128, &mapV, 64 * h, (c0 + c) * C, u, b);
   };
   auto fetch_rec = [&](int c) {
     const uint32_t b = bar(m->rec_full[c % 3]);
     tc::mbar_arrive_expect_tx(b, REC);
-    tc::bulk_g2s(tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD), records + ((size_t)u * NC + c) * REC, REC, b);
+    tc::bulk_g2s(tc::smem_u32(sm + CH_REC + (c % 3) * REC_PAD), records + ((size_t)u * NCT + c0 + c) * REC, REC, b);
   };
   if (warp == 0) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
   if (tid == 128) {
@@ -244,10 +347,14 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
     u64 S[D / 2];
     {
-      const float4 *src = a.S0 ? reinterpret_cast<const float4 *>(a.S0 + ((size_t)u * D + r) * D) : nullptr;
+      const size_t at = SEG || seg == 0 ? ((size_t)u * D + r) * D : (size_t)r * D;
+      const float4 *src = start ? reinterpret_cast<const float4 *>(start + at) : nullptr;
 #pragma unroll
       for (int g = 0; g < D / 4; g++) {
-        const float4 x = src ? src[g] : make_float4(0, 0, 0, 0);
+        float4 x = src ? src[g] : make_float4(0, 0, 0, 0);
+        if (identity)
+          x = make_float4(r == 4 * g ? 1.0f : 0.0f, r == 4 * g + 1 ? 1.0f : 0.0f, r == 4 * g + 2 ? 1.0f : 0.0f,
+                          r == 4 * g + 3 ? 1.0f : 0.0f);
         S[2 * g] = pack2(x.x, x.y);
         S[2 * g + 1] = pack2(x.z, x.w);
       }
@@ -267,7 +374,7 @@ __global__ void __launch_bounds__(384, 1)
     // the bound that scales the operand: the row's, or that of all rows where the operand is kept
     auto all_rows = [&](float b) -> float {  // after a barrier that follows put_rows
       const float4 x = *reinterpret_cast<const float4 *>(m->bmax);
-      return FWD ? b : fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
+      return KEEP ? fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) : b;
     };
     auto put_rows = [&](float b) {
       const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(b));
@@ -277,7 +384,7 @@ __global__ void __launch_bounds__(384, 1)
       *reinterpret_cast<float4 *>(sm + CH_STAGE + tile_off(r, 2 * k, 128)) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4 *>(sm + CH_STAGE + tile_off(r, 2 * k + 1, 128)) = make_float4(v[4], v[5], v[6], v[7]);
     };
-    if constexpr (!FWD) {
+    if constexpr (KEEP) {
       put_rows(bS);
       group_or(1, 128, false);
     }
@@ -290,7 +397,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = half2_bits(mul2(S[8 * k + i], s2));
         tc::tmem_st8(tl + T_S + 8 * k, v);
-        if constexpr (!FWD) keep_words(k, v);
+        if constexpr (KEEP) keep_words(k, v);
       }
       tc::tmem_st_wait();
     }
@@ -312,7 +419,7 @@ __global__ void __launch_bounds__(384, 1)
                   *inv = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_S);
       ok &= wait(bar(m->tile_full[c % NT]), (c / NT) & 1, limit, gave_up);
       if (c > 0) ok &= wait(bar(m->o_free), (c - 1) & 1, limit, gave_up);  // (the last readout is read)
-      if constexpr (!FWD) tc::fence_smem_to_async();
+      if constexpr (KEEP) tc::fence_smem_to_async();
       if (meet()) break;
       if (warp == 0 && elect_one()) {
         const uint64_t kq = tc::kmajor_desc(tile, 128, 0);
@@ -321,11 +428,12 @@ __global__ void __launch_bounds__(384, 1)
           tc::mma_f16_ts(tbase + T_D1, tbase + T_S + 8 * s, kq + step128(s), FWD ? id128 : id64, s > 0);
         tc::mma_commit(bar(m->mma1));
       }
-      if constexpr (!FWD) {
+      if constexpr (KEEP) {
         if (r == 32) {
-          bulk_s2g(so.S + ((size_t)u * NC + c) * TILE, tc::smem_u32(sm + CH_STAGE), TILE);
+          const size_t at = (size_t)u * NCT + c0 + c;
+          bulk_s2g(so.S + at * TILE, tc::smem_u32(sm + CH_STAGE), TILE);
           tc::bulk_commit();
-          so.iS[(size_t)u * NC + c] = iS;
+          so.iS[at] = iS;
         }
       }
       ok &= wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
@@ -334,10 +442,10 @@ __global__ void __launch_bounds__(384, 1)
       if constexpr (FWD) m->o1[ph][r] = -a.scale * iS * inv[1];
       const float w1 = iS * iK;  // units of D1
       float iR;
-      const float sR = bound_scale(fmaf((float)D * kmax, bS, m->vmax[warp]), FWD ? kTopRow : kTopRow - 2, iR);  // (beta < 4)
+      const float sR = bound_scale(fmaf((float)D * kmax, bS, m->vmax[warp]), BETA ? kTopRow - 2 : kTopRow, iR);  // (beta < 4)
       const u64 w1_2 = pack2(w1, w1), sR2 = pack2(sR, sR);
       const float *be = cc + C;
-      if constexpr (!FWD) m->o1[ph][r] = iR;
+      if constexpr (KEEP) m->o1[ph][r] = iR;
       ok &= wait(bar(m->mma1), ph, limit, gave_up);
       tc::fence_after_sync();
       // R = V^T - f D1, 16 tokens at a time (few registers beside the state's 128: what spills
@@ -359,7 +467,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int k = 0; k < 4; k++) {
             ulonglong2 bb = make_ulonglong2(sR2, sR2);
-            if constexpr (!FWD) {
+            if constexpr (BETA) {
               bb = *reinterpret_cast<const ulonglong2 *>(be + 16 * h + 4 * k);
               bb = make_ulonglong2(mul2(bb.x, sR2), mul2(bb.y, sR2));
             }
@@ -420,7 +528,7 @@ __global__ void __launch_bounds__(384, 1)
       bS = fmaf(all, bS, (float)C * uU * iR * kmax);
       if constexpr (FWD) {
         m->o2[ph][r] = a.scale * w3 * inv[1];
-      } else {
+      } else if constexpr (KEEP) {
         put_rows(bS);
         const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(uU * iR));
         if (lane == 0) m->umax[ph][warp] = __uint_as_float(w);
@@ -454,17 +562,31 @@ __global__ void __launch_bounds__(384, 1)
             v[i] = half2_bits(mul2(S[8 * k + i], sS2));
           }
           tc::tmem_st8(tl + T_S + 8 * k, v);  // the next chunk's operand
-          if constexpr (!FWD) keep_words(k, v);
+          if constexpr (KEEP) keep_words(k, v);
         }
         tc::tmem_st_wait();
       }
       if ((c & 7) == 7) row_max();  // (before the bound is loose)
     }
-    if constexpr (!FWD) {
+    if constexpr (KEEP) {
       if (r == 32) tc::bulk_wait_all();
     }
-    if (!group_or(1, 128, !ok) && FWD && a.S_final) {
-      float4 *dst = reinterpret_cast<float4 *>(a.S_final + ((size_t)u * D + r) * D);
+    float *final = SEG ? (identity ? sg.Tr : sg.loc) + ((size_t)u * sg.n + seg) * D * D
+                   : FWD && a.S_final && c0 + NC == NCT ? a.S_final + (size_t)u * D * D : nullptr;
+    if (SEG && tail) {  // is that all?  (a NaN or an infinity anywhere: no)
+      row_max();
+      float before = m->rest;
+      if (a.S0) {
+        const float *src = a.S0 + ((size_t)u * D + r) * D;
+        float x = 0.0f;
+        for (int j = 0; j < D; j++) x += fabsf(src[j]);
+        before = fmaf(x, m->rest0, before);
+      }
+      const int more = group_or(1, 128, !(before <= 0x1p-26f * bS));
+      if (r == 0) sg.whole[(size_t)u * sg.n + seg] = more;
+    }
+    if (!group_or(1, 128, !ok) && final) {
+      float4 *dst = reinterpret_cast<float4 *>(final + (size_t)r * D);
 #pragma unroll
       for (int g = 0; g < D / 4; g++) {
         float4 x;
@@ -480,6 +602,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tl = tbase + ((uint32_t)(32 * (warp - 4)) << 16);
     auto transpose = [&](int c) -> bool {  // chunk c's values (the last chunk's have been used)
       if (group_or(2, 128, !wait(bar(m->v_full), c & 1, limit, gave_up))) return false;
+      const uint32_t live = identity ? 0u : 0xffffffffu;  // (rows of the identity take no values)
       // channels 32 w .. 32 w + 31 by warp w: eight channels x 32 tokens at a time
       uint32_t mv = 0;
 #pragma unroll 1
@@ -489,6 +612,8 @@ __global__ void __launch_bounds__(384, 1)
         for (int t = 0; t < 2; t++) {
           uint32_t x[4];
           ldmatrix_x4_trans(x, tc::smem_u32(sm + CH_V + tile_off(32 * t + lane, ch8, C)));
+#pragma unroll
+          for (int k = 0; k < 4; k++) x[k] &= live;
           mv = absmax_words(mv, make_uint4(x[0], x[1], x[2], x[3]));
           const int r = 8 * ch8 + (lane >> 2);
 #pragma unroll
@@ -533,6 +658,14 @@ __global__ void __launch_bounds__(384, 1)
         ok = false;
         break;
       }
+      if constexpr (SEG) {  // nothing to write
+        warp_arrive(m->o_free);
+        if (c + 3 < NC) {
+          if (h == 0) fetch_rec(c + 3);
+          rec_sent++;
+        }
+        continue;
+      }
       tc::fence_after_sync();
       const float *nf = reinterpret_cast<const float *>(sm + CH_REC + (c % 3) * REC_PAD + REC_F);
       // 16 channels at a time in fragments of 8 tokens (this thread: channels T / 4 and T / 4 + 8, tokens
@@ -546,7 +679,7 @@ __global__ void __launch_bounds__(384, 1)
       warp_arrive(m->o_free);
       const int w = warp - 4, q = 2 * (lane & 3);
       float su = 1.0f, iu = 1.0f;
-      if constexpr (!FWD) {
+      if constexpr (KEEP) {
         const float4 b = *reinterpret_cast<const float4 *>(m->umax[c & 1]);
         su = bound_scale(fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)), kTopRow, iu);
       }
@@ -568,7 +701,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
             const int j = 8 * p + 4 * e;
-            if constexpr (!FWD) {
+            if constexpr (KEEP) {
               o[2 * e] = __float_as_uint(half2_bits(mul2(pack2(z[j], z[j + 1]), a1)));
               o[2 * e + 1] = __float_as_uint(half2_bits(mul2(pack2(z[j + 2], z[j + 3]), b1)));
               continue;
@@ -589,10 +722,11 @@ __global__ void __launch_bounds__(384, 1)
       if (h == 0) {
         if constexpr (FWD) {
 #pragma unroll
-          for (int b = 0; b < 2; b++) tensor_s2g_3d(&mapO, tc::smem_u32(sm + CH_OUT + b * C * 128), 64 * b, c * C, u);
+          for (int b = 0; b < 2; b++) tensor_s2g_3d(&mapO, tc::smem_u32(sm + CH_OUT + b * C * 128), 64 * b, (c0 + c) * C, u);
         } else {
-          bulk_s2g(so.U + ((size_t)u * NC + c) * ROWS64, tc::smem_u32(sm + CH_OUT), ROWS64);
-          so.iU[(size_t)u * NC + c] = iu;
+          const size_t at = (size_t)u * NCT + c0 + c;
+          bulk_s2g(so.U + at * ROWS64, tc::smem_u32(sm + CH_OUT), ROWS64);
+          so.iU[at] = iu;
         }
         tc::bulk_commit();
         if (c + 3 < NC) fetch_rec(c + 3);  // (the chain is past this record, and so is the group)
@@ -605,11 +739,11 @@ __global__ void __launch_bounds__(384, 1)
     // ---- K and Q as operands, up to three chunks in flight ----
     regs_down<kRegConvert>();
     const int h = tid - 256, r0 = h >> 4, c8 = h & 15, uk = a.qk_unit(u);  // rows r0, r0 + 8 ..; 8 channels
-    const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + ((size_t)uk * T + r0) * D + 8 * c8;
-    const __nv_bfloat16 *qp = (const __nv_bfloat16 *)a.q + ((size_t)uk * T + r0) * D + 8 * c8;
+    const size_t first = ((size_t)uk * T + (size_t)c0 * C + r0) * D + 8 * c8;
+    const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + first, *qp = (const __nv_bfloat16 *)a.q + first;
     uint4 x[8], y[8];  // the next chunk's rows, on their way while this one's are converted
     auto load = [&](int c) {
-      const int n = T - c * C - r0;
+      const int n = T - (c0 + c) * C - r0;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         x[i] = y[i] = make_uint4(0, 0, 0, 0);
@@ -663,43 +797,131 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0) tc::tmem_free(tbase, 512);
 }
 
-template <bool FWD>
-int launch_chain(const RuleArgs &a, const uint8_t *records, const RuleOperands &so, const CUtensorMap &mapV,
-                 const CUtensorMap &mapO, cudaStream_t st) {
-  auto kfn = mesa_rule_chain_kernel<FWD>;
+// The state before each segment from the segments' own: S_{y+1} = S_y Tr_y + loc_y (S_1 = loc_0), sixteen
+// rows by a CTA of 256 threads; grid (8, U).
+__global__ void __launch_bounds__(256) mesa_rule_join_kernel(RuleSegments sg) {
+  __shared__ float rows[16][D + 4];
+  const int u = blockIdx.y, row0 = 16 * blockIdx.x, tid = threadIdx.x;
+  const int r = tid >> 4, c0 = (tid & 15) * 8;  // row r, columns c0 ..
+  for (int y = 0; y + 1 < sg.n; y++) {
+    const size_t at = (size_t)u * sg.n + y;
+    const float *loc = sg.loc + at * D * D + (size_t)(row0 + r) * D + c0;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = loc[i];
+    if (y > 0 && sg.whole[at]) {
+      const float *Tr = sg.Tr + at * D * D + c0;
+      for (int k = 0; k < D; k++) {
+        const float s = rows[r][k];
+        const float4 p = *reinterpret_cast<const float4 *>(Tr + (size_t)k * D);
+        const float4 q = *reinterpret_cast<const float4 *>(Tr + (size_t)k * D + 4);
+        x[0] = fmaf(s, p.x, x[0]);
+        x[1] = fmaf(s, p.y, x[1]);
+        x[2] = fmaf(s, p.z, x[2]);
+        x[3] = fmaf(s, p.w, x[3]);
+        x[4] = fmaf(s, q.x, x[4]);
+        x[5] = fmaf(s, q.y, x[5]);
+        x[6] = fmaf(s, q.z, x[6]);
+        x[7] = fmaf(s, q.w, x[7]);
+      }
+    }
+    __syncthreads();
+    float *dst = sg.S + (at + 1) * D * D + (size_t)(row0 + r) * D + c0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      rows[r][c0 + i] = x[i];
+      dst[i] = x[i];
+    }
+    __syncthreads();
+  }
+}
+
+template <int MODE>
+int launch_chain(const RuleArgs &a, const uint8_t *records, const RuleOperands &so, const RuleSegments &sg, dim3 grid,
+                 const CUtensorMap &mapV, const CUtensorMap &mapO, cudaStream_t st) {
+  auto kfn = mesa_rule_chain_kernel<MODE>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)CH_SMEM) != cudaSuccess) return -1;
-  timing_mark_begin(K_RULE_CHAIN, st);
-  kfn<<<a.units(), 384, CH_SMEM, st>>>(a, records, so, mapV, mapO);
-  timing_mark_end(K_RULE_CHAIN, st);
+  timing_mark_begin(MODE >= kSegment ? K_RULE_SEGMENT : K_RULE_CHAIN, st);
+  kfn<<<grid, 384, CH_SMEM, st>>>(a, records, so, sg, mapV, mapO);
+  timing_mark_end(MODE >= kSegment ? K_RULE_SEGMENT : K_RULE_CHAIN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
+// Segments of a unit's NC chunks: as many CTAs as a GB300 has SMs (152), at least six chunks each.  Where
+// gates hardly decay the two starting passes take as long as two segments, so n segments take 3/n of
+// the time of one pass, and fewer than five are not worth it.
+int segments(int U, int NC) {
+  const int n = U > 0 ? (152 / U < NC / 6 ? 152 / U : NC / 6) : 1;
+  return n < 5 ? 1 : n;
+}
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
 }  // namespace
 
+// [records | chunk bounds | states before segments, their own states, matrices | matrix flags]
 size_t rule_tc_workspace(int U, int T) {
-  return (size_t)U * (((size_t)T + C - 1) / C) * REC;
+  const int NC = (T + C - 1) / C, n = segments(U, NC);
+  const size_t rec = up256((size_t)U * NC * REC);
+  return n == 1 ? rec : rec + up256((size_t)U * NC * 8) + 3 * (size_t)U * n * D * D * 4 + up256((size_t)U * n * 4);
+}
+RuleSegments rule_tc_segments(int U, int T, void *workspace) {
+  const int NC = (T + C - 1) / C;
+  RuleSegments sg;
+  sg.n = segments(U, NC);
+  if (sg.n == 1) return sg;
+  sg.per = (NC + sg.n - 1) / sg.n;
+  sg.n = (NC + sg.per - 1) / sg.per;  // (no empty one; the strides of the arrays are this count's)
+  uint8_t *w = (uint8_t *)workspace + up256((size_t)U * NC * REC);
+  const size_t mats = (size_t)U * sg.n * D * D;
+  sg.bounds = (float2 *)w;
+  sg.S = (float *)(w + up256((size_t)U * NC * 8));
+  sg.loc = sg.S + mats;
+  sg.Tr = sg.loc + mats;
+  sg.whole = (int *)(sg.Tr + mats);
+  return sg;
 }
 
-int launch_rule_prep(const RuleArgs &a, void *records, bool with_beta, cudaStream_t st) {
+int launch_rule_prep(const RuleArgs &a, void *records, const RuleSegments &sg, bool with_beta, cudaStream_t st) {
   auto kfn = with_beta ? mesa_rule_prep_kernel<true> : mesa_rule_prep_kernel<false>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PR_SMEM) != cudaSuccess) return -1;
   timing_mark_begin(K_RULE_PREP, st);
-  kfn<<<dim3((a.T + C - 1) / C, a.units()), 128, PR_SMEM, st>>>(a, (uint8_t *)records);
+  kfn<<<dim3((a.T + C - 1) / C, a.units()), 128, PR_SMEM, st>>>(a, (uint8_t *)records, sg.bounds);
   timing_mark_end(K_RULE_PREP, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
+namespace {
+// What every segment but the first starts from.
+template <bool WITH_BETA>
+int launch_segments(const RuleArgs &a, const uint8_t *records, const RuleSegments &sg, const CUtensorMap &mapV,
+                    cudaStream_t st) {
+  if (sg.n == 1) return 0;
+  for (int z = 1; z <= 2; z++)
+    if (launch_chain<WITH_BETA ? kSegment : kSegmentT>(a, records, RuleOperands{}, sg, dim3(a.units(), sg.n - 1, z), mapV, mapV,
+                                                       st) != 0)
+      return -1;
+  timing_mark_begin(K_RULE_JOIN, st);
+  mesa_rule_join_kernel<<<dim3(8, a.units()), 256, 0, st>>>(sg);
+  timing_mark_end(K_RULE_JOIN, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+}  // namespace
+
 int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st) {
+  const RuleSegments sg = rule_tc_segments(a.units(), a.T, workspace);
+  const uint8_t *records = (const uint8_t *)workspace;
   CUtensorMap mapV{}, mapO{};
   if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T) || !tmap_units128_bf16(&mapO, a.out, a.units(), a.T)) return -1;
-  if (launch_rule_prep(a, workspace, true, st) != 0) return -1;
-  return launch_chain<true>(a, (const uint8_t *)workspace, RuleOperands{}, mapV, mapO, st);
+  if (launch_rule_prep(a, workspace, sg, true, st) != 0 || launch_segments<true>(a, records, sg, mapV, st) != 0) return -1;
+  return launch_chain<kFwd>(a, records, RuleOperands{}, sg, dim3(a.units(), sg.n), mapV, mapO, st);
 }
 
-int launch_rule_states_tc(const RuleArgs &a, const void *records, const RuleOperands &so, cudaStream_t st) {
+int launch_rule_states_tc(const RuleArgs &a, const void *records, const RuleSegments &sg, const RuleOperands &so,
+                          cudaStream_t st) {
   CUtensorMap mapV{};
   if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T)) return -1;
-  return launch_chain<false>(a, (const uint8_t *)records, so, mapV, mapV, st);
+  if (launch_segments<false>(a, (const uint8_t *)records, sg, mapV, st) != 0) return -1;
+  return launch_chain<kKeep>(a, (const uint8_t *)records, so, sg, dim3(a.units(), sg.n), mapV, mapV, st);
 }
 
 }  // namespace mesa

@@ -94,7 +94,7 @@ enum KernelKind {
   K_PREPROC = 8, K_BWD_RHS = 9, K_BWD_STATES = 10, K_BWD_GRAD = 11, K_BWD_FSTATES = 12,
   K_CG_TC64 = 13, K_CARRY_TC = 14, K_BWD_SPROD = 15, K_RULE_SCAN = 16, K_RULE_GRADS = 17, K_RULE_GROUP = 18,
   K_RULE_STEP = 19, K_NORM = 20, K_NORM_BWD = 21, K_NORM_COLS = 22, K_RULE_PREP = 23, K_RULE_CHAIN = 24,
-  K_RULE_ADJOINT = 25, K_NUM_KINDS = 26
+  K_RULE_ADJOINT = 25, K_RULE_SEGMENT = 26, K_RULE_JOIN = 27, K_NUM_KINDS = 28
 };
 
 // Record a timing event before / after a launch of `kind` on `st` (no-op unless enabled).

@@ -313,3 +313,85 @@ def test_wait_give_up_reports_timeout_and_the_next_call_is_clean():
     got, codes = run()
     assert codes == [(binding.MESA_OK, 0)] * 2
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def _long_inputs(T, gates, S0, seed=31):
+    """One (batch, head) unit pair of T tokens, bf16, d = 128: so few units that the sequence is cut
+    into segments."""
+    s = ref.rule_inputs(seed, "bf16", 1, 2, 2, T, 128, 128, "open", S0)
+    r = np.random.default_rng(seed + 1)
+    if gates == "kept":  # hardly any decay: every segment needs the state before it
+        s["gamma"] = r.uniform(0.9995, 1.0, s["gamma"].shape).astype(np.float32)
+    elif gates == "loud":  # the first half 2^30 times louder than the rest: still there after a long decay
+        s["v"][:, :, :T // 2] *= 2.0 ** 15
+        s["v"][:, :, T // 2:] *= 2.0 ** -15
+        s["gamma"] = r.uniform(0.97, 1.0, s["gamma"].shape).astype(np.float32)
+    elif gates == "mixed":  # one unit that keeps, one that forgets; a closed gate and zero betas
+        s["gamma"][:, 0] = r.uniform(0.999, 1.0, s["gamma"][:, 0].shape).astype(np.float32)
+        s["gamma"][:, 1, T // 3] = 0.0
+        s["beta"][:, :, T - T // 5:] = 0.0
+    return s
+
+
+LONG = [(1921, "open", True), (2500, "kept", True), (2048, "loud", False), (3001, "mixed", True), (2111, "kept", False)]
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_sequences_of_few_units(case):
+    import torch
+
+    from mesa_layer_gb300 import binding
+    T, gates, S0 = case
+    s = _long_inputs(T, gates, S0)
+    t = upload(s, "bf16")
+    SF = torch.full((1, 2, 128, 128), float("nan"), device="cuda")
+    out = binding.mesa_delta_forward_chunked(t["q"], t["k"], t["v"], t["gamma"], t["beta"], SCALE, S0=t["S0"], S_final=SF)
+    o, S = ref.rule_forward(s["q"], s["k"], s["v"], s["gamma"], s["beta"], SCALE, s["S0"])
+    if gates == "loud":  # (token norms span 2^30: by parts)
+        parts = [slice(i, i + 64) for i in range(0, T, 64)]
+        assert max(err(out[:, :, p], o[:, :, p]) for p in parts) <= TOL["bf16"]
+    assert err(out, o) <= TOL["bf16"]
+    assert err(SF, S) <= STATE_TOL["bf16"]
+
+
+@pytest.mark.parametrize("case", LONG[:2] + LONG[3:], ids=str)
+def test_gradients_of_long_sequences_of_few_units(case):
+    import torch
+
+    from mesa_layer_gb300 import binding
+    T, gates, S0 = case
+    s = _long_inputs(T, gates, S0)
+    t = upload(s, "bf16")
+    dS0 = torch.full((1, 2, 128, 128), float("nan"), device="cuda") if S0 else None
+    got = dict(zip(("dq", "dk", "dv", "dgamma", "dbeta"), binding.mesa_delta_backward_chunked(
+        t["q"], t["k"], t["v"], t["gamma"], t["beta"], t["dout"], SCALE, S0=t["S0"], dS_final=t["dS_final"], dS0=dS0)))
+    want = ref.rule_backward(s["q"], s["k"], s["v"], s["gamma"], s["beta"], SCALE, s["dout"], s["S0"], s["dS_final"])
+    found = {n: err(x, want[n]) for n, x in got.items()}
+    assert max(found.values()) <= TOL["bf16"], found
+    if S0:
+        assert err(dS0, want["dS0"]) <= STATE_TOL["bf16"]
+
+
+@pytest.mark.parametrize("what", ["v", "beta", "S0"])
+def test_nonfinite_values_last_through_long_sequences(what):
+    """A NaN early in a long sequence is still in the state at its end (0.9 ^ 3000 of it)."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    s = _long_inputs(3000 + 1, "open", True)
+    t = upload(s, "bf16")
+    if what == "S0":
+        t["S0"][0, 1, 5, 7] = float("nan")
+    elif what == "v":
+        t["v"][0, 1, 70, 5] = float("inf")
+    else:
+        t["beta"][0, 1, 70] = float("nan")
+    SF = torch.zeros((1, 2, 128, 128), device="cuda")
+    ws = torch.empty(binding.mesa_delta_workspace_size(1, 2, 2, 3001, 128, 128, torch.bfloat16), dtype=torch.uint8,
+                     device="cuda")
+    out = binding.mesa_delta_forward_chunked(t["q"], t["k"], t["v"], t["gamma"], t["beta"], SCALE, S0=t["S0"], S_final=SF,
+                                             workspace=ws)
+    assert binding.mesa_forward_status(ws) != 0
+    assert torch.isfinite(SF[0, 0]).all() and torch.isfinite(out[0, 0]).all()
+    assert not torch.isfinite(SF[0, 1, 5]).any()
+    assert not torch.isfinite(out[0, 1, -1, 5])
