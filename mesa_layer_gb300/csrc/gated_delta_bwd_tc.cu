@@ -448,16 +448,18 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
 
 // ---- the gradients of a chunk ---------------------------------------------------------------------
 // shared memory: [g; du] | u | [Q; K] | S0 | A | products' operand | X | misc.  (u as rows 64 .. 127 of a
-// 128-row operand: its descriptor starts 8 KB before it.)  dq and dk leave through [g; du]'s place.
+// 128-row operand: its descriptor starts 8 KB before it.)  dq and dk leave through the products' operand.
 constexpr uint32_t GR_A1 = 0, GR_U = TILE, GR_QK = GR_U + ROWS64, GR_S = GR_QK + TILE, GR_DS = GR_S + TILE, GR_A5 = GR_DS + TILE;
 constexpr int X_LD = 65;
 constexpr uint32_t GR_X = GR_A5 + TILE, GR_MISC = GR_X + ((C * X_LD * 4 + 127) & ~127);
+constexpr int GR_WARPS = 16, GR_SEGS = 8;
 struct GradsMisc {
-  float l[C], gam[C], nf[C], c[C], beta[C];
-  int z[C];
-  float duv[C], dbeta[2][C], xin[2][2][C], xout[2][C];
-  uint32_t red[8];
-  float cross[8];
+  float l[C], nf[C], c[C], beta[C], gam[C];
+  alignas(16) int z[C];
+  float duv[C], dbeta[4][C], xin[4][2][C], xout[4][C];
+  float head[GR_SEGS][C], dgam[2][C];
+  alignas(16) uint32_t red[GR_WARPS];
+  float cross[GR_WARPS];
   uint64_t load, mma_a, mma_b, mma_c, drain;
   uint32_t tmem;
 };
@@ -468,117 +470,156 @@ constexpr uint32_t T_G1 = 0, T_G2 = 128, T_G3 = 256, T_G4 = 320, T_G5 = 384;
 
 __device__ __forceinline__ float2 half2_at(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
-// grid (NC, U), 256 threads: warps w and w + 4 share tensor-memory lanes 32 w .., each half the columns.
-__global__ void __launch_bounds__(256, 1)
-    mesa_rule_grads_tc_kernel(RuleArgs a, const uint8_t *records, RuleOperands so, RuleOperands ao, float *dqp, float *dkp,
-                              const __grid_constant__ CUtensorMap mapDq, const __grid_constant__ CUtensorMap mapDk) {
+// 512 threads, one CTA per SM over `chunks` chunks of all units: the warps that share a quarter of the
+// tensor memory's lanes take a quarter of the columns each.  A chunk is a row of short steps that wait
+// for one another, so the next chunk's rows are on their way (in registers) from the middle of this one's, its states
+// and u from where this one's have been read.  (One CTA per chunk, 256 threads, nothing on its way: 875 us
+// at 8 x 16 x 4096 against the time below.)
+__global__ void __launch_bounds__(32 * GR_WARPS, 1)
+    mesa_rule_grads_tc_kernel(RuleArgs a, int NC, int chunks, const uint8_t *records, RuleOperands so, RuleOperands ao,
+                              float *dqp, float *dkp, const __grid_constant__ CUtensorMap mapDq,
+                              const __grid_constant__ CUtensorMap mapDk) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   GradsMisc *m = reinterpret_cast<GradsMisc *>(sm + GR_MISC);
   float *X = reinterpret_cast<float *>(sm + GR_X);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int c = blockIdx.x, u = blockIdx.y, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
-  const size_t at = (size_t)u * NC + c, tok0 = (size_t)u * a.T + t0, row0 = (size_t)a.qk_unit(u) * a.T + t0;
   const uint32_t bl = tc::smem_u32(&m->load), ba = tc::smem_u32(&m->mma_a), bb = tc::smem_u32(&m->mma_b),
                  bc = tc::smem_u32(&m->mma_c);
+  const int r0 = tid >> 4, c8 = tid & 15;  // rows of Q, K, g and v: 16 threads a row, rows r0 and r0 + 32
 
+  // what is read ahead
+  uint4 q4[2], k4[2], g4[2], v4[2];
+  float4 inv;
+  float iS, iu, iA, idu, tok;
+  auto fetch_rows = [&](int at) {
+    const int u = at / NC, t0 = (at - u * NC) * C, n = min(C, a.T - t0);
+    const size_t tok0 = (size_t)u * a.T + t0, row0 = (size_t)a.qk_unit(u) * a.T + t0;
+    const uint8_t *rec = records + (size_t)at * REC;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int r = r0 + 32 * i;
+      q4[i] = k4[i] = g4[i] = v4[i] = make_uint4(0, 0, 0, 0);
+      if (r < n) {
+        q4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + (row0 + r) * D + 8 * c8);
+        k4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + (row0 + r) * D + 8 * c8);
+        g4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.dout + (tok0 + r) * D + 8 * c8);
+        v4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + (tok0 + r) * D + 8 * c8);
+      }
+    }
+    inv = *reinterpret_cast<const float4 *>(rec + REC_S);
+    iS = so.iS[at], iu = so.iU[at], iA = ao.iS[at], idu = ao.iU[at];
+    const int t = tid & (C - 1), which = tid >> 6;  // a token's numbers, one kind to two warps
+    tok = which == 0   ? reinterpret_cast<const float *>(rec + REC_F)[t]
+          : which == 1 ? reinterpret_cast<const float *>(rec + REC_C)[t]
+          : which == 2 ? reinterpret_cast<const float *>(rec + REC_B)[t]
+          : t < n      ? a.gamma[tok0 + t]
+                       : 1.0f;
+  };
+  auto fetch_operands = [&](int at) {  // one thread
+    tc::mbar_arrive_expect_tx(bl, 2 * TILE + 2 * ROWS64);
+    tc::bulk_g2s(tc::smem_u32(sm + GR_U), so.U + (size_t)at * ROWS64, ROWS64, bl);
+#pragma unroll
+    for (int h = 0; h < 2; h++)  // du: rows 64 .. of both column halves
+      tc::bulk_g2s(tc::smem_u32(sm + GR_A1 + h * ROWS64 + C * 128), ao.U + (size_t)at * ROWS64 + h * C * 128, C * 128, bl);
+    tc::bulk_g2s(tc::smem_u32(sm + GR_S), so.S + (size_t)at * TILE, TILE, bl);
+    tc::bulk_g2s(tc::smem_u32(sm + GR_DS), ao.S + (size_t)at * TILE, TILE, bl);
+  };
+
+  int at = blockIdx.x;
   if (warp == 0) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
   if (tid == 32) {
     for (uint32_t b : {bl, ba, bb, bc, tc::smem_u32(&m->drain)}) tc::mbar_init(b, 1);
-    tc::mbar_arrive_expect_tx(bl, 2 * TILE + 2 * ROWS64);
-    tc::bulk_g2s(tc::smem_u32(sm + GR_U), so.U + at * ROWS64, ROWS64, bl);
-#pragma unroll
-    for (int h = 0; h < 2; h++)  // du: rows 64 .. of both column halves
-      tc::bulk_g2s(tc::smem_u32(sm + GR_A1 + h * ROWS64 + C * 128), ao.U + at * ROWS64 + h * C * 128, C * 128, bl);
-    tc::bulk_g2s(tc::smem_u32(sm + GR_S), so.S + at * TILE, TILE, bl);
-    tc::bulk_g2s(tc::smem_u32(sm + GR_DS), ao.S + at * TILE, TILE, bl);
+    fetch_operands(at);
   }
-  const uint8_t *rec = records + at * REC;
-  const float4 inv = *reinterpret_cast<const float4 *>(rec + REC_S);
-  const float iS = so.iS[at], iu = so.iU[at], iA = ao.iS[at], idu = ao.iU[at];
-  if (tid < C) {
-    m->nf[tid] = reinterpret_cast<const float *>(rec + REC_F)[tid];
-    m->c[tid] = reinterpret_cast<const float *>(rec + REC_C)[tid];
-    m->beta[tid] = reinterpret_cast<const float *>(rec + REC_B)[tid];
-    m->gam[tid] = tid < n ? a.gamma[tok0 + tid] : 1.0f;
-  }
-  if (warp == 7) {
-    const float *gp = a.gamma + tok0;
-    const GatePair g =
-        gate_scan(make_float2(2 * lane < n ? gp[2 * lane] : 1.0f, 2 * lane + 1 < n ? gp[2 * lane + 1] : 1.0f), lane);
-    *reinterpret_cast<float2 *>(&m->l[2 * lane]) = make_float2(g.l0, g.l1);
-    *reinterpret_cast<int2 *>(&m->z[2 * lane]) = make_int2(g.z0, g.z1);
-  }
-  // rows of Q, K and g: 16 threads a row, 16 rows a pass
-  const int r0 = tid >> 4, c8 = tid & 15;
-  uint4 g4[4];
-  uint32_t mg = 0;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int r = r0 + 16 * i;
-    uint4 k4 = make_uint4(0, 0, 0, 0), q4 = k4;
-    g4[i] = k4;
-    if (r < n) {
-      q4 = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + (row0 + r) * D + 8 * c8);
-      k4 = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + (row0 + r) * D + 8 * c8);
-      g4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.dout + (tok0 + r) * D + 8 * c8);
-    }
-    *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(r, c8, 128)) = to_half8(q4, pack2(inv.w, inv.w));
-    *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(C + r, c8, 128)) = to_half8(k4, pack2(inv.z, inv.z));
-    mg = absmax_words(mg, g4[i]);
-  }
-  mg = absmax_fold(mg);
-  if (lane == 0) m->red[warp] = mg;
-  // the products' operand: its block of Q columns for dq is zero
-  for (int i = tid; i < C * 8; i += 256)
-    *reinterpret_cast<uint4 *>(sm + GR_A5 + tile_off(i >> 3, i & 7, 128)) = make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  mg = 0;
-#pragma unroll
-  for (int w = 0; w < 8; w++) mg = max(mg, m->red[w]);
-  float ig;
-  const float sg = bound_scale(__uint_as_float(mg << 16), kTopTile, ig);
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-    *reinterpret_cast<uint4 *>(sm + GR_A1 + tile_off(r0 + 16 * i, c8, 128)) = to_half8(g4[i], pack2(sg, sg));
-  tc::fence_smem_to_async();
+  fetch_rows(at);
+  int fetched = 1;  // chunks' operands asked for
   tc::fence_before_sync();
-  const bool loaded = tc::mbar_wait(bl, 0, a.wait_limit);
-  bool stop = __syncthreads_or(!loaded);
+  __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = __shfl_sync(0xffffffffu, m->tmem, 0);
-  const uint64_t dA1 = tc::kmajor_desc(tc::smem_u32(sm + GR_A1), 128, 0), dQK = tc::kmajor_desc(tc::smem_u32(sm + GR_QK), 128, 0);
-  if (!stop && warp == 0 && elect_one()) {
-    const uint32_t id64 = tc::idesc_f16(128, C, false, false), idN = tc::idesc_f16(128, D, false, true);
-    const uint64_t dU = tc::kmajor_desc(tc::smem_u32(sm + GR_U), C, 0), dUhi = tc::kmajor_desc(tc::smem_u32(sm + GR_U) - C * 128, C, 0);
-    const uint64_t dK = tc::kmajor_desc(tc::smem_u32(sm + GR_QK) + C * 128, 128, 0);
-    const uint64_t nS = tc::mnmajor_desc(tc::smem_u32(sm + GR_S), 128, 0), nA = tc::mnmajor_desc(tc::smem_u32(sm + GR_DS), 128, 0);
-    // (a 64-row tile's second column half is 8 KB on)
-    auto step64x128 = [](int s) { return (uint64_t)((s >> 2) * 512 + (s & 3) * 2); };
-#pragma unroll
-    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G3, dA1 + step128(s), dU + step64x128(s), id64, s > 0);
-#pragma unroll
-    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G4, dQK + step128(s), dK + step128(s), id64, s > 0);
-    tc::mma_commit(ba);
-#pragma unroll
-    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G1, dA1 + step128(s), nS + step_mn(s), idN, s > 0);
-#pragma unroll
-    for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G2, dUhi + step64x128(s), nA + step_mn(s), idN, s > 0);
-    tc::mma_commit(bb);
-  }
-  __syncwarp();
+  // rows of the token x token products: row < 64: g_i and q_i, else du_i and k_i; a quarter of the columns
+  const int quad = warp & 3, part = warp >> 2, row = 32 * quad + lane, i = row & 63;
+  const bool upper = row < C;
+  const uint32_t tl = tbase + ((uint32_t)(32 * quad) << 16);
+  bool stop = false;
   float bad = 0.0f;  // NaN once a gradient was not finite
-  if (!stop) {
+
+  for (int it = 0; at < chunks; it++, at += gridDim.x) {
+    const uint32_t ph = it & 1;
+    const int u = at / NC, t0 = (at - u * NC) * C, n = min(C, a.T - t0);
+    const size_t tok0 = (size_t)u * a.T + t0;
+    const int next = at + (int)gridDim.x;
+    // this chunk's numbers (the read-ahead's registers take the next one's below)
+    const float4 cinv = inv;
+    const float ciS = iS, ciu = iu, ciA = iA, cidu = idu;
+    {
+      const int t = tid & (C - 1), which = tid >> 6;
+      if (which < 4) (which == 0 ? m->nf : which == 1 ? m->c : which == 2 ? m->beta : m->gam)[t] = tok;
+    }
+    uint32_t mg = 0;
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const int r = r0 + 32 * k;
+      *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(r, c8, 128)) = to_half8(q4[k], pack2(cinv.w, cinv.w));
+      *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(C + r, c8, 128)) = to_half8(k4[k], pack2(cinv.z, cinv.z));
+      mg = absmax_words(mg, g4[k]);
+    }
+    mg = absmax_fold(mg);
+    if (lane == 0) m->red[warp] = mg;
+    if (tid == 0) tc::bulk_wait_read();  // the last chunk's dq and dk have left their place
+    __syncthreads();
+    // the products' operand: its block of Q columns for dq is zero
+    *reinterpret_cast<uint4 *>(sm + GR_A5 + tile_off(tid >> 3, tid & 7, 128)) = make_uint4(0, 0, 0, 0);
+    mg = 0;
+#pragma unroll
+    for (int w = 0; w < GR_WARPS / 4; w++) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(m->red + 4 * w);
+      mg = max(mg, max(max(x.x, x.y), max(x.z, x.w)));
+    }
+    float ig;
+    const float sg = bound_scale(__uint_as_float(mg << 16), kTopTile, ig);
+#pragma unroll
+    for (int k = 0; k < 2; k++)
+      *reinterpret_cast<uint4 *>(sm + GR_A1 + tile_off(r0 + 32 * k, c8, 128)) = to_half8(g4[k], pack2(sg, sg));
+    if (warp == GR_WARPS - 1) {
+      const GatePair g = gate_scan(make_float2(m->gam[2 * lane], m->gam[2 * lane + 1]), lane);
+      *reinterpret_cast<float2 *>(&m->l[2 * lane]) = make_float2(g.l0, g.l1);
+      *reinterpret_cast<int2 *>(&m->z[2 * lane]) = make_int2(g.z0, g.z1);
+    }
+    tc::fence_smem_to_async();
+    tc::fence_before_sync();
+    const bool loaded = tc::mbar_wait(bl, ph, a.wait_limit);
+    stop = __syncthreads_or(!loaded);
+    tc::fence_after_sync();
+    if (stop) break;
+    const uint64_t dA1 = tc::kmajor_desc(tc::smem_u32(sm + GR_A1), 128, 0), dQK = tc::kmajor_desc(tc::smem_u32(sm + GR_QK), 128, 0);
+    if (warp == 0 && elect_one()) {
+      const uint32_t id64 = tc::idesc_f16(128, C, false, false), idN = tc::idesc_f16(128, D, false, true);
+      const uint64_t dU = tc::kmajor_desc(tc::smem_u32(sm + GR_U), C, 0), dUhi = tc::kmajor_desc(tc::smem_u32(sm + GR_U) - C * 128, C, 0);
+      const uint64_t dK = tc::kmajor_desc(tc::smem_u32(sm + GR_QK) + C * 128, 128, 0);
+      const uint64_t nS = tc::mnmajor_desc(tc::smem_u32(sm + GR_S), 128, 0), nA = tc::mnmajor_desc(tc::smem_u32(sm + GR_DS), 128, 0);
+      // (a 64-row tile's second column half is 8 KB on)
+      auto step64x128 = [](int s) { return (uint64_t)((s >> 2) * 512 + (s & 3) * 2); };
+#pragma unroll
+      for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G3, dA1 + step128(s), dU + step64x128(s), id64, s > 0);
+#pragma unroll
+      for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G4, dQK + step128(s), dK + step128(s), id64, s > 0);
+      tc::mma_commit(ba);
+#pragma unroll
+      for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G1, dA1 + step128(s), nS + step_mn(s), idN, s > 0);
+#pragma unroll
+      for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G2, dUhi + step64x128(s), nA + step_mn(s), idN, s > 0);
+      tc::mma_commit(bb);
+    }
+    __syncwarp();
     // dv = beta du, du . v, and <A, S0>, while the products run
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int r = r0 + 16 * i;
+    for (int p = 0; p < 2; p++) {
+      const int r = r0 + 32 * p;
       const uint4 d4 = *reinterpret_cast<const uint4 *>(sm + GR_A1 + tile_off(C + r, c8, 128));
-      const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
-      uint4 v4 = make_uint4(0, 0, 0, 0);
-      if (r < n) v4 = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + (tok0 + r) * D + 8 * c8);
-      const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
-      const float b = m->beta[r] * idu;
+      const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w}, vw[4] = {v4[p].x, v4[p].y, v4[p].z, v4[p].w};
+      const float b = m->beta[r] * cidu;
       float s = 0.0f;
       __align__(16) __nv_bfloat162 o[4];
 #pragma unroll
@@ -590,184 +631,219 @@ __global__ void __launch_bounds__(256, 1)
       if (r < n) *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.dv_out + (tok0 + r) * D + 8 * c8) = *reinterpret_cast<uint4 *>(o);
       s = group_sum<16>(s);
       bad = fmaf(s, 0.0f, bad);
-      if (c8 == 0) m->duv[r] = s * idu;
+      if (c8 == 0) m->duv[r] = s * cidu;
     }
-    float s = 0.0f;
+    if (next < chunks) fetch_rows(next);
+    {
+      float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < (int)(TILE / 16 / 256); i++) {
-      const uint4 x = *reinterpret_cast<const uint4 *>(sm + GR_S + 16 * (tid + 256 * i));
-      const uint4 y = *reinterpret_cast<const uint4 *>(sm + GR_DS + 16 * (tid + 256 * i));
-      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+      for (int k = 0; k < (int)(TILE / 16 / (32 * GR_WARPS)); k++) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(sm + GR_S + 16 * (tid + 32 * GR_WARPS * k));
+        const uint4 y = *reinterpret_cast<const uint4 *>(sm + GR_DS + 16 * (tid + 32 * GR_WARPS * k));
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
-        const float2 p = half2_at(xw[k]), q = half2_at(yw[k]);
-        s = fmaf(p.x, q.x, fmaf(p.y, q.y, s));
+        for (int e = 0; e < 4; e++) {
+          const float2 p = half2_at(xw[e]), q = half2_at(yw[e]);
+          s = fmaf(p.x, q.x, fmaf(p.y, q.y, s));
+        }
       }
+      s = warp_sum(s);
+      if (lane == 0) m->cross[warp] = s * ciS * ciA;
     }
-    s = warp_sum(s);
-    if (lane == 0) m->cross[warp] = s * iS * iA;
-  }
-  // rows of the token x token products: row < 64: g_i and q_i, else du_i and k_i; columns 32 half ..
-  const int quad = warp & 3, half = warp >> 2, row = 32 * quad + lane, i = row & 63;
-  const bool upper = row < C;
-  const uint32_t tl = tbase + ((uint32_t)(32 * quad) << 16);
-  const float mul = upper ? a.scale * ig * iu : idu * iu, be = upper ? 1.0f : m->beta[i];
-  // the operand's units: W alpha, V alpha sq / sk, both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
-  // 128 products, beta < 4, V + V^T)
-  float ialpha;
-  const float vq = inv.w * inv.x;  // sq / sk
-  const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * iu * 33554432.0f, 8.0f * idu * iu * vq * 137438953472.0f),
-                                  kTopRow, ialpha);
-  if (!stop) stop = !tc::mbar_wait(ba, 0, a.wait_limit);
-  tc::fence_after_sync();
-  stop = __syncthreads_or(stop);
-  if (!stop) {
-    float x[32], y[32];
-    tc::tmem_ld32(tl + T_G3 + 32 * half, x);
-    tc::tmem_ld32(tl + T_G4 + 32 * half, y);
-    tc::tmem_ld_wait();
-    const float li = m->l[i];
-    const int zi = m->z[i];
-    const float qk = upper ? inv.x * inv.y : inv.x * inv.x;  // real q . k, k . k
-    const float op = upper ? alpha : -alpha * vq * be;
-    float db = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 32; k++) {
-      const int j = 32 * half + k;
-      const float w = x[k] * mul, pair = w * (y[k] * qk);
-      const float dec = m->z[j] == zi ? ex2(li - m->l[j]) : 0.0f;
-      const bool keep = upper ? j <= i : j < i;
-      y[k] = pair * be;                   // X's part, without the decay
-      x[k] = keep ? w * dec * op : 0.0f;  // the operand
-      if (j < i) db = fmaf(dec, pair, db);  // du_i against sum_j D_ij (k_i . k_j) u_j (no beta: it may be 0)
-    }
-    if (upper) {
-#pragma unroll
-      for (int k = 0; k < 4; k++) {  // W: row i of dq's, K columns
-        const float4 o = make_float4(half2_bits(x[8 * k], x[8 * k + 1]), half2_bits(x[8 * k + 2], x[8 * k + 3]),
-                                     half2_bits(x[8 * k + 4], x[8 * k + 5]), half2_bits(x[8 * k + 6], x[8 * k + 7]));
-        *reinterpret_cast<float4 *>(sm + GR_A5 + tile_off(i, 8 + 4 * half + k, 128)) = o;
-      }
-#pragma unroll
-      for (int k = 0; k < 32; k++) {
-        const int j = 32 * half + k;
-        *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, i, 128)) = __float2half_rn(x[k]);  // W^T
-        if (j < C - 1) X[i * X_LD + j + 1] = y[k];
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; k++) {
-        const int j = 32 * half + k;
-        if (j > i) continue;
-        const __half v = __float2half_rn(x[k]);  // -V (zero on the diagonal), both triangles
-        *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + i, C + j, 128)) = v;
-        *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, C + i, 128)) = v;
-      }
-    }
-    tc::fence_smem_to_async();
-    tc::fence_before_sync();
-    __syncthreads();
+    const float mul = upper ? a.scale * ig * ciu : cidu * ciu, be = upper ? 1.0f : m->beta[i];
+    // the operand's units: W alpha, V alpha sq / sk, both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
+    // 128 products, beta < 4, V + V^T)
+    float ialpha;
+    const float vq = cinv.w * cinv.x;  // sq / sk
+    const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * ciu * 33554432.0f, 8.0f * cidu * ciu * vq * 137438953472.0f),
+                                    kTopRow, ialpha);
+    const bool got_a = tc::mbar_wait(ba, ph, a.wait_limit);
     tc::fence_after_sync();
-    if (warp == 0 && elect_one()) {
-      const uint32_t idN = tc::idesc_f16(128, D, false, true);
-      const uint64_t dA5 = tc::kmajor_desc(tc::smem_u32(sm + GR_A5), 128, 0), nQK = tc::mnmajor_desc(tc::smem_u32(sm + GR_QK), 128, 0);
-#pragma unroll
-      for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G5, dA5 + step128(s), nQK + step_mn(s), idN, s > 0);
-      tc::mma_commit(bc);
-    }
-    __syncwarp();
-    if (!upper) {
-#pragma unroll
-      for (int k = 0; k < 32; k++) {
-        const int j = 32 * half + k;
-        if (j < C - 1) X[i * X_LD + j + 1] -= y[k];
-      }
-      m->dbeta[half][i] = db;
-    }
-  }
-  if (!stop) stop = !tc::mbar_wait(bb, 0, a.wait_limit);
-  tc::fence_after_sync();
-  stop = __syncthreads_or(stop);
-  // rows against q_i or k_i: what the gates and betas need of the state products; columns 64 half ..
-  if (!stop) {
-    float d1 = 0.0f, d2 = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 4; h++) {
+    stop = __syncthreads_or(!got_a);
+    if (stop) break;
+    {
       float x[16], y[16];
-      tc::tmem_ld16(tl + T_G1 + 64 * half + 16 * h, x);
-      if (!upper) tc::tmem_ld16(tl + T_G2 + 64 * half + 16 * h, y);
-      const uint4 p = *reinterpret_cast<const uint4 *>(sm + GR_QK + tile_off(row, 8 * half + 2 * h, 128));
-      const uint4 q = *reinterpret_cast<const uint4 *>(sm + GR_QK + tile_off(row, 8 * half + 2 * h + 1, 128));
-      const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+      tc::tmem_ld16(tl + T_G3 + 16 * part, x);
+      tc::tmem_ld16(tl + T_G4 + 16 * part, y);
+      const float li = m->l[i];
+      const int zi = m->z[i];
+      const float qk = (upper ? cinv.y : cinv.x) * cinv.x;  // real q . k, k . k
+      const float op = upper ? alpha : -alpha * vq * be;
+      float db = 0.0f, dec[16];
+#pragma unroll
+      for (int k = 0; k < 16; k++) {
+        const int j = 16 * part + k;
+        dec[k] = m->z[j] == zi ? ex2(li - m->l[j]) : 0.0f;
+      }
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const float2 f = half2_at(w[k]);
-        d1 = fmaf(x[2 * k], f.x, fmaf(x[2 * k + 1], f.y, d1));
-        if (!upper) d2 = fmaf(y[2 * k], f.x, fmaf(y[2 * k + 1], f.y, d2));
+      for (int k = 0; k < 16; k++) {
+        const int j = 16 * part + k;
+        const float w = x[k] * mul, pair = w * (y[k] * qk);
+        y[k] = pair * be;                                            // X's part, without the decay
+        x[k] = (upper ? j <= i : j < i) ? w * dec[k] * op : 0.0f;  // the operand
+        if (j < i) db = fmaf(dec[k], pair, db);  // du_i against sum_j D_ij (k_i . k_j) u_j (no beta: it may be 0)
+      }
+      if (upper) {
+#pragma unroll
+        for (int k = 0; k < 2; k++) {  // W: row i of dq's, K columns
+          const float4 o = make_float4(half2_bits(x[8 * k], x[8 * k + 1]), half2_bits(x[8 * k + 2], x[8 * k + 3]),
+                                       half2_bits(x[8 * k + 4], x[8 * k + 5]), half2_bits(x[8 * k + 6], x[8 * k + 7]));
+          *reinterpret_cast<float4 *>(sm + GR_A5 + tile_off(i, 8 + 2 * part + k, 128)) = o;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; k++) {
+          const int j = 16 * part + k;
+          *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, i, 128)) = __float2half_rn(x[k]);  // W^T
+          if (j < C - 1) X[i * X_LD + j + 1] = y[k];
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; k++) {
+          const int j = 16 * part + k;
+          if (j > i) continue;
+          const __half v = __float2half_rn(x[k]);  // -V (zero on the diagonal), both triangles
+          *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + i, C + j, 128)) = v;
+          *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, C + i, 128)) = v;
+        }
+      }
+      tc::fence_smem_to_async();
+      tc::fence_before_sync();
+      __syncthreads();
+      tc::fence_after_sync();
+      if (warp == 0 && elect_one()) {
+        const uint32_t idN = tc::idesc_f16(128, D, false, true);
+        const uint64_t dA5 = tc::kmajor_desc(tc::smem_u32(sm + GR_A5), 128, 0), nQK = tc::mnmajor_desc(tc::smem_u32(sm + GR_QK), 128, 0);
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G5, dA5 + step128(s), nQK + step_mn(s), idN, s > 0);
+        tc::mma_commit(bc);
+      }
+      __syncwarp();
+      if (!upper) {
+#pragma unroll
+        for (int k = 0; k < 16; k++) {
+          const int j = 16 * part + k;
+          if (j < C - 1) X[i * X_LD + j + 1] -= y[k];
+        }
+        m->dbeta[part][i] = db;
       }
     }
-    if (upper) {
-      m->xin[half][0][i] = d1 * (a.scale * ig * iS * inv.y);
-    } else {
-      m->xin[half][1][i] = d1 * (idu * iS * inv.x);  // (times beta below)
-      m->xout[half][i] = d2 * (iu * iA * inv.x);
+    const bool got_b = tc::mbar_wait(bb, ph, a.wait_limit);
+    tc::fence_after_sync();
+    stop = __syncthreads_or(!got_b);
+    if (stop) break;
+    if (next < chunks) {  // the states, u and du have been read
+      if (tid == 32) fetch_operands(next);
+      fetched++;
+    }
+    {  // rows against q_i or k_i: what the gates and betas need of the state products; columns 32 part ..
+      float d1 = 0.0f, d2 = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        float x[16], y[16];
+        tc::tmem_ld16(tl + T_G1 + 32 * part + 16 * h, x);
+        if (!upper) tc::tmem_ld16(tl + T_G2 + 32 * part + 16 * h, y);
+        const uint4 p = *reinterpret_cast<const uint4 *>(sm + GR_QK + tile_off(row, 4 * part + 2 * h, 128));
+        const uint4 q = *reinterpret_cast<const uint4 *>(sm + GR_QK + tile_off(row, 4 * part + 2 * h + 1, 128));
+        const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const float2 f = half2_at(w[k]);
+          d1 = fmaf(x[2 * k], f.x, fmaf(x[2 * k + 1], f.y, d1));
+          if (!upper) d2 = fmaf(y[2 * k], f.x, fmaf(y[2 * k + 1], f.y, d2));
+        }
+      }
+      if (upper) {
+        m->xin[part][0][i] = d1 * (a.scale * ig * ciS * cinv.y);
+      } else {
+        m->xin[part][1][i] = d1 * (cidu * ciS * cinv.x);  // (times beta below)
+        m->xout[part][i] = d2 * (ciu * ciA * cinv.x);
+      }
     }
     __syncthreads();
     if (tid < C) {
-      const float kS = m->xin[0][1][tid] + m->xin[1][1][tid];
-      X[tid * X_LD] = m->xin[0][0][tid] + m->xin[1][0][tid] - m->beta[tid] * kS;
+      const float kS = (m->xin[0][1][tid] + m->xin[1][1][tid]) + (m->xin[2][1][tid] + m->xin[3][1][tid]);
+      X[tid * X_LD] = (m->xin[0][0][tid] + m->xin[1][0][tid]) + (m->xin[2][0][tid] + m->xin[3][0][tid]) - m->beta[tid] * kS;
       m->duv[tid] += m->nf[tid] * kS;
     }
     __syncthreads();
-    // columns of X, upwards from the last token: Z_t = X_t + gamma_{t+1} Z_{t+1}, times the decay from the
-    // writer to t - 1; column 0: the state before the chunk
-    if (tid <= C - 1) {
-      const int j = tid - 1;
-      float Z;
-      if (j < 0) {
-        Z = 0.0f;
+    // columns of X (column 0: the state before the chunk; column j + 1: token j as the writer), upwards from the
+    // last token: Z_t = X_t + gamma_{t+1} Z_{t+1}, times the decay from the writer to t - 1, summed over the
+    // writers before t.  Eight tokens a thread, joined over the segments above.
+    {
+      const int seg = warp >> 1, col = 32 * (warp & 1) + lane, t8 = 8 * seg, j = col - 1;
+      float Z[8];
 #pragma unroll
-        for (int w = 0; w < 8; w++) Z += m->cross[w];
+      for (int k = 0; k < 8; k++) Z[k] = X[(t8 + k) * X_LD + col];
+#pragma unroll
+      for (int k = 6; k >= 0; k--) Z[k] = fmaf(m->gam[t8 + k + 1], Z[k + 1], Z[k]);
+      m->head[seg][col] = Z[0];
+      __syncthreads();
+      float in;  // Z of the token above the segment
+      if (col == 0) {
+        in = 0.0f;
+#pragma unroll
+        for (int w = 0; w < GR_WARPS; w++) in += m->cross[w];
       } else {
-        Z = m->xout[0][j] + m->xout[1][j];
+        in = (m->xout[0][j] + m->xout[1][j]) + (m->xout[2][j] + m->xout[3][j]);
+      }
+      float through = 1.0f;  // (the last token's gate to the state after the chunk: in c)
+      for (int s = GR_SEGS - 1; s > seg; s--) {
+        float g = s == GR_SEGS - 1 ? 1.0f : m->gam[8 * s + 8];
+#pragma unroll
+        for (int k = 1; k < 8; k++) g *= m->gam[8 * s + k];
+        in = fmaf(g, in, m->head[s][col]);
       }
       const float lj = j < 0 ? 0.0f : m->l[j];
       const int zj = j < 0 ? 0 : m->z[j];
-      for (int t = C - 1; t > j; t--) {
-        Z = fmaf(t == C - 1 ? 1.0f : m->gam[t + 1], Z, X[t * X_LD + tid]);
+      if (seg < GR_SEGS - 1) through = m->gam[t8 + 8];
+      float carry = through * in;
+#pragma unroll
+      for (int k = 7; k >= 0; k--) {
+        const int t = t8 + k;
         const float lp = t > 0 ? m->l[t - 1] : 0.0f;
         const int zp = t > 0 ? m->z[t - 1] : 0;
-        X[t * X_LD + tid] = zp == zj ? Z * ex2(lp - lj) : 0.0f;
+        const float z = Z[k] + carry;
+        carry *= m->gam[t];
+        Z[k] = t > j && zp == zj ? z * ex2(lp - lj) : 0.0f;
       }
-    }
-    __syncthreads();
-    {  // four threads a token: its gate's gradient
-      const int t = tid >> 2, part = tid & 3;
-      float s = 0.0f;
-      for (int k = part; k <= t; k += 4) s += X[t * X_LD + k];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      bad = fmaf(s, 0.0f, bad);
-      if (part == 0 && t < n) st((__nv_bfloat16 *)a.dgamma, tok0 + t, s);
-    }
-    if (tid < n) st((__nv_bfloat16 *)a.dbeta, tok0 + tid, m->duv[tid] - (m->dbeta[0][tid] + m->dbeta[1][tid]));
-  }
-  if (!stop) stop = !tc::mbar_wait(bc, 0, a.wait_limit);
-  tc::fence_after_sync();
-  stop = __syncthreads_or(stop);
-  if (!stop) {
-    // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 64 half ..
-    const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;
-    const float f2 = m->c[i] * iu * iA, f5 = ialpha * (upper ? inv.x : inv.y);
-    uint8_t *out = sm + GR_A1 + (upper ? 0 : ROWS64);
-    float *part = upper ? dqp : dkp;
+      // over the warp's columns: lanes 4 m .. hold token m's
 #pragma unroll
-    for (int h = 0; h < 4; h++) {
+      for (int o = 16, w = 4; o >= 4; o >>= 1, w >>= 1) {
+        const bool hi = lane & o;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+          if (k >= w) continue;
+          const float give = hi ? Z[k] : Z[k + w];
+          Z[k] = (hi ? Z[k + w] : Z[k]) + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+      float s = Z[0] + __shfl_xor_sync(0xffffffffu, Z[0], 2);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      bad = fmaf(s, 0.0f, bad);
+      if ((lane & 3) == 0) m->dgam[warp & 1][t8 + (lane >> 2)] = s;
+    }
+    const bool got_c = tc::mbar_wait(bc, ph, a.wait_limit);
+    tc::fence_after_sync();
+    stop = __syncthreads_or(!got_c);
+    if (stop) break;
+    if (tid < n) {
+      st((__nv_bfloat16 *)a.dgamma, tok0 + tid, m->dgam[0][tid] + m->dgam[1][tid]);
+      st((__nv_bfloat16 *)a.dbeta, tok0 + tid,
+         m->duv[tid] - ((m->dbeta[0][tid] + m->dbeta[1][tid]) + (m->dbeta[2][tid] + m->dbeta[3][tid])));
+    }
+    // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 32 part ..
+    const float f1 = upper ? -m->nf[i] * a.scale * ig * ciS : m->nf[i] * m->beta[i] * cidu * ciS;
+    const float f2 = m->c[i] * ciu * ciA, f5 = ialpha * (upper ? cinv.x : cinv.y);
+    uint8_t *out = sm + GR_A5 + (upper ? 0 : ROWS64);
+    float *sum = upper ? dqp : dkp;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
       float x[16], y[16], z[16];
-      tc::tmem_ld16(tl + T_G1 + 64 * half + 16 * h, x);
-      tc::tmem_ld16(tl + T_G5 + 64 * half + 16 * h, z);
-      if (!upper) tc::tmem_ld16(tl + T_G2 + 64 * half + 16 * h, y);
+      tc::tmem_ld16(tl + T_G1 + 32 * part + 16 * h, x);
+      tc::tmem_ld16(tl + T_G5 + 32 * part + 16 * h, z);
+      if (!upper) tc::tmem_ld16(tl + T_G2 + 32 * part + 16 * h, y);
       tc::tmem_ld_wait();
 #pragma unroll
       for (int k = 0; k < 16; k++) {
@@ -775,9 +851,9 @@ __global__ void __launch_bounds__(256, 1)
         if (!upper) x[k] = fmaf(y[k], f2, x[k]);
         bad = fmaf(x[k], 0.0f, bad);
       }
-      if (part) {
+      if (sum) {
         if (i < n) {
-          float4 *dst = reinterpret_cast<float4 *>(part + (tok0 + i) * D + 64 * half + 16 * h);
+          float4 *dst = reinterpret_cast<float4 *>(sum + (tok0 + i) * D + 32 * part + 16 * h);
 #pragma unroll
           for (int k = 0; k < 4; k++) dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         }
@@ -785,27 +861,29 @@ __global__ void __launch_bounds__(256, 1)
         __align__(16) __nv_bfloat162 o[8];
 #pragma unroll
         for (int k = 0; k < 8; k++) o[k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-        *reinterpret_cast<uint4 *>(out + tile_off(i, 8 * half + 2 * h, C)) = *reinterpret_cast<const uint4 *>(o);
-        *reinterpret_cast<uint4 *>(out + tile_off(i, 8 * half + 2 * h + 1, C)) = *reinterpret_cast<const uint4 *>(o + 4);
+        *reinterpret_cast<uint4 *>(out + tile_off(i, 4 * part + 2 * h, C)) = *reinterpret_cast<const uint4 *>(o);
+        *reinterpret_cast<uint4 *>(out + tile_off(i, 4 * part + 2 * h + 1, C)) = *reinterpret_cast<const uint4 *>(o + 4);
       }
     }
-    if (!(bad == 0.0f)) atomicOr(a.status, tc::kErrNonFinite);
     tc::fence_smem_to_async();
+    tc::fence_before_sync();  // (the next chunk's products write what was read)
     __syncthreads();
-    if (!part && tid == 0) {
+    if (!dqp && tid == 0) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
-        tensor_s2g_3d(&mapDq, tc::smem_u32(sm + GR_A1 + h * C * 128), 64 * h, t0, u);
-        tensor_s2g_3d(&mapDk, tc::smem_u32(sm + GR_A1 + ROWS64 + h * C * 128), 64 * h, t0, u);
+        tensor_s2g_3d(&mapDq, tc::smem_u32(sm + GR_A5 + h * C * 128), 64 * h, t0, u);
+        tensor_s2g_3d(&mapDk, tc::smem_u32(sm + GR_A5 + ROWS64 + h * C * 128), 64 * h, t0, u);
       }
       tc::bulk_commit();
-      tc::bulk_wait_all();
     }
-  } else {  // a wait gave up: what is in flight finishes before the memory is released
+  }
+  if (tid == 0) tc::bulk_wait_all();
+  if (!(bad == 0.0f)) atomicOr(a.status, tc::kErrNonFinite);
+  if (stop) {  // a wait gave up: what is in flight finishes before the memory is released
     if (tid == 0) atomicOr(a.status, tc::kErrMmaTimeout);
     const bool issuer = warp == 0 && elect_one();
     tc::drain_mmas(tc::smem_u32(&m->drain), issuer, a.status);
-    if (tid == 0 && !tc::mbar_wait(bl, 0, tc::kWaitLimit)) atomicOr(a.status, tc::kErrDrainTimeout);
+    if (tid == 0 && !tc::mbar_wait(bl, (fetched - 1) & 1, tc::kWaitLimit)) atomicOr(a.status, tc::kErrDrainTimeout);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -830,8 +908,9 @@ int launch_rule_grads_tc(const RuleArgs &a, const void *records, const RuleOpera
   if (cudaFuncSetAttribute(mesa_rule_grads_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GR_SMEM) != cudaSuccess)
     return -1;
   timing_mark_begin(K_RULE_GRADS, st);
-  mesa_rule_grads_tc_kernel<<<dim3((a.T + C - 1) / C, a.units()), 256, GR_SMEM, st>>>(a, (const uint8_t *)records, so, ao, dqp,
-                                                                                      dkp, mapDq, mapDk);
+  const int NC = (a.T + C - 1) / C, chunks = NC * a.units(), sms = sm_count();
+  mesa_rule_grads_tc_kernel<<<chunks < sms ? chunks : sms, 32 * GR_WARPS, GR_SMEM, st>>>(
+      a, NC, chunks, (const uint8_t *)records, so, ao, dqp, dkp, mapDq, mapDk);
   timing_mark_end(K_RULE_GRADS, st);
   if (cudaPeekAtLastError() != cudaSuccess) return -1;
   return dqp ? launch_rule_group_sum(a, dqp, dkp, st) : 0;
