@@ -454,10 +454,10 @@ constexpr int X_LD = 65;
 constexpr uint32_t GR_X = GR_A5 + TILE, GR_MISC = GR_X + ((C * X_LD * 4 + 127) & ~127);
 constexpr int GR_WARPS = 16, GR_SEGS = 8;
 struct GradsMisc {
-  float l[C], nf[C], c[C], beta[C], gam[C];
+  float l[C], nf[C], c[C], beta[C], gam[C], num[8];  // num: 1 / scale of K, Q, S0, u, A, du; scale of K, Q
   alignas(16) int z[C];
   float duv[C], dbeta[4][C], xin[4][2][C], xout[4][C];
-  float head[GR_SEGS][C], dgam[2][C];
+  float head[GR_SEGS][C], pass[GR_SEGS], dgam[2][C];
   alignas(16) uint32_t red[GR_WARPS];
   float cross[GR_WARPS];
   uint64_t load, mma_a, mma_b, mma_c, drain;
@@ -469,6 +469,11 @@ static_assert(GR_SMEM <= 232448, "shared memory per block");
 constexpr uint32_t T_G1 = 0, T_G2 = 128, T_G3 = 256, T_G4 = 320, T_G5 = 384;
 
 __device__ __forceinline__ float2 half2_at(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+__device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {  // (16-byte aligned, multiples of 16)
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void l2_prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
 
 // 512 threads, one CTA per SM over `chunks` chunks of all units: the warps that share a quarter of the
 // tensor memory's lanes take a quarter of the columns each.  A chunk is a row of short steps that wait
@@ -490,8 +495,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
 
   // what is read ahead
   uint4 q4[2], k4[2], g4[2], v4[2];
-  float4 inv;
-  float iS, iu, iA, idu, tok;
+  float tok;
   auto fetch_rows = [&](int at) {
     const int u = at / NC, t0 = (at - u * NC) * C, n = min(C, a.T - t0);
     const size_t tok0 = (size_t)u * a.T + t0, row0 = (size_t)a.qk_unit(u) * a.T + t0;
@@ -507,14 +511,14 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
         v4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + (tok0 + r) * D + 8 * c8);
       }
     }
-    inv = *reinterpret_cast<const float4 *>(rec + REC_S);
-    iS = so.iS[at], iu = so.iU[at], iA = ao.iS[at], idu = ao.iU[at];
-    const int t = tid & (C - 1), which = tid >> 6;  // a token's numbers, one kind to two warps
-    tok = which == 0   ? reinterpret_cast<const float *>(rec + REC_F)[t]
-          : which == 1 ? reinterpret_cast<const float *>(rec + REC_C)[t]
-          : which == 2 ? reinterpret_cast<const float *>(rec + REC_B)[t]
-          : t < n      ? a.gamma[tok0 + t]
-                       : 1.0f;
+    const int t = tid & (C - 1), which = tid >> 6;  // a token's numbers, one kind to two warps; the chunk's
+    const float *src = which < 3 ? reinterpret_cast<const float *>(rec + REC_F) + tid
+                       : which == 3 ? a.gamma + tok0 + t
+                       : t < 2      ? reinterpret_cast<const float *>(rec + REC_S) + t
+                       : t < 6      ? (t == 2 ? so.iS : t == 3 ? so.iU : t == 4 ? ao.iS : ao.iU) + at
+                                    : reinterpret_cast<const float *>(rec + REC_S) + t - 4;
+    tok = 1.0f;
+    if (which < 3 || (which == 3 && t < n) || (which == 4 && t < 8)) tok = *src;
   };
   auto fetch_operands = [&](int at) {  // one thread
     tc::mbar_arrive_expect_tx(bl, 2 * TILE + 2 * ROWS64);
@@ -550,25 +554,29 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     const int u = at / NC, t0 = (at - u * NC) * C, n = min(C, a.T - t0);
     const size_t tok0 = (size_t)u * a.T + t0;
     const int next = at + (int)gridDim.x;
-    // this chunk's numbers (the read-ahead's registers take the next one's below)
-    const float4 cinv = inv;
-    const float ciS = iS, ciu = iu, ciA = iA, cidu = idu;
     {
       const int t = tid & (C - 1), which = tid >> 6;
-      if (which < 4) (which == 0 ? m->nf : which == 1 ? m->c : which == 2 ? m->beta : m->gam)[t] = tok;
+      if (which < 4) {
+        (which == 0 ? m->nf : which == 1 ? m->c : which == 2 ? m->beta : m->gam)[t] = tok;
+      } else if (which == 4 && t < 8) {
+        m->num[t] = tok;
+      }
     }
     uint32_t mg = 0;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-      const int r = r0 + 32 * k;
-      *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(r, c8, 128)) = to_half8(q4[k], pack2(cinv.w, cinv.w));
-      *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(C + r, c8, 128)) = to_half8(k4[k], pack2(cinv.z, cinv.z));
-      mg = absmax_words(mg, g4[k]);
-    }
+    for (int k = 0; k < 2; k++) mg = absmax_words(mg, g4[k]);
     mg = absmax_fold(mg);
     if (lane == 0) m->red[warp] = mg;
     if (tid == 0) tc::bulk_wait_read();  // the last chunk's dq and dk have left their place
     __syncthreads();
+    const float ik = m->num[0], iq = m->num[1], iS = m->num[2], iu = m->num[3], iA = m->num[4], idu = m->num[5];
+    const float2 sk_sq = *reinterpret_cast<const float2 *>(m->num + 6);
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const int r = r0 + 32 * k;
+      *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(r, c8, 128)) = to_half8(q4[k], pack2(sk_sq.y, sk_sq.y));
+      *reinterpret_cast<uint4 *>(sm + GR_QK + tile_off(C + r, c8, 128)) = to_half8(k4[k], pack2(sk_sq.x, sk_sq.x));
+    }
     // the products' operand: its block of Q columns for dq is zero
     *reinterpret_cast<uint4 *>(sm + GR_A5 + tile_off(tid >> 3, tid & 7, 128)) = make_uint4(0, 0, 0, 0);
     mg = 0;
@@ -586,6 +594,12 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       const GatePair g = gate_scan(make_float2(m->gam[2 * lane], m->gam[2 * lane + 1]), lane);
       *reinterpret_cast<float2 *>(&m->l[2 * lane]) = make_float2(g.l0, g.l1);
       *reinterpret_cast<int2 *>(&m->z[2 * lane]) = make_int2(g.z0, g.z1);
+      if (lane < GR_SEGS) {
+        float x = lane == GR_SEGS - 1 ? 1.0f : m->gam[8 * lane + 8];
+#pragma unroll
+        for (int k = 1; k < 8; k++) x *= m->gam[8 * lane + k];
+        m->pass[lane] = x;
+      }
     }
     tc::fence_smem_to_async();
     tc::fence_before_sync();
@@ -613,13 +627,31 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       tc::mma_commit(bb);
     }
     __syncwarp();
+    if (warp == GR_WARPS - 1 && next < chunks) {  // the next chunk comes to the L2 cache
+      const int nu = next / NC, nt0 = (next - nu * NC) * C, nn = min(C, a.T - nt0);
+      const size_t ntok = (size_t)nu * a.T + nt0, nrow = (size_t)a.qk_unit(nu) * a.T + nt0;
+      if (lane < 4) {
+        const void *base = lane == 0 ? a.q : lane == 1 ? a.k : lane == 2 ? a.dout : a.v;
+        l2_prefetch((const __nv_bfloat16 *)base + (lane < 2 ? nrow : ntok) * D, nn * D * 2);
+      } else if (lane < 8) {
+        l2_prefetch((lane & 1 ? ao.S : so.S) + (size_t)next * TILE + (lane < 6 ? 0 : TILE / 2), TILE / 2);
+      } else if (lane < 10) {
+        l2_prefetch((lane & 1 ? ao.U : so.U) + (size_t)next * ROWS64, ROWS64);
+      } else if (lane == 10) {
+        l2_prefetch(records + (size_t)next * REC + REC_F, REC - REC_F);
+      } else if (lane < 15) {
+        l2_prefetch((lane == 11 ? so.iS : lane == 12 ? so.iU : lane == 13 ? ao.iS : ao.iU) + next);
+      } else if (lane >= 16 && 4 * (lane - 16) < nn) {
+        l2_prefetch(a.gamma + ntok + 4 * (lane - 16));
+      }
+    }
     // dv = beta du, du . v, and <A, S0>, while the products run
 #pragma unroll
     for (int p = 0; p < 2; p++) {
       const int r = r0 + 32 * p;
       const uint4 d4 = *reinterpret_cast<const uint4 *>(sm + GR_A1 + tile_off(C + r, c8, 128));
       const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w}, vw[4] = {v4[p].x, v4[p].y, v4[p].z, v4[p].w};
-      const float b = m->beta[r] * cidu;
+      const float b = m->beta[r] * idu;
       float s = 0.0f;
       __align__(16) __nv_bfloat162 o[4];
 #pragma unroll
@@ -631,9 +663,8 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       if (r < n) *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.dv_out + (tok0 + r) * D + 8 * c8) = *reinterpret_cast<uint4 *>(o);
       s = group_sum<16>(s);
       bad = fmaf(s, 0.0f, bad);
-      if (c8 == 0) m->duv[r] = s * cidu;
+      if (c8 == 0) m->duv[r] = s * idu;
     }
-    if (next < chunks) fetch_rows(next);
     {
       float s = 0.0f;
 #pragma unroll
@@ -648,14 +679,14 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
         }
       }
       s = warp_sum(s);
-      if (lane == 0) m->cross[warp] = s * ciS * ciA;
+      if (lane == 0) m->cross[warp] = s * iS * iA;
     }
-    const float mul = upper ? a.scale * ig * ciu : cidu * ciu, be = upper ? 1.0f : m->beta[i];
+    const float mul = upper ? a.scale * ig * iu : idu * iu, be = upper ? 1.0f : m->beta[i];
     // the operand's units: W alpha, V alpha sq / sk, both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
     // 128 products, beta < 4, V + V^T)
     float ialpha;
-    const float vq = cinv.w * cinv.x;  // sq / sk
-    const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * ciu * 33554432.0f, 8.0f * cidu * ciu * vq * 137438953472.0f),
+    const float vq = sk_sq.y * ik;  // sq / sk
+    const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * iu * 33554432.0f, 8.0f * idu * iu * vq * 137438953472.0f),
                                     kTopRow, ialpha);
     const bool got_a = tc::mbar_wait(ba, ph, a.wait_limit);
     tc::fence_after_sync();
@@ -666,46 +697,60 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       tc::tmem_ld16(tl + T_G3 + 16 * part, x);
       tc::tmem_ld16(tl + T_G4 + 16 * part, y);
       const float li = m->l[i];
-      const int zi = m->z[i];
-      const float qk = (upper ? cinv.y : cinv.x) * cinv.x;  // real q . k, k . k
+      const u64 li2 = pack2(li, li), mul2x = pack2(mul, mul);
+      const float qk = (upper ? iq : ik) * ik;  // real q . k, k . k
       const float op = upper ? alpha : -alpha * vq * be;
-      float db = 0.0f, dec[16];
+      const u64 qk2 = pack2(qk, qk), op2 = pack2(op, op);
+      const int keep = (upper ? i : i - 1) - 16 * part;  // the last column of the operand
+      float dec[16], db = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 16; k++) {
-        const int j = 16 * part + k;
-        dec[k] = m->z[j] == zi ? ex2(li - m->l[j]) : 0.0f;
+      for (int k = 0; k < 16; k += 4) {
+        const ulonglong2 lj = *reinterpret_cast<const ulonglong2 *>(&m->l[16 * part + k]);
+        unpack2(sub2(li2, lj.x), dec[k], dec[k + 1]);
+        unpack2(sub2(li2, lj.y), dec[k + 2], dec[k + 3]);
+      }
+#pragma unroll
+      for (int k = 0; k < 16; k++) dec[k] = k <= keep ? ex2(dec[k]) : 0.0f;
+      if (m->z[C - 1] != 0) {  // a closed gate in the chunk
+        const int zi = m->z[i];
+#pragma unroll
+        for (int k = 0; k < 16; k++)
+          if (m->z[16 * part + k] != zi) dec[k] = 0.0f;
       }
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 16; k++) {
-        const int j = 16 * part + k;
-        const float w = x[k] * mul, pair = w * (y[k] * qk);
-        y[k] = pair * be;                                            // X's part, without the decay
-        x[k] = (upper ? j <= i : j < i) ? w * dec[k] * op : 0.0f;  // the operand
-        if (j < i) db = fmaf(dec[k], pair, db);  // du_i against sum_j D_ij (k_i . k_j) u_j (no beta: it may be 0)
+      for (int k = 0; k < 16; k += 2) {
+        const u64 w = mul2(pack2(x[k], x[k + 1]), mul2x);
+        unpack2(mul2(w, mul2(pack2(y[k], y[k + 1]), qk2)), y[k], y[k + 1]);  // X's part, without the decay
+        unpack2(mul2(mul2(w, op2), pack2(dec[k], dec[k + 1])), x[k], x[k + 1]);  // the operand
+      }
+      // (columns without a decay are none of the operand's, whatever their products are)
+#pragma unroll
+      for (int k = 0; k < 16; k++) x[k] = k <= keep ? x[k] : 0.0f;
+      // the first rows' and the later columns' addresses: row C + j of the operand, column i or C + i
+      const uint32_t tr = (C + 16 * part) * 128 + (upper ? 0 : 128 * 128) + ((i & 7) << 1), ib = (i >> 3) << 4;
+      auto at_tr = [&](int k) { return reinterpret_cast<__half *>(sm + GR_A5 + tr + (ib ^ ((k & 7) << 4)) + k * 128); };
+      // W: row i of dq's, K columns;  -V: row i of dk's, K columns (zero above the diagonal)
+#pragma unroll
+      for (int k = 0; k < 2; k++) {
+        const float4 o = make_float4(half2_bits(x[8 * k], x[8 * k + 1]), half2_bits(x[8 * k + 2], x[8 * k + 3]),
+                                     half2_bits(x[8 * k + 4], x[8 * k + 5]), half2_bits(x[8 * k + 6], x[8 * k + 7]));
+        *reinterpret_cast<float4 *>(sm + GR_A5 + tile_off(row, 8 + 2 * part + k, 128)) = o;
       }
       if (upper) {
 #pragma unroll
-        for (int k = 0; k < 2; k++) {  // W: row i of dq's, K columns
-          const float4 o = make_float4(half2_bits(x[8 * k], x[8 * k + 1]), half2_bits(x[8 * k + 2], x[8 * k + 3]),
-                                       half2_bits(x[8 * k + 4], x[8 * k + 5]), half2_bits(x[8 * k + 6], x[8 * k + 7]));
-          *reinterpret_cast<float4 *>(sm + GR_A5 + tile_off(i, 8 + 2 * part + k, 128)) = o;
-        }
+        for (int k = 0; k < 16; k++) *at_tr(k) = __float2half_rn(x[k]);  // W^T
 #pragma unroll
-        for (int k = 0; k < 16; k++) {
-          const int j = 16 * part + k;
-          *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, i, 128)) = __float2half_rn(x[k]);  // W^T
-          if (j < C - 1) X[i * X_LD + j + 1] = y[k];
-        }
+        for (int k = 0; k < 16; k++)
+          if (k < 15 || part < 3) X[i * X_LD + 16 * part + k + 1] = y[k];
       } else {
+        group_or(1, 16 * GR_WARPS, false);  // (their zeros are in place)
 #pragma unroll
-        for (int k = 0; k < 16; k++) {
-          const int j = 16 * part + k;
-          if (j > i) continue;
-          const __half v = __float2half_rn(x[k]);  // -V (zero on the diagonal), both triangles
-          *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + i, C + j, 128)) = v;
-          *reinterpret_cast<__half *>(sm + GR_A5 + tc::sw128_offset(C + j, C + i, 128)) = v;
-        }
+        for (int k = 0; k < 16; k++)
+          if (k <= keep) *at_tr(k) = __float2half_rn(x[k]);  // -V^T
+#pragma unroll
+        for (int k = 0; k < 16; k++)
+          if (k <= keep) db = fmaf(dec[k], y[k], db);  // du_i against sum_j D_ij (k_i . k_j) u_j
       }
       tc::fence_smem_to_async();
       tc::fence_before_sync();
@@ -722,8 +767,8 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       if (!upper) {
 #pragma unroll
         for (int k = 0; k < 16; k++) {
-          const int j = 16 * part + k;
-          if (j < C - 1) X[i * X_LD + j + 1] -= y[k];
+          float *x1 = &X[i * X_LD + 16 * part + k + 1];
+          if (k < 15 || part < 3) *x1 = fmaf(-be, y[k], *x1);
         }
         m->dbeta[part][i] = db;
       }
@@ -755,10 +800,10 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
         }
       }
       if (upper) {
-        m->xin[part][0][i] = d1 * (a.scale * ig * ciS * cinv.y);
+        m->xin[part][0][i] = d1 * (a.scale * ig * iS * iq);
       } else {
-        m->xin[part][1][i] = d1 * (cidu * ciS * cinv.x);  // (times beta below)
-        m->xout[part][i] = d2 * (ciu * ciA * cinv.x);
+        m->xin[part][1][i] = d1 * (idu * iS * ik);  // (times beta below)
+        m->xout[part][i] = d2 * (iu * iA * ik);
       }
     }
     __syncthreads();
@@ -788,17 +833,12 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       } else {
         in = (m->xout[0][j] + m->xout[1][j]) + (m->xout[2][j] + m->xout[3][j]);
       }
-      float through = 1.0f;  // (the last token's gate to the state after the chunk: in c)
-      for (int s = GR_SEGS - 1; s > seg; s--) {
-        float g = s == GR_SEGS - 1 ? 1.0f : m->gam[8 * s + 8];
 #pragma unroll
-        for (int k = 1; k < 8; k++) g *= m->gam[8 * s + k];
-        in = fmaf(g, in, m->head[s][col]);
-      }
+      for (int s = GR_SEGS - 1; s > 0; s--)
+        if (s > seg) in = fmaf(m->pass[s], in, m->head[s][col]);
       const float lj = j < 0 ? 0.0f : m->l[j];
       const int zj = j < 0 ? 0 : m->z[j];
-      if (seg < GR_SEGS - 1) through = m->gam[t8 + 8];
-      float carry = through * in;
+      float carry = seg < GR_SEGS - 1 ? m->gam[t8 + 8] * in : in;  // (the last token's gate to the state after: in c)
 #pragma unroll
       for (int k = 7; k >= 0; k--) {
         const int t = t8 + k;
@@ -833,24 +873,28 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       st((__nv_bfloat16 *)a.dbeta, tok0 + tid,
          m->duv[tid] - ((m->dbeta[0][tid] + m->dbeta[1][tid]) + (m->dbeta[2][tid] + m->dbeta[3][tid])));
     }
+    if (next < chunks) fetch_rows(next);
     // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 32 part ..
-    const float f1 = upper ? -m->nf[i] * a.scale * ig * ciS : m->nf[i] * m->beta[i] * cidu * ciS;
-    const float f2 = m->c[i] * ciu * ciA, f5 = ialpha * (upper ? cinv.x : cinv.y);
+    const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;
+    const float f2 = m->c[i] * iu * iA, f5 = ialpha * (upper ? ik : iq);
     uint8_t *out = sm + GR_A5 + (upper ? 0 : ROWS64);
     float *sum = upper ? dqp : dkp;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      float x[16], y[16], z[16];
-      tc::tmem_ld16(tl + T_G1 + 32 * part + 16 * h, x);
-      tc::tmem_ld16(tl + T_G5 + 32 * part + 16 * h, z);
-      if (!upper) tc::tmem_ld16(tl + T_G2 + 32 * part + 16 * h, y);
+      float x[16], y[16];
+      tc::tmem_ld16(tl + T_G5 + 32 * part + 16 * h, x);
+      tc::tmem_ld16(tl + T_G1 + 32 * part + 16 * h, y);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 16; k++) {
-        x[k] = fmaf(x[k], f1, z[k] * f5);
-        if (!upper) x[k] = fmaf(y[k], f2, x[k]);
-        bad = fmaf(x[k], 0.0f, bad);
+      for (int k = 0; k < 16; k++) x[k] = fmaf(y[k], f1, x[k] * f5);
+      if (!upper) {
+        tc::tmem_ld16(tl + T_G2 + 32 * part + 16 * h, y);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; k++) x[k] = fmaf(y[k], f2, x[k]);
       }
+#pragma unroll
+      for (int k = 0; k < 16; k++) bad = fmaf(x[k], 0.0f, bad);
       if (sum) {
         if (i < n) {
           float4 *dst = reinterpret_cast<float4 *>(sum + (tok0 + i) * D + 32 * part + 16 * h);
