@@ -32,13 +32,13 @@ int check_sizes(int B, int H, int Hk, int T, int dk, int dv, int dtype, float sc
   return MESA_OK;
 }
 
-// Backward workspace of the CUDA-core path: [status | S | dS | e | du | per-head dq, dk].
-constexpr int kBwdParts = 6;
+// Backward workspace of the CUDA-core path: [status | S | dS | e | du | per-head dq, dk | segments].
+constexpr int kBwdParts = 7;
 size_t backward_parts(int B, int H, int Hk, int T, int dk, int dv, size_t *off) {
   const size_t U = (size_t)B * H, NC = ((size_t)T + mesa::kRuleChunk - 1) / mesa::kRuleChunk;
   const size_t st = U * NC * dv * dk * sizeof(float), rows = U * T * dv * sizeof(float);
   const size_t part = Hk != H ? U * T * dk * sizeof(float) : 0;
-  const size_t sizes[kBwdParts] = {st, st, rows, rows, part, part};
+  const size_t sizes[kBwdParts] = {st, st, rows, rows, part, part, mesa::rule_scan_workspace(B * H, T, dk, dv, true)};
   size_t at = kStatusBytes;
   for (int i = 0; i < kBwdParts; i++) {
     off[i] = at;
@@ -69,7 +69,8 @@ extern "C" {
 
 size_t mesa_delta_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   if (check_sizes(B, H, Hk, T, dk, dv, dtype, 1.0f) != MESA_OK) return 0;
-  return kStatusBytes + (rule_tc(dtype, dk, dv) ? mesa::rule_tc_workspace(B * H, T) : 0);
+  return kStatusBytes + (rule_tc(dtype, dk, dv) ? mesa::rule_tc_workspace(B * H, T)
+                                                 : mesa::rule_scan_workspace(B * H, T, dk, dv, false));
 }
 
 int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,
@@ -99,8 +100,10 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
   a.status = (unsigned *)workspace;
   a.wait_limit = mesa::wait_limit();
   if (cudaMemsetAsync(a.status, 0, sizeof(unsigned), stream) != cudaSuccess) return MESA_ERR_CUDA;
-  const int rc = rule_tc(dtype, dk, dv) ? mesa::launch_rule_forward_tc(a, (char *)workspace + kStatusBytes, stream)
-                                        : mesa::launch_rule_forward(a, stream);
+  char *rest = (char *)workspace + kStatusBytes;
+  const int rc = rule_tc(dtype, dk, dv)
+                     ? mesa::launch_rule_forward_tc(a, rest, stream)
+                     : mesa::launch_rule_forward(a, mesa::rule_scan_parts(B * H, T, dk, dv, false, rest), stream);
   return rc == 0 ? MESA_OK : MESA_ERR_CUDA;
 }
 
@@ -163,7 +166,8 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
   mesa::RuleBwdWorkspace ws{(float *)(w + off[0]), (float *)(w + off[1]), (float *)(w + off[2]),
                             (float *)(w + off[3]), Hk != H ? (float *)(w + off[4]) : nullptr,
                             Hk != H ? (float *)(w + off[5]) : nullptr};
-  return mesa::launch_rule_backward(a, ws, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
+  const mesa::RuleScanSegments sg = mesa::rule_scan_parts(B * H, T, dk, dv, true, w + off[6]);
+  return mesa::launch_rule_backward(a, ws, sg, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
 }
 
 int mesa_delta_step(int N, int H, int Hk, int dk, int dv, int dtype, float *S_state, const void *q,

@@ -30,7 +30,7 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-enum ScanMode { kForward = 0, kStates = 1, kAdjoint = 2 };
+enum ScanMode { kForward = 0, kStates = 1, kAdjoint = 2, kSegment = 3, kSegAdjoint = 4 };
 constexpr int TB = 16;    // tokens staged at a time
 constexpr int ROWS = 32;  // state rows per CTA, four lanes each
 
@@ -42,20 +42,31 @@ constexpr int ROWS = 32;  // state rows per CTA, four lanes each
 // (packed fp32 pairs halve the issue slots).
 //   kForward: out, S_final.  kStates: e and the state before each 32-token chunk.
 //   kAdjoint: tokens descending; du and the adjoint after each chunk, dS0.
+// Few units: the tokens are cut into segments (blockIdx.z) that run side by side, each from the state
+// before it, which two more modes and mesa_rule_scan_join_kernel find first.
+//   kSegment: what segment z leaves of a state of zero (the first: of S0), and, in the CTAs past the
+//   state's rows, of the rows of the identity without values: the matrix that takes the state before
+//   the segment to its part of the state after it (and that matrix transposed, which takes the adjoint back).
+//   kSegAdjoint: the adjoint before segment z + 1 from zero after it (the last: dS_final).
 template <int DK, typename TIO, int MODE>
-__global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwdWorkspace ws) {
+__global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwdWorkspace ws, RuleScanSegments sg) {
+  constexpr bool ADJ = MODE == kAdjoint || MODE == kSegAdjoint, SEG = MODE == kSegment || MODE == kSegAdjoint;
   constexpr int VPL = DK / 4, NG = VPL / 4;  // values and 16-byte groups per lane
   constexpr bool WIDE = sizeof(TIO) == 4;
-  constexpr bool USEQ = MODE != kStates;
+  constexpr bool USEQ = MODE == kForward || ADJ;
   __shared__ __align__(16) TIO kraw[2][TB * DK], qraw[2][USEQ ? TB * DK : 8], xraw[2][TB * ROWS];
   __shared__ __align__(16) float kwide[WIDE ? 4 : TB * DK], qwide[WIDE || !USEQ ? 4 : TB * DK];
   __shared__ float os[TB * ROWS], gs[2][TB], bs[2][TB];
-  const int u = blockIdx.y, r0 = blockIdx.x * ROWS, tid = threadIdx.x;
-  const int r = tid >> 2, j = tid & 3, nr = min(ROWS, a.dv - r0);
-  const int T = a.T, nblk = (T + TB - 1) / TB;
+  const int u = blockIdx.y, tiles = (a.dv + ROWS - 1) / ROWS, tid = threadIdx.x;
+  const bool matrix = MODE == kSegment && (int)blockIdx.x >= tiles;
+  const int r0 = (blockIdx.x - (matrix ? tiles : 0)) * ROWS;
+  const int r = tid >> 2, j = tid & 3, nr = min(ROWS, (matrix ? DK : a.dv) - r0);
+  const int T = a.T, seg = blockIdx.z + (MODE == kSegAdjoint ? 1 : 0);
+  const int b0 = seg * sg.per, b1 = min((T + TB - 1) / TB, b0 + sg.per), nblk = b1 - b0;  // its blocks of tokens
+  if (matrix && seg == 0) return;
   const size_t qk0 = (size_t)a.qk_unit(u) * T, tu = (size_t)u * T;
   const TIO *kp = (const TIO *)a.k + qk0 * DK, *qp = (const TIO *)a.q + qk0 * DK;
-  const TIO *xp = (const TIO *)(MODE == kAdjoint ? a.dout : a.v) + tu * a.dv + r0;
+  const TIO *xp = (const TIO *)(ADJ ? a.dout : a.v) + tu * a.dv + r0;
   const bool rin = r < nr;
 
   auto fetch = [&](int blk, int buf) {
@@ -65,7 +76,7 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
       cp16(&kraw[buf][i * E], kp + (size_t)t0 * DK + i * E);
       if (USEQ) cp16(&qraw[buf][i * E], qp + (size_t)t0 * DK + i * E);
     }
-    const int per = nr / E;
+    const int per = matrix ? 0 : nr / E;
     for (int i = tid; i < n * per; i += 128) {
       const int t = i / per, c = i % per;
       cp16(&xraw[buf][t * ROWS + c * E], xp + (size_t)(t0 + t) * a.dv + c * E);
@@ -79,13 +90,19 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
 
   u64 s[2 * NG];
   {
-    const float *init = MODE == kAdjoint ? a.dS_final : a.S0;
-    const float *src = init ? init + ((size_t)u * a.dv + r0 + r) * DK : nullptr;
+    const bool first = seg == (ADJ ? sg.n - 1 : 0);  // (from here the sweep starts)
+    const float *init = first ? (ADJ ? a.dS_final : a.S0) : SEG ? nullptr : ADJ ? sg.A : sg.S;
+    const float *src = init ? init + (((size_t)u * (first ? 1 : sg.n) + (first ? 0 : seg)) * a.dv + r0 + r) * DK : nullptr;
 #pragma unroll
     for (int g = 0; g < NG; g++) {
       const float4 x = (src && rin) ? *reinterpret_cast<const float4 *>(src + 4 * (j + 4 * g)) : make_float4(0, 0, 0, 0);
       s[2 * g] = pack2(x.x, x.y);
       s[2 * g + 1] = pack2(x.z, x.w);
+      if (matrix) {
+        const int d = r0 + r - 4 * (j + 4 * g);  // the diagonal's place in this group
+        s[2 * g] = pack2(d == 0 ? 1.0f : 0.0f, d == 1 ? 1.0f : 0.0f);
+        s[2 * g + 1] = pack2(d == 2 ? 1.0f : 0.0f, d == 3 ? 1.0f : 0.0f);
+      }
     }
   }
   auto store_state = [&](float *dst) {  // this lane's part of row r (dst: the unit's matrix)
@@ -98,12 +115,12 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
 
   const int NC = (T + kRuleChunk - 1) / kRuleChunk;
   constexpr int BPC = kRuleChunk / TB;  // blocks per chunk
-  fetch(MODE == kAdjoint ? nblk - 1 : 0, 0);
+  fetch(ADJ ? b1 - 1 : b0, 0);
   for (int it = 0; it < nblk; it++) {
-    const int blk = MODE == kAdjoint ? nblk - 1 - it : it, buf = it & 1;
+    const int blk = ADJ ? b1 - 1 - it : b0 + it, buf = it & 1;
     const int t0 = blk * TB, n = min(TB, T - t0);
     if (it + 1 < nblk) {
-      fetch(MODE == kAdjoint ? blk - 1 : blk + 1, buf ^ 1);
+      fetch(ADJ ? blk - 1 : blk + 1, buf ^ 1);
       cp_wait<1>();
     } else {
       cp_wait<0>();
@@ -123,15 +140,15 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
       __syncthreads();
     }
     if (MODE == kStates && blk % BPC == 0) store_state(ws.S + ((size_t)u * NC + blk / BPC) * a.dv * DK);
-    if (MODE == kAdjoint && (blk % BPC == BPC - 1 || blk == nblk - 1))
+    if (MODE == kAdjoint && (blk % BPC == BPC - 1 || blk == b1 - 1))
       store_state(ws.dS + ((size_t)u * NC + blk / BPC) * a.dv * DK);
     for (int tt = 0; tt < n; tt++) {
-      const int t = MODE == kAdjoint ? n - 1 - tt : tt;
+      const int t = ADJ ? n - 1 - tt : tt;
       const float g = gs[buf][t], b = bs[buf][t];
-      const float x = ld(xraw[buf], t * ROWS + r);
+      const float x = matrix ? 0.0f : ld(xraw[buf], t * ROWS + r);
       const ulonglong2 *kv = reinterpret_cast<const ulonglong2 *>(kf + t * DK);
       const ulonglong2 *qv = reinterpret_cast<const ulonglong2 *>(qf + t * DK);
-      if constexpr (MODE == kAdjoint) {
+      if constexpr (ADJ) {
         const u64 gx = pack2(a.scale * x, a.scale * x);
         u64 d0 = 0, d1 = 0;
         ulonglong2 kk[NG];
@@ -153,7 +170,7 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
           s[2 * i] = mul2(g2, fma2(w, kk[i].x, s[2 * i]));
           s[2 * i + 1] = mul2(g2, fma2(w, kk[i].y, s[2 * i + 1]));
         }
-        if (j == 0) os[t * ROWS + r] = du;
+        if (!SEG && j == 0) os[t * ROWS + r] = du;
       } else {
         u64 d0 = 0, d1 = 0;
         ulonglong2 kk[NG];
@@ -185,13 +202,13 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
           o += __shfl_xor_sync(0xffffffffu, o, 2);
           if (j == 0) os[t * ROWS + r] = a.scale * o;
         } else {
-          if (j == 0) os[t * ROWS + r] = e;
+          if (!SEG && j == 0) os[t * ROWS + r] = e;
         }
       }
     }
     __syncthreads();
     bool bad = false;
-    for (int i = tid; i < n * ROWS; i += 128) {
+    for (int i = tid; i < (SEG ? 0 : n * ROWS); i += 128) {
       const int t = i / ROWS, rr = i % ROWS;
       if (rr >= nr) continue;
       const size_t at = (tu + t0 + t) * a.dv + r0 + rr;
@@ -205,8 +222,93 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
     }
     if (MODE == kForward && bad) atomicOr(a.status, tc_err_nonfinite());
   }
-  if (MODE == kForward && a.S_final) store_state(a.S_final + (size_t)u * a.dv * DK);
-  if (MODE == kAdjoint && a.dS0) store_state(a.dS0 + (size_t)u * a.dv * DK);
+  if (MODE == kForward && a.S_final && seg == sg.n - 1) store_state(a.S_final + (size_t)u * a.dv * DK);
+  if (MODE == kAdjoint && a.dS0 && seg == 0) store_state(a.dS0 + (size_t)u * a.dv * DK);
+  if (SEG && !matrix) store_state((ADJ ? sg.adj : sg.loc) + ((size_t)u * sg.n + seg) * a.dv * DK);
+  if (matrix) {
+    const size_t at = ((size_t)u * sg.n + seg) * DK * DK;
+    store_state(sg.Tr + at);
+    if (sg.TrT && rin) {
+#pragma unroll
+      for (int i = 0; i < 2 * NG; i++) {
+        const int c = 4 * (j + 4 * (i >> 1)) + 2 * (i & 1);
+        float x, y;
+        unpack2(s[i], x, y);
+        sg.TrT[at + (size_t)c * DK + r0 + r] = x;
+        sg.TrT[at + (size_t)(c + 1) * DK + r0 + r] = y;
+      }
+    }
+  }
+}
+
+// The state before each segment: start[y + 1] = start[y] M[y] + local[y] (the first: local[0]); downwards for
+// the adjoint.  A chain of n short products, so what counts is a step's latency: eight rows by a CTA of
+// 128 threads (more rows would read a matrix from shared memory more often in a step), DK / 16 columns
+// a thread, the matrices and local states of the next two or three steps on their way by cp.async.
+constexpr int JROWS = 8;
+template <int DK>
+struct JoinBuffers {
+  static constexpr int n = DK == 128 ? 3 : 4, bytes = n * (DK * DK + JROWS * DK) * (int)sizeof(float);
+};
+template <int DK>
+__global__ void __launch_bounds__(128) mesa_rule_scan_join_kernel(RuleScanSegments sg, int dv, bool adjoint) {
+  constexpr int CPT = DK / 16, MAT = DK * DK, BUF = MAT + JROWS * DK, NB = JoinBuffers<DK>::n;
+  extern __shared__ __align__(16) float jm[];  // NB buffers: a matrix, the local rows
+  __shared__ __align__(16) float rows[2][JROWS][DK];
+  const int u = blockIdx.y, tid = threadIdx.x, r = tid >> 4, c0 = (tid & 15) * CPT, row0 = blockIdx.x * JROWS;
+  const float *local = adjoint ? sg.adj : sg.loc, *M = adjoint ? sg.TrT : sg.Tr;
+  float *start = adjoint ? sg.A : sg.S;
+  auto at = [&](int i) { return (size_t)u * sg.n + (adjoint ? sg.n - 1 - i : i); };
+  auto fetch = [&](int i) {  // (a step past the last: an empty group)
+    if (i + 1 < sg.n) {
+      float *buf = jm + (i % NB) * BUF;
+      for (int e = tid; e < (i > 0 ? MAT / 4 : 0); e += 128) cp16(buf + 4 * e, M + at(i) * MAT + 4 * e);
+      for (int e = tid; e < JROWS * DK / 4; e += 128) cp16(buf + MAT + 4 * e, local + (at(i) * dv + row0) * DK + 4 * e);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < NB - 1; i++) fetch(i);
+  for (int i = 0; i + 1 < sg.n; i++) {
+    cp_wait<NB - 2>();
+    __syncthreads();  // the rows and this step's buffer are there, the last step's has been read
+    fetch(i + NB - 1);
+    float x[CPT];
+    const float *m = jm + (i % NB) * BUF + c0;
+#pragma unroll
+    for (int c = 0; c < CPT; c++) x[c] = m[MAT + r * DK + c];
+    if (i > 0) {
+      float y[CPT] = {};  // (a second sum: half the chain)
+#pragma unroll
+      for (int k = 0; k < DK; k += 4) {
+        const float4 s4 = *reinterpret_cast<const float4 *>(&rows[i & 1][r][k]);
+        const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          float w[CPT];
+          if constexpr (CPT >= 4) {
+#pragma unroll
+            for (int c = 0; c < CPT; c += 4)
+              *reinterpret_cast<float4 *>(&w[c]) = *reinterpret_cast<const float4 *>(m + (k + e) * DK + c);
+          } else {
+#pragma unroll
+            for (int c = 0; c < CPT; c++) w[c] = m[(k + e) * DK + c];
+          }
+#pragma unroll
+          for (int c = 0; c < CPT; c++) (e & 1 ? y : x)[c] = fmaf(s[e], w[c], (e & 1 ? y : x)[c]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < CPT; c++) x[c] += y[c];
+    }
+    float *dst = start + ((at(i) + (adjoint ? -1 : 1)) * dv + row0 + r) * DK + c0;
+#pragma unroll
+    for (int c = 0; c < CPT; c++) {
+      rows[(i + 1) & 1][r][c0 + c] = x[c];
+      dst[c] = x[c];
+    }
+  }
+  cp_wait<0>();
 }
 
 // The gradients of one 32-token chunk of one unit, from the state before it, the adjoint after
@@ -478,16 +580,44 @@ __global__ void __launch_bounds__(128) mesa_rule_step_kernel(RuleStepArgs a) {
 }
 
 template <int DK, typename TIO, int MODE>
-int launch_scan(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st) {
+int launch_scan(const RuleArgs &a, const RuleBwdWorkspace &ws, const RuleScanSegments &sg, cudaStream_t st) {
+  const int tiles = (a.dv + ROWS - 1) / ROWS + (MODE == kSegment ? (DK + ROWS - 1) / ROWS : 0);
+  const int segs = MODE == kSegment || MODE == kSegAdjoint ? sg.n - 1 : sg.n;
   timing_mark_begin(K_RULE_SCAN, st);
-  mesa_rule_scan_kernel<DK, TIO, MODE><<<dim3((a.dv + ROWS - 1) / ROWS, a.units()), 128, 0, st>>>(a, ws);
+  mesa_rule_scan_kernel<DK, TIO, MODE><<<dim3(tiles, a.units(), segs), 128, 0, st>>>(a, ws, sg);
   timing_mark_end(K_RULE_SCAN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
+template <int DK>
+int launch_scan_join(const RuleArgs &a, const RuleScanSegments &sg, bool adjoint, cudaStream_t st) {
+  const int smem = JoinBuffers<DK>::bytes;
+  auto kfn = mesa_rule_scan_join_kernel<DK>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+  timing_mark_begin(K_RULE_JOIN, st);
+  kfn<<<dim3(a.dv / JROWS, a.units()), 128, smem, st>>>(sg, a.dv, adjoint);  // (dv: a multiple of 16)
+  timing_mark_end(K_RULE_JOIN, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+// Segments of a unit's tokens: about four CTAs for each of a GB300's 152 SMs (the chain of one leaves most of an
+// SM idle), whole chunks, at least two each (shorter ones gain less than the joining costs), at most 16 (2 x 4 heads
+// x 2048 x 64 fp32: 12 segments 110 us, 16: 90, 24 and 32: 94, one: 447); fewer than four are not worth the two
+// more passes.
+int scan_segments(int U, int T, int dv) {
+  const int NC = (T + kRuleChunk - 1) / kRuleChunk, ctas = U * ((dv + ROWS - 1) / ROWS);
+  int n = ctas > 0 ? 4 * 152 / ctas : 1;
+  if (n > NC / 2) n = NC / 2;
+  if (n > 16) n = 16;
+  return n < 4 ? 1 : n;
+}
+
 template <int DK, typename TIO>
-int launch_bwd_t(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st) {
-  if (launch_scan<DK, TIO, kStates>(a, ws, st) != 0 || launch_scan<DK, TIO, kAdjoint>(a, ws, st) != 0) return -1;
+int launch_bwd_t(const RuleArgs &a, const RuleBwdWorkspace &ws, const RuleScanSegments &sg, cudaStream_t st) {
+  if (sg.n > 1 && (launch_scan<DK, TIO, kSegment>(a, ws, sg, st) != 0 || launch_scan_join<DK>(a, sg, false, st) != 0 ||
+                   launch_scan<DK, TIO, kSegAdjoint>(a, ws, sg, st) != 0 || launch_scan_join<DK>(a, sg, true, st) != 0))
+    return -1;
+  if (launch_scan<DK, TIO, kStates>(a, ws, sg, st) != 0 || launch_scan<DK, TIO, kAdjoint>(a, ws, sg, st) != 0) return -1;
   const int smem = (2 * kRuleChunk * (DK + 4) + 3 * kRuleChunk * (a.dv + 4) + 4 * kRuleChunk * (kRuleChunk + 1) +
                     5 * kRuleChunk + 8) * (int)sizeof(float);
   auto kfn = mesa_rule_grads_kernel<DK, TIO>;
@@ -519,15 +649,43 @@ int launch_step_t(const RuleStepArgs &a, cudaStream_t st) {
   return -1
 
 template <int DK, typename TIO>
-int launch_fwd_t(const RuleArgs &a, cudaStream_t st) {
-  return launch_scan<DK, TIO, kForward>(a, RuleBwdWorkspace{}, st);
+int launch_fwd_t(const RuleArgs &a, const RuleScanSegments &sg, cudaStream_t st) {
+  const RuleBwdWorkspace none{};
+  if (sg.n > 1 && (launch_scan<DK, TIO, kSegment>(a, none, sg, st) != 0 || launch_scan_join<DK>(a, sg, false, st) != 0))
+    return -1;
+  return launch_scan<DK, TIO, kForward>(a, none, sg, st);
 }
 
 }  // namespace
 
-int launch_rule_forward(const RuleArgs &a, cudaStream_t st) { MESA_RULE_DISPATCH(launch_fwd_t, a, a, st); }
-int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st) {
-  MESA_RULE_DISPATCH(launch_bwd_t, a, a, ws, st);
+size_t rule_scan_workspace(int U, int T, int dk, int dv, bool backward) {
+  const size_t n = scan_segments(U, T, dv), mat = (size_t)dk * dk * sizeof(float), state = (size_t)dv * dk * sizeof(float);
+  return n == 1 ? 0 : U * n * (2 * state + mat) * (backward ? 2 : 1);
+}
+RuleScanSegments rule_scan_parts(int U, int T, int dk, int dv, bool backward, void *workspace) {
+  const int blocks = kRuleChunk / TB, NC = (T + kRuleChunk - 1) / kRuleChunk;
+  RuleScanSegments sg;
+  sg.n = scan_segments(U, T, dv);
+  sg.per = (NC + sg.n - 1) / sg.n * blocks;
+  if (sg.n == 1) return sg;
+  const size_t mat = (size_t)U * sg.n * dk * dk, state = (size_t)U * sg.n * dv * dk;
+  sg.n = (NC * blocks + sg.per - 1) / sg.per;  // (no empty one)
+  sg.S = (float *)workspace;
+  sg.loc = sg.S + state;
+  sg.Tr = sg.loc + state;
+  if (backward) {
+    sg.A = sg.Tr + mat;
+    sg.adj = sg.A + state;
+    sg.TrT = sg.adj + state;
+  }
+  return sg;
+}
+
+int launch_rule_forward(const RuleArgs &a, const RuleScanSegments &sg, cudaStream_t st) {
+  MESA_RULE_DISPATCH(launch_fwd_t, a, a, sg, st);
+}
+int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, const RuleScanSegments &sg, cudaStream_t st) {
+  MESA_RULE_DISPATCH(launch_bwd_t, a, a, ws, sg, st);
 }
 int launch_rule_step(const RuleStepArgs &a, cudaStream_t st) { MESA_RULE_DISPATCH(launch_step_t, a, a, st); }
 

@@ -36,6 +36,14 @@ struct RuleBwdWorkspace {
   float *dqp, *dkp;    // [U, T, dk] per-unit dq, dk (nullptr when every head has its own q, k)
 };
 
+// Few units: n segments of `per` blocks of tokens that run side by side (one: nothing is used).
+struct RuleScanSegments {
+  int n = 1, per = 0;
+  float *S = nullptr, *loc = nullptr;   // [U, n][dv, dk] the state before a segment; what it leaves from zero
+  float *A = nullptr, *adj = nullptr;   // [U, n][dv, dk] the adjoint after a segment; what it gives from zero
+  float *Tr = nullptr, *TrT = nullptr;  // [U, n][dk, dk] the matrix from the state before to the state after
+};
+
 struct RuleStepArgs {
   int N, H, Hk, dk, dv, dtype;
   float *S;
@@ -46,8 +54,10 @@ struct RuleStepArgs {
 };
 
 // Each returns 0 when every launch was enqueued, -1 otherwise.
-int launch_rule_forward(const RuleArgs &a, cudaStream_t st);
-int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, cudaStream_t st);
+size_t rule_scan_workspace(int U, int T, int dk, int dv, bool backward);
+RuleScanSegments rule_scan_parts(int U, int T, int dk, int dv, bool backward, void *workspace);
+int launch_rule_forward(const RuleArgs &a, const RuleScanSegments &sg, cudaStream_t st);
+int launch_rule_backward(const RuleArgs &a, const RuleBwdWorkspace &ws, const RuleScanSegments &sg, cudaStream_t st);
 int launch_rule_step(const RuleStepArgs &a, cudaStream_t st);
 // The tensor-core path (bf16, dk = dv = 128): workspace bytes, the chunks' records (with_beta: the
 // forward's), the forward.

@@ -61,6 +61,14 @@ FWD = [  # dtype, B, H, Hk, T, dk, dv, gates, states
     ("bf16", 1, 2, 2, 200, 128, 128, "one", False),
     ("bf16", 1, 2, 2, 150, 128, 128, "shut", True),
     ("bf16", 1, 1, 1, 2500, 128, 128, "open", True),
+    # few units on the CUDA cores: segments of tokens side by side
+    ("f32", 1, 2, 1, 256, 16, 32, "open", True),
+    ("f32", 1, 3, 3, 777, 32, 32, "packed", True),
+    ("f32", 2, 2, 2, 1025, 64, 64, "one", True),
+    ("f32", 1, 1, 1, 2048, 128, 128, "open", False),
+    ("f32", 1, 1, 1, 500, 64, 16, "wide", True),
+    ("bf16", 1, 2, 1, 999, 64, 64, "open", True),
+    ("bf16", 1, 1, 1, 400, 128, 32, "shut", True),
 ]
 
 
@@ -98,6 +106,11 @@ BWD = [
     ("bf16", 1, 2, 2, 300, 128, 128, "wide", True),
     ("bf16", 1, 2, 2, 190, 128, 128, "one", False),
     ("bf16", 1, 2, 1, 99, 128, 128, "shut", True),
+    ("f32", 1, 2, 1, 256, 16, 32, "open", True),
+    ("f32", 1, 3, 1, 777, 32, 32, "packed", True),
+    ("f32", 1, 1, 1, 1025, 64, 64, "one", True),
+    ("f32", 1, 1, 1, 700, 128, 32, "wide", False),
+    ("bf16", 1, 2, 1, 600, 64, 64, "open", True),
 ]
 
 
