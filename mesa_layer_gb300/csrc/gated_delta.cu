@@ -24,6 +24,10 @@ __device__ __forceinline__ void cp16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                : "memory");
 }
+__device__ __forceinline__ void cp4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -32,14 +36,16 @@ __device__ __forceinline__ void cp_wait() {
 
 enum ScanMode { kForward = 0, kStates = 1, kAdjoint = 2, kSegment = 3, kSegAdjoint = 4 };
 constexpr int TB = 16;    // tokens staged at a time
-constexpr int ROWS = 32;  // state rows per CTA, four lanes each
+constexpr int ROWS = 32;  // state rows per CTA
+constexpr int lanes_per_row(int dk) { return dk == 128 ? 4 : 2; }
 
 // One CTA: 32 rows of one unit's state through all tokens.  The recurrence is a dependent
-// chain per token (sum over dk, two shuffles, rank-one update); four lanes a row keep the
-// in-lane sums short and leave enough CTAs for small batches.  k, q and v (or dout) of the
-// next 16 tokens arrive by cp.async while a block of 16 is worked on; bf16 is widened once per
-// block.  Bound by the chain's latency when units are few, by FMA issue when they are many
-// (packed fp32 pairs halve the issue slots).
+// chain per token (sum over dk, shuffles, rank-one update).  Few lanes a row: the sum's tail (shuffles, gate,
+// error) and the reads of k and q then cost fewer instructions beside the products (2 x 4 x 2048 x 64 fp32,
+// both passes: four lanes 63 us, two 55; 32 columns, four passes: four 50, two 48, one 56).  k, q and v (or dout)
+// of the next 16 tokens arrive by cp.async while a block of 16 is worked on; bf16 is widened once per
+// block.  Bound by the chain's latency when units are few, by FMA issue when they are many (packed
+// fp32 pairs halve the issue slots).
 //   kForward: out, S_final.  kStates: e and the state before each 32-token chunk.
 //   kAdjoint: tokens descending; du and the adjoint after each chunk, dS0.
 // Few units: the tokens are cut into segments (blockIdx.z) that run side by side, each from the state
@@ -49,18 +55,20 @@ constexpr int ROWS = 32;  // state rows per CTA, four lanes each
 //   the segment to its part of the state after it (and that matrix transposed, which takes the adjoint back).
 //   kSegAdjoint: the adjoint before segment z + 1 from zero after it (the last: dS_final).
 template <int DK, typename TIO, int MODE>
-__global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwdWorkspace ws, RuleScanSegments sg) {
+__global__ void __launch_bounds__(ROWS * lanes_per_row(DK)) mesa_rule_scan_kernel(RuleArgs a, RuleBwdWorkspace ws, RuleScanSegments sg) {
   constexpr bool ADJ = MODE == kAdjoint || MODE == kSegAdjoint, SEG = MODE == kSegment || MODE == kSegAdjoint;
-  constexpr int VPL = DK / 4, NG = VPL / 4;  // values and 16-byte groups per lane
+  constexpr int LPR = lanes_per_row(DK), NT = ROWS * LPR, RPW = 32 / LPR;  // threads, rows of a warp
+  constexpr int VPL = DK / LPR, NG = VPL / 4;                              // values and 16-byte groups per lane
   constexpr bool WIDE = sizeof(TIO) == 4;
   constexpr bool USEQ = MODE == kForward || ADJ;
   __shared__ __align__(16) TIO kraw[2][TB * DK], qraw[2][USEQ ? TB * DK : 8], xraw[2][TB * ROWS];
   __shared__ __align__(16) float kwide[WIDE ? 4 : TB * DK], qwide[WIDE || !USEQ ? 4 : TB * DK];
-  __shared__ float os[TB * ROWS], gs[2][TB], bs[2][TB];
+  __shared__ __align__(16) float os[TB * ROWS * (MODE == kForward ? LPR : 1)];
+  __shared__ float gs[2][TB], bs[2][TB];
   const int u = blockIdx.y, tiles = (a.dv + ROWS - 1) / ROWS, tid = threadIdx.x;
   const bool matrix = MODE == kSegment && (int)blockIdx.x >= tiles;
   const int r0 = (blockIdx.x - (matrix ? tiles : 0)) * ROWS;
-  const int r = tid >> 2, j = tid & 3, nr = min(ROWS, (matrix ? DK : a.dv) - r0);
+  const int r = tid / LPR, j = tid % LPR, nr = min(ROWS, (matrix ? DK : a.dv) - r0);
   const int T = a.T, seg = blockIdx.z + (MODE == kSegAdjoint ? 1 : 0);
   const int b0 = seg * sg.per, b1 = min((T + TB - 1) / TB, b0 + sg.per), nblk = b1 - b0;  // its blocks of tokens
   if (matrix && seg == 0) return;
@@ -71,19 +79,24 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
 
   auto fetch = [&](int blk, int buf) {
     const int t0 = blk * TB, n = min(TB, T - t0);
-    constexpr int E = 16 / sizeof(TIO);
-    for (int i = tid; i < n * DK / E; i += 128) {
-      cp16(&kraw[buf][i * E], kp + (size_t)t0 * DK + i * E);
-      if (USEQ) cp16(&qraw[buf][i * E], qp + (size_t)t0 * DK + i * E);
+    constexpr int E = 16 / sizeof(TIO), KV = TB * DK / E, XV = ROWS / E;
+    const TIO *ks = kp + (size_t)t0 * DK, *qs = qp + (size_t)t0 * DK, *xs = xp + (size_t)t0 * a.dv;
+#pragma unroll
+    for (int i0 = 0; i0 < KV; i0 += NT) {
+      const int i = i0 + tid;
+      if (i * E < n * DK) {
+        cp16(&kraw[buf][i * E], ks + i * E);
+        if (USEQ) cp16(&qraw[buf][i * E], qs + i * E);
+      }
     }
-    const int per = matrix ? 0 : nr / E;
-    for (int i = tid; i < n * per; i += 128) {
-      const int t = i / per, c = i % per;
-      cp16(&xraw[buf][t * ROWS + c * E], xp + (size_t)(t0 + t) * a.dv + c * E);
+#pragma unroll
+    for (int i0 = 0; i0 < TB * XV; i0 += NT) {
+      const int i = i0 + tid, t = i / XV, c = i % XV * E;
+      if (t < n && c < nr && !matrix) cp16(&xraw[buf][t * ROWS + c], xs + (size_t)t * a.dv + c);
     }
     if (tid < n) {
-      gs[buf][tid] = a.gamma[tu + t0 + tid];
-      bs[buf][tid] = a.beta[tu + t0 + tid];
+      cp4(&gs[buf][tid], a.gamma + tu + t0 + tid);
+      cp4(&bs[buf][tid], a.beta + tu + t0 + tid);
     }
     cp_commit();
   };
@@ -95,11 +108,11 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
     const float *src = init ? init + (((size_t)u * (first ? 1 : sg.n) + (first ? 0 : seg)) * a.dv + r0 + r) * DK : nullptr;
 #pragma unroll
     for (int g = 0; g < NG; g++) {
-      const float4 x = (src && rin) ? *reinterpret_cast<const float4 *>(src + 4 * (j + 4 * g)) : make_float4(0, 0, 0, 0);
+      const float4 x = (src && rin) ? *reinterpret_cast<const float4 *>(src + 4 * (j + LPR * g)) : make_float4(0, 0, 0, 0);
       s[2 * g] = pack2(x.x, x.y);
       s[2 * g + 1] = pack2(x.z, x.w);
       if (matrix) {
-        const int d = r0 + r - 4 * (j + 4 * g);  // the diagonal's place in this group
+        const int d = r0 + r - 4 * (j + LPR * g);  // the diagonal's place in this group
         s[2 * g] = pack2(d == 0 ? 1.0f : 0.0f, d == 1 ? 1.0f : 0.0f);
         s[2 * g + 1] = pack2(d == 2 ? 1.0f : 0.0f, d == 3 ? 1.0f : 0.0f);
       }
@@ -109,7 +122,7 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
     if (!rin) return;
 #pragma unroll
     for (int g = 0; g < NG; g++)
-      *reinterpret_cast<ulonglong2 *>(dst + (size_t)(r0 + r) * DK + 4 * (j + 4 * g)) =
+      *reinterpret_cast<ulonglong2 *>(dst + (size_t)(r0 + r) * DK + 4 * (j + LPR * g)) =
           make_ulonglong2(s[2 * g], s[2 * g + 1]);
   };
 
@@ -119,19 +132,15 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
   for (int it = 0; it < nblk; it++) {
     const int blk = ADJ ? b1 - 1 - it : b0 + it, buf = it & 1;
     const int t0 = blk * TB, n = min(TB, T - t0);
-    if (it + 1 < nblk) {
-      fetch(ADJ ? blk - 1 : blk + 1, buf ^ 1);
-      cp_wait<1>();
-    } else {
-      cp_wait<0>();
-    }
-    __syncthreads();
+    cp_wait<0>();
+    __syncthreads();  // this block is there, and the last one has been used
+    if (it + 1 < nblk) fetch(ADJ ? blk - 1 : blk + 1, buf ^ 1);
     const float *kf, *qf;
     if constexpr (WIDE) {
       kf = kraw[buf];
       qf = qraw[buf];
     } else {
-      for (int i = tid; i < TB * DK / 4; i += 128) {
+      for (int i = tid; i < TB * DK / 4; i += NT) {
         *reinterpret_cast<float4 *>(&kwide[4 * i]) = load4(kraw[buf], 4 * i);
         if (USEQ) *reinterpret_cast<float4 *>(&qwide[4 * i]) = load4(qraw[buf], 4 * i);
       }
@@ -142,85 +151,117 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
     if (MODE == kStates && blk % BPC == 0) store_state(ws.S + ((size_t)u * NC + blk / BPC) * a.dv * DK);
     if (MODE == kAdjoint && (blk % BPC == BPC - 1 || blk == b1 - 1))
       store_state(ws.dS + ((size_t)u * NC + blk / BPC) * a.dv * DK);
-    for (int tt = 0; tt < n; tt++) {
-      const int t = ADJ ? n - 1 - tt : tt;
-      const float g = gs[buf][t], b = bs[buf][t];
-      const float x = matrix ? 0.0f : ld(xraw[buf], t * ROWS + r);
+    // a token's key, gates and value are read a token ahead, its query at its start: nothing on the
+    // chain waits for shared memory
+    struct Token {
+      ulonglong2 k[NG];
+      float x, g, b;
+    } cur, nxt;
+    auto load_token = [&](int t, Token &w) {
       const ulonglong2 *kv = reinterpret_cast<const ulonglong2 *>(kf + t * DK);
+#pragma unroll
+      for (int i = 0; i < NG; i++) w.k[i] = kv[j + LPR * i];
+      w.x = matrix ? 0.0f : ld(xraw[buf], t * ROWS + r);
+      w.g = gs[buf][t];
+      w.b = bs[buf][t];
+    };
+    auto token = [&](int t, const Token &w) {
       const ulonglong2 *qv = reinterpret_cast<const ulonglong2 *>(qf + t * DK);
+      const u64 g2 = pack2(w.g, w.g);
+      ulonglong2 qq[NG];
+      if constexpr (USEQ) {
+#pragma unroll
+        for (int i = 0; i < NG; i++) qq[i] = qv[j + LPR * i];
+      }
+      u64 d[4] = {};  // (four sums: short chains)
       if constexpr (ADJ) {
-        const u64 gx = pack2(a.scale * x, a.scale * x);
-        u64 d0 = 0, d1 = 0;
-        ulonglong2 kk[NG];
+        const u64 gx = pack2(a.scale * w.x, a.scale * w.x);
 #pragma unroll
         for (int i = 0; i < NG; i++) {
-          const ulonglong2 qq = qv[j + 4 * i];
-          kk[i] = kv[j + 4 * i];
-          s[2 * i] = fma2(gx, qq.x, s[2 * i]);
-          s[2 * i + 1] = fma2(gx, qq.y, s[2 * i + 1]);
-          d0 = fma2(s[2 * i], kk[i].x, d0);
-          d1 = fma2(s[2 * i + 1], kk[i].y, d1);
+          s[2 * i] = fma2(gx, qq[i].x, s[2 * i]);
+          s[2 * i + 1] = fma2(gx, qq[i].y, s[2 * i + 1]);
+          d[2 * (i & 1)] = fma2(s[2 * i], w.k[i].x, d[2 * (i & 1)]);
+          d[2 * (i & 1) + 1] = fma2(s[2 * i + 1], w.k[i].y, d[2 * (i & 1) + 1]);
         }
-        float du = sum2(d0) + sum2(d1);
-        du += __shfl_xor_sync(0xffffffffu, du, 1);
-        du += __shfl_xor_sync(0xffffffffu, du, 2);
-        const u64 w = pack2(-b * du, -b * du), g2 = pack2(g, g);
+        float du = sum2(add2(add2(d[0], d[1]), add2(d[2], d[3])));
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) du += __shfl_xor_sync(0xffffffffu, du, o);
+        const u64 p = pack2(-w.b * du, -w.b * du);
 #pragma unroll
         for (int i = 0; i < NG; i++) {
-          s[2 * i] = mul2(g2, fma2(w, kk[i].x, s[2 * i]));
-          s[2 * i + 1] = mul2(g2, fma2(w, kk[i].y, s[2 * i + 1]));
+          s[2 * i] = mul2(g2, fma2(p, w.k[i].x, s[2 * i]));
+          s[2 * i + 1] = mul2(g2, fma2(p, w.k[i].y, s[2 * i + 1]));
         }
         if (!SEG && j == 0) os[t * ROWS + r] = du;
       } else {
-        u64 d0 = 0, d1 = 0;
-        ulonglong2 kk[NG];
 #pragma unroll
         for (int i = 0; i < NG; i++) {
-          kk[i] = kv[j + 4 * i];
-          d0 = fma2(s[2 * i], kk[i].x, d0);
-          d1 = fma2(s[2 * i + 1], kk[i].y, d1);
+          d[2 * (i & 1)] = fma2(s[2 * i], w.k[i].x, d[2 * (i & 1)]);
+          d[2 * (i & 1) + 1] = fma2(s[2 * i + 1], w.k[i].y, d[2 * (i & 1) + 1]);
+          s[2 * i] = mul2(g2, s[2 * i]);
+          s[2 * i + 1] = mul2(g2, s[2 * i + 1]);
         }
-        float d = sum2(d0) + sum2(d1);
-        d += __shfl_xor_sync(0xffffffffu, d, 1);
-        d += __shfl_xor_sync(0xffffffffu, d, 2);
-        const float e = fmaf(-g, d, x), uu = b * e;
-        const u64 u2 = pack2(uu, uu), g2 = pack2(g, g);
-        u64 o0 = 0, o1 = 0;
+        float sk = sum2(add2(add2(d[0], d[1]), add2(d[2], d[3])));
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) sk += __shfl_xor_sync(0xffffffffu, sk, o);
+        const float e = fmaf(-w.g, sk, w.x), uu = w.b * e;
+        const u64 u2 = pack2(uu, uu);
+        u64 o[4] = {};
 #pragma unroll
         for (int i = 0; i < NG; i++) {
-          s[2 * i] = fma2(u2, kk[i].x, mul2(g2, s[2 * i]));
-          s[2 * i + 1] = fma2(u2, kk[i].y, mul2(g2, s[2 * i + 1]));
+          s[2 * i] = fma2(u2, w.k[i].x, s[2 * i]);
+          s[2 * i + 1] = fma2(u2, w.k[i].y, s[2 * i + 1]);
           if constexpr (MODE == kForward) {
-            const ulonglong2 qq = qv[j + 4 * i];
-            o0 = fma2(s[2 * i], qq.x, o0);
-            o1 = fma2(s[2 * i + 1], qq.y, o1);
+            o[2 * (i & 1)] = fma2(s[2 * i], qq[i].x, o[2 * (i & 1)]);
+            o[2 * (i & 1) + 1] = fma2(s[2 * i + 1], qq[i].y, o[2 * (i & 1) + 1]);
           }
         }
         if constexpr (MODE == kForward) {
-          float o = sum2(o0) + sum2(o1);
-          o += __shfl_xor_sync(0xffffffffu, o, 1);
-          o += __shfl_xor_sync(0xffffffffu, o, 2);
-          if (j == 0) os[t * ROWS + r] = a.scale * o;
+          os[(t * ROWS + r) * LPR + j] = sum2(add2(add2(o[0], o[1]), add2(o[2], o[3])));  // (added over the lanes when the block is written)
         } else {
           if (!SEG && j == 0) os[t * ROWS + r] = e;
         }
       }
-    }
-    __syncthreads();
-    bool bad = false;
-    for (int i = tid; i < (SEG ? 0 : n * ROWS); i += 128) {
-      const int t = i / ROWS, rr = i % ROWS;
-      if (rr >= nr) continue;
-      const size_t at = (tu + t0 + t) * a.dv + r0 + rr;
-      const float y = os[i];
-      if (MODE == kForward) {
-        st((TIO *)a.out, at, y);
-        bad |= !isfinite(y);
-      } else {
-        (MODE == kStates ? ws.e : ws.du)[at] = y;
+    };
+    auto nth = [&](int tt) { return ADJ ? max(n - 1 - tt, 0) : min(tt, n - 1); };
+    load_token(nth(0), cur);
+    if (n == TB) {
+#pragma unroll 4
+      for (int tt = 0; tt < TB; tt += 2) {
+        load_token(nth(tt + 1), nxt);
+        token(nth(tt), cur);
+        load_token(nth(tt + 2), cur);
+        token(nth(tt + 1), nxt);
+      }
+    } else {
+      for (int tt = 0; tt < n; tt++) {
+        load_token(nth(tt), cur);
+        token(nth(tt), cur);
       }
     }
-    if (MODE == kForward && bad) atomicOr(a.status, tc_err_nonfinite());
+    if constexpr (!SEG) {  // a warp writes its own rows
+      __syncwarp();
+      bool bad = false;
+#pragma unroll
+      for (int i0 = 0; i0 < TB * RPW; i0 += 32) {
+        const int i = i0 + (tid & 31), t = i / RPW, rr = (tid >> 5) * RPW + i % RPW;
+        if (t < n && rr < nr) {
+          const size_t at = (tu + t0 + t) * a.dv + r0 + rr;
+          if constexpr (MODE == kForward) {
+            float y = 0.0f;
+#pragma unroll
+            for (int l = 0; l < LPR; l++) y += os[(t * ROWS + rr) * LPR + l];
+            y *= a.scale;
+            st((TIO *)a.out, at, y);
+            bad |= !isfinite(y);
+          } else {
+            (MODE == kStates ? ws.e : ws.du)[at] = os[t * ROWS + rr];
+          }
+        }
+      }
+      if (MODE == kForward && bad) atomicOr(a.status, tc_err_nonfinite());
+      __syncwarp();
+    }
   }
   if (MODE == kForward && a.S_final && seg == sg.n - 1) store_state(a.S_final + (size_t)u * a.dv * DK);
   if (MODE == kAdjoint && a.dS0 && seg == 0) store_state(a.dS0 + (size_t)u * a.dv * DK);
@@ -231,7 +272,7 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
     if (sg.TrT && rin) {
 #pragma unroll
       for (int i = 0; i < 2 * NG; i++) {
-        const int c = 4 * (j + 4 * (i >> 1)) + 2 * (i & 1);
+        const int c = 4 * (j + LPR * (i >> 1)) + 2 * (i & 1);
         float x, y;
         unpack2(s[i], x, y);
         sg.TrT[at + (size_t)c * DK + r0 + r] = x;
@@ -243,27 +284,34 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_kernel(RuleArgs a, RuleBwd
 
 // The state before each segment: start[y + 1] = start[y] M[y] + local[y] (the first: local[0]); downwards for
 // the adjoint.  A chain of n short products, so what counts is a step's latency: eight rows by a CTA of
-// 128 threads (more rows would read a matrix from shared memory more often in a step), DK / 16 columns
-// a thread, the matrices and local states of the next two or three steps on their way by cp.async.
+// 256 threads, a thread two rows, DK / 16 columns and a quarter of the sum (so that a matrix is read
+// from shared memory four times in a step, not eight, by eight warps), the matrices and local states of the
+// next steps on their way by cp.async.  (One row and the whole sum a thread: 1.0 us a step at DK = 64.)
 constexpr int JROWS = 8;
 template <int DK>
 struct JoinBuffers {
   static constexpr int n = DK == 128 ? 3 : 4, bytes = n * (DK * DK + JROWS * DK) * (int)sizeof(float);
 };
 template <int DK>
-__global__ void __launch_bounds__(128) mesa_rule_scan_join_kernel(RuleScanSegments sg, int dv, bool adjoint) {
-  constexpr int CPT = DK / 16, MAT = DK * DK, BUF = MAT + JROWS * DK, NB = JoinBuffers<DK>::n;
+__global__ void __launch_bounds__(256) mesa_rule_scan_join_kernel(RuleScanSegments sg, int dv, bool adjoint) {
+  constexpr int CPT = DK / 16, MAT = DK * DK, BUF = MAT + JROWS * DK, NB = JoinBuffers<DK>::n, KP = DK / 4;
   extern __shared__ __align__(16) float jm[];  // NB buffers: a matrix, the local rows
-  __shared__ __align__(16) float rows[2][JROWS][DK];
-  const int u = blockIdx.y, tid = threadIdx.x, r = tid >> 4, c0 = (tid & 15) * CPT, row0 = blockIdx.x * JROWS;
+  __shared__ __align__(16) float rows[JROWS][DK], part[4][JROWS][DK];
+  const int u = blockIdx.y, tid = threadIdx.x, row0 = blockIdx.x * JROWS;
+  const int kp = tid >> 6, r = (tid >> 4 & 3) * 2, c0 = (tid & 15) * CPT;
   const float *local = adjoint ? sg.adj : sg.loc, *M = adjoint ? sg.TrT : sg.Tr;
   float *start = adjoint ? sg.A : sg.S;
   auto at = [&](int i) { return (size_t)u * sg.n + (adjoint ? sg.n - 1 - i : i); };
   auto fetch = [&](int i) {  // (a step past the last: an empty group)
     if (i + 1 < sg.n) {
       float *buf = jm + (i % NB) * BUF;
-      for (int e = tid; e < (i > 0 ? MAT / 4 : 0); e += 128) cp16(buf + 4 * e, M + at(i) * MAT + 4 * e);
-      for (int e = tid; e < JROWS * DK / 4; e += 128) cp16(buf + MAT + 4 * e, local + (at(i) * dv + row0) * DK + 4 * e);
+      const float *src = M + at(i) * MAT, *lsrc = local + (at(i) * dv + row0) * DK;
+      if (i > 0) {
+#pragma unroll
+        for (int e = 0; e < MAT / 4; e += 256)
+          if (e + tid < MAT / 4) cp16(buf + 4 * (e + tid), src + 4 * (e + tid));
+      }
+      if (tid < JROWS * DK / 4) cp16(buf + MAT + 4 * tid, lsrc + 4 * tid);
     }
     cp_commit();
   };
@@ -273,16 +321,15 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_join_kernel(RuleScanSegmen
     cp_wait<NB - 2>();
     __syncthreads();  // the rows and this step's buffer are there, the last step's has been read
     fetch(i + NB - 1);
-    float x[CPT];
-    const float *m = jm + (i % NB) * BUF + c0;
-#pragma unroll
-    for (int c = 0; c < CPT; c++) x[c] = m[MAT + r * DK + c];
+    const float *buf = jm + (i % NB) * BUF;
     if (i > 0) {
-      float y[CPT] = {};  // (a second sum: half the chain)
+      const float *m = buf + kp * KP * DK + c0;
+      float x[CPT] = {}, y[CPT] = {};
 #pragma unroll
-      for (int k = 0; k < DK; k += 4) {
-        const float4 s4 = *reinterpret_cast<const float4 *>(&rows[i & 1][r][k]);
-        const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+      for (int k = 0; k < KP; k += 4) {
+        const float4 p4 = *reinterpret_cast<const float4 *>(&rows[r][kp * KP + k]);
+        const float4 q4 = *reinterpret_cast<const float4 *>(&rows[r + 1][kp * KP + k]);
+        const float p[4] = {p4.x, p4.y, p4.z, p4.w}, q[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           float w[CPT];
@@ -295,17 +342,29 @@ __global__ void __launch_bounds__(128) mesa_rule_scan_join_kernel(RuleScanSegmen
             for (int c = 0; c < CPT; c++) w[c] = m[(k + e) * DK + c];
           }
 #pragma unroll
-          for (int c = 0; c < CPT; c++) (e & 1 ? y : x)[c] = fmaf(s[e], w[c], (e & 1 ? y : x)[c]);
+          for (int c = 0; c < CPT; c++) {
+            x[c] = fmaf(p[e], w[c], x[c]);
+            y[c] = fmaf(q[e], w[c], y[c]);
+          }
         }
       }
 #pragma unroll
-      for (int c = 0; c < CPT; c++) x[c] += y[c];
+      for (int c = 0; c < CPT; c++) {
+        part[kp][r][c0 + c] = x[c];
+        part[kp][r + 1][c0 + c] = y[c];
+      }
+      __syncthreads();
     }
-    float *dst = start + ((at(i) + (adjoint ? -1 : 1)) * dv + row0 + r) * DK + c0;
+    float *dst = start + ((at(i) + (adjoint ? -1 : 1)) * dv + row0) * DK;
 #pragma unroll
-    for (int c = 0; c < CPT; c++) {
-      rows[(i + 1) & 1][r][c0 + c] = x[c];
-      dst[c] = x[c];
+    for (int e0 = 0; e0 < JROWS * DK; e0 += 256) {
+      const int e = e0 + tid;
+      if (e >= JROWS * DK) break;
+      const int rr = e / DK, c = e % DK;
+      float x = buf[MAT + e];
+      if (i > 0) x += (part[0][rr][c] + part[1][rr][c]) + (part[2][rr][c] + part[3][rr][c]);
+      rows[rr][c] = x;
+      dst[e] = x;
     }
   }
   cp_wait<0>();
@@ -584,7 +643,7 @@ int launch_scan(const RuleArgs &a, const RuleBwdWorkspace &ws, const RuleScanSeg
   const int tiles = (a.dv + ROWS - 1) / ROWS + (MODE == kSegment ? (DK + ROWS - 1) / ROWS : 0);
   const int segs = MODE == kSegment || MODE == kSegAdjoint ? sg.n - 1 : sg.n;
   timing_mark_begin(K_RULE_SCAN, st);
-  mesa_rule_scan_kernel<DK, TIO, MODE><<<dim3(tiles, a.units(), segs), 128, 0, st>>>(a, ws, sg);
+  mesa_rule_scan_kernel<DK, TIO, MODE><<<dim3(tiles, a.units(), segs), ROWS * lanes_per_row(DK), 0, st>>>(a, ws, sg);
   timing_mark_end(K_RULE_SCAN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
@@ -595,19 +654,18 @@ int launch_scan_join(const RuleArgs &a, const RuleScanSegments &sg, bool adjoint
   auto kfn = mesa_rule_scan_join_kernel<DK>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
   timing_mark_begin(K_RULE_JOIN, st);
-  kfn<<<dim3(a.dv / JROWS, a.units()), 128, smem, st>>>(sg, a.dv, adjoint);  // (dv: a multiple of 16)
+  kfn<<<dim3(a.dv / JROWS, a.units()), 256, smem, st>>>(sg, a.dv, adjoint);  // (dv: a multiple of 16)
   timing_mark_end(K_RULE_JOIN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 // Segments of a unit's tokens: about four CTAs for each of a GB300's 152 SMs (the chain of one leaves most of an
-// SM idle), whole chunks, at least two each (shorter ones gain less than the joining costs), at most 16 (2 x 4 heads
-// x 2048 x 64 fp32: 12 segments 110 us, 16: 90, 24 and 32: 94, one: 447); fewer than four are not worth the two
-// more passes.
+// SM idle), whole chunks, at most 16 (the join is a chain over them: 2 x 4 heads x 2048 x 64 fp32, 16 segments 69 us,
+// 24: 78, 32: 74, one: 447); fewer than four are not worth the two more passes.
 int scan_segments(int U, int T, int dv) {
   const int NC = (T + kRuleChunk - 1) / kRuleChunk, ctas = U * ((dv + ROWS - 1) / ROWS);
   int n = ctas > 0 ? 4 * 152 / ctas : 1;
-  if (n > NC / 2) n = NC / 2;
+  if (n > NC) n = NC;
   if (n > 16) n = 16;
   return n < 4 ? 1 : n;
 }
