@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) mbar_arrive(bar(b));
   };
   bool ok = true;
-  int v_sent = 1, rec_sent = min(NC, 3);  // fetches issued (thread 128)
+  int v_sent = 1, rec_sent = min(NC, 3);  // fetches issued (threads 256 and 128)
 
   if (warp < 4) {
     // ---- the chain: thread r holds row r of the state ----
@@ -596,52 +596,13 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
   } else if (warp < 8) {
-    // ---- transpose the values; write the readout ----
+    // ---- write the readout ----
     regs_down<kRegHelper>();
     const int h = tid - 128;
     const uint32_t tl = tbase + ((uint32_t)(32 * (warp - 4)) << 16);
-    auto transpose = [&](int c) -> bool {  // chunk c's values (the last chunk's have been used)
-      if (group_or(2, 128, !wait(bar(m->v_full), c & 1, limit, gave_up))) return false;
-      const uint32_t live = identity ? 0u : 0xffffffffu;  // (rows of the identity take no values)
-      // channels 32 w .. 32 w + 31 by warp w: eight channels x 32 tokens at a time
-      uint32_t mv = 0;
-#pragma unroll 1
-      for (int g = 0; g < 4; g++) {
-        const int ch8 = 4 * (warp - 4) + g;
-#pragma unroll
-        for (int t = 0; t < 2; t++) {
-          uint32_t x[4];
-          ldmatrix_x4_trans(x, tc::smem_u32(sm + CH_V + tile_off(32 * t + lane, ch8, C)));
-#pragma unroll
-          for (int k = 0; k < 4; k++) x[k] &= live;
-          mv = absmax_words(mv, make_uint4(x[0], x[1], x[2], x[3]));
-          const int r = 8 * ch8 + (lane >> 2);
-#pragma unroll
-          for (int k = 0; k < 4; k++)  // tokens 32 t + 8 k + 2 (lane % 4), + 1
-            *reinterpret_cast<float2 *>(sm + CH_VT + vt_off(r, 8 * t + 2 * k + ((lane & 3) >> 1)) + 8 * (lane & 1)) =
-                make_float2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
-        }
-      }
-      mv = absmax_fold(mv);
-      if (lane == 0) m->vmax[warp - 4] = __uint_as_float(mv << 16);  // of this warp's channels
-      warp_arrive(m->vt_full);
-      group_or(2, 128, false);
-      if (c + 1 < NC) {
-        if (h == 0) fetch_v(c + 1);
-        v_sent++;
-      }
-      return true;
-    };
     const uint32_t id64 = tc::idesc_f16(128, C, false, false);
     u64 nonfinite = 0;  // a NaN once an output was not finite
-    ok = transpose(0);
-    for (int c = 0; c < NC && ok; c++) {
-      if (c + 1 < NC) {
-        if (group_or(2, 128, !wait(bar(m->r_ready), c & 1, limit, gave_up)) || !transpose(c + 1)) {
-          ok = false;
-          break;
-        }
-      }
+    for (int c = 0; c < NC; c++) {
       bool got = wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
       got &= wait(bar(m->u_ready), c & 1, limit, gave_up);
       got = __all_sync(0xffffffffu, got);
@@ -736,7 +697,7 @@ __global__ void __launch_bounds__(384, 1)
     if (!(sum2(nonfinite) == 0.0f)) atomicOr(a.status, tc::kErrNonFinite);
     if (h == 0) tc::bulk_wait_all();
   } else {
-    // ---- K and Q as operands, up to three chunks in flight ----
+    // ---- K and Q as operands, up to three chunks in flight; the values transposed, one ahead ----
     regs_down<kRegConvert>();
     const int h = tid - 256, r0 = h >> 4, c8 = h & 15, uk = a.qk_unit(u);  // rows r0, r0 + 8 ..; 8 channels
     const size_t first = ((size_t)uk * T + (size_t)c0 * C + r0) * D + 8 * c8;
@@ -753,8 +714,48 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
     };
+    auto transpose = [&](int c) -> bool {  // chunk c's values, once the last chunk's have been used
+      if (group_or(3, 128, !(wait(bar(m->v_full), c & 1, limit, gave_up) &
+                             (c == 0 || wait(bar(m->r_ready), (c - 1) & 1, limit, gave_up))))) return false;
+      const uint32_t live = identity ? 0u : 0xffffffffu;  // (rows of the identity take no values)
+      // channels 32 w .. 32 w + 31 by warp w: eight channels x 32 tokens at a time
+      uint32_t mv = 0;
+#pragma unroll 1
+      for (int g = 0; g < 4; g++) {
+        const int ch8 = 4 * (warp - 8) + g;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+          uint32_t x[4];
+          ldmatrix_x4_trans(x, tc::smem_u32(sm + CH_V + tile_off(32 * t + lane, ch8, C)));
+#pragma unroll
+          for (int k = 0; k < 4; k++) x[k] &= live;
+          mv = absmax_words(mv, make_uint4(x[0], x[1], x[2], x[3]));
+          const int r = 8 * ch8 + (lane >> 2);
+#pragma unroll
+          for (int k = 0; k < 4; k++)  // tokens 32 t + 8 k + 2 (lane % 4), + 1
+            *reinterpret_cast<float2 *>(sm + CH_VT + vt_off(r, 8 * t + 2 * k + ((lane & 3) >> 1)) + 8 * (lane & 1)) =
+                make_float2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
+        }
+      }
+      mv = absmax_fold(mv);
+      if (lane == 0) m->vmax[warp - 8] = __uint_as_float(mv << 16);  // of this warp's channels
+      warp_arrive(m->vt_full);
+      group_or(3, 128, false);
+      if (c + 1 < NC) {
+        if (h == 0) fetch_v(c + 1);
+        v_sent++;
+      }
+      return true;
+    };
     load(0);
-    for (int c = 0; c < NC; c++) {
+    // tile 0, values 0, tiles up to NT - 1, then values c + 1 (once those of c are used) before tile c + NT
+    for (int c = 0; c < NC + NT - 1; c++) {
+      const int tv = c == 1 ? 0 : c < NT ? -1 : c - NT + 1;
+      if (tv >= 0 && !transpose(tv)) {
+        ok = false;
+        break;
+      }
+      if (c >= NC) continue;
       bool got = wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
       if (c >= NT) got &= wait(bar(m->tile_free[c % NT]), (c / NT - 1) & 1, limit, gave_up);
       if (!__all_sync(0xffffffffu, got)) {
@@ -785,8 +786,9 @@ __global__ void __launch_bounds__(384, 1)
       if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
       atomicOr(a.status, bits);
     }
+    if (tid == 256 && !tc::mbar_wait(bar(m->v_full), (v_sent - 1) & 1, tc::kWaitLimit)) atomicOr(a.status, tc::kErrDrainTimeout);
     if (tid == 128) {
-      bool in = tc::mbar_wait(bar(m->v_full), (v_sent - 1) & 1, tc::kWaitLimit);
+      bool in = true;
       for (int c = max(0, rec_sent - 3); c < rec_sent; c++)
         in &= tc::mbar_wait(bar(m->rec_full[c % 3]), (c / 3) & 1, tc::kWaitLimit);
       if (!in) atomicOr(a.status, tc::kErrDrainTimeout);
