@@ -702,9 +702,11 @@ __global__ void __launch_bounds__(384, 1)
     const int h = tid - 256, r0 = h >> 4, c8 = h & 15, uk = a.qk_unit(u);  // rows r0, r0 + 8 ..; 8 channels
     const size_t first = ((size_t)uk * T + (size_t)c0 * C + r0) * D + 8 * c8;
     const __nv_bfloat16 *kp = (const __nv_bfloat16 *)a.k + first, *qp = (const __nv_bfloat16 *)a.q + first;
-    uint4 x[8], y[8];  // the next chunk's rows, on their way while this one's are converted
+    uint4 x[8], y[8];  // the next chunk's rows, on their way while this one's are converted,
+    float2 scales;     // and its scales (not from the records in shared memory: those come later)
     auto load = [&](int c) {
       const int n = T - (c0 + c) * C - r0;
+      scales = *reinterpret_cast<const float2 *>(records + ((size_t)u * NCT + c0 + c) * REC + REC_S + 8);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         x[i] = y[i] = make_uint4(0, 0, 0, 0);
@@ -756,14 +758,12 @@ __global__ void __launch_bounds__(384, 1)
         break;
       }
       if (c >= NC) continue;
-      bool got = wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
-      if (c >= NT) got &= wait(bar(m->tile_free[c % NT]), (c / NT - 1) & 1, limit, gave_up);
+      const bool got = c < NT || wait(bar(m->tile_free[c % NT]), (c / NT - 1) & 1, limit, gave_up);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
         break;
       }
-      const float4 inv = *reinterpret_cast<const float4 *>(sm + CH_REC + (c % 3) * REC_PAD + REC_S);
-      const u64 sk2 = pack2(inv.z, inv.z), sq2 = pack2(inv.w, inv.w);
+      const u64 sk2 = pack2(scales.x, scales.x), sq2 = pack2(scales.y, scales.y);
       uint8_t *dst = sm + CH_TILE + (c % NT) * TILE + tile_off(r0, c8, 128);
 #pragma unroll
       for (int k = 0; k < 8; k++) {
