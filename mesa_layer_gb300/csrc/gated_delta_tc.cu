@@ -452,10 +452,11 @@ __global__ void __launch_bounds__(384, 1)
       // here is paid for on the chain)
       {
         const uint8_t *V = sm + CH_VT + r * 256;
+        float y[2][16];
+        tc::tmem_ld16(tl + T_D1, y[0]);
 #pragma unroll
         for (int h = 0; h < 4; h++) {
-          float z[16];
-          tc::tmem_ld16(tl + T_D1 + 16 * h, z);
+          float *z = y[h & 1];
           ulonglong2 vv[4], ff[4];
 #pragma unroll
           for (int k = 0; k < 4; k++) {
@@ -463,6 +464,7 @@ __global__ void __launch_bounds__(384, 1)
             vv[k] = *reinterpret_cast<const ulonglong2 *>(V + (((4 * h + k) ^ (r & 7)) << 4));
           }
           tc::tmem_ld_wait();
+          if (h < 3) tc::tmem_ld16(tl + T_D1 + 16 * (h + 1), y[(h + 1) & 1]);
           float v[8];
 #pragma unroll
           for (int k = 0; k < 4; k++) {
@@ -504,11 +506,13 @@ __global__ void __launch_bounds__(384, 1)
         uU = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float sU = bound_scale(uU, kTopRow, iU);
         const u64 sU2 = pack2(sU, sU);
+        float y[2][16];
+        tc::tmem_ld16(tl + T_D2, y[0]);
 #pragma unroll
         for (int h = 0; h < 4; h++) {
-          float x[16], v[8], w[8];
-          tc::tmem_ld16(tl + T_D2 + 16 * h, x);
+          float v[8], w[8], *x = y[h & 1];
           tc::tmem_ld_wait();
+          if (h < 3) tc::tmem_ld16(tl + T_D2 + 16 * (h + 1), y[(h + 1) & 1]);
 #pragma unroll
           for (int k = 0; k < 4; k++) {
             const ulonglong2 ff = *reinterpret_cast<const ulonglong2 *>(cc + 16 * h + 4 * k);
@@ -551,11 +555,13 @@ __global__ void __launch_bounds__(384, 1)
       tc::fence_after_sync();
       if (r == 0) mbar_arrive(bar(m->tile_free[c % NT]));
       {
+        float y[2][16];  // these columns and the next ones, on their way
+        tc::tmem_ld16(tl + T_DS, y[0]);
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-          float z[16], v[8];
-          tc::tmem_ld16(tl + T_DS + 16 * k, z);
+          float v[8], *z = y[k & 1];
           tc::tmem_ld_wait();
+          if (k < 7) tc::tmem_ld16(tl + T_DS + 16 * (k + 1), y[(k + 1) & 1]);
 #pragma unroll
           for (int i = 0; i < 8; i++) {
             S[8 * k + i] = fma2(pack2(z[2 * i], z[2 * i + 1]), w3_2, mul2(S[8 * k + i], dec));
