@@ -424,6 +424,14 @@ def _new(shape, dtype, device, stream):
     return t
 
 
+def _like(like, stream):
+    """_new of the shape and type of `like` (a shorter way through the allocator)."""
+    t = torch.empty_like(like)
+    if stream is not None and t.numel():
+        t.record_stream(stream)
+    return t
+
+
 def _workspace(workspace, nbytes, device, stream):
     if workspace is None:
         return _new(max(nbytes, 256), torch.uint8, device, stream)
@@ -511,7 +519,7 @@ def mesa_delta_step(S_state, q, k, v, gamma, beta, scale=1.0, out=None, stream=N
     N, Hk, dk = shape = q.shape
     _, H, dv = v.shape
     dev, dtype, vshape, gates = q.device, q.dtype, (N, H, dv), (N, H)
-    out = _new(vshape, dtype, dev, stream) if out is None else out
+    out = _like(v, stream) if out is None else out
     _require_all(dev, (q, "q", dtype, shape), (k, "k", dtype, shape), (v, "v", dtype, vshape),
                  (gamma, "gamma", torch.float32, gates), (beta, "beta", torch.float32, gates),
                  (S_state, "S_state", torch.float32, (N, H, dv, dk)), (out, "out", dtype, vshape))
@@ -542,9 +550,9 @@ def mesa_block_norm(x, y, gate=None, w_post=None, res_scale=None, w_pre=None, ep
     lib = load()
     code = _dtype_code(y)
     N, D = _norm_check(x, y, gate, w_post, res_scale, w_pre)
-    x_out = _new(y.shape, y.dtype, y.device, stream) if x_out is None else x_out
+    x_out = _like(y, stream) if x_out is None else x_out
     if w_pre is not None and h_out is None:
-        h_out = _new(y.shape, y.dtype, y.device, stream)
+        h_out = _like(y, stream)
     _require_all(y.device, (x_out, "x_out", y.dtype, y.shape), (h_out, "h_out", y.dtype, y.shape))
     _check(lib.mesa_block_norm(N, D, code, _at(x), _at(y), _at(gate), _at(w_post), _at(res_scale), _at(w_pre), eps,
                                _at(x_out), _at(h_out), _raw_stream(stream, y.device)), "mesa_block_norm")
@@ -566,15 +574,15 @@ def mesa_block_norm_backward(x, y, dx_out, dh=None, gate=None, w_post=None, res_
     N, D = _norm_check(x, y, gate, w_post, res_scale, w_pre)
     dev = y.device
 
-    def out(t, like, dtype):
-        return _new(like.shape, dtype, dev, stream) if t is None and like is not None else t
+    def out(t, like):
+        return _like(like, stream) if t is None and like is not None else t
 
-    dx, dy, dgate = out(dx, x, y.dtype), out(dy, y, y.dtype), out(dgate, gate, y.dtype)
-    dw_post, dres_scale, dw_pre = (out(t, w, torch.float32) for t, w in (
-        (dw_post, w_post), (dres_scale, res_scale), (dw_pre, w_pre)))
-    _require_all(dev, *[(t, n, y.dtype, y.shape) for t, n in (
-        (dx_out, "dx_out"), (dh, "dh"), (dx, "dx"), (dy, "dy"), (dgate, "dgate"))],
-        *[(t, n, torch.float32, (D,)) for t, n in ((dw_post, "dw_post"), (dres_scale, "dres_scale"), (dw_pre, "dw_pre"))])
+    dx, dy, dgate = out(dx, x), out(dy, y), out(dgate, gate)
+    dw_post, dres_scale, dw_pre = out(dw_post, w_post), out(dres_scale, res_scale), out(dw_pre, w_pre)
+    dtype, shape, f32, weight = y.dtype, y.shape, torch.float32, (D,)
+    _require_all(dev, (dx_out, "dx_out", dtype, shape), (dh, "dh", dtype, shape), (dx, "dx", dtype, shape),
+                 (dy, "dy", dtype, shape), (dgate, "dgate", dtype, shape), (dw_post, "dw_post", f32, weight),
+                 (dres_scale, "dres_scale", f32, weight), (dw_pre, "dw_pre", f32, weight))
     workspace = _workspace(workspace, int(lib.mesa_block_norm_backward_workspace_size(N, D)), dev, stream)
     _check(lib.mesa_block_norm_backward(N, D, code, _at(x), _at(y), _at(gate), _at(w_post), _at(res_scale), _at(w_pre),
                                         eps, _at(dx_out), _at(dh), _at(dx), _at(dy), _at(dgate), _at(dw_post),

@@ -28,10 +28,10 @@ namespace {
 
 // ---- per-chunk preparation --------------------------------------------------------------------
 // shared memory: the operand tile, and once its products are done record | scratch in its place
-// (39 KB: five CTAs on an SM hide each other's substitution) | misc
-constexpr uint32_t PR_REC = 0, PR_SCR = REC_PAD;
+// (36 KB: six CTAs on an SM hide each other's substitution) | misc
+constexpr uint32_t PR_REC = 0, PR_SCR = REC;
 constexpr uint32_t PR_MISC = (PR_SCR + sizeof(Factor) > TILE ? PR_SCR + sizeof(Factor) : TILE);
-static_assert(PR_MISC % 16 == 0, "misc alignment");
+static_assert(PR_MISC % 16 == 0 && PR_SCR % 16 == 0, "alignment");
 struct PrepMisc {
   alignas(16) uint32_t red[8];
   float grow[C], give[C];
@@ -40,6 +40,7 @@ struct PrepMisc {
   uint32_t tmem;
 };
 constexpr uint32_t PR_SMEM = PR_MISC + sizeof(PrepMisc) + 1024;
+static_assert(6 * (PR_SMEM + 1024) <= 228 * 1024, "six CTAs on an SM");
 
 // grid (NC, U), 128 threads.  WITH_BETA: the record's factor is T diag(beta), else T.  bounds [U, NC]
 // (or nullptr): log2 of how much of a state the chunk leaves, at most, the product over its tokens of
@@ -47,7 +48,7 @@ constexpr uint32_t PR_SMEM = PR_MISC + sizeof(PrepMisc) + 1024;
 // to a row of the state, the largest |v| times the sum of beta |k|.  Numbers that are none (or
 // that could end in an overflow) bound nothing: infinity or NaN.
 template <bool WITH_BETA>
-__global__ void __launch_bounds__(128, 5) mesa_rule_prep_kernel(RuleArgs a, uint8_t *records, float2 *bounds) {
+__global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint8_t *records, float2 *bounds) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   PrepMisc *m = reinterpret_cast<PrepMisc *>(sm + PR_MISC);

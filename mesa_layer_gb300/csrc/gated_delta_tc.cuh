@@ -207,7 +207,7 @@ __device__ __forceinline__ void tensor_s2g_3d(const void *map, uint32_t src, int
 
 // ---- the factors of a chunk, by 128 threads ------------------------------------------------------
 struct Factor {
-  __half Ah[C][72];      // A, fp16 (the blocks below the diagonal are used)
+  __half Ah[C - 16][56]; // A's blocks below the diagonal, fp16 (from row 16 on)
   float Ad[C][20];       // its diagonal 16 x 16 blocks: row i, columns of block i / 16
   __half Tb[4][16][24];  // inverses of the diagonal blocks of I + A, and their transposes
   __half Yb[4][16][24];
@@ -268,10 +268,10 @@ __device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk,
     for (int k = 0; k < 2; k++) {
       const float4 o = make_float4(half2_bits(v[8 * k], v[8 * k + 1]), half2_bits(v[8 * k + 2], v[8 * k + 3]),
                                    half2_bits(v[8 * k + 4], v[8 * k + 5]), half2_bits(v[8 * k + 6], v[8 * k + 7]));
-      if (isA)
-        *reinterpret_cast<float4 *>(&s.Ah[i][16 * h + 8 * k]) = o;
-      else
+      if (!isA)
         *reinterpret_cast<float4 *>(P + tile_off(i, 2 * h + k, C)) = o;
+      else if (h < diag)
+        *reinterpret_cast<float4 *>(&s.Ah[i - 16][16 * h + 8 * k]) = o;
     }
     if (isA && h == diag) {  // its part of the diagonal block, in fp32
 #pragma unroll
@@ -284,8 +284,10 @@ __device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk,
     for (int j = 0; j < i; j++) {
       if (s.z[j] == zi) continue;
       if (isA) {
-        s.Ah[i][j] = __float2half_rn(0.0f);
-        if (j >> 4 == i >> 4) s.Ad[i][j & 15] = 0.0f;
+        if (j >> 4 == diag)
+          s.Ad[i][j & 15] = 0.0f;
+        else
+          s.Ah[i - 16][j] = __float2half_rn(0.0f);
       } else {
         *reinterpret_cast<uint16_t *>(P + tc::sw128_offset(i, j, C)) = 0;
       }
@@ -349,8 +351,8 @@ __device__ __forceinline__ void factor_columns(Factor &s, uint8_t *M, int c, int
 #pragma unroll
       for (int k = 0; k < b; k++) {
         if (k < c) continue;
-        mma_16816(z0, y[k], word(&s.Ah[16 * b + g][16 * k + q]), word(&s.Ah[16 * b + g][16 * k + q + 8]));
-        mma_16816(z1, y[k], word(&s.Ah[16 * b + g + 8][16 * k + q]), word(&s.Ah[16 * b + g + 8][16 * k + q + 8]));
+        mma_16816(z0, y[k], word(&s.Ah[16 * b - 16 + g][16 * k + q]), word(&s.Ah[16 * b - 16 + g][16 * k + q + 8]));
+        mma_16816(z1, y[k], word(&s.Ah[16 * b - 8 + g][16 * k + q]), word(&s.Ah[16 * b - 8 + g][16 * k + q + 8]));
       }
       const uint32_t za[4] = {pack(-z0[0], -z0[1]), pack(-z0[2], -z0[3]), pack(-z1[0], -z1[1]), pack(-z1[2], -z1[3])};
       float w0[4] = {}, w1[4] = {};
