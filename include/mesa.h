@@ -283,8 +283,13 @@ int mesa_forward_chunked_noalloc(int B, int H, int T, int dk, int dv, int dtype,
  * dk, dv in {16, 32, 64, 128}, not necessarily equal; T >= 0; B * H <= 65535.  q, k, v, out, S0
  * and S_final 16-byte aligned (MESA_ERR_INVALID_ARG otherwise).
  * workspace: at least mesa_delta_workspace_size() bytes, 256-byte aligned; its first word is the
- * status word read by mesa_forward_status.  Any chunk length gives the same result up to
- * rounding; the library picks its own.
+ * status word read by mesa_forward_status (MESA_ERR_NONFINITE: a non-finite out).  Any chunk
+ * length gives the same result up to rounding; the library picks its own.
+ * Arithmetic: sums, states and gates in fp32.  bf16 with dk = dv = 128 runs on the tensor cores with
+ * fp16 operands scaled by powers of two (each rounded to 2^-12 of its row's largest element, S_final
+ * with them); there the products of a 64-token chunk want |beta| |k|^2 of order one.  Everything
+ * else is a token recurrence in fp32.  Long sequences of few (batch, head) units are cut into
+ * segments that run side by side.
  */
 size_t mesa_delta_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,
@@ -303,7 +308,8 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
  * dgamma, dbeta [B, H, T]: all of dtype -- the gates' gradients come from the same products as
  * the others and carry no more digits.  dS0: NULL or [B, H, dv, dk] fp32, dL/dS0.  The states
  * are recomputed; every sum has a fixed order.  S0 as given to the forward.
- * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward.
+ * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward; on the
+ * tensor cores |beta| < 4 (a larger one can overflow an operand: MESA_ERR_NONFINITE).
  */
 size_t mesa_delta_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,

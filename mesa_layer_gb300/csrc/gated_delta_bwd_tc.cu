@@ -1,20 +1,22 @@
 // gated_delta_bwd_tc.cu -- the gated delta rule's backward on the tensor cores (bf16, dk = dv = 128;
 // the chunk algebra, the records and the operand formats are in gated_delta_tc.cuh).
 //
-// After the records (T without beta) and a pass over the states (mesa_rule_chain_kernel<false>, which
+// After the records (T without beta) and a pass over the states (mesa_rule_chain_kernel<kKeep>, which
 // keeps the state S0 before each chunk and the chunk's u), two kernels:
 //  - mesa_rule_adjoint_kernel, one CTA per unit, walks the chunks backwards with the adjoint A of the
 //    state after the chunk in registers, like the forward's chain (g = dL/do, scale in P and Q):
 //        R' = (c A K^T + g^T P),   du = R' T,   A <- f_last A + g^T (f Q) - (beta f du)^T K;
-//  - mesa_rule_grads_tc_kernel, one CTA per chunk, takes every gradient from S0, A, u, du and the
+//  - mesa_rule_grads_tc_kernel, a resident CTA per SM over all chunks, takes every gradient from S0, A, u, du and the
 //    chunk's rows:
 //        W = g u^T o D, V = beta du u^T o D (strictly lower),
 //        dq = f (g S0) + W K,   dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0),
 //        dv = beta du,          dbeta = du . (v - f S0 k - sum_j D_ij (k_i . k_j) u_j),
 //        dgamma_t: every pair (reader i >= t or the state after, writer j < t or the state before)
 //        that the gate separates, with the decay between them but for gamma_t's own.
-// States, adjoints, u and du go through memory as fp16 operands with one scale a chunk: what
-// bounds the path is that traffic and the two chains' latency.
+// States, adjoints, u and du go through memory as fp16 operands with one scale a chunk (2^-12 of a
+// chunk's largest).  Measured at 8 x 16 x 4096: records 109 us, states 154, adjoint 230 (64 dependent steps of
+// 3.6 us), gradients 490 (1.7 GB of operands, rows and gradients: 3.5 TB/s); each bound by the latency of
+// its dependent steps on one CTA per SM, the last also by shared memory (its products' operands).
 #include "gated_delta_tc.cuh"
 
 namespace mesa {
@@ -479,7 +481,7 @@ __device__ __forceinline__ void l2_prefetch(const void *p) { asm volatile("prefe
 // tensor memory's lanes take a quarter of the columns each.  A chunk is a row of short steps that wait
 // for one another, so the next chunk's rows are on their way (in registers) from the middle of this one's, its states
 // and u from where this one's have been read.  (One CTA per chunk, 256 threads, nothing on its way: 875 us
-// at 8 x 16 x 4096 against the time below.)
+// at 8 x 16 x 4096; so, 490.)
 __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     mesa_rule_grads_tc_kernel(RuleArgs a, int NC, int chunks, const uint8_t *records, RuleOperands so, RuleOperands ao,
                               float *dqp, float *dkp, const __grid_constant__ CUtensorMap mapDq,

@@ -3,7 +3,7 @@
 //
 // Two kernels.  mesa_rule_prep_kernel, one CTA per chunk: K K^T and Q K^T in one product, decays,
 // masks and the triangular inverse, written as a record.  mesa_rule_chain_kernel, one CTA per
-// unit, walks the unit's chunks with the state in registers (thread r of the chain holds row r,
+// unit (or segment of a unit), walks the unit's chunks with the state in registers (thread r of the chain holds row r,
 // 128 values) and everything laid out by state row, so that a chunk's chain of dependent
 // products never crosses threads:
 //     D1 = S0 K^T          -> R = V^T - f D1      (row r of the accumulator is thread r's)
@@ -13,11 +13,14 @@
 // O = f (S0 Q^T) + U P^T shares the first product (K and Q rows are one operand tile).  The chain
 // bounds the kernel, so all else runs beside it, in warp groups of their own:
 //     chain    the three epilogues above;
-//     helper   transposes V one chunk ahead, writes the readout of the chunk before;
-//     convert  K and Q as fp16 operands, up to three chunks ahead.
+//     helper   writes the readout (and with the transposition, too, it held up the chain: 188 us);
+//     convert  V transposed one chunk ahead, K and Q as fp16 operands, up to three chunks ahead.
+// Measured at 8 x 16 x 4096 (8192 chunks): preparation 110 us (400 MB of rows and records: 3.7 TB/s; the
+// substitution's latency and instruction fetch), chain 179 us (64 dependent steps of 2.8 us; issue slots
+// 37 %, tensor pipe 19 % busy: the latency of four products and three epilogues a step, 128 of 152 SMs).
 // (With the preparation in the same kernel, as a fourth group, nothing but the inputs and the output
 // went to memory, but the groups' code no longer fitted the instruction caches and every
-// group slowed down: 268 us at 8 x 16 x 4096 against the two kernels' time below.)
+// group slowed down: at best 268 us, at 8 x 16 x 4096, in some runs 300.)
 #include "gated_delta_tc.cuh"
 
 namespace mesa {
@@ -856,7 +859,8 @@ int launch_chain(const RuleArgs &a, const uint8_t *records, const RuleOperands &
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
-// Segments of a unit's NC chunks: as many CTAs as a GB300 has SMs (152), at least six chunks each.  Where
+// Segments of a unit's NC chunks: as many CTAs as a GB300 has SMs (152), at least six chunks each (1 x 16 x
+// 65536: nine segments, 645 us against 2850 for one; 72 of them the segments' starts, 14 the join).  Where
 // gates hardly decay the two starting passes take as long as two segments, so n segments take 3/n of
 // the time of one pass, and fewer than five are not worth it.
 int segments(int U, int NC) {
