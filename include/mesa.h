@@ -277,7 +277,8 @@ int mesa_forward_chunked_noalloc(int B, int H, int T, int dk, int dv, int dtype,
  * and k (mesa_qk_preprocess); beta in [0, 2] with unit keys keeps the recurrence bounded.
  *   q, k [B, Hk, T, dk] dtype; v, out [B, H, T, dv] dtype; gamma, beta [B, H, T] fp32.
  *   Hk divides H: value head h reads query / key head h / (H / Hk).
- *   S0, S_final: NULL or [B, H, dv, dk] fp32 (each may be given without the other).
+ *   S0, S_final: NULL or [B, H, dv, dk] fp32 (each may be given without the other; they may be the
+ *   same memory).
  *   gamma_t = 0 forgets everything before token t (a packed document's first token); beta_t = 0
  *   leaves a token unwritten (padding).  gamma below e^-80 counts as 0 on the tensor-core path.
  * dk, dv in {16, 32, 64, 128}, not necessarily equal; T >= 0; B * H <= 65535.  q, k, v, out, S0
@@ -306,8 +307,8 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
  *     dbeta_t = du_t . e_t,              dgamma_t = <N_t, S_{t-1}>   (also where gamma_t = 0).
  * dq, dk_out [B, Hk, T, dk] (summed over the value heads of a key head), dv_out [B, H, T, dv],
  * dgamma, dbeta [B, H, T]: all of dtype -- the gates' gradients come from the same products as
- * the others and carry no more digits.  dS0: NULL or [B, H, dv, dk] fp32, dL/dS0.  The states
- * are recomputed; every sum has a fixed order.  S0 as given to the forward.
+ * the others and carry no more digits.  dS0: NULL or [B, H, dv, dk] fp32, dL/dS0
+ * (it may be dS_final's memory).  The states are recomputed; every sum has a fixed order.  S0 as given to the forward.
  * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward; on the
  * tensor cores |beta| < 4 (a larger one can overflow an operand: MESA_ERR_NONFINITE).
  */

@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(ROWS * lanes_per_row(DK)) mesa_rule_scan_kerne
 
   u64 s[2 * NG];
   {
-    const bool first = seg == (ADJ ? sg.n - 1 : 0);  // (from here the sweep starts)
-    const float *init = first ? (ADJ ? a.dS_final : a.S0) : SEG ? nullptr : ADJ ? sg.A : sg.S;
-    const float *src = init ? init + (((size_t)u * (first ? 1 : sg.n) + (first ? 0 : seg)) * a.dv + r0 + r) * DK : nullptr;
+    const bool first = seg == (ADJ ? sg.n - 1 : 0), kept = !SEG && sg.n > 1;  // (first: the sweep starts here)
+    const float *init = kept ? (ADJ ? sg.A : sg.S) : first ? (ADJ ? a.dS_final : a.S0) : nullptr;
+    const float *src = init ? init + ((kept ? (size_t)u * sg.n + seg : (size_t)u) * a.dv + r0 + r) * DK : nullptr;
 #pragma unroll
     for (int g = 0; g < NG; g++) {
       const float4 x = (src && rin) ? *reinterpret_cast<const float4 *>(src + 4 * (j + LPR * g)) : make_float4(0, 0, 0, 0);
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(ROWS * lanes_per_row(DK)) mesa_rule_scan_kerne
   }
 }
 
-// The state before each segment: start[y + 1] = start[y] M[y] + local[y] (the first: local[0]); downwards for
-// the adjoint.  A chain of n short products, so what counts is a step's latency: eight rows by a CTA of
+// The state before each segment: start[y + 1] = start[y] M[y] + local[y] (the first: local[0], and start[0] a
+// copy of `given`: the final state may be written over it); downwards for the adjoint.  A chain of n short products, so what counts is a step's latency: eight rows by a CTA of
 // 256 threads, a thread two rows, DK / 16 columns and a quarter of the sum (so that a matrix is read
 // from shared memory four times in a step, not eight, by eight warps), the matrices and local states of the
 // next steps on their way by cp.async.  (One row and the whole sum a thread: 1.0 us a step at DK = 64.)
@@ -293,7 +293,7 @@ struct JoinBuffers {
   static constexpr int n = DK == 128 ? 3 : 4, bytes = n * (DK * DK + JROWS * DK) * (int)sizeof(float);
 };
 template <int DK>
-__global__ void __launch_bounds__(256) mesa_rule_scan_join_kernel(RuleScanSegments sg, int dv, bool adjoint) {
+__global__ void __launch_bounds__(256) mesa_rule_scan_join_kernel(RuleScanSegments sg, const float *given, int dv, bool adjoint) {
   constexpr int CPT = DK / 16, MAT = DK * DK, BUF = MAT + JROWS * DK, NB = JoinBuffers<DK>::n, KP = DK / 4;
   extern __shared__ __align__(16) float jm[];  // NB buffers: a matrix, the local rows
   __shared__ __align__(16) float rows[JROWS][DK], part[4][JROWS][DK];
@@ -317,6 +317,8 @@ __global__ void __launch_bounds__(256) mesa_rule_scan_join_kernel(RuleScanSegmen
   };
 #pragma unroll
   for (int i = 0; i < NB - 1; i++) fetch(i);
+  for (int e = tid; e < JROWS * DK; e += 256)
+    start[(at(0) * dv + row0) * DK + e] = given ? given[((size_t)u * dv + row0) * DK + e] : 0.0f;
   for (int i = 0; i + 1 < sg.n; i++) {
     cp_wait<NB - 2>();
     __syncthreads();  // the rows and this step's buffer are there, the last step's has been read
@@ -654,7 +656,7 @@ int launch_scan_join(const RuleArgs &a, const RuleScanSegments &sg, bool adjoint
   auto kfn = mesa_rule_scan_join_kernel<DK>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
   timing_mark_begin(K_RULE_JOIN, st);
-  kfn<<<dim3(a.dv / JROWS, a.units()), 256, smem, st>>>(sg, a.dv, adjoint);  // (dv: a multiple of 16)
+  kfn<<<dim3(a.dv / JROWS, a.units()), 256, smem, st>>>(sg, adjoint ? a.dS_final : a.S0, a.dv, adjoint);  // (dv: a multiple of 16)
   timing_mark_end(K_RULE_JOIN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

@@ -257,7 +257,9 @@ __global__ void __launch_bounds__(384, 1)
   const bool identity = SEG && blockIdx.z == 1, tail = SEG && gridDim.z == 1;
   // this CTA's chunks: NC of them from c0 on (the loops count them from 0)
   int c0 = sg.n > 1 ? seg * sg.per : 0, NC = sg.n > 1 ? min(NCT - c0, sg.per) : NCT;
-  const float *start = seg == 0 ? a.S0 : sg.S + ((size_t)u * sg.n + seg) * D * D;  // (nullptr: zero)
+  const float *start = !SEG && sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * D * D  // (nullptr: zero)
+                       : a.S0         ? a.S0 + (size_t)u * D * D
+                                      : nullptr;
   if constexpr (SEG) {
     int *whole = sg.whole + (size_t)u * sg.n + seg;
     if (seg > 0 || tail) start = nullptr;
@@ -351,8 +353,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
     u64 S[D / 2];
     {
-      const size_t at = SEG || seg == 0 ? ((size_t)u * D + r) * D : (size_t)r * D;
-      const float4 *src = start ? reinterpret_cast<const float4 *>(start + at) : nullptr;
+      const float4 *src = start ? reinterpret_cast<const float4 *>(start + (size_t)r * D) : nullptr;
 #pragma unroll
       for (int g = 0; g < D / 4; g++) {
         float4 x = src ? src[g] : make_float4(0, 0, 0, 0);
@@ -809,12 +810,17 @@ __global__ void __launch_bounds__(384, 1)
   if (warp == 0) tc::tmem_free(tbase, 512);
 }
 
-// The state before each segment from the segments' own: S_{y+1} = S_y Tr_y + loc_y (S_1 = loc_0), sixteen
-// rows by a CTA of 256 threads; grid (8, U).
-__global__ void __launch_bounds__(256) mesa_rule_join_kernel(RuleSegments sg) {
+// The state before each segment from the segments' own: S_{y+1} = S_y Tr_y + loc_y (S_1 = loc_0; S_0 is a
+// copy: the last segment may write its final state over the caller's), sixteen rows by a CTA of 256
+// threads; grid (8, U).
+__global__ void __launch_bounds__(256) mesa_rule_join_kernel(RuleSegments sg, const float *S0) {
   __shared__ float rows[16][D + 4];
   const int u = blockIdx.y, row0 = 16 * blockIdx.x, tid = threadIdx.x;
   const int r = tid >> 4, c0 = (tid & 15) * 8;  // row r, columns c0 ..
+  for (int i = 0; i < 8; i++) {
+    const size_t at = (size_t)(row0 + r) * D + c0 + i;
+    sg.S[(size_t)u * sg.n * D * D + at] = S0 ? S0[(size_t)u * D * D + at] : 0.0f;
+  }
   for (int y = 0; y + 1 < sg.n; y++) {
     const size_t at = (size_t)u * sg.n + y;
     const float *loc = sg.loc + at * D * D + (size_t)(row0 + r) * D + c0;
@@ -914,7 +920,7 @@ int launch_segments(const RuleArgs &a, const uint8_t *records, const RuleSegment
                                                        st) != 0)
       return -1;
   timing_mark_begin(K_RULE_JOIN, st);
-  mesa_rule_join_kernel<<<dim3(8, a.units()), 256, 0, st>>>(sg);
+  mesa_rule_join_kernel<<<dim3(8, a.units()), 256, 0, st>>>(sg, a.S0);
   timing_mark_end(K_RULE_JOIN, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }

@@ -408,3 +408,67 @@ def test_nonfinite_values_last_through_long_sequences(what):
     assert torch.isfinite(SF[0, 0]).all() and torch.isfinite(out[0, 0]).all()
     assert not torch.isfinite(SF[0, 1, 5]).any()
     assert not torch.isfinite(out[0, 1, -1, 5])
+
+
+@pytest.mark.parametrize("dtype,d,T", [("f32", 64, 100), ("f32", 64, 1500), ("bf16", 128, 100), ("bf16", 128, 2500)])
+def test_final_states_may_replace_the_first(dtype, d, T):
+    import torch
+
+    from mesa_layer_gb300 import binding
+    s = ref.rule_inputs(41, dtype, 1, 2, 1, T, d, d, "open", True)
+    t = upload(s, dtype)
+    args = [t[n] for n in ("q", "k", "v", "gamma", "beta")]
+    S, A = torch.empty_like(t["S0"]), torch.empty_like(t["S0"])
+    out = binding.mesa_delta_forward_chunked(*args, S0=t["S0"], S_final=S)
+    grads = binding.mesa_delta_backward_chunked(*args, t["dout"], S0=t["S0"], dS_final=t["dS_final"], dS0=A)
+    S2, A2 = t["S0"].clone(), t["dS_final"].clone()
+    assert torch.equal(binding.mesa_delta_forward_chunked(*args, S0=S2, S_final=S2), out) and torch.equal(S2, S)
+    again = binding.mesa_delta_backward_chunked(*args, t["dout"], S0=t["S0"], dS_final=A2, dS0=A2)
+    assert torch.equal(A2, A) and all(torch.equal(x, y) for x, y in zip(again, grads))
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 128)])
+def test_long_sequences_write_inside_their_buffers_and_repeat(dtype, d):
+    import torch
+
+    from mesa_layer_gb300 import binding
+    from test_gpu_canary import Guarded, workspace
+    T = 2345
+    s = ref.rule_inputs(42, dtype, 1, 2, 2, T, d, d, "packed", True)
+    t = upload(s, dtype)
+    td = t["q"].dtype
+    args = [t[n] for n in ("q", "k", "v", "gamma", "beta")]
+    wf = workspace(binding.mesa_delta_workspace_size(1, 2, 2, T, d, d, td))
+    wb = workspace(binding.mesa_delta_backward_workspace_size(1, 2, 2, T, d, d, td))
+    runs = []
+    for _ in range(2):
+        out, SF, dS0 = Guarded((1, 2, T, d), td), Guarded((1, 2, d, d), torch.float32), Guarded((1, 2, d, d), torch.float32)
+        g = [Guarded((1, 2, T, d), td) for _ in range(3)] + [Guarded((1, 2, T), td) for _ in range(2)]
+        binding.mesa_delta_forward_chunked(*args, out=out.t, S0=t["S0"], S_final=SF.t, workspace=wf.t)
+        binding.mesa_delta_backward_chunked(*args, t["dout"], 1.0, t["S0"], t["dS_final"], *(x.t for x in g), dS0=dS0.t,
+                                            workspace=wb.t)
+        assert all(x.intact() for x in (out, SF, dS0, wf, wb, *g))
+        runs.append([x.t for x in (out, SF, dS0, *g)])
+    assert all(torch.equal(x, y) for x, y in zip(*runs))
+
+
+def test_wait_give_up_in_a_long_sequence_reports_timeout():
+    import torch
+
+    from mesa_layer_gb300 import binding
+    s = ref.rule_inputs(43, "bf16", 1, 1, 1, 2100, 128, 128, "open")
+    t = upload(s, "bf16")
+    args = [t[n] for n in ("q", "k", "v", "gamma", "beta")]
+    ws = torch.empty(binding.mesa_delta_workspace_size(1, 1, 1, 2100, 128, 128, torch.bfloat16), dtype=torch.uint8,
+                     device="cuda")
+    want = binding.mesa_delta_forward_chunked(*args, workspace=ws)
+    assert binding.mesa_forward_status(ws) == 0
+    binding.mesa_debug_set_wait_limit(0)
+    try:
+        binding.mesa_delta_forward_chunked(*args, workspace=ws)
+        code, bits = binding.mesa_forward_status_code(ws)
+    finally:
+        binding.mesa_debug_set_wait_limit(-1)
+    assert code == binding.MESA_ERR_TIMEOUT and bits & 1 and not bits & 4
+    assert torch.equal(binding.mesa_delta_forward_chunked(*args, workspace=ws), want)
+    assert binding.mesa_forward_status(ws) == 0
