@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
 // shared memory: [g; du] | u | [Q; K] | S0 | A | products' operand | X | misc.  (u as rows 64 .. 127 of a
 // 128-row operand: its descriptor starts 8 KB before it.)  dq and dk leave through the products' operand.
 constexpr uint32_t GR_A1 = 0, GR_U = TILE, GR_QK = GR_U + ROWS64, GR_S = GR_QK + TILE, GR_DS = GR_S + TILE, GR_A5 = GR_DS + TILE;
-constexpr int X_LD = 65;
+constexpr int X_LD = 72;  // (rows of a fragment in different banks)
 constexpr uint32_t GR_X = GR_A5 + TILE, GR_MISC = GR_X + ((C * X_LD * 4 + 127) & ~127);
 constexpr int GR_WARPS = 16, GR_SEGS = 8;
 struct GradsMisc {
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       s = warp_sum(s);
       if (lane == 0) m->cross[warp] = s * iS * iA;
     }
-    const float mul = upper ? a.scale * ig * iu : idu * iu, be = upper ? 1.0f : m->beta[i];
+    const float mul = upper ? a.scale * ig * iu : idu * iu;
     // the operand's units: W alpha, V alpha sq / sk, both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
     // 128 products, beta < 4, V + V^T)
     float ialpha;
@@ -695,64 +695,81 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     stop = __syncthreads_or(!got_a);
     if (stop) break;
     {
-      float x[16], y[16];
-      tc::tmem_ld16(tl + T_G3 + 16 * part, x);
-      tc::tmem_ld16(tl + T_G4 + 16 * part, y);
-      const float li = m->l[i];
-      const u64 li2 = pack2(li, li), mul2x = pack2(mul, mul);
-      const float qk = (upper ? iq : ik) * ik;  // real q . k, k . k
-      const float op = upper ? alpha : -alpha * vq * be;
-      const u64 qk2 = pack2(qk, qk), op2 = pack2(op, op);
-      const int keep = (upper ? i : i - 1) - 16 * part;  // the last column of the operand
-      float dec[16], db = 0.0f;
+      // in fragments of 8 x 8: of the rows 16 h + 8 e + lane / 4 of the warp's 32 (mod 64: i0 ..), columns 16 part +
+      // 8 b + 2 (lane % 4) and the next
+      const int i0 = 32 * (quad & 1), g = lane >> 2, q = 2 * (lane & 3), col = 16 * part + q;
+      u64 x[2][4], y[2][4];  // [h][2 b + e]
 #pragma unroll
-      for (int k = 0; k < 16; k += 4) {
-        const ulonglong2 lj = *reinterpret_cast<const ulonglong2 *>(&m->l[16 * part + k]);
-        unpack2(sub2(li2, lj.x), dec[k], dec[k + 1]);
-        unpack2(sub2(li2, lj.y), dec[k + 2], dec[k + 3]);
+      for (int h = 0; h < 2; h++) {
+        tmem_ld_frag16(tl + ((uint32_t)(16 * h) << 16) + T_G3 + 16 * part, x[h]);
+        tmem_ld_frag16(tl + ((uint32_t)(16 * h) << 16) + T_G4 + 16 * part, y[h]);
       }
-#pragma unroll
-      for (int k = 0; k < 16; k++) dec[k] = k <= keep ? ex2(dec[k]) : 0.0f;
-      if (m->z[C - 1] != 0) {  // a closed gate in the chunk
-        const int zi = m->z[i];
-#pragma unroll
-        for (int k = 0; k < 16; k++)
-          if (m->z[16 * part + k] != zi) dec[k] = 0.0f;
-      }
+      const u64 lj[2] = {*reinterpret_cast<const u64 *>(&m->l[col]), *reinterpret_cast<const u64 *>(&m->l[col + 8])};
+      const float qk = (upper ? iq : ik) * ik, op0 = upper ? alpha : -alpha * vq;  // real q . k, k . k
+      const u64 mul2x = pack2(mul, mul), qk2 = pack2(qk, qk);
+      const bool closed = m->z[C - 1] != 0;  // a gate in the chunk
+      uint32_t p[2][4];  // the operand's fragments
+      float db[2][2];
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < 16; k += 2) {
-        const u64 w = mul2(pack2(x[k], x[k + 1]), mul2x);
-        unpack2(mul2(w, mul2(pack2(y[k], y[k + 1]), qk2)), y[k], y[k + 1]);  // X's part, without the decay
-        unpack2(mul2(mul2(w, op2), pack2(dec[k], dec[k + 1])), x[k], x[k + 1]);  // the operand
-      }
-      // (columns without a decay are none of the operand's, whatever their products are)
+      for (int h = 0; h < 2; h++) {
 #pragma unroll
-      for (int k = 0; k < 16; k++) x[k] = k <= keep ? x[k] : 0.0f;
-      // the first rows' and the later columns' addresses: row C + j of the operand, column i or C + i
-      const uint32_t tr = (C + 16 * part) * 128 + (upper ? 0 : 128 * 128) + ((i & 7) << 1), ib = (i >> 3) << 4;
-      auto at_tr = [&](int k) { return reinterpret_cast<__half *>(sm + GR_A5 + tr + (ib ^ ((k & 7) << 4)) + k * 128); };
-      // W: row i of dq's, K columns;  -V: row i of dk's, K columns (zero above the diagonal)
+        for (int e = 0; e < 2; e++) {
+          const int i = i0 + 16 * h + 8 * e + g, keep = upper ? i : i - 1;  // the last column of the operand
+          const float li = m->l[i], op = upper ? op0 : op0 * m->beta[i];
+          const u64 li2 = pack2(li, li), op2 = pack2(op, op);
+          float sum = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 2; k++) {
-        const float4 o = make_float4(half2_bits(x[8 * k], x[8 * k + 1]), half2_bits(x[8 * k + 2], x[8 * k + 3]),
-                                     half2_bits(x[8 * k + 4], x[8 * k + 5]), half2_bits(x[8 * k + 6], x[8 * k + 7]));
-        *reinterpret_cast<float4 *>(sm + GR_A5 + tile_off(row, 8 + 2 * part + k, 128)) = o;
+          for (int b = 0; b < 2; b++) {
+            const int j = col + 8 * b;
+            float d0, d1, y0, y1, x0, x1;
+            unpack2(sub2(li2, lj[b]), d0, d1);
+            d0 = j <= keep ? ex2(d0) : 0.0f;
+            d1 = j + 1 <= keep ? ex2(d1) : 0.0f;
+            if (closed) {
+              if (m->z[j] != m->z[i]) d0 = 0.0f;
+              if (m->z[j + 1] != m->z[i]) d1 = 0.0f;
+            }
+            const u64 w = mul2(x[h][2 * b + e], mul2x);
+            y[h][2 * b + e] = mul2(w, mul2(y[h][2 * b + e], qk2));  // X's part, without the decay
+            unpack2(y[h][2 * b + e], y0, y1);
+            unpack2(mul2(mul2(w, op2), pack2(d0, d1)), x0, x1);
+            // (columns without a decay are none of the operand's, whatever their products are)
+            p[h][2 * b + e] = __float_as_uint(half2_bits(j <= keep ? x0 : 0.0f, j + 1 <= keep ? x1 : 0.0f));
+            if (j <= keep) sum = fmaf(d0, y0, sum);
+            if (j + 1 <= keep) sum = fmaf(d1, y1, sum);
+          }
+          db[h][e] = sum;
+        }
       }
+      const int l8 = lane & 7, lb = lane >> 3;  // this lane's row and block of a matrix store
       if (upper) {
 #pragma unroll
-        for (int k = 0; k < 16; k++) *at_tr(k) = __float2half_rn(x[k]);  // W^T
+        for (int h = 0; h < 2; h++) {
+          // W: row i of dq's, K columns; W^T: row j of dk's, Q columns
+          stmatrix_x4(tc::smem_u32(sm + GR_A5 + tile_off(i0 + 16 * h + 8 * (lb & 1) + l8, 8 + 2 * part + (lb >> 1), 128)),
+                      p[h][0], p[h][1], p[h][2], p[h][3]);
+          stmatrix_x4_trans(tc::smem_u32(sm + GR_A5 + tile_off(C + 16 * part + 8 * (lb >> 1) + l8, (i0 >> 3) + 2 * h + (lb & 1), 128)),
+                            p[h][0], p[h][1], p[h][2], p[h][3]);
 #pragma unroll
-        for (int k = 0; k < 16; k++)
-          if (k < 15 || part < 3) X[i * X_LD + 16 * part + k + 1] = y[k];
+          for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int b = 0; b < 2; b++)
+              *reinterpret_cast<u64 *>(&X[(i0 + 16 * h + 8 * e + g) * X_LD + col + 8 * b]) = y[h][2 * b + e];
+        }
       } else {
-        group_or(1, 16 * GR_WARPS, false);  // (their zeros are in place)
+        // -(V + V^T), block by block: a diagonal one is the sum of its two triangles (disjoint), one below is
+        // written twice, one above by its mirror image
 #pragma unroll
-        for (int k = 0; k < 16; k++)
-          if (k <= keep) *at_tr(k) = __float2half_rn(x[k]);  // -V^T
+        for (int h = 0; h < 2; h++)
 #pragma unroll
-        for (int k = 0; k < 16; k++)
-          if (k <= keep) db = fmaf(dec[k], y[k], db);  // du_i against sum_j D_ij (k_i . k_j) u_j
+          for (int t = 0; t < 4; t++) {
+            const int bi = (i0 >> 3) + 2 * h + (t & 1), bj = 2 * part + (t >> 1);
+            if (bj > bi) continue;
+            const uint32_t f = bj == bi ? p[h][t] | transposed(p[h][t]) : p[h][t];
+            stmatrix_x1(tc::smem_u32(sm + GR_A5 + tile_off(C + 8 * bi + l8, 8 + bj, 128)), f);
+            if (bj < bi) stmatrix_x1_trans(tc::smem_u32(sm + GR_A5 + tile_off(C + 8 * bj + l8, 8 + bi, 128)), f);
+          }
       }
       tc::fence_smem_to_async();
       tc::fence_before_sync();
@@ -768,11 +785,22 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       __syncwarp();
       if (!upper) {
 #pragma unroll
-        for (int k = 0; k < 16; k++) {
-          float *x1 = &X[i * X_LD + 16 * part + k + 1];
-          if (k < 15 || part < 3) *x1 = fmaf(-be, y[k], *x1);
-        }
-        m->dbeta[part][i] = db;
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const int i = i0 + 16 * h + 8 * e + g;
+            const u64 nb = pack2(-m->beta[i], -m->beta[i]);
+#pragma unroll
+            for (int b = 0; b < 2; b++) {
+              u64 *x1 = reinterpret_cast<u64 *>(&X[i * X_LD + col + 8 * b]);
+              *x1 = fma2(nb, y[h][2 * b + e], *x1);
+            }
+            // du_i against sum_j D_ij (k_i . k_j) u_j
+            float sum = db[h][e];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (q == 0) m->dbeta[part][i] = sum;
+          }
       }
     }
     const bool got_b = tc::mbar_wait(bb, ph, a.wait_limit);
@@ -811,15 +839,15 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     __syncthreads();
     if (tid < C) {
       const float kS = (m->xin[0][1][tid] + m->xin[1][1][tid]) + (m->xin[2][1][tid] + m->xin[3][1][tid]);
-      X[tid * X_LD] = (m->xin[0][0][tid] + m->xin[1][0][tid]) + (m->xin[2][0][tid] + m->xin[3][0][tid]) - m->beta[tid] * kS;
+      X[tid * X_LD + C - 1] = (m->xin[0][0][tid] + m->xin[1][0][tid]) + (m->xin[2][0][tid] + m->xin[3][0][tid]) - m->beta[tid] * kS;
       m->duv[tid] += m->nf[tid] * kS;
     }
     __syncthreads();
-    // columns of X (column 0: the state before the chunk; column j + 1: token j as the writer), upwards from the
+    // columns of X (column j: token j as the writer; the last: the state before the chunk), upwards from the
     // last token: Z_t = X_t + gamma_{t+1} Z_{t+1}, times the decay from the writer to t - 1, summed over the
     // writers before t.  Eight tokens a thread, joined over the segments above.
     {
-      const int seg = warp >> 1, col = 32 * (warp & 1) + lane, t8 = 8 * seg, j = col - 1;
+      const int seg = warp >> 1, col = 32 * (warp & 1) + lane, t8 = 8 * seg, j = col == C - 1 ? -1 : col;
       float Z[8];
 #pragma unroll
       for (int k = 0; k < 8; k++) Z[k] = X[(t8 + k) * X_LD + col];
@@ -828,7 +856,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       m->head[seg][col] = Z[0];
       __syncthreads();
       float in;  // Z of the token above the segment
-      if (col == 0) {
+      if (j < 0) {
         in = 0.0f;
 #pragma unroll
         for (int w = 0; w < GR_WARPS; w++) in += m->cross[w];

@@ -198,6 +198,31 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                "r"(d)
                : "memory");
 }
+// The same of 16 columns, pairs together: v[2 j + e] is lane T / 4 + 8 e, columns 8 j + 2 (T % 4) and the next.
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, u64 (&v)[4]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] = (u64)r[2 * i] | (u64)r[2 * i + 1] << 32;
+}
+// 8 x 8 blocks of 16-bit fragments to shared memory (lane l % 8: row of block l / 8), one of them also transposed.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_x1(uint32_t addr, uint32_t a) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x1.shared.b16 [%0], {%1};\n" ::"r"(addr), "r"(a) : "memory");
+}
+__device__ __forceinline__ void stmatrix_x1_trans(uint32_t addr, uint32_t a) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x1.trans.shared.b16 [%0], {%1};\n" ::"r"(addr), "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {  // an 8 x 8 block of fragments
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(a));
+  return d;
+}
 // Tiled store of a box of a 3-D tensor map; tokens past the end are not written.
 __device__ __forceinline__ void tensor_s2g_3d(const void *map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(map), "r"(src),
