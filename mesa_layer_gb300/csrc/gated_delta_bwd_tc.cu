@@ -498,19 +498,28 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
   // what is read ahead
   uint4 q4[2], k4[2], g4[2], v4[2];
   float tok;
-  auto fetch_rows = [&](int at) {
+  auto fetch_qk = [&](int at) {
     const int u = at / NC, t0 = (at - u * NC) * C, n = min(C, a.T - t0);
-    const size_t tok0 = (size_t)u * a.T + t0, row0 = (size_t)a.qk_unit(u) * a.T + t0;
+    const size_t first = ((size_t)a.qk_unit(u) * a.T + t0 + r0) * D + 8 * c8;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      q4[i] = k4[i] = make_uint4(0, 0, 0, 0);
+      if (r0 + 32 * i < n) {
+        q4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + first + 32 * i * D);
+        k4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + first + 32 * i * D);
+      }
+    }
+  };
+  auto fetch_gv = [&](int at) {
+    const int u = at / NC, t0 = (at - u * NC) * C, n = min(C, a.T - t0);
+    const size_t tok0 = (size_t)u * a.T + t0, first = (tok0 + r0) * D + 8 * c8;
     const uint8_t *rec = records + (size_t)at * REC;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const int r = r0 + 32 * i;
-      q4[i] = k4[i] = g4[i] = v4[i] = make_uint4(0, 0, 0, 0);
-      if (r < n) {
-        q4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.q + (row0 + r) * D + 8 * c8);
-        k4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.k + (row0 + r) * D + 8 * c8);
-        g4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.dout + (tok0 + r) * D + 8 * c8);
-        v4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + (tok0 + r) * D + 8 * c8);
+      g4[i] = v4[i] = make_uint4(0, 0, 0, 0);
+      if (r0 + 32 * i < n) {
+        g4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.dout + first + 32 * i * D);
+        v4[i] = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + first + 32 * i * D);
       }
     }
     const int t = tid & (C - 1), which = tid >> 6;  // a token's numbers, one kind to two warps; the chunk's
@@ -538,7 +547,8 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     for (uint32_t b : {bl, ba, bb, bc, tc::smem_u32(&m->drain)}) tc::mbar_init(b, 1);
     fetch_operands(at);
   }
-  fetch_rows(at);
+  fetch_qk(at);
+  fetch_gv(at);
   int fetched = 1;  // chunks' operands asked for
   tc::fence_before_sync();
   __syncthreads();
@@ -810,6 +820,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     if (next < chunks) {  // the states, u and du have been read
       if (tid == 32) fetch_operands(next);
       fetched++;
+      fetch_qk(next);
     }
     {  // rows against q_i or k_i: what the gates and betas need of the state products; columns 32 part ..
       float d1 = 0.0f, d2 = 0.0f;
@@ -903,7 +914,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       st((__nv_bfloat16 *)a.dbeta, tok0 + tid,
          m->duv[tid] - ((m->dbeta[0][tid] + m->dbeta[1][tid]) + (m->dbeta[2][tid] + m->dbeta[3][tid])));
     }
-    if (next < chunks) fetch_rows(next);
+    if (next < chunks) fetch_gv(next);
     // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 32 part ..
     const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;
     const float f2 = m->c[i] * iu * iA, f5 = ialpha * (upper ? ik : iq);
