@@ -700,6 +700,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     const float vq = sk_sq.y * ik;  // sq / sk
     const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * iu * 33554432.0f, 8.0f * idu * iu * vq * 137438953472.0f),
                                     kTopRow, ialpha);
+    if (next < chunks) fetch_qk(next);
     const bool got_a = tc::mbar_wait(ba, ph, a.wait_limit);
     tc::fence_after_sync();
     stop = __syncthreads_or(!got_a);
@@ -813,6 +814,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
           }
       }
     }
+    if (next < chunks) fetch_gv(next);
     const bool got_b = tc::mbar_wait(bb, ph, a.wait_limit);
     tc::fence_after_sync();
     stop = __syncthreads_or(!got_b);
@@ -820,7 +822,6 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     if (next < chunks) {  // the states, u and du have been read
       if (tid == 32) fetch_operands(next);
       fetched++;
-      fetch_qk(next);
     }
     {  // rows against q_i or k_i: what the gates and betas need of the state products; columns 32 part ..
       float d1 = 0.0f, d2 = 0.0f;
@@ -914,7 +915,6 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       st((__nv_bfloat16 *)a.dbeta, tok0 + tid,
          m->duv[tid] - ((m->dbeta[0][tid] + m->dbeta[1][tid]) + (m->dbeta[2][tid] + m->dbeta[3][tid])));
     }
-    if (next < chunks) fetch_gv(next);
     // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 32 part ..
     const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;
     const float f2 = m->c[i] * iu * iA, f5 = ialpha * (upper ? ik : iq);
