@@ -216,7 +216,7 @@ const char *mesa_kernel_name(int kind) {
     case mesa::K_RULE_PREP: return "mesa_rule_prep_kernel";
     case mesa::K_RULE_CHAIN: return "mesa_rule_chain_kernel";
     case mesa::K_RULE_SEGMENT: return "mesa_rule_chain_kernel<segments>";
-    case mesa::K_RULE_JOIN: return "mesa_rule_join_kernel|mesa_rule_scan_join_kernel";
+    case mesa::K_RULE_JOIN: return "mesa_rule_join_kernel|mesa_rule_join_adjoint_kernel|mesa_rule_scan_join_kernel";
     case mesa::K_RULE_ADJOINT: return "mesa_rule_adjoint_kernel";
     case mesa::K_NORM_COLS: return "mesa_block_norm_cols_kernel";
   }

@@ -57,7 +57,7 @@ constexpr int kTcParts = 10;
 size_t backward_tc_parts(int B, int H, int Hk, int T, size_t *off) {
   const size_t U = (size_t)B * H, n = U * (((size_t)T + 63) / 64);
   const size_t part = Hk != H ? U * T * 128 * sizeof(float) : 0;
-  const size_t sizes[kTcParts + 1] = {mesa::rule_tc_workspace(B * H, T), n * 32768, n * 32768, n * 16384, n * 16384,
+  const size_t sizes[kTcParts + 1] = {mesa::rule_tc_workspace(B * H, T, true), n * 32768, n * 32768, n * 16384, n * 16384,
                                       n * 4, n * 4, n * 4, n * 4, part, part};
   size_t at = kStatusBytes;
   for (int i = 0; i <= kTcParts; i++) {
@@ -73,7 +73,7 @@ extern "C" {
 
 size_t mesa_delta_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   if (check_sizes(B, H, Hk, T, dk, dv, dtype, 1.0f) != MESA_OK) return 0;
-  return kStatusBytes + (rule_tc_forward(dtype, dk, dv, T) ? mesa::rule_tc_workspace(B * H, T)
+  return kStatusBytes + (rule_tc_forward(dtype, dk, dv, T) ? mesa::rule_tc_workspace(B * H, T, false)
                                                             : mesa::rule_scan_workspace(B * H, T, dk, dv, false));
 }
 
@@ -159,10 +159,11 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
     auto f = [&](int i) { return (float *)(w + off[i]); };
     auto b8 = [&](int i) { return (uint8_t *)(w + off[i]); };
     const mesa::RuleOperands so{b8(1), b8(3), f(5), f(6)}, ao{b8(2), b8(4), f(7), f(8)};
-    const mesa::RuleSegments sg = mesa::rule_tc_segments(a.units(), T, b8(0));
+    const mesa::RuleSegments sg = mesa::rule_tc_segments(a.units(), T, true, b8(0));
     const bool ok = mesa::launch_rule_prep(a, b8(0), sg, false, stream) == 0 &&
+                    mesa::launch_rule_adjoint_tails(a, b8(0), sg, stream) == 0 &&
                     mesa::launch_rule_states_tc(a, b8(0), sg, so, stream) == 0 &&
-                    mesa::launch_rule_adjoint_tc(a, b8(0), ao, stream) == 0 &&
+                    mesa::launch_rule_adjoint_tc(a, b8(0), sg, ao, stream) == 0 &&
                     mesa::launch_rule_grads_tc(a, b8(0), so, ao, Hk != H ? f(9) : nullptr, Hk != H ? f(10) : nullptr,
                                                stream) == 0;
     return ok ? MESA_OK : MESA_ERR_CUDA;

@@ -73,16 +73,22 @@ struct RuleSegments {
   float2 *bounds = nullptr;  // [U, NC] log2 of what a chunk leaves of a state; what it adds to a row (bounds)
   float *S = nullptr, *loc = nullptr, *Tr = nullptr;  // [U, n][128 x 128] the state before; what it leaves
   int *whole = nullptr;  // [U, n] whether what went before counts (Tr is there and to be applied)
+  // the backward's: what a chunk adds to a row of the adjoint (bounds), the adjoints after the segments, what
+  // they give from zero, whether what comes after counts
+  float *adds = nullptr, *A = nullptr, *adj = nullptr;
+  int *whole_adj = nullptr;
 };
-size_t rule_tc_workspace(int U, int T);
-RuleSegments rule_tc_segments(int U, int T, void *workspace);
+size_t rule_tc_workspace(int U, int T, bool backward);
+RuleSegments rule_tc_segments(int U, int T, bool backward, void *workspace);
 int launch_rule_prep(const RuleArgs &a, void *records, const RuleSegments &sg, bool with_beta, cudaStream_t st);
 int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st);
 // The backward on the tensor cores, from the records (without beta): the states and u before the
 // adjoint chain, the adjoint chain, the gradients.
 int launch_rule_states_tc(const RuleArgs &a, const void *records, const RuleSegments &sg, const RuleOperands &so,
                           cudaStream_t st);
-int launch_rule_adjoint_tc(const RuleArgs &a, const void *records, const RuleOperands &ao, cudaStream_t st);
+int launch_rule_adjoint_tails(const RuleArgs &a, const void *records, const RuleSegments &sg, cudaStream_t st);  // (first)
+int launch_rule_adjoint_tc(const RuleArgs &a, const void *records, const RuleSegments &sg, const RuleOperands &ao,
+                           cudaStream_t st);
 int launch_rule_grads_tc(const RuleArgs &a, const void *records, const RuleOperands &so, const RuleOperands &ao,
                          float *dqp, float *dkp, cudaStream_t st);
 // dq, dk [B, Hk, T, dk] = sums of the per-unit fp32 parts over the value heads of a key head.

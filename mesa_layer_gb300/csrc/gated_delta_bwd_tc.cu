@@ -39,6 +39,7 @@ struct AdjointMisc {
   float ig[2];                // 1 / scale of the g tiles
   uint64_t tile_full[2], tile_free[2], rec_full[3], r_ready, u_ready, o_free, upd, dp_full, dq_full;
   uint64_t mma1, mma2, mma3, drain;
+  float rest, rest0;  // a bound of what the chunks after can give, of the part of dS_final that can come through
   uint32_t tmem;
   int gave_up;
 };
@@ -48,21 +49,83 @@ static_assert(AD_SMEM <= 232448, "shared memory per block");
 constexpr uint32_t T_DS = 0, T_DQ = 128, T_S = 256, T_D1 = 320, T_DP = 384, T_D2 = 448;
 constexpr uint32_t T_R = T_D1, T_CU = T_D1;
 
-// grid U, 384 threads: warps 0-3 chain (thread r: row r of A), 4-7 write du, 8-11 convert.
-__global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, const uint8_t *records, RuleOperands ao) {
+// grid (U, segments), 384 threads: warps 0-3 chain (thread r: row r of A), 4-7 write du, 8-11 convert.
+// SEG, grid (U, segments - 1): what the segments from 1 on give from an adjoint of zero after them (the last: from
+// dS_final), nothing kept.  `tail`: of the chunks at the segment's start only those of whose end 2^-40 of an
+// adjoint comes through, all there is when the bounds of what follows say that it adds less than 2^-26 of each
+// row's largest element (as for the states); not tail: the segments where it was not, in full.
+template <bool SEG>
+__global__ void __launch_bounds__(384, 1)
+    mesa_rule_adjoint_kernel(RuleArgs a, const uint8_t *records, RuleOperands ao, RuleSegments sg, bool tail) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   AdjointMisc *m = reinterpret_cast<AdjointMisc *>(sm + AD_MISC);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // (warp: uniform)
-  const int u = blockIdx.x, T = a.T, NC = (T + C - 1) / C;
+  const int u = blockIdx.x, seg = blockIdx.y + (SEG ? 1 : 0), T = a.T, NCT = (T + C - 1) / C;
+  const int c0 = sg.n > 1 ? seg * sg.per : 0;
+  int NC = sg.n > 1 ? min(NCT - c0, sg.per) : NCT;  // this CTA's chunks, from c0 on
+  const float *start = !SEG && sg.n > 1 ? sg.A + ((size_t)u * sg.n + seg) * D * D  // (nullptr: zero)
+                       : a.dS_final && (!SEG || seg == sg.n - 1) ? a.dS_final + (size_t)u * D * D
+                                                                 : nullptr;
+  if constexpr (SEG) {
+    int *whole = sg.whole_adj + (size_t)u * sg.n + seg;
+    if (tail) {
+      const float2 *left_of = sg.bounds + (size_t)u * NCT;
+      float left = 0.0f;
+      int n = 0;
+      while (n < NC && !(left <= -40.0f)) left += left_of[c0 + n++].x;
+      if (!(left <= -40.0f)) {
+        if (tid == 0) *whole = 1;
+        return;
+      }
+      NC = n;
+      start = nullptr;
+      if (warp == 11) {  // what the chunks after can give: four a lane
+        float rest = 0.0f;
+        for (int j0 = c0 + NC; j0 < NCT; j0 += 128) {
+          const int j = j0 + 4 * lane;
+          float l[4], b[4], mine = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            l[i] = j + i < NCT ? left_of[j + i].x : 0.0f;
+            b[i] = j + i < NCT ? sg.adds[(size_t)u * NCT + j + i] : 0.0f;
+            mine += l[i];
+          }
+          float run = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += x;
+          }
+          const float total = __shfl_sync(0xffffffffu, run, 31);
+          float before = left + __shfl_up_sync(0xffffffffu, run, 1);
+          if (lane == 0) before = left;
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            rest = fmaf(b[i], exp2f(before), rest);
+            before += l[i];
+          }
+          left += total;
+        }
+        rest = warp_sum(rest);
+        if (lane == 0) {
+          m->rest = rest;
+          m->rest0 = exp2f(left);  // of dS_final
+        }
+      }
+    } else if (!*whole) {
+      return;
+    }
+  }
+  const int last = c0 + NC - 1;
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
-  // step it works on chunk NC - 1 - it
+  // step it works on chunk last - it
   auto fetch_rec = [&](int it) {
     const uint32_t b = bar(m->rec_full[it % 3]);
     tc::mbar_arrive_expect_tx(b, REC);
-    tc::bulk_g2s(tc::smem_u32(sm + AD_REC + (it % 3) * REC_PAD), records + ((size_t)u * NC + NC - 1 - it) * REC, REC, b);
+    tc::bulk_g2s(tc::smem_u32(sm + AD_REC + (it % 3) * REC_PAD), records + ((size_t)u * NCT + last - it) * REC, REC, b);
   };
   if (warp == 0) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
   if (tid == 128) {
@@ -92,7 +155,7 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
     const uint32_t tl = tbase + ((uint32_t)(32 * warp) << 16);
     u64 S[D / 2];
     {
-      const float4 *src = a.dS_final ? reinterpret_cast<const float4 *>(a.dS_final + ((size_t)u * D + r) * D) : nullptr;
+      const float4 *src = start ? reinterpret_cast<const float4 *>(start + (size_t)r * D) : nullptr;
 #pragma unroll
       for (int g = 0; g < D / 4; g++) {
         const float4 x = src ? src[g] : make_float4(0, 0, 0, 0);
@@ -121,6 +184,7 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
     };
     auto keep_words = [&](int k, const float (&v)[8]) {  // columns 16 k .. of this row
       tc::tmem_st8(tl + T_S + 8 * k, v);
+      if constexpr (SEG) return;
       *reinterpret_cast<float4 *>(sm + AD_STAGE + tile_off(r, 2 * k, 128)) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4 *>(sm + AD_STAGE + tile_off(r, 2 * k + 1, 128)) = make_float4(v[4], v[5], v[6], v[7]);
     };
@@ -163,8 +227,8 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
           tc::mma_f16_ts(tbase + T_D1, tbase + T_S + 8 * s, kd + step128(s), id64, s > 0);
         tc::mma_commit(bar(m->mma1));
       }
-      if (r == 32) {  // the adjoint after the chunk
-        const size_t at = (size_t)u * NC + NC - 1 - it;
+      if (!SEG && r == 32) {  // the adjoint after the chunk
+        const size_t at = (size_t)u * NCT + last - it;
         bulk_s2g(ao.S + at * TILE, tc::smem_u32(sm + AD_STAGE), TILE);
         tc::bulk_commit();
         ao.iS[at] = iS;
@@ -285,8 +349,23 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
       if ((it & 7) == 7) row_max();  // (before the bound is loose)
     }
     if (r == 32) tc::bulk_wait_all();
-    if (!group_or(1, 128, !ok) && a.dS0) {
-      float4 *dst = reinterpret_cast<float4 *>(a.dS0 + ((size_t)u * D + r) * D);
+    if (SEG && tail) {  // is that all?  (a NaN or an infinity anywhere: no)
+      row_max();
+      float after = m->rest;
+      if (a.dS_final) {
+        const float *src = a.dS_final + ((size_t)u * D + r) * D;
+        float x = 0.0f;
+        for (int j = 0; j < D; j++) x += fabsf(src[j]);
+        after = fmaf(x, m->rest0, after);
+      }
+      const int more = group_or(1, 128, !(after <= 0x1p-26f * bS));
+      if (r == 0) sg.whole_adj[(size_t)u * sg.n + seg] = more;
+    }
+    float *final = SEG              ? sg.adj + ((size_t)u * sg.n + seg) * D * D
+                   : a.dS0 && seg == 0 ? a.dS0 + (size_t)u * D * D
+                                       : nullptr;
+    if (!group_or(1, 128, !ok) && final) {
+      float4 *dst = reinterpret_cast<float4 *>(final + (size_t)r * D);
 #pragma unroll
       for (int g = 0; g < D / 4; g++) {
         float4 x;
@@ -306,6 +385,14 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
       if (group_or(2, 128, !got)) {
         ok = false;
         break;
+      }
+      if constexpr (SEG) {  // nothing to write
+        warp_arrive(m->o_free);
+        if (it + 3 < NC) {
+          if (h == 0) fetch_rec(it + 3);
+          rec_sent++;
+        }
+        continue;
       }
       tc::fence_after_sync();
       float x[2][32];
@@ -339,7 +426,7 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
       tc::fence_smem_to_async();
       group_or(2, 128, false);
       if (h == 0) {
-        const size_t at = (size_t)u * NC + NC - 1 - it;
+        const size_t at = (size_t)u * NCT + last - it;
         bulk_s2g(ao.U + at * ROWS64, tc::smem_u32(sm + AD_OUT), ROWS64);
         tc::bulk_commit();
         ao.iU[at] = iu;
@@ -370,7 +457,7 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
       }
     };
     const uint32_t idP = tc::idesc_f16(128, C, true, true), idQ = tc::idesc_f16(128, D, true, true);
-    load(NC - 1);
+    load(last);
     for (int it = 0; it < NC; it++) {
       const int b = it & 1;
       uint32_t mg = 0;
@@ -401,7 +488,7 @@ __global__ void __launch_bounds__(384, 1) mesa_rule_adjoint_kernel(RuleArgs a, c
       }
       tc::fence_smem_to_async();
       warp_arrive(m->tile_full[b]);
-      if (it + 1 < NC) load(NC - 2 - it);
+      if (it + 1 < NC) load(last - 1 - it);
       if (warp == 8) {
         const uint64_t gd = tc::mnmajor_desc(tc::smem_u32(sm + AD_G + b * ROWS64), C, 0);
         const uint64_t pd = tc::mnmajor_desc(tc::smem_u32(sm + AD_REC + (it % 3) * REC_PAD + REC_P), C, 0);
@@ -695,11 +782,12 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     }
     const float mul = upper ? a.scale * ig * iu : idu * iu;
     // the operand's units: W alpha, V alpha sq / sk, both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
-    // 128 products, beta < 4, V + V^T)
-    float ialpha;
+    // 128 products, beta < 4, V + V^T); in dq's rows, where W stands alone, its own (V can be far larger)
+    float ialpha, ialpha_q;
     const float vq = sk_sq.y * ik;  // sq / sk
     const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * iu * 33554432.0f, 8.0f * idu * iu * vq * 137438953472.0f),
                                     kTopRow, ialpha);
+    const float alpha_q = bound_scale(fabsf(a.scale) * ig * iu * 33554432.0f, kTopRow, ialpha_q);
     if (next < chunks) fetch_qk(next);
     const bool got_a = tc::mbar_wait(ba, ph, a.wait_limit);
     tc::fence_after_sync();
@@ -716,10 +804,11 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
         tmem_ld_frag16(tl + ((uint32_t)(16 * h) << 16) + T_G4 + 16 * part, y[h]);
       }
       const u64 lj[2] = {*reinterpret_cast<const u64 *>(&m->l[col]), *reinterpret_cast<const u64 *>(&m->l[col + 8])};
-      const float qk = (upper ? iq : ik) * ik, op0 = upper ? alpha : -alpha * vq;  // real q . k, k . k
+      const float qk = (upper ? iq : ik) * ik, op0 = upper ? alpha_q : -alpha * vq;  // real q . k, k . k
       const u64 mul2x = pack2(mul, mul), qk2 = pack2(qk, qk);
       const bool closed = m->z[C - 1] != 0;  // a gate in the chunk
-      uint32_t p[2][4];  // the operand's fragments
+      uint32_t p[2][4], pt[2][4];  // the operand's fragments (W: as it stands, and for its transpose)
+      const float down = alpha * ialpha_q;
       float db[2][2];
       tc::tmem_ld_wait();
 #pragma unroll
@@ -746,7 +835,10 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
             unpack2(y[h][2 * b + e], y0, y1);
             unpack2(mul2(mul2(w, op2), pack2(d0, d1)), x0, x1);
             // (columns without a decay are none of the operand's, whatever their products are)
-            p[h][2 * b + e] = __float_as_uint(half2_bits(j <= keep ? x0 : 0.0f, j + 1 <= keep ? x1 : 0.0f));
+            x0 = j <= keep ? x0 : 0.0f;
+            x1 = j + 1 <= keep ? x1 : 0.0f;
+            p[h][2 * b + e] = __float_as_uint(half2_bits(x0, x1));
+            pt[h][2 * b + e] = __float_as_uint(half2_bits(x0 * down, x1 * down));
             if (j <= keep) sum = fmaf(d0, y0, sum);
             if (j + 1 <= keep) sum = fmaf(d1, y1, sum);
           }
@@ -761,7 +853,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
           stmatrix_x4(tc::smem_u32(sm + GR_A5 + tile_off(i0 + 16 * h + 8 * (lb & 1) + l8, 8 + 2 * part + (lb >> 1), 128)),
                       p[h][0], p[h][1], p[h][2], p[h][3]);
           stmatrix_x4_trans(tc::smem_u32(sm + GR_A5 + tile_off(C + 16 * part + 8 * (lb >> 1) + l8, (i0 >> 3) + 2 * h + (lb & 1), 128)),
-                            p[h][0], p[h][1], p[h][2], p[h][3]);
+                            pt[h][0], pt[h][1], pt[h][2], pt[h][3]);
 #pragma unroll
           for (int e = 0; e < 2; e++)
 #pragma unroll
@@ -917,7 +1009,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     }
     // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 32 part ..
     const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;
-    const float f2 = m->c[i] * iu * iA, f5 = ialpha * (upper ? ik : iq);
+    const float f2 = m->c[i] * iu * iA, f5 = upper ? ialpha_q * ik : ialpha * iq;
     uint8_t *out = sm + GR_A5 + (upper ? 0 : ROWS64);
     float *sum = upper ? dqp : dkp;
 #pragma unroll
@@ -977,13 +1069,69 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
 
 }  // namespace
 
-int launch_rule_adjoint_tc(const RuleArgs &a, const void *records, const RuleOperands &ao, cudaStream_t st) {
-  if (cudaFuncSetAttribute(mesa_rule_adjoint_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AD_SMEM) != cudaSuccess)
-    return -1;
-  timing_mark_begin(K_RULE_ADJOINT, st);
-  mesa_rule_adjoint_kernel<<<a.units(), 384, AD_SMEM, st>>>(a, (const uint8_t *)records, ao);
-  timing_mark_end(K_RULE_ADJOINT, st);
+namespace {
+// The adjoint after each segment: A_{y-1} = A_y Tr_y^T + adj_y (A_{n-2} = adj_{n-1}; A_{n-1} is a copy of dS_final: dS0
+// may be its memory), sixteen rows by a CTA of 256 threads; grid (8, U).
+__global__ void __launch_bounds__(256) mesa_rule_join_adjoint_kernel(RuleSegments sg, const float *dS_final) {
+  __shared__ __align__(16) float rows[16][D + 4];
+  const int u = blockIdx.y, row0 = 16 * blockIdx.x, tid = threadIdx.x;
+  const int r = tid >> 4, c0 = (tid & 15) * 8;  // row r, columns c0 ..
+  const size_t own = (size_t)(row0 + r) * D + c0;
+  for (int i = 0; i < 8; i++)
+    sg.A[((size_t)u * sg.n + sg.n - 1) * D * D + own + i] = dS_final ? dS_final[(size_t)u * D * D + own + i] : 0.0f;
+  for (int y = sg.n - 1; y > 0; y--) {
+    const size_t at = (size_t)u * sg.n + y;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = sg.adj[at * D * D + own + i];
+    if (y < sg.n - 1 && sg.whole_adj[at]) {
+      const float *Tr = sg.Tr + at * D * D + (size_t)c0 * D;
+#pragma unroll 2
+      for (int k = 0; k < D; k += 4) {
+        const float4 s = *reinterpret_cast<const float4 *>(&rows[r][k]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const float4 p = *reinterpret_cast<const float4 *>(Tr + i * D + k);
+          x[i] = fmaf(s.x, p.x, fmaf(s.y, p.y, fmaf(s.z, p.z, fmaf(s.w, p.w, x[i]))));
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      rows[r][c0 + i] = x[i];
+      sg.A[(at - 1) * D * D + own + i] = x[i];
+    }
+    __syncthreads();
+  }
+}
+
+template <bool SEG>
+int launch_adjoint(const RuleArgs &a, const void *records, const RuleOperands &ao, const RuleSegments &sg, bool tail,
+                   cudaStream_t st) {
+  auto kfn = mesa_rule_adjoint_kernel<SEG>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)AD_SMEM) != cudaSuccess) return -1;
+  const int kind = SEG ? K_RULE_SEGMENT : K_RULE_ADJOINT;
+  timing_mark_begin(kind, st);
+  kfn<<<dim3(a.units(), SEG ? sg.n - 1 : sg.n), 384, AD_SMEM, st>>>(a, (const uint8_t *)records, ao, sg, tail);
+  timing_mark_end(kind, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+}  // namespace
+
+int launch_rule_adjoint_tails(const RuleArgs &a, const void *records, const RuleSegments &sg, cudaStream_t st) {
+  return sg.n == 1 ? 0 : launch_adjoint<true>(a, records, RuleOperands{}, sg, true, st);
+}
+int launch_rule_adjoint_tc(const RuleArgs &a, const void *records, const RuleSegments &sg, const RuleOperands &ao,
+                           cudaStream_t st) {
+  if (sg.n > 1) {
+    if (launch_adjoint<true>(a, records, RuleOperands{}, sg, false, st) != 0) return -1;
+    timing_mark_begin(K_RULE_JOIN, st);
+    mesa_rule_join_adjoint_kernel<<<dim3(8, a.units()), 256, 0, st>>>(sg, a.dS_final);
+    timing_mark_end(K_RULE_JOIN, st);
+    if (cudaPeekAtLastError() != cudaSuccess) return -1;
+  }
+  return launch_adjoint<false>(a, records, ao, sg, false, st);
 }
 
 int launch_rule_grads_tc(const RuleArgs &a, const void *records, const RuleOperands &so, const RuleOperands &ao,

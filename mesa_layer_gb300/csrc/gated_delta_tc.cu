@@ -38,7 +38,7 @@ static_assert(PR_MISC % 16 == 0 && PR_SCR % 16 == 0, "alignment");
 struct PrepMisc {
   alignas(16) uint32_t red[8];
   float grow[C], give[C];
-  uint32_t vmax[4];
+  uint32_t vmax[4], gmax[4];
   uint64_t mbar, drain;
   uint32_t tmem;
 };
@@ -48,10 +48,11 @@ static_assert(6 * (PR_SMEM + 1024) <= 228 * 1024, "six CTAs on an SM");
 // grid (NC, U), 128 threads.  WITH_BETA: the record's factor is T diag(beta), else T.  bounds [U, NC]
 // (or nullptr): log2 of how much of a state the chunk leaves, at most, the product over its tokens of
 // gamma max(1, |1 - beta k.k|) (the norm of gamma (I - beta k k^T)); and a bound of the norm of what it adds
-// to a row of the state, the largest |v| times the sum of beta |k|.  Numbers that are none (or
-// that could end in an overflow) bound nothing: infinity or NaN.
+// to a row of the state, the largest |v| times the sum of beta |k|.  adds [U, NC] (or nullptr): the same of the
+// adjoint before the chunk, from the largest |dout| and |q|.  Numbers that are none (or that could end
+// in an overflow) bound nothing: infinity or NaN.
 template <bool WITH_BETA>
-__global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint8_t *records, float2 *bounds) {
+__global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint8_t *records, float2 *bounds, float *adds) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   PrepMisc *m = reinterpret_cast<PrepMisc *>(sm + PR_MISC);
@@ -117,6 +118,11 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
     const uint4 *vp = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + tok0 * D);
 #pragma unroll
     for (int i = 0; i < 8; i++) x[i] = 128 * i + tid < n * (D / 8) ? vp[128 * i + tid] : make_uint4(0, 0, 0, 0);
+    if (adds) {
+      const uint4 *gp = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.dout + tok0 * D);
+#pragma unroll
+      for (int i = 0; i < 8; i++) y[i] = 128 * i + tid < n * (D / 8) ? gp[128 * i + tid] : make_uint4(0, 0, 0, 0);
+    }
   }
   if (warp == 0 && elect_one()) {  // rows 0..63: K K^T, rows 64..127: Q K^T
     const uint32_t id = tc::idesc_f16(128, C, false, false);
@@ -133,6 +139,13 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
     for (int i = 0; i < 8; i++) mv = absmax_words(mv, x[i]);
     mv = absmax_fold(mv);
     if (lane == 0) m->vmax[warp] = mv;
+    if (adds) {
+      mv = 0;
+#pragma unroll
+      for (int i = 0; i < 8; i++) mv = absmax_words(mv, y[i]);
+      mv = absmax_fold(mv);
+      if (lane == 0) m->gmax[warp] = mv;
+    }
   }
   if (__syncthreads_or(!done)) {
     if (tid == 0) atomicOr(a.status, tc::kErrMmaTimeout);
@@ -158,7 +171,8 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
       }
       kk *= ik * ik;
       const float grow = fabsf(1.0f - be * kk);  // (0.003: k's rounding to fp16)
-      m->grow[tid] = grow <= 1.0f ? 0.0f : grow < INFINITY ? log2f(grow) + 0.003f : INFINITY;
+      const float up = s.l[tid] - (tid > 0 ? s.l[tid - 1] : 0.0f);  // (of a gate above 1)
+      m->grow[tid] = (grow <= 1.0f ? 0.0f : grow < INFINITY ? log2f(grow) + 0.003f : INFINITY) + fmaxf(up, 0.0f);
       m->give[tid] = fabsf(be) * sqrtf(kk) * 1.002f;
     }
     factor_rows(s, tbase, ik * ik, rec + SQ, tid);
@@ -167,9 +181,15 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
     if (bounds && warp == 3) {
       const float grow = warp_sum(m->grow[lane] + m->grow[lane + 32]), give = warp_sum(m->give[lane] + m->give[lane + 32]);
       const float vmax = __uint_as_float(max(max(m->vmax[0], m->vmax[1]), max(m->vmax[2], m->vmax[3])) << 16);
-      const float adds = vmax * give * exp2f(grow);
+      const float add = vmax * give * exp2f(grow);
       if (lane == 0)
-        bounds[(size_t)u * NC + c] = make_float2((s.z[C - 1] != 0 ? -1e30f : s.l[C - 1]) + grow, adds < 1e30f ? adds : INFINITY);
+        bounds[(size_t)u * NC + c] = make_float2((s.z[C - 1] != 0 ? -1e30f : s.l[C - 1]) + grow, add < 1e30f ? add : INFINITY);
+      if (adds && lane == 0) {
+        const float gmax = __uint_as_float(max(max(m->gmax[0], m->gmax[1]), max(m->gmax[2], m->gmax[3])) << 16);
+        const float qmax = __uint_as_float(max(max(q4.x, q4.y), max(q4.z, q4.w)) << 16);
+        const float g = fabsf(a.scale) * gmax * qmax * exp2f(grow) * (C * 11.4f);  // (C tokens, sqrt(D))
+        adds[(size_t)u * NC + c] = g < 1e30f ? g : INFINITY;
+      }
     }
     factor_diagonal<WITH_BETA>(s, rec, warp, lane);
     __syncthreads();
@@ -303,7 +323,7 @@ __global__ void __launch_bounds__(384, 1)
           m->rest0 = exp2f(left);  // of S0
         }
       }
-    } else if (!*whole || (identity && seg == 0)) {
+    } else if (identity ? seg == 0 || (!*whole && !(sg.whole_adj && sg.whole_adj[(size_t)u * sg.n + seg])) : !*whole) {
       return;
     }
   }
@@ -877,26 +897,35 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// [records | chunk bounds | states before segments, their own states, matrices | matrix flags]
-size_t rule_tc_workspace(int U, int T) {
+// [records | chunk bounds | states before segments, their own states, matrices | matrix flags], and for the backward
+// [bounds of the adjoint | adjoints after segments, their own | flags]
+size_t rule_tc_workspace(int U, int T, bool backward) {
   const int NC = (T + C - 1) / C, n = segments(U, NC);
-  const size_t rec = up256((size_t)U * NC * REC);
-  return n == 1 ? rec : rec + up256((size_t)U * NC * 8) + 3 * (size_t)U * n * D * D * 4 + up256((size_t)U * n * 4);
+  const size_t rec = up256((size_t)U * NC * REC), mats = (size_t)U * n * D * D * 4, flags = up256((size_t)U * n * 4);
+  if (n == 1) return rec;
+  return rec + up256((size_t)U * NC * 8) + 3 * mats + flags + (backward ? up256((size_t)U * NC * 4) + 2 * mats + flags : 0);
 }
-RuleSegments rule_tc_segments(int U, int T, void *workspace) {
+RuleSegments rule_tc_segments(int U, int T, bool backward, void *workspace) {
   const int NC = (T + C - 1) / C;
   RuleSegments sg;
   sg.n = segments(U, NC);
   if (sg.n == 1) return sg;
+  const size_t mats = (size_t)U * sg.n * D * D, flags = up256((size_t)U * sg.n * 4);
   sg.per = (NC + sg.n - 1) / sg.n;
   sg.n = (NC + sg.per - 1) / sg.per;  // (no empty one; the strides of the arrays are this count's)
   uint8_t *w = (uint8_t *)workspace + up256((size_t)U * NC * REC);
-  const size_t mats = (size_t)U * sg.n * D * D;
   sg.bounds = (float2 *)w;
   sg.S = (float *)(w + up256((size_t)U * NC * 8));
   sg.loc = sg.S + mats;
   sg.Tr = sg.loc + mats;
   sg.whole = (int *)(sg.Tr + mats);
+  if (backward) {
+    w = (uint8_t *)sg.whole + flags;
+    sg.adds = (float *)w;
+    sg.A = (float *)(w + up256((size_t)U * NC * 4));
+    sg.adj = sg.A + mats;
+    sg.whole_adj = (int *)(sg.adj + mats);
+  }
   return sg;
 }
 
@@ -904,7 +933,7 @@ int launch_rule_prep(const RuleArgs &a, void *records, const RuleSegments &sg, b
   auto kfn = with_beta ? mesa_rule_prep_kernel<true> : mesa_rule_prep_kernel<false>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PR_SMEM) != cudaSuccess) return -1;
   timing_mark_begin(K_RULE_PREP, st);
-  kfn<<<dim3((a.T + C - 1) / C, a.units()), 128, PR_SMEM, st>>>(a, (uint8_t *)records, sg.bounds);
+  kfn<<<dim3((a.T + C - 1) / C, a.units()), 128, PR_SMEM, st>>>(a, (uint8_t *)records, sg.bounds, sg.adds);
   timing_mark_end(K_RULE_PREP, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
@@ -927,7 +956,7 @@ int launch_segments(const RuleArgs &a, const uint8_t *records, const RuleSegment
 }  // namespace
 
 int launch_rule_forward_tc(const RuleArgs &a, void *workspace, cudaStream_t st) {
-  const RuleSegments sg = rule_tc_segments(a.units(), a.T, workspace);
+  const RuleSegments sg = rule_tc_segments(a.units(), a.T, false, workspace);
   const uint8_t *records = (const uint8_t *)workspace;
   CUtensorMap mapV{}, mapO{};
   if (!tmap_units128_bf16(&mapV, a.v, a.units(), a.T) || !tmap_units128_bf16(&mapO, a.out, a.units(), a.T)) return -1;

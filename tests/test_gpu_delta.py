@@ -472,3 +472,43 @@ def test_wait_give_up_in_a_long_sequence_reports_timeout():
     assert code == binding.MESA_ERR_TIMEOUT and bits & 1 and not bits & 4
     assert torch.equal(binding.mesa_delta_forward_chunked(*args, workspace=ws), want)
     assert binding.mesa_forward_status(ws) == 0
+
+
+def test_gradients_across_a_long_sequence_with_loud_ends():
+    """dL/dout 2^30 times louder in the second half: it still rules the gradients of the first half
+    long before it (0.985 ^ 1000 = 2^-22 of it), compared chunk by chunk."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    T = 2048
+    s = _long_inputs(T, "open", True, 51)
+    s["gamma"] = np.random.default_rng(52).uniform(0.97, 1.0, s["gamma"].shape).astype(np.float32)
+    s["dout"][:, :, T // 2:] *= 2.0 ** 15
+    s["dout"][:, :, :T // 2] *= 2.0 ** -15
+    t = upload(s, "bf16")
+    dS0 = torch.full((1, 2, 128, 128), float("nan"), device="cuda")
+    got = dict(zip(("dq", "dk", "dv", "dgamma", "dbeta"), binding.mesa_delta_backward_chunked(
+        t["q"], t["k"], t["v"], t["gamma"], t["beta"], t["dout"], SCALE, S0=t["S0"], dS_final=t["dS_final"], dS0=dS0)))
+    want = ref.rule_backward(s["q"], s["k"], s["v"], s["gamma"], s["beta"], SCALE, s["dout"], s["S0"], s["dS_final"])
+    for n in ("dq", "dk", "dv"):
+        for i in range(0, T, 64):
+            assert err(got[n][:, :, i:i + 64], want[n][:, :, i:i + 64]) <= TOL["bf16"], (n, i)
+    assert err(dS0, want["dS0"]) <= STATE_TOL["bf16"]
+
+
+@pytest.mark.parametrize("what", ["dout", "dS_final"])
+def test_nonfinite_gradients_last_through_long_sequences(what):
+    """A NaN late in a long sequence reaches the first token's gradients (0.9 ^ 3000 of it)."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    t = upload(_long_inputs(3001, "open", True), "bf16")
+    if what == "dout":
+        t["dout"][0, 1, 2950, 5] = float("nan")
+    else:
+        t["dS_final"][0, 1, 5, 7] = float("inf")
+    dS0 = torch.zeros((1, 2, 128, 128), device="cuda")
+    dv = binding.mesa_delta_backward_chunked(t["q"], t["k"], t["v"], t["gamma"], t["beta"], t["dout"], SCALE, S0=t["S0"],
+                                             dS_final=t["dS_final"], dS0=dS0)[2]
+    assert torch.isfinite(dS0[0, 0]).all() and torch.isfinite(dv[0, 0]).all()
+    assert not torch.isfinite(dS0[0, 1, 5]).any() and not torch.isfinite(dv[0, 1, 0, 5])
