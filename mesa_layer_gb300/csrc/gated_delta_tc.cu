@@ -15,7 +15,7 @@
 //     chain    the three epilogues above;
 //     helper   writes the readout (and with the transposition, too, it held up the chain: 188 us);
 //     convert  V transposed one chunk ahead, K and Q as fp16 operands, up to three chunks ahead.
-// Measured at 8 x 16 x 4096 (8192 chunks): preparation 110 us (400 MB of rows and records: 3.7 TB/s; the
+// Measured at 8 x 16 x 4096 (8192 chunks): preparation 113 us (400 MB of rows and records: 3.5 TB/s; the
 // substitution's latency and instruction fetch), chain 179 us (64 dependent steps of 2.8 us; issue slots
 // 37 %, tensor pipe 19 % busy: the latency of four products and three epilogues a step, 128 of 152 SMs).
 // (With the preparation in the same kernel, as a fourth group, nothing but the inputs and the output
