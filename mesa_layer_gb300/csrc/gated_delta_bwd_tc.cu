@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(384, 1)
       const float2 *left_of = sg.bounds + (size_t)u * NCT;
       float left = 0.0f;
       int n = 0;
-      while (n < NC && !(left <= -40.0f)) left += left_of[c0 + n++].x;
-      if (!(left <= -40.0f)) {
+      while (n < NC && !(left <= kLittle)) left += left_of[c0 + n++].x;
+      if (!(left <= kLittle)) {
         if (tid == 0) *whole = 1;
         return;
       }

@@ -15,7 +15,7 @@
 //     chain    the three epilogues above;
 //     helper   writes the readout (and with the transposition, too, it held up the chain: 188 us);
 //     convert  V transposed one chunk ahead, K and Q as fp16 operands, up to three chunks ahead.
-// Measured at 8 x 16 x 4096 (8192 chunks): preparation 113 us (400 MB of rows and records: 3.5 TB/s; the
+// Measured at 8 x 16 x 4096 (8192 chunks): preparation 110 us (400 MB of rows and records: 3.7 TB/s; the
 // substitution's latency and instruction fetch), chain 179 us (64 dependent steps of 2.8 us; issue slots
 // 37 %, tensor pipe 19 % busy: the latency of four products and three epilogues a step, 128 of 152 SMs).
 // (With the preparation in the same kernel, as a fourth group, nothing but the inputs and the output
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
     const uint4 *vp = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.v + tok0 * D);
 #pragma unroll
     for (int i = 0; i < 8; i++) x[i] = 128 * i + tid < n * (D / 8) ? vp[128 * i + tid] : make_uint4(0, 0, 0, 0);
-    if (adds) {
+    if (!WITH_BETA && adds) {  // (the backward's)
       const uint4 *gp = reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)a.dout + tok0 * D);
 #pragma unroll
       for (int i = 0; i < 8; i++) y[i] = 128 * i + tid < n * (D / 8) ? gp[128 * i + tid] : make_uint4(0, 0, 0, 0);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
     for (int i = 0; i < 8; i++) mv = absmax_words(mv, x[i]);
     mv = absmax_fold(mv);
     if (lane == 0) m->vmax[warp] = mv;
-    if (adds) {
+    if (!WITH_BETA && adds) {
       mv = 0;
 #pragma unroll
       for (int i = 0; i < 8; i++) mv = absmax_words(mv, y[i]);
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
       const float add = vmax * give * exp2f(grow);
       if (lane == 0)
         bounds[(size_t)u * NC + c] = make_float2((s.z[C - 1] != 0 ? -1e30f : s.l[C - 1]) + grow, add < 1e30f ? add : INFINITY);
-      if (adds && lane == 0) {
+      if (!WITH_BETA && adds && lane == 0) {
         const float gmax = __uint_as_float(max(max(m->gmax[0], m->gmax[1]), max(m->gmax[2], m->gmax[3])) << 16);
         const float qmax = __uint_as_float(max(max(q4.x, q4.y), max(q4.z, q4.w)) << 16);
         const float g = fabsf(a.scale) * gmax * qmax * exp2f(grow) * (C * 11.4f);  // (C tokens, sqrt(D))
@@ -261,7 +261,6 @@ static_assert(kRegChain + kRegHelper + kRegConvert <= 3 * 168, "register file");
 // operands carry 2^-12).  Then, grid (U, segments - 1, 2), the segments where it was not: all their chunks
 // (z = 0), the matrix (z = 1).
 // kSegmentT: the same from records without beta.
-constexpr float kLittle = -40.0f;  // log2
 enum ChainMode { kFwd = 0, kKeep = 1, kSegment = 2, kSegmentT = 3 };
 template <int MODE>
 __global__ void __launch_bounds__(384, 1)

@@ -53,6 +53,7 @@ __device__ __forceinline__ float bound_scale(float bound, int top, float &inv) {
   return __uint_as_float((uint32_t)(253 + top - e) << 23);
 }
 constexpr int kTopRow = 15;   // state rows, R and U rows: bound to 2^15
+constexpr float kLittle = -40.0f;  // log2 of what is left of a state at the end of a segment's tail
 constexpr int kTopTile = 3;   // K and Q tiles: 128 products of two stay below 2^13
 // Largest |x| of 2 x 16-bit bf16 words, as an integer (the order of positive floats is theirs).
 __device__ __forceinline__ uint32_t absmax_words(uint32_t m, uint4 x) {
