@@ -781,13 +781,17 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       if (lane == 0) m->cross[warp] = s * iS * iA;
     }
     const float mul = upper ? a.scale * ig * iu : idu * iu;
-    // the operand's units: W alpha, V alpha sq / sk, both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
-    // 128 products, beta < 4, V + V^T); in dq's rows, where W stands alone, its own (V can be far larger)
-    float ialpha, ialpha_q;
+    // the operand's units: W alpha, V alpha sq / sk (= op_v), both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
+    // 128 products, beta < 4, V + V^T); in dq's rows, where W stands alone, its own (V can be far larger).  sq / sk
+    // has no bound (2^61 for unit keys without queries), so V's units come from V alone: where they are the
+    // smaller ones alpha = op_v sk / sq, which may be 0 (W^T Q is then nothing beside (V + V^T) K), and dk's unit
+    // is 1 / (op_v sk), not 1 / (alpha sq).
+    float ialpha_v, ialpha_q;
     const float vq = sk_sq.y * ik;  // sq / sk
-    const float alpha = bound_scale(fmaxf(fabsf(a.scale) * ig * iu * 33554432.0f, 8.0f * idu * iu * vq * 137438953472.0f),
-                                    kTopRow, ialpha);
+    const float alpha_v = bound_scale(8.0f * idu * iu * 137438953472.0f, kTopRow, ialpha_v);
     const float alpha_q = bound_scale(fabsf(a.scale) * ig * iu * 33554432.0f, kTopRow, ialpha_q);
+    const bool of_v = alpha_q * vq > alpha_v;  // (2^77 2^126 at most: infinity is greater, too)
+    const float alpha = of_v ? alpha_v * (iq * sk_sq.x) : alpha_q, op_v = of_v ? alpha_v : alpha_q * vq;
     if (next < chunks) fetch_qk(next);
     const bool got_a = tc::mbar_wait(ba, ph, a.wait_limit);
     tc::fence_after_sync();
@@ -804,7 +808,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
         tmem_ld_frag16(tl + ((uint32_t)(16 * h) << 16) + T_G4 + 16 * part, y[h]);
       }
       const u64 lj[2] = {*reinterpret_cast<const u64 *>(&m->l[col]), *reinterpret_cast<const u64 *>(&m->l[col + 8])};
-      const float qk = (upper ? iq : ik) * ik, op0 = upper ? alpha_q : -alpha * vq;  // real q . k, k . k
+      const float qk = (upper ? iq : ik) * ik, op0 = upper ? alpha_q : -op_v;  // real q . k, k . k
       const u64 mul2x = pack2(mul, mul), qk2 = pack2(qk, qk);
       const bool closed = m->z[C - 1] != 0;  // a gate in the chunk
       uint32_t p[2][4], pt[2][4];  // the operand's fragments (W: as it stands, and for its transpose)
@@ -1009,7 +1013,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     }
     // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 32 part ..
     const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;
-    const float f2 = m->c[i] * iu * iA, f5 = upper ? ialpha_q * ik : ialpha * iq;
+    const float f2 = m->c[i] * iu * iA, f5 = upper ? ialpha_q * ik : of_v ? ialpha_v * ik : ialpha_q * iq;
     uint8_t *out = sm + GR_A5 + (upper ? 0 : ROWS64);
     float *sum = upper ? dqp : dkp;
 #pragma unroll

@@ -1,0 +1,100 @@
+"""The gated delta rule on the GPU where inputs are unusual: chunks without queries, gates above one,
+correlated keys, non-finite values, other streams.  Against the 64-bit restatement with the tolerances of
+test_gpu_delta.py, whose derivation does not depend on the inputs, unless a test says otherwise."""
+import numpy as np
+import pytest
+
+import delta_reference as ref
+from test_gpu_delta import SCALE, STATE_TOL, TOL, err, upload
+
+pytestmark = pytest.mark.gpu
+GRADS = ("dq", "dk", "dv", "dgamma", "dbeta")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from mesa_layer_gb300 import binding, build
+    build.build()
+    binding.load()
+
+
+def sizes(t):
+    B, H, T, dv = t["v"].shape
+    return B, H, t["q"].shape[1], T, t["q"].shape[-1], dv, t["q"].dtype
+
+
+def forward(t):
+    """out, S_final, (status code, flags)."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    B, H, Hk, T, dk, dv, td = sizes(t)
+    SF = torch.full((B, H, dv, dk), float("nan"), device="cuda")
+    ws = torch.empty(binding.mesa_delta_workspace_size(*sizes(t)), dtype=torch.uint8, device="cuda")
+    out = binding.mesa_delta_forward_chunked(t["q"], t["k"], t["v"], t["gamma"], t["beta"], SCALE, S0=t["S0"], S_final=SF,
+                                             workspace=ws)
+    return out, SF, binding.mesa_forward_status_code(ws)
+
+
+def backward(t):
+    """The gradients by name (dS0 among them), (status code, flags)."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    B, H, Hk, T, dk, dv, td = sizes(t)
+    dS0 = torch.full((B, H, dv, dk), float("nan"), device="cuda")
+    ws = torch.empty(binding.mesa_delta_backward_workspace_size(*sizes(t)), dtype=torch.uint8, device="cuda")
+    got = binding.mesa_delta_backward_chunked(t["q"], t["k"], t["v"], t["gamma"], t["beta"], t["dout"], SCALE, S0=t["S0"],
+                                              dS_final=t["dS_final"], dS0=dS0, workspace=ws)
+    return dict(zip((*GRADS, "dS0"), (*got, dS0))), binding.mesa_forward_status_code(ws)
+
+
+def check_forward(s, dtype):
+    out, SF, status = forward(upload(s, dtype))
+    assert status == (0, 0)
+    o, S = ref.rule_forward(s["q"], s["k"], s["v"], s["gamma"], s["beta"], SCALE, s["S0"])
+    found = {"out": err(out, o), "S_final": err(SF, S)}
+    assert found["out"] <= TOL[dtype] and found["S_final"] <= STATE_TOL[dtype], found
+
+
+def check_backward(s, dtype):
+    got, status = backward(upload(s, dtype))
+    assert status == (0, 0)
+    want = ref.rule_backward(s["q"], s["k"], s["v"], s["gamma"], s["beta"], SCALE, s["dout"], s["S0"], s["dS_final"])
+    found = {n: err(x, want[n]) for n, x in got.items()}
+    assert max(found[n] for n in GRADS) <= TOL[dtype] and found["dS0"] <= STATE_TOL[dtype], found
+
+
+@pytest.mark.parametrize("what", ["no queries", "no queries, loud gradients", "padding without queries", "faint queries",
+                                  "no queries anywhere", "no keys"])
+def test_gradients_of_chunks_without_queries(what):
+    """The second 64-token chunk (of three) has no queries, or far smaller ones than its keys; as padding it
+    writes nothing and is not read either."""
+    s = ref.rule_inputs(61, "bf16", 1, 2, 1, 150, 128, 128, "open", True)
+    mid = slice(64, 128)
+    if what == "no queries":
+        s["q"][:, :, mid] = 0.0
+    elif what == "no queries, loud gradients":
+        s["q"][:, :, mid] = 0.0
+        for n in ("dout", "dS_final"):
+            s[n] *= 2.0 ** 12
+    elif what == "padding without queries":  # the last chunk
+        for n in ("q", "beta", "dout"):
+            s[n][:, :, 128:] = 0.0
+        s["dS_final"][:] = 0.0
+    elif what == "faint queries":
+        s["q"][:, :, mid] *= 2.0 ** -60
+        s["dout"] *= 2.0 ** 12
+    elif what == "no queries anywhere":
+        s["q"][:] = 0.0
+    else:
+        s["k"][:, :, mid] = 0.0
+    got, status = backward(upload(s, "bf16"))
+    assert status == (0, 0)
+    want = ref.rule_backward(s["q"], s["k"], s["v"], s["gamma"], s["beta"], SCALE, s["dout"], s["S0"], s["dS_final"])
+    for n in GRADS:  # chunk by chunk
+        for i in range(0, 150, 64):
+            assert err(got[n][:, :, i:i + 64], want[n][:, :, i:i + 64]) <= TOL["bf16"], (n, i)
+    assert err(got["dS0"], want["dS0"]) <= STATE_TOL["bf16"]
