@@ -237,9 +237,10 @@ __global__ void __launch_bounds__(384, 1)
       const float4 inv = *reinterpret_cast<const float4 *>(sm + AD_REC + (it % 3) * REC_PAD + REC_S);
       const float iK = inv.x, iQ = inv.y, ig = m->ig[ph], top = (float)(1 << kTopTile);
       const float kmax = top * iK, qmax = top * iQ, gmax = top * ig, all = -nf[C - 1];  // all: the chunk's decay
-      const float w1 = iS * iK, w2 = a.scale * ig * iK * iQ;  // units of D1 and of g^T P
+      const float gm = reinterpret_cast<const float *>(sm + AD_REC + (it % 3) * REC_PAD + REC_S)[4];  // no decay in it is greater
+      const float w1 = iS * iK, w2 = a.scale * ig * iK * iQ * gm;  // units of D1 and of g^T P
       float iR;
-      const float sR = bound_scale((float)D * kmax * fmaf((float)C * gmax * ascale, qmax, bS), kTopRow, iR);
+      const float sR = bound_scale((float)D * gm * kmax * fmaf((float)C * gmax * ascale, qmax, bS), kTopRow, iR);
       m->iR[ph][r] = iR;
       const u64 w1_2 = pack2(w1 * sR, w1 * sR), w2_2 = pack2(w2 * sR, w2 * sR);
       ok &= wait(bar(m->dp_full), ph, limit, gave_up);
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
         }
         uU = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float sU = bound_scale(uU, kTopRow - 2, iU);
+        const float sU = bound_scale(uU * gm, kTopRow - 2, iU);
         const u64 sU2 = pack2(sU, sU);
 #pragma unroll
         for (int h = 0; h < 4; h++) {
@@ -307,8 +308,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         tc::tmem_st_wait();
       }
-      const float w3 = iU * iR * iK, w4 = a.scale * ig * iQ;  // units of the two sums into A
-      bS = fmaf(all, bS, (float)C * fmaf(4.0f * uU * iR, kmax, gmax * qmax * ascale));
+      const float w3 = iU * iR * iK, w4 = a.scale * ig * iQ * gm;  // units of the two sums into A
+      bS = fmaf(all, bS, (float)C * gm * fmaf(4.0f * uU * iR, kmax, gmax * qmax * ascale));
       put_rows(bS);
       {
         const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(uU * iR));
@@ -477,11 +478,12 @@ __global__ void __launch_bounds__(384, 1)
       if (h == 0) m->ig[b] = ig;
       const float *nf = reinterpret_cast<const float *>(sm + AD_REC + (it % 3) * REC_PAD + REC_F);
       const float4 inv = *reinterpret_cast<const float4 *>(sm + AD_REC + (it % 3) * REC_PAD + REC_S);
+      const float f_unit = inv.w * reinterpret_cast<const float *>(sm + AD_REC + (it % 3) * REC_PAD + REC_S)[5];
       const u64 sk2 = pack2(inv.z, inv.z), sg2 = pack2(sg, sg);
       uint8_t *dst = sm + AD_TILE + b * TILE + tile_off(r0, c8, 128), *dg = sm + AD_G + b * ROWS64 + tile_off(r0, c8, C);
 #pragma unroll
       for (int k = 0; k < 8; k++) {
-        const float fq = -nf[r0 + 8 * k] * inv.w;
+        const float fq = -nf[r0 + 8 * k] * f_unit;
         *reinterpret_cast<uint4 *>(dst + 1024 * k) = to_half8(x[k], sk2);
         *reinterpret_cast<uint4 *>(dst + C * 128 + 1024 * k) = to_half8(y[k], pack2(fq, fq));
         *reinterpret_cast<uint4 *>(dg + 1024 * k) = to_half8(z[k], sg2);
@@ -543,7 +545,7 @@ constexpr int X_LD = 72;  // (rows of a fragment in different banks)
 constexpr uint32_t GR_X = GR_A5 + TILE, GR_MISC = GR_X + ((C * X_LD * 4 + 127) & ~127);
 constexpr int GR_WARPS = 16, GR_SEGS = 8;
 struct GradsMisc {
-  float l[C], nf[C], c[C], beta[C], gam[C], num[8];  // num: 1 / scale of K, Q, S0, u, A, du; scale of K, Q
+  float l[C], nf[C], c[C], beta[C], gam[C], num[12];  // num: 1 / scale of K, Q, S0, u, A, du; scale of K, Q; gm
   alignas(16) int z[C];
   float duv[C], dbeta[4][C], xin[4][2][C], xout[4][C];
   float head[GR_SEGS][C], pass[GR_SEGS], dgam[2][C];
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
                        : t < 6      ? (t == 2 ? so.iS : t == 3 ? so.iU : t == 4 ? ao.iS : ao.iU) + at
                                     : reinterpret_cast<const float *>(rec + REC_S) + t - 4;
     tok = 1.0f;
-    if (which < 3 || (which == 3 && t < n) || (which == 4 && t < 8)) tok = *src;
+    if (which < 3 || (which == 3 && t < n) || (which == 4 && t < 9)) tok = *src;
   };
   auto fetch_operands = [&](int at) {  // one thread
     tc::mbar_arrive_expect_tx(bl, 2 * TILE + 2 * ROWS64);
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
       const int t = tid & (C - 1), which = tid >> 6;
       if (which < 4) {
         (which == 0 ? m->nf : which == 1 ? m->c : which == 2 ? m->beta : m->gam)[t] = tok;
-      } else if (which == 4 && t < 8) {
+      } else if (which == 4 && t < 9) {
         m->num[t] = tok;
       }
     }
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     if (lane == 0) m->red[warp] = mg;
     if (tid == 0) tc::bulk_wait_read();  // the last chunk's dq and dk have left their place
     __syncthreads();
-    const float ik = m->num[0], iq = m->num[1], iS = m->num[2], iu = m->num[3], iA = m->num[4], idu = m->num[5];
+    const float ik = m->num[0], iq = m->num[1], iS = m->num[2], iu = m->num[3], iA = m->num[4], idu = m->num[5], gm = m->num[8];
     const float2 sk_sq = *reinterpret_cast<const float2 *>(m->num + 6);
 #pragma unroll
     for (int k = 0; k < 2; k++) {
@@ -782,14 +784,14 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     }
     const float mul = upper ? a.scale * ig * iu : idu * iu;
     // the operand's units: W alpha, V alpha sq / sk (= op_v), both below 2^15 (|g16| <= 2^3, |u16|, |du16| <= 2^15,
-    // 128 products, beta < 4, V + V^T); in dq's rows, where W stands alone, its own (V can be far larger).  sq / sk
-    // has no bound (2^61 for unit keys without queries), so V's units come from V alone: where they are the
+    // 128 products, decays up to gm, beta < 4, V + V^T); in dq's rows, where W stands alone, its own (V can be far
+    // larger).  sq / sk has no bound (2^61 for unit keys without queries), so V's units come from V alone: where they are the
     // smaller ones alpha = op_v sk / sq, which may be 0 (W^T Q is then nothing beside (V + V^T) K), and dk's unit
     // is 1 / (op_v sk), not 1 / (alpha sq).
     float ialpha_v, ialpha_q;
     const float vq = sk_sq.y * ik;  // sq / sk
-    const float alpha_v = bound_scale(8.0f * idu * iu * 137438953472.0f, kTopRow, ialpha_v);
-    const float alpha_q = bound_scale(fabsf(a.scale) * ig * iu * 33554432.0f, kTopRow, ialpha_q);
+    const float alpha_v = bound_scale(8.0f * gm * idu * iu * 137438953472.0f, kTopRow, ialpha_v);
+    const float alpha_q = bound_scale(fabsf(a.scale) * gm * ig * iu * 33554432.0f, kTopRow, ialpha_q);
     const bool of_v = alpha_q * vq > alpha_v;  // (2^77 2^126 at most: infinity is greater, too)
     const float alpha = of_v ? alpha_v * (iq * sk_sq.x) : alpha_q, op_v = of_v ? alpha_v : alpha_q * vq;
     if (next < chunks) fetch_qk(next);

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
   } else {
     if (tid == 0) *reinterpret_cast<float4 *>(inv) = make_float4(ik, iq, sk, sq);
     if (tid < C) s.beta[tid] = reinterpret_cast<float *>(rec + REC_B)[tid] = be;
-    if (warp == 3) factor_gates(s, g, nf, cc, lane);
+    if (warp == 3) factor_gates(s, g, nf, cc, inv + 4, lane);
     factor_clear(rec, tid);
     factor_clear(rec + SQ, tid);
     __syncthreads();
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
       m->grow[tid] = (grow <= 1.0f ? 0.0f : grow < INFINITY ? log2f(grow) + 0.003f : INFINITY) + fmaxf(up, 0.0f);
       m->give[tid] = fabsf(be) * sqrtf(kk) * 1.002f;
     }
-    factor_rows(s, tbase, ik * ik, rec + SQ, tid);
+    factor_rows(s, tbase, ik * ik, inv[5], rec + SQ, tid);
     tc::fence_before_sync();
     __syncthreads();
     if (bounds && warp == 3) {
@@ -462,11 +462,12 @@ __global__ void __launch_bounds__(384, 1)
       }
       ok &= wait(bar(m->rec_full[c % 3]), (c / 3) & 1, limit, gave_up);
       ok &= wait(bar(m->vt_full), ph, limit, gave_up);
-      const float iK = inv[0], kmax = (float)(1 << kTopTile) * iK, all = -nf[C - 1];  // all: the chunk's decay
+      // all: the chunk's decay; gm: no decay in it is greater
+      const float iK = inv[0], kmax = (float)(1 << kTopTile) * iK, all = -nf[C - 1], gm = inv[4];
       if constexpr (FWD) m->o1[ph][r] = -a.scale * iS * inv[1];
       const float w1 = iS * iK;  // units of D1
       float iR;
-      const float sR = bound_scale(fmaf((float)D * kmax, bS, m->vmax[warp]), BETA ? kTopRow - 2 : kTopRow, iR);  // (beta < 4)
+      const float sR = bound_scale(fmaf((float)D * kmax * gm, bS, m->vmax[warp]), BETA ? kTopRow - 2 : kTopRow, iR);  // (beta < 4)
       const u64 w1_2 = pack2(w1, w1), sR2 = pack2(sR, sR);
       const float *be = cc + C;
       if constexpr (KEEP) m->o1[ph][r] = iR;
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 3] = fmaxf(mx[(i >> 1) & 3], fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
         }
         uU = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        const float sU = bound_scale(uU, kTopRow, iU);
+        const float sU = bound_scale(uU * gm, kTopRow, iU);  // (c U, too)
         const u64 sU2 = pack2(sU, sU);
         float y[2][16];
         tc::tmem_ld16(tl + T_D2, y[0]);
@@ -552,10 +553,10 @@ __global__ void __launch_bounds__(384, 1)
         tc::tmem_st_wait();
       }
       const float w3 = iU * iR * iK;  // units of dS
-      // 64 products of |c u| <= |u| and |k| bound what is added to the state
-      bS = fmaf(all, bS, (float)C * uU * iR * kmax);
+      // 64 products of |c u| <= gm |u| and |k| bound what is added to the state
+      bS = fmaf(all, bS, (float)C * gm * uU * iR * kmax);
       if constexpr (FWD) {
-        m->o2[ph][r] = a.scale * w3 * inv[1];
+        m->o2[ph][r] = a.scale * w3 * gm * inv[1];
       } else if constexpr (KEEP) {
         put_rows(bS);
         const uint32_t w = __reduce_max_sync(0xffffffffu, __float_as_uint(uU * iR));

@@ -32,7 +32,8 @@ constexpr uint32_t TILE = 2 * C * D * 2;     // [128 x 128] operand: K rows, the
 constexpr uint32_t SQ = C * C * 2;           // [64 x 64] operand
 constexpr uint32_t ROWS64 = C * D * 2;       // 64 rows of bf16
 // A chunk's record: the factor T or T diag(beta) and P = Q K^T o D, swizzled K-major operands, then
-// minus f, c, beta, and {1 / scale of K, of Q, scale of K, of Q}.  REC_PAD: its place in shared memory.
+// minus f, c, beta, and {1 / scale of K, of Q, scale of K, of Q; a power of two that no decay in the chunk
+// exceeds (1 but for gates above one), 1 / it: P is times that}.  REC_PAD: its place in shared memory.
 constexpr uint32_t REC_P = SQ, REC_F = 2 * SQ, REC_C = REC_F + 4 * C, REC_B = REC_C + 4 * C, REC_S = REC_B + 4 * C,
                    REC = REC_S + 128, REC_PAD = 18 * 1024;
 static_assert(REC % 16 == 0 && REC <= REC_PAD, "records are bulk copied");
@@ -54,6 +55,7 @@ __device__ __forceinline__ float bound_scale(float bound, int top, float &inv) {
 }
 constexpr int kTopRow = 15;   // state rows, R and U rows: bound to 2^15
 constexpr float kLittle = -40.0f;  // log2 of what is left of a state at the end of a segment's tail
+constexpr float kMostGrowth = 8.0f;  // log2 of what a chunk's gates above one multiply to, at most
 constexpr int kTopTile = 3;   // K and Q tiles: 128 products of two stay below 2^13
 // Largest |x| of 2 x 16-bit bf16 words, as an integer (the order of positive floats is theirs).
 __device__ __forceinline__ uint32_t absmax_words(uint32_t m, uint4 x) {
@@ -116,13 +118,14 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned lim
 
 // Decays of a chunk's tokens in log2, with closed gates counted apart: the decay from token j
 // to token i >= j is 2^(l_i - l_j) if z_i = z_j, else 0.  Lane l of a whole warp handles
-// tokens 2l and 2l + 1 (gates past the end: 1).  Gates below e^-80 count as closed.
+// tokens 2l and 2l + 1 (gates past the end: 1).  Gates below e^-80 count as closed; a negative one has no
+// logarithm (NaN, and so is all that it decays).
 struct GatePair {
   float l0, l1;
   int z0, z1;
 };
 __device__ __forceinline__ GatePair gate_scan(float2 gamma, int lane) {
-  const bool sa = gamma.x < 1.8048514e-35f, sb = gamma.y < 1.8048514e-35f;
+  const bool sa = fabsf(gamma.x) < 1.8048514e-35f, sb = fabsf(gamma.y) < 1.8048514e-35f;
   const float a = sa ? 0.0f : log2f(gamma.x), b = sb ? 0.0f : log2f(gamma.y);
   float l = a + b;
   int z = (int)sa + (int)sb;
@@ -241,8 +244,22 @@ struct Factor {
   int z[C];
 };
 // Decays from the gates of one warp's scan: l, z, minus f (chunk start to token) and c (token to
-// end).
-__device__ __forceinline__ void factor_gates(Factor &s, const GatePair &g, float *nf, float *c, int lane) {
+// end); most[0] a power of two that none exceeds (all gates above one together; 64 gates of up to 2^0.001
+// stay inside the scales' factor of two), most[1] 1 / it.  The scales take it into account, up to 2^8: three
+// such bounds multiply in the backward's operands, whose fp16 range is 2^29 (growth of 2^8 in a chunk costs no
+// accuracy, 2^10 up to 2e-2 of a gradient).  What grows more has no decays: NaN, and is reported.
+__device__ __forceinline__ void factor_gates(Factor &s, GatePair g, float *nf, float *c, float *most, int lane) {
+  const float before = __shfl_up_sync(0xffffffffu, g.l1, 1), up0 = g.l0 - (lane > 0 ? before : 0.0f), up1 = g.l1 - g.l0;
+  const float up = (up0 > 0.001f ? up0 : 0.0f) + (up1 > 0.001f ? up1 : 0.0f);
+  int e = 0;
+  if (__any_sync(0xffffffffu, up > 0.0f)) {
+    const float all = warp_sum(up);
+    e = (int)ceilf(fminf(all, kMostGrowth));
+    if (!(all <= kMostGrowth)) g.l0 = g.l1 = NAN;
+  }
+  if (lane == 0)
+    *reinterpret_cast<float2 *>(most) =
+        make_float2(__uint_as_float((uint32_t)(127 + e) << 23), __uint_as_float((uint32_t)(127 - e) << 23));
   const float end = __shfl_sync(0xffffffffu, g.l1, 31);
   const int zend = __shfl_sync(0xffffffffu, g.z1, 31);
   *reinterpret_cast<float2 *>(&s.l[2 * lane]) = make_float2(g.l0, g.l1);
@@ -253,12 +270,12 @@ __device__ __forceinline__ void factor_gates(Factor &s, const GatePair &g, float
 }
 // Thread `tid` (warp w reads tensor-memory lanes 32 w ..): row tid of [K K^T; Q K^T] at tensor
 // memory `t`, in operand units (inv_kk: 1 / scale of K, squared).  Rows of A go to s, rows of P,
-// still in operand units, to the swizzled operand P.  Columns
+// still in operand units (times p_unit), to the swizzled operand P.  Columns
 // right of the diagonal's 32 are skipped.
-__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, uint8_t *P, int tid) {
+__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, float p_unit, uint8_t *P, int tid) {
   const int warp = tid >> 5, i = tid & 63;
   const bool isA = tid < C, low = i >= 32;  // (uniform in a warp)
-  const float li = s.l[i], mul = isA ? s.beta[i] * inv_kk : 1.0f;
+  const float li = s.l[i], mul = isA ? s.beta[i] * inv_kk : p_unit;
   const int zi = s.z[i], last = isA ? i - 1 : i;  // last column kept
   const bool cut = s.z[C - 1] != 0;                       // a closed gate in the chunk
   const uint32_t tl = t + ((uint32_t)(32 * warp) << 16);

@@ -98,3 +98,45 @@ def test_gradients_of_chunks_without_queries(what):
         for i in range(0, 150, 64):
             assert err(got[n][:, :, i:i + 64], want[n][:, :, i:i + 64]) <= TOL["bf16"], (n, i)
     assert err(got["dS0"], want["dS0"]) <= STATE_TOL["bf16"]
+
+
+@pytest.mark.parametrize("T", [16, 17, 64, 130, 300])
+@pytest.mark.parametrize("gates", [(1.0, 1.03), (1.03, 1.03), (1.0, 1.05), (0.9, 1.1), (1.09, 1.09)], ids=str)
+def test_gates_above_one(T, gates):
+    """A state that grows: the same on both sides of the 16 tokens from which chunks are taken."""
+    s = ref.rule_inputs(62, "bf16", 1, 2, 2, T, 128, 128, "open", True)
+    s["gamma"] = np.random.default_rng(63).uniform(*gates, s["gamma"].shape).astype(np.float32)
+    check_forward(s, "bf16")
+    check_backward(s, "bf16")
+
+
+@pytest.mark.parametrize("T", [16, 17, 64, 130, 300])
+def test_a_burst_of_gates_is_reported_by_the_chunked_form(T):
+    """1.5^24 = 2^14 in a chunk is more than its fp16 operands hold beside the decays: reported, not rounded
+    away.  (Up to 16 tokens the forward is a recurrence, which takes any gate.)"""
+    from mesa_layer_gb300 import binding
+    s = ref.rule_inputs(62, "bf16", 1, 2, 2, T, 128, 128, "open", True)
+    s["gamma"][:] = 1.5
+    s["gamma"][:, :, 24:] = 0.95
+    if T <= 16:
+        check_forward(s, "bf16")
+    else:
+        out, SF, status = forward(upload(s, "bf16"))
+        assert status == (binding.MESA_ERR_NONFINITE, 2)
+        assert not out.isfinite().any() and not SF.isfinite().any()
+    got, status = backward(upload(s, "bf16"))
+    assert status == (binding.MESA_ERR_NONFINITE, 2)
+    assert not got["dS0"].isfinite().any() and not got["dk"][:, :, :64].isfinite().any()
+
+
+def test_negative_gates_are_reported_by_the_chunked_form():
+    """Chunks take decays as logarithms: a gate below zero has none."""
+    t = upload(ref.rule_inputs(64, "bf16", 1, 2, 2, 100, 128, 128, "open", True), "bf16")
+    t["gamma"][0, 1, 70] = -0.5
+    from mesa_layer_gb300 import binding
+    out, _, status = forward(t)
+    assert status == (binding.MESA_ERR_NONFINITE, 2)
+    assert out[0, 0].isfinite().all() and not out[0, 1, 70:].isfinite().any()
+    got, status = backward(t)
+    assert status == (binding.MESA_ERR_NONFINITE, 2)
+    assert got["dv"][0, 0].isfinite().all()
