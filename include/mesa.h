@@ -311,8 +311,9 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
  * dgamma, dbeta [B, H, T]: all of dtype -- the gates' gradients come from the same products as
  * the others and carry no more digits.  dS0: NULL or [B, H, dv, dk] fp32, dL/dS0
  * (it may be dS_final's memory).  The states are recomputed; every sum has a fixed order.  S0 as given to the forward.
- * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward; on the
- * tensor cores |beta| < 4 (a larger one can overflow an operand: MESA_ERR_NONFINITE).
+ * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward
+ * (MESA_ERR_NONFINITE: a gradient other than dS0 is not finite); on the tensor cores |beta| < 4 (a
+ * larger one can overflow an operand: MESA_ERR_NONFINITE).
  */
 size_t mesa_delta_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,

@@ -34,6 +34,10 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ float nonfinite4(const float4 &x, float bad) {  // NaN once one of them was not finite
+  return fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, fmaf(x.w, 0.0f, bad))));
+}
+
 enum ScanMode { kForward = 0, kStates = 1, kAdjoint = 2, kSegment = 3, kSegAdjoint = 4 };
 constexpr int TB = 16;    // tokens staged at a time
 constexpr int ROWS = 32;  // state rows per CTA
@@ -405,6 +409,7 @@ __global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBw
     *reinterpret_cast<float4 *>(K + t * kp + d) = in ? load4((const TIO *)a.k, qk0 + i) : make_float4(0, 0, 0, 0);
     *reinterpret_cast<float4 *>(Q + t * kp + d) = in ? load4((const TIO *)a.q, qk0 + i) : make_float4(0, 0, 0, 0);
   }
+  float bad = 0.0f;  // NaN once a gradient was not finite
   // tokens' rows; dv and dbeta on the way (a warp per token)
   for (int t = warp; t < C; t += 8) {
     float db_sum = 0.0f;
@@ -416,6 +421,7 @@ __global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBw
         e = ws.e[at];
         du = ws.du[at];
         st((TIO *)a.dv_out, at, bet[t] * du);
+        bad = fmaf(bet[t] * du, 0.0f, bad);
       }
       db_sum = fmaf(du, e, db_sum);
       G[t * vp + d] = a.scale * g;
@@ -423,6 +429,7 @@ __global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBw
       Db[t * vp + d] = bet[t] * du;
     }
     db_sum = warp_sum(db_sum);
+    bad = fmaf(db_sum, 0.0f, bad);
     if (lane == 0 && t < n) st((TIO *)a.dbeta, tu + t, db_sum);
   }
   // decays: D[i][j] = gamma_{j+1} .. gamma_i (j <= i), from0[i] = gamma_0 .. gamma_i
@@ -526,6 +533,7 @@ __global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBw
         axpy(-(V[t * P + s] + V[s * P + t]), ks, dk);
       }
       if (t < n) {
+        bad = nonfinite4(dq, nonfinite4(dk, bad));
         if (ws.dqp) {
           const size_t at = (tu + t) * DK + 4 * cg;
           *reinterpret_cast<float4 *>(ws.dqp + at) = dq;
@@ -557,9 +565,11 @@ __global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBw
     float col = 0.0f;  // sum over i >= t of D[i][t] X[i][lane]
     for (int i = t; i < C; i++) col = fmaf(D[i * P + t], X[i * P + lane], col);
     float s = (lane < t ? dprev * (col + toC * xout[lane]) : 0.0f) + prev0 * (D[lane * P + t] * xin[lane]);
-    s = warp_sum(s);
-    if (lane == 0) st((TIO *)a.dgamma, tu + t, fmaf(toC * prev0, cross, s));
+    s = fmaf(toC * prev0, cross, warp_sum(s));
+    bad = fmaf(s, 0.0f, bad);
+    if (lane == 0) st((TIO *)a.dgamma, tu + t, s);
   }
+  if (!(bad == 0.0f)) atomicOr(a.status, tc_err_nonfinite());
 }
 
 // The sums over the value heads of a key head, in a fixed order (memory).
@@ -567,6 +577,7 @@ template <typename TIO>
 __global__ void __launch_bounds__(256) mesa_rule_group_sum_kernel(RuleArgs a, const float *dqp, const float *dkp) {
   const size_t per = (size_t)a.T * a.dk, total = (size_t)a.B * a.Hk * per;
   const int group = a.H / a.Hk;
+  float bad = 0.0f;  // NaN once a sum was not finite
   for (size_t i = 4 * ((size_t)blockIdx.x * 256 + threadIdx.x); i < total; i += (size_t)gridDim.x * 1024) {
     const size_t uk = i / per, at = i % per, b = uk / a.Hk, hk = uk % a.Hk;
     float4 q = make_float4(0, 0, 0, 0), k = q;
@@ -585,7 +596,9 @@ __global__ void __launch_bounds__(256) mesa_rule_group_sum_kernel(RuleArgs a, co
     st(dk, 1, k.y);
     st(dk, 2, k.z);
     st(dk, 3, k.w);
+    bad = nonfinite4(q, nonfinite4(k, bad));
   }
+  if (!(bad == 0.0f)) atomicOr(a.status, tc_err_nonfinite());
 }
 
 // One decode step.  A lane holds 16 values of a row (float4 groups DK/16 lanes apart, so that

@@ -140,3 +140,47 @@ def test_negative_gates_are_reported_by_the_chunked_form():
     got, status = backward(t)
     assert status == (binding.MESA_ERR_NONFINITE, 2)
     assert got["dv"][0, 0].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype,dk,dv,Hk,T", [("f32", 64, 64, 2, 70), ("f32", 16, 32, 1, 200), ("bf16", 64, 64, 1, 90),
+                                              ("bf16", 32, 128, 2, 5), ("f32", 32, 16, 1, 900), ("bf16", 128, 128, 2, 70)],
+                         ids=str)
+@pytest.mark.parametrize("what", ["dout", "beta", "dS_final", "overflow"])
+def test_nonfinite_gradients_are_reported(dtype, dk, dv, Hk, T, what):
+    from mesa_layer_gb300 import binding
+    t = upload(ref.rule_inputs(65, dtype, 1, 2, Hk, T, dk, dv, "open", True), dtype)
+    assert backward(t)[1] == (binding.MESA_OK, 0)
+    if what == "dout":
+        t["dout"][0, 1, T // 2, 3] = float("nan")
+    elif what == "beta":
+        t["beta"][0, 1, T // 2] = float("inf")
+    elif what == "dS_final":
+        t["dS_final"][0, 1, 5, 7] = float("nan")
+    else:  # finite inputs, a sum that is not
+        t["dS_final"][0, 1] = 3e38
+    got, status = backward(t)
+    assert status == (binding.MESA_ERR_NONFINITE, 2)
+    assert got["dv"][0, 0].isfinite().all() and not got["dv"][0, 1].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_whose_sum_over_heads_overflows_are_reported(dtype):
+    """Two value heads share a key head; each part of dq is below the largest fp32 value, their sum is not."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    td = torch.float32 if dtype == "f32" else torch.bfloat16
+    t = {n: torch.zeros(1, h, 1, 32, device="cuda", dtype=td) for n, h in (("q", 1), ("k", 1), ("v", 2), ("dout", 2))}
+    t["k"][..., 0] = 1.0  # S = v k^T, dq = S^T dout = k (v . dout)
+    t["v"][..., 0] = 2.0 ** 63
+    t["dout"][..., 0] = 2.0 ** 64
+    t.update(gamma=torch.ones(1, 2, 1, device="cuda"), beta=torch.ones(1, 2, 1, device="cuda"), S0=None, dS_final=None)
+    ws = torch.empty(binding.mesa_delta_backward_workspace_size(*sizes(t)), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        dq = binding.mesa_delta_backward_chunked(t["q"], t["k"], t["v"], t["gamma"], t["beta"], t["dout"], workspace=ws)[0]
+        status = binding.mesa_forward_status_code(ws)
+        if t["v"][0, 1, 0, 0] == 0:
+            break
+        assert status == (binding.MESA_ERR_NONFINITE, 2) and dq[0, 0, 0, 0].isinf()
+        t["v"][0, 1] = 0.0
+    assert status == (binding.MESA_OK, 0) and dq[0, 0, 0, 0] == 2.0 ** 127
