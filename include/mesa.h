@@ -327,7 +327,7 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
  * One recurrent step of the gated delta rule for N sequences x H heads, in place on the caller's
  * fp32 states S_state [N, H, dv, dk] (16-byte aligned).  q, k [N, Hk, dk], v, out [N, H, dv]
  * dtype (q, k 16-byte aligned); gamma, beta [N, H] fp32.  Sizes and errors as the forward, with
- * any N * H.
+ * any N * H; a non-finite out is reported through mesa_decode_status.
  */
 int mesa_delta_step(int N, int H, int Hk, int dk, int dv, int dtype, float *S_state, const void *q,
                     const void *k, const void *v, const float *gamma, const float *beta, float scale,
@@ -387,8 +387,8 @@ int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void 
 int mesa_forward_status(const void *workspace, cudaStream_t stream, unsigned *flags);
 
 /*
- * Device status word of the decode steps (mesa_decode_step, mesa_decode_step_warm) on the
- * current device -- one word per device, shared by every decode call on it: copies it to
+ * Device status word of the decode steps (mesa_decode_step, mesa_decode_step_warm,
+ * mesa_delta_step) on the current device -- one word per device, shared by every decode call on it: copies it to
  * *flags (host), clears it, both on `stream`, and synchronises `stream`.  Bit 0 (1): a
  * bounded wait for the bulk copy of a unit's H or G gave up (dk = 128; see mesa_decode_step);
  * bit 2 (4): the wait for that copy to land expired too; bit 1 (2): a decode step wrote

@@ -185,7 +185,8 @@ int mesa_delta_step(int N, int H, int Hk, int dk, int dv, int dtype, float *S_st
   if ((size_t)N * H > 0x7fffffff) return MESA_ERR_UNSUPPORTED;
   if (!S_state || !q || !k || !v || !gamma || !beta || !out) return MESA_ERR_INVALID_ARG;
   if (!all_aligned16(S_state, q, k)) return MESA_ERR_INVALID_ARG;
-  mesa::RuleStepArgs a{N, H, Hk, dk, dv, dtype, S_state, q, k, v, gamma, beta, scale, out};
+  mesa::RuleStepArgs a{N, H, Hk, dk, dv, dtype, S_state, q, k, v, gamma, beta, scale, out, mesa::decode_status_word()};
+  if (!a.status) return MESA_ERR_CUDA;
   return mesa::launch_rule_step(a, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
 }
 

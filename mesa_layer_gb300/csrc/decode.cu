@@ -16,7 +16,7 @@
 
 namespace mesa {
 // Status word of the decode kernels on this device (each device that loads the library has
-// its own copy): bit tc_err_nonfinite() when a decode step wrote a non-finite output.  Read
+// its own copy): bit tc_err_nonfinite() when a decode step (of the delta rule, too) wrote a non-finite output.  Read
 // and cleared by decode_status (mesa_decode_status).
 __device__ unsigned g_decode_status = 0;
 }  // namespace mesa
@@ -409,6 +409,11 @@ static int launch_dec_t(const DecArgs &a, cudaStream_t st) {
   }
   timing_mark_end(K_DECODE, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+unsigned *decode_status_word() {
+  void *p = nullptr;
+  return cudaGetSymbolAddress(&p, g_decode_status) == cudaSuccess ? (unsigned *)p : nullptr;
 }
 
 int decode_status(cudaStream_t st, unsigned *flags) {

@@ -650,8 +650,11 @@ __global__ void __launch_bounds__(128) mesa_rule_step_kernel(RuleStepArgs a) {
       s[p][i].w = fmaf(g, s[p][i].w, uu * k[i].w);
       if (row < a.dv) dst[j + LPR * i] = s[p][i];
     }
-    const float o = dot(s[p], q);
-    if (row < a.dv && j == 0) st((TIO *)a.out, (size_t)u * a.dv + row, a.scale * o);
+    const float o = a.scale * dot(s[p], q);
+    if (row < a.dv && j == 0) {
+      st((TIO *)a.out, (size_t)u * a.dv + row, o);
+      if (!isfinite(o)) atomicOr(a.status, tc_err_nonfinite());
+    }
   }
 }
 

@@ -51,6 +51,7 @@ struct RuleStepArgs {
   const float *gamma, *beta;
   float scale;
   void *out;
+  unsigned *status;  // the device's status word of the decode steps
 };
 
 // Each returns 0 when every launch was enqueued, -1 otherwise.

@@ -59,6 +59,7 @@ struct DecArgs {
 // it): `flags` receives it and it is cleared, both ordered on `st`, which is then
 // synchronised.  Returns 0, or -1 when a copy failed.
 int decode_status(cudaStream_t st, unsigned *flags);
+unsigned *decode_status_word();  // that word on the current device, nullptr when it cannot be had
 
 // Backward pass (chunks of kBwdChunk tokens; the states, log-decays and solves come from the
 // forward pipeline run at that chunk length).

@@ -184,3 +184,20 @@ def test_gradients_whose_sum_over_heads_overflows_are_reported(dtype):
         assert status == (binding.MESA_ERR_NONFINITE, 2) and dq[0, 0, 0, 0].isinf()
         t["v"][0, 1] = 0.0
     assert status == (binding.MESA_OK, 0) and dq[0, 0, 0, 0] == 2.0 ** 127
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128), ("bf16", 16)])
+def test_a_step_reports_its_nonfinite_outputs(dtype, d):
+    from mesa_layer_gb300 import binding
+    t = upload(ref.rule_inputs(66, dtype, 3, 2, 1, 1, d, d, "open", True), dtype)
+    args = [t[n][:, :, 0].contiguous() for n in ("q", "k", "v", "gamma", "beta")]
+    binding.mesa_decode_status()  # clear
+    clean = binding.mesa_delta_step(t["S0"].clone(), *args)
+    assert binding.mesa_decode_status() == (binding.MESA_OK, 0)
+    args[2][1, 0, 3] = float("inf")
+    out = binding.mesa_delta_step(t["S0"].clone(), *args)
+    assert binding.mesa_decode_status() == (binding.MESA_ERR_NONFINITE, 2)
+    assert not out[1, 0, 3].isfinite()
+    out[1, 0, 3] = clean[1, 0, 3]
+    assert out.equal(clean)
+    assert binding.mesa_decode_status() == (binding.MESA_OK, 0)
