@@ -415,21 +415,28 @@ def _raw_stream(stream, device):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _new(shape, dtype, device, stream):
-    """An output or scratch tensor for work on `stream`: when that is not the current stream, the
-    allocator is told, so that the memory is not handed out again before that work is done."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.numel():
-        t.record_stream(stream)
+def _for_stream(stream, make):
+    """make() for work on `stream`.  The allocator hands a freed block out again in the order of the
+    stream that it was allocated on: one of the current stream's may still be in use by work queued
+    there, so the memory is taken from `stream`'s own.  The caller may go on to use it on the current
+    stream, so that is noted, too.  (The tensors that the caller gives are the caller's to order.)"""
+    with torch.cuda.stream(stream):
+        t = make()
+    if t.numel():
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
+
+
+def _new(shape, dtype, device, stream):
+    """An output or scratch tensor for work on `stream` (None: the current one)."""
+    if stream is not None:
+        return _for_stream(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _like(like, stream):
     """_new of the shape and type of `like` (a shorter way through the allocator)."""
-    t = torch.empty_like(like)
-    if stream is not None and t.numel():
-        t.record_stream(stream)
-    return t
+    return torch.empty_like(like) if stream is None else _for_stream(stream, lambda: torch.empty_like(like))
 
 
 def _workspace(workspace, nbytes, device, stream):

@@ -201,3 +201,38 @@ def test_a_step_reports_its_nonfinite_outputs(dtype, d):
     out[1, 0, 3] = clean[1, 0, 3]
     assert out.equal(clean)
     assert binding.mesa_decode_status() == (binding.MESA_OK, 0)
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 32), ("bf16", 128)])
+def test_another_stream_leaves_freed_blocks_of_this_one_alone(dtype, d):
+    """Blocks of the outputs' sizes freed here while work that writes them is still queued: a call on
+    another stream in the meantime takes other memory."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    t = upload(ref.rule_inputs(75, dtype, 1, 4, 2, 300, d, d, "open"), dtype)
+    args = [t[n] for n in ("q", "k", "v", "gamma", "beta")]
+    y, w = t["v"].reshape(-1, d), torch.ones(d, device="cuda")
+
+    def calls(stream=None):
+        return [binding.mesa_delta_forward_chunked(*args, stream=stream),
+                *binding.mesa_delta_backward_chunked(*args, t["dout"], stream=stream),
+                *binding.mesa_block_norm(y, y, w_post=w, w_pre=w, stream=stream),
+                *(x for x in binding.mesa_block_norm_backward(y, y, y, dh=y, w_post=w, w_pre=w, stream=stream)
+                  if x is not None)]
+
+    want = calls()
+    blocks = [x.nbytes for x in want] + [binding.mesa_delta_workspace_size(*sizes(t)),
+                                         binding.mesa_delta_backward_workspace_size(*sizes(t))]
+    a = torch.ones(4096, 4096, device="cuda", dtype=torch.bfloat16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(100):  # milliseconds of work
+        b = a @ a
+    for n in 2 * blocks:
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)  # freed at once, written later
+    got = calls(side)
+    busy = not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert busy  # (else it showed nothing)
+    assert all(x.equal(z) for x, z in zip(got, want))
