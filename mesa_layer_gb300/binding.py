@@ -158,14 +158,14 @@ def mesa_forward_chunked(q, k, v, gamma, lambda_diag, cg_iters, cg_tol, chunk, o
     for name, t in (("H0", H0), ("G0", G0), ("H_final", H_final), ("G_final", G_final)):
         _require(t, name, torch.float32)
     if out is None:
-        out = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
+        out = _new((B, H, T, dv), q.dtype, q.device, stream)
     if iters_used is None:
-        iters_used = torch.empty((B, H, T), dtype=torch.int32, device=q.device)
+        iters_used = _new((B, H, T), torch.int32, q.device, stream)
     _require(out, "out", q.dtype)
     _require(iters_used, "iters_used", torch.int32)
     need = mesa_forward_workspace_size(B, H, T, dk, dv, chunk)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 256), torch.uint8, q.device, stream)
     _require(workspace, "workspace")
     st = lib.mesa_forward_chunked(B, H, T, dk, dv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
                                   _ptr(lambda_diag), int(cg_iters), float(cg_tol), int(chunk),
@@ -196,14 +196,14 @@ def mesa_forward_chunked_pre(q_raw, k_raw, wq, wk, v, gamma, lambda_diag, cg_ite
     if tuple(wk.shape) != tuple(wq.shape):
         raise MesaError("wq and wk must have the same shape [H, dk, W]")
     if out is None:
-        out = torch.empty((B, H, T, dv), dtype=q_raw.dtype, device=q_raw.device)
+        out = _new((B, H, T, dv), q_raw.dtype, q_raw.device, stream)
     if iters_used is None:
-        iters_used = torch.empty((B, H, T), dtype=torch.int32, device=q_raw.device)
+        iters_used = _new((B, H, T), torch.int32, q_raw.device, stream)
     _require(out, "out", q_raw.dtype)
     _require(iters_used, "iters_used", torch.int32)
     need = mesa_forward_pre_workspace_size(B, H, T, dk, dv, chunk, code)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q_raw.device)
+        workspace = _new(max(need, 256), torch.uint8, q_raw.device, stream)
     _require(workspace, "workspace")
     st = lib.mesa_forward_chunked_pre(B, H, T, dk, dv, code, _ptr(q_raw), _ptr(k_raw), _ptr(wq), _ptr(wk), int(W),
                                       _ptr(v), _ptr(gamma), _ptr(lambda_diag), int(cg_iters), float(cg_tol),
@@ -229,15 +229,15 @@ def mesa_forward_chunked_save(q, k, v, gamma, lambda_diag, cg_iters, cg_tol, chu
         _require(t, name, q.dtype)
     _require(gamma, "gamma", torch.float32)
     _require(lambda_diag, "lambda_diag", torch.float32)
-    out = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device) if out is None else out
-    iters_used = torch.empty((B, H, T), dtype=torch.int32, device=q.device) if iters_used is None else iters_used
-    x_saved = torch.empty((B, H, T, dk), dtype=torch.float32, device=q.device) if x_saved is None else x_saved
+    out = _new((B, H, T, dv), q.dtype, q.device, stream) if out is None else out
+    iters_used = _new((B, H, T), torch.int32, q.device, stream) if iters_used is None else iters_used
+    x_saved = _new((B, H, T, dk), torch.float32, q.device, stream) if x_saved is None else x_saved
     _require(out, "out", q.dtype)
     _require(iters_used, "iters_used", torch.int32)
     _require(x_saved, "x_saved", torch.float32)
     need = mesa_forward_workspace_size(B, H, T, dk, dv, chunk)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 256), torch.uint8, q.device, stream)
     _require(workspace, "workspace")
     st = lib.mesa_forward_chunked_save(B, H, T, dk, dv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
                                        _ptr(lambda_diag), int(cg_iters), float(cg_tol), int(chunk), _ptr(out),
@@ -264,13 +264,13 @@ def mesa_backward_chunked(q, k, v, gamma, lambda_diag, dout, cg_iters, cg_tol, d
     _require(gamma, "gamma", torch.float32)
     _require(lambda_diag, "lambda_diag", torch.float32)
     dev = q.device
-    dq = torch.empty((B, H, T, dkk), dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.empty((B, H, T, dkk), dtype=q.dtype, device=dev) if dk is None else dk
-    dv = torch.empty((B, H, T, dvv), dtype=q.dtype, device=dev) if dv is None else dv
-    dgamma = torch.empty((B, H, T), dtype=torch.float32, device=dev) if dgamma is None else dgamma
-    dlambda = torch.empty((H, dkk), dtype=torch.float32, device=dev) if dlambda is None else dlambda
-    iters_fwd = torch.empty((B, H, T), dtype=torch.int32, device=dev) if iters_fwd is None else iters_fwd
-    iters_bwd = torch.empty((B, H, T), dtype=torch.int32, device=dev) if iters_bwd is None else iters_bwd
+    dq = _new((B, H, T, dkk), q.dtype, dev, stream) if dq is None else dq
+    dk = _new((B, H, T, dkk), q.dtype, dev, stream) if dk is None else dk
+    dv = _new((B, H, T, dvv), q.dtype, dev, stream) if dv is None else dv
+    dgamma = _new((B, H, T), torch.float32, dev, stream) if dgamma is None else dgamma
+    dlambda = _new((H, dkk), torch.float32, dev, stream) if dlambda is None else dlambda
+    iters_fwd = _new((B, H, T), torch.int32, dev, stream) if iters_fwd is None else iters_fwd
+    iters_bwd = _new((B, H, T), torch.int32, dev, stream) if iters_bwd is None else iters_bwd
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _require(t, name, q.dtype)
     for name, t in (("dgamma", dgamma), ("dlambda", dlambda)):
@@ -280,7 +280,7 @@ def mesa_backward_chunked(q, k, v, gamma, lambda_diag, dout, cg_iters, cg_tol, d
     _require(x_saved, "x_saved", torch.float32)
     need = mesa_backward_workspace_size(B, H, T, dkk, dvv)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _new(max(need, 256), torch.uint8, dev, stream)
     _require(workspace, "workspace")
     st = lib.mesa_backward_chunked(B, H, T, dkk, dvv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
                                    _ptr(lambda_diag), _ptr(dout), _ptr(x_saved), int(cg_iters), float(cg_tol), _ptr(dq),
@@ -305,9 +305,9 @@ def mesa_decode_step(H_state, G_state, q, k, v, gamma, lambda_diag, cg_iters, cg
     _require(gamma, "gamma", torch.float32)
     _require(lambda_diag, "lambda_diag", torch.float32)
     if out is None:
-        out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        out = _new((N, H, dv), q.dtype, q.device, stream)
     if iters_used is None:
-        iters_used = torch.empty((N, H), dtype=torch.int32, device=q.device)
+        iters_used = _new((N, H), torch.int32, q.device, stream)
     st = lib.mesa_decode_step(N, H, dk, dv, code, _ptr(H_state), _ptr(G_state), _ptr(q), _ptr(k),
                               _ptr(v), _ptr(gamma), _ptr(lambda_diag), int(cg_iters), float(cg_tol),
                               _ptr(out), _ptr(iters_used), _stream(stream))
@@ -328,9 +328,9 @@ def mesa_qk_preprocess(q_raw, k_raw, wq, wk, q_out=None, k_out=None, stream=None
     _require(wq, "wq", torch.float32)
     _require(wk, "wk", torch.float32)
     if q_out is None:
-        q_out = torch.empty_like(q_raw)
+        q_out = _like(q_raw, stream)
     if k_out is None:
-        k_out = torch.empty_like(k_raw)
+        k_out = _like(k_raw, stream)
     st = lib.mesa_qk_preprocess(B, H, T, d, W, code, _ptr(q_raw), _ptr(k_raw), _ptr(wq), _ptr(wk),
                                 _ptr(q_out), _ptr(k_out), _stream(stream))
     _check(st, "mesa_qk_preprocess")
@@ -350,9 +350,9 @@ def mesa_qk_preprocess_step(q_raw, k_raw, wq, wk, conv_state, q_out=None, k_out=
     _require(wk, "wk", torch.float32)
     _require(conv_state, "conv_state", torch.float32)
     if q_out is None:
-        q_out = torch.empty_like(q_raw)
+        q_out = _like(q_raw, stream)
     if k_out is None:
-        k_out = torch.empty_like(k_raw)
+        k_out = _like(k_raw, stream)
     st = lib.mesa_qk_preprocess_step(N, H, d, W, code, _ptr(q_raw), _ptr(k_raw), _ptr(wq), _ptr(wk),
                                      _ptr(conv_state), _ptr(q_out), _ptr(k_out), _stream(stream))
     _check(st, "mesa_qk_preprocess_step")
@@ -373,9 +373,9 @@ def mesa_decode_step_warm(H_state, G_state, X_state, q, k, v, gamma, lambda_diag
                     ("lambda_diag", lambda_diag)):
         _require(t, name, torch.float32)
     if out is None:
-        out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        out = _new((N, H, dv), q.dtype, q.device, stream)
     if iters_used is None:
-        iters_used = torch.empty((N, H), dtype=torch.int32, device=q.device)
+        iters_used = _new((N, H), torch.int32, q.device, stream)
     st = lib.mesa_decode_step_warm(N, H, dk, dv, code, _ptr(H_state), _ptr(G_state), _ptr(X_state), _ptr(q),
                                    _ptr(k), _ptr(v), _ptr(gamma), _ptr(lambda_diag), int(cg_iters), float(cg_tol),
                                    _ptr(out), _ptr(iters_used), _stream(stream))
@@ -640,10 +640,13 @@ def mesa_tc_selftest(A, B, stream=None):
     lib = load()
     _require(A, "A", torch.float32)
     _require(B, "B", torch.float32)
-    C1 = torch.empty(128, 128, device=A.device)
-    C2 = torch.empty(128, 128, device=A.device)
-    C3 = torch.empty(128, 128, device=A.device)
-    status = torch.zeros(1, dtype=torch.int32, device=A.device)
+    C1 = _new((128, 128), torch.float32, A.device, stream)
+    C2 = _new((128, 128), torch.float32, A.device, stream)
+    C3 = _new((128, 128), torch.float32, A.device, stream)
+    def zero():
+        return torch.zeros(1, dtype=torch.int32, device=A.device)
+
+    status = zero() if stream is None else _for_stream(stream, zero)
     _check(lib.mesa_tc_selftest(_ptr(A), _ptr(B), _ptr(C1), _ptr(C2), _ptr(C3), _ptr(status),
                                 _stream(stream)), "mesa_tc_selftest")
     return C1, C2, C3, status
@@ -665,9 +668,9 @@ def mesa_forward_chunked_noalloc(q, k, v, gamma, lambda_diag, cg_iters, cg_tol, 
     _require(gamma, "gamma", torch.float32)
     _require(lambda_diag, "lambda_diag", torch.float32)
     if out is None:
-        out = torch.empty((B, H, T, dv), dtype=q.dtype, device=q.device)
+        out = _new((B, H, T, dv), q.dtype, q.device, stream)
     if iters_used is None:
-        iters_used = torch.empty((B, H, T), dtype=torch.int32, device=q.device)
+        iters_used = _new((B, H, T), torch.int32, q.device, stream)
     st = lib.mesa_forward_chunked_noalloc(B, H, T, dk, dv, code, _ptr(q), _ptr(k), _ptr(v), _ptr(gamma),
                                           _ptr(lambda_diag), int(cg_iters), float(cg_tol), int(chunk),
                                           _ptr(out), _ptr(iters_used), _stream(stream))
