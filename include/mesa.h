@@ -288,11 +288,17 @@ int mesa_forward_chunked_noalloc(int B, int H, int T, int dk, int dv, int dtype,
  * workspace: at least mesa_delta_workspace_size() bytes, 256-byte aligned; its first word is the
  * status word read by mesa_forward_status (MESA_ERR_NONFINITE: a non-finite out).  Any chunk
  * length gives the same result up to rounding; the library picks its own.
- * Arithmetic: sums, states and gates in fp32.  bf16 with dk = dv = 128 runs on the tensor cores with
- * fp16 operands scaled by powers of two (each rounded to 2^-12 of its row's largest element, S_final
- * with them); there the products of a 64-token chunk want |beta| |k|^2 of order one.  Everything
- * else is a token recurrence in fp32.  Long sequences of few (batch, head) units are cut into
- * segments that run side by side.
+ * Arithmetic: sums, states and gates in fp32.  bf16 with dk = dv = 128 and T > 16 runs on the tensor
+ * cores in chunks of 64 tokens, with fp16 operands scaled by powers of two, each value rounded once to
+ * 2^-12 of itself or, far below the largest of its scale, to 2^-40 of that.  Scales: a chunk's q and k (bf16:
+ * exact but for elements 2^16 below the chunk's largest); rows of the state and of what is written
+ * (S_final carries these roundings); in the backward a chunk's state, adjoint, u and du.  There
+ * |beta| |k|^2 has to be of order one, and where keys are alike the outputs are small sums of large rounded
+ * terms: the relative error of out (bf16's own rounding is 1.7e-3) is 1.7e-3 for independent keys, 2.5e-3 at
+ * a cosine of 0.9 between all keys and queries with beta < 1, 5e-3 with beta in 1..2 (of S_final 4e-4, 8e-4,
+ * 1.7e-3; of a gradient at most 2e-3, 2.4e-3, 6e-3).  fp32 calls keep 1e-5 throughout: they, and
+ * everything else, are a token recurrence in fp32.  Long sequences of few (batch, head) units are cut
+ * into segments that run side by side.
  */
 size_t mesa_delta_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,

@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
     if (tid == 0) *reinterpret_cast<float4 *>(inv) = make_float4(ik, iq, sk, sq);
     if (tid < C) s.beta[tid] = reinterpret_cast<float *>(rec + REC_B)[tid] = be;
     if (warp == 3) factor_gates(s, g, nf, cc, inv + 4, lane);
-    factor_clear(rec, tid);
     factor_clear(rec + SQ, tid);
     __syncthreads();
     if (bounds && tid < C) {  // (the diagonal of K K^T: column i of row i)
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
       m->grow[tid] = (grow <= 1.0f ? 0.0f : grow < INFINITY ? log2f(grow) + 0.003f : INFINITY) + fmaxf(up, 0.0f);
       m->give[tid] = fabsf(be) * sqrtf(kk) * 1.002f;
     }
-    factor_rows(s, tbase, ik * ik, inv[5], rec + SQ, tid);
+    factor_rows(s, tbase, ik * ik, inv[5], rec, rec + SQ, tid);
     tc::fence_before_sync();
     __syncthreads();
     if (bounds && warp == 3) {
@@ -194,6 +193,8 @@ __global__ void __launch_bounds__(128, 6) mesa_rule_prep_kernel(RuleArgs a, uint
     factor_diagonal<WITH_BETA>(s, rec, warp, lane);
     __syncthreads();
     if (warp < 3) factor_columns<WITH_BETA>(s, rec, warp, lane);
+    __syncthreads();
+    factor_clear_upper(rec, tid);
     tc::fence_smem_to_async();
     __syncthreads();
     if (tid == 0) {

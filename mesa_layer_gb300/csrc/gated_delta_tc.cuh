@@ -15,7 +15,9 @@
 // element: fp16 covers 2^29 in full precision, so a bound 2^15 above the values costs nothing.
 // The state itself stays fp32 in registers, so a chunk's operand rounding enters the next
 // one only through u.  The inverse is formed in fp32 (diagonal blocks) and from fp16 blocks with
-// fp32 sums (the rest).
+// fp32 sums (the rest), A's blocks as two fp16 values each: where keys are alike the inverse is a small sum of
+// large products of A's entries (keys of cosine 0.9, beta 1 to 2: rounded once they cost T 2.4e-3, so 5e-4; its
+// other roundings cost 2e-4).
 #pragma once
 
 #include "common.cuh"
@@ -236,7 +238,7 @@ __device__ __forceinline__ void tensor_s2g_3d(const void *map, uint32_t src, int
 
 // ---- the factors of a chunk, by 128 threads ------------------------------------------------------
 struct Factor {
-  __half Ah[C - 16][56]; // A's blocks below the diagonal, fp16 (from row 16 on)
+  __half Ah[C - 16][56]; // A's blocks below the diagonal, fp16 (from row 16 on; the rest of it: factor_rows)
   float Ad[C][20];       // its diagonal 16 x 16 blocks: row i, columns of block i / 16
   __half Tb[4][16][24];  // inverses of the diagonal blocks of I + A, and their transposes
   __half Yb[4][16][24];
@@ -269,10 +271,11 @@ __device__ __forceinline__ void factor_gates(Factor &s, GatePair g, float *nf, f
       make_float2(g.z0 == zend ? ex2(end - g.l0) : 0.0f, g.z1 == zend ? ex2(end - g.l1) : 0.0f);
 }
 // Thread `tid` (warp w reads tensor-memory lanes 32 w ..): row tid of [K K^T; Q K^T] at tensor
-// memory `t`, in operand units (inv_kk: 1 / scale of K, squared).  Rows of A go to s, rows of P,
+// memory `t`, in operand units (inv_kk: 1 / scale of K, squared).  Rows of A go to s, what their fp16 values
+// leave of block (b, k) to block (k, b) of M, which is not used yet; rows of P,
 // still in operand units (times p_unit), to the swizzled operand P.  Columns
 // right of the diagonal's 32 are skipped.
-__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, float p_unit, uint8_t *P, int tid) {
+__device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk, float p_unit, uint8_t *M, uint8_t *P, int tid) {
   const int warp = tid >> 5, i = tid & 63;
   const bool isA = tid < C, low = i >= 32;  // (uniform in a warp)
   const float li = s.l[i], mul = isA ? s.beta[i] * inv_kk : p_unit;
@@ -313,8 +316,16 @@ __device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk,
                                    half2_bits(v[8 * k + 4], v[8 * k + 5]), half2_bits(v[8 * k + 6], v[8 * k + 7]));
       if (!isA)
         *reinterpret_cast<float4 *>(P + tile_off(i, 2 * h + k, C)) = o;
-      else if (h < diag)
+      else if (h < diag) {
         *reinterpret_cast<float4 *>(&s.Ah[i - 16][16 * h + 8 * k]) = o;
+        auto rest = [&](int e, float bits) {
+          const uint32_t w = __float_as_uint(bits);
+          const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+          return half2_bits(v[8 * k + e] - hi.x, v[8 * k + e + 1] - hi.y);
+        };
+        *reinterpret_cast<float4 *>(M + tile_off(16 * h + (i & 15), 2 * diag + k, C)) =
+            make_float4(rest(0, o.x), rest(2, o.y), rest(4, o.z), rest(6, o.w));
+      }
     }
     if (isA && h == diag) {  // its part of the diagonal block, in fp32
 #pragma unroll
@@ -327,10 +338,12 @@ __device__ __forceinline__ void factor_rows(Factor &s, uint32_t t, float inv_kk,
     for (int j = 0; j < i; j++) {
       if (s.z[j] == zi) continue;
       if (isA) {
-        if (j >> 4 == diag)
+        if (j >> 4 == diag) {
           s.Ad[i][j & 15] = 0.0f;
-        else
+        } else {
           s.Ah[i - 16][j] = __float2half_rn(0.0f);
+          *reinterpret_cast<uint16_t *>(M + tc::sw128_offset((j & ~15) + (i & 15), 16 * diag + (j & 15), C)) = 0;
+        }
       } else {
         *reinterpret_cast<uint16_t *>(P + tc::sw128_offset(i, j, C)) = 0;
       }
@@ -391,9 +404,14 @@ __device__ __forceinline__ void factor_columns(Factor &s, uint8_t *M, int c, int
       y[b][3] = word(&s.Yb[b][g + 8][q + 8]);
     } else if (b > c) {
       float z0[4] = {}, z1[4] = {};
+      auto rest = [&](int k, int row, int col) {  // of A's block (b, k)
+        return *reinterpret_cast<const uint32_t *>(M + tc::sw128_offset(16 * k + row, 16 * b + col, C));
+      };
 #pragma unroll
       for (int k = 0; k < b; k++) {
         if (k < c) continue;
+        mma_16816(z0, y[k], rest(k, g, q), rest(k, g, q + 8));
+        mma_16816(z1, y[k], rest(k, g + 8, q), rest(k, g + 8, q + 8));
         mma_16816(z0, y[k], word(&s.Ah[16 * b - 16 + g][16 * k + q]), word(&s.Ah[16 * b - 16 + g][16 * k + q + 8]));
         mma_16816(z1, y[k], word(&s.Ah[16 * b - 8 + g][16 * k + q]), word(&s.Ah[16 * b - 8 + g][16 * k + q + 8]));
       }
@@ -418,10 +436,16 @@ __device__ __forceinline__ void factor_columns(Factor &s, uint8_t *M, int c, int
     }
   }
 }
-// What lies above the diagonal blocks of M (and above the 32-column halves of P) is never written:
-// cleared once by 128 threads.
-__device__ __forceinline__ void factor_clear(uint8_t *M, int tid) {
-  for (int i = tid; i < (int)(SQ / 16); i += 128) reinterpret_cast<uint4 *>(M)[i] = make_uint4(0, 0, 0, 0);
+// What lies above the 32-column halves of P is never written: cleared once by 128 threads.
+__device__ __forceinline__ void factor_clear(uint8_t *P, int tid) {
+  for (int i = tid; i < (int)(SQ / 16); i += 128) reinterpret_cast<uint4 *>(P)[i] = make_uint4(0, 0, 0, 0);
+}
+// M above its diagonal blocks, once A's rests there have been read.
+__device__ __forceinline__ void factor_clear_upper(uint8_t *M, int tid) {
+  for (int i = tid; i < 8 * (C - 16); i += 128) {
+    const int r = i >> 3, c8 = i & 7;
+    if (c8 >= 2 * (r >> 4) + 2) *reinterpret_cast<uint4 *>(M + tile_off(r, c8, C)) = make_uint4(0, 0, 0, 0);
+  }
 }
 
 }  // namespace rule

@@ -236,3 +236,38 @@ def test_another_stream_leaves_freed_blocks_of_this_one_alone(dtype, d):
     torch.cuda.synchronize()
     assert busy  # (else it showed nothing)
     assert all(x.equal(z) for x, z in zip(got, want))
+
+
+def correlated(seed, T, cosine, betas, queries, S0=True, H=2, Hk=2):
+    """Keys (and queries) of a head about a common direction; slow gates."""
+    s = ref.rule_inputs(seed, "bf16", 1, H, Hk, T, 128, 128, "open", S0)
+    r = np.random.default_rng(seed + 1)
+
+    def unit(x):
+        return x / np.linalg.norm(x, axis=-1, keepdims=True)
+
+    c = unit(r.standard_normal((1, Hk, 1, 128)))
+    for n in ("k", "q") if queries else ("k",):
+        s[n] = ref.round_bf16(unit(np.sqrt(cosine) * c + np.sqrt(1.0 - cosine) * unit(s[n])))
+    s["beta"] = r.uniform(*betas, s["beta"].shape).astype(np.float32)
+    s["gamma"] = r.uniform(0.99, 1.0, s["gamma"].shape).astype(np.float32)
+    return s
+
+
+CORRELATED = [(0.5, (0.0, 1.0), False), (0.9, (0.0, 1.0), True), (0.9, (1.0, 2.0), False)]
+
+
+@pytest.mark.parametrize("cosine,betas,queries", CORRELATED, ids=str)
+def test_correlated_keys(cosine, betas, queries):
+    """The triangular factor is far from the identity and the outputs are small sums of large terms."""
+    s = correlated(67, 512, cosine, betas, queries)
+    check_forward(s, "bf16")
+    check_backward(s, "bf16")
+
+
+@pytest.mark.parametrize("cosine,betas,queries", [*CORRELATED, (0.9, (1.0, 2.0), True)], ids=str)
+def test_correlated_keys_in_fp32(cosine, betas, queries):
+    """What the header offers where the terms are too large for fp16 operands."""
+    s = correlated(67, 512, cosine, betas, queries)
+    check_forward(s, "f32")
+    check_backward(s, "f32")
