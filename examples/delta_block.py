@@ -32,8 +32,9 @@ class GatedDelta(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, gamma, beta = ctx.saved_tensors
-        dq, dk, dv, dgamma, dbeta = binding.mesa_delta_backward_chunked(q, k, v, gamma, beta, dout.contiguous(), ctx.scale)
-        return dq, dk, dv, dgamma.to(gamma.dtype), dbeta.to(beta.dtype), None
+        dq, dk, dv, dgamma, dbeta = binding.mesa_delta_backward_chunked(q, k, v, gamma, beta, dout.contiguous(), ctx.scale,
+                                                                       gates_dtype=gamma.dtype)
+        return dq, dk, dv, dgamma, dbeta, None
 
 
 class BlockNorm(torch.autograd.Function):

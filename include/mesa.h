@@ -314,13 +314,14 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
  *     dk_t = dS_t^T u_t - beta_t gamma_t S_{t-1}^T du_t,        dv_t = beta_t du_t,
  *     dbeta_t = du_t . e_t,              dgamma_t = <N_t, S_{t-1}>   (also where gamma_t = 0).
  * dq, dk_out [B, Hk, T, dk] (summed over the value heads of a key head), dv_out [B, H, T, dv],
- * dgamma, dbeta [B, H, T]: all of dtype -- the gates' gradients come from the same products as
- * the others and carry no more digits.  dS0: NULL or [B, H, dv, dk] fp32, dL/dS0
+ * dgamma, dbeta [B, H, T]: all of dtype, or, with dtype | MESA_GATE_GRADS_F32, the gates' gradients
+ * in fp32 like the gates themselves.  dS0: NULL or [B, H, dv, dk] fp32, dL/dS0
  * (it may be dS_final's memory).  The states are recomputed; every sum has a fixed order.  S0 as given to the forward.
  * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward
  * (MESA_ERR_NONFINITE: a gradient other than dS0 is not finite); on the tensor cores |beta| < 4 (a
  * larger one can overflow an operand: MESA_ERR_NONFINITE).
  */
+enum mesa_delta_backward_option { MESA_GATE_GRADS_F32 = 256 };
 size_t mesa_delta_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q,
                                 const void *k, const void *v, const float *gamma, const float *beta,

@@ -15,6 +15,7 @@ import torch
 from . import build as _build
 
 MESA_F32, MESA_BF16 = 0, 1
+MESA_GATE_GRADS_F32 = 256
 _DTYPE_CODES = {torch.float32: MESA_F32, torch.bfloat16: MESA_BF16}
 MESA_OK, MESA_ERR_TIMEOUT, MESA_ERR_NONFINITE = 0, 5, 6
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported size or option",
@@ -488,10 +489,12 @@ def mesa_delta_backward_workspace_size(B, H, Hk, T, dk, dv, dtype) -> int:
 
 
 def mesa_delta_backward_chunked(q, k, v, gamma, beta, dout, scale=1.0, S0=None, dS_final=None, dq=None, dk=None,
-                                dv=None, dgamma=None, dbeta=None, dS0=None, workspace=None, stream=None):
+                                dv=None, dgamma=None, dbeta=None, dS0=None, workspace=None, stream=None,
+                                gates_dtype=None):
     """Gradients of mesa_delta_forward_chunked given dout = dL/dout (and dS_final = dL/dS_final):
-    returns (dq, dk, dv, dgamma, dbeta), all of q's dtype; dS0 [B, H, dv, dk] fp32, when given,
-    receives dL/dS0."""
+    returns (dq, dk, dv, dgamma, dbeta), all of q's dtype, the gates' dgamma and dbeta of
+    gates_dtype (None: of a given dgamma or dbeta, or q's dtype; torch.float32: not rounded, like
+    the gates); dS0 [B, H, dv, dk] fp32, when given, receives dL/dS0."""
     lib = load()
     code = _dtype_code(q)
     B, H, Hk, T, dkk, dvv = _delta_dims(q, k, v, gamma, beta)
@@ -499,12 +502,19 @@ def mesa_delta_backward_chunked(q, k, v, gamma, beta, dout, scale=1.0, S0=None, 
     dq = _new(q.shape, q.dtype, dev, stream) if dq is None else dq
     dk = _new(q.shape, q.dtype, dev, stream) if dk is None else dk
     dv = _new(v.shape, q.dtype, dev, stream) if dv is None else dv
-    dgamma = _new((B, H, T), q.dtype, dev, stream) if dgamma is None else dgamma
-    dbeta = _new((B, H, T), q.dtype, dev, stream) if dbeta is None else dbeta
+    if gates_dtype is None:
+        given = dgamma if dgamma is not None else dbeta
+        gates_dtype = q.dtype if given is None else given.dtype
+    if gates_dtype is not q.dtype and gates_dtype is not torch.float32:
+        raise MesaError(f"dgamma and dbeta must be {q.dtype} or {torch.float32}, got {gates_dtype}")
+    dgamma = _new((B, H, T), gates_dtype, dev, stream) if dgamma is None else dgamma
+    dbeta = _new((B, H, T), gates_dtype, dev, stream) if dbeta is None else dbeta
+    if gates_dtype is torch.float32:
+        code |= MESA_GATE_GRADS_F32
     state = (B, H, dvv, dkk)
     _require_all(dev, (dout, "dout", q.dtype, v.shape), (dq, "dq", q.dtype, q.shape), (dk, "dk", q.dtype, q.shape),
-                 (dv, "dv", q.dtype, v.shape), (dgamma, "dgamma", q.dtype, (B, H, T)),
-                 (dbeta, "dbeta", q.dtype, (B, H, T)), (S0, "S0", torch.float32, state),
+                 (dv, "dv", q.dtype, v.shape), (dgamma, "dgamma", gates_dtype, (B, H, T)),
+                 (dbeta, "dbeta", gates_dtype, (B, H, T)), (S0, "S0", torch.float32, state),
                  (dS_final, "dS_final", torch.float32, state), (dS0, "dS0", torch.float32, state))
     workspace = _workspace(workspace, int(lib.mesa_delta_backward_workspace_size(B, H, Hk, T, dkk, dvv, code)), dev,
                            stream)

@@ -112,6 +112,7 @@ int mesa_delta_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int 
 }
 
 size_t mesa_delta_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
+  dtype &= ~MESA_GATE_GRADS_F32;  // (the same workspace)
   if (check_sizes(B, H, Hk, T, dk, dv, dtype, 1.0f) != MESA_OK) return 0;
   size_t off[kTcParts + 1];
   return rule_tc(dtype, dk, dv) ? backward_tc_parts(B, H, Hk, T, off) : backward_parts(B, H, Hk, T, dk, dv, off);
@@ -123,6 +124,8 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
                                 void *dq, void *dk_out, void *dv_out, void *dgamma, void *dbeta,
                                 float *dS0, void *workspace, size_t workspace_bytes,
                                 cudaStream_t stream) {
+  const bool gates_f32 = (dtype & MESA_GATE_GRADS_F32) != 0;
+  dtype &= ~MESA_GATE_GRADS_F32;
   const int bad = check_sizes(B, H, Hk, T, dk, dv, dtype, scale);
   if (bad != MESA_OK) return bad;
   const size_t U = (size_t)B * H;
@@ -149,6 +152,7 @@ int mesa_delta_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int
   a.dq = dq;
   a.dk_out = dk_out;
   a.dv_out = dv_out;
+  a.gates_f32 = gates_f32 || dtype == MESA_F32;
   a.dgamma = dgamma;
   a.dbeta = dbeta;
   a.dS0 = dS0;

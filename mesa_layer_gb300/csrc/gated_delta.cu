@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBw
     }
     db_sum = warp_sum(db_sum);
     bad = fmaf(db_sum, 0.0f, bad);
-    if (lane == 0 && t < n) st((TIO *)a.dbeta, tu + t, db_sum);
+    if (lane == 0 && t < n) st_gate<TIO>(a, a.dbeta, tu + t, db_sum);
   }
   // decays: D[i][j] = gamma_{j+1} .. gamma_i (j <= i), from0[i] = gamma_0 .. gamma_i
   if (warp == 0) {
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(256) mesa_rule_grads_kernel(RuleArgs a, RuleBw
     float s = (lane < t ? dprev * (col + toC * xout[lane]) : 0.0f) + prev0 * (D[lane * P + t] * xin[lane]);
     s = fmaf(toC * prev0, cross, warp_sum(s));
     bad = fmaf(s, 0.0f, bad);
-    if (lane == 0) st((TIO *)a.dgamma, tu + t, s);
+    if (lane == 0) st_gate<TIO>(a, a.dgamma, tu + t, s);
   }
   if (!(bad == 0.0f)) atomicOr(a.status, tc_err_nonfinite());
 }

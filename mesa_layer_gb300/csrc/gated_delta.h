@@ -21,12 +21,22 @@ struct RuleArgs {
   const void *dout = nullptr;          // [B, H, T, dv]
   const float *dS_final = nullptr;     // [B, H, dv, dk] or nullptr
   void *dq = nullptr, *dk_out = nullptr, *dv_out = nullptr, *dgamma = nullptr, *dbeta = nullptr;
+  bool gates_f32 = false;              // dgamma, dbeta [B, H, T] in fp32 (else of dtype)
   float *dS0 = nullptr;
   unsigned *status = nullptr;
   unsigned wait_limit = 0;
   __host__ __device__ int units() const { return B * H; }
   __host__ __device__ int qk_unit(int u) const { return (u / H) * Hk + (u % H) / (H / Hk); }
 };
+
+// A gate's gradient, in fp32 or in the call's type TIO.
+template <typename TIO>
+__device__ __forceinline__ void st_gate(const RuleArgs &a, void *p, size_t i, float x) {
+  if (a.gates_f32)
+    static_cast<float *>(p)[i] = x;
+  else
+    static_cast<TIO *>(p)[i] = TIO(x);
+}
 
 // CUDA-core path: chunks of kRuleChunk tokens in the backward pass.
 constexpr int kRuleChunk = 32;

@@ -1009,9 +1009,10 @@ __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     stop = __syncthreads_or(!got_c);
     if (stop) break;
     if (tid < n) {
-      st((__nv_bfloat16 *)a.dgamma, tok0 + tid, m->dgam[0][tid] + m->dgam[1][tid]);
-      st((__nv_bfloat16 *)a.dbeta, tok0 + tid,
-         m->duv[tid] - ((m->dbeta[0][tid] + m->dbeta[1][tid]) + (m->dbeta[2][tid] + m->dbeta[3][tid])));
+      st_gate<__nv_bfloat16>(a, a.dgamma, tok0 + tid, m->dgam[0][tid] + m->dgam[1][tid]);
+      st_gate<__nv_bfloat16>(
+          a, a.dbeta, tok0 + tid,
+          m->duv[tid] - ((m->dbeta[0][tid] + m->dbeta[1][tid]) + (m->dbeta[2][tid] + m->dbeta[3][tid])));
     }
     // dq = f (g S0) + W K;  dk = W^T Q - (V + V^T) K + c (u A) - f beta (du S0); columns 32 part ..
     const float f1 = upper ? -m->nf[i] * a.scale * ig * iS : m->nf[i] * m->beta[i] * idu * iS;

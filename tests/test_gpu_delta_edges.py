@@ -271,3 +271,42 @@ def test_correlated_keys_in_fp32(cosine, betas, queries):
     s = correlated(67, 512, cosine, betas, queries)
     check_forward(s, "f32")
     check_backward(s, "f32")
+
+
+@pytest.mark.parametrize("dk,dv,T", [(64, 64, 90), (32, 128, 300), (128, 128, 150)])
+def test_gate_gradients_in_fp32(dk, dv, T):
+    """What bf16 calls round: on the CUDA cores all the digits of fp32, and rounded the same values."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    s = ref.rule_inputs(76, "bf16", 1, 2, 1, T, dk, dv, "packed", True)
+    t = upload(s, "bf16")
+    args = [t[n] for n in ("q", "k", "v", "gamma", "beta", "dout")]
+    states = dict(S0=t["S0"], dS_final=t["dS_final"])
+    want = ref.rule_backward(s["q"], s["k"], s["v"], s["gamma"], s["beta"], SCALE, s["dout"], s["S0"], s["dS_final"])
+    rounded = binding.mesa_delta_backward_chunked(*args, SCALE, **states)
+    mine = torch.full((1, 2, T), float("nan"), device="cuda")
+    for options in (dict(gates_dtype=torch.float32), dict(dgamma=mine), dict(dbeta=mine)):
+        got = binding.mesa_delta_backward_chunked(*args, SCALE, **states, **options)
+        assert got[3].dtype is got[4].dtype is torch.float32
+        assert all(x.to(torch.bfloat16).equal(y) for x, y in zip(got, rounded))
+        for x, n in zip(got[3:], GRADS[3:]):
+            assert err(x, want[n]) <= TOL["bf16" if dk == dv == 128 else "f32"]
+    assert mine.isfinite().all()
+
+
+def test_gate_gradients_of_other_types_are_refused():
+    import torch
+
+    from mesa_layer_gb300 import binding
+    t = upload(ref.rule_inputs(77, "bf16", 1, 2, 1, 20, 16, 16, "open"), "bf16")
+    args = [t[n] for n in ("q", "k", "v", "gamma", "beta", "dout")]
+    full = torch.zeros(1, 2, 20, device="cuda")
+    for options in (dict(gates_dtype=torch.float64), dict(dgamma=full.half()), dict(dgamma=full, dbeta=full.bfloat16()),
+                    dict(dgamma=full, gates_dtype=torch.bfloat16), dict(dbeta=full[:, :1].contiguous())):
+        with pytest.raises(binding.MesaError):
+            binding.mesa_delta_backward_chunked(*args, **options)
+    f = {n: x.float() for n, x in t.items() if x is not None}
+    with pytest.raises(binding.MesaError):  # an fp32 call has no bf16 gradients
+        binding.mesa_delta_backward_chunked(*(f[n] for n in ("q", "k", "v", "gamma", "beta", "dout")),
+                                            gates_dtype=torch.bfloat16)
