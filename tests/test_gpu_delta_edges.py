@@ -310,3 +310,70 @@ def test_gate_gradients_of_other_types_are_refused():
     with pytest.raises(binding.MesaError):  # an fp32 call has no bf16 gradients
         binding.mesa_delta_backward_chunked(*(f[n] for n in ("q", "k", "v", "gamma", "beta", "dout")),
                                             gates_dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("H,T", [(2, 300), (1, 2100)])
+def test_wait_give_up_of_the_gradients_reports_timeout(H, T):
+    """Every tensor-core kernel of the backward (in segments, too) told to give up at its first wait."""
+    from mesa_layer_gb300 import binding
+    t = upload(ref.rule_inputs(68, "bf16", 1, H, 1, T, 128, 128, "open", True), "bf16")
+    want, status = backward(t)
+    assert status == (binding.MESA_OK, 0)
+    binding.mesa_debug_set_wait_limit(0)
+    try:
+        _, (code, bits) = backward(t)
+    finally:
+        binding.mesa_debug_set_wait_limit(-1)
+    assert code == binding.MESA_ERR_TIMEOUT and bits & 1 and not bits & 4
+    got, status = backward(t)
+    assert status == (binding.MESA_OK, 0)
+    assert all(got[n].equal(want[n]) for n in want)
+
+
+@pytest.mark.parametrize("T", [1921, 2500])
+def test_long_sequences_with_shared_key_heads(T):
+    """Segments of sequences whose value heads share queries and keys."""
+    s = ref.rule_inputs(69, "bf16", 1, 4, 2, T, 128, 128, "open", True)
+    s["gamma"] = np.random.default_rng(70).uniform(0.998, 1.0, s["gamma"].shape).astype(np.float32)
+    check_forward(s, "bf16")
+    check_backward(s, "bf16")
+
+
+@pytest.mark.parametrize("dtype,d,T", [("f32", 32, 150), ("bf16", 128, 150), ("bf16", 128, 2100)])
+def test_calls_in_a_graph(dtype, d, T):
+    """Every entry point captured into one graph and replayed on other inputs."""
+    import torch
+
+    from mesa_layer_gb300 import binding
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    ins = [upload(ref.rule_inputs(71 + i, dtype, 1, 2, 1, T, d, d, "packed", True), dtype) for i in range(2)]
+    x = {n: a.clone() for n, a in ins[0].items()}
+    y = torch.randn(T, d, device="cuda").to(td)
+    w = torch.ones(d, device="cuda")
+    S = x["S0"].clone()
+
+    def calls():
+        args = [x[n] for n in ("q", "k", "v", "gamma", "beta")]
+        out = binding.mesa_delta_forward_chunked(*args, SCALE, S0=x["S0"])
+        grads = binding.mesa_delta_backward_chunked(*args, x["dout"], SCALE, S0=x["S0"], dS_final=x["dS_final"])
+        o = binding.mesa_delta_step(S, *(a[:, :, 0].contiguous() for a in args))
+        h = binding.mesa_block_norm(y, y, w_post=w, w_pre=w)
+        n = binding.mesa_block_norm_backward(y, y, y, dh=y, w_post=w, w_pre=w)
+        return [out, *grads, o, *h, *(a for a in n if a is not None)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    for a in ins[::-1]:
+        for n in x:
+            x[n].copy_(a[n])
+        S.copy_(a["S0"])
+        graph.replay()
+        got = [c.clone() for c in captured]
+        S.copy_(a["S0"])
+        assert all(p.equal(q) for p, q in zip(got, calls()))
