@@ -886,12 +886,17 @@ int launch_chain(const RuleArgs &a, const uint8_t *records, const RuleOperands &
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
-// Segments of a unit's NC chunks: as many CTAs as a GB300 has SMs (152), at least six chunks each (1 x 16 x
-// 65536: nine segments, 645 us against 2850 for one; 72 of them the segments' starts, 14 the join).  Where
-// gates hardly decay the two starting passes take as long as two segments, so n segments take 3/n of
-// the time of one pass, and fewer than five are not worth it.
+// Segments of a unit's NC chunks: as many CTAs as a GB300 has SMs (152), at least 20 chunks each, at most 24.
+// They run one pass over a segment's chunks in place of one over the unit's, and the starts: the chunks at each
+// segment's end where 20 of them forget (2^-40), else two more passes and the join, a chain of 27 us a
+// step (34 in the backward) where matrices are applied.  us of a forward, one chain against n segments, gates
+// about 0.98 / above 0.99999: 1 unit x 65536 tokens 2450, 24: 211 / 847, 152: 4090 / 4090; 16 x 65536 2800, 9: 641 /
+// 1289; 1 x 8192 312, 6: 123 / 240, 19: 538 / 539; 16 x 8192 366, 6: 169 / 287; 16 x 4096 183, 5: 194 / 196, 9: 279 / 279;
+// 16 x 2048 97, 5: 160 / 160.  (The backward likewise: 1 x 65536 5230, 501 / 1947; 16 x 4096 432, 5: 476.)
 int segments(int U, int NC) {
-  const int n = U > 0 ? (152 / U < NC / 6 ? 152 / U : NC / 6) : 1;
+  int n = U > 0 ? 152 / U : 1;
+  n = n < NC / 20 ? n : NC / 20;
+  n = n < 24 ? n : 24;
   return n < 5 ? 1 : n;
 }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
