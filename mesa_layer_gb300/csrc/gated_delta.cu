@@ -679,13 +679,17 @@ int launch_scan_join(const RuleArgs &a, const RuleScanSegments &sg, bool adjoint
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
-// Segments of a unit's tokens: about four CTAs for each of a GB300's 152 SMs (the chain of one leaves most of an
-// SM idle), whole chunks, at most 16 (the join is a chain over them: 2 x 4 heads x 2048 x 64 fp32, 16 segments 69 us,
-// 24: 78, 32: 74, one: 447); fewer than four are not worth the two more passes.
-int scan_segments(int U, int T, int dv) {
+// Segments of a unit's tokens: about 256 threads for each of a GB300's 152 SMs (the chain of one CTA leaves most of an
+// SM idle; the rows of d = 128 take twice the threads of the others and fill it twice as soon), whole chunks (two at
+// least for d = 128), at most 16 (the join is a chain over them); fewer than four are not worth the two more passes.
+// us of one scan, of n segments: forward of 2 x 4 x 2048 x 64 fp32 447, 16: 69, 24: 78, 32: 74; forward / backward of 32
+// units x 1024, d 128, 219 / 831, four: 307 / 999; of 8 units 219 / 471, eight: 109 / 303, 16: 132 / 348; of one
+// unit x 128 36 / 115, four: 35 / 139; 32 units x 1024, d 64, 170 / 473, nine: 86 / 321.
+int scan_segments(int U, int T, int dk, int dv) {
   const int NC = (T + kRuleChunk - 1) / kRuleChunk, ctas = U * ((dv + ROWS - 1) / ROWS);
-  int n = ctas > 0 ? 4 * 152 / ctas : 1;
-  if (n > NC) n = NC;
+  int n = ctas > 0 ? 152 * 256 / (ctas * ROWS * lanes_per_row(dk)) : 1;
+  const int most = dk == 128 ? NC / 2 : NC;
+  if (n > most) n = most;
   if (n > 16) n = 16;
   return n < 4 ? 1 : n;
 }
@@ -737,13 +741,13 @@ int launch_fwd_t(const RuleArgs &a, const RuleScanSegments &sg, cudaStream_t st)
 }  // namespace
 
 size_t rule_scan_workspace(int U, int T, int dk, int dv, bool backward) {
-  const size_t n = scan_segments(U, T, dv), mat = (size_t)dk * dk * sizeof(float), state = (size_t)dv * dk * sizeof(float);
+  const size_t n = scan_segments(U, T, dk, dv), mat = (size_t)dk * dk * sizeof(float), state = (size_t)dv * dk * sizeof(float);
   return n == 1 ? 0 : U * n * (2 * state + mat) * (backward ? 2 : 1);
 }
 RuleScanSegments rule_scan_parts(int U, int T, int dk, int dv, bool backward, void *workspace) {
   const int blocks = kRuleChunk / TB, NC = (T + kRuleChunk - 1) / kRuleChunk;
   RuleScanSegments sg;
-  sg.n = scan_segments(U, T, dv);
+  sg.n = scan_segments(U, T, dk, dv);
   sg.per = (NC + sg.n - 1) / sg.n * blocks;
   if (sg.n == 1) return sg;
   const size_t mat = (size_t)U * sg.n * dk * dk, state = (size_t)U * sg.n * dv * dk;

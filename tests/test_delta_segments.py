@@ -19,3 +19,11 @@ def segmented(U, T, d, dtype):
     (1, 6400, True), (1, 8192, True), (16, 8192, True), (16, 65536, True), (30, 65536, True), (31, 65536, False)])
 def test_tensor_core_sequences(U, T, want):
     assert segmented(U, T, 128, torch.bfloat16) == want
+
+
+@pytest.mark.parametrize("U,T,d,want", [
+    # fp32, us of one scan, of segments: 32 units of 1024 tokens, d 128, 219, 307; 8 units 219, 109; 32 units, d 64, 170, 86
+    (32, 1024, 128, False), (32, 8192, 128, False), (128, 2048, 128, False), (8, 1024, 128, True), (1, 256, 128, True),
+    (32, 1024, 64, True), (128, 2048, 64, False), (128, 1024, 32, True), (8, 64, 64, False)])
+def test_sequences_on_the_cuda_cores(U, T, d, want):
+    assert segmented(U, T, d, torch.float32) == want
