@@ -228,7 +228,8 @@ struct Backward {
   static int run(const NormArgs &a, cudaStream_t st) {
     const int most = norm_bwd_ctas(a.N, a.D), ctas = most < 152 * resident<T, G>() ? most : 152 * resident<T, G>();
     constexpr int smem = 3 * norm::EPT * G * (int)sizeof(float);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(mesa_block_norm_bwd_kernel<T, VEC, G>,
+    // (48 KB without being asked for, the row sums' static part among them: rows of more than 2048 channels)
+    if (smem >= 48 * 1024 && cudaFuncSetAttribute(mesa_block_norm_bwd_kernel<T, VEC, G>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
       return -1;
     timing_mark_begin(K_NORM_BWD, st);
