@@ -280,9 +280,10 @@ int mesa_forward_chunked_noalloc(int B, int H, int T, int dk, int dv, int dtype,
  *   S0, S_final: NULL or [B, H, dv, dk] fp32 (each may be given without the other; they may be the
  *   same memory).
  *   gamma_t = 0 forgets everything before token t (a packed document's first token); beta_t = 0
- *   leaves a token unwritten (padding).  On the tensor-core path, where decays are logarithms, gamma
- *   below e^-80 counts as 0; a negative gate, or gates above one that multiply to more than 2^8 in one of
- *   the 64-token chunks from token 0 on, give NaN (MESA_ERR_NONFINITE).
+ *   leaves a token unwritten (padding; its q, k and v have to be finite).  On the tensor-core path,
+ *   where decays are logarithms, gamma below e^-80 counts as 0; a negative gate, or gates above one that
+ *   multiply to more than 2^8 in one of the 64-token chunks from token 0 on, give NaN
+ *   (MESA_ERR_NONFINITE).
  * dk, dv in {16, 32, 64, 128}, not necessarily equal; T >= 0; B * H <= 65535.  q, k, v, out, S0
  * and S_final 16-byte aligned (MESA_ERR_INVALID_ARG otherwise).
  * workspace: at least mesa_delta_workspace_size() bytes, 256-byte aligned; its first word is the

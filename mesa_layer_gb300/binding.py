@@ -555,7 +555,10 @@ def _norm_check(x, y, gate, w_post, res_scale, w_pre):
     _require_all(y.device, (y, "y", dtype, shape), (x, "x", dtype, shape), (gate, "gate", dtype, shape),
                  (w_post, "w_post", torch.float32, weight), (res_scale, "res_scale", torch.float32, weight),
                  (w_pre, "w_pre", torch.float32, weight))
-    return y.numel() // D, D
+    N = y.numel() // D
+    if N > 0x7fffffff:  # (an int of the C interface)
+        raise MesaError(f"y may have 2^31 - 1 rows at most, got {N}")
+    return N, D
 
 
 def mesa_block_norm(x, y, gate=None, w_post=None, res_scale=None, w_pre=None, eps=1e-6, x_out=None, h_out=None,
