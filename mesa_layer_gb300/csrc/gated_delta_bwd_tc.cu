@@ -14,8 +14,8 @@
 //        dgamma_t: every pair (reader i >= t or the state after, writer j < t or the state before)
 //        that the gate separates, with the decay between them but for gamma_t's own.
 // States, adjoints, u and du go through memory as fp16 operands with one scale a chunk (2^-12 of a
-// chunk's largest).  Measured at 8 x 16 x 4096: records 113 us, states 154, adjoint 218 (64 dependent steps of
-// 3.4 us), gradients 467 (1.7 GB of operands, rows and gradients: 3.7 TB/s); each bound by the latency of
+// chunk's largest).  Measured at 8 x 16 x 4096: records 122 us, states 155, adjoint 217 (64 dependent steps of
+// 3.4 us), gradients 461 (1.7 GB of operands, rows and gradients: 3.7 TB/s); each bound by the latency of
 // its dependent steps on one CTA per SM, the last also by shared memory (its products' operands).
 #include "gated_delta_tc.cuh"
 
@@ -570,7 +570,7 @@ __device__ __forceinline__ void l2_prefetch(const void *p) { asm volatile("prefe
 // tensor memory's lanes take a quarter of the columns each.  A chunk is a row of short steps that wait
 // for one another, so the next chunk's rows are on their way (in registers) from the middle of this one's, its states
 // and u from where this one's have been read.  (One CTA per chunk, 256 threads, nothing on its way: 875 us
-// at 8 x 16 x 4096; so, 467.)
+// at 8 x 16 x 4096; so, 461.)
 __global__ void __launch_bounds__(32 * GR_WARPS, 1)
     mesa_rule_grads_tc_kernel(RuleArgs a, int NC, int chunks, const uint8_t *records, RuleOperands so, RuleOperands ao,
                               float *dqp, float *dkp, const __grid_constant__ CUtensorMap mapDq,

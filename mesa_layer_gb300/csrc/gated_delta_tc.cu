@@ -15,8 +15,9 @@
 //     chain    the three epilogues above;
 //     helper   writes the readout (and with the transposition, too, it held up the chain: 188 us);
 //     convert  V transposed one chunk ahead, K and Q as fp16 operands, up to three chunks ahead.
-// Measured at 8 x 16 x 4096 (8192 chunks): preparation 110 us (400 MB of rows and records: 3.7 TB/s; the
-// substitution's latency and instruction fetch), chain 179 us (64 dependent steps of 2.8 us; issue slots
+// Measured at 8 x 16 x 4096 (8192 chunks): preparation 120 us (400 MB of rows and records: 3.3 TB/s; the
+// substitution's latency and instruction fetch; 10 us of it for the second fp16 value of A's blocks), chain
+// 180 us (64 dependent steps of 2.8 us; issue slots
 // 37 %, tensor pipe 19 % busy: the latency of four products and three epilogues a step, 128 of 152 SMs).
 // (With the preparation in the same kernel, as a fourth group, nothing but the inputs and the output
 // went to memory, but the groups' code no longer fitted the instruction caches and every
@@ -833,7 +834,8 @@ __global__ void __launch_bounds__(384, 1)
 
 // The state before each segment from the segments' own: S_{y+1} = S_y Tr_y + loc_y (S_1 = loc_0; S_0 is a
 // copy: the last segment may write its final state over the caller's), sixteen rows by a CTA of 256
-// threads; grid (8, U).
+// threads; grid (8, U).  A chain of steps that read a 64 KB matrix from the L2 cache with nothing on its way: 27 us
+// each where matrices are applied, 1.2 where not.
 __global__ void __launch_bounds__(256) mesa_rule_join_kernel(RuleSegments sg, const float *S0) {
   __shared__ float rows[16][D + 4];
   const int u = blockIdx.y, row0 = 16 * blockIdx.x, tid = threadIdx.x;
