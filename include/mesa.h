@@ -374,8 +374,9 @@ int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void 
                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
- * Device status word of the last mesa_forward_chunked (or _save, or mesa_backward_chunked)
- * call that used `workspace`: copies the word to *flags (host) on `stream` and synchronises
+ * Device status word of the last mesa_forward_chunked (or _save, mesa_backward_chunked,
+ * mesa_delta_forward_chunked, mesa_delta_backward_chunked) call that used `workspace` (a call
+ * without tokens or units uses none): copies the word to *flags (host) on `stream` and synchronises
  * it.  Bits: 0 (1) a tensor-core kernel's bounded wait for its matrix multiplies gave up --
  * the kernel then waits for the multiplies still in flight, releases its tensor memory and
  * returns, and the affected chunks' outputs are not written; 1 (2) a non-finite output was
@@ -385,7 +386,7 @@ int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void 
  * MESA_ERR_NONFINITE if bit 1 is set, else MESA_OK (MESA_ERR_INVALID_ARG / MESA_ERR_CUDA
  * when the word could not be read).
  *
- * Non-finite inputs: the call still ends (in dynamic mode a token whose residual is NaN runs
+ * Non-finite inputs of the Mesa layer: the call still ends (in dynamic mode a token whose residual is NaN runs
  * to cg_iters).  A NaN or infinity in q_t affects o_t alone (non-finite in general; zero when
  * an infinite query meets the dynamic stopping rule at once, inf <= tol * inf).  One in k_t,
  * v_t or gamma_t (a NaN gate stays NaN) leaves that unit's tokens before the 128-token block
