@@ -374,9 +374,125 @@ int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void 
                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Selective state space scan: the recurrent layer of a hybrid stack whose forget gate and input gate come from one step
+ * length ("Declaracao do Problema" lists the layer's linear recurrent relatives), in the layouts and with the states of the
+ * gated delta rule.  q, k and v are what its literature calls C, B and x.  Per (batch, head) unit, with the state S
+ * [dv, dk] (zero, or S0, before token 0):
+ *     D_t = softplus(dt_t + dt_bias_h),          a_t = e^(D_t A_h)  (0 where starts_t is set),
+ *     S_t = a_t S_{t-1} + D_t v_t k_t^T,         o_t = S_t q_t + skip_h v_t.
+ *   q, k [B, Hk, T, dk] dtype; v, out [B, H, T, dv] dtype; dt [B, H, T] fp32; A, dt_bias, skip [H] fp32 (A < 0; dt_bias
+ *   and skip may be NULL: none).  Hk divides H: value head h reads query / key head h / (H / Hk).
+ *   starts: NULL or [B, T] bytes, not 0 where a packed document begins: nothing from before that token comes through,
+ *   S0 among it (what is non-finite there may all the same).  dt_t = -infinity leaves a token unwritten and the state as
+ *   it is (padding; its q, k and v have to be finite).
+ *   S0, S_final: NULL or [B, H, dv, dk] fp32 (each may be given without the other; they may be the same memory).
+ * dk, dv in {16, 32, 64, 128}, not necessarily equal; T >= 0; B * H <= 65535.  q, k, v, out, S0 and S_final 16-byte
+ * aligned (MESA_ERR_INVALID_ARG otherwise).
+ * workspace: at least mesa_ssm_workspace_size() bytes, 256-byte aligned; its first word is the status word read by
+ * mesa_forward_status (MESA_ERR_NONFINITE: a non-finite out).
+ * Arithmetic: sums, states and gates in fp32, log-decays as sums of two fp32 values.  Decays below 2^-150 count as that.
+ */
+size_t mesa_ssm_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
+int mesa_ssm_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q, const void *k,
+                             const void *v, const float *dt, const float *A, const float *dt_bias,
+                             const float *skip, const uint8_t *starts, void *out, const float *S0,
+                             float *S_final, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Gradients of mesa_ssm_forward_chunked for dout = dL/dout and, optionally, dS_final = dL/dS_final.  With R_t the
+ * adjoint of S_t (R_t = a_{t+1} R_{t+1} + dout_t q_t^T):
+ *     dq_t = S_t^T dout_t,   dk_t = D_t R_t^T v_t,   dv_t = D_t R_t k_t + skip_h dout_t,
+ *     dD_t = v_t . R_t k_t + A_h a_t <R_t, S_{t-1}>,   ddt_t = dD_t sigmoid(dt_t + dt_bias_h),
+ *     dA_h = sum D_t a_t <R_t, S_{t-1}>,   ddt_bias_h = sum ddt_t,   dskip_h = sum dout_t . v_t   (over batch and time).
+ * dq, dk_out [B, Hk, T, dk] (summed over the value heads of a key head), dv_out [B, H, T, dv], ddt [B, H, T] and dA,
+ * ddt_bias, dskip [H] (each NULL or given; the last two only with dt_bias and skip): all of dtype, or, with
+ * dtype | MESA_GATE_GRADS_F32, the last four in fp32 like their parameters.  dS0: NULL or [B, H, dv, dk] fp32 (it may be
+ * dS_final's memory).  The states are recomputed; every sum has a fixed order.  S0 as given to the forward.
+ * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward (MESA_ERR_NONFINITE: dq, dk, dv
+ * or ddt is not finite).
+ */
+size_t mesa_ssm_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
+int mesa_ssm_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q, const void *k,
+                              const void *v, const float *dt, const float *A, const float *dt_bias,
+                              const float *skip, const uint8_t *starts, const void *dout, const float *S0,
+                              const float *dS_final, void *dq, void *dk_out, void *dv_out, void *ddt, void *dA,
+                              void *ddt_bias, void *dskip, float *dS0, void *workspace, size_t workspace_bytes,
+                              cudaStream_t stream);
+
+/*
+ * One recurrent step of the scan for N sequences x H heads, in place on the caller's fp32 states S_state
+ * [N, H, dv, dk] (16-byte aligned).  q, k [N, Hk, dk], v, out [N, H, dv] dtype (q, k 16-byte aligned); dt [N, H] fp32.
+ * Sizes and errors as the forward, with any N * H; a non-finite out is reported through mesa_decode_status.
+ */
+int mesa_ssm_step(int N, int H, int Hk, int dk, int dv, int dtype, float *S_state, const void *q, const void *k,
+                  const void *v, const float *dt, const float *A, const float *dt_bias, const float *skip,
+                  void *out, cudaStream_t stream);
+
+/*
+ * Short causal depthwise convolution of any layer's inputs ("Arquitetura (MesaNet)", "Pre-processamento": the small
+ * window in front of a recurrent layer), here with a bias and SiLU instead of the normalisation of mesa_qk_preprocess:
+ *     y_t[c] = bias[h][c] + sum_{s < W} w[h][c][s] x_{t-s}[c],     out_t = silu(y_t) or y_t.
+ *   x, out [B, H, T, d] dtype (different memory); w [H, d, W], bias [H, d] (or NULL) fp32; starts: NULL or [B, T] bytes,
+ *   not 0 where a packed document begins: taps do not reach before it.
+ *   state0: NULL (zeros) or [B, H, W-1, d] fp32, the inputs before token 0, [.., s, :] the one s + 1 tokens back;
+ *   state_final: NULL or the same of the last token (what a document's start cuts off as zeros), not state0's memory.
+ *   d a multiple of 8, at most 65536; 1 <= W <= 8; B * H <= 65535; activations and states 16-byte aligned.
+ * Arithmetic is fp32; SiLU from the hardware's exponential and division (2^-21).
+ */
+int mesa_causal_conv(int B, int H, int T, int d, int W, int dtype, int silu, const void *x, const float *w,
+                     const float *bias, const uint8_t *starts, const float *state0, float *state_final, void *out,
+                     cudaStream_t stream);
+
+/*
+ * One decode step of mesa_causal_conv: x, out [N, H, d] (out may be x); conv_state [N, H, W-1, d] fp32 in place (the
+ * caller zeroes it where a sequence begins; may be NULL when W = 1).
+ */
+int mesa_causal_conv_step(int N, int H, int d, int W, int dtype, int silu, const void *x, const float *w,
+                          const float *bias, float *conv_state, void *out, cudaStream_t stream);
+
+/*
+ * Gradients of mesa_causal_conv without state0: dx [B, H, T, d] dtype (not x's or dout's memory), dw [H, d, W], dbias
+ * [H, d] fp32 or NULL, overwritten with the sums over batch and time in a fixed order.
+ * workspace: at least mesa_causal_conv_backward_workspace_size() bytes (256-byte aligned); may be NULL without dw and dbias.
+ */
+size_t mesa_causal_conv_backward_workspace_size(int B, int H, int T, int d, int W);
+int mesa_causal_conv_backward(int B, int H, int T, int d, int W, int dtype, int silu, const void *x, const float *w,
+                              const float *bias, const uint8_t *starts, const void *dout, void *dx, float *dw,
+                              float *dbias, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Norms of queries and keys per head with the position rotation in the same pass, for whole sequences or single tokens
+ * (T = 1).  Per row x of d channels: n = x rsqrt(mean(x^2) + eps) w (norm != 0; w NULL: ones; norm = 0: n = x), then the
+ * first R channels turn by the angles pos f_j, in pairs (j, j + R/2) or, interleaved, (2j, 2j + 1):
+ *     out_a = rot_scale (n_a cos - n_b sin),   out_b = rot_scale (n_b cos + n_a sin);   the channels from R on stay n.
+ *   q, q_out [B, H, T, d], k, k_out [B, Hk, T, d] dtype (either head count may be 0: that side is left out; outputs may
+ *   replace their inputs); wq, wk [d] fp32 or NULL; inv_freq [R / 2] fp32, the frequencies f_j as the model wants them
+ *   (scaled for long contexts by the caller); positions: NULL (pos = offset + t) or [B, T] int32, any value.
+ *   d in {16, 32, 64, 128}; R even, 0 <= R <= d (0: no rotation); B * T < 2^31; activations 16-byte aligned.
+ * Arithmetic is fp32; angles are reduced from exact products (pos f_j to 2^-24 of a turn for |pos| < 2^24).
+ */
+int mesa_qk_norm_rotary(int B, int H, int Hk, int T, int d, int R, int dtype, int interleaved, int norm, const void *q,
+                        const void *k, const float *wq, const float *wk, const float *inv_freq,
+                        const int32_t *positions, int offset, float rot_scale, float eps, void *q_out, void *k_out,
+                        cudaStream_t stream);
+
+/*
+ * Gradients of mesa_qk_norm_rotary for dq_out, dk_out (q and k as given to the forward; not read without norm): dq, dk
+ * dtype (each may be its dq_out's or q's memory); dwq, dwk [d] fp32 or NULL, overwritten with the sums over batch, heads
+ * and time in a fixed order.  workspace: at least mesa_qk_norm_rotary_backward_workspace_size() bytes (256-byte
+ * aligned); may be NULL without dwq and dwk.
+ */
+size_t mesa_qk_norm_rotary_backward_workspace_size(int B, int H, int Hk, int T, int d);
+int mesa_qk_norm_rotary_backward(int B, int H, int Hk, int T, int d, int R, int dtype, int interleaved, int norm,
+                                 const void *q, const void *k, const float *wq, const float *wk, const float *inv_freq,
+                                 const int32_t *positions, int offset, float rot_scale, float eps, const void *dq_out,
+                                 const void *dk_out, void *dq, void *dk, float *dwq, float *dwk, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Device status word of the last mesa_forward_chunked (or _save, mesa_backward_chunked,
- * mesa_delta_forward_chunked, mesa_delta_backward_chunked) call that used `workspace` (a call
- * without tokens or units uses none): copies the word to *flags (host) on `stream` and synchronises
+ * mesa_delta_forward_chunked, mesa_delta_backward_chunked, mesa_ssm_forward_chunked,
+ * mesa_ssm_backward_chunked) call that used `workspace` (a call without tokens or units uses none): copies the word to *flags (host) on `stream` and synchronises
  * it.  Bits: 0 (1) a tensor-core kernel's bounded wait for its matrix multiplies gave up --
  * the kernel then waits for the multiplies still in flight, releases its tensor memory and
  * returns, and the affected chunks' outputs are not written; 1 (2) a non-finite output was
@@ -397,7 +513,7 @@ int mesa_forward_status(const void *workspace, cudaStream_t stream, unsigned *fl
 
 /*
  * Device status word of the decode steps (mesa_decode_step, mesa_decode_step_warm,
- * mesa_delta_step) on the current device -- one word per device, shared by every decode call on it: copies it to
+ * mesa_delta_step, mesa_ssm_step) on the current device -- one word per device, shared by every decode call on it: copies it to
  * *flags (host), clears it, both on `stream`, and synchronises `stream`.  Bit 0 (1): a
  * bounded wait for the bulk copy of a unit's H or G gave up (dk = 128; see mesa_decode_step);
  * bit 2 (4): the wait for that copy to land expired too; bit 1 (2): a decode step wrote

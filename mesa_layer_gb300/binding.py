@@ -102,6 +102,32 @@ def load(build_if_missing: bool = True):
     lib.mesa_block_norm_backward.restype = _i
     lib.mesa_block_norm_backward.argtypes = [_i] * 3 + [_vp] * 3 + [_fp] * 3 + [_f] + [_vp] * 5 + [_fp] * 3 + [
         _vp, _sz, _vp]
+    lib.mesa_ssm_workspace_size.restype = _sz
+    lib.mesa_ssm_workspace_size.argtypes = [_i] * 7
+    lib.mesa_ssm_forward_chunked.restype = _i
+    lib.mesa_ssm_forward_chunked.argtypes = [_i] * 7 + [_vp] * 3 + [_fp] * 4 + [_vp, _vp, _fp, _fp, _vp, _sz, _vp]
+    lib.mesa_ssm_backward_workspace_size.restype = _sz
+    lib.mesa_ssm_backward_workspace_size.argtypes = [_i] * 7
+    lib.mesa_ssm_backward_chunked.restype = _i
+    lib.mesa_ssm_backward_chunked.argtypes = [_i] * 7 + [_vp] * 3 + [_fp] * 4 + [_vp, _vp, _fp, _fp] + [_vp] * 7 + [
+        _fp, _vp, _sz, _vp]
+    lib.mesa_ssm_step.restype = _i
+    lib.mesa_ssm_step.argtypes = [_i] * 6 + [_fp] + [_vp] * 3 + [_fp] * 4 + [_vp, _vp]
+    lib.mesa_causal_conv.restype = _i
+    lib.mesa_causal_conv.argtypes = [_i] * 7 + [_vp, _fp, _fp, _vp, _fp, _fp, _vp, _vp]
+    lib.mesa_causal_conv_step.restype = _i
+    lib.mesa_causal_conv_step.argtypes = [_i] * 6 + [_vp, _fp, _fp, _fp, _vp, _vp]
+    lib.mesa_causal_conv_backward_workspace_size.restype = _sz
+    lib.mesa_causal_conv_backward_workspace_size.argtypes = [_i] * 5
+    lib.mesa_causal_conv_backward.restype = _i
+    lib.mesa_causal_conv_backward.argtypes = [_i] * 7 + [_vp, _fp, _fp, _vp, _vp, _vp, _fp, _fp, _vp, _sz, _vp]
+    lib.mesa_qk_norm_rotary.restype = _i
+    lib.mesa_qk_norm_rotary.argtypes = [_i] * 9 + [_vp, _vp, _fp, _fp, _fp, _ip, _i, _f, _f, _vp, _vp, _vp]
+    lib.mesa_qk_norm_rotary_backward_workspace_size.restype = _sz
+    lib.mesa_qk_norm_rotary_backward_workspace_size.argtypes = [_i] * 5
+    lib.mesa_qk_norm_rotary_backward.restype = _i
+    lib.mesa_qk_norm_rotary_backward.argtypes = [_i] * 9 + [_vp, _vp, _fp, _fp, _fp, _ip, _i, _f, _f] + [_vp] * 4 + [
+        _fp, _fp, _vp, _sz, _vp]
     _lib = lib
     return lib
 
@@ -609,6 +635,264 @@ def mesa_block_norm_backward(x, y, dx_out, dh=None, gate=None, w_post=None, res_
                                         _at(dres_scale), _at(dw_pre), _at(workspace), workspace.numel(),
                                         _raw_stream(stream, dev)), "mesa_block_norm_backward")
     return dx, dy, dgate, dw_post, dres_scale, dw_pre
+
+
+def _starts(starts, shape, device):
+    """Check the marks of the documents' first tokens (bool or uint8, or None)."""
+    if starts is not None:
+        if starts.dtype is not torch.bool and starts.dtype is not torch.uint8:
+            raise MesaError(f"starts must be torch.bool or torch.uint8, got {starts.dtype}")
+        _require_all(device, (starts, "starts", starts.dtype, shape))
+    return starts
+
+
+def _ssm_dims(q, k, v, dt, A, dt_bias, skip, starts):
+    """(B, H, Hk, T, dk, dv) of the scan's sequence forms, every shape checked."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise MesaError("q, k must be [B, Hk, T, dk] and v [B, H, T, dv]")
+    _require_cuda(q, "q")
+    B, Hk, T, dk = shape = q.shape
+    _, H, _, dv = v.shape
+    dtype, f32, heads = q.dtype, torch.float32, (H,)
+    _require_all(q.device, (q, "q", dtype, shape), (k, "k", dtype, shape), (v, "v", dtype, (B, H, T, dv)),
+                 (dt, "dt", f32, (B, H, T)), (A, "A", f32, heads), (dt_bias, "dt_bias", f32, heads),
+                 (skip, "skip", f32, heads))
+    _starts(starts, (B, T), q.device)
+    return B, H, Hk, T, dk, dv
+
+
+def mesa_ssm_workspace_size(B, H, Hk, T, dk, dv, dtype) -> int:
+    """Bytes of workspace of mesa_ssm_forward_chunked (dtype: torch.float32 or torch.bfloat16)."""
+    return int(load().mesa_ssm_workspace_size(B, H, Hk, T, dk, dv, _DTYPE_CODES[dtype]))
+
+
+def mesa_ssm_forward_chunked(q, k, v, dt, A, dt_bias=None, skip=None, starts=None, out=None, S0=None, S_final=None,
+                             workspace=None, stream=None):
+    """Selective state space scan over whole sequences (q, k, v: the scan's C, B, x).  q, k [B, Hk, T, dk], v
+    [B, H, T, dv] (fp32 or bf16; Hk divides H), dt [B, H, T] fp32 (before its softplus), A, dt_bias, skip [H] fp32
+    (the last two may be None); starts [B, T] bool or None, set where a packed document begins; S0 [B, H, dv, dk]
+    fp32 or None (zero); S_final [B, H, dv, dk] fp32 or None, written.  Returns out [B, H, T, dv]."""
+    lib = load()
+    code = _dtype_code(q)
+    B, H, Hk, T, dk, dv = _ssm_dims(q, k, v, dt, A, dt_bias, skip, starts)
+    out = _new((B, H, T, dv), q.dtype, q.device, stream) if out is None else out
+    _require_all(q.device, (out, "out", q.dtype, (B, H, T, dv)), (S0, "S0", torch.float32, (B, H, dv, dk)),
+                 (S_final, "S_final", torch.float32, (B, H, dv, dk)))
+    workspace = _workspace(workspace, int(lib.mesa_ssm_workspace_size(B, H, Hk, T, dk, dv, code)), q.device, stream)
+    _check(lib.mesa_ssm_forward_chunked(B, H, Hk, T, dk, dv, code, _at(q), _at(k), _at(v), _at(dt), _at(A), _at(dt_bias),
+                                        _at(skip), _at(starts), _at(out), _at(S0), _at(S_final), _at(workspace),
+                                        workspace.numel(), _raw_stream(stream, q.device)), "mesa_ssm_forward_chunked")
+    return out
+
+
+def mesa_ssm_backward_workspace_size(B, H, Hk, T, dk, dv, dtype) -> int:
+    """Bytes of workspace of mesa_ssm_backward_chunked."""
+    return int(load().mesa_ssm_backward_workspace_size(B, H, Hk, T, dk, dv, _DTYPE_CODES[dtype]))
+
+
+def mesa_ssm_backward_chunked(q, k, v, dt, A, dout, dt_bias=None, skip=None, starts=None, S0=None, dS_final=None,
+                              dq=None, dk=None, dv=None, ddt=None, dA=None, ddt_bias=None, dskip=None, dS0=None,
+                              workspace=None, stream=None, gates_dtype=None):
+    """Gradients of mesa_ssm_forward_chunked given dout = dL/dout (and dS_final = dL/dS_final): returns (dq, dk, dv,
+    ddt, dA, ddt_bias, dskip), None for what the forward did not have; all of q's dtype, the last four of gates_dtype
+    (None: of the first of them that is given, or q's dtype; torch.float32: not rounded, like their parameters); dS0
+    [B, H, dv, dk] fp32, when given, receives dL/dS0."""
+    lib = load()
+    code = _dtype_code(q)
+    B, H, Hk, T, dkk, dvv = _ssm_dims(q, k, v, dt, A, dt_bias, skip, starts)
+    dev, dtype = q.device, q.dtype
+    if gates_dtype is None:
+        given = next((t for t in (ddt, dA, ddt_bias, dskip) if t is not None), q)
+        gates_dtype = given.dtype
+    if gates_dtype is not dtype and gates_dtype is not torch.float32:
+        raise MesaError(f"ddt, dA, ddt_bias and dskip must be {dtype} or {torch.float32}, got {gates_dtype}")
+    if (ddt_bias is not None and dt_bias is None) or (dskip is not None and skip is None):
+        raise MesaError("ddt_bias and dskip need dt_bias and skip")
+    dq = _new(q.shape, dtype, dev, stream) if dq is None else dq
+    dk = _new(q.shape, dtype, dev, stream) if dk is None else dk
+    dv = _new(v.shape, dtype, dev, stream) if dv is None else dv
+    ddt = _new((B, H, T), gates_dtype, dev, stream) if ddt is None else ddt
+    dA = _new((H,), gates_dtype, dev, stream) if dA is None else dA
+    if dt_bias is not None and ddt_bias is None:
+        ddt_bias = _new((H,), gates_dtype, dev, stream)
+    if skip is not None and dskip is None:
+        dskip = _new((H,), gates_dtype, dev, stream)
+    if gates_dtype is torch.float32:
+        code |= MESA_GATE_GRADS_F32
+    state, heads = (B, H, dvv, dkk), (H,)
+    _require_all(dev, (dout, "dout", dtype, v.shape), (dq, "dq", dtype, q.shape), (dk, "dk", dtype, q.shape),
+                 (dv, "dv", dtype, v.shape), (ddt, "ddt", gates_dtype, (B, H, T)), (dA, "dA", gates_dtype, heads),
+                 (ddt_bias, "ddt_bias", gates_dtype, heads), (dskip, "dskip", gates_dtype, heads),
+                 (S0, "S0", torch.float32, state), (dS_final, "dS_final", torch.float32, state),
+                 (dS0, "dS0", torch.float32, state))
+    workspace = _workspace(workspace, int(lib.mesa_ssm_backward_workspace_size(B, H, Hk, T, dkk, dvv, code)), dev, stream)
+    _check(lib.mesa_ssm_backward_chunked(B, H, Hk, T, dkk, dvv, code, _at(q), _at(k), _at(v), _at(dt), _at(A),
+                                         _at(dt_bias), _at(skip), _at(starts), _at(dout), _at(S0), _at(dS_final), _at(dq),
+                                         _at(dk), _at(dv), _at(ddt), _at(dA), _at(ddt_bias), _at(dskip), _at(dS0),
+                                         _at(workspace), workspace.numel(), _raw_stream(stream, dev)),
+           "mesa_ssm_backward_chunked")
+    return dq, dk, dv, ddt, dA, ddt_bias, dskip
+
+
+def mesa_ssm_step(S_state, q, k, v, dt, A, dt_bias=None, skip=None, out=None, stream=None):
+    """One step of the scan in place on S_state [N, H, dv, dk] (fp32).  q, k [N, Hk, dk], v [N, H, dv] (fp32 or bf16),
+    dt [N, H], A, dt_bias, skip [H] fp32.  Returns out [N, H, dv]."""
+    lib = load()
+    code = _dtype_code(q)
+    if q.dim() != 3 or v.dim() != 3:
+        raise MesaError("q, k must be [N, Hk, dk] and v [N, H, dv]")
+    _require_cuda(q, "q")
+    N, Hk, dk = shape = q.shape
+    _, H, dv = v.shape
+    dev, dtype, vshape, f32, heads = q.device, q.dtype, (N, H, dv), torch.float32, (H,)
+    out = _like(v, stream) if out is None else out
+    _require_all(dev, (q, "q", dtype, shape), (k, "k", dtype, shape), (v, "v", dtype, vshape), (dt, "dt", f32, (N, H)),
+                 (A, "A", f32, heads), (dt_bias, "dt_bias", f32, heads), (skip, "skip", f32, heads),
+                 (S_state, "S_state", f32, (N, H, dv, dk)), (out, "out", dtype, vshape))
+    _check(lib.mesa_ssm_step(N, H, Hk, dk, dv, code, _at(S_state), _at(q), _at(k), _at(v), _at(dt), _at(A), _at(dt_bias),
+                             _at(skip), _at(out), _raw_stream(stream, dev)), "mesa_ssm_step")
+    return out
+
+
+def _conv_dims(x, w, bias, tokens):
+    """(B, H, T, d, W) of the causal convolution, x [B, H, T, d] (tokens) or [N, H, d], every shape checked."""
+    if x.dim() != (4 if tokens else 3) or w.dim() != 3:
+        raise MesaError(f"x must be {'[B, H, T, d]' if tokens else '[N, H, d]'} and w [H, d, W]")
+    _require_cuda(x, "x")
+    B, H, d, W = x.shape[0], x.shape[1], x.shape[-1], w.shape[-1]
+    _require_all(x.device, (x, "x", x.dtype, x.shape), (w, "w", torch.float32, (H, d, W)), (bias, "bias", torch.float32, (H, d)))
+    return B, H, x.shape[2] if tokens else 1, d, W
+
+
+def mesa_causal_conv(x, w, bias=None, silu=True, starts=None, state0=None, state_final=None, out=None, stream=None):
+    """Causal depthwise convolution over time, with a bias and SiLU: x [B, H, T, d] (fp32 or bf16), w [H, d, W], bias
+    [H, d] fp32 or None; starts [B, T] bool or None, set where a packed document begins; state0 [B, H, W-1, d] fp32 or
+    None (zeros), the inputs before token 0, [.., s, :] s + 1 tokens back; state_final, when given, receives the same
+    of the last token.  Returns out [B, H, T, d]."""
+    lib = load()
+    code = _dtype_code(x)
+    B, H, T, d, W = _conv_dims(x, w, bias, True)
+    _starts(starts, (B, T), x.device)
+    out = _like(x, stream) if out is None else out
+    state = (B, H, W - 1, d)
+    _require_all(x.device, (out, "out", x.dtype, x.shape), (state0, "state0", torch.float32, state),
+                 (state_final, "state_final", torch.float32, state))
+    _check(lib.mesa_causal_conv(B, H, T, d, W, code, bool(silu), _at(x), _at(w), _at(bias), _at(starts), _at(state0),
+                                _at(state_final), _at(out), _raw_stream(stream, x.device)), "mesa_causal_conv")
+    return out
+
+
+def mesa_causal_conv_step(x, w, conv_state, bias=None, silu=True, out=None, stream=None):
+    """One decode step of mesa_causal_conv: x [N, H, d]; conv_state [N, H, W-1, d] fp32, updated in place (None when
+    W = 1).  Returns out [N, H, d]."""
+    lib = load()
+    code = _dtype_code(x)
+    N, H, _, d, W = _conv_dims(x, w, bias, False)
+    out = _like(x, stream) if out is None else out
+    _require_all(x.device, (conv_state, "conv_state", torch.float32, (N, H, W - 1, d)), (out, "out", x.dtype, x.shape))
+    _check(lib.mesa_causal_conv_step(N, H, d, W, code, bool(silu), _at(x), _at(w), _at(bias), _at(conv_state), _at(out),
+                                     _raw_stream(stream, x.device)), "mesa_causal_conv_step")
+    return out
+
+
+def mesa_causal_conv_backward_workspace_size(B, H, T, d, W) -> int:
+    return int(load().mesa_causal_conv_backward_workspace_size(B, H, T, d, W))
+
+
+def mesa_causal_conv_backward(x, w, dout, bias=None, silu=True, starts=None, dx=None, dw=None, dbias=None, workspace=None,
+                              stream=None):
+    """Gradients of mesa_causal_conv (no state0) given dout = dL/dout.  Returns (dx, dw, dbias), dbias None without
+    bias; dw and dbias are fp32 sums over batch and time."""
+    lib = load()
+    code = _dtype_code(x)
+    B, H, T, d, W = _conv_dims(x, w, bias, True)
+    _starts(starts, (B, T), x.device)
+    if dbias is not None and bias is None:
+        raise MesaError("dbias needs bias")
+    dx = _like(x, stream) if dx is None else dx
+    dw = _like(w, stream) if dw is None else dw
+    dbias = _like(bias, stream) if dbias is None and bias is not None else dbias
+    _require_all(x.device, (dout, "dout", x.dtype, x.shape), (dx, "dx", x.dtype, x.shape), (dw, "dw", torch.float32, w.shape),
+                 (dbias, "dbias", torch.float32, (H, d)))
+    workspace = _workspace(workspace, int(lib.mesa_causal_conv_backward_workspace_size(B, H, T, d, W)), x.device, stream)
+    _check(lib.mesa_causal_conv_backward(B, H, T, d, W, code, bool(silu), _at(x), _at(w), _at(bias), _at(starts), _at(dout),
+                                         _at(dx), _at(dw), _at(dbias), _at(workspace), workspace.numel(),
+                                         _raw_stream(stream, x.device)), "mesa_causal_conv_backward")
+    return dx, dw, dbias
+
+
+def _rotary_dims(q, k, wq, wk, inv_freq, positions, norm):
+    """(B, H, Hk, T, d, R) of the norm and rotation, every shape checked."""
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise MesaError("q must be [B, H, T, d] and k [B, Hk, T, d]")
+    _require_cuda(q, "q")
+    B, H, T, d = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    if not norm and (wq is not None or wk is not None):
+        raise MesaError("wq and wk need norm")
+    if inv_freq is not None and inv_freq.dim() != 1:
+        raise MesaError("inv_freq must be [R / 2]")
+    R = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if R > d:
+        raise MesaError(f"inv_freq may hold {d // 2} frequencies at most, got {R // 2}")
+    f32, weight = torch.float32, (d,)
+    _require_all(q.device, (q, "q", q.dtype, q.shape), (k, "k", q.dtype, (B, Hk, T, d)), (wq, "wq", f32, weight),
+                 (wk, "wk", f32, weight), (inv_freq, "inv_freq", f32, (R // 2,)),
+                 (positions, "positions", torch.int32, (B, T)))
+    return B, H, Hk, T, d, R
+
+
+def mesa_qk_norm_rotary(q, k=None, wq=None, wk=None, inv_freq=None, positions=None, offset=0, interleaved=False,
+                        rot_scale=1.0, norm=True, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Per-head RMS norm of queries and keys (norm; weights wq, wk [d] fp32 or None: ones) and, with inv_freq [R/2] fp32,
+    the rotation of their first R channels by pos * inv_freq, in pairs (j, j + R/2) or, interleaved, (2j, 2j + 1), times
+    rot_scale.  q [B, H, T, d], k [B, Hk, T, d] or None (fp32 or bf16); positions [B, T] int32, or None: offset + t.
+    The outputs may be the inputs.  Returns (q_out, k_out), k_out None without k."""
+    lib = load()
+    code = _dtype_code(q)
+    B, H, Hk, T, d, R = _rotary_dims(q, k, wq, wk, inv_freq, positions, norm)
+    q_out = _like(q, stream) if q_out is None else q_out
+    k_out = _like(k, stream) if k_out is None and k is not None else k_out
+    _require_all(q.device, (q_out, "q_out", q.dtype, q.shape), (k_out, "k_out", q.dtype, (B, Hk, T, d)))
+    _check(lib.mesa_qk_norm_rotary(B, H, Hk, T, d, R, code, bool(interleaved), bool(norm), _at(q), _at(k), _at(wq), _at(wk),
+                                   _at(inv_freq), _at(positions), int(offset), rot_scale, eps, _at(q_out), _at(k_out),
+                                   _raw_stream(stream, q.device)), "mesa_qk_norm_rotary")
+    return q_out, k_out
+
+
+def mesa_qk_norm_rotary_backward_workspace_size(B, H, Hk, T, d) -> int:
+    return int(load().mesa_qk_norm_rotary_backward_workspace_size(B, H, Hk, T, d))
+
+
+def mesa_qk_norm_rotary_backward(q, k, dq_out, dk_out=None, wq=None, wk=None, inv_freq=None, positions=None, offset=0,
+                                 interleaved=False, rot_scale=1.0, norm=True, eps=1e-6, dq=None, dk=None, dwq=None,
+                                 dwk=None, workspace=None, stream=None):
+    """Gradients of mesa_qk_norm_rotary given dq_out and dk_out (with k).  Returns (dq, dk, dwq, dwk), None for what
+    the forward did not have; dwq and dwk [d] are fp32 sums over batch, heads and time."""
+    lib = load()
+    code = _dtype_code(q)
+    B, H, Hk, T, d, R = _rotary_dims(q, k, wq, wk, inv_freq, positions, norm)
+    if (k is None) != (dk_out is None):
+        raise MesaError("dk_out and k come together")
+    if (dwq is not None and wq is None) or (dwk is not None and wk is None):
+        raise MesaError("dwq and dwk need wq and wk")
+    if k is None and wk is not None:
+        raise MesaError("wk needs k")
+    dev, dtype, f32, weight = q.device, q.dtype, torch.float32, (d,)
+    dq = _like(q, stream) if dq is None else dq
+    dk = _like(k, stream) if dk is None and k is not None else dk
+    dwq = _new(weight, f32, dev, stream) if dwq is None and wq is not None else dwq
+    dwk = _new(weight, f32, dev, stream) if dwk is None and wk is not None else dwk
+    kshape = (B, Hk, T, d)
+    _require_all(dev, (dq_out, "dq_out", dtype, q.shape), (dk_out, "dk_out", dtype, kshape), (dq, "dq", dtype, q.shape),
+                 (dk, "dk", dtype, kshape), (dwq, "dwq", f32, weight), (dwk, "dwk", f32, weight))
+    workspace = _workspace(workspace, int(lib.mesa_qk_norm_rotary_backward_workspace_size(B, H, Hk, T, d)), dev, stream)
+    _check(lib.mesa_qk_norm_rotary_backward(B, H, Hk, T, d, R, code, bool(interleaved), bool(norm), _at(q), _at(k), _at(wq),
+                                            _at(wk), _at(inv_freq), _at(positions), int(offset), rot_scale, eps,
+                                            _at(dq_out), _at(dk_out), _at(dq), _at(dk), _at(dwq), _at(dwk),
+                                            _at(workspace), workspace.numel(), _raw_stream(stream, dev)),
+           "mesa_qk_norm_rotary_backward")
+    return dq, dk, dwq, dwk
 
 
 def mesa_forward_status(workspace, stream=None) -> int:

@@ -219,6 +219,19 @@ const char *mesa_kernel_name(int kind) {
     case mesa::K_RULE_JOIN: return "mesa_rule_join_kernel|mesa_rule_join_adjoint_kernel|mesa_rule_scan_join_kernel";
     case mesa::K_RULE_ADJOINT: return "mesa_rule_adjoint_kernel";
     case mesa::K_NORM_COLS: return "mesa_block_norm_cols_kernel";
+    case mesa::K_SSM_STATES: return "mesa_ssm_states_kernel";
+    case mesa::K_SSM_SCAN: return "mesa_ssm_scan_kernel";
+    case mesa::K_SSM_OUT: return "mesa_ssm_out_kernel";
+    case mesa::K_SSM_STEP: return "mesa_ssm_step_kernel";
+    case mesa::K_SSM_GRADS: return "mesa_ssm_grads_kernel";
+    case mesa::K_SSM_PARAMS: return "mesa_ssm_params_kernel";
+    case mesa::K_CONV: return "mesa_causal_conv_kernel";
+    case mesa::K_CONV_STEP: return "mesa_causal_conv_step_kernel";
+    case mesa::K_CONV_BWD: return "mesa_causal_conv_bwd_kernel";
+    case mesa::K_CONV_COLS: return "mesa_causal_conv_cols_kernel";
+    case mesa::K_ROTARY: return "mesa_qk_norm_rotary_kernel";
+    case mesa::K_ROTARY_BWD: return "mesa_qk_norm_rotary_bwd_kernel";
+    case mesa::K_ROTARY_COLS: return "mesa_qk_norm_rotary_cols_kernel";
   }
   return nullptr;
 }

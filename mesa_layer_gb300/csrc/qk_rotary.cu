@@ -1,0 +1,346 @@
+// qk_rotary.cu -- norms of queries and keys per head with the position rotation in the same pass, and their gradients.
+//
+// Per row x of d channels: n = x rsqrt(mean(x^2) + eps) w; the first R channels turn by the angles pos f_j,
+//     o_a = s (n_a cos - n_b sin),   o_b = s (n_b cos + n_a sin),
+// in pairs (a, b) = (j, j + R/2) or (2j, 2j + 1).  So o_c = n_c C_c + n_{pair(c)} S_c with C = s cos, S = -s sin for
+// a, s sin for b, and C = 1, S = 0 past R.  L = d / VEC lanes hold a row; a lane takes the angles of its channels once for a token and
+// walks over heads, so that the sines cost little and what bounds it is memory.  Gradients turn back
+// (n_c <- g_c C_c - g_{pair(c)} S_c) and go through the norm:
+//     dx = r (m - xn mean(m xn)),   m = dn w,   xn = x r,   dw = sum over rows of dn xn.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "launch.h"
+#include "mixer_ops.h"
+
+namespace mesa {
+
+namespace {
+
+constexpr int kBlock = 256;
+enum Pairs { kNone = 0, kNeighbours = 1, kHalves = 2, kAnyHalves = 3 };  // kHalves: R/2 a multiple of a lane's channels
+
+template <typename TIO>
+struct Row;
+template <>
+struct Row<float> {
+  static constexpr int VEC = 4;
+  using Raw = uint4;
+  __device__ static void unpack(Raw r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+  }
+  __device__ static Raw pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Row<__nv_bfloat16> {
+  static constexpr int VEC = 8;
+  using Raw = uint4;
+  __device__ static void unpack(Raw r, float (&v)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  __device__ static Raw pack(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// cos and sin of pos f, for any 32-bit position: the turns pos f / (2 pi) as a sum of exact parts (the position in two
+// pieces of 19 and 12 bits, f / (2 pi) in two fp32 values), whole turns taken out of each.
+__device__ __forceinline__ void rotation(int pos, float f, float &c, float &s) {
+  constexpr float kHi = 0.15915494f, kLo = 6.4206383e-9f;  // 1 / (2 pi) = kHi + kLo
+  const float g = f * kHi, gl = fmaf(f, kHi, -g) + f * kLo;
+  const float a = (float)(pos & ~4095), b = (float)(pos & 4095);
+  float p = a * g, q = b * g;
+  const float e = (fmaf(a, g, -p) + fmaf(b, g, -q)) + (a * gl + b * gl);
+  p -= rintf(p);
+  q -= rintf(q);
+  float t = (p + q) + e;
+  t -= rintf(t);
+  sincospif(2.0f * t, &s, &c);
+}
+
+// A lane's share of a token's rotation: C and S of its channels c0 ..
+template <int VEC, int PAIRS>
+__device__ __forceinline__ void token_angles(const RotaryArgs &a, size_t token, int c0, float (&C)[VEC], float (&S)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; i++) C[i] = 1.0f, S[i] = 0.0f;
+  if constexpr (PAIRS == kNone) return;
+  const int pos = a.positions ? a.positions[token] : a.offset + (int)(token % a.T), half = a.R / 2;
+  float co, si;
+  if constexpr (PAIRS == kNeighbours) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) {
+      if (c0 + i >= a.R) continue;
+      rotation(pos, a.inv_freq[(c0 + i) / 2], co, si);
+      C[i] = C[i + 1] = a.rot_scale * co;
+      S[i] = -a.rot_scale * si;
+      S[i + 1] = a.rot_scale * si;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i++) {
+      const int c = c0 + i;
+      if (c >= a.R) continue;
+      rotation(pos, a.inv_freq[c < half ? c : c - half], co, si);
+      C[i] = a.rot_scale * co;
+      S[i] = c < half ? -a.rot_scale * si : a.rot_scale * si;
+    }
+  }
+}
+
+// The pairs' values of this lane's channels of one row (raw: the lane's own; row: the row in memory).
+template <typename TIO, int PAIRS>
+__device__ __forceinline__ void pairs_of(const RotaryArgs &a, const TIO *row, uint4 raw, int c0, float (&p)[Row<TIO>::VEC]) {
+  constexpr int VEC = Row<TIO>::VEC;
+  const int half = a.R / 2;
+  if constexpr (PAIRS == kNeighbours) {
+    float v[VEC];
+    Row<TIO>::unpack(raw, v);
+#pragma unroll
+    for (int i = 0; i < VEC; i++) p[i] = v[i ^ 1];
+  } else if constexpr (PAIRS == kHalves) {  // another lane's channels, in the same places
+    const int lane = threadIdx.x & 31, from = c0 < half ? lane + half / VEC : c0 < a.R ? lane - half / VEC : lane;
+    raw.x = __shfl_sync(0xffffffffu, raw.x, from);
+    raw.y = __shfl_sync(0xffffffffu, raw.y, from);
+    raw.z = __shfl_sync(0xffffffffu, raw.z, from);
+    raw.w = __shfl_sync(0xffffffffu, raw.w, from);
+    Row<TIO>::unpack(raw, p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i++) {
+      const int c = c0 + i;
+      p[i] = c < half ? ld(row, c + half) : c < a.R ? ld(row, c - half) : 0.0f;
+    }
+  }
+}
+__device__ __forceinline__ float lanes_sum(float x, int L) {
+  for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// L lanes a token, grid.y groups of `heads` heads (the query heads, then the key heads).  The lanes past the last
+// token work on it and write nothing.  Outputs may replace inputs: a warp reads its rows before it writes.
+template <typename TIO, int PAIRS>
+__global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_kernel(RotaryArgs a, int heads) {
+  using R = Row<TIO>;
+  constexpr int VEC = R::VEC, BATCH = 4;
+  const int L = a.d / VEC, c0 = (threadIdx.x % L) * VEC;
+  const size_t tokens = (size_t)a.B * a.T, mine = ((size_t)blockIdx.x * kBlock + threadIdx.x) / L;
+  const bool in = mine < tokens;
+  const size_t token = in ? mine : tokens - 1, b = token / a.T, t = token % a.T;
+  float C[VEC], S[VEC];
+  token_angles<VEC, PAIRS>(a, token, c0, C, S);
+  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.H + a.Hk);
+  for (int h = h0; h < h1; h += BATCH) {
+    uint4 raw[BATCH];
+    float p[BATCH][VEC];
+    const TIO *row[BATCH];
+    TIO *out[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; i++) {
+      const int hh = min(h + i, h1 - 1);
+      const bool isq = hh < a.H;
+      const size_t at = ((b * (isq ? a.H : a.Hk) + (isq ? hh : hh - a.H)) * a.T + t) * a.d;
+      row[i] = static_cast<const TIO *>(isq ? a.q : a.k) + at;
+      out[i] = static_cast<TIO *>(isq ? a.q_out : a.k_out) + at;
+      raw[i] = *reinterpret_cast<const uint4 *>(row[i] + c0);
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; i++)
+      if constexpr (PAIRS != kNone) pairs_of<TIO, PAIRS>(a, row[i], raw[i], c0, p[i]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < BATCH; i++) {
+      float x[VEC];
+      R::unpack(raw[i], x);
+      float r = 1.0f;
+      const float *w = nullptr;
+      if (a.norm) {
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VEC; j++) ss = fmaf(x[j], x[j], ss);
+        r = rsqrtf(lanes_sum(ss, L) / a.d + a.eps);
+        w = h + i < a.H ? a.wq : a.wk;
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const int c = c0 + j;
+        float n = x[j] * r, m = 0.0f;
+        if constexpr (PAIRS != kNone) m = p[i][j] * r;
+        if (w) {
+          n *= w[c];
+          if constexpr (PAIRS == kNeighbours) m *= w[c ^ 1];
+          if constexpr (PAIRS >= kHalves) m *= w[c < a.R / 2 ? c + a.R / 2 : c < a.R ? c - a.R / 2 : c];
+        }
+        x[j] = PAIRS == kNone ? n : fmaf(m, S[j], n * C[j]);
+      }
+      if (in && h + i < h1) *reinterpret_cast<uint4 *>(out[i] + c0) = R::pack(x);
+    }
+  }
+}
+
+// A resident grid walks over the tokens; sums of the weights' gradients stay in registers until the end.
+template <typename TIO, int PAIRS>
+__global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_bwd_kernel(RotaryArgs a) {
+  using R = Row<TIO>;
+  constexpr int VEC = R::VEC, BATCH = 2;
+  __shared__ float sums[kBlock][VEC + 1];
+  const int L = a.d / VEC, c0 = (threadIdx.x % L) * VEC, per = kBlock / L;
+  const size_t tokens = (size_t)a.B * a.T;
+  float dw[2][VEC] = {};
+  for (size_t first = (size_t)blockIdx.x * per; first < tokens; first += (size_t)gridDim.x * per) {
+    const size_t mine = first + threadIdx.x / L;
+    const bool in = mine < tokens;
+    const size_t token = in ? mine : tokens - 1, b = token / a.T, t = token % a.T;
+    float C[VEC], S[VEC];
+    token_angles<VEC, PAIRS>(a, token, c0, C, S);
+#pragma unroll
+    for (int which = 0; which < 2; which++) {
+      const int H = which == 0 ? a.H : a.Hk;
+      const TIO *xs = static_cast<const TIO *>(which == 0 ? a.q : a.k), *gs = static_cast<const TIO *>(which == 0 ? a.dq_out : a.dk_out);
+      TIO *ds = static_cast<TIO *>(which == 0 ? a.q_out : a.k_out);
+      const float *w = which == 0 ? a.wq : a.wk;
+      for (int h = 0; h < H; h += BATCH) {
+        uint4 xr[BATCH], gr[BATCH];
+        float p[BATCH][VEC];
+        size_t at[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; i++) {
+          at[i] = ((b * H + min(h + i, H - 1)) * a.T + t) * a.d;
+          gr[i] = *reinterpret_cast<const uint4 *>(gs + at[i] + c0);
+          if (a.norm) xr[i] = *reinterpret_cast<const uint4 *>(xs + at[i] + c0);
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; i++)
+          if constexpr (PAIRS != kNone) pairs_of<TIO, PAIRS>(a, gs + at[i], gr[i], c0, p[i]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < BATCH; i++) {
+          const bool on = in && h + i < H;
+          float g[VEC];
+          R::unpack(gr[i], g);
+          if constexpr (PAIRS != kNone) {
+#pragma unroll
+            for (int j = 0; j < VEC; j++) g[j] = fmaf(-p[i][j], S[j], g[j] * C[j]);
+          }
+          if (a.norm) {
+            float x[VEC], ss = 0.0f, mx = 0.0f;
+            R::unpack(xr[i], x);
+#pragma unroll
+            for (int j = 0; j < VEC; j++) {
+              ss = fmaf(x[j], x[j], ss);
+              mx = fmaf(w ? g[j] * w[c0 + j] : g[j], x[j], mx);
+            }
+            const float r = rsqrtf(lanes_sum(ss, L) / a.d + a.eps), mean = lanes_sum(mx, L) * r / a.d;
+#pragma unroll
+            for (int j = 0; j < VEC; j++) {
+              const float xn = x[j] * r;
+              if (on) dw[which][j] = fmaf(g[j], xn, dw[which][j]);
+              g[j] = r * ((w ? g[j] * w[c0 + j] : g[j]) - xn * mean);
+            }
+          }
+          if (on) *reinterpret_cast<uint4 *>(ds + at[i] + c0) = R::pack(g);
+        }
+      }
+    }
+  }
+  if (!a.partial) return;
+#pragma unroll
+  for (int which = 0; which < 2; which++) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < VEC; j++) sums[threadIdx.x][j] = dw[which][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.d; c += kBlock) {
+      float x = 0.0f;
+      for (int r = 0; r < per; r++) x += sums[r * L + c / VEC][c % VEC];
+      a.partial[((size_t)blockIdx.x * 2 + which) * a.d + c] = x;
+    }
+  }
+}
+
+// A warp a channel over the CTAs' sums.
+__global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_cols_kernel(RotaryArgs a, int parts) {
+  const int i = (blockIdx.x * kBlock + threadIdx.x) / 32, lane = threadIdx.x & 31;
+  if (i >= 2 * a.d) return;
+  float x = 0.0f;
+  for (int p = lane; p < parts; p += 32) x += a.partial[(size_t)p * 2 * a.d + i];
+  x = warp_sum(x);
+  float *dst = i < a.d ? a.dwq : a.dwk;
+  if (lane == 0 && dst) dst[i % a.d] = x;
+}
+
+int pairs_kind(const RotaryArgs &a) {
+  const int vec = a.dtype == 1 ? 8 : 4;
+  return a.R == 0 ? kNone : a.interleaved ? kNeighbours : a.R / 2 % vec == 0 ? kHalves : kAnyHalves;
+}
+template <typename F>
+int by_pairs(int kind, F f) {
+  switch (kind) {
+    case kNone: return f(std::integral_constant<int, kNone>());
+    case kNeighbours: return f(std::integral_constant<int, kNeighbours>());
+    case kHalves: return f(std::integral_constant<int, kHalves>());
+    default: return f(std::integral_constant<int, kAnyHalves>());
+  }
+}
+int done() { return cudaPeekAtLastError() == cudaSuccess ? 0 : -1; }
+
+template <typename TIO>
+int forward(const RotaryArgs &a, cudaStream_t st) {
+  const size_t blocks = ((size_t)a.B * a.T * (a.d / Row<TIO>::VEC) + kBlock - 1) / kBlock;
+  if (blocks > 0x7fffffff) return -1;
+  // all heads of a token in one thread where that fills the SMs twice, else fewer
+  int heads = a.H + a.Hk;
+  while (heads > 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 16) heads = (heads + 1) / 2;
+  if (heads <= 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 4) heads = 1;
+  return by_pairs(pairs_kind(a), [&](auto p) {
+    timing_mark_begin(K_ROTARY, st);
+    mesa_qk_norm_rotary_kernel<TIO, decltype(p)::value>
+        <<<dim3((unsigned)blocks, (a.H + a.Hk + heads - 1) / heads), kBlock, 0, st>>>(a, heads);
+    timing_mark_end(K_ROTARY, st);
+    return done();
+  });
+}
+template <typename TIO>
+int backward(const RotaryArgs &a, cudaStream_t st) {
+  const int parts = rotary_bwd_parts(a.B, a.H, a.Hk, a.T, a.d);
+  return by_pairs(pairs_kind(a), [&](auto p) {
+    timing_mark_begin(K_ROTARY_BWD, st);
+    mesa_qk_norm_rotary_bwd_kernel<TIO, decltype(p)::value><<<parts, kBlock, 0, st>>>(a);
+    timing_mark_end(K_ROTARY_BWD, st);
+    if (a.partial) {
+      timing_mark_begin(K_ROTARY_COLS, st);
+      mesa_qk_norm_rotary_cols_kernel<<<(2 * a.d * 32 + kBlock - 1) / kBlock, kBlock, 0, st>>>(a, parts);
+      timing_mark_end(K_ROTARY_COLS, st);
+    }
+    return done();
+  });
+}
+
+}  // namespace
+
+// Four CTAs for each of a GB300's 152 SMs, no more than there are tokens for (16 a CTA at d = 128).
+int rotary_bwd_parts(int B, int, int, int T, int d) {
+  const size_t n = ((size_t)B * T * (d / 4) + kBlock - 1) / kBlock;
+  return n < 1 ? 1 : n < 152 * 4 ? (int)n : 152 * 4;
+}
+
+int launch_qk_norm_rotary(const RotaryArgs &a, cudaStream_t st) {
+  return a.dtype == 1 ? forward<__nv_bfloat16>(a, st) : forward<float>(a, st);
+}
+int launch_qk_norm_rotary_backward(const RotaryArgs &a, cudaStream_t st) {
+  return a.dtype == 1 ? backward<__nv_bfloat16>(a, st) : backward<float>(a, st);
+}
+
+}  // namespace mesa

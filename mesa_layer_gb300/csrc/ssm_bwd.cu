@@ -1,0 +1,288 @@
+// ssm_bwd.cu -- gradients of the selective state space scan on the CUDA cores.
+//
+// With S the state before a chunk of 32 tokens, R the adjoint of the state after it (both from ssm.cu's passes), g =
+// dL/do, E_ij = e^{l_i - l_j} (0 for j > i and across starts), f_i the decay from before the chunk, c_j to its end:
+//     W = (g V^T) o E D,   dq = f (g S) + W K,   dk = W^T Q + c D (V R),
+//     du = ((Q K^T) o E)^T g + c (K R^T),   dv = D du + skip g,
+//     d log a_t = sum over readers i >= t (or the state after) and writers j < t (or the state before) of what passes
+//     between them: (Q K^T o W) inside the chunk, f (g S) . q into it, c D (V R) . k out of it, <R, S> across,
+//     d dt = (du . v + A d log a) sigmoid(dt + bias),   dA = sum D d log a.
+// The pairs are summed as they are, never as a difference of sums, so that a gate's gradient is as exact as its terms.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "gated_delta.h"
+#include "launch.h"
+#include "ssm_simt.cuh"
+
+namespace mesa {
+
+using namespace ssm;
+
+int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoint, cudaStream_t st);
+
+namespace {
+
+__device__ __forceinline__ float sum16(float x) {  // over a row's 16 threads
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// grid (NC, U)
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, SsmWorkspace ws) {
+  constexpr int LK = DK + 4, LV = DV + 4;
+  extern __shared__ float4 smem4[];
+  float *q = reinterpret_cast<float *>(smem4), *k = q + C * LK, *v = k + C * LK, *g = v + C * LV, *S = g + C * LV,
+        *M = S + DV * LK, *W = M + C * LDC;
+  __shared__ Gates ga;
+  __shared__ float X[C][C + 1], x_in[C], x_out[C], duv[C], gv[C], across[kThreads / 32];
+  const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0), h = u % a.H;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
+  const size_t at = ((size_t)u * NC + c) * a.dv * a.dk;
+  load_rows<DK, C>(q, a.q, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
+  load_rows<DK, C>(k, a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
+  load_rows<DV, C>(v, a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
+  load_rows<DV, C>(g, a.dout, a.dtype, (size_t)u * a.T + t0, n, a.dv);
+  load_rows<DK, DV>(S, ws.S + at, 0, 0, a.dv, a.dk);
+  if (warp == 0) gates_load(ga, a, u, t0, n, lane);
+  __syncthreads();
+  {
+    float G[2][2], Hm[2][2];
+    zero(G);
+    zero(Hm);
+    mm_nt<DK>(G, q, LK, k, LK, ty, tx);
+    mm_nt<DV>(Hm, g, LV, v, LV, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const int r = ty + 16 * i, t = tx + 16 * j;
+        const bool on = t <= r && t >= ga.s[r];
+        const float d = ga.decay(r, t), w = on ? Hm[i][j] * d * ga.step[t] : 0.0f;
+        M[r * LDC + t] = on ? G[i][j] * d : 0.0f;
+        W[r * LDC + t] = w;
+        X[r][t] = on && t < r ? G[i][j] * w : 0.0f;
+        if (r == t) gv[r] = Hm[i][j];
+      }
+  }
+  const bool own = ws.dqp == nullptr;  // every head has its own q, k
+  const size_t krow = (own ? (size_t)a.qk_unit(u) : (size_t)u) * a.T + t0, vrow = (size_t)u * a.T + t0;
+  bool bad = false;
+  {
+    float acc[2][DK / 16];
+    zero(acc);
+    mm_nn<DV>(acc, g, LV, S, LK, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int r = ty + 16 * i;
+      const float f = ga.f[r];
+      float x = 0.0f;
+#pragma unroll
+      for (int j = 0; j < DK / 16; j++) {
+        acc[i][j] = ga.s[r] < 0 ? acc[i][j] * f : 0.0f;
+        x = fmaf(acc[i][j], q[r * LK + tx + 16 * j], x);
+      }
+      x = sum16(x);
+      if (tx == 0) x_in[r] = x;
+    }
+    __syncthreads();  // M, W, X
+    mm_nn<C>(acc, W, LDC, k, LK, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int j = 0; j < DK / 16; j++)
+        if (ty + 16 * i < n && tx + 16 * j < a.dk) {
+          bad |= !isfinite(acc[i][j]);
+          store(own ? a.dq : ws.dqp, !own || a.dtype == 0, (krow + ty + 16 * i) * a.dk + tx + 16 * j, acc[i][j]);
+        }
+  }
+  {  // R takes S's place
+    constexpr int N4 = DV * DK / 4 / kThreads;
+    float4 r[N4];
+    float x = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N4; i++) {
+      const int e = tid + i * kThreads, p = e / (DK / 4), cc = 4 * (e % (DK / 4));
+      r[i] = p < a.dv && cc < a.dk ? *reinterpret_cast<const float4 *>(ws.R + at + (size_t)p * a.dk + cc) : make_float4(0, 0, 0, 0);
+      const float4 s = *reinterpret_cast<const float4 *>(S + p * LK + cc);
+      x = fmaf(r[i].x, s.x, fmaf(r[i].y, s.y, fmaf(r[i].z, s.z, fmaf(r[i].w, s.w, x))));
+    }
+    x = warp_sum(x);
+    if (lane == 0) across[warp] = x;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N4; i++) {
+      const int e = tid + i * kThreads;
+      *reinterpret_cast<float4 *>(S + e / (DK / 4) * LK + 4 * (e % (DK / 4))) = r[i];
+    }
+    // X[i][t] <- sum over j < t (a warp: four rows)
+#pragma unroll
+    for (int i = warp; i < C; i += kThreads / 32) {
+      float x = X[i][lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const float before = __shfl_up_sync(0xffffffffu, x, 1);
+      X[i][lane] = lane > 0 ? before : 0.0f;
+    }
+    __syncthreads();
+  }
+  const float *R = S;
+  {
+    float acc[2][DK / 16];
+    zero(acc);
+    mm_nn<DV>(acc, v, LV, R, LK, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int r = ty + 16 * i;
+      const float w = ga.c[r] * ga.step[r];
+      float x = 0.0f;
+#pragma unroll
+      for (int j = 0; j < DK / 16; j++) {
+        acc[i][j] *= w;
+        x = fmaf(acc[i][j], k[r * LK + tx + 16 * j], x);
+      }
+      x = sum16(x);
+      if (tx == 0) x_out[r] = x;
+    }
+    mm_tn<C>(acc, W, LDC, q, LK, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int j = 0; j < DK / 16; j++)
+        if (ty + 16 * i < n && tx + 16 * j < a.dk) {
+          bad |= !isfinite(acc[i][j]);
+          store(own ? a.dk_out : ws.dkp, !own || a.dtype == 0, (krow + ty + 16 * i) * a.dk + tx + 16 * j, acc[i][j]);
+        }
+  }
+  {
+    const float skip = a.skip ? a.skip[h] : 0.0f;
+    float acc[2][DV / 16];
+    zero(acc);
+    mm_nt<DK>(acc, k, LK, R, LK, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int j = 0; j < DV / 16; j++) acc[i][j] *= ga.c[ty + 16 * i];
+    mm_tn<C>(acc, M, LDC, g, LV, ty, tx);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int r = ty + 16 * i;
+      float x = 0.0f;
+#pragma unroll
+      for (int j = 0; j < DV / 16; j++) {
+        const int p = tx + 16 * j;
+        x = fmaf(acc[i][j], v[r * LV + p], x);
+        if (r < n && p < a.dv) {
+          const float o = ga.step[r] * acc[i][j], y = a.skip ? fmaf(skip, g[r * LV + p], o) : o;
+          bad |= !isfinite(y);
+          store(a.dv_out, a.dtype == 0, (vrow + r) * a.dv + p, y);
+        }
+      }
+      x = sum16(x);
+      if (tx == 0) duv[r] = x;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {  // token `lane`
+    const int t = lane;
+    float in = x_in[t], out = x_out[t], all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; i++) all += across[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {  // readers from t on, writers up to t
+      const float y = __shfl_down_sync(0xffffffffu, in, o), z = __shfl_up_sync(0xffffffffu, out, o);
+      if (lane + o < 32) in += y;
+      if (lane >= o) out += z;
+    }
+    out = __shfl_up_sync(0xffffffffu, out, 1);
+    if (lane == 0) out = 0.0f;
+    float pairs = 0.0f;
+    for (int i = t; i < C; i++) pairs += X[i][t];
+    const bool start = ga.s[t] == t;
+    const float left = ga.s[C - 1] < 0 ? ga.f[C - 1] * all : 0.0f;
+    const float da = start ? 0.0f : pairs + in + out + left;
+    const float dstep = fmaf(a.A[h], da, duv[t]);
+    const float draw = t < n ? dstep * sigmoid(ga.raw[t]) : 0.0f;
+    if (t < n) {
+      bad |= !isfinite(draw);
+      store(a.ddt, a.gates_f32 || a.dtype == 0, vrow + t, draw);
+    }
+    const float sA = warp_sum(t < n ? ga.step[t] * da : 0.0f), sb = warp_sum(draw), sg = warp_sum(t < n ? gv[t] : 0.0f);
+    if (lane == 0) {
+      const size_t UN = (size_t)gridDim.y * NC, i = (size_t)u * NC + c;
+      ws.sums[i] = sA;
+      ws.sums[UN + i] = sb;
+      ws.sums[2 * UN + i] = sg;
+    }
+  }
+  if (bad) atomicOr(a.status, tc_err_nonfinite());
+}
+
+// grid (H, 3): one parameter's gradient of one head, the sum over its units' chunks in a fixed order.
+__global__ void __launch_bounds__(256) mesa_ssm_params_kernel(SsmArgs a, const float *sums, int n) {
+  __shared__ float part[8];
+  const int h = blockIdx.x, which = blockIdx.y;
+  void *dst = which == 0 ? a.dA : which == 1 ? a.dbias : a.dskip;
+  if (!dst) return;
+  const size_t U = (size_t)a.units();
+  float x = 0.0f;
+  for (int b = 0; b < a.B; b++) {
+    const float *s = sums + (which * U + (size_t)b * a.H + h) * n;
+    float y = 0.0f;
+    for (int i = threadIdx.x; i < n; i += 256) y += s[i];
+    x += y;
+  }
+  x = warp_sum(x);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    x = 0.0f;
+    for (int i = 0; i < 8; i++) x += part[i];
+    store(dst, a.gates_f32 || a.dtype == 0, h, x);
+  }
+}
+
+template <int DK, int DV>
+struct Grads {
+  static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, cudaStream_t st) {
+    const size_t smem = sizeof(float) * (2 * C * (DK + 4) + 2 * C * (DV + 4) + DV * (DK + 4) + 2 * C * LDC);
+    timing_mark_begin(K_SSM_GRADS, st);
+    const bool ok = launch(mesa_ssm_grads_kernel<DK, DV>, dim3(NC, a.units()), smem, st, a, ws);
+    timing_mark_end(K_SSM_GRADS, st);
+    return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  }
+};
+
+}  // namespace
+
+int launch_ssm_param_sums(const SsmArgs &a, const float *sums, int n, cudaStream_t st) {
+  if (!a.dA && !a.dbias && !a.dskip) return 0;
+  timing_mark_begin(K_SSM_PARAMS, st);
+  mesa_ssm_params_kernel<<<dim3(a.H, 3), 256, 0, st>>>(a, sums, n);
+  timing_mark_end(K_SSM_PARAMS, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+int launch_ssm_group_sum(const SsmArgs &a, const float *dqp, const float *dkp, cudaStream_t st) {
+  RuleArgs r{a.B, a.H, a.Hk, a.T, a.dk, a.dv, a.dtype};  // the same sum as the delta rule's
+  r.dq = a.dq;
+  r.dk_out = a.dk_out;
+  r.status = a.status;
+  return launch_rule_group_sum(r, dqp, dkp, st);
+}
+
+int launch_ssm_backward(const SsmArgs &a, const SsmWorkspace &ws, cudaStream_t st) {
+  const int NC = (a.T + C - 1) / C;
+  if (launch_ssm_states(a, ws, false, st) != 0 || launch_ssm_states(a, ws, true, st) != 0) return -1;
+  if (by_size<Grads>(a.dk, a.dv, a, ws, NC, st) != 0) return -1;
+  if (ws.dqp && launch_ssm_group_sum(a, ws.dqp, ws.dkp, st) != 0) return -1;
+  return launch_ssm_param_sums(a, ws.sums, NC, st);
+}
+
+}  // namespace mesa

@@ -1,0 +1,158 @@
+// ssm_simt.cuh -- what the CUDA-core kernels of the selective scan share: the gates of a chunk of 32 tokens, rows in
+// shared memory as fp32, and small products by 16 x 16 threads.
+#pragma once
+
+#include "ssm.h"
+#include "ssm_common.cuh"
+
+namespace mesa {
+namespace ssm {
+
+constexpr int C = kSsmChunk;  // a warp's lanes: one token each
+constexpr int kThreads = 256;
+constexpr int LDC = C + 4;    // row stride of a [C x C] matrix
+
+struct Gates {
+  float step[C], hi[C], lo[C];  // lengths of the steps; log2 decay from the chunk's start
+  int s[C];                     // the last start up to a token, -1: none in the chunk
+  float f[C], c[C];             // decay from before the chunk to a token, from a token to the chunk's end
+  float raw[C];
+  __device__ __forceinline__ float decay(int i, int j) const {  // from token j to token i >= j
+    return j <= i && j >= s[i] ? exp2f((hi[i] - hi[j]) + (lo[i] - lo[j])) : 0.0f;
+  }
+};
+
+// By one warp: the gates of tokens t0 .. t0 + n - 1 of unit u (the others do nothing).
+__device__ __forceinline__ void gates_load(Gates &g, const SsmArgs &a, int u, int t0, int n, int lane) {
+  const int h = u % a.H, b = u / a.H;
+  const bool in = lane < n;
+  const float raw = in ? a.dt[(size_t)u * a.T + t0 + lane] + (a.dt_bias ? a.dt_bias[h] : 0.0f) : 0.0f;
+  const float step = in ? softplus(raw) : 0.0f;
+  const bool start = in && a.starts && a.starts[(size_t)b * a.T + t0 + lane];
+  Two l = start ? Two{0.0f, 0.0f} : log2_decay(step, a.A[h]);
+  int s = start ? lane : -1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two p = {__shfl_up_sync(0xffffffffu, l.hi, o), __shfl_up_sync(0xffffffffu, l.lo, o)};
+    const int ps = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) {
+      l = two_add(p, l);
+      s = max(s, ps);
+    }
+  }
+  const Two end = {__shfl_sync(0xffffffffu, l.hi, 31), __shfl_sync(0xffffffffu, l.lo, 31)};
+  const int send = __shfl_sync(0xffffffffu, s, 31);
+  g.step[lane] = step;
+  g.hi[lane] = l.hi;
+  g.lo[lane] = l.lo;
+  g.s[lane] = s;
+  g.raw[lane] = raw;
+  g.f[lane] = s < 0 ? exp2f(l.hi + l.lo) : 0.0f;
+  g.c[lane] = lane >= send ? exp2f(two_sub(end, l)) : 0.0f;
+}
+
+// n rows of d channels (fp32 or bf16) to fp32 rows of D channels, stride D + 4, what is missing as zeros.
+template <int D, int ROWS>
+__device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype, size_t first, int n, int d) {
+  for (int i = threadIdx.x; i < ROWS * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+    float4 x = make_float4(0, 0, 0, 0);
+    if (r < n && c < d) {
+      const size_t at = (first + r) * d + c;
+      x = dtype == 1 ? load4(static_cast<const __nv_bfloat16 *>(src), at) : load4(static_cast<const float *>(src), at);
+    }
+    *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+  }
+}
+__device__ __forceinline__ void store(void *p, bool f32, size_t i, float x) {
+  if (f32)
+    static_cast<float *>(p)[i] = x;
+  else
+    static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+}
+
+// Products by 16 x 16 threads (ty, tx): this thread's rows ty + 16 i, columns tx + 16 j.
+// acc += A B^T, A [.][K], B [.][K] (row strides lda, ldb).
+template <int K, int RI, int CJ>
+__device__ __forceinline__ void mm_nt(float (&acc)[RI][CJ], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
+#pragma unroll 4
+  for (int k = 0; k < K; k += 4) {
+    float4 x[RI];
+#pragma unroll
+    for (int i = 0; i < RI; i++) x[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * lda + k);
+#pragma unroll
+    for (int j = 0; j < CJ; j++) {
+      const float4 y = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + k);
+#pragma unroll
+      for (int i = 0; i < RI; i++)
+        acc[i][j] = fmaf(x[i].w, y.w, fmaf(x[i].z, y.z, fmaf(x[i].y, y.y, fmaf(x[i].x, y.x, acc[i][j]))));
+    }
+  }
+}
+// acc += A B, A [.][K], B [K][.].
+template <int K, int RI, int CJ>
+__device__ __forceinline__ void mm_nn(float (&acc)[RI][CJ], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
+#pragma unroll 2
+  for (int k = 0; k < K; k += 4) {
+    float4 x[RI];
+#pragma unroll
+    for (int i = 0; i < RI; i++) x[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * lda + k);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+#pragma unroll
+      for (int j = 0; j < CJ; j++) {
+        const float y = B[(k + e) * ldb + tx + 16 * j];
+#pragma unroll
+        for (int i = 0; i < RI; i++) acc[i][j] = fmaf(e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w, y, acc[i][j]);
+      }
+  }
+}
+// acc += A^T B, A [K][.], B [K][.].
+template <int K, int RI, int CJ>
+__device__ __forceinline__ void mm_tn(float (&acc)[RI][CJ], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
+#pragma unroll 4
+  for (int k = 0; k < K; k++) {
+    float x[RI], y[CJ];
+#pragma unroll
+    for (int i = 0; i < RI; i++) x[i] = A[k * lda + ty + 16 * i];
+#pragma unroll
+    for (int j = 0; j < CJ; j++) y[j] = B[k * ldb + tx + 16 * j];
+#pragma unroll
+    for (int i = 0; i < RI; i++)
+#pragma unroll
+      for (int j = 0; j < CJ; j++) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+  }
+}
+template <int RI, int CJ>
+__device__ __forceinline__ void zero(float (&acc)[RI][CJ]) {
+#pragma unroll
+  for (int i = 0; i < RI; i++)
+#pragma unroll
+    for (int j = 0; j < CJ; j++) acc[i][j] = 0.0f;
+}
+
+// Sizes are padded to 32, 64 or 128 channels in shared memory (16 to 32).
+template <template <int, int> class F, typename... Args>
+int by_size(int dk, int dv, Args &&...args) {
+  auto k = [&](auto dkc) {
+    constexpr int DK = decltype(dkc)::value;
+    if (dv <= 32) return F<DK, 32>::run(args...);
+    if (dv == 64) return F<DK, 64>::run(args...);
+    return F<DK, 128>::run(args...);
+  };
+  if (dk <= 32) return k(std::integral_constant<int, 32>());
+  if (dk == 64) return k(std::integral_constant<int, 64>());
+  return k(std::integral_constant<int, 128>());
+}
+
+// Launch with `smem` bytes of dynamic shared memory (48 KB without being asked for, the static part among them).
+template <typename K, typename... Args>
+bool launch(K kernel, dim3 grid, size_t smem, cudaStream_t st, const Args &...args) {
+  if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  kernel<<<grid, kThreads, smem, st>>>(args...);
+  return true;
+}
+
+}  // namespace ssm
+}  // namespace mesa
