@@ -30,6 +30,9 @@ int check_scan(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   return MESA_OK;
 }
 
+// The tensor-core path: bf16, dk = 128, dv 64 or 128.
+bool scan_tc(int dtype, int dk, int dv) { return dtype == MESA_BF16 && dk == 128 && (dv == 64 || dv == 128); }
+
 // Workspace of the CUDA-core path: [status | S | decay], and for the backward [R | sums | per-head dq, dk].
 size_t scan_parts(int B, int H, int Hk, int T, int dk, int dv, bool backward, mesa::SsmWorkspace *ws, char *base) {
   const size_t U = (size_t)B * H, NC = ((size_t)T + mesa::kSsmChunk - 1) / mesa::kSsmChunk;
@@ -58,6 +61,7 @@ extern "C" {
 
 size_t mesa_ssm_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   if (check_scan(B, H, Hk, T, dk, dv, dtype) != MESA_OK) return 0;
+  if (scan_tc(dtype, dk, dv)) return kStatusBytes + mesa::ssm_tc_workspace(B * H, T, dv);
   return scan_parts(B, H, Hk, T, dk, dv, false, nullptr, nullptr);
 }
 
@@ -84,6 +88,8 @@ int mesa_ssm_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dt
   a.status = (unsigned *)workspace;
   a.wait_limit = mesa::wait_limit();
   if (bad_memset(workspace, sizeof(unsigned), stream)) return MESA_ERR_CUDA;
+  if (scan_tc(dtype, dk, dv))
+    return mesa::launch_ssm_forward_tc(a, (char *)workspace + kStatusBytes, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
   mesa::SsmWorkspace ws;
   scan_parts(B, H, Hk, T, dk, dv, false, &ws, (char *)workspace);
   return mesa::launch_ssm_forward(a, ws, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;

@@ -97,7 +97,7 @@ enum KernelKind {
   K_RULE_STEP = 19, K_NORM = 20, K_NORM_BWD = 21, K_NORM_COLS = 22, K_RULE_PREP = 23, K_RULE_CHAIN = 24,
   K_RULE_ADJOINT = 25, K_RULE_SEGMENT = 26, K_RULE_JOIN = 27, K_SSM_STATES = 28, K_SSM_SCAN = 29, K_SSM_OUT = 30,
   K_SSM_STEP = 31, K_SSM_GRADS = 32, K_SSM_PARAMS = 33, K_CONV = 34, K_CONV_STEP = 35, K_CONV_BWD = 36, K_CONV_COLS = 37,
-  K_ROTARY = 38, K_ROTARY_BWD = 39, K_ROTARY_COLS = 40, K_NUM_KINDS = 41
+  K_ROTARY = 38, K_ROTARY_BWD = 39, K_ROTARY_COLS = 40, K_SSM_FORWARD = 41, K_SSM_CHAIN = 42, K_NUM_KINDS = 43
 };
 
 // Record a timing event before / after a launch of `kind` on `st` (no-op unless enabled).
@@ -138,6 +138,9 @@ bool tmap_rows128_f32(CUtensorMap *map, float *base, size_t rows);
 // Tensor map of a [units, T, 128] bf16 array (16-byte aligned) with boxes of 64 channels x 64
 // tokens of one unit and the 128-byte swizzle; tokens past T read as zero.
 bool tmap_units128_bf16(CUtensorMap *map, const void *base, int units, int T);
+// Tensor map of a [units, T, d] bf16 array (16-byte aligned) with boxes of 64 channels x 128 tokens of one unit and the
+// 128-byte swizzle; tokens past T read as zero and are not written.
+bool tmap_units_bf16(CUtensorMap *map, const void *base, int units, int T, int d);
 // The backward pass's 32-token chunk states (bwd = false) or state adjoints (bwd = true) on
 // the tensor cores, d = 128 (sweep_tc.cu).
 int launch_sweep_tc(const BwdArgs &a, const FwdWorkspace &ws, bool bwd, cudaStream_t st);
