@@ -222,6 +222,7 @@ const char *mesa_kernel_name(int kind) {
     case mesa::K_SSM_STATES: return "mesa_ssm_states_kernel";
     case mesa::K_SSM_SCAN: return "mesa_ssm_scan_kernel|mesa_ssm_join_kernel";
     case mesa::K_SSM_FORWARD: return "mesa_ssm_forward_tc_kernel";
+    case mesa::K_SSM_GATES: return "mesa_ssm_gates_kernel";
     case mesa::K_SSM_CHAIN: return "mesa_ssm_chain_tc_kernel";
     case mesa::K_SSM_OUT: return "mesa_ssm_out_kernel";
     case mesa::K_SSM_STEP: return "mesa_ssm_step_kernel";

@@ -97,7 +97,8 @@ enum KernelKind {
   K_RULE_STEP = 19, K_NORM = 20, K_NORM_BWD = 21, K_NORM_COLS = 22, K_RULE_PREP = 23, K_RULE_CHAIN = 24,
   K_RULE_ADJOINT = 25, K_RULE_SEGMENT = 26, K_RULE_JOIN = 27, K_SSM_STATES = 28, K_SSM_SCAN = 29, K_SSM_OUT = 30,
   K_SSM_STEP = 31, K_SSM_GRADS = 32, K_SSM_PARAMS = 33, K_CONV = 34, K_CONV_STEP = 35, K_CONV_BWD = 36, K_CONV_COLS = 37,
-  K_ROTARY = 38, K_ROTARY_BWD = 39, K_ROTARY_COLS = 40, K_SSM_FORWARD = 41, K_SSM_CHAIN = 42, K_NUM_KINDS = 43
+  K_ROTARY = 38, K_ROTARY_BWD = 39, K_ROTARY_COLS = 40, K_SSM_FORWARD = 41, K_SSM_CHAIN = 42, K_SSM_GATES = 43,
+  K_NUM_KINDS = 44
 };
 
 // Record a timing event before / after a launch of `kind` on `st` (no-op unless enabled).

@@ -3,11 +3,10 @@
 //
 // In a chunk of 128 tokens, S the state before it, f_i the decay from before the chunk to token i, E_ij from token j to i:
 //     O = f (Q S^T) + M V + skip V,   M = (Q K^T) o E D,     S' = f_end S + (w V)^T K, w_j = E_{end,j} D_j.
-// One CTA per SM walks a unit's chunks (or those of a segment of it) with the state in tensor memory; q, k and v are read
-// and o is written once.  Warps: four turn Q K^T into M and write the outputs, four weigh K's rows and turn the state
-// into the next operand, one issues the products, one the copies.  Two chains run side by side, Q K^T -> M -> M V and
-// state -> Q S^T -> state, each about 2.5 k cycles a chunk, while a chunk's 128 KB take 5.9 k at an SM's share of the
-// memory's rate.
+// The gates come first, a record for each chunk (2.6 KB beside its 128).  Then one CTA per SM walks a unit's chunks (or
+// those of a segment of it) with the state in tensor memory; q, k and v are read and o is written once.  Warps: four turn
+// Q K^T into M, four write the outputs, four weigh K's rows, four turn the state into the next operand, one issues the
+// products, one the copies.  Two chains run side by side, Q K^T -> M -> M V and state -> Q S^T -> state.
 #include "launch.h"
 #include "ssm_tc.cuh"
 
@@ -17,6 +16,54 @@ using namespace ssm;
 
 namespace {
 
+// grid (NC, U), a thread a token: the chunks' records.  (In the chain's own warps the two scans of sums, the exponentials
+// and the logarithm were on its way: 225 us for 8 x 16 x 4096, against 0000 with this before it.)
+__global__ void __launch_bounds__(L) mesa_ssm_gates_kernel(SsmArgs a, float *records) {
+  __shared__ float thi[4], tlo[4];
+  __shared__ int ts[4];
+  const int u = blockIdx.y, h = u % a.H, c = blockIdx.x, t = threadIdx.x, w = t >> 5, lane = t & 31, at = c * L + t;
+  float *r = records + ((size_t)u * gridDim.x + c) * REC;
+  float raw = -INFINITY;  // (past the end: nothing is forgotten, nothing written)
+  bool start = false;
+  if (at < a.T) {
+    raw = a.dt[(size_t)u * a.T + at] + (a.dt_bias ? a.dt_bias[h] : 0.0f);
+    start = a.starts && a.starts[(size_t)(u / a.H) * a.T + at];
+  }
+  const float step = softplus(raw);
+  Two l = start ? Two{0.0f, 0.0f} : log2_decay(step, a.A[h]);
+  int s = start ? t : -1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two p = {__shfl_up_sync(0xffffffffu, l.hi, o), __shfl_up_sync(0xffffffffu, l.lo, o)};
+    const int ps = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) {
+      l = two_add(p, l);
+      s = max(s, ps);
+    }
+  }
+  if (lane == 31) thi[w] = l.hi, tlo[w] = l.lo, ts[w] = s;
+  const Two end = {__shfl_sync(0xffffffffu, l.hi, 31), __shfl_sync(0xffffffffu, l.lo, 31)};
+  const int send = __shfl_sync(0xffffffffu, s, 31);
+  r[R_OUT + t] = t >= send ? exp2f(two_sub(end, l)) : 0.0f;
+  r[R_IN + t] = s < 0 ? exp2f(l.hi + l.lo) : 0.0f;
+  r[R_LOG + t] = l.hi + l.lo;
+  r[R_STEP + t] = step;
+  __syncthreads();
+  int before = -1;
+  for (int i = 0; i < w; i++) before = max(before, ts[i]);
+  r[R_START + t] = __int_as_float(max(s, before));
+  if (t < 32) {  // decays over whole warps' tokens, from..to
+    const int from = t < 16 ? t % 4 + 1 : t < 20 ? 0 : t < 24 ? t - 20 + 1 : 0, to = t < 16 ? t / 4 : t < 20 ? t - 16 : 4;
+    Two d = {0.0f, 0.0f};
+    bool cut = false;
+    for (int i = from; i < to; i++) {
+      d = two_add(d, Two{thi[i], tlo[i]});
+      cut |= ts[i] >= 0;
+    }
+    r[R_BETWEEN + t] = cut ? 0.0f : exp2f(d.hi + d.lo);
+  }
+}
+
 constexpr uint32_t T_G = 0, T_Y1 = 128, T_Y2 = 256, T_S = 384;  // tensor memory columns; M replaces Q K^T
 
 // shared memory: two q tiles | two k tiles | two v tiles | the state as an operand | misc
@@ -25,20 +72,22 @@ struct Fwd {
   static constexpr uint32_t K = 2 * QK_TILE, V = 4 * QK_TILE, S = V + 2 * V_TILE<P>, MISC = S + V_TILE<P>;
 };
 struct FwdMisc {
-  float cw[L], local[L], step[L];  // step e^(log-decay from a token to its warp's end); for the diagonal blocks
-  WarpTotals tot[2][2];
-  uint64_t full[2], y_staged[2], g_full, m_full, y_full, y_free, s_full, hi_full, cs_done, lo_full, st_done, drain;
+  float cw[2][L], log[L], step[L];  // step and decay from a token to its warp's end; for the diagonal blocks
+  uint64_t full[2], y_staged[2], st_done[2], g_full, m_full, y_full, y_free, s_full, hi_full, cs_done, lo_full, drain;
   uint32_t tmem;
   int gave_up;
 };
 template <int P>
 constexpr uint32_t kFwdSmem = Fwd<P>::MISC + sizeof(FwdMisc);
 static_assert(kFwdSmem<128> <= 232448, "shared memory per block");
+// Registers a thread of the five groups of four warps (96 at launch).
+constexpr int kRegM = 96, kRegY = 128, kRegW = 128, kRegS = 96, kRegIssue = 32;
+static_assert(kRegM + kRegY + kRegW + kRegS + kRegIssue <= 5 * 96, "register file");
 
-// grid (U, segments), 320 threads.
+// grid (U, segments), 640 threads.
 template <int P>
-__global__ void __launch_bounds__(320, 1)
-    mesa_ssm_forward_tc_kernel(SsmArgs a, SsmSegments sg, const __grid_constant__ CUtensorMap mapQ,
+__global__ void __launch_bounds__(640, 1)
+    mesa_ssm_forward_tc_kernel(SsmArgs a, SsmSegments sg, const float *records, const __grid_constant__ CUtensorMap mapQ,
                                const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                                const __grid_constant__ CUtensorMap mapO) {
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -53,11 +102,12 @@ __global__ void __launch_bounds__(320, 1)
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
-  if (warp == 8) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
-  if (tid == 288) {
-    for (uint64_t *b : {&m->full[0], &m->full[1], &m->g_full, &m->y_full, &m->cs_done, &m->st_done, &m->drain})
+  if (warp == 16) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
+  if (tid == 544) {
+    for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->g_full, &m->y_full, &m->cs_done, &m->drain})
       tc::mbar_init(bar(*b), 1);
-    for (uint64_t *b : {&m->m_full, &m->y_free, &m->y_staged[0], &m->y_staged[1], &m->s_full, &m->hi_full, &m->lo_full}) tc::mbar_init(bar(*b), 4);
+    for (uint64_t *b : {&m->m_full, &m->y_free, &m->y_staged[0], &m->y_staged[1], &m->s_full, &m->hi_full, &m->lo_full})
+      tc::mbar_init(bar(*b), 4);
     m->gave_up = 0;
   }
   tc::fence_before_sync();
@@ -68,225 +118,242 @@ __global__ void __launch_bounds__(320, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
   };
+  // a warp's wait; once a lane has given up, the warp has
   bool ok = true;
-  int sent = 0;  // tiles asked for (warp 9)
+  auto need = [&](uint64_t &b, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, ok && wait(bar(b), parity, limit, gave_up));
+    tc::fence_after_sync();
+    return ok;
+  };
+  int sent = 0;  // tiles asked for (warp 17)
+  const int t = tid & 127, w = warp & 3;  // token, or lane of the state
+  const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
 
-  if (warp < 8) {
-    const int t = tid & 127, w = warp & 3, group = warp < 4 ? 1 : 2;  // token (or lane of the state) t
-    const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f, A = a.A[h];
-    TokenIn in = token_load(a, u, c0 * L + t);
-    if (warp < 4) {
-      // ---- M, then the outputs ----
-      const float skip = a.skip ? a.skip[h] : 0.0f;
-      uint32_t bad = 0;
-      for (int c = 0; c < NC; c++) {
-        const uint32_t ph = c & 1;
-        uint8_t *X = sm + Fwd<P>::V + ph * V_TILE<P>;
-        const TokenIn now = in;
-        if (c + 1 < NC) in = token_load(a, u, (c0 + c + 1) * L + t);
-        Token g;
-        if (token_gates(g, now, bias, A, m->tot[0][ph], t, group, ok)) {
-          ok = false;
-          break;
-        }
-        // (to the warp's end)
-        const Two wend = {__shfl_sync(0xffffffffu, g.local.hi, 31), __shfl_sync(0xffffffffu, g.local.lo, 31)};
-        m->cw[t] = t >= g.s_warp ? g.step * exp2f(two_sub(wend, g.local)) : 0.0f;
-        m->local[t] = g.local.hi + g.local.lo;
-        m->step[t] = g.step;
-        const float f = g.s < 0 ? exp2_of(g.l) : 0.0f, mine = g.local.hi + g.local.lo;
-        group_or(group, 128, false);
-        ok &= wait(bar(m->g_full), ph, limit, gave_up);
-        tc::fence_after_sync();
-        Two from = {0.0f, 0.0f};  // log2 decay from the chunk's start to the end of block b
+  if (warp < 4) {
+    // ---- M ----
+    regs_set<kRegM>();
+    const float *r = record(records, u, NCT, c0);
+    float out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
+    for (int c = 0; c < NC; c++) {
+      const uint32_t ph = c & 1;
+      const int s = __float_as_int(start);
+      const float mine = log, from = in;
+      float between[3];
 #pragma unroll
-        for (int b = 0; b < 4; b++) {
-          float v[32];
-          uint32_t o[16];
-          if (b <= w) {
-            tc::tmem_ld32(tl + T_G + 32 * b, v);
-            from = two_add(from, Two{m->tot[0][ph].hi[b], m->tot[0][ph].lo[b]});
-          }
-          if (b < w) {  // tokens of an earlier warp: through the end of their block
-            const float r = g.s <= 32 * b + 31 ? exp2f(two_sub(g.before, from) + mine) : 0.0f;
-            tc::tmem_ld_wait();
+      for (int b = 0; b < 3; b++) between[b] = b < w ? r[R_BETWEEN + 4 * w + b] * from : 0.0f;
+      m->cw[ph][t] = out * step;
+      m->log[t] = log;
+      m->step[t] = step;
+      if (c + 1 < NC) {
+        r += REC;
+        out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
+      }
+      if (group_or(1, 128, !ok)) {  // (also: the others' columns)
+        ok = false;
+        break;
+      }
+      need(m->g_full, ph);
+      float v[2][32];
+      tc::tmem_ld32(tl + T_G, v[0]);
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-              const float4 x = *reinterpret_cast<const float4 *>(&m->cw[32 * b + 4 * i]);
-              o[2 * i] = bf2(v[4 * i] * (r * x.x), v[4 * i + 1] * (r * x.y));
-              o[2 * i + 1] = bf2(v[4 * i + 2] * (r * x.z), v[4 * i + 3] * (r * x.w));
-            }
-          } else if (b == w) {
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-              const float4 x = *reinterpret_cast<const float4 *>(&m->local[32 * b + 4 * i]);
-              const float4 y = *reinterpret_cast<const float4 *>(&m->step[32 * b + 4 * i]);
-              const int j = 32 * b + 4 * i;
-              auto one = [&](int jj, float gk, float l, float s) {
-                return jj <= t && jj >= g.s ? gk * (rule::ex2(mine - l) * s) : 0.0f;
-              };
-              o[2 * i] = bf2(one(j, v[4 * i], x.x, y.x), one(j + 1, v[4 * i + 1], x.y, y.y));
-              o[2 * i + 1] = bf2(one(j + 2, v[4 * i + 2], x.z, y.z), one(j + 3, v[4 * i + 3], x.w, y.w));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; i++) o[i] = 0;
-          }
-          float of[16];
-#pragma unroll
-          for (int i = 0; i < 16; i++) of[i] = __uint_as_float(o[i]);
-          tc::tmem_st16(tl + T_G + 16 * b, of);
-        }
-        tc::tmem_st_wait();
-        tc::fence_before_sync();
-        warp_arrive(m->m_full);
-        // outputs
-        ok &= wait(bar(m->full[ph]), (c >> 1) & 1, limit, gave_up);
-        ok &= wait(bar(m->y_full), ph, limit, gave_up);
-        tc::fence_after_sync();
-        uint4 y[P / 8];
-#pragma unroll
-        for (int hh = 0; hh < P / 16; hh++) {
-          float p[16], r[16];
-          tc::tmem_ld16(tl + T_Y1 + 16 * hh, p);
-          tc::tmem_ld16(tl + T_Y2 + 16 * hh, r);
-          uint4 x[2];
-#pragma unroll
-          for (int k = 0; k < 2; k++) x[k] = *reinterpret_cast<const uint4 *>(X + tile_off(t, 2 * hh + k, L));
+      for (int b = 0; b < 4; b++) {
+        uint32_t o[16];
+        if (b <= w) {
           tc::tmem_ld_wait();
+          if (b < w && b < 3) tc::tmem_ld32(tl + T_G + 32 * (b + 1), v[(b + 1) & 1]);
+        }
+        const float *x = v[b & 1];
+        if (b < w) {  // tokens of an earlier warp: through the end of theirs
+          const float f = between[b < 3 ? b : 0];
 #pragma unroll
-          for (int k = 0; k < 2; k++) {
-            const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              const int e = 8 * k + 2 * i;
-              float p0 = f == 0.0f ? r[e] : fmaf(f, p[e], r[e]), p1 = f == 0.0f ? r[e + 1] : fmaf(f, p[e + 1], r[e + 1]);
-              if (a.skip) p0 = fmaf(skip, lo_of(xs[i]), p0), p1 = fmaf(skip, hi_of(xs[i]), p1);
-              o[i] = bf2(p0, p1);
-            }
-            y[2 * hh + k] = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int i = 0; i < 8; i++) {
+            const float4 y = *reinterpret_cast<const float4 *>(&m->cw[ph][32 * b + 4 * i]);
+            o[2 * i] = bf2(x[4 * i] * (f * y.x), x[4 * i + 1] * (f * y.y));
+            o[2 * i + 1] = bf2(x[4 * i + 2] * (f * y.z), x[4 * i + 3] * (f * y.w));
           }
-        }
-        tc::fence_before_sync();
-        warp_arrive(m->y_free);
-        if ((c0 + c) * L + t < a.T) {
+        } else if (b == w) {
 #pragma unroll
-          for (int k = 0; k < P / 8; k++) bad = rule::absmax_words(bad, y[k]);
-        }
-        ok &= wait(bar(m->st_done), ph, limit, gave_up);  // (the products have read V)
+          for (int i = 0; i < 8; i++) {
+            const float4 l = *reinterpret_cast<const float4 *>(&m->log[32 * b + 4 * i]);
+            const float4 y = *reinterpret_cast<const float4 *>(&m->step[32 * b + 4 * i]);
+            const int j = 32 * b + 4 * i;
+            auto one = [&](int jj, float g, float lj, float sj) {
+              return jj <= t && jj >= s ? g * (rule::ex2(mine - lj) * sj) : 0.0f;
+            };
+            o[2 * i] = bf2(one(j, x[4 * i], l.x, y.x), one(j + 1, x[4 * i + 1], l.y, y.y));
+            o[2 * i + 1] = bf2(one(j + 2, x[4 * i + 2], l.z, y.z), one(j + 3, x[4 * i + 3], l.w, y.w));
+          }
+        } else {
 #pragma unroll
-        for (int k = 0; k < P / 8; k++) *reinterpret_cast<uint4 *>(X + tile_off(t, k, L)) = y[k];
-        tc::fence_smem_to_async();
-        warp_arrive(m->y_staged[ph]);
-      }
-      if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
-    } else {
-      // ---- K's rows weighed, the state ----
-      const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
-      for (int c = 0; c < NC; c++) {
-        const uint32_t ph = c & 1;
-        const TokenIn now = in;
-        if (c + 1 < NC) in = token_load(a, u, (c0 + c + 1) * L + t);
-        Token g;
-        if (token_gates(g, now, bias, A, m->tot[1][ph], t, group, ok)) {
-          ok = false;
-          break;
+          for (int i = 0; i < 16; i++) o[i] = 0;
         }
-        const float wt = t >= g.s_end ? g.step * exp2f(two_sub(g.end, g.l)) : 0.0f, all = g.s_end < 0 ? exp2_of(g.end) : 0.0f;
-        if (c > 0) ok &= wait(bar(m->st_done), (c - 1) & 1, limit, gave_up);
-        tc::fence_after_sync();
-        state_step<P>(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0);
-        tc::fence_smem_to_async();
-        tc::fence_before_sync();
-        warp_arrive(m->s_full);
-        ok &= wait(bar(m->full[ph]), (c >> 1) & 1, limit, gave_up);
-        ok &= wait(bar(m->g_full), ph, limit, gave_up);  // (Q K^T has read K)
-        uint4 rest[16];
-        weigh_row(sm + Fwd<P>::K + ph * QK_TILE, t, wt, rest);
-        tc::fence_smem_to_async();
-        warp_arrive(m->hi_full);
-        ok &= wait(bar(m->cs_done), ph, limit, gave_up);  // (Q S^T has read Q)
-        put_row(sm + ph * QK_TILE, t, rest);
-        tc::fence_smem_to_async();
-        warp_arrive(m->lo_full);
+        float of[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) of[i] = __uint_as_float(o[i]);
+        tc::tmem_st16(tl + T_G + 16 * b, of);
       }
-      if (NC > 0) ok &= wait(bar(m->st_done), (NC - 1) & 1, limit, gave_up);
-      tc::fence_after_sync();
-      if (!group_or(group, 128, !ok) && a.S_final && seg == sg.n - 1) state_out<P>(tl + T_S, a.S_final + (size_t)u * P * DK, t);
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      warp_arrive(m->m_full);
     }
-  } else if (warp == 8) {
-    // ---- products ----
-    const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
-                   idS = idesc_bf16(128, P, true, true);
-    const uint32_t sS = tc::smem_u32(sm + Fwd<P>::S);
-    auto need = [&](uint64_t &b, uint32_t parity) {
-      ok &= wait(bar(b), parity, limit, gave_up);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::fence_after_sync();
-      return ok;
-    };
-    auto scores = [&](int c) -> bool {  // Q K^T of chunk c
+  } else if (warp < 8) {
+    // ---- outputs ----
+    regs_set<kRegY>();
+    const float skip = a.skip ? a.skip[h] : 0.0f;
+    const float *r = record(records, u, NCT, c0);
+    float f = r[R_IN + t] * r[R_FIRST + w];
+    uint32_t bad = 0;
+    for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
-      if (!need(m->full[ph], (c >> 1) & 1)) return false;
-      if (elect_one()) {
-        const uint64_t q = tc::kmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
-                       k = tc::kmajor_desc(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), L, 0);
-#pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
-        tc::mma_commit(bar(m->g_full));
+      uint8_t *X = sm + Fwd<P>::V + ph * V_TILE<P>;
+      const float mine = f;
+      if (c + 1 < NC) {
+        r += REC;
+        f = r[R_IN + t] * r[R_FIRST + w];
       }
-      return true;
-    };
-    bool go = scores(0);
-    for (int c = 0; go && c < NC; c++) {
-      const uint32_t ph = c & 1, q = tc::smem_u32(sm + ph * QK_TILE), k = tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE),
-                     v = tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>);
-      const uint64_t vd = tc::mnmajor_desc(v, L, 0), kd = tc::mnmajor_desc(k, L, 0), rd = tc::mnmajor_desc(q, L, 0);
-      go = need(m->s_full, ph) && (c == 0 || need(m->y_free, (c - 1) & 1));
-      if (!go) break;
-      if (elect_one()) {
-        const uint64_t qd = tc::kmajor_desc(q, L, 0), sd = tc::mnmajor_desc(sS, L, 0);
+      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->y_full, ph)) break;
+      uint4 y[P / 8];
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
-        tc::mma_commit(bar(m->cs_done));
-      }
-      if (!(go = need(m->hi_full, ph))) break;
-      if (elect_one()) {
+      for (int hh = 0; hh < P / 16; hh++) {
+        float p[16], q[16];
+        tc::tmem_ld16(tl + T_Y1 + 16 * hh, p);
+        tc::tmem_ld16(tl + T_Y2 + 16 * hh, q);
+        uint4 x[2];
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, kd + step_mn(s), vd + step_mn(s), idS, true);
-      }
-      if (!(go = need(m->m_full, ph))) break;
-      if (elect_one()) {
+        for (int k = 0; k < 2; k++) x[k] = *reinterpret_cast<const uint4 *>(X + tile_off(t, 2 * hh + k, L));
+        tc::tmem_ld_wait();
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16_ts(tbase + T_Y2, tbase + T_G + 8 * s, vd + step_mn(s), idY, s > 0);
-        tc::mma_commit(bar(m->y_full));
-      }
-      if (!(go = need(m->lo_full, ph))) break;
-      if (elect_one()) {
+        for (int k = 0; k < 2; k++) {
+          const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint32_t o[4];
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, rd + step_mn(s), vd + step_mn(s), idS, true);
-        tc::mma_commit(bar(m->st_done));
+          for (int i = 0; i < 4; i++) {
+            const int e = 8 * k + 2 * i;
+            float p0 = mine == 0.0f ? q[e] : fmaf(mine, p[e], q[e]), p1 = mine == 0.0f ? q[e + 1] : fmaf(mine, p[e + 1], q[e + 1]);
+            if (a.skip) p0 = fmaf(skip, lo_of(xs[i]), p0), p1 = fmaf(skip, hi_of(xs[i]), p1);
+            o[i] = bf2(p0, p1);
+          }
+          y[2 * hh + k] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
-      if (c + 1 < NC) go = need(m->y_full, ph) && scores(c + 1);  // (M has been read)
+      tc::fence_before_sync();
+      warp_arrive(m->y_free);
+      if ((c0 + c) * L + t < a.T) {
+#pragma unroll
+        for (int k = 0; k < P / 8; k++) bad = rule::absmax_words(bad, y[k]);
+      }
+      if (!need(m->st_done[ph], (c >> 1) & 1)) break;  // (the products have read V)
+#pragma unroll
+      for (int k = 0; k < P / 8; k++) *reinterpret_cast<uint4 *>(X + tile_off(t, k, L)) = y[k];
+      tc::fence_smem_to_async();
+      warp_arrive(m->y_staged[ph]);
     }
-    ok &= go;
+    if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
+  } else if (warp < 12) {
+    // ---- K's rows weighed ----
+    regs_set<kRegW>();
+    const float *r = record(records, u, NCT, c0);
+    float next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
+    for (int c = 0; c < NC; c++) {
+      const uint32_t ph = c & 1;
+      const float mine = next;
+      if (c + 1 < NC) {
+        r += REC;
+        next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
+      }
+      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->g_full, ph)) break;  // (Q K^T has read K)
+      uint4 rest[16];
+      weigh_row(sm + Fwd<P>::K + ph * QK_TILE, t, mine, rest);
+      tc::fence_smem_to_async();
+      warp_arrive(m->hi_full);
+      if (!need(m->cs_done, ph)) break;  // (Q S^T has read Q)
+      put_row(sm + ph * QK_TILE, t, rest);
+      tc::fence_smem_to_async();
+      warp_arrive(m->lo_full);
+    }
+  } else if (warp < 16) {
+    // ---- the state ----
+    regs_set<kRegS>();
+    const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
+    const float *r = record(records, u, NCT, c0);
+    float next = r[R_ALL];
+    for (int c = 0; c < NC; c++) {
+      const float all = next;
+      if (c + 1 < NC) {
+        r += REC;
+        next = r[R_ALL];
+      }
+      if (c > 0 && !need(m->st_done[(c - 1) & 1], ((c - 1) >> 1) & 1)) break;
+      state_step<P>(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0);
+      tc::fence_smem_to_async();
+      tc::fence_before_sync();
+      warp_arrive(m->s_full);
+    }
+    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && a.S_final && seg == sg.n - 1)
+      state_out<P>(tl + T_S, a.S_final + (size_t)u * P * DK, t);
   } else {
-    // ---- copies ----
-    const int uk = a.qk_unit(u);
-    auto fetch_qk = [&](int c) {
-      const uint32_t ph = c & 1, b = bar(m->full[ph]);
-      tc::mbar_arrive_expect_tx(b, 2 * QK_TILE + V_TILE<P>);
-      load_tile<DK>(tc::smem_u32(sm + ph * QK_TILE), &mapQ, (c0 + c) * L, uk, b);
-      load_tile<DK>(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), &mapK, (c0 + c) * L, uk, b);
-    };
-    auto fetch_v = [&](int c) {
-      const uint32_t ph = c & 1;
-      load_tile<P>(tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>), &mapV, (c0 + c) * L, u, bar(m->full[ph]));
-    };
-    if (lane == 0) {
+    regs_set<kRegIssue>();
+    if (warp == 16) {
+      // ---- products ----
+      const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
+                     idS = idesc_bf16(128, P, true, true);
+      const uint32_t sS = tc::smem_u32(sm + Fwd<P>::S);
+      auto scores = [&](int c) -> bool {  // Q K^T of chunk c
+        const uint32_t ph = c & 1;
+        if (!need(m->full[ph], (c >> 1) & 1)) return false;
+        if (elect_one()) {
+          const uint64_t q = tc::kmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
+                         k = tc::kmajor_desc(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), L, 0);
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
+          tc::mma_commit(bar(m->g_full));
+        }
+        return true;
+      };
+      scores(0);
+      for (int c = 0; ok && c < NC; c++) {
+        const uint32_t ph = c & 1, q = tc::smem_u32(sm + ph * QK_TILE), k = tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE),
+                       v = tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>);
+        const uint64_t vd = tc::mnmajor_desc(v, L, 0), kd = tc::mnmajor_desc(k, L, 0), rd = tc::mnmajor_desc(q, L, 0);
+        if (!need(m->s_full, ph) || (c > 0 && !need(m->y_free, (c - 1) & 1))) break;
+        if (elect_one()) {
+          const uint64_t qd = tc::kmajor_desc(q, L, 0), sd = tc::mnmajor_desc(sS, L, 0);
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
+          tc::mma_commit(bar(m->cs_done));
+        }
+        if (!need(m->hi_full, ph)) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, kd + step_mn(s), vd + step_mn(s), idS, true);
+        }
+        if (!need(m->m_full, ph)) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16_ts(tbase + T_Y2, tbase + T_G + 8 * s, vd + step_mn(s), idY, s > 0);
+          tc::mma_commit(bar(m->y_full));
+        }
+        if (!need(m->lo_full, ph)) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, rd + step_mn(s), vd + step_mn(s), idS, true);
+          tc::mma_commit(bar(m->st_done[ph]));
+        }
+        if (c + 1 < NC && need(m->y_full, ph)) scores(c + 1);  // (M has been read)
+      }
+    } else if (tid == 544) {
+      // ---- copies ----
+      const int uk = a.qk_unit(u);
+      auto fetch_qk = [&](int c) {
+        const uint32_t ph = c & 1, b = bar(m->full[ph]);
+        tc::mbar_arrive_expect_tx(b, 2 * QK_TILE + V_TILE<P>);
+        load_tile<DK>(tc::smem_u32(sm + ph * QK_TILE), &mapQ, (c0 + c) * L, uk, b);
+        load_tile<DK>(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), &mapK, (c0 + c) * L, uk, b);
+      };
+      auto fetch_v = [&](int c) {
+        const uint32_t ph = c & 1;
+        load_tile<P>(tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>), &mapV, (c0 + c) * L, u, bar(m->full[ph]));
+      };
       for (; sent < min(NC, 2); sent++) {
         fetch_qk(sent);
         fetch_v(sent);
@@ -312,13 +379,13 @@ __global__ void __launch_bounds__(320, 1)
   __syncthreads();
   // a wait gave up: products and copies still in flight finish before the memory is released
   if (*gave_up) {
-    if (warp == 8 && elect_one()) tc::mma_commit(bar(m->drain));
+    if (warp == 16 && elect_one()) tc::mma_commit(bar(m->drain));
     if (tid == 0) {
       unsigned bits = tc::kErrMmaTimeout;
       if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
       atomicOr(a.status, bits);
     }
-    if (tid == 288) {
+    if (tid == 544) {
       bool landed = true;
       for (int c = max(0, sent - 2); c < sent; c++)
         landed &= tc::mbar_wait(bar(m->full[c & 1]), (c >> 1) & 1, tc::kWaitLimit);
@@ -327,7 +394,7 @@ __global__ void __launch_bounds__(320, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 8) tc::tmem_free(tbase, 512);
+  if (warp == 16) tc::tmem_free(tbase, 512);
 }
 
 // ---- the states alone ------------------------------------------------------------------------------------
@@ -342,9 +409,7 @@ struct Chain {
   static constexpr uint32_t R = 2 * QK_TILE, V = 4 * QK_TILE, S = V + 2 * V_TILE<P>, MISC = S + V_TILE<P>;
 };
 struct ChainMisc {
-  WarpTotals tot[2][2];
   uint64_t full[2], w_full[2], st_done[2], s_full, kept, drain;
-  float all[2];
   uint32_t tmem;
   int gave_up;
 };
@@ -355,7 +420,7 @@ constexpr uint32_t kChainSmem = Chain<P>::MISC + sizeof(ChainMisc);
 // rows, 4-7 the state, 8 products, 9 copies.  kept: [U, NC][V_TILE] operand tiles.
 template <int P, int MODE>
 __global__ void __launch_bounds__(320, 1)
-    mesa_ssm_chain_tc_kernel(SsmArgs a, SsmSegments sg, uint8_t *kept, const __grid_constant__ CUtensorMap mapK,
+    mesa_ssm_chain_tc_kernel(SsmArgs a, SsmSegments sg, const float *records, uint8_t *kept, const __grid_constant__ CUtensorMap mapK,
                              const __grid_constant__ CUtensorMap mapV) {
   constexpr bool ADJ = MODE == kAdjoint || MODE == kAdjointSegment, KEEP = MODE == kKeep || MODE == kAdjoint;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -365,7 +430,7 @@ __global__ void __launch_bounds__(320, 1)
   }
   ChainMisc *m = reinterpret_cast<ChainMisc *>(sm + Chain<P>::MISC);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int u = blockIdx.x, h = u % a.H, seg = blockIdx.y + (MODE == kAdjointSegment ? 1 : 0), NCT = (a.T + L - 1) / L;
+  const int u = blockIdx.x, seg = blockIdx.y + (MODE == kAdjointSegment ? 1 : 0), NCT = (a.T + L - 1) / L;
   const int c0 = seg * sg.per, NC = sg.n > 1 ? min(NCT - c0, sg.per) : NCT;
   auto chunk = [&](int c) { return ADJ ? c0 + NC - 1 - c : c0 + c; };  // of step c
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
@@ -388,56 +453,56 @@ __global__ void __launch_bounds__(320, 1)
   bool ok = true;
   int sent = 0;
 
-  if (warp < 8) {
-    const int t = tid & 127, w = warp & 3, group = warp < 4 ? 1 : 2;
-    const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f, A = a.A[h];
-    TokenIn in = token_load(a, u, chunk(0) * L + t);
-    float left = 1.0f;  // of a state, after the segment
+  auto need = [&](uint64_t &b, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, ok && wait(bar(b), parity, limit, gave_up));
+    tc::fence_after_sync();
+    return ok;
+  };
+  const int t = tid & 127, w = warp & 3;  // token, or lane of the state
+  const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
+
+  if (warp < 4) {
+    auto weight = [&](int c) {
+      const float *r = record(records, u, NCT, chunk(c));
+      return ADJ ? r[R_IN + t] * r[R_FIRST + w] : r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
+    };
+    float next = weight(0);
+    for (int c = 0; c < NC; c++) {
+      const uint32_t ph = c & 1;
+      const float mine = next;
+      if (c + 1 < NC) next = weight(c + 1);
+      if (c > 1 && !need(m->st_done[ph], ((c - 2) >> 1) & 1)) break;  // (its tiles are free)
+      if (!need(m->full[ph], (c >> 1) & 1)) break;
+      uint4 rest[16];
+      weigh_row(sm + ph * QK_TILE, t, mine, rest);
+      put_row(sm + Chain<P>::R + ph * QK_TILE, t, rest);
+      tc::fence_smem_to_async();
+      warp_arrive(m->w_full[ph]);
+    }
+  } else if (warp < 8) {
     const float *from = nullptr;
     if constexpr (MODE == kKeep) from = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
     if constexpr (MODE == kAdjoint)
       from = sg.n > 1 ? sg.R + ((size_t)u * sg.n + seg) * P * DK : a.dS_final ? a.dS_final + (size_t)u * P * DK : nullptr;
+    float next = record(records, u, NCT, chunk(0))[R_ALL], left = 1.0f;  // (left: of a state, after the segment)
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
-      const TokenIn now = in;
-      if (c + 1 < NC) in = token_load(a, u, chunk(c + 1) * L + t);
-      if (warp < 4 && c > 1) ok &= wait(bar(m->st_done[ph]), ((c - 2) >> 1) & 1, limit, gave_up);  // (its tiles are free)
-      Token g;
-      if (token_gates(g, now, bias, A, m->tot[group - 1][ph], t, group, ok)) {
-        ok = false;
-        break;
-      }
-      const float all = g.s_end < 0 ? exp2_of(g.end) : 0.0f;
-      if (warp < 4) {
-        const float wt = ADJ ? (g.s < 0 ? exp2_of(g.l) : 0.0f) : t >= g.s_end ? g.step * exp2f(two_sub(g.end, g.l)) : 0.0f;
-        ok &= wait(bar(m->full[ph]), (c >> 1) & 1, limit, gave_up);
-        uint4 rest[16];
-        weigh_row(sm + ph * QK_TILE, t, wt, rest);
-        put_row(sm + Chain<P>::R + ph * QK_TILE, t, rest);
-        tc::fence_smem_to_async();
-        warp_arrive(m->w_full[ph]);
-      } else {
-        left *= all;
-        if (c > 0) ok &= wait(bar(m->st_done[ph ^ 1]), ((c - 1) >> 1) & 1, limit, gave_up);
-        if (KEEP && c > 0) ok &= wait(bar(m->kept), (c - 1) & 1, limit, gave_up);  // (the last tile has left)
-        tc::fence_after_sync();
-        state_step<P>(tl + T_G, KEEP ? sm + Chain<P>::S : nullptr, t, all, c == 0, from);
-        if (KEEP) tc::fence_smem_to_async();
-        tc::fence_before_sync();
-        warp_arrive(m->s_full);
-      }
+      const float all = next;
+      if (c + 1 < NC) next = record(records, u, NCT, chunk(c + 1))[R_ALL];
+      left *= all;
+      if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
+      if (KEEP && c > 0 && !need(m->kept, (c - 1) & 1)) break;  // (the last tile has left)
+      state_step<P>(tl + T_G, KEEP ? sm + Chain<P>::S : nullptr, t, all, c == 0, from);
+      if (KEEP) tc::fence_smem_to_async();
+      tc::fence_before_sync();
+      warp_arrive(m->s_full);
     }
-    if (warp >= 4) {
-      if (NC > 0) ok &= wait(bar(m->st_done[(NC - 1) & 1]), ((NC - 1) >> 1) & 1, limit, gave_up);
-      tc::fence_after_sync();
-      float *to = nullptr;
-      if constexpr (MODE == kSegment) to = sg.S + ((size_t)u * sg.n + seg) * P * DK;
-      if constexpr (MODE == kAdjointSegment) to = sg.R + ((size_t)u * sg.n + seg) * P * DK;
-      if constexpr (MODE == kAdjoint) to = a.dS0 && seg == 0 ? a.dS0 + (size_t)u * P * DK : nullptr;
-      if (!group_or(group, 128, !ok) && to) state_out<P>(tl + T_G, to, t);
-      if (!KEEP && t == 0) sg.decay[(size_t)u * sg.n + seg] = left;
-    }
+    float *to = nullptr;
+    if constexpr (MODE == kSegment) to = sg.S + ((size_t)u * sg.n + seg) * P * DK;
+    if constexpr (MODE == kAdjointSegment) to = sg.R + ((size_t)u * sg.n + seg) * P * DK;
+    if constexpr (MODE == kAdjoint) to = a.dS0 && seg == 0 ? a.dS0 + (size_t)u * P * DK : nullptr;
+    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && to) state_out<P>(tl + T_G, to, t);
+    if (!KEEP && t == 0) sg.decay[(size_t)u * sg.n + seg] = left;
   } else if (warp == 8) {
     const uint32_t idS = idesc_bf16(128, P, true, true);
     for (int c = 0; c < NC; c++) {
@@ -523,10 +588,10 @@ __global__ void __launch_bounds__(128) mesa_ssm_join_kernel(SsmArgs a, SsmSegmen
 }
 
 template <typename K, typename... Args>
-bool launch_tc(int kind, K kernel, dim3 grid, uint32_t smem, cudaStream_t st, const Args &...args) {
+bool launch_tc(int kind, K kernel, dim3 grid, int threads, uint32_t smem, cudaStream_t st, const Args &...args) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
   timing_mark_begin(kind, st);
-  kernel<<<grid, 320, smem, st>>>(args...);
+  kernel<<<grid, threads, smem, st>>>(args...);
   timing_mark_end(kind, st);
   return cudaPeekAtLastError() == cudaSuccess;
 }
@@ -538,15 +603,17 @@ int forward(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&o, a.out, a.units(), a.T, P))
     return -1;
   if (sg.n > 1) {
-    if (!launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<P, kSegment>, dim3(a.units(), sg.n - 1), kChainSmem<P>, st, a, sg,
-                   (uint8_t *)nullptr, k, v))
+    if (!launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<P, kSegment>, dim3(a.units(), sg.n - 1), 320, kChainSmem<P>, st, a, sg,
+                   sg.records, (uint8_t *)nullptr, k, v))
       return -1;
     timing_mark_begin(K_SSM_SCAN, st);
     mesa_ssm_join_kernel<<<dim3(P * DK / 512, a.units()), 128, 0, st>>>(a, sg, false);
     timing_mark_end(K_SSM_SCAN, st);
   }
-  return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<P>, dim3(a.units(), sg.n), kFwdSmem<P>, st, a, sg, q, k, v, o) ? 0
-                                                                                                                          : -1;
+  return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<P>, dim3(a.units(), sg.n), 640, kFwdSmem<P>, st, a, sg, sg.records, q, k,
+                   v, o)
+             ? 0
+             : -1;
 }
 
 }  // namespace
@@ -560,19 +627,29 @@ SsmSegments ssm_segments(int U, int T, int dv, bool backward, void *workspace, s
   if (n < 2) n = 1;
   sg.per = (NC + n - 1) / n;
   sg.n = n > 1 ? (NC + sg.per - 1) / sg.per : 1;  // (no empty one)
-  const size_t state = sg.n > 1 ? (size_t)U * sg.n * dv * DK * sizeof(float) : 0,
-               decay = sg.n > 1 ? ((size_t)U * sg.n * sizeof(float) + 255) / 256 * 256 : 0;
-  if (bytes) *bytes = state * (backward ? 2 : 1) + decay;
-  if (sg.n > 1 && workspace) {
-    sg.decay = (float *)workspace;
-    sg.S = (float *)((char *)workspace + decay);
-    if (backward) sg.R = (float *)((char *)sg.S + state);
+  auto up256 = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t state = sg.n > 1 ? (size_t)U * sg.n * dv * DK * sizeof(float) : 0, decay = up256((size_t)U * sg.n * sizeof(float)),
+               recs = up256((size_t)U * NC * REC * sizeof(float));
+  if (bytes) *bytes = recs + decay + state * (backward ? 2 : 1);
+  if (workspace) {
+    sg.records = (float *)workspace;
+    sg.decay = (float *)((char *)workspace + recs);
+    sg.S = (float *)((char *)sg.decay + decay);
+    sg.R = (float *)((char *)sg.S + state);
   }
   return sg;
 }
 
+int launch_ssm_gates(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
+  timing_mark_begin(K_SSM_GATES, st);
+  mesa_ssm_gates_kernel<<<dim3((a.T + L - 1) / L, a.units()), L, 0, st>>>(a, sg.records);
+  timing_mark_end(K_SSM_GATES, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
 int launch_ssm_forward_tc(const SsmArgs &a, void *workspace, cudaStream_t st) {
   const SsmSegments sg = ssm_segments(a.units(), a.T, a.dv, false, workspace, nullptr);
+  if (launch_ssm_gates(a, sg, st) != 0) return -1;
   return a.dv == 128 ? forward<128>(a, sg, st) : forward<64>(a, sg, st);
 }
 size_t ssm_tc_workspace(int U, int T, int dv) {

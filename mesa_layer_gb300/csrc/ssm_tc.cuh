@@ -31,6 +31,12 @@ constexpr uint32_t HALF = L * 64 * 2;
 template <int P>
 constexpr uint32_t V_TILE = L * P * 2;
 
+// The registers of a group of four warps (setmaxnreg), up or down from the 96 that 640 threads start with.
+template <int N>
+__device__ __forceinline__ void regs_set() {
+  if constexpr (N > 96) rule::regs_up<N>();
+  if constexpr (N < 96) rule::regs_down<N>();
+}
 // Instruction descriptor: bf16 operands, fp32 sums.
 __device__ __forceinline__ uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
   return tc::idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);
@@ -42,68 +48,15 @@ __device__ __forceinline__ uint32_t bf2(float a, float b) {  // two bf16 values,
 __device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// A token's gates inside its chunk, thread t of a group of 128: its step; its log2 decay from the chunk's start and from
-// its warp's first token's; the last start up to it (-1: none in the chunk).
-struct Token {
-  float step;
-  Two l, local;
-  int s;
-  Two before, end;  // log2 decay from the chunk's start to before the warp's first token, to the chunk's end
-  int s_warp, s_end;  // the last start in the warp's tokens and before, in the chunk
-};
-struct WarpTotals {
-  float hi[4], lo[4];
-  int s[4];
-};
-struct TokenIn {
-  float raw;
-  bool start;
-};
-// Token t0 + t of unit u (past the end: nothing is forgotten, nothing written).
-__device__ __forceinline__ TokenIn token_load(const SsmArgs &a, int u, int t) {
-  TokenIn x = {-INFINITY, false};
-  if (t < a.T) {
-    x.raw = a.dt[(size_t)u * a.T + t];
-    x.start = a.starts && a.starts[(size_t)(u / a.H) * a.T + t];
-  }
-  return x;
+// A chunk's gates, one record of floats [U, NC]: for each token the decay from it to the end of its warp's 32 tokens and
+// from before them to it (0 across a start), log2 of the latter, the step's length, the last start up to it inside the
+// chunk (-1: none); then the decays from before warp w to ... [w][b]: from the end of warp b's tokens (b < w), FIRST[w]: from
+// before the chunk to before warp w, LAST[w]: from the end of warp w to the chunk's end, ALL: across the chunk.
+constexpr int R_OUT = 0, R_IN = L, R_LOG = 2 * L, R_STEP = 3 * L, R_START = 4 * L, R_BETWEEN = 5 * L, R_FIRST = R_BETWEEN + 16,
+              R_LAST = R_FIRST + 4, R_ALL = R_LAST + 4, REC = R_BETWEEN + 32;
+__device__ __forceinline__ const float *record(const float *records, int u, int NC, int c) {
+  return records + ((size_t)u * NC + c) * REC;
 }
-// group: named barrier of the 128 threads; true when one of them gave up.  `tot` is another one in the next call.
-__device__ __forceinline__ bool token_gates(Token &g, TokenIn in, float bias, float A, WarpTotals &tot, int t, int group, bool ok) {
-  const int lane = t & 31, w = t >> 5;
-  g.step = softplus(in.raw + bias);
-  Two l = in.start ? Two{0.0f, 0.0f} : log2_decay(g.step, A);
-  int s = in.start ? t : -1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Two p = {__shfl_up_sync(0xffffffffu, l.hi, o), __shfl_up_sync(0xffffffffu, l.lo, o)};
-    const int ps = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) {
-      l = two_add(p, l);
-      s = max(s, ps);
-    }
-  }
-  if (lane == 31) tot.hi[w] = l.hi, tot.lo[w] = l.lo, tot.s[w] = s;
-  const bool stop = group_or(group, 128, !ok);
-  g.local = l;
-  g.before = Two{0.0f, 0.0f};
-  g.s = s;
-  g.s_warp = -1;
-  Two sum = {0.0f, 0.0f};
-  int last = -1;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    if (i == w) g.before = sum, g.s = max(g.s, last);
-    sum = two_add(sum, Two{tot.hi[i], tot.lo[i]});
-    last = max(last, tot.s[i]);
-    if (i == w) g.s_warp = last;
-  }
-  g.l = two_add(g.before, l);
-  g.end = sum;
-  g.s_end = last;
-  return stop;
-}
-__device__ __forceinline__ float exp2_of(Two x) { return exp2f(x.hi + x.lo); }
 
 // Row t of a 128-row tile of 128 columns times w: rounded to bf16 in place, what that leaves as bf16 pairs in `rest`.
 __device__ __forceinline__ void weigh_row(uint8_t *tile, int t, float w, uint4 (&rest)[16]) {
@@ -178,6 +131,7 @@ struct SsmSegments {
   int n = 1, per = 0;
   float *S = nullptr, *decay = nullptr;  // [U, n][dv, dk] what a segment leaves, then the state before it; [U, n]
   float *R = nullptr;                    // the same of the adjoint
+  float *records = nullptr;              // [U, NC] the chunks' gates
 };
 
 }  // namespace mesa
