@@ -66,27 +66,24 @@ __global__ void __launch_bounds__(L) mesa_ssm_gates_kernel(SsmArgs a, float *rec
 
 constexpr uint32_t T_G = 0, T_Y1 = 128, T_Y2 = 256, T_S = 384;  // tensor memory columns; M replaces Q K^T
 
-// shared memory: two q tiles | two k tiles | two v tiles | the state as an operand | misc
+// shared memory: two q tiles | two k tiles | two v tiles | the state as an operand, then the rests of K's rows | misc
 template <int P>
 struct Fwd {
-  static constexpr uint32_t K = 2 * QK_TILE, V = 4 * QK_TILE, S = V + 2 * V_TILE<P>, MISC = S + V_TILE<P>;
+  static constexpr uint32_t K = 2 * QK_TILE, V = 4 * QK_TILE, S = V + 2 * V_TILE<P>, MISC = S + QK_TILE;
 };
 struct FwdMisc {
   float cw[2][L], log[L], step[L];  // step and decay from a token to its warp's end; for the diagonal blocks
-  uint64_t full[2], y_staged[2], st_done[2], g_full, m_full, y_full, y_free, s_full, hi_full, cs_done, lo_full, drain;
+  uint64_t full[2], y_staged[2], st_done[2], g_full, m_full, y_full, y_free, s_full, w_full, cs_done, drain;
   uint32_t tmem;
   int gave_up;
 };
 template <int P>
 constexpr uint32_t kFwdSmem = Fwd<P>::MISC + sizeof(FwdMisc);
 static_assert(kFwdSmem<128> <= 232448, "shared memory per block");
-// Registers a thread of the five groups of four warps (96 at launch).
-constexpr int kRegM = 96, kRegY = 128, kRegW = 128, kRegS = 96, kRegIssue = 32;
-static_assert(kRegM + kRegY + kRegW + kRegS + kRegIssue <= 5 * 96, "register file");
 
-// grid (U, segments), 640 threads.
+// grid (U, segments), 576 threads.
 template <int P>
-__global__ void __launch_bounds__(640, 1)
+__global__ void __launch_bounds__(576, 1)
     mesa_ssm_forward_tc_kernel(SsmArgs a, SsmSegments sg, const float *records, const __grid_constant__ CUtensorMap mapQ,
                                const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
                                const __grid_constant__ CUtensorMap mapO) {
@@ -106,7 +103,7 @@ __global__ void __launch_bounds__(640, 1)
   if (tid == 544) {
     for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->g_full, &m->y_full, &m->cs_done, &m->drain})
       tc::mbar_init(bar(*b), 1);
-    for (uint64_t *b : {&m->m_full, &m->y_free, &m->y_staged[0], &m->y_staged[1], &m->s_full, &m->hi_full, &m->lo_full})
+    for (uint64_t *b : {&m->m_full, &m->y_free, &m->y_staged[0], &m->y_staged[1], &m->s_full, &m->w_full})
       tc::mbar_init(bar(*b), 4);
     m->gave_up = 0;
   }
@@ -131,16 +128,13 @@ __global__ void __launch_bounds__(640, 1)
 
   if (warp < 4) {
     // ---- M ----
-    regs_set<kRegM>();
     const float *r = record(records, u, NCT, c0);
     float out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
       const int s = __float_as_int(start);
       const float mine = log, from = in;
-      float between[3];
-#pragma unroll
-      for (int b = 0; b < 3; b++) between[b] = b < w ? r[R_BETWEEN + 4 * w + b] * from : 0.0f;
+      const float *between = r + R_BETWEEN + 4 * w;
       m->cw[ph][t] = out * step;
       m->log[t] = log;
       m->step[t] = step;
@@ -153,74 +147,69 @@ __global__ void __launch_bounds__(640, 1)
         break;
       }
       need(m->g_full, ph);
-      float v[2][32];
-      tc::tmem_ld32(tl + T_G, v[0]);
+#pragma unroll 1
+      for (int b = 0; b < w; b++) {  // tokens of an earlier warp: through the end of theirs
+        float x[32], o[16];
+        tc::tmem_ld32(tl + T_G + 32 * b, x);
+        const float f = between[b] * from;
+        const u64 f2 = pack2(f, f);
+        tc::tmem_ld_wait();
 #pragma unroll
-      for (int b = 0; b < 4; b++) {
-        uint32_t o[16];
-        if (b <= w) {
-          tc::tmem_ld_wait();
-          if (b < w && b < 3) tc::tmem_ld32(tl + T_G + 32 * (b + 1), v[(b + 1) & 1]);
+        for (int i = 0; i < 8; i++) {
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&m->cw[ph][32 * b + 4 * i]);
+          o[2 * i] = __uint_as_float(bf2(mul2(pack2(x[4 * i], x[4 * i + 1]), mul2(f2, y.x))));
+          o[2 * i + 1] = __uint_as_float(bf2(mul2(pack2(x[4 * i + 2], x[4 * i + 3]), mul2(f2, y.y))));
         }
-        const float *x = v[b & 1];
-        if (b < w) {  // tokens of an earlier warp: through the end of theirs
-          const float f = between[b < 3 ? b : 0];
+        tc::tmem_st16(tl + T_G + 16 * b, o);
+      }
+      {
+        float x[32], o[16];
+        tc::tmem_ld32(tl + T_G + 32 * w, x);
+        const int first = max(s - 32 * w, 0);
+        const uint32_t on = (0xffffffffu >> (31 - lane)) & (0xffffffffu << first);  // the columns that count
+        tc::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const float4 y = *reinterpret_cast<const float4 *>(&m->cw[ph][32 * b + 4 * i]);
-            o[2 * i] = bf2(x[4 * i] * (f * y.x), x[4 * i + 1] * (f * y.y));
-            o[2 * i + 1] = bf2(x[4 * i + 2] * (f * y.z), x[4 * i + 3] * (f * y.w));
-          }
-        } else if (b == w) {
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const float4 l = *reinterpret_cast<const float4 *>(&m->log[32 * b + 4 * i]);
-            const float4 y = *reinterpret_cast<const float4 *>(&m->step[32 * b + 4 * i]);
-            const int j = 32 * b + 4 * i;
-            auto one = [&](int jj, float g, float lj, float sj) {
-              return jj <= t && jj >= s ? g * (rule::ex2(mine - lj) * sj) : 0.0f;
-            };
-            o[2 * i] = bf2(one(j, x[4 * i], l.x, y.x), one(j + 1, x[4 * i + 1], l.y, y.y));
-            o[2 * i + 1] = bf2(one(j + 2, x[4 * i + 2], l.z, y.z), one(j + 3, x[4 * i + 3], l.w, y.w));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; i++) o[i] = 0;
+        for (int i = 0; i < 8; i++) {
+          const float4 l = *reinterpret_cast<const float4 *>(&m->log[32 * w + 4 * i]);
+          const float4 y = *reinterpret_cast<const float4 *>(&m->step[32 * w + 4 * i]);
+          auto one = [&](int j, float lj, float sj) { return on >> j & 1 ? x[j] * (rule::ex2(mine - lj) * sj) : 0.0f; };
+          o[2 * i] = __uint_as_float(bf2(one(4 * i, l.x, y.x), one(4 * i + 1, l.y, y.y)));
+          o[2 * i + 1] = __uint_as_float(bf2(one(4 * i + 2, l.z, y.z), one(4 * i + 3, l.w, y.w)));
         }
-        float of[16];
+        tc::tmem_st16(tl + T_G + 16 * w, o);
 #pragma unroll
-        for (int i = 0; i < 16; i++) of[i] = __uint_as_float(o[i]);
-        tc::tmem_st16(tl + T_G + 16 * b, of);
+        for (int i = 0; i < 16; i++) o[i] = 0.0f;
+#pragma unroll 1
+        for (int b = w + 1; b < 4; b++) tc::tmem_st16(tl + T_G + 16 * b, o);
       }
       tc::tmem_st_wait();
       tc::fence_before_sync();
       warp_arrive(m->m_full);
     }
   } else if (warp < 8) {
-    // ---- outputs ----
-    regs_set<kRegY>();
+    // ---- outputs: from tensor memory to the place of Q, and out from there ----
     const float skip = a.skip ? a.skip[h] : 0.0f;
+    const u64 skip2 = pack2(skip, skip);
     const float *r = record(records, u, NCT, c0);
     float f = r[R_IN + t] * r[R_FIRST + w];
     uint32_t bad = 0;
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
-      uint8_t *X = sm + Fwd<P>::V + ph * V_TILE<P>;
-      const float mine = f;
+      uint8_t *X = sm + Fwd<P>::V + ph * V_TILE<P>, *Y = sm + ph * QK_TILE;
+      const u64 f2 = pack2(f, f);
+      const bool in = (c0 + c) * L + t < a.T;
       if (c + 1 < NC) {
         r += REC;
         f = r[R_IN + t] * r[R_FIRST + w];
       }
       if (!need(m->full[ph], (c >> 1) & 1) || !need(m->y_full, ph)) break;
-      uint4 y[P / 8];
-#pragma unroll
+#pragma unroll 1
       for (int hh = 0; hh < P / 16; hh++) {
         float p[16], q[16];
         tc::tmem_ld16(tl + T_Y1 + 16 * hh, p);
         tc::tmem_ld16(tl + T_Y2 + 16 * hh, q);
-        uint4 x[2];
-#pragma unroll
-        for (int k = 0; k < 2; k++) x[k] = *reinterpret_cast<const uint4 *>(X + tile_off(t, 2 * hh + k, L));
+        const uint32_t at[2] = {tile_off(t, 2 * hh, L), tile_off(t, 2 * hh + 1, L)};
+        const uint4 x[2] = {*reinterpret_cast<const uint4 *>(X + at[0]), *reinterpret_cast<const uint4 *>(X + at[1])};
         tc::tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 2; k++) {
@@ -229,29 +218,23 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int e = 8 * k + 2 * i;
-            float p0 = mine == 0.0f ? q[e] : fmaf(mine, p[e], q[e]), p1 = mine == 0.0f ? q[e + 1] : fmaf(mine, p[e + 1], q[e + 1]);
-            if (a.skip) p0 = fmaf(skip, lo_of(xs[i]), p0), p1 = fmaf(skip, hi_of(xs[i]), p1);
-            o[i] = bf2(p0, p1);
+            u64 y = fma2(f2, pack2(p[e], p[e + 1]), pack2(q[e], q[e + 1]));
+            if (a.skip) y = fma2(skip2, of_bf2(xs[i]), y);
+            o[i] = bf2(y);
           }
-          y[2 * hh + k] = make_uint4(o[0], o[1], o[2], o[3]);
+          const uint4 y = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(Y + at[k]) = y;
+          if (in) bad = rule::absmax_words(bad, y);
         }
       }
       tc::fence_before_sync();
       warp_arrive(m->y_free);
-      if ((c0 + c) * L + t < a.T) {
-#pragma unroll
-        for (int k = 0; k < P / 8; k++) bad = rule::absmax_words(bad, y[k]);
-      }
-      if (!need(m->st_done[ph], (c >> 1) & 1)) break;  // (the products have read V)
-#pragma unroll
-      for (int k = 0; k < P / 8; k++) *reinterpret_cast<uint4 *>(X + tile_off(t, k, L)) = y[k];
       tc::fence_smem_to_async();
       warp_arrive(m->y_staged[ph]);
     }
     if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
   } else if (warp < 12) {
     // ---- K's rows weighed ----
-    regs_set<kRegW>();
     const float *r = record(records, u, NCT, c0);
     float next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
     for (int c = 0; c < NC; c++) {
@@ -261,19 +244,14 @@ __global__ void __launch_bounds__(640, 1)
         r += REC;
         next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
       }
-      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->g_full, ph)) break;  // (Q K^T has read K)
-      uint4 rest[16];
-      weigh_row(sm + Fwd<P>::K + ph * QK_TILE, t, mine, rest);
+      // (Q K^T has read K, Q S^T the state)
+      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->cs_done, ph)) break;
+      weigh_row(sm + Fwd<P>::K + ph * QK_TILE, sm + Fwd<P>::S, t, mine);
       tc::fence_smem_to_async();
-      warp_arrive(m->hi_full);
-      if (!need(m->cs_done, ph)) break;  // (Q S^T has read Q)
-      put_row(sm + ph * QK_TILE, t, rest);
-      tc::fence_smem_to_async();
-      warp_arrive(m->lo_full);
+      warp_arrive(m->w_full);
     }
   } else if (warp < 16) {
     // ---- the state ----
-    regs_set<kRegS>();
     const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
     const float *r = record(records, u, NCT, c0);
     float next = r[R_ALL];
@@ -291,89 +269,82 @@ __global__ void __launch_bounds__(640, 1)
     }
     if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && a.S_final && seg == sg.n - 1)
       state_out<P>(tl + T_S, a.S_final + (size_t)u * P * DK, t);
-  } else {
-    regs_set<kRegIssue>();
-    if (warp == 16) {
-      // ---- products ----
-      const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
-                     idS = idesc_bf16(128, P, true, true);
-      const uint32_t sS = tc::smem_u32(sm + Fwd<P>::S);
-      auto scores = [&](int c) -> bool {  // Q K^T of chunk c
-        const uint32_t ph = c & 1;
-        if (!need(m->full[ph], (c >> 1) & 1)) return false;
-        if (elect_one()) {
-          const uint64_t q = tc::kmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
-                         k = tc::kmajor_desc(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), L, 0);
+  } else if (warp == 16) {
+    // ---- products ----
+    const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
+                   idS = idesc_bf16(128, P, true, true);
+    const uint32_t sS = tc::smem_u32(sm + Fwd<P>::S);
+    const uint64_t sd = tc::mnmajor_desc(sS, L, 0);  // (the state, or the rests: the same form)
+    auto scores = [&](int c) -> bool {  // Q K^T of chunk c
+      const uint32_t ph = c & 1;
+      if (!need(m->full[ph], (c >> 1) & 1)) return false;
+      if (elect_one()) {
+        const uint64_t q = tc::kmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
+                       k = tc::kmajor_desc(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), L, 0);
 #pragma unroll
-          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
-          tc::mma_commit(bar(m->g_full));
-        }
-        return true;
-      };
-      scores(0);
-      for (int c = 0; ok && c < NC; c++) {
-        const uint32_t ph = c & 1, q = tc::smem_u32(sm + ph * QK_TILE), k = tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE),
-                       v = tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>);
-        const uint64_t vd = tc::mnmajor_desc(v, L, 0), kd = tc::mnmajor_desc(k, L, 0), rd = tc::mnmajor_desc(q, L, 0);
-        if (!need(m->s_full, ph) || (c > 0 && !need(m->y_free, (c - 1) & 1))) break;
-        if (elect_one()) {
-          const uint64_t qd = tc::kmajor_desc(q, L, 0), sd = tc::mnmajor_desc(sS, L, 0);
-#pragma unroll
-          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
-          tc::mma_commit(bar(m->cs_done));
-        }
-        if (!need(m->hi_full, ph)) break;
-        if (elect_one()) {
-#pragma unroll
-          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, kd + step_mn(s), vd + step_mn(s), idS, true);
-        }
-        if (!need(m->m_full, ph)) break;
-        if (elect_one()) {
-#pragma unroll
-          for (int s = 0; s < 8; s++) tc::mma_f16_ts(tbase + T_Y2, tbase + T_G + 8 * s, vd + step_mn(s), idY, s > 0);
-          tc::mma_commit(bar(m->y_full));
-        }
-        if (!need(m->lo_full, ph)) break;
-        if (elect_one()) {
-#pragma unroll
-          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, rd + step_mn(s), vd + step_mn(s), idS, true);
-          tc::mma_commit(bar(m->st_done[ph]));
-        }
-        if (c + 1 < NC && need(m->y_full, ph)) scores(c + 1);  // (M has been read)
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
+        tc::mma_commit(bar(m->g_full));
       }
-    } else if (tid == 544) {
-      // ---- copies ----
-      const int uk = a.qk_unit(u);
-      auto fetch_qk = [&](int c) {
-        const uint32_t ph = c & 1, b = bar(m->full[ph]);
-        tc::mbar_arrive_expect_tx(b, 2 * QK_TILE + V_TILE<P>);
-        load_tile<DK>(tc::smem_u32(sm + ph * QK_TILE), &mapQ, (c0 + c) * L, uk, b);
-        load_tile<DK>(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), &mapK, (c0 + c) * L, uk, b);
-      };
-      auto fetch_v = [&](int c) {
-        const uint32_t ph = c & 1;
-        load_tile<P>(tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>), &mapV, (c0 + c) * L, u, bar(m->full[ph]));
-      };
-      for (; sent < min(NC, 2); sent++) {
-        fetch_qk(sent);
-        fetch_v(sent);
-      }
-      for (int c = 0; c < NC; c++) {
-        const uint32_t ph = c & 1;
-        if (!(ok = wait(bar(m->y_staged[ph]), (c >> 1) & 1, limit, gave_up))) break;  // (all products are done, too)
-        const uint32_t X = tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>);
-        if (c + 2 < NC) fetch_qk(c + 2);
+      return true;
+    };
+    scores(0);
+    for (int c = 0; ok && c < NC; c++) {
+      const uint32_t ph = c & 1, q = tc::smem_u32(sm + ph * QK_TILE), k = tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE),
+                     v = tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>);
+      const uint64_t vd = tc::mnmajor_desc(v, L, 0), kd = tc::mnmajor_desc(k, L, 0);
+      if (!need(m->s_full, ph) || (c > 0 && !need(m->y_free, (c - 1) & 1))) break;
+      if (elect_one()) {
+        const uint64_t qd = tc::kmajor_desc(q, L, 0);
 #pragma unroll
-        for (int i = 0; i < P / 64; i++) tensor_s2g_3d(&mapO, X + i * HALF, 64 * i, (c0 + c) * L, u);
-        tc::bulk_commit();
-        if (c + 2 < NC) {
-          tc::bulk_wait_read();
-          fetch_v(c + 2);
-          sent++;
-        }
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
+        tc::mma_commit(bar(m->cs_done));
       }
-      tc::bulk_wait_all();
+      if (!need(m->m_full, ph)) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16_ts(tbase + T_Y2, tbase + T_G + 8 * s, vd + step_mn(s), idY, s > 0);
+        tc::mma_commit(bar(m->y_full));
+      }
+      if (!need(m->w_full, ph)) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, kd + step_mn(s), vd + step_mn(s), idS, true);
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, sd + step_mn(s), vd + step_mn(s), idS, true);
+        tc::mma_commit(bar(m->st_done[ph]));
+      }
+      if (c + 1 < NC && need(m->y_full, ph)) scores(c + 1);  // (M has been read)
     }
+  } else if (lane == 0) {
+    // ---- copies ----
+    const int uk = a.qk_unit(u);
+    auto at = [&](uint32_t where, int c) { return tc::smem_u32(sm + where) + (c & 1) * (where == Fwd<P>::V ? V_TILE<P> : QK_TILE); };
+    auto fetch_kv = [&](int c) {
+      const uint32_t b = bar(m->full[c & 1]);
+      tc::mbar_arrive_expect_tx(b, 2 * QK_TILE + V_TILE<P>);
+      load_tile<DK>(at(Fwd<P>::K, c), &mapK, (c0 + c) * L, uk, b);
+      load_tile<P>(at(Fwd<P>::V, c), &mapV, (c0 + c) * L, u, b);
+    };
+    auto fetch_q = [&](int c) { load_tile<DK>(at(0, c), &mapQ, (c0 + c) * L, uk, bar(m->full[c & 1])); };
+    for (; sent < min(NC, 2); sent++) {
+      fetch_kv(sent);
+      fetch_q(sent);
+    }
+    for (int c = 0; c < NC; c++) {
+      const uint32_t ph = c & 1, par = (c >> 1) & 1;
+      if (!(ok = wait(bar(m->y_staged[ph]), par, limit, gave_up))) break;
+#pragma unroll
+      for (int i = 0; i < P / 64; i++) tensor_s2g_3d(&mapO, at(0, c) + i * HALF, 64 * i, (c0 + c) * L, u);
+      tc::bulk_commit();
+      if (!(ok = wait(bar(m->st_done[ph]), par, limit, gave_up))) break;
+      if (c + 2 < NC) {
+        fetch_kv(c + 2);
+        tc::bulk_wait_read();
+        fetch_q(c + 2);
+        sent++;
+      }
+    }
+    tc::bulk_wait_all();
   }
   if (!ok) *gave_up = 1;
   __syncthreads();
@@ -473,9 +444,7 @@ __global__ void __launch_bounds__(320, 1)
       if (c + 1 < NC) next = weight(c + 1);
       if (c > 1 && !need(m->st_done[ph], ((c - 2) >> 1) & 1)) break;  // (its tiles are free)
       if (!need(m->full[ph], (c >> 1) & 1)) break;
-      uint4 rest[16];
-      weigh_row(sm + ph * QK_TILE, t, mine, rest);
-      put_row(sm + Chain<P>::R + ph * QK_TILE, t, rest);
+      weigh_row(sm + ph * QK_TILE, sm + Chain<P>::R + ph * QK_TILE, t, mine);
       tc::fence_smem_to_async();
       warp_arrive(m->w_full[ph]);
     }
@@ -610,7 +579,7 @@ int forward(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
     mesa_ssm_join_kernel<<<dim3(P * DK / 512, a.units()), 128, 0, st>>>(a, sg, false);
     timing_mark_end(K_SSM_SCAN, st);
   }
-  return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<P>, dim3(a.units(), sg.n), 640, kFwdSmem<P>, st, a, sg, sg.records, q, k,
+  return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<P>, dim3(a.units(), sg.n), 576, kFwdSmem<P>, st, a, sg, sg.records, q, k,
                    v, o)
              ? 0
              : -1;

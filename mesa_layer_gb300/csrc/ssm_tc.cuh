@@ -31,12 +31,6 @@ constexpr uint32_t HALF = L * 64 * 2;
 template <int P>
 constexpr uint32_t V_TILE = L * P * 2;
 
-// The registers of a group of four warps (setmaxnreg), up or down from the 96 that 640 threads start with.
-template <int N>
-__device__ __forceinline__ void regs_set() {
-  if constexpr (N > 96) rule::regs_up<N>();
-  if constexpr (N < 96) rule::regs_down<N>();
-}
 // Instruction descriptor: bf16 operands, fp32 sums.
 __device__ __forceinline__ uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
   return tc::idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);
@@ -45,8 +39,12 @@ __device__ __forceinline__ uint32_t bf2(float a, float b) {  // two bf16 values,
   const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&x);
 }
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ u64 of_bf2(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t bf2(u64 x) {
+  float a, b;
+  unpack2(x, a, b);
+  return bf2(a, b);
+}
 
 // A chunk's gates, one record of floats [U, NC]: for each token the decay from it to the end of its warp's 32 tokens and
 // from before them to it (0 across a start), log2 of the latter, the step's length, the last start up to it inside the
@@ -58,31 +56,37 @@ __device__ __forceinline__ const float *record(const float *records, int u, int 
   return records + ((size_t)u * NC + c) * REC;
 }
 
-// Row t of a 128-row tile of 128 columns times w: rounded to bf16 in place, what that leaves as bf16 pairs in `rest`.
-__device__ __forceinline__ void weigh_row(uint8_t *tile, int t, float w, uint4 (&rest)[16]) {
-#pragma unroll
+// Loops over a row's pieces stay loops: unrolled, the parts of a chain's warps do not fit the instruction cache together
+// (a third of all cycles went by waiting for instructions).
+
+// Row t of a 128-row tile of 128 columns times w: rounded to bf16 in place, what that leaves as bf16 to `rest`.
+__device__ __forceinline__ void weigh_row(uint8_t *tile, uint8_t *rest, int t, float w) {
+  const u64 w2 = pack2(w, w);
+#pragma unroll 2
   for (int c = 0; c < 16; c++) {
-    uint4 *at = reinterpret_cast<uint4 *>(tile + tile_off(t, c, L));
-    const uint4 x = *at;
-    auto one = [w](uint32_t v, uint32_t &r) {
-      const float a = lo_of(v) * w, b = hi_of(v) * w;
-      const uint32_t h = bf2(a, b);
-      r = bf2(a - lo_of(h), b - hi_of(h));
-      return h;
+    const uint32_t at = tile_off(t, c, L);
+    const uint4 x = *reinterpret_cast<const uint4 *>(tile + at);
+    uint4 h, r;
+    auto one = [w2](uint32_t v, uint32_t &h, uint32_t &r) {
+      const u64 p = mul2(of_bf2(v), w2);
+      h = bf2(p);
+      r = bf2(sub2(p, of_bf2(h)));
     };
-    *at = make_uint4(one(x.x, rest[c].x), one(x.y, rest[c].y), one(x.z, rest[c].z), one(x.w, rest[c].w));
+    one(x.x, h.x, r.x);
+    one(x.y, h.y, r.y);
+    one(x.z, h.z, r.z);
+    one(x.w, h.w, r.w);
+    *reinterpret_cast<uint4 *>(tile + at) = h;
+    *reinterpret_cast<uint4 *>(rest + at) = r;
   }
-}
-__device__ __forceinline__ void put_row(uint8_t *tile, int t, const uint4 (&x)[16]) {
-#pragma unroll
-  for (int c = 0; c < 16; c++) *reinterpret_cast<uint4 *>(tile + tile_off(t, c, L)) = x[c];
 }
 
 // Lane n's P columns of the state in tensor memory (from global memory [P][dk], or zero, where `first`) become the
 // operand row n at `op` (nullptr: none), and are multiplied by `all` where they lie.
 template <int P>
 __device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, float all, bool first, const float *S0) {
-#pragma unroll
+  const u64 all2 = pack2(all, all);
+#pragma unroll 1
   for (int h = 0; h < P / 32; h++) {
     float x[32];
     if (first) {
@@ -100,7 +104,7 @@ __device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, floa
                        bf2(x[8 * c + 6], x[8 * c + 7]));
     }
 #pragma unroll
-    for (int i = 0; i < 32; i++) x[i] = all == 0.0f ? 0.0f : x[i] * all;  // (a start: nothing of it is left)
+    for (int i = 0; i < 32; i += 2) unpack2(mul2(pack2(x[i], x[i + 1]), all2), x[i], x[i + 1]);
     tc::tmem_st32(tS + 32 * h, x);
   }
   tc::tmem_st_wait();
