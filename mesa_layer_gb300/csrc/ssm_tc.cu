@@ -5,7 +5,7 @@
 //     O = f (Q S^T) + M V + skip V,   M = (Q K^T) o E D,     S' = f_end S + (w V)^T K, w_j = E_{end,j} D_j.
 // The gates come first, a record for each chunk (2.6 KB beside its 128).  Then one CTA per SM walks a unit's chunks (or
 // those of a segment of it) with the state in tensor memory; q, k and v are read and o is written once.  Warps: four turn
-// Q K^T into M, four write the outputs, four weigh K's rows, four turn the state into the next operand, one issues the
+// Q K^T into M, four write the outputs, eight turn the state into the next operand and weigh K's rows, one issues the
 // products, one the copies.  Two chains run side by side, Q K^T -> M -> M V and state -> Q S^T -> state.
 #include "launch.h"
 #include "ssm_tc.cuh"
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(576, 1)
   if (tid == 544) {
     for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->g_full, &m->y_full, &m->cs_done, &m->drain})
       tc::mbar_init(bar(*b), 1);
-    for (uint64_t *b : {&m->m_full, &m->y_free, &m->y_staged[0], &m->y_staged[1], &m->s_full, &m->w_full})
-      tc::mbar_init(bar(*b), 4);
+    for (uint64_t *b : {&m->m_full, &m->y_free, &m->y_staged[0], &m->y_staged[1]}) tc::mbar_init(bar(*b), 4);
+    for (uint64_t *b : {&m->s_full, &m->w_full}) tc::mbar_init(bar(*b), 8);
     m->gave_up = 0;
   }
   tc::fence_before_sync();
@@ -233,42 +233,33 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->y_staged[ph]);
     }
     if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
-  } else if (warp < 12) {
-    // ---- K's rows weighed ----
+  } else if (warp < 16) {
+    // ---- the state, then K's rows weighed: two warps for each 32 lanes (rows), half of the columns each ----
+    const int hf = warp < 12 ? 0 : 1, h0 = hf * P / 64, h1 = h0 + P / 64;
+    const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
     const float *r = record(records, u, NCT, c0);
-    float next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
+    float next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w], left = r[R_ALL];
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
-      const float mine = next;
+      const float mine = next, all = left;
       if (c + 1 < NC) {
         r += REC;
         next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
+        left = r[R_ALL];
       }
-      // (Q K^T has read K, Q S^T the state)
-      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->cs_done, ph)) break;
-      weigh_row(sm + Fwd<P>::K + ph * QK_TILE, sm + Fwd<P>::S, t, mine);
-      tc::fence_smem_to_async();
-      warp_arrive(m->w_full);
-    }
-  } else if (warp < 16) {
-    // ---- the state ----
-    const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
-    const float *r = record(records, u, NCT, c0);
-    float next = r[R_ALL];
-    for (int c = 0; c < NC; c++) {
-      const float all = next;
-      if (c + 1 < NC) {
-        r += REC;
-        next = r[R_ALL];
-      }
-      if (c > 0 && !need(m->st_done[(c - 1) & 1], ((c - 1) >> 1) & 1)) break;
-      state_step<P>(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0);
+      if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
+      state_step(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0, h0, h1);
       tc::fence_smem_to_async();
       tc::fence_before_sync();
       warp_arrive(m->s_full);
+      // (Q K^T has read K, Q S^T the state)
+      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->cs_done, ph)) break;
+      weigh_row(sm + Fwd<P>::K + ph * QK_TILE, sm + Fwd<P>::S, t, mine, 8 * hf, 8 * hf + 8);
+      tc::fence_smem_to_async();
+      warp_arrive(m->w_full);
     }
     if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && a.S_final && seg == sg.n - 1)
-      state_out<P>(tl + T_S, a.S_final + (size_t)u * P * DK, t);
+      state_out(tl + T_S, a.S_final + (size_t)u * P * DK, t, h0, h1);
   } else if (warp == 16) {
     // ---- products ----
     const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
@@ -387,10 +378,10 @@ struct ChainMisc {
 template <int P>
 constexpr uint32_t kChainSmem = Chain<P>::MISC + sizeof(ChainMisc);
 
-// grid (U, segments (from 1 on for adjoint segments, all but the last for segments)), 320 threads: warps 0-3 weigh
-// rows, 4-7 the state, 8 products, 9 copies.  kept: [U, NC][V_TILE] operand tiles.
+// grid (U, segments (from 1 on for adjoint segments, all but the last for segments)), 448 threads: warps 0-7 weigh
+// rows, 8-11 the state, 12 products, 13 copies.  kept: [U, NC][V_TILE] operand tiles.
 template <int P, int MODE>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(448, 1)
     mesa_ssm_chain_tc_kernel(SsmArgs a, SsmSegments sg, const float *records, uint8_t *kept, const __grid_constant__ CUtensorMap mapK,
                              const __grid_constant__ CUtensorMap mapV) {
   constexpr bool ADJ = MODE == kAdjoint || MODE == kAdjointSegment, KEEP = MODE == kKeep || MODE == kAdjoint;
@@ -407,10 +398,11 @@ __global__ void __launch_bounds__(320, 1)
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
-  if (warp == 8) tc::tmem_alloc(tc::smem_u32(&m->tmem), 128);
-  if (tid == 288) {
+  if (warp == 12) tc::tmem_alloc(tc::smem_u32(&m->tmem), 128);
+  if (tid == 416) {
     for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->kept, &m->drain}) tc::mbar_init(bar(*b), 1);
-    for (uint64_t *b : {&m->w_full[0], &m->w_full[1], &m->s_full}) tc::mbar_init(bar(*b), 4);
+    for (uint64_t *b : {&m->w_full[0], &m->w_full[1]}) tc::mbar_init(bar(*b), 8);
+    tc::mbar_init(bar(m->s_full), 4);
     m->gave_up = 0;
   }
   tc::fence_before_sync();
@@ -432,7 +424,8 @@ __global__ void __launch_bounds__(320, 1)
   const int t = tid & 127, w = warp & 3;  // token, or lane of the state
   const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
 
-  if (warp < 4) {
+  if (warp < 8) {
+    const int hf = warp >> 2;  // two warps for each 32 rows, half of the columns each
     auto weight = [&](int c) {
       const float *r = record(records, u, NCT, chunk(c));
       return ADJ ? r[R_IN + t] * r[R_FIRST + w] : r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
@@ -444,11 +437,11 @@ __global__ void __launch_bounds__(320, 1)
       if (c + 1 < NC) next = weight(c + 1);
       if (c > 1 && !need(m->st_done[ph], ((c - 2) >> 1) & 1)) break;  // (its tiles are free)
       if (!need(m->full[ph], (c >> 1) & 1)) break;
-      weigh_row(sm + ph * QK_TILE, sm + Chain<P>::R + ph * QK_TILE, t, mine);
+      weigh_row(sm + ph * QK_TILE, sm + Chain<P>::R + ph * QK_TILE, t, mine, 8 * hf, 8 * hf + 8);
       tc::fence_smem_to_async();
       warp_arrive(m->w_full[ph]);
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     const float *from = nullptr;
     if constexpr (MODE == kKeep) from = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
     if constexpr (MODE == kAdjoint)
@@ -461,7 +454,7 @@ __global__ void __launch_bounds__(320, 1)
       left *= all;
       if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
       if (KEEP && c > 0 && !need(m->kept, (c - 1) & 1)) break;  // (the last tile has left)
-      state_step<P>(tl + T_G, KEEP ? sm + Chain<P>::S : nullptr, t, all, c == 0, from);
+      state_step(tl + T_G, KEEP ? sm + Chain<P>::S : nullptr, t, all, c == 0, from, 0, P / 32);
       if (KEEP) tc::fence_smem_to_async();
       tc::fence_before_sync();
       warp_arrive(m->s_full);
@@ -470,9 +463,9 @@ __global__ void __launch_bounds__(320, 1)
     if constexpr (MODE == kSegment) to = sg.S + ((size_t)u * sg.n + seg) * P * DK;
     if constexpr (MODE == kAdjointSegment) to = sg.R + ((size_t)u * sg.n + seg) * P * DK;
     if constexpr (MODE == kAdjoint) to = a.dS0 && seg == 0 ? a.dS0 + (size_t)u * P * DK : nullptr;
-    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && to) state_out<P>(tl + T_G, to, t);
+    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && to) state_out(tl + T_G, to, t, 0, P / 32);
     if (!KEEP && t == 0) sg.decay[(size_t)u * sg.n + seg] = left;
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     const uint32_t idS = idesc_bf16(128, P, true, true);
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
@@ -517,13 +510,13 @@ __global__ void __launch_bounds__(320, 1)
   if (!ok) *gave_up = 1;
   __syncthreads();
   if (*gave_up) {
-    if (warp == 8 && elect_one()) tc::mma_commit(bar(m->drain));
+    if (warp == 12 && elect_one()) tc::mma_commit(bar(m->drain));
     if (tid == 0) {
       unsigned bits = tc::kErrMmaTimeout;
       if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
       atomicOr(a.status, bits);
     }
-    if (tid == 288) {
+    if (tid == 416) {
       bool landed = true;
       for (int c = max(0, sent - 2); c < sent; c++)
         landed &= tc::mbar_wait(bar(m->full[c & 1]), (c >> 1) & 1, tc::kWaitLimit);
@@ -532,7 +525,7 @@ __global__ void __launch_bounds__(320, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 8) tc::tmem_free(tbase, 128);
+  if (warp == 12) tc::tmem_free(tbase, 128);
 }
 
 // The states before the segments from what each leaves: S_{y+1} = decay_y S_y + left_y, S_0 the call's (copied: the last
@@ -572,7 +565,7 @@ int forward(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&o, a.out, a.units(), a.T, P))
     return -1;
   if (sg.n > 1) {
-    if (!launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<P, kSegment>, dim3(a.units(), sg.n - 1), 320, kChainSmem<P>, st, a, sg,
+    if (!launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<P, kSegment>, dim3(a.units(), sg.n - 1), 448, kChainSmem<P>, st, a, sg,
                    sg.records, (uint8_t *)nullptr, k, v))
       return -1;
     timing_mark_begin(K_SSM_SCAN, st);

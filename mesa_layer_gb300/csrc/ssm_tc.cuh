@@ -59,11 +59,11 @@ __device__ __forceinline__ const float *record(const float *records, int u, int 
 // Loops over a row's pieces stay loops: unrolled, the parts of a chain's warps do not fit the instruction cache together
 // (a third of all cycles went by waiting for instructions).
 
-// Row t of a 128-row tile of 128 columns times w: rounded to bf16 in place, what that leaves as bf16 to `rest`.
-__device__ __forceinline__ void weigh_row(uint8_t *tile, uint8_t *rest, int t, float w) {
+// Columns 8 c0 .. 8 c1 - 1 of row t of a 128-row tile times w: rounded to bf16 in place, what that leaves as bf16 to `rest`.
+__device__ __forceinline__ void weigh_row(uint8_t *tile, uint8_t *rest, int t, float w, int c0, int c1) {
   const u64 w2 = pack2(w, w);
 #pragma unroll 2
-  for (int c = 0; c < 16; c++) {
+  for (int c = c0; c < c1; c++) {
     const uint32_t at = tile_off(t, c, L);
     const uint4 x = *reinterpret_cast<const uint4 *>(tile + at);
     uint4 h, r;
@@ -81,13 +81,12 @@ __device__ __forceinline__ void weigh_row(uint8_t *tile, uint8_t *rest, int t, f
   }
 }
 
-// Lane n's P columns of the state in tensor memory (from global memory [P][dk], or zero, where `first`) become the
-// operand row n at `op` (nullptr: none), and are multiplied by `all` where they lie.
-template <int P>
-__device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, float all, bool first, const float *S0) {
+// Columns 32 h0 .. 32 h1 - 1 of lane n of the state in tensor memory (from global memory [P][dk], or zero, where `first`)
+// become the operand row n at `op` (nullptr: none), and are multiplied by `all` where they lie.
+__device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, float all, bool first, const float *S0, int h0, int h1) {
   const u64 all2 = pack2(all, all);
 #pragma unroll 1
-  for (int h = 0; h < P / 32; h++) {
+  for (int h = h0; h < h1; h++) {
     float x[32];
     if (first) {
 #pragma unroll
@@ -109,10 +108,9 @@ __device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, floa
   }
   tc::tmem_st_wait();
 }
-template <int P>
-__device__ __forceinline__ void state_out(uint32_t tS, float *dst, int n) {
-#pragma unroll
-  for (int h = 0; h < P / 32; h++) {
+__device__ __forceinline__ void state_out(uint32_t tS, float *dst, int n, int h0, int h1) {
+#pragma unroll 1
+  for (int h = h0; h < h1; h++) {
     float x[32];
     tc::tmem_ld32(tS + 32 * h, x);
     tc::tmem_ld_wait();
