@@ -98,6 +98,7 @@ int mesa_ssm_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dt
 size_t mesa_ssm_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   dtype &= ~MESA_GATE_GRADS_F32;  // (the same workspace)
   if (check_scan(B, H, Hk, T, dk, dv, dtype) != MESA_OK) return 0;
+  if (scan_tc(dtype, dk, dv)) return kStatusBytes + mesa::ssm_tc_backward_workspace(B, H, Hk, T, dv);
   return scan_parts(B, H, Hk, T, dk, dv, true, nullptr, nullptr);
 }
 
@@ -141,6 +142,8 @@ int mesa_ssm_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int d
   a.status = (unsigned *)workspace;
   a.wait_limit = mesa::wait_limit();
   if (bad_memset(workspace, sizeof(unsigned), stream)) return MESA_ERR_CUDA;
+  if (scan_tc(dtype, dk, dv))
+    return mesa::launch_ssm_backward_tc(a, (char *)workspace + kStatusBytes, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
   mesa::SsmWorkspace ws;
   scan_parts(B, H, Hk, T, dk, dv, true, &ws, (char *)workspace);
   return mesa::launch_ssm_backward(a, ws, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;

@@ -57,6 +57,8 @@ int launch_ssm_step(const SsmStepArgs &a, cudaStream_t st);
 // The tensor-core path (bf16, dk = 128, dv 64 or 128).
 size_t ssm_tc_workspace(int U, int T, int dv);
 int launch_ssm_forward_tc(const SsmArgs &a, void *workspace, cudaStream_t st);
+size_t ssm_tc_backward_workspace(int B, int H, int Hk, int T, int dv);
+int launch_ssm_backward_tc(const SsmArgs &a, void *workspace, cudaStream_t st);
 // dA, dbias, dskip from n sums a unit, [3][U, n].
 int launch_ssm_param_sums(const SsmArgs &a, const float *sums, int n, cudaStream_t st);
 // dq, dk [B, Hk, T, dk] = sums of the per-unit fp32 parts over the value heads of a key head.

@@ -1,0 +1,510 @@
+// ssm_bwd_tc.cu -- the selective scan's gradients on the tensor cores (bf16, dk = 128, dv 64 or 128; formulas in
+// ssm_bwd.cu, operand formats in ssm_tc.cuh).
+//
+// Two walks over the chunks (mesa_ssm_chain_tc_kernel) leave the states before and the adjoints after every chunk as
+// bf16 operands S^T, R^T [dk][dv]; then every chunk's gradients come from its rows and these two, chunk by chunk:
+//     Q K^T, g V^T -> M' = (Q K^T) o E, W = (g V^T) o E D;    dQ = f (g S) + W K,   dK = c D (V R) + W^T Q,
+//     du = c (K R^T) + M'^T g,   dV = D du + skip g.
+// Eight products of 128^3 a chunk (P = 128).  The scales f, c D and c are put on where the products lie in tensor memory,
+// with the sums that the decays' gradients need on the way.  The pairs' terms X = (Q K^T) o W stay fp32, and the sum over
+// readers i >= t and writers j < t runs as F(t + 1) = F(t) - sum_j X_tj + sum_i X_it inside a chunk (2^-24 of the terms).
+#include "launch.h"
+#include "ssm_tc.cuh"
+
+namespace mesa {
+
+using namespace ssm;
+
+namespace {
+
+// shared memory: Q | K | V | G | R | S (dv = 128: then W) | [W] | M' | misc
+template <int P>
+struct Grad {
+  static constexpr uint32_t K = QK_TILE, V = 2 * QK_TILE, G = V + V_TILE<P>, R = G + V_TILE<P>, S = R + V_TILE<P>,
+                            W = P == 128 ? S : S + V_TILE<P>, M = W + QK_TILE, MISC = M + QK_TILE;
+};
+struct GradMisc {
+  float col[4][L];  // by rows' warp: sum over its rows of X
+  float frob[2][16];
+  float scan[2][4];
+  uint64_t full1, full2, c1, c2, e, fg, h, a_done, b_done, c_done, f_done, qk_staged, v_staged, drain;
+  uint32_t tmem;
+  int gave_up;
+};
+template <int P>
+constexpr uint32_t kGradSmem = Grad<P>::MISC + sizeof(GradMisc);
+static_assert(kGradSmem<128> <= 232448, "shared memory per block");
+// Tensor memory: Q K^T, then du | g V^T, then sums by token | dQ | dK.  The sums' columns, by quarter of the channels:
+constexpr uint32_t T_A = 0, T_B = 128, T_DQ = 256, T_DK = 384;
+constexpr int X_ROW = 0, X_IN = 4, X_OUT = 8, X_DUV = 12, X_GV = 16;
+
+__device__ __forceinline__ void tmem_put(uint32_t taddr, float x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
+}
+// Lane l's sum over the warp's lanes of x[l].
+__device__ __forceinline__ float transposed_sum(float (&x)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; i++) {
+      const float give = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return x[0];
+}
+
+// A resident CTA per SM over `chunks` chunks of all units, 576 threads: warps 0-15 (lane quarter warp % 4, column
+// quarter warp / 4), 16 products, 17 copies.
+template <int P>
+__global__ void __launch_bounds__(576, 1)
+    mesa_ssm_grads_tc_kernel(SsmArgs a, int NC, int chunks, const float *records, const uint8_t *states, const uint8_t *adjoints,
+                             float *sums, float *dqp, float *dkp, const __grid_constant__ CUtensorMap mapQ,
+                             const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+                             const __grid_constant__ CUtensorMap mapG, const __grid_constant__ CUtensorMap mapDq,
+                             const __grid_constant__ CUtensorMap mapDk, const __grid_constant__ CUtensorMap mapDv) {
+  using O = Grad<P>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (tc::smem_u32(sm) & 1023) {  // (swizzled tiles need it; the declaration asks for it)
+    if (threadIdx.x == 0) atomicOr(a.status, tc::kErrMmaTimeout);
+    return;
+  }
+  GradMisc *m = reinterpret_cast<GradMisc *>(sm + O::MISC);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // (warp: uniform)
+  auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
+  volatile int *gave_up = &m->gave_up;
+  const unsigned limit = a.wait_limit;
+  if (warp == 16) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
+  if (tid == 544) {
+    for (uint64_t *b : {&m->full1, &m->full2, &m->c1, &m->c2, &m->e, &m->fg, &m->h, &m->drain}) tc::mbar_init(bar(*b), 1);
+    for (uint64_t *b : {&m->a_done, &m->b_done, &m->c_done, &m->qk_staged, &m->v_staged}) tc::mbar_init(bar(*b), 16);
+    tc::mbar_init(bar(m->f_done), 4);
+    m->gave_up = 0;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = __shfl_sync(0xffffffffu, m->tmem, 0);
+  auto warp_arrive = [&](uint64_t &b) {  // one arrival per warp, after what its lanes did
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
+  bool ok = true;
+  auto need = [&](uint64_t &b, uint32_t parity) {  // a warp's wait; once a lane has given up, the warp has
+    ok = __all_sync(0xffffffffu, ok && wait(bar(b), parity, limit, gave_up));
+    tc::fence_after_sync();
+    return ok;
+  };
+  int sent = 0;  // chunks asked for (warp 17)
+
+  if (warp < 16) {
+    const int w = warp & 3, b = warp >> 2, t = 32 * w + lane;  // row t, columns of quarter b
+    const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
+    uint32_t bad = 0;
+    for (int at = blockIdx.x, it = 0; at < chunks; at += gridDim.x, it++) {
+      const uint32_t par = it & 1;
+      const int u = at / NC, c = at - u * NC, h = u % a.H;
+      const bool in = c * L + t < a.T;
+      const float *r = record(records, u, NC, c);
+      const float r_in = r[R_IN + t], step = r[R_STEP + t], f = r_in * r[R_FIRST + w], ct = r[R_OUT + t] * r[R_LAST + w];
+      // <S, R>: 8 P bytes a thread of each
+      if (!need(m->full2, par)) break;
+      {
+        u64 x2 = 0;
+#pragma unroll 2
+        for (int i = tid; i < (int)(V_TILE<P> / 16); i += 512) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(sm + O::S + 16 * i), y = *reinterpret_cast<const uint4 *>(sm + O::R + 16 * i);
+          x2 = fma2(of_bf2(x.x), of_bf2(y.x), x2);
+          x2 = fma2(of_bf2(x.y), of_bf2(y.y), x2);
+          x2 = fma2(of_bf2(x.z), of_bf2(y.z), x2);
+          x2 = fma2(of_bf2(x.w), of_bf2(y.w), x2);
+        }
+        const float x = warp_sum(sum2(x2));
+        if (lane == 0) m->frob[par][warp] = x;
+      }
+      if (group_or(1, 512, !ok)) {  // (S has been read: W may take its place)
+        ok = false;
+        break;
+      }
+      // ---- M', W and the pairs' sums: block (w, b) ----
+      float row = 0.0f, gv = 0.0f;
+      need(m->c1, par);
+      if (b <= w) {
+        float x[32], y[32];
+        tc::tmem_ld32(tl + T_A + 32 * b, x);
+        tc::tmem_ld32(tl + T_B + 32 * b, y);
+        const float fac = b < w ? r[R_BETWEEN + 4 * w + b] * r_in : 1.0f, mine = r[R_LOG + t];
+        const int first = max(__float_as_int(r[R_START + t]) - 32 * w, 0);
+        const uint32_t on = b < w ? 0xffffffffu : (0xffffffffu >> (31 - lane)) & (0xffffffffu << first);  // columns that count
+        const float4 *rj = reinterpret_cast<const float4 *>(r + (b < w ? R_OUT : R_LOG) + 32 * b),
+                     *sj = reinterpret_cast<const float4 *>(r + R_STEP + 32 * b);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int cc = 0; cc < 4; cc++) {
+          uint32_t om[4], ow[4];
+#pragma unroll
+          for (int q = 0; q < 2; q++) {
+            const float4 rv = rj[2 * cc + q], sv = sj[2 * cc + q];
+            const float re[4] = {rv.x, rv.y, rv.z, rv.w}, se[4] = {sv.x, sv.y, sv.z, sv.w};
+            float mm[4], ww[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              const int j = 8 * cc + 4 * q + i;
+              const float e = b < w ? fac * re[i] : rule::ex2(mine - re[i]);
+              const bool keep = on >> j & 1;
+              if (b == w && j == lane) gv = y[j];
+              mm[i] = keep ? x[j] * e : 0.0f;
+              ww[i] = keep ? y[j] * (e * se[i]) : 0.0f;
+              x[j] = keep && !(b == w && j == lane) ? x[j] * ww[i] : 0.0f;
+              row += x[j];
+            }
+            om[2 * q] = bf2(mm[0], mm[1]), om[2 * q + 1] = bf2(mm[2], mm[3]);
+            ow[2 * q] = bf2(ww[0], ww[1]), ow[2 * q + 1] = bf2(ww[2], ww[3]);
+          }
+          const uint32_t to = tile_off(t, 4 * b + cc, L);
+          *reinterpret_cast<uint4 *>(sm + O::M + to) = make_uint4(om[0], om[1], om[2], om[3]);
+          *reinterpret_cast<uint4 *>(sm + O::W + to) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+        }
+        m->col[w][32 * b + lane] = transposed_sum(x, lane);
+      } else {
+#pragma unroll
+        for (int cc = 0; cc < 4; cc++) {
+          const uint32_t to = tile_off(t, 4 * b + cc, L);
+          *reinterpret_cast<uint4 *>(sm + O::M + to) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(sm + O::W + to) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      tc::fence_smem_to_async();
+      tc::fence_before_sync();
+      warp_arrive(m->a_done);
+      // ---- f (g S) and c D (V R), with what passes into and out of the chunk ----
+      need(m->c2, par);
+      float x_in, x_out;
+      auto scaled = [&](uint32_t col, const uint8_t *tile, float s) {  // returns the row's product with the tile's
+        float x[32];
+        tc::tmem_ld32(tl + col + 32 * b, x);
+        const u64 s2 = pack2(s, s);
+        u64 dot = 0;
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int cc = 0; cc < 4; cc++) {
+          const uint4 q = *reinterpret_cast<const uint4 *>(tile + tile_off(t, 4 * b + cc, L));
+          const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int e = 8 * cc + 2 * i;
+            const u64 y = mul2(pack2(x[e], x[e + 1]), s2);
+            dot = fma2(y, of_bf2(qs[i]), dot);
+            unpack2(y, x[e], x[e + 1]);
+          }
+        }
+        tc::tmem_st32(tl + col + 32 * b, x);
+        return sum2(dot);
+      };
+      x_in = scaled(T_DQ, sm, f);
+      x_out = scaled(T_DK, sm + O::K, ct * step);
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      warp_arrive(m->b_done);
+      // ---- c (K R^T); the sums so far ----
+      need(m->e, par);
+      {
+        constexpr int N = P / 4;
+        float x[N];
+        tc::tmem_ld<N>(tl + T_A + N * b, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < N; i++) x[i] *= ct;
+        tc::tmem_st<N>(tl + T_A + N * b, x);
+        tmem_put(tl + T_B + X_ROW + b, row);
+        tmem_put(tl + T_B + X_IN + b, x_in);
+        tmem_put(tl + T_B + X_OUT + b, x_out);
+        if (b == w) tmem_put(tl + T_B + X_GV, gv);
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        warp_arrive(m->c_done);
+      }
+      // ---- dQ, dK ----
+      need(m->fg, par);
+      auto put = [&](uint32_t col, uint8_t *tile, float *part) {
+        float x[32];
+        tc::tmem_ld32(tl + col + 32 * b, x);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int cc = 0; cc < 4; cc++) {
+          const uint4 o = make_uint4(bf2(x[8 * cc], x[8 * cc + 1]), bf2(x[8 * cc + 2], x[8 * cc + 3]), bf2(x[8 * cc + 4], x[8 * cc + 5]),
+                                     bf2(x[8 * cc + 6], x[8 * cc + 7]));
+          if (in) bad = rule::absmax_words(bad, o);
+          if (!part) {
+            *reinterpret_cast<uint4 *>(tile + tile_off(t, 4 * b + cc, L)) = o;
+          } else if (in) {
+            float4 *dst = reinterpret_cast<float4 *>(part + ((size_t)u * a.T + c * L + t) * DK + 32 * b + 8 * cc);
+            dst[0] = make_float4(x[8 * cc], x[8 * cc + 1], x[8 * cc + 2], x[8 * cc + 3]);
+            dst[1] = make_float4(x[8 * cc + 4], x[8 * cc + 5], x[8 * cc + 6], x[8 * cc + 7]);
+          }
+        }
+      };
+      put(T_DQ, sm, dqp);
+      put(T_DK, sm + O::K, dkp);
+      tc::fence_smem_to_async();
+      warp_arrive(m->qk_staged);
+      // ---- dV ----
+      need(m->h, par);
+      {
+        constexpr int N = P / 4;
+        float x[N];
+        tc::tmem_ld<N>(tl + T_A + N * b, x);
+        const float skip = a.skip ? a.skip[h] : 0.0f;
+        const u64 step2 = pack2(step, step), skip2 = pack2(skip, skip);
+        u64 dot = 0;
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int cc = 0; cc < N / 8; cc++) {
+          const uint32_t to = tile_off(t, N / 8 * b + cc, L);
+          const uint4 v = *reinterpret_cast<const uint4 *>(sm + O::V + to), g = *reinterpret_cast<const uint4 *>(sm + O::G + to);
+          const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, gs[4] = {g.x, g.y, g.z, g.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const u64 du = pack2(x[8 * cc + 2 * i], x[8 * cc + 2 * i + 1]);
+            dot = fma2(du, of_bf2(vs[i]), dot);
+            o[i] = bf2(a.skip ? fma2(skip2, of_bf2(gs[i]), mul2(step2, du)) : mul2(step2, du));
+          }
+          const uint4 y = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(sm + O::G + to) = y;
+          if (in) bad = rule::absmax_words(bad, y);
+        }
+        tmem_put(tl + T_B + X_DUV + b, sum2(dot));
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        tc::fence_smem_to_async();
+        warp_arrive(m->v_staged);
+      }
+      if (group_or(1, 512, !ok)) {
+        ok = false;
+        break;
+      }
+      if (b > 0) continue;
+      // ---- the steps' gradients: token t ----
+      tc::fence_after_sync();
+      float x[32];
+      tc::tmem_ld32(tl + T_B, x);
+      tc::tmem_ld_wait();
+      tc::fence_before_sync();
+      auto four = [&](int i) { return (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]); };
+      float col = 0.0f, all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (i >= w) col += m->col[i][t];
+#pragma unroll
+      for (int i = 0; i < 16; i++) all += m->frob[par][i];
+      const float xi = four(X_IN), moved = col - four(X_ROW) + four(X_OUT);
+      float suf = xi, pre = moved;  // readers from t on, writers before t (with the pairs)
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float p = __shfl_down_sync(0xffffffffu, suf, o), q = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane + o < 32) suf += p;
+        if (lane >= o) pre += q;
+      }
+      if (lane == 0) m->scan[0][w] = suf;
+      if (lane == 31) m->scan[1][w] = pre;
+      group_or(2, 128, false);
+      pre -= moved;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if (i > w) suf += m->scan[0][i];
+        if (i < w) pre += m->scan[1][i];
+      }
+      const bool start = __float_as_int(r[R_START + t]) == t;
+      const float da = start ? 0.0f : pre + suf + r[R_ALL] * all;
+      const float raw = in ? a.dt[(size_t)u * a.T + c * L + t] + (a.dt_bias ? a.dt_bias[h] : 0.0f) : 0.0f;
+      const float dd = in ? fmaf(a.A[h], da, four(X_DUV)) * sigmoid(raw) : 0.0f;
+      if (in) {
+        if (!isfinite(dd)) bad = 0x7f80u;
+        const size_t i = (size_t)u * a.T + c * L + t;
+        if (a.gates_f32)
+          static_cast<float *>(a.ddt)[i] = dd;
+        else
+          static_cast<__nv_bfloat16 *>(a.ddt)[i] = __float2bfloat16_rn(dd);
+      }
+      const float sA = warp_sum(in ? step * da : 0.0f), sb = warp_sum(dd), sg = warp_sum(x[X_GV]);
+      warp_arrive(m->f_done);
+      if (lane == 0) {  // a warp's tokens each
+        const size_t n = (size_t)chunks * 4, i = (size_t)at * 4 + w;
+        sums[i] = sA;
+        sums[n + i] = sb;
+        sums[2 * n + i] = sg;
+      }
+    }
+    if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
+  } else if (warp == 16) {
+    // ---- products ----
+    const uint32_t id = idesc_bf16(128, 128, false, false), idB = idesc_bf16(128, 128, false, true),
+                   idAB = idesc_bf16(128, 128, true, true), idP = idesc_bf16(128, P, false, true), idPA = idesc_bf16(128, P, true, true);
+    auto km = [&](uint32_t where) { return tc::kmajor_desc(tc::smem_u32(sm + where), L, 0); };
+    auto mn = [&](uint32_t where) { return tc::mnmajor_desc(tc::smem_u32(sm + where), L, 0); };
+    const uint64_t qk = km(0), qm = mn(0), kk = km(O::K), kmn = mn(O::K), vk = km(O::V), gk = km(O::G), gm = mn(O::G), sk = km(O::S),
+                   rk = km(O::R), rm = mn(O::R), wk = km(O::W), wm = mn(O::W), mm = mn(O::M);
+    for (int at = blockIdx.x, it = 0; at < chunks; at += gridDim.x, it++) {
+      const uint32_t par = it & 1;
+      if (!need(m->full1, par) || (it > 0 && !need(m->f_done, par ^ 1))) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_A, qk + step128(s), kk + step128(s), id, s > 0);
+#pragma unroll
+        for (int s = 0; s < P / 16; s++) tc::mma_f16(tbase + T_B, gk + step128(s), vk + step128(s), id, s > 0);
+      }
+      if (!need(m->full2, par)) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < P / 16; s++) tc::mma_f16(tbase + T_DQ, gk + step128(s), sk + step128(s), id, s > 0);
+        tc::mma_commit(bar(m->c1));
+#pragma unroll
+        for (int s = 0; s < P / 16; s++) tc::mma_f16(tbase + T_DK, vk + step128(s), rk + step128(s), id, s > 0);
+        tc::mma_commit(bar(m->c2));
+      }
+      if (!need(m->a_done, par)) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_A, kk + step128(s), rm + step_mn(s), idP, s > 0);
+        tc::mma_commit(bar(m->e));
+      }
+      if (!need(m->b_done, par)) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_DQ, wk + step128(s), kmn + step_mn(s), idB, true);
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_DK, wm + step_mn(s), qm + step_mn(s), idAB, true);
+        tc::mma_commit(bar(m->fg));
+      }
+      if (!need(m->c_done, par)) break;
+      if (elect_one()) {
+#pragma unroll
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_A, mm + step_mn(s), gm + step_mn(s), idPA, true);
+        tc::mma_commit(bar(m->h));
+      }
+    }
+  } else if (lane == 0) {
+    // ---- copies ----
+    auto fetch_rows = [&](int at) {
+      const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u);
+      const uint32_t b = bar(m->full1);
+      tc::mbar_arrive_expect_tx(b, 2 * QK_TILE + 2 * V_TILE<P>);
+      load_tile<DK>(tc::smem_u32(sm), &mapQ, y, uk, b);
+      load_tile<DK>(tc::smem_u32(sm + O::K), &mapK, y, uk, b);
+      load_tile<P>(tc::smem_u32(sm + O::G), &mapG, y, u, b);
+      load_tile<P>(tc::smem_u32(sm + O::V), &mapV, y, u, b);
+    };
+    auto fetch_states = [&](int at) {
+      const uint32_t b = bar(m->full2);
+      tc::mbar_arrive_expect_tx(b, 2 * V_TILE<P>);
+      tc::bulk_g2s(tc::smem_u32(sm + O::S), states + (size_t)at * V_TILE<P>, V_TILE<P>, b);
+      tc::bulk_g2s(tc::smem_u32(sm + O::R), adjoints + (size_t)at * V_TILE<P>, V_TILE<P>, b);
+    };
+    if ((int)blockIdx.x < chunks) {
+      fetch_rows(blockIdx.x);
+      fetch_states(blockIdx.x);
+      sent = 1;
+    }
+    for (int at = blockIdx.x, it = 0; at < chunks; at += gridDim.x, it++) {
+      const uint32_t par = it & 1;
+      const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u), next = at + gridDim.x;
+      if (!(ok = wait(bar(m->qk_staged), par, limit, gave_up))) break;
+      if (!dqp) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          tensor_s2g_3d(&mapDq, tc::smem_u32(sm) + i * HALF, 64 * i, y, uk);
+          tensor_s2g_3d(&mapDk, tc::smem_u32(sm + O::K) + i * HALF, 64 * i, y, uk);
+        }
+        tc::bulk_commit();
+      }
+      if (!(ok = wait(bar(m->v_staged), par, limit, gave_up))) break;
+#pragma unroll
+      for (int i = 0; i < P / 64; i++) tensor_s2g_3d(&mapDv, tc::smem_u32(sm + O::G) + i * HALF, 64 * i, y, u);
+      tc::bulk_commit();
+      if (next < chunks) {
+        fetch_states(next);
+        tc::bulk_wait_read();
+        fetch_rows(next);
+        sent++;
+      }
+    }
+    tc::bulk_wait_all();
+  }
+  if (!ok) *gave_up = 1;
+  __syncthreads();
+  // a wait gave up: products and copies still in flight finish before the memory is released
+  if (*gave_up) {
+    if (warp == 16 && elect_one()) tc::mma_commit(bar(m->drain));
+    if (tid == 0) {
+      unsigned bits = tc::kErrMmaTimeout;
+      if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
+      atomicOr(a.status, bits);
+    }
+    if (tid == 544 && sent > 0 &&
+        !(tc::mbar_wait(bar(m->full1), (sent - 1) & 1, tc::kWaitLimit) && tc::mbar_wait(bar(m->full2), (sent - 1) & 1, tc::kWaitLimit)))
+      atomicOr(a.status, tc::kErrDrainTimeout);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 16) tc::tmem_free(tbase, 512);
+}
+
+template <int P>
+int grads(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStream_t st) {
+  CUtensorMap q{}, k{}, v{}, g{}, dq{}, dk{}, dv{};
+  const int shared = a.B * a.Hk, NC = (a.T + L - 1) / L, chunks = a.units() * NC, sms = sm_count();
+  if (!tmap_units_bf16(&q, a.q, shared, a.T, DK) || !tmap_units_bf16(&k, a.k, shared, a.T, DK) ||
+      !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&g, a.dout, a.units(), a.T, P) ||
+      !tmap_units_bf16(&dq, a.dq, shared, a.T, DK) || !tmap_units_bf16(&dk, a.dk_out, shared, a.T, DK) ||
+      !tmap_units_bf16(&dv, a.dv_out, a.units(), a.T, P) || sms <= 0)
+    return -1;
+  if (cudaFuncSetAttribute(mesa_ssm_grads_tc_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem<P>) != cudaSuccess)
+    return -1;
+  timing_mark_begin(K_SSM_GRADS, st);
+  mesa_ssm_grads_tc_kernel<P><<<chunks < sms ? chunks : sms, 576, kGradSmem<P>, st>>>(a, NC, chunks, sg.records, ws.S, ws.R, ws.sums,
+                                                                                     ws.dqp, ws.dkp, q, k, v, g, dq, dk, dv);
+  timing_mark_end(K_SSM_GRADS, st);
+  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+}
+
+// [segments, records | S | R | sums | per-head dq, dk]
+size_t parts(const SsmArgs &a, void *workspace, SsmSegments *sg, SsmTcBwd *ws) {
+  auto up256 = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t U = a.units(), NC = ((size_t)a.T + L - 1) / L, tiles = U * NC * L * a.dv * 2, part = a.Hk != a.H ? U * a.T * DK * 4 : 0;
+  size_t at;
+  const SsmSegments s = ssm_segments(a.units(), a.T, a.dv, true, workspace, &at);
+  if (sg) *sg = s;
+  char *base = (char *)workspace;
+  at = up256(at);
+  const size_t sizes[5] = {tiles, tiles, 3 * U * NC * 4 * sizeof(float), part, part};
+  size_t off[5];
+  for (int i = 0; i < 5; i++) {
+    off[i] = at;
+    at += up256(sizes[i]);
+  }
+  if (ws && workspace)
+    *ws = SsmTcBwd{(uint8_t *)base + off[0], (uint8_t *)base + off[1], (float *)(base + off[2]), part ? (float *)(base + off[3]) : nullptr,
+                   part ? (float *)(base + off[4]) : nullptr};
+  return at;
+}
+
+}  // namespace
+
+size_t ssm_tc_backward_workspace(int B, int H, int Hk, int T, int dv) {
+  SsmArgs a{B, H, Hk, T, DK, dv, 1};
+  return parts(a, nullptr, nullptr, nullptr);
+}
+
+int launch_ssm_backward_tc(const SsmArgs &a, void *workspace, cudaStream_t st) {
+  SsmSegments sg;
+  SsmTcBwd ws;
+  parts(a, workspace, &sg, &ws);
+  if (launch_ssm_gates(a, sg, st) != 0 || launch_ssm_chains_tc(a, sg, ws, st) != 0) return -1;
+  if ((a.dv == 128 ? grads<128>(a, sg, ws, st) : grads<64>(a, sg, ws, st)) != 0) return -1;
+  if (ws.dqp && launch_ssm_group_sum(a, ws.dqp, ws.dkp, st) != 0) return -1;
+  return launch_ssm_param_sums(a, ws.sums, 4 * ((a.T + L - 1) / L), st);
+}
+
+}  // namespace mesa

@@ -558,6 +558,18 @@ bool launch_tc(int kind, K kernel, dim3 grid, int threads, uint32_t smem, cudaSt
   return cudaPeekAtLastError() == cudaSuccess;
 }
 
+void launch_join(const SsmArgs &a, const SsmSegments &sg, bool adjoint, cudaStream_t st) {
+  timing_mark_begin(K_SSM_SCAN, st);
+  mesa_ssm_join_kernel<<<dim3(a.dv * DK / 512, a.units()), 128, 0, st>>>(a, sg, adjoint);
+  timing_mark_end(K_SSM_SCAN, st);
+}
+template <int P, int MODE>
+bool launch_chain(const SsmArgs &a, const SsmSegments &sg, uint8_t *kept, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
+  const int n = MODE == kSegment || MODE == kAdjointSegment ? sg.n - 1 : sg.n;
+  return launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<P, MODE>, dim3(a.units(), n), 448, kChainSmem<P>, st, a, sg, sg.records, kept, k,
+                   v);
+}
+
 template <int P>
 int forward(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
   CUtensorMap q{}, k{}, v{}, o{};
@@ -565,17 +577,29 @@ int forward(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&o, a.out, a.units(), a.T, P))
     return -1;
   if (sg.n > 1) {
-    if (!launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<P, kSegment>, dim3(a.units(), sg.n - 1), 448, kChainSmem<P>, st, a, sg,
-                   sg.records, (uint8_t *)nullptr, k, v))
-      return -1;
-    timing_mark_begin(K_SSM_SCAN, st);
-    mesa_ssm_join_kernel<<<dim3(P * DK / 512, a.units()), 128, 0, st>>>(a, sg, false);
-    timing_mark_end(K_SSM_SCAN, st);
+    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st)) return -1;
+    launch_join(a, sg, false, st);
   }
   return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<P>, dim3(a.units(), sg.n), 576, kFwdSmem<P>, st, a, sg, sg.records, q, k,
                    v, o)
              ? 0
              : -1;
+}
+
+// The states before every chunk and the adjoints after it.
+template <int P>
+int chains(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStream_t st) {
+  CUtensorMap q{}, k{}, v{}, g{};
+  if (!tmap_units_bf16(&q, a.q, a.B * a.Hk, a.T, DK) || !tmap_units_bf16(&k, a.k, a.B * a.Hk, a.T, DK) ||
+      !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&g, a.dout, a.units(), a.T, P))
+    return -1;
+  if (sg.n > 1) {
+    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st)) return -1;
+    launch_join(a, sg, false, st);
+    if (!launch_chain<P, kAdjointSegment>(a, sg, nullptr, q, g, st)) return -1;
+    launch_join(a, sg, true, st);
+  }
+  return launch_chain<P, kKeep>(a, sg, ws.S, k, v, st) && launch_chain<P, kAdjoint>(a, sg, ws.R, q, g, st) ? 0 : -1;
 }
 
 }  // namespace
@@ -613,6 +637,9 @@ int launch_ssm_forward_tc(const SsmArgs &a, void *workspace, cudaStream_t st) {
   const SsmSegments sg = ssm_segments(a.units(), a.T, a.dv, false, workspace, nullptr);
   if (launch_ssm_gates(a, sg, st) != 0) return -1;
   return a.dv == 128 ? forward<128>(a, sg, st) : forward<64>(a, sg, st);
+}
+int launch_ssm_chains_tc(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStream_t st) {
+  return a.dv == 128 ? chains<128>(a, sg, ws, st) : chains<64>(a, sg, ws, st);
 }
 size_t ssm_tc_workspace(int U, int T, int dv) {
   size_t n;

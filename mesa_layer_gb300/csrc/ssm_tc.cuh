@@ -136,4 +136,16 @@ struct SsmSegments {
   float *records = nullptr;              // [U, NC] the chunks' gates
 };
 
+// workspace nullptr: the bytes alone.
+SsmSegments ssm_segments(int U, int T, int dv, bool backward, void *workspace, size_t *bytes);
+
+// The backward's workspace: [U, NC] operand tiles of the states before the chunks and the adjoints after them; [3][U, 4 NC]
+// sums for the parameters; per-unit dq, dk [U, T, dk] (nullptr when every head has its own q, k).
+struct SsmTcBwd {
+  uint8_t *S, *R;
+  float *sums, *dqp, *dkp;
+};
+int launch_ssm_gates(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st);
+int launch_ssm_chains_tc(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStream_t st);
+
 }  // namespace mesa
