@@ -8,6 +8,8 @@
 // Eight products of 128^3 a chunk (P = 128).  The scales f, c D and c are put on where the products lie in tensor memory,
 // with the sums that the decays' gradients need on the way.  The pairs' terms X = (Q K^T) o W stay fp32, and the sum over
 // readers i >= t and writers j < t runs as F(t + 1) = F(t) - sum_j X_tj + sum_i X_it inside a chunk (2^-24 of the terms).
+// du . v is the sum of the same terms (X / D over a token's readers) and c (V R) . k, not a product with du: M's rounding
+// to bf16 would be in it (ddt 1.6e-3 off before its own rounding, so 3e-4; the sum of ddt over a head 3.7e-3, so 7e-4).
 #include "launch.h"
 #include "ssm_tc.cuh"
 
@@ -24,7 +26,7 @@ struct Grad {
                             W = P == 128 ? S : S + V_TILE<P>, M = W + QK_TILE, MISC = M + QK_TILE;
 };
 struct GradMisc {
-  float col[4][L];  // by rows' warp: sum over its rows of X
+  float col[4][L];  // by rows' warp: sum over its rows of X / D
   float frob[2][16];
   float scan[2][4];
   uint64_t full1, full2, c1, c2, e, fg, h, a_done, b_done, c_done, f_done, qk_staged, v_staged, drain;
@@ -36,7 +38,7 @@ constexpr uint32_t kGradSmem = Grad<P>::MISC + sizeof(GradMisc);
 static_assert(kGradSmem<128> <= 232448, "shared memory per block");
 // Tensor memory: Q K^T, then du | g V^T, then sums by token | dQ | dK.  The sums' columns, by quarter of the channels:
 constexpr uint32_t T_A = 0, T_B = 128, T_DQ = 256, T_DK = 384;
-constexpr int X_ROW = 0, X_IN = 4, X_OUT = 8, X_DUV = 12, X_GV = 16;
+constexpr int X_ROW = 0, X_IN = 4, X_OUT = 8, X_GV = 12, X_DIAG = 13;
 
 __device__ __forceinline__ void tmem_put(uint32_t taddr, float x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
@@ -128,7 +130,7 @@ __global__ void __launch_bounds__(576, 1)
         break;
       }
       // ---- M', W and the pairs' sums: block (w, b) ----
-      float row = 0.0f, gv = 0.0f;
+      float row = 0.0f, gv = 0.0f, diag = 0.0f;
       need(m->c1, par);
       if (b <= w) {
         float x[32], y[32];
@@ -153,11 +155,11 @@ __global__ void __launch_bounds__(576, 1)
               const int j = 8 * cc + 4 * q + i;
               const float e = b < w ? fac * re[i] : rule::ex2(mine - re[i]);
               const bool keep = on >> j & 1;
-              if (b == w && j == lane) gv = y[j];
               mm[i] = keep ? x[j] * e : 0.0f;
               ww[i] = keep ? y[j] * (e * se[i]) : 0.0f;
-              x[j] = keep && !(b == w && j == lane) ? x[j] * ww[i] : 0.0f;
-              row += x[j];
+              x[j] = mm[i] * y[j];
+              if (b == w && j == lane) gv = y[j], diag = x[j], x[j] = 0.0f;
+              row = fmaf(x[j], se[i], row);
             }
             om[2 * q] = bf2(mm[0], mm[1]), om[2 * q + 1] = bf2(mm[2], mm[3]);
             ow[2 * q] = bf2(ww[0], ww[1]), ow[2 * q + 1] = bf2(ww[2], ww[3]);
@@ -180,8 +182,7 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->a_done);
       // ---- f (g S) and c D (V R), with what passes into and out of the chunk ----
       need(m->c2, par);
-      float x_in, x_out;
-      auto scaled = [&](uint32_t col, const uint8_t *tile, float s) {  // returns the row's product with the tile's
+      auto scaled = [&](uint32_t col, const uint8_t *tile, float s) {  // returns the row's product with the tile's, unscaled
         float x[32];
         tc::tmem_ld32(tl + col + 32 * b, x);
         const u64 s2 = pack2(s, s);
@@ -194,16 +195,15 @@ __global__ void __launch_bounds__(576, 1)
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const int e = 8 * cc + 2 * i;
-            const u64 y = mul2(pack2(x[e], x[e + 1]), s2);
+            const u64 y = pack2(x[e], x[e + 1]);
             dot = fma2(y, of_bf2(qs[i]), dot);
-            unpack2(y, x[e], x[e + 1]);
+            unpack2(mul2(y, s2), x[e], x[e + 1]);
           }
         }
         tc::tmem_st32(tl + col + 32 * b, x);
         return sum2(dot);
       };
-      x_in = scaled(T_DQ, sm, f);
-      x_out = scaled(T_DK, sm + O::K, ct * step);
+      const float x_in = f * scaled(T_DQ, sm, f), x_out = ct * scaled(T_DK, sm + O::K, ct * step);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       warp_arrive(m->b_done);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(576, 1)
         tmem_put(tl + T_B + X_ROW + b, row);
         tmem_put(tl + T_B + X_IN + b, x_in);
         tmem_put(tl + T_B + X_OUT + b, x_out);
-        if (b == w) tmem_put(tl + T_B + X_GV, gv);
+        if (b == w) tmem_put(tl + T_B + X_GV, gv), tmem_put(tl + T_B + X_DIAG, diag);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         warp_arrive(m->c_done);
@@ -257,26 +257,22 @@ __global__ void __launch_bounds__(576, 1)
         tc::tmem_ld<N>(tl + T_A + N * b, x);
         const float skip = a.skip ? a.skip[h] : 0.0f;
         const u64 step2 = pack2(step, step), skip2 = pack2(skip, skip);
-        u64 dot = 0;
         tc::tmem_ld_wait();
 #pragma unroll
         for (int cc = 0; cc < N / 8; cc++) {
           const uint32_t to = tile_off(t, N / 8 * b + cc, L);
-          const uint4 v = *reinterpret_cast<const uint4 *>(sm + O::V + to), g = *reinterpret_cast<const uint4 *>(sm + O::G + to);
-          const uint32_t vs[4] = {v.x, v.y, v.z, v.w}, gs[4] = {g.x, g.y, g.z, g.w};
+          const uint4 g = *reinterpret_cast<const uint4 *>(sm + O::G + to);
+          const uint32_t gs[4] = {g.x, g.y, g.z, g.w};
           uint32_t o[4];
 #pragma unroll
           for (int i = 0; i < 4; i++) {
             const u64 du = pack2(x[8 * cc + 2 * i], x[8 * cc + 2 * i + 1]);
-            dot = fma2(du, of_bf2(vs[i]), dot);
             o[i] = bf2(a.skip ? fma2(skip2, of_bf2(gs[i]), mul2(step2, du)) : mul2(step2, du));
           }
           const uint4 y = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4 *>(sm + O::G + to) = y;
           if (in) bad = rule::absmax_words(bad, y);
         }
-        tmem_put(tl + T_B + X_DUV + b, sum2(dot));
-        tc::tmem_st_wait();
         tc::fence_before_sync();
         tc::fence_smem_to_async();
         warp_arrive(m->v_staged);
@@ -288,8 +284,8 @@ __global__ void __launch_bounds__(576, 1)
       if (b > 0) continue;
       // ---- the steps' gradients: token t ----
       tc::fence_after_sync();
-      float x[32];
-      tc::tmem_ld32(tl + T_B, x);
+      float x[16];
+      tc::tmem_ld16(tl + T_B, x);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       auto four = [&](int i) { return (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]); };
@@ -299,7 +295,7 @@ __global__ void __launch_bounds__(576, 1)
         if (i >= w) col += m->col[i][t];
 #pragma unroll
       for (int i = 0; i < 16; i++) all += m->frob[par][i];
-      const float xi = four(X_IN), moved = col - four(X_ROW) + four(X_OUT);
+      const float xi = four(X_IN), xo = four(X_OUT), moved = fmaf(step, col + xo, -four(X_ROW)), duv = (col + x[X_DIAG]) + xo;
       float suf = xi, pre = moved;  // readers from t on, writers before t (with the pairs)
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -319,7 +315,7 @@ __global__ void __launch_bounds__(576, 1)
       const bool start = __float_as_int(r[R_START + t]) == t;
       const float da = start ? 0.0f : pre + suf + r[R_ALL] * all;
       const float raw = in ? a.dt[(size_t)u * a.T + c * L + t] + (a.dt_bias ? a.dt_bias[h] : 0.0f) : 0.0f;
-      const float dd = in ? fmaf(a.A[h], da, four(X_DUV)) * sigmoid(raw) : 0.0f;
+      const float dd = in ? fmaf(a.A[h], da, duv) * sigmoid(raw) : 0.0f;
       if (in) {
         if (!isfinite(dd)) bad = 0x7f80u;
         const size_t i = (size_t)u * a.T + c * L + t;
