@@ -26,7 +26,7 @@ struct Grad {
                             W = P == 128 ? S : S + V_TILE<P>, M = W + QK_TILE, MISC = M + QK_TILE;
 };
 struct GradMisc {
-  float col[4][L];  // by rows' warp: sum over its rows of X / D
+  alignas(16) float rec[REC];  // the chunk's gates
   float frob[2][16];
   float scan[2][4];
   uint64_t full1, full2, c1, c2, e, fg, h, a_done, b_done, c_done, f_done, qk_staged, v_staged, drain;
@@ -40,13 +40,15 @@ static_assert(kGradSmem<128> <= 232448, "shared memory per block");
 constexpr uint32_t T_A = 0, T_B = 128, T_DQ = 256, T_DK = 384;
 constexpr int X_ROW = 0, X_IN = 4, X_OUT = 8, X_GV = 12, X_DIAG = 13;
 
+// (By rows' warp and token: the sum over its rows of X / D, in V's place once the products have read V.)
+__device__ __forceinline__ float *columns(uint8_t *v) { return reinterpret_cast<float *>(v); }
 __device__ __forceinline__ void tmem_put(uint32_t taddr, float x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
 }
-// Lane l's sum over the warp's lanes of x[l].
-__device__ __forceinline__ float transposed_sum(float (&x)[32], int lane) {
+// The sum over the warp's lanes of x[lane % 8].
+__device__ __forceinline__ float transposed_sum(float (&x)[8], int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 4; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; i++) {
@@ -54,7 +56,16 @@ __device__ __forceinline__ float transposed_sum(float (&x)[32], int lane) {
       x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
-  return x[0];
+  float y = x[0];
+  y += __shfl_xor_sync(0xffffffffu, y, 8);
+  return y + __shfl_xor_sync(0xffffffffu, y, 16);
+}
+// L2 prefetches of what the next chunk's copies will read.
+__device__ __forceinline__ void prefetch_tile(const void *map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n" ::"l"(map), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void prefetch_bytes(const void *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // A resident CTA per SM over `chunks` chunks of all units, 576 threads: warps 0-15 (lane quarter warp % 4, column
@@ -108,10 +119,13 @@ __global__ void __launch_bounds__(576, 1)
       const uint32_t par = it & 1;
       const int u = at / NC, c = at - u * NC, h = u % a.H;
       const bool in = c * L + t < a.T;
-      const float *r = record(records, u, NC, c);
-      const float r_in = r[R_IN + t], step = r[R_STEP + t], f = r_in * r[R_FIRST + w], ct = r[R_OUT + t] * r[R_LAST + w];
+      const float raw = in ? a.dt[(size_t)u * a.T + c * L + t] + (a.dt_bias ? a.dt_bias[h] : 0.0f) : 0.0f;
       // <S, R>: 8 P bytes a thread of each
       if (!need(m->full2, par)) break;
+      const float *r = m->rec;
+      const float r_in = r[R_IN + t], step = r[R_STEP + t], f = r_in * r[R_FIRST + w], ct = r[R_OUT + t] * r[R_LAST + w],
+                  mine = r[R_LOG + t], across = r[R_ALL];
+      const int start = __float_as_int(r[R_START + t]);
       {
         u64 x2 = 0;
 #pragma unroll 2
@@ -129,46 +143,53 @@ __global__ void __launch_bounds__(576, 1)
         ok = false;
         break;
       }
-      // ---- M', W and the pairs' sums: block (w, b) ----
-      float row = 0.0f, gv = 0.0f, diag = 0.0f;
+      // ---- M', W and the pairs' sums: block (w, b), eight columns at a time ----
+      float row = 0.0f, gv = 0.0f, diag = 0.0f, col = 0.0f;  // col: column 32 b + lane
       need(m->c1, par);
       if (b <= w) {
-        float x[32], y[32];
-        tc::tmem_ld32(tl + T_A + 32 * b, x);
-        tc::tmem_ld32(tl + T_B + 32 * b, y);
-        const float fac = b < w ? r[R_BETWEEN + 4 * w + b] * r_in : 1.0f, mine = r[R_LOG + t];
-        const int first = max(__float_as_int(r[R_START + t]) - 32 * w, 0);
-        const uint32_t on = b < w ? 0xffffffffu : (0xffffffffu >> (31 - lane)) & (0xffffffffu << first);  // columns that count
-        const float4 *rj = reinterpret_cast<const float4 *>(r + (b < w ? R_OUT : R_LOG) + 32 * b),
-                     *sj = reinterpret_cast<const float4 *>(r + R_STEP + 32 * b);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int cc = 0; cc < 4; cc++) {
-          uint32_t om[4], ow[4];
+        const float fac = b < w ? r[R_BETWEEN + 4 * w + b] * r_in : 1.0f;
+        const uint32_t on = b < w ? 0xffffffffu : (0xffffffffu >> (31 - lane)) & (0xffffffffu << max(start - 32 * w, 0));  // columns that count
+        const float *rj = r + (b < w ? R_OUT : R_LOG) + 32 * b, *sj = r + R_STEP + 32 * b;
+        float x[2][8], y[2][8];
+        tc::tmem_ld8(tl + T_A + 32 * b, x[0]);
+        tc::tmem_ld8(tl + T_B + 32 * b, y[0]);
+        auto piece = [&](int cc, float (&x)[8], float (&y)[8]) {
+          float mm[8], ww[8];
 #pragma unroll
           for (int q = 0; q < 2; q++) {
-            const float4 rv = rj[2 * cc + q], sv = sj[2 * cc + q];
+            const float4 rv = *reinterpret_cast<const float4 *>(rj + 8 * cc + 4 * q), sv = *reinterpret_cast<const float4 *>(sj + 8 * cc + 4 * q);
             const float re[4] = {rv.x, rv.y, rv.z, rv.w}, se[4] = {sv.x, sv.y, sv.z, sv.w};
-            float mm[4], ww[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-              const int j = 8 * cc + 4 * q + i;
+              const int j = 4 * q + i;
               const float e = b < w ? fac * re[i] : rule::ex2(mine - re[i]);
-              const bool keep = on >> j & 1;
-              mm[i] = keep ? x[j] * e : 0.0f;
-              ww[i] = keep ? y[j] * (e * se[i]) : 0.0f;
-              x[j] = mm[i] * y[j];
-              if (b == w && j == lane) gv = y[j], diag = x[j], x[j] = 0.0f;
+              const bool keep = on >> (8 * cc + j) & 1;
+              mm[j] = keep ? x[j] * e : 0.0f;
+              ww[j] = keep ? y[j] * (e * se[i]) : 0.0f;
+              x[j] = mm[j] * y[j];
+              if (b == w && 8 * cc + j == lane) gv = y[j], diag = x[j], x[j] = 0.0f;
               row = fmaf(x[j], se[i], row);
             }
-            om[2 * q] = bf2(mm[0], mm[1]), om[2 * q + 1] = bf2(mm[2], mm[3]);
-            ow[2 * q] = bf2(ww[0], ww[1]), ow[2 * q + 1] = bf2(ww[2], ww[3]);
           }
           const uint32_t to = tile_off(t, 4 * b + cc, L);
-          *reinterpret_cast<uint4 *>(sm + O::M + to) = make_uint4(om[0], om[1], om[2], om[3]);
-          *reinterpret_cast<uint4 *>(sm + O::W + to) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+          *reinterpret_cast<uint4 *>(sm + O::M + to) = make_uint4(bf2(mm[0], mm[1]), bf2(mm[2], mm[3]), bf2(mm[4], mm[5]), bf2(mm[6], mm[7]));
+          *reinterpret_cast<uint4 *>(sm + O::W + to) = make_uint4(bf2(ww[0], ww[1]), bf2(ww[2], ww[3]), bf2(ww[4], ww[5]), bf2(ww[6], ww[7]));
+          const float sum = transposed_sum(x, lane);
+          if (lane >> 3 == cc) col = sum;
+        };
+#pragma unroll 1
+        for (int cc = 0; cc < 4; cc += 2) {
+          tc::tmem_ld_wait();
+          tc::tmem_ld8(tl + T_A + 32 * b + 8 * cc + 8, x[1]);
+          tc::tmem_ld8(tl + T_B + 32 * b + 8 * cc + 8, y[1]);
+          piece(cc, x[0], y[0]);
+          tc::tmem_ld_wait();
+          if (cc == 0) {
+            tc::tmem_ld8(tl + T_A + 32 * b + 16, x[0]);
+            tc::tmem_ld8(tl + T_B + 32 * b + 16, y[0]);
+          }
+          piece(cc + 1, x[1], y[1]);
         }
-        m->col[w][32 * b + lane] = transposed_sum(x, lane);
       } else {
 #pragma unroll
         for (int cc = 0; cc < 4; cc++) {
@@ -182,25 +203,25 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->a_done);
       // ---- f (g S) and c D (V R), with what passes into and out of the chunk ----
       need(m->c2, par);
+      if (b <= w) columns(sm + O::V)[w * L + 32 * b + lane] = col;
       auto scaled = [&](uint32_t col, const uint8_t *tile, float s) {  // returns the row's product with the tile's, unscaled
-        float x[32];
-        tc::tmem_ld32(tl + col + 32 * b, x);
         const u64 s2 = pack2(s, s);
         u64 dot = 0;
-        tc::tmem_ld_wait();
-#pragma unroll
+#pragma unroll 2
         for (int cc = 0; cc < 4; cc++) {
+          float x[8];
+          tc::tmem_ld8(tl + col + 32 * b + 8 * cc, x);
           const uint4 q = *reinterpret_cast<const uint4 *>(tile + tile_off(t, 4 * b + cc, L));
           const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
+          tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const int e = 8 * cc + 2 * i;
-            const u64 y = pack2(x[e], x[e + 1]);
+            const u64 y = pack2(x[2 * i], x[2 * i + 1]);
             dot = fma2(y, of_bf2(qs[i]), dot);
-            unpack2(mul2(y, s2), x[e], x[e + 1]);
+            unpack2(mul2(y, s2), x[2 * i], x[2 * i + 1]);
           }
+          tc::tmem_st8(tl + col + 32 * b + 8 * cc, x);
         }
-        tc::tmem_st32(tl + col + 32 * b, x);
         return sum2(dot);
       };
       const float x_in = f * scaled(T_DQ, sm, f), x_out = ct * scaled(T_DK, sm + O::K, ct * step);
@@ -227,21 +248,26 @@ __global__ void __launch_bounds__(576, 1)
       }
       // ---- dQ, dK ----
       need(m->fg, par);
-      auto put = [&](uint32_t col, uint8_t *tile, float *part) {
-        float x[32];
-        tc::tmem_ld32(tl + col + 32 * b, x);
-        tc::tmem_ld_wait();
+      float sum = 0.0f;
+      if (b == 0) {  // (all warps' columns are there)
 #pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (i >= w) sum += columns(sm + O::V)[i * L + t];
+      }
+      auto put = [&](uint32_t col, uint8_t *tile, float *part) {
+#pragma unroll 2
         for (int cc = 0; cc < 4; cc++) {
-          const uint4 o = make_uint4(bf2(x[8 * cc], x[8 * cc + 1]), bf2(x[8 * cc + 2], x[8 * cc + 3]), bf2(x[8 * cc + 4], x[8 * cc + 5]),
-                                     bf2(x[8 * cc + 6], x[8 * cc + 7]));
+          float x[8];
+          tc::tmem_ld8(tl + col + 32 * b + 8 * cc, x);
+          tc::tmem_ld_wait();
+          const uint4 o = make_uint4(bf2(x[0], x[1]), bf2(x[2], x[3]), bf2(x[4], x[5]), bf2(x[6], x[7]));
           if (in) bad = rule::absmax_words(bad, o);
           if (!part) {
             *reinterpret_cast<uint4 *>(tile + tile_off(t, 4 * b + cc, L)) = o;
           } else if (in) {
             float4 *dst = reinterpret_cast<float4 *>(part + ((size_t)u * a.T + c * L + t) * DK + 32 * b + 8 * cc);
-            dst[0] = make_float4(x[8 * cc], x[8 * cc + 1], x[8 * cc + 2], x[8 * cc + 3]);
-            dst[1] = make_float4(x[8 * cc + 4], x[8 * cc + 5], x[8 * cc + 6], x[8 * cc + 7]);
+            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
           }
         }
       };
@@ -253,20 +279,20 @@ __global__ void __launch_bounds__(576, 1)
       need(m->h, par);
       {
         constexpr int N = P / 4;
-        float x[N];
-        tc::tmem_ld<N>(tl + T_A + N * b, x);
         const float skip = a.skip ? a.skip[h] : 0.0f;
         const u64 step2 = pack2(step, step), skip2 = pack2(skip, skip);
-        tc::tmem_ld_wait();
-#pragma unroll
+#pragma unroll 2
         for (int cc = 0; cc < N / 8; cc++) {
+          float x[8];
+          tc::tmem_ld8(tl + T_A + N * b + 8 * cc, x);
           const uint32_t to = tile_off(t, N / 8 * b + cc, L);
           const uint4 g = *reinterpret_cast<const uint4 *>(sm + O::G + to);
           const uint32_t gs[4] = {g.x, g.y, g.z, g.w};
           uint32_t o[4];
+          tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const u64 du = pack2(x[8 * cc + 2 * i], x[8 * cc + 2 * i + 1]);
+            const u64 du = pack2(x[2 * i], x[2 * i + 1]);
             o[i] = bf2(a.skip ? fma2(skip2, of_bf2(gs[i]), mul2(step2, du)) : mul2(step2, du));
           }
           const uint4 y = make_uint4(o[0], o[1], o[2], o[3]);
@@ -288,14 +314,15 @@ __global__ void __launch_bounds__(576, 1)
       tc::tmem_ld16(tl + T_B, x);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
+      warp_arrive(m->f_done);
       auto four = [&](int i) { return (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]); };
-      float col = 0.0f, all = 0.0f;
+      float all = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        if (i >= w) col += m->col[i][t];
-#pragma unroll
-      for (int i = 0; i < 16; i++) all += m->frob[par][i];
-      const float xi = four(X_IN), xo = four(X_OUT), moved = fmaf(step, col + xo, -four(X_ROW)), duv = (col + x[X_DIAG]) + xo;
+      for (int i = 0; i < 4; i++) {
+        const float4 y = *reinterpret_cast<const float4 *>(&m->frob[par][4 * i]);
+        all += (y.x + y.y) + (y.z + y.w);
+      }
+      const float xi = four(X_IN), xo = four(X_OUT), moved = fmaf(step, sum + xo, -four(X_ROW)), duv = (sum + x[X_DIAG]) + xo;
       float suf = xi, pre = moved;  // readers from t on, writers before t (with the pairs)
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -312,9 +339,7 @@ __global__ void __launch_bounds__(576, 1)
         if (i > w) suf += m->scan[0][i];
         if (i < w) pre += m->scan[1][i];
       }
-      const bool start = __float_as_int(r[R_START + t]) == t;
-      const float da = start ? 0.0f : pre + suf + r[R_ALL] * all;
-      const float raw = in ? a.dt[(size_t)u * a.T + c * L + t] + (a.dt_bias ? a.dt_bias[h] : 0.0f) : 0.0f;
+      const float da = start == t ? 0.0f : pre + suf + across * all;
       const float dd = in ? fmaf(a.A[h], da, duv) * sigmoid(raw) : 0.0f;
       if (in) {
         if (!isfinite(dd)) bad = 0x7f80u;
@@ -325,7 +350,6 @@ __global__ void __launch_bounds__(576, 1)
           static_cast<__nv_bfloat16 *>(a.ddt)[i] = __float2bfloat16_rn(dd);
       }
       const float sA = warp_sum(in ? step * da : 0.0f), sb = warp_sum(dd), sg = warp_sum(x[X_GV]);
-      warp_arrive(m->f_done);
       if (lane == 0) {  // a warp's tokens each
         const size_t n = (size_t)chunks * 4, i = (size_t)at * 4 + w;
         sums[i] = sA;
@@ -394,9 +418,20 @@ __global__ void __launch_bounds__(576, 1)
     };
     auto fetch_states = [&](int at) {
       const uint32_t b = bar(m->full2);
-      tc::mbar_arrive_expect_tx(b, 2 * V_TILE<P>);
+      tc::mbar_arrive_expect_tx(b, 2 * V_TILE<P> + REC * 4);
+      tc::bulk_g2s(tc::smem_u32(m->rec), records + (size_t)at * REC, REC * 4, b);
       tc::bulk_g2s(tc::smem_u32(sm + O::S), states + (size_t)at * V_TILE<P>, V_TILE<P>, b);
       tc::bulk_g2s(tc::smem_u32(sm + O::R), adjoints + (size_t)at * V_TILE<P>, V_TILE<P>, b);
+    };
+    auto prefetch = [&](int at) {
+      const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u);
+#pragma unroll
+      for (int i = 0; i < 2; i++) prefetch_tile(&mapQ, 64 * i, y, uk), prefetch_tile(&mapK, 64 * i, y, uk);
+#pragma unroll
+      for (int i = 0; i < P / 64; i++) prefetch_tile(&mapV, 64 * i, y, u), prefetch_tile(&mapG, 64 * i, y, u);
+      prefetch_bytes(states + (size_t)at * V_TILE<P>, V_TILE<P>);
+      prefetch_bytes(adjoints + (size_t)at * V_TILE<P>, V_TILE<P>);
+      prefetch_bytes(records + (size_t)at * REC, REC * 4);
     };
     if ((int)blockIdx.x < chunks) {
       fetch_rows(blockIdx.x);
@@ -406,6 +441,7 @@ __global__ void __launch_bounds__(576, 1)
     for (int at = blockIdx.x, it = 0; at < chunks; at += gridDim.x, it++) {
       const uint32_t par = it & 1;
       const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u), next = at + gridDim.x;
+      if (next < chunks) prefetch(next);
       if (!(ok = wait(bar(m->qk_staged), par, limit, gave_up))) break;
       if (!dqp) {
 #pragma unroll
