@@ -232,11 +232,10 @@ __global__ void __launch_bounds__(256) mesa_ssm_params_kernel(SsmArgs a, const f
   if (!dst) return;
   const size_t U = (size_t)a.units();
   float x = 0.0f;
-  for (int b = 0; b < a.B; b++) {
-    const float *s = sums + (which * U + (size_t)b * a.H + h) * n;
-    float y = 0.0f;
-    for (int i = threadIdx.x; i < n; i += 256) y += s[i];
-    x += y;
+#pragma unroll 4
+  for (size_t i = threadIdx.x; i < (size_t)a.B * n; i += 256) {
+    const size_t b = i / n;
+    x += sums[(which * U + b * a.H + h) * n + (i - b * n)];
   }
   x = warp_sum(x);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(576, 1)
     tc::fence_after_sync();
     return ok;
   };
-  int sent = 0;  // chunks asked for (warp 17)
+  int sent1 = 0, sent2 = 0;  // chunks asked for (warp 17)
 
   if (warp < 16) {
     const int w = warp & 3, b = warp >> 2, t = 32 * w + lane;  // row t, columns of quarter b
@@ -148,32 +148,49 @@ __global__ void __launch_bounds__(576, 1)
       need(m->c1, par);
       if (b <= w) {
         const float fac = b < w ? r[R_BETWEEN + 4 * w + b] * r_in : 1.0f;
+        const u64 fac2 = pack2(fac, fac);
+        u64 row2 = 0;
         const uint32_t on = b < w ? 0xffffffffu : (0xffffffffu >> (31 - lane)) & (0xffffffffu << max(start - 32 * w, 0));  // columns that count
         const float *rj = r + (b < w ? R_OUT : R_LOG) + 32 * b, *sj = r + R_STEP + 32 * b;
         float x[2][8], y[2][8];
         tc::tmem_ld8(tl + T_A + 32 * b, x[0]);
         tc::tmem_ld8(tl + T_B + 32 * b, y[0]);
         auto piece = [&](int cc, float (&x)[8], float (&y)[8]) {
-          float mm[8], ww[8];
+          uint32_t om[4], ow[4];
 #pragma unroll
           for (int q = 0; q < 2; q++) {
-            const float4 rv = *reinterpret_cast<const float4 *>(rj + 8 * cc + 4 * q), sv = *reinterpret_cast<const float4 *>(sj + 8 * cc + 4 * q);
-            const float re[4] = {rv.x, rv.y, rv.z, rv.w}, se[4] = {sv.x, sv.y, sv.z, sv.w};
+            const ulonglong2 rv = *reinterpret_cast<const ulonglong2 *>(rj + 8 * cc + 4 * q),
+                             sv = *reinterpret_cast<const ulonglong2 *>(sj + 8 * cc + 4 * q);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-              const int j = 4 * q + i;
-              const float e = b < w ? fac * re[i] : rule::ex2(mine - re[i]);
-              const bool keep = on >> (8 * cc + j) & 1;
-              mm[j] = keep ? x[j] * e : 0.0f;
-              ww[j] = keep ? y[j] * (e * se[i]) : 0.0f;
-              x[j] = mm[j] * y[j];
-              if (b == w && 8 * cc + j == lane) gv = y[j], diag = x[j], x[j] = 0.0f;
-              row = fmaf(x[j], se[i], row);
+            for (int i = 0; i < 2; i++) {
+              const int j = 4 * q + 2 * i;
+              const u64 se = i ? sv.y : sv.x, x2 = pack2(x[j], x[j + 1]), y2 = pack2(y[j], y[j + 1]);
+              u64 e = i ? rv.y : rv.x;
+              if (b < w) {
+                e = mul2(fac2, e);
+              } else {  // the diagonal block: e = 0 where a column does not count
+                float l0, l1;
+                unpack2(e, l0, l1);
+                e = pack2(on >> (8 * cc + j) & 1 ? rule::ex2(mine - l0) : 0.0f, on >> (8 * cc + j + 1) & 1 ? rule::ex2(mine - l1) : 0.0f);
+              }
+              const u64 m2 = mul2(x2, e);
+              u64 z2 = mul2(m2, y2);
+              om[2 * q + i] = bf2(m2);
+              ow[2 * q + i] = bf2(mul2(y2, mul2(e, se)));
+              if (b == w) {
+                float z0, z1;
+                unpack2(z2, z0, z1);
+                if (8 * cc + j == lane) gv = y[j], diag = z0, z0 = 0.0f;
+                if (8 * cc + j + 1 == lane) gv = y[j + 1], diag = z1, z1 = 0.0f;
+                z2 = pack2(z0, z1);
+              }
+              row2 = fma2(z2, se, row2);
+              unpack2(z2, x[j], x[j + 1]);
             }
           }
           const uint32_t to = tile_off(t, 4 * b + cc, L);
-          *reinterpret_cast<uint4 *>(sm + O::M + to) = make_uint4(bf2(mm[0], mm[1]), bf2(mm[2], mm[3]), bf2(mm[4], mm[5]), bf2(mm[6], mm[7]));
-          *reinterpret_cast<uint4 *>(sm + O::W + to) = make_uint4(bf2(ww[0], ww[1]), bf2(ww[2], ww[3]), bf2(ww[4], ww[5]), bf2(ww[6], ww[7]));
+          *reinterpret_cast<uint4 *>(sm + O::M + to) = make_uint4(om[0], om[1], om[2], om[3]);
+          *reinterpret_cast<uint4 *>(sm + O::W + to) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
           const float sum = transposed_sum(x, lane);
           if (lane >> 3 == cc) col = sum;
         };
@@ -190,6 +207,7 @@ __global__ void __launch_bounds__(576, 1)
           }
           piece(cc + 1, x[1], y[1]);
         }
+        row = sum2(row2);
       } else {
 #pragma unroll
         for (int cc = 0; cc < 4; cc++) {
@@ -407,22 +425,28 @@ __global__ void __launch_bounds__(576, 1)
     }
   } else if (lane == 0) {
     // ---- copies ----
-    auto fetch_rows = [&](int at) {
-      const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u);
-      const uint32_t b = bar(m->full1);
-      tc::mbar_arrive_expect_tx(b, 2 * QK_TILE + 2 * V_TILE<P>);
-      load_tile<DK>(tc::smem_u32(sm), &mapQ, y, uk, b);
-      load_tile<DK>(tc::smem_u32(sm + O::K), &mapK, y, uk, b);
-      load_tile<P>(tc::smem_u32(sm + O::G), &mapG, y, u, b);
-      load_tile<P>(tc::smem_u32(sm + O::V), &mapV, y, u, b);
+    // Q and K, V, G arrive at full1, S, R and the gates at full2; the first of each announces them all.
+    auto tile = [&](uint32_t where, const CUtensorMap &map, int d, int at, uint64_t &b, int unit_of) {
+      const int u = at / NC, y = (at - u * NC) * L, z = unit_of ? a.qk_unit(u) : u;
+      for (int i = 0; i < d / 64; i++) tensor_g2s_3d(tc::smem_u32(sm + where) + i * HALF, &map, 64 * i, y, z, bar(b));
     };
-    auto fetch_states = [&](int at) {
-      const uint32_t b = bar(m->full2);
-      tc::mbar_arrive_expect_tx(b, 2 * V_TILE<P> + REC * 4);
-      tc::bulk_g2s(tc::smem_u32(m->rec), records + (size_t)at * REC, REC * 4, b);
-      tc::bulk_g2s(tc::smem_u32(sm + O::S), states + (size_t)at * V_TILE<P>, V_TILE<P>, b);
-      tc::bulk_g2s(tc::smem_u32(sm + O::R), adjoints + (size_t)at * V_TILE<P>, V_TILE<P>, b);
+    auto fetch_adjoint = [&](int at) {
+      tc::mbar_arrive_expect_tx(bar(m->full2), 2 * V_TILE<P> + REC * 4);
+      tc::bulk_g2s(tc::smem_u32(sm + O::R), adjoints + (size_t)at * V_TILE<P>, V_TILE<P>, bar(m->full2));
     };
+    auto fetch_state = [&](int at) {
+      tc::bulk_g2s(tc::smem_u32(m->rec), records + (size_t)at * REC, REC * 4, bar(m->full2));
+      tc::bulk_g2s(tc::smem_u32(sm + O::S), states + (size_t)at * V_TILE<P>, V_TILE<P>, bar(m->full2));
+    };
+    auto fetch_v = [&](int at) {
+      tc::mbar_arrive_expect_tx(bar(m->full1), 2 * QK_TILE + 2 * V_TILE<P>);
+      tile(O::V, mapV, P, at, m->full1, 0);
+    };
+    auto fetch_qk = [&](int at) {
+      tile(0, mapQ, DK, at, m->full1, 1);
+      tile(O::K, mapK, DK, at, m->full1, 1);
+    };
+    auto fetch_g = [&](int at) { tile(O::G, mapG, P, at, m->full1, 0); };
     auto prefetch = [&](int at) {
       const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u);
 #pragma unroll
@@ -434,15 +458,28 @@ __global__ void __launch_bounds__(576, 1)
       prefetch_bytes(records + (size_t)at * REC, REC * 4);
     };
     if ((int)blockIdx.x < chunks) {
-      fetch_rows(blockIdx.x);
-      fetch_states(blockIdx.x);
-      sent = 1;
+      fetch_v(blockIdx.x);
+      fetch_qk(blockIdx.x);
+      fetch_g(blockIdx.x);
+      fetch_adjoint(blockIdx.x);
+      fetch_state(blockIdx.x);
+      sent1 = sent2 = 1;
     }
+    // (each tile as soon as nothing reads it: R after K R^T, S or W after dQ and dK's products, V's place after the columns'
+    // sums, the others after their gradients have left from there)
     for (int at = blockIdx.x, it = 0; at < chunks; at += gridDim.x, it++) {
       const uint32_t par = it & 1;
       const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u), next = at + gridDim.x;
-      if (next < chunks) prefetch(next);
-      if (!(ok = wait(bar(m->qk_staged), par, limit, gave_up))) break;
+      const bool more = next < chunks;
+      if (more) prefetch(next);
+      if (!(ok = wait(bar(m->e), par, limit, gave_up))) break;
+      if (more) {
+        fetch_adjoint(next);
+        sent2++;
+      }
+      ok = wait(bar(m->fg), par, limit, gave_up);
+      if (more) fetch_state(next);  // (announced: it is sent whatever happened)
+      if (!ok || !(ok = wait(bar(m->qk_staged), par, limit, gave_up))) break;
       if (!dqp) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -451,16 +488,22 @@ __global__ void __launch_bounds__(576, 1)
         }
         tc::bulk_commit();
       }
-      if (!(ok = wait(bar(m->v_staged), par, limit, gave_up))) break;
-#pragma unroll
-      for (int i = 0; i < P / 64; i++) tensor_s2g_3d(&mapDv, tc::smem_u32(sm + O::G) + i * HALF, 64 * i, y, u);
-      tc::bulk_commit();
-      if (next < chunks) {
-        fetch_states(next);
+      if (more) {
+        fetch_v(next);
+        sent1++;
         tc::bulk_wait_read();
-        fetch_rows(next);
-        sent++;
+        fetch_qk(next);
       }
+      ok = wait(bar(m->v_staged), par, limit, gave_up);
+#pragma unroll
+      for (int i = 0; i < P / 64; i++)
+        if (ok) tensor_s2g_3d(&mapDv, tc::smem_u32(sm + O::G) + i * HALF, 64 * i, y, u);
+      tc::bulk_commit();
+      if (more) {
+        tc::bulk_wait_read();
+        fetch_g(next);
+      }
+      if (!ok) break;
     }
     tc::bulk_wait_all();
   }
@@ -474,8 +517,8 @@ __global__ void __launch_bounds__(576, 1)
       if (!tc::mbar_wait(bar(m->drain), 0, tc::kWaitLimit)) bits |= tc::kErrDrainTimeout;
       atomicOr(a.status, bits);
     }
-    if (tid == 544 && sent > 0 &&
-        !(tc::mbar_wait(bar(m->full1), (sent - 1) & 1, tc::kWaitLimit) && tc::mbar_wait(bar(m->full2), (sent - 1) & 1, tc::kWaitLimit)))
+    if (tid == 544 && sent1 > 0 &&
+        !(tc::mbar_wait(bar(m->full1), (sent1 - 1) & 1, tc::kWaitLimit) && tc::mbar_wait(bar(m->full2), (sent2 - 1) & 1, tc::kWaitLimit)))
       atomicOr(a.status, tc::kErrDrainTimeout);
   }
   tc::fence_before_sync();
