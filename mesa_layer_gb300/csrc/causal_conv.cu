@@ -17,7 +17,7 @@ namespace mesa {
 
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 256, kFwdBlock = 128;
 
 // VEC consecutive channels as fp32 pairs.
 template <typename TIO, int VEC>
@@ -65,12 +65,17 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int h, int c0, u64 
   }
 }
 // sigmoid(y) from the hardware's exponential and division (2^-21 relative error).
-__device__ __forceinline__ float fast_sigmoid(float y) { return __fdividef(1.0f, 1.0f + __expf(-y)); }
-__device__ __forceinline__ u64 silu2(u64 y) {
+__device__ __forceinline__ u64 sigmoid2(u64 y) {
   float p, q;
-  unpack2(y, p, q);
-  return pack2(p * fast_sigmoid(p), q * fast_sigmoid(q));
+  unpack2(mul2(y, pack2(-1.4426950408889634f, -1.4426950408889634f)), p, q);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(p));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(q));
+  unpack2(add2(pack2(p, q), pack2(1.0f, 1.0f)), p, q);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(p));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(q));
+  return pack2(p, q);
 }
+__device__ __forceinline__ u64 silu2(u64 y) { return mul2(y, sigmoid2(y)); }
 
 // The inputs before token t0 of unit u that tap windows from there reach: x[s] the one s tokens back, s = 1 .. W - 1,
 // zero across a document's start.  Returns how many of them belong to token t0 - 1's document.
@@ -101,39 +106,41 @@ __device__ __forceinline__ int load_window(const ConvArgs &a, int u, int t0, int
   return alive;
 }
 
-// Thread (unit, run, channel group) over runs of `run` tokens (a multiple of AHEAD, whose loads are in flight together).
-template <typename TIO, int VEC, int W>
-__global__ void __launch_bounds__(kBlock) mesa_causal_conv_kernel(ConvArgs a, int run, int runs) {
+// Thread (unit, run, channel group) over runs of `run` tokens; the next AHEAD tokens' inputs are on their way while the
+// present ones are worked on.
+// (Seven CTAs per SM where that fits: 60 -> 58 us at 8 x 16 x 4096 x 128.)
+template <typename TIO, int VEC, int W, bool PACKED>
+__global__ void __launch_bounds__(kFwdBlock, sizeof(TIO) == 2 && W <= 4 && !PACKED ? 7 : 1) mesa_causal_conv_kernel(ConvArgs a, int run, int runs) {
   using V = Vec<TIO, VEC>;
-  constexpr int AHEAD = 8, P = VEC / 2;
+  constexpr int AHEAD = 4, P = VEC / 2;
   const int groups = a.d / VEC;
-  const size_t i = (size_t)blockIdx.x * kBlock + threadIdx.x, total = (size_t)a.B * a.H * runs * groups;
+  const size_t i = (size_t)blockIdx.x * kFwdBlock + threadIdx.x, total = (size_t)a.B * a.H * runs * groups;
   if (i >= total) return;
   const int c0 = (int)(i % groups) * VEC, r = (int)(i / groups % runs), u = (int)(i / groups / runs);
   const int t0 = r * run, t1 = min(t0 + run, a.T);
   const TIO *src = static_cast<const TIO *>(a.x) + (size_t)u * a.T * a.d + c0;
   TIO *dst = static_cast<TIO *>(a.out) + (size_t)u * a.T * a.d + c0;
-  const uint8_t *starts = a.starts ? a.starts + (size_t)(u / a.H) * a.T : nullptr;
+  const uint8_t *starts = PACKED ? a.starts + (size_t)(u / a.H) * a.T : nullptr;
   u64 w[W][P], bias[P], x[W][P];
-  load_taps<VEC, W>(a, u % a.H, c0, w, bias);
-  load_window<TIO, VEC, W>(a, u, t0, c0, x);
-  for (int t = t0; t < t1; t += AHEAD) {
-    typename V::Raw raw[AHEAD];
-    bool cut[AHEAD];
+  typename V::Raw raw[2][AHEAD];
+  bool cut[2][AHEAD];
+  auto load = [&](int t, typename V::Raw (&x)[AHEAD], bool (&c)[AHEAD], bool whole) {
 #pragma unroll
     for (int j = 0; j < AHEAD; j++)
-      if (t + j < t1) {
-        raw[j] = *reinterpret_cast<const typename V::Raw *>(src + (size_t)(t + j) * a.d);
-        cut[j] = starts && starts[t + j];
+      if (whole || t + j < t1) {
+        x[j] = *reinterpret_cast<const typename V::Raw *>(src + (size_t)(t + j) * a.d);
+        if (PACKED) c[j] = starts[t + j];
       }
+  };
+  auto work = [&](int t, typename V::Raw (&raw)[AHEAD], bool (&cut)[AHEAD], bool whole) {
 #pragma unroll
     for (int j = 0; j < AHEAD; j++) {
-      if (t + j >= t1) break;
-      if (cut[j]) {
+      if (!whole && t + j >= t1) break;
+      if (PACKED && cut[j]) {
 #pragma unroll
         for (int s = 1; s < W; s++)
 #pragma unroll
-          for (int p = 0; p < P; p++) x[s][p] = pack2(0.0f, 0.0f);
+          for (int p = 0; p < P; p++) x[s][p] = 0;
       }
       V::unpack(raw[j], x[0]);
       u64 y[P];
@@ -150,6 +157,22 @@ __global__ void __launch_bounds__(kBlock) mesa_causal_conv_kernel(ConvArgs a, in
 #pragma unroll
         for (int p = 0; p < P; p++) x[s][p] = x[s - 1][p];
     }
+  };
+  load(t0, raw[0], cut[0], false);
+  load_window<TIO, VEC, W>(a, u, t0, c0, x);
+  load_taps<VEC, W>(a, u % a.H, c0, w, bias);
+  int t = t0;
+#pragma unroll 1
+  for (; t + 3 * AHEAD <= t1; t += 2 * AHEAD) {
+    load(t + AHEAD, raw[1], cut[1], true);
+    work(t, raw[0], cut[0], true);
+    load(t + 2 * AHEAD, raw[0], cut[0], true);
+    work(t + AHEAD, raw[1], cut[1], true);
+  }
+#pragma unroll 1
+  for (; t < t1; t += AHEAD) {  // the last tokens
+    work(t, raw[0], cut[0], false);
+    load(t + AHEAD, raw[0], cut[0], false);
   }
   if (W > 1 && a.state && t1 == a.T) {
 #pragma unroll
@@ -196,11 +219,12 @@ __global__ void __launch_bounds__(128) mesa_causal_conv_step_kernel(ConvArgs a) 
 // dy_t = do_t silu'(y_t),   dx_t = sum_s w_s dy_{t+s} (inside the document),   dw_s = sum_t dy_t x_{t-s}.
 // Block: GX channel groups of four x rows of runs; part p of a head's (batch, run) pairs; sums over a part's tokens stay
 // in registers, those of the parts are added by mesa_causal_conv_cols_kernel, both in a fixed order.
-constexpr int kBwdRun = 32;
+constexpr int kBwdRun = 64;
 __host__ __device__ inline int bwd_gx(int d) { return d / 4 < 32 ? d / 4 : 32; }
 
-template <typename TIO, int W>
-__global__ void __launch_bounds__(kBlock) mesa_causal_conv_bwd_kernel(ConvArgs a, int parts, int runs) {
+// (Two CTAs per SM: 203 -> 140 us at 8 x 16 x 4096 x 128; runs of 64 tokens instead of 32: 138.)
+template <typename TIO, int W, bool PACKED>
+__global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArgs a, int parts, int runs) {
   using V = Vec<TIO, 4>;
   constexpr int AHEAD = 4, N = 4 * (W + 1);
   extern __shared__ float sm[];
@@ -216,69 +240,108 @@ __global__ void __launch_bounds__(kBlock) mesa_causal_conv_bwd_kernel(ConvArgs a
       const size_t base = (size_t)u * a.T * a.d + c0;
       const TIO *src = static_cast<const TIO *>(a.x) + base, *dout = static_cast<const TIO *>(a.dout) + base;
       TIO *dx = static_cast<TIO *>(a.dx) + base;
-      const uint8_t *starts = a.starts ? a.starts + (size_t)b * a.T : nullptr;
+      const uint8_t *starts = PACKED ? a.starts + (size_t)b * a.T : nullptr;
       u64 x[W][2], pend[W][2] = {};  // pend[s]: what the tokens so far give dx_{t-s}
-      int age = load_window<TIO, 4, W>(a, u, t0, c0, x);  // tokens before t of its document, W - 1 at most
-      for (int t = t0; t < t1 + W - 1; t += AHEAD) {
-        typename V::Raw rx[AHEAD], rg[AHEAD];
-        bool cut[AHEAD];
+      int age;  // tokens before t of its document, W - 1 at most
+      struct Token {
+        typename V::Raw x, g;
+        bool cut;
+      };
+      auto load = [&](int t, Token &in) {
+        in.x = *reinterpret_cast<const typename V::Raw *>(src + (size_t)t * a.d);
+        in.g = *reinterpret_cast<const typename V::Raw *>(dout + (size_t)t * a.d);
+        if (PACKED) in.cut = starts[t];
+      };
+      // Token t: dx of token t - (W - 1) is complete (EMIT: it is the run's own); MINE: so is t.
+      auto token = [&](int t, const Token &in, auto mine, auto emit) {
+        if (PACKED && in.cut) {
+          age = 0;
 #pragma unroll
-        for (int j = 0; j < AHEAD; j++)
-          if (t + j < a.T && t + j < t1 + W - 1) {
-            rx[j] = *reinterpret_cast<const typename V::Raw *>(src + (size_t)(t + j) * a.d);
-            rg[j] = *reinterpret_cast<const typename V::Raw *>(dout + (size_t)(t + j) * a.d);
-            cut[j] = starts && starts[t + j];
-          }
-#pragma unroll
-        for (int j = 0; j < AHEAD; j++) {
-          const int tt = t + j;
-          if (tt >= t1 + W - 1) break;
-          u64 dy[2] = {0, 0};
-          if (tt < a.T) {
-            if (cut[j]) {
-              age = 0;
-#pragma unroll
-              for (int s = 1; s < W; s++) x[s][0] = x[s][1] = 0;
-            }
-            V::unpack(rx[j], x[0]);
-            V::unpack(rg[j], dy);
-            if (a.silu) {
-#pragma unroll
-              for (int p = 0; p < 2; p++) {
-                u64 y = fma2(w[0][p], x[0][p], bias[p]);
-#pragma unroll
-                for (int s = 1; s < W; s++) y = fma2(w[s][p], x[s][p], y);
-                float y0, y1;
-                unpack2(y, y0, y1);
-                const float s0 = fast_sigmoid(y0), s1 = fast_sigmoid(y1);
-                dy[p] = mul2(dy[p], pack2(s0 * fmaf(y0, 1.0f - s0, 1.0f), s1 * fmaf(y1, 1.0f - s1, 1.0f)));
-              }
-            }
-            if (tt < t1) {
-#pragma unroll
-              for (int p = 0; p < 2; p++) {
-                db[p] = add2(db[p], dy[p]);
-#pragma unroll
-                for (int s = 0; s < W; s++) dw[s][p] = fma2(dy[p], x[s][p], dw[s][p]);
-              }
-            }
-          }
+          for (int s = 1; s < W; s++) x[s][0] = x[s][1] = 0;
+        }
+        u64 dy[2];
+        V::unpack(in.x, x[0]);
+        V::unpack(in.g, dy);
+        if (a.silu) {
 #pragma unroll
           for (int p = 0; p < 2; p++) {
+            u64 y = fma2(w[0][p], x[0][p], bias[p]);
 #pragma unroll
-            for (int s = W - 1; s > 0; s--) {
-              const u64 add = starts && age < s ? pack2(0.0f, 0.0f) : dy[p];
-              pend[s][p] = fma2(w[s][p], add, pend[s - 1][p]);
-            }
-            pend[0][p] = mul2(w[0][p], dy[p]);
+            for (int s = 1; s < W; s++) y = fma2(w[s][p], x[s][p], y);
+            const u64 one = pack2(1.0f, 1.0f), g = sigmoid2(y);  // silu' = g (1 + y (1 - g))
+            dy[p] = mul2(dy[p], mul2(g, fma2(y, sub2(one, g), one)));
           }
-          const int done = tt - (W - 1);
-          if (done >= t0 && done < t1) *reinterpret_cast<typename V::Raw *>(dx + (size_t)done * a.d) = V::pack(pend[W - 1]);
-          age = min(age + 1, W - 1);
-#pragma unroll
-          for (int s = W - 1; s > 0; s--) x[s][0] = x[s - 1][0], x[s][1] = x[s - 1][1];
         }
+        if constexpr (decltype(mine)::value) {
+#pragma unroll
+          for (int p = 0; p < 2; p++) {
+            db[p] = add2(db[p], dy[p]);
+#pragma unroll
+            for (int s = 0; s < W; s++) dw[s][p] = fma2(dy[p], x[s][p], dw[s][p]);
+          }
+        }
+        if (!PACKED || age >= W - 1) {
+#pragma unroll
+          for (int p = 0; p < 2; p++)
+#pragma unroll
+            for (int s = W - 1; s > 0; s--) pend[s][p] = fma2(w[s][p], dy[p], pend[s - 1][p]);
+        } else {  // a document's first tokens: nothing of theirs reaches the one before
+#pragma unroll
+          for (int p = 0; p < 2; p++)
+#pragma unroll
+            for (int s = W - 1; s > 0; s--) pend[s][p] = age < s ? pend[s - 1][p] : fma2(w[s][p], dy[p], pend[s - 1][p]);
+        }
+#pragma unroll
+        for (int p = 0; p < 2; p++) pend[0][p] = mul2(w[0][p], dy[p]);
+        if constexpr (decltype(emit)::value)
+          *reinterpret_cast<typename V::Raw *>(dx + (size_t)(t - (W - 1)) * a.d) = V::pack(pend[W - 1]);
+        if (PACKED) age = min(age + 1, W - 1);
+#pragma unroll
+        for (int s = W - 1; s > 0; s--) x[s][0] = x[s - 1][0], x[s][1] = x[s - 1][1];
+      };
+      constexpr std::true_type yes{};
+      constexpr std::false_type no{};
+      Token in[2][AHEAD];
+      int t = t0;
+      age = load_window<TIO, 4, W>(a, u, t0, c0, x);
+      const int lead = min(t0 + W - 1, t1);
+#pragma unroll 1
+      for (; t < lead; t++) {  // nothing of the run's own is complete yet
+        load(t, in[0][0]);
+        token(t, in[0][0], yes, no);
       }
+      if (t + 2 * AHEAD <= t1) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; j++) load(t + j, in[0][j]);
+#pragma unroll 1
+        for (; t + 3 * AHEAD <= t1; t += 2 * AHEAD) {  // (the next tokens are on their way)
+#pragma unroll
+          for (int j = 0; j < AHEAD; j++) load(t + AHEAD + j, in[1][j]);
+#pragma unroll
+          for (int j = 0; j < AHEAD; j++) token(t + j, in[0][j], yes, yes);
+#pragma unroll
+          for (int j = 0; j < AHEAD; j++) load(t + 2 * AHEAD + j, in[0][j]);
+#pragma unroll
+          for (int j = 0; j < AHEAD; j++) token(t + AHEAD + j, in[1][j], yes, yes);
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; j++) token(t + j, in[0][j], yes, yes);
+        t += AHEAD;
+      }
+#pragma unroll 1
+      for (; t < t1; t++) {
+        load(t, in[0][0]);
+        token(t, in[0][0], yes, yes);
+      }
+#pragma unroll 1
+      for (; t < t1 + W - 1 && t < a.T; t++) {  // the next run's first tokens
+        load(t, in[0][0]);
+        token(t, in[0][0], no, yes);
+      }
+#pragma unroll
+      for (int s = W - 1; s >= 1; s--)  // the sequence's end (t = T): token t - s's sum is in pend[s - 1]
+        if (t < t1 + W - 1 && t - s >= t0 && t - s < t1)
+          *reinterpret_cast<typename V::Raw *>(dx + (size_t)(t - s) * a.d) = V::pack(pend[s - 1]);
     }
   }
   if (!a.partial) return;
@@ -339,16 +402,19 @@ int done() { return cudaPeekAtLastError() == cudaSuccess ? 0 : -1; }
 
 template <typename TIO, int VEC>
 int forward(const ConvArgs &a, cudaStream_t st) {
-  // runs of 32 tokens (W - 1 are read twice), shorter ones where that leaves SMs idle
+  // runs of 64 tokens (W - 1 are read twice), shorter ones where that leaves SMs idle
   const size_t lanes = (size_t)a.B * a.H * (a.d / VEC);
-  int run = 32;
+  int run = 64;
   while (run > 8 && lanes * ((a.T + run - 1) / run) < 152 * 1024) run /= 2;
   const int runs = (a.T + run - 1) / run;
-  const size_t blocks = (lanes * runs + kBlock - 1) / kBlock;
+  const size_t blocks = (lanes * runs + kFwdBlock - 1) / kFwdBlock;
   if (blocks > 0x7fffffff) return -1;
   return by_width(a.W, [&](auto w) {
     timing_mark_begin(K_CONV, st);
-    mesa_causal_conv_kernel<TIO, VEC, decltype(w)::value><<<(unsigned)blocks, kBlock, 0, st>>>(a, run, runs);
+    if (a.starts)
+      mesa_causal_conv_kernel<TIO, VEC, decltype(w)::value, true><<<(unsigned)blocks, kFwdBlock, 0, st>>>(a, run, runs);
+    else
+      mesa_causal_conv_kernel<TIO, VEC, decltype(w)::value, false><<<(unsigned)blocks, kFwdBlock, 0, st>>>(a, run, runs);
     timing_mark_end(K_CONV, st);
     return done();
   });
@@ -361,7 +427,11 @@ int backward(const ConvArgs &a, cudaStream_t st) {
     constexpr int W = decltype(w)::value;
     const size_t smem = a.partial ? (size_t)(kBlock / gx) * gx * 4 * (W + 1) * sizeof(float) : 0;
     timing_mark_begin(K_CONV_BWD, st);
-    mesa_causal_conv_bwd_kernel<TIO, W><<<dim3(parts, (a.d / 4 + gx - 1) / gx, a.H), kBlock, smem, st>>>(a, parts, runs);
+    const dim3 grid(parts, (a.d / 4 + gx - 1) / gx, a.H);
+    if (a.starts)
+      mesa_causal_conv_bwd_kernel<TIO, W, true><<<grid, kBlock, smem, st>>>(a, parts, runs);
+    else
+      mesa_causal_conv_bwd_kernel<TIO, W, false><<<grid, kBlock, smem, st>>>(a, parts, runs);
     timing_mark_end(K_CONV_BWD, st);
     if (a.partial) {
       timing_mark_begin(K_CONV_COLS, st);
@@ -386,17 +456,18 @@ int step(const ConvArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Six CTAs for each of a GB300's 152 SMs over all heads and channels, no more than there are runs.
+// Two CTAs for each of a GB300's 152 SMs (what their registers allow at once) over all heads and channels, no more than
+// there are runs.  (us of 8 x 16 x 4096 x 128: two 166, three 221, four 189, six 192)
 int conv_bwd_parts(int B, int H, int T, int d) {
   const int gx = bwd_gx(d), rows = kBlock / gx, slabs = (d / 4 + gx - 1) / gx;
   const size_t pairs = (size_t)B * ((T + kBwdRun - 1) / kBwdRun), most = (pairs + rows - 1) / rows;
-  size_t n = (152 * 6 + (size_t)H * slabs - 1) / ((size_t)H * slabs);
+  size_t n = 152 * 2 / ((size_t)H * slabs);
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
 
 int launch_causal_conv(const ConvArgs &a, cudaStream_t st) {
-  return a.dtype == 1 ? forward<__nv_bfloat16, 8>(a, st) : forward<float, 4>(a, st);
+  return a.dtype == 1 ? forward<__nv_bfloat16, 4>(a, st) : forward<float, 4>(a, st);
 }
 int launch_causal_conv_step(const ConvArgs &a, cudaStream_t st) {
   return a.dtype == 1 ? step<__nv_bfloat16>(a, st) : step<float>(a, st);

@@ -124,79 +124,85 @@ __device__ __forceinline__ void pairs_of(const RotaryArgs &a, const TIO *row, ui
     }
   }
 }
-__device__ __forceinline__ float lanes_sum(float x, int L) {
-  for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+// The channel that c turns with.
+template <int PAIRS>
+__device__ __forceinline__ int pair_of(const RotaryArgs &a, int c) {
+  if constexpr (PAIRS == kNeighbours) return c ^ 1;
+  return c < a.R / 2 ? c + a.R / 2 : c < a.R ? c - a.R / 2 : c;
 }
 
 // L lanes a token, grid.y groups of `heads` heads (the query heads, then the key heads).  The lanes past the last
 // token work on it and write nothing.  Outputs may replace inputs: a warp reads its rows before it writes.
-template <typename TIO, int PAIRS>
+template <typename TIO, int D, int PAIRS>
 __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_kernel(RotaryArgs a, int heads) {
   using R = Row<TIO>;
-  constexpr int VEC = R::VEC, BATCH = 4;
-  const int L = a.d / VEC, c0 = (threadIdx.x % L) * VEC;
+  constexpr int VEC = R::VEC, BATCH = 4, L = D / VEC;
+  const int c0 = (threadIdx.x % L) * VEC;
   const size_t tokens = (size_t)a.B * a.T, mine = ((size_t)blockIdx.x * kBlock + threadIdx.x) / L;
   const bool in = mine < tokens;
   const size_t token = in ? mine : tokens - 1, b = token / a.T, t = token % a.T;
   float C[VEC], S[VEC];
   token_angles<VEC, PAIRS>(a, token, c0, C, S);
-  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, a.H + a.Hk);
-  for (int h = h0; h < h1; h += BATCH) {
-    uint4 raw[BATCH];
-    float p[BATCH][VEC];
-    const TIO *row[BATCH];
-    TIO *out[BATCH];
+  const int first = blockIdx.y * heads, last = min(first + heads, a.H + a.Hk);
 #pragma unroll
-    for (int i = 0; i < BATCH; i++) {
-      const int hh = min(h + i, h1 - 1);
-      const bool isq = hh < a.H;
-      const size_t at = ((b * (isq ? a.H : a.Hk) + (isq ? hh : hh - a.H)) * a.T + t) * a.d;
-      row[i] = static_cast<const TIO *>(isq ? a.q : a.k) + at;
-      out[i] = static_cast<TIO *>(isq ? a.q_out : a.k_out) + at;
-      raw[i] = *reinterpret_cast<const uint4 *>(row[i] + c0);
+  for (int which = 0; which < 2; which++) {
+    const int H = which == 0 ? a.H : a.Hk, h0 = which == 0 ? first : max(first - a.H, 0), h1 = which == 0 ? min(last, H) : last - a.H;
+    const TIO *src = static_cast<const TIO *>(which == 0 ? a.q : a.k);
+    TIO *dst = static_cast<TIO *>(which == 0 ? a.q_out : a.k_out);
+    const float *w = which == 0 ? a.wq : a.wk;
+    float cw[VEC], sw[VEC];  // C and S times the weights
+#pragma unroll
+    for (int j = 0; j < VEC; j++) {
+      cw[j] = w ? C[j] * w[c0 + j] : C[j];
+      sw[j] = w && PAIRS != kNone ? S[j] * w[pair_of<PAIRS>(a, c0 + j)] : S[j];
     }
+#pragma unroll 1
+    for (int h = h0; h < h1; h += BATCH) {
+      uint4 raw[BATCH];
+      float p[BATCH][VEC];
+      size_t at[BATCH];
 #pragma unroll
-    for (int i = 0; i < BATCH; i++)
-      if constexpr (PAIRS != kNone) pairs_of<TIO, PAIRS>(a, row[i], raw[i], c0, p[i]);
-    __syncwarp();
+      for (int i = 0; i < BATCH; i++) {
+        at[i] = ((b * H + min(h + i, h1 - 1)) * a.T + t) * D;
+        raw[i] = *reinterpret_cast<const uint4 *>(src + at[i] + c0);
+      }
 #pragma unroll
-    for (int i = 0; i < BATCH; i++) {
-      float x[VEC];
-      R::unpack(raw[i], x);
-      float r = 1.0f;
-      const float *w = nullptr;
+      for (int i = 0; i < BATCH; i++)
+        if constexpr (PAIRS != kNone) pairs_of<TIO, PAIRS>(a, src + at[i], raw[i], c0, p[i]);
+      __syncwarp();
+      float r[BATCH];
       if (a.norm) {
-        float ss = 0.0f;
 #pragma unroll
-        for (int j = 0; j < VEC; j++) ss = fmaf(x[j], x[j], ss);
-        r = rsqrtf(lanes_sum(ss, L) / a.d + a.eps);
-        w = h + i < a.H ? a.wq : a.wk;
-      }
+        for (int i = 0; i < BATCH; i++) {
+          float x[VEC];
+          R::unpack(raw[i], x);
+          r[i] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < VEC; j++) {
-        const int c = c0 + j;
-        float n = x[j] * r, m = 0.0f;
-        if constexpr (PAIRS != kNone) m = p[i][j] * r;
-        if (w) {
-          n *= w[c];
-          if constexpr (PAIRS == kNeighbours) m *= w[c ^ 1];
-          if constexpr (PAIRS >= kHalves) m *= w[c < a.R / 2 ? c + a.R / 2 : c < a.R ? c - a.R / 2 : c];
+          for (int j = 0; j < VEC; j++) r[i] = fmaf(x[j], x[j], r[i]);
         }
-        x[j] = PAIRS == kNone ? n : fmaf(m, S[j], n * C[j]);
+#pragma unroll
+        for (int i = 0; i < BATCH; i++) r[i] = rsqrtf(fmaf(group_sum<L>(r[i]), 1.0f / D, a.eps));
       }
-      if (in && h + i < h1) *reinterpret_cast<uint4 *>(out[i] + c0) = R::pack(x);
+#pragma unroll
+      for (int i = 0; i < BATCH; i++) {
+        float x[VEC];
+        R::unpack(raw[i], x);
+        const float f = a.norm ? r[i] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < VEC; j++) x[j] = f * (PAIRS == kNone ? x[j] * cw[j] : fmaf(p[i][j], sw[j], x[j] * cw[j]));
+        if (in && h + i < h1) *reinterpret_cast<uint4 *>(dst + at[i] + c0) = R::pack(x);
+      }
     }
   }
 }
 
 // A resident grid walks over the tokens; sums of the weights' gradients stay in registers until the end.
-template <typename TIO, int PAIRS>
+template <typename TIO, int D, int PAIRS>
 __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_bwd_kernel(RotaryArgs a) {
   using R = Row<TIO>;
-  constexpr int VEC = R::VEC, BATCH = 2;
+  constexpr int VEC = R::VEC, BATCH = 2, L = D / VEC, per = kBlock / L;
   __shared__ float sums[kBlock][VEC + 1];
-  const int L = a.d / VEC, c0 = (threadIdx.x % L) * VEC, per = kBlock / L;
+  const int c0 = (threadIdx.x % L) * VEC;
   const size_t tokens = (size_t)a.B * a.T;
   float dw[2][VEC] = {};
   for (size_t first = (size_t)blockIdx.x * per; first < tokens; first += (size_t)gridDim.x * per) {
@@ -211,13 +217,17 @@ __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_bwd_kernel(RotaryA
       const TIO *xs = static_cast<const TIO *>(which == 0 ? a.q : a.k), *gs = static_cast<const TIO *>(which == 0 ? a.dq_out : a.dk_out);
       TIO *ds = static_cast<TIO *>(which == 0 ? a.q_out : a.k_out);
       const float *w = which == 0 ? a.wq : a.wk;
+      float wc[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; j++) wc[j] = w ? w[c0 + j] : 1.0f;
+#pragma unroll 1
       for (int h = 0; h < H; h += BATCH) {
         uint4 xr[BATCH], gr[BATCH];
         float p[BATCH][VEC];
         size_t at[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; i++) {
-          at[i] = ((b * H + min(h + i, H - 1)) * a.T + t) * a.d;
+          at[i] = ((b * H + min(h + i, H - 1)) * a.T + t) * D;
           gr[i] = *reinterpret_cast<const uint4 *>(gs + at[i] + c0);
           if (a.norm) xr[i] = *reinterpret_cast<const uint4 *>(xs + at[i] + c0);
         }
@@ -240,14 +250,15 @@ __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_bwd_kernel(RotaryA
 #pragma unroll
             for (int j = 0; j < VEC; j++) {
               ss = fmaf(x[j], x[j], ss);
-              mx = fmaf(w ? g[j] * w[c0 + j] : g[j], x[j], mx);
+              mx = fmaf(g[j] * wc[j], x[j], mx);
             }
-            const float r = rsqrtf(lanes_sum(ss, L) / a.d + a.eps), mean = lanes_sum(mx, L) * r / a.d;
+            ss = group_sum<L>(ss);
+            mx = group_sum<L>(mx);
+            const float r = rsqrtf(fmaf(ss, 1.0f / D, a.eps)), mean = mx * r * (1.0f / D), rr = on ? r : 0.0f;
 #pragma unroll
             for (int j = 0; j < VEC; j++) {
-              const float xn = x[j] * r;
-              if (on) dw[which][j] = fmaf(g[j], xn, dw[which][j]);
-              g[j] = r * ((w ? g[j] * w[c0 + j] : g[j]) - xn * mean);
+              dw[which][j] = fmaf(g[j] * rr, x[j], dw[which][j]);
+              g[j] = r * fmaf(-(x[j] * r), mean, g[j] * wc[j]);
             }
           }
           if (on) *reinterpret_cast<uint4 *>(ds + at[i] + c0) = R::pack(g);
@@ -262,10 +273,10 @@ __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_bwd_kernel(RotaryA
 #pragma unroll
     for (int j = 0; j < VEC; j++) sums[threadIdx.x][j] = dw[which][j];
     __syncthreads();
-    for (int c = threadIdx.x; c < a.d; c += kBlock) {
+    for (int c = threadIdx.x; c < D; c += kBlock) {
       float x = 0.0f;
       for (int r = 0; r < per; r++) x += sums[r * L + c / VEC][c % VEC];
-      a.partial[((size_t)blockIdx.x * 2 + which) * a.d + c] = x;
+      a.partial[((size_t)blockIdx.x * 2 + which) * D + c] = x;
     }
   }
 }
@@ -285,13 +296,22 @@ int pairs_kind(const RotaryArgs &a) {
   const int vec = a.dtype == 1 ? 8 : 4;
   return a.R == 0 ? kNone : a.interleaved ? kNeighbours : a.R / 2 % vec == 0 ? kHalves : kAnyHalves;
 }
+// f(channels, kind of pairs)
 template <typename F>
-int by_pairs(int kind, F f) {
-  switch (kind) {
-    case kNone: return f(std::integral_constant<int, kNone>());
-    case kNeighbours: return f(std::integral_constant<int, kNeighbours>());
-    case kHalves: return f(std::integral_constant<int, kHalves>());
-    default: return f(std::integral_constant<int, kAnyHalves>());
+int by_pairs(const RotaryArgs &a, F f) {
+  auto d = [&](auto pairs) {
+    switch (a.d) {
+      case 16: return f(std::integral_constant<int, 16>(), pairs);
+      case 32: return f(std::integral_constant<int, 32>(), pairs);
+      case 64: return f(std::integral_constant<int, 64>(), pairs);
+      default: return f(std::integral_constant<int, 128>(), pairs);
+    }
+  };
+  switch (pairs_kind(a)) {
+    case kNone: return d(std::integral_constant<int, kNone>());
+    case kNeighbours: return d(std::integral_constant<int, kNeighbours>());
+    case kHalves: return d(std::integral_constant<int, kHalves>());
+    default: return d(std::integral_constant<int, kAnyHalves>());
   }
 }
 int done() { return cudaPeekAtLastError() == cudaSuccess ? 0 : -1; }
@@ -304,9 +324,9 @@ int forward(const RotaryArgs &a, cudaStream_t st) {
   int heads = a.H + a.Hk;
   while (heads > 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 16) heads = (heads + 1) / 2;
   if (heads <= 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 4) heads = 1;
-  return by_pairs(pairs_kind(a), [&](auto p) {
+  return by_pairs(a, [&](auto d, auto p) {
     timing_mark_begin(K_ROTARY, st);
-    mesa_qk_norm_rotary_kernel<TIO, decltype(p)::value>
+    mesa_qk_norm_rotary_kernel<TIO, decltype(d)::value, decltype(p)::value>
         <<<dim3((unsigned)blocks, (a.H + a.Hk + heads - 1) / heads), kBlock, 0, st>>>(a, heads);
     timing_mark_end(K_ROTARY, st);
     return done();
@@ -315,9 +335,9 @@ int forward(const RotaryArgs &a, cudaStream_t st) {
 template <typename TIO>
 int backward(const RotaryArgs &a, cudaStream_t st) {
   const int parts = rotary_bwd_parts(a.B, a.H, a.Hk, a.T, a.d);
-  return by_pairs(pairs_kind(a), [&](auto p) {
+  return by_pairs(a, [&](auto d, auto p) {
     timing_mark_begin(K_ROTARY_BWD, st);
-    mesa_qk_norm_rotary_bwd_kernel<TIO, decltype(p)::value><<<parts, kBlock, 0, st>>>(a);
+    mesa_qk_norm_rotary_bwd_kernel<TIO, decltype(d)::value, decltype(p)::value><<<parts, kBlock, 0, st>>>(a);
     timing_mark_end(K_ROTARY_BWD, st);
     if (a.partial) {
       timing_mark_begin(K_ROTARY_COLS, st);
