@@ -19,7 +19,7 @@ namespace mesa {
 
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 256, kFwdBlock = 128;
 enum Pairs { kNone = 0, kNeighbours = 1, kHalves = 2, kAnyHalves = 3 };  // kHalves: R/2 a multiple of a lane's channels
 
 template <typename TIO>
@@ -133,12 +133,14 @@ __device__ __forceinline__ int pair_of(const RotaryArgs &a, int c) {
 
 // L lanes a token, grid.y groups of `heads` heads (the query heads, then the key heads).  The lanes past the last
 // token work on it and write nothing.  Outputs may replace inputs: a warp reads its rows before it writes.
+// (Four rows in flight a lane, eight CTAs of 128 threads per SM.  us of 8 x (16 + 16) x 4096 x 128, pairs of halves /
+// neighbours: CTAs of 256 threads without a bound of registers 127 / 96, with it 109 / 90; so, 105 / 88.)
 template <typename TIO, int D, int PAIRS>
-__global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_kernel(RotaryArgs a, int heads) {
+__global__ void __launch_bounds__(kFwdBlock, 8) mesa_qk_norm_rotary_kernel(RotaryArgs a, int heads) {
   using R = Row<TIO>;
   constexpr int VEC = R::VEC, BATCH = 4, L = D / VEC;
   const int c0 = (threadIdx.x % L) * VEC;
-  const size_t tokens = (size_t)a.B * a.T, mine = ((size_t)blockIdx.x * kBlock + threadIdx.x) / L;
+  const size_t tokens = (size_t)a.B * a.T, mine = ((size_t)blockIdx.x * kFwdBlock + threadIdx.x) / L;
   const bool in = mine < tokens;
   const size_t token = in ? mine : tokens - 1, b = token / a.T, t = token % a.T;
   float C[VEC], S[VEC];
@@ -159,17 +161,15 @@ __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_kernel(RotaryArgs 
 #pragma unroll 1
     for (int h = h0; h < h1; h += BATCH) {
       uint4 raw[BATCH];
-      float p[BATCH][VEC];
+      float far[PAIRS == kAnyHalves ? BATCH : 1][VEC];
       size_t at[BATCH];
 #pragma unroll
       for (int i = 0; i < BATCH; i++) {
         at[i] = ((b * H + min(h + i, h1 - 1)) * a.T + t) * D;
         raw[i] = *reinterpret_cast<const uint4 *>(src + at[i] + c0);
+        if constexpr (PAIRS == kAnyHalves) pairs_of<TIO, PAIRS>(a, src + at[i], raw[i], c0, far[i]);
       }
-#pragma unroll
-      for (int i = 0; i < BATCH; i++)
-        if constexpr (PAIRS != kNone) pairs_of<TIO, PAIRS>(a, src + at[i], raw[i], c0, p[i]);
-      __syncwarp();
+      if constexpr (PAIRS == kAnyHalves) __syncwarp();  // (the row is read: it may be written)
       float r[BATCH];
       if (a.norm) {
 #pragma unroll
@@ -185,22 +185,25 @@ __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_kernel(RotaryArgs 
       }
 #pragma unroll
       for (int i = 0; i < BATCH; i++) {
-        float x[VEC];
+        float x[VEC], p[VEC];
         R::unpack(raw[i], x);
+        if constexpr (PAIRS == kNeighbours || PAIRS == kHalves) pairs_of<TIO, PAIRS>(a, src, raw[i], c0, p);
         const float f = a.norm ? r[i] : 1.0f;
 #pragma unroll
-        for (int j = 0; j < VEC; j++) x[j] = f * (PAIRS == kNone ? x[j] * cw[j] : fmaf(p[i][j], sw[j], x[j] * cw[j]));
+        for (int j = 0; j < VEC; j++)
+          x[j] = f * (PAIRS == kNone ? x[j] * cw[j] : fmaf(PAIRS == kAnyHalves ? far[PAIRS == kAnyHalves ? i : 0][j] : p[j], sw[j], x[j] * cw[j]));
         if (in && h + i < h1) *reinterpret_cast<uint4 *>(dst + at[i] + c0) = R::pack(x);
       }
     }
   }
 }
 
+// (Four rows in flight a lane, two CTAs per SM: 166 / 152 us, halves / neighbours; two rows and four CTAs 185 / 188.)
 // A resident grid walks over the tokens; sums of the weights' gradients stay in registers until the end.
 template <typename TIO, int D, int PAIRS>
-__global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_bwd_kernel(RotaryArgs a) {
+__global__ void __launch_bounds__(kBlock, 2) mesa_qk_norm_rotary_bwd_kernel(RotaryArgs a) {
   using R = Row<TIO>;
-  constexpr int VEC = R::VEC, BATCH = 2, L = D / VEC, per = kBlock / L;
+  constexpr int VEC = R::VEC, BATCH = 4, L = D / VEC, per = kBlock / L;
   __shared__ float sums[kBlock][VEC + 1];
   const int c0 = (threadIdx.x % L) * VEC;
   const size_t tokens = (size_t)a.B * a.T;
@@ -223,26 +226,26 @@ __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_bwd_kernel(RotaryA
 #pragma unroll 1
       for (int h = 0; h < H; h += BATCH) {
         uint4 xr[BATCH], gr[BATCH];
-        float p[BATCH][VEC];
+        float far[PAIRS == kAnyHalves ? BATCH : 1][VEC];
         size_t at[BATCH];
 #pragma unroll
         for (int i = 0; i < BATCH; i++) {
           at[i] = ((b * H + min(h + i, H - 1)) * a.T + t) * D;
           gr[i] = *reinterpret_cast<const uint4 *>(gs + at[i] + c0);
           if (a.norm) xr[i] = *reinterpret_cast<const uint4 *>(xs + at[i] + c0);
+          if constexpr (PAIRS == kAnyHalves) pairs_of<TIO, PAIRS>(a, gs + at[i], gr[i], c0, far[i]);
         }
-#pragma unroll
-        for (int i = 0; i < BATCH; i++)
-          if constexpr (PAIRS != kNone) pairs_of<TIO, PAIRS>(a, gs + at[i], gr[i], c0, p[i]);
-        __syncwarp();
+        if constexpr (PAIRS == kAnyHalves) __syncwarp();  // (the row is read: it may be written)
 #pragma unroll
         for (int i = 0; i < BATCH; i++) {
           const bool on = in && h + i < H;
           float g[VEC];
           R::unpack(gr[i], g);
           if constexpr (PAIRS != kNone) {
+            float p[VEC];
+            if constexpr (PAIRS != kAnyHalves) pairs_of<TIO, PAIRS>(a, gs, gr[i], c0, p);
 #pragma unroll
-            for (int j = 0; j < VEC; j++) g[j] = fmaf(-p[i][j], S[j], g[j] * C[j]);
+            for (int j = 0; j < VEC; j++) g[j] = fmaf(PAIRS == kAnyHalves ? -far[PAIRS == kAnyHalves ? i : 0][j] : -p[j], S[j], g[j] * C[j]);
           }
           if (a.norm) {
             float x[VEC], ss = 0.0f, mx = 0.0f;
@@ -318,16 +321,16 @@ int done() { return cudaPeekAtLastError() == cudaSuccess ? 0 : -1; }
 
 template <typename TIO>
 int forward(const RotaryArgs &a, cudaStream_t st) {
-  const size_t blocks = ((size_t)a.B * a.T * (a.d / Row<TIO>::VEC) + kBlock - 1) / kBlock;
+  const size_t blocks = ((size_t)a.B * a.T * (a.d / Row<TIO>::VEC) + kFwdBlock - 1) / kFwdBlock;
   if (blocks > 0x7fffffff) return -1;
   // all heads of a token in one thread where that fills the SMs twice, else fewer
   int heads = a.H + a.Hk;
-  while (heads > 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 16) heads = (heads + 1) / 2;
-  if (heads <= 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 4) heads = 1;
+  while (heads > 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 32) heads = (heads + 1) / 2;
+  if (heads <= 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 8) heads = 1;
   return by_pairs(a, [&](auto d, auto p) {
     timing_mark_begin(K_ROTARY, st);
     mesa_qk_norm_rotary_kernel<TIO, decltype(d)::value, decltype(p)::value>
-        <<<dim3((unsigned)blocks, (a.H + a.Hk + heads - 1) / heads), kBlock, 0, st>>>(a, heads);
+        <<<dim3((unsigned)blocks, (a.H + a.Hk + heads - 1) / heads), kFwdBlock, 0, st>>>(a, heads);
     timing_mark_end(K_ROTARY, st);
     return done();
   });
@@ -350,10 +353,10 @@ int backward(const RotaryArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Four CTAs for each of a GB300's 152 SMs, no more than there are tokens for (16 a CTA at d = 128).
+// Two CTAs for each of a GB300's 152 SMs, no more than there are tokens for (16 a CTA at d = 128).
 int rotary_bwd_parts(int B, int, int, int T, int d) {
   const size_t n = ((size_t)B * T * (d / 4) + kBlock - 1) / kBlock;
-  return n < 1 ? 1 : n < 152 * 4 ? (int)n : 152 * 4;
+  return n < 1 ? 1 : n < 152 * 2 ? (int)n : 152 * 2;
 }
 
 int launch_qk_norm_rotary(const RotaryArgs &a, cudaStream_t st) {
