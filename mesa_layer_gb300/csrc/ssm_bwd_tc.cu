@@ -26,7 +26,7 @@ struct Grad {
                             W = P == 128 ? S : S + V_TILE<P>, M = W + QK_TILE, MISC = M + QK_TILE;
 };
 struct GradMisc {
-  alignas(16) float rec[REC];  // the chunk's gates
+  alignas(16) float rec[REC];  // the chunk's gates; once every block is done, by rows' warp and token: its rows' sum of X / D
   float frob[2][16];
   float scan[2][4];
   uint64_t full1, full2, c1, c2, e, fg, h, a_done, b_done, c_done, f_done, qk_staged, v_staged, drain;
@@ -40,8 +40,6 @@ static_assert(kGradSmem<128> <= 232448, "shared memory per block");
 constexpr uint32_t T_A = 0, T_B = 128, T_DQ = 256, T_DK = 384;
 constexpr int X_ROW = 0, X_IN = 4, X_OUT = 8, X_GV = 12, X_DIAG = 13;
 
-// (By rows' warp and token: the sum over its rows of X / D, in V's place once the products have read V.)
-__device__ __forceinline__ float *columns(uint8_t *v) { return reinterpret_cast<float *>(v); }
 __device__ __forceinline__ void tmem_put(uint32_t taddr, float x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
 }
@@ -115,13 +113,56 @@ __global__ void __launch_bounds__(576, 1)
     const int w = warp & 3, b = warp >> 2, t = 32 * w + lane;  // row t, columns of quarter b
     const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
     uint32_t bad = 0;
+    // What the steps' gradients of a chunk need (warps 0-3, token t).  They are put together while the next chunk's products run.
+    struct Steps {
+      float xi, moved, duv, gv, across, raw, step;
+      int at, start;
+    } last;
+    last.at = -1;
+    auto steps = [&]() {
+      const int u = last.at / NC, c = last.at - u * NC, h = u % a.H;
+      const bool in = c * L + t < a.T;
+      float suf = last.xi, pre = last.moved;  // readers from t on, writers before t (with the pairs)
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float p = __shfl_down_sync(0xffffffffu, suf, o), q = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane + o < 32) suf += p;
+        if (lane >= o) pre += q;
+      }
+      if (lane == 0) m->scan[0][w] = suf;
+      if (lane == 31) m->scan[1][w] = pre;
+      group_or(2, 128, false);
+      pre -= last.moved;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if (i > w) suf += m->scan[0][i];
+        if (i < w) pre += m->scan[1][i];
+      }
+      const float da = last.start == t ? 0.0f : pre + suf + last.across;
+      const float dd = in ? fmaf(a.A[h], da, last.duv) * sigmoid(last.raw) : 0.0f;
+      if (in) {
+        if (!isfinite(dd)) bad = 0x7f80u;
+        const size_t i = (size_t)u * a.T + c * L + t;
+        if (a.gates_f32)
+          static_cast<float *>(a.ddt)[i] = dd;
+        else
+          static_cast<__nv_bfloat16 *>(a.ddt)[i] = __float2bfloat16_rn(dd);
+      }
+      const float sA = warp_sum(in ? last.step * da : 0.0f), sb = warp_sum(dd), sg = warp_sum(last.gv);
+      if (lane == 0) {  // a warp's tokens each
+        const size_t n = (size_t)chunks * 4, i = (size_t)last.at * 4 + w;
+        sums[i] = sA;
+        sums[n + i] = sb;
+        sums[2 * n + i] = sg;
+      }
+    };
     for (int at = blockIdx.x, it = 0; at < chunks; at += gridDim.x, it++) {
       const uint32_t par = it & 1;
       const int u = at / NC, c = at - u * NC, h = u % a.H;
       const bool in = c * L + t < a.T;
       const float raw = in ? a.dt[(size_t)u * a.T + c * L + t] + (a.dt_bias ? a.dt_bias[h] : 0.0f) : 0.0f;
       // <S, R>: 8 P bytes a thread of each
-      if (!need(m->full2, par)) break;
+      need(m->full2, par);  // (a warp that gives up goes on to the next barrier with the others)
       const float *r = m->rec;
       const float r_in = r[R_IN + t], step = r[R_STEP + t], f = r_in * r[R_FIRST + w], ct = r[R_OUT + t] * r[R_LAST + w],
                   mine = r[R_LOG + t], across = r[R_ALL];
@@ -144,6 +185,7 @@ __global__ void __launch_bounds__(576, 1)
         break;
       }
       // ---- M', W and the pairs' sums: block (w, b), eight columns at a time ----
+      if (b == 0 && it > 0) steps();
       float row = 0.0f, gv = 0.0f, diag = 0.0f, col = 0.0f;  // col: column 32 b + lane
       need(m->c1, par);
       if (b <= w) {
@@ -221,24 +263,29 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->a_done);
       // ---- f (g S) and c D (V R), with what passes into and out of the chunk ----
       need(m->c2, par);
-      if (b <= w) columns(sm + O::V)[w * L + 32 * b + lane] = col;
       auto scaled = [&](uint32_t col, const uint8_t *tile, float s) {  // returns the row's product with the tile's, unscaled
         const u64 s2 = pack2(s, s);
         u64 dot = 0;
-#pragma unroll 2
-        for (int cc = 0; cc < 4; cc++) {
-          float x[8];
-          tc::tmem_ld8(tl + col + 32 * b + 8 * cc, x);
-          const uint4 q = *reinterpret_cast<const uint4 *>(tile + tile_off(t, 4 * b + cc, L));
-          const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int hh = 0; hh < 2; hh++) {
+          float x[16];
+          tc::tmem_ld16(tl + col + 32 * b + 16 * hh, x);
+          uint4 q[2];
+#pragma unroll
+          for (int k = 0; k < 2; k++) q[k] = *reinterpret_cast<const uint4 *>(tile + tile_off(t, 4 * b + 2 * hh + k, L));
           tc::tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const u64 y = pack2(x[2 * i], x[2 * i + 1]);
-            dot = fma2(y, of_bf2(qs[i]), dot);
-            unpack2(mul2(y, s2), x[2 * i], x[2 * i + 1]);
+          for (int k = 0; k < 2; k++) {
+            const uint32_t qs[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              const int e = 8 * k + 2 * i;
+              const u64 y = pack2(x[e], x[e + 1]);
+              dot = fma2(y, of_bf2(qs[i]), dot);
+              unpack2(mul2(y, s2), x[e], x[e + 1]);
+            }
           }
-          tc::tmem_st8(tl + col + 32 * b + 8 * cc, x);
+          tc::tmem_st16(tl + col + 32 * b + 16 * hh, x);
         }
         return sum2(dot);
       };
@@ -256,6 +303,7 @@ __global__ void __launch_bounds__(576, 1)
 #pragma unroll
         for (int i = 0; i < N; i++) x[i] *= ct;
         tc::tmem_st<N>(tl + T_A + N * b, x);
+        if (b <= w) m->rec[w * L + 32 * b + lane] = col;  // (every block is done: the gates have been read)
         tmem_put(tl + T_B + X_ROW + b, row);
         tmem_put(tl + T_B + X_IN + b, x_in);
         tmem_put(tl + T_B + X_OUT + b, x_out);
@@ -266,26 +314,21 @@ __global__ void __launch_bounds__(576, 1)
       }
       // ---- dQ, dK ----
       need(m->fg, par);
-      float sum = 0.0f;
-      if (b == 0) {  // (all warps' columns are there)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          if (i >= w) sum += columns(sm + O::V)[i * L + t];
-      }
       auto put = [&](uint32_t col, uint8_t *tile, float *part) {
-#pragma unroll 2
+        float x[32];
+        tc::tmem_ld32(tl + col + 32 * b, x);
+        tc::tmem_ld_wait();
+#pragma unroll
         for (int cc = 0; cc < 4; cc++) {
-          float x[8];
-          tc::tmem_ld8(tl + col + 32 * b + 8 * cc, x);
-          tc::tmem_ld_wait();
-          const uint4 o = make_uint4(bf2(x[0], x[1]), bf2(x[2], x[3]), bf2(x[4], x[5]), bf2(x[6], x[7]));
+          const uint4 o = make_uint4(bf2(x[8 * cc], x[8 * cc + 1]), bf2(x[8 * cc + 2], x[8 * cc + 3]), bf2(x[8 * cc + 4], x[8 * cc + 5]),
+                                     bf2(x[8 * cc + 6], x[8 * cc + 7]));
           if (in) bad = rule::absmax_words(bad, o);
           if (!part) {
             *reinterpret_cast<uint4 *>(tile + tile_off(t, 4 * b + cc, L)) = o;
           } else if (in) {
             float4 *dst = reinterpret_cast<float4 *>(part + ((size_t)u * a.T + c * L + t) * DK + 32 * b + 8 * cc);
-            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+            dst[0] = make_float4(x[8 * cc], x[8 * cc + 1], x[8 * cc + 2], x[8 * cc + 3]);
+            dst[1] = make_float4(x[8 * cc + 4], x[8 * cc + 5], x[8 * cc + 6], x[8 * cc + 7]);
           }
         }
       };
@@ -295,22 +338,28 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->qk_staged);
       // ---- dV ----
       need(m->h, par);
+      float sum = 0.0f;
+      if (b == 0) {  // (all warps' columns are there)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (i >= w) sum += m->rec[i * L + t];
+      }
       {
         constexpr int N = P / 4;
         const float skip = a.skip ? a.skip[h] : 0.0f;
         const u64 step2 = pack2(step, step), skip2 = pack2(skip, skip);
-#pragma unroll 2
+        float x[N];
+        tc::tmem_ld<N>(tl + T_A + N * b, x);
+        tc::tmem_ld_wait();
+#pragma unroll
         for (int cc = 0; cc < N / 8; cc++) {
-          float x[8];
-          tc::tmem_ld8(tl + T_A + N * b + 8 * cc, x);
           const uint32_t to = tile_off(t, N / 8 * b + cc, L);
           const uint4 g = *reinterpret_cast<const uint4 *>(sm + O::G + to);
           const uint32_t gs[4] = {g.x, g.y, g.z, g.w};
           uint32_t o[4];
-          tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const u64 du = pack2(x[2 * i], x[2 * i + 1]);
+            const u64 du = pack2(x[8 * cc + 2 * i], x[8 * cc + 2 * i + 1]);
             o[i] = bf2(a.skip ? fma2(skip2, of_bf2(gs[i]), mul2(step2, du)) : mul2(step2, du));
           }
           const uint4 y = make_uint4(o[0], o[1], o[2], o[3]);
@@ -326,55 +375,23 @@ __global__ void __launch_bounds__(576, 1)
         break;
       }
       if (b > 0) continue;
-      // ---- the steps' gradients: token t ----
       tc::fence_after_sync();
       float x[16];
       tc::tmem_ld16(tl + T_B, x);
-      tc::tmem_ld_wait();
-      tc::fence_before_sync();
-      warp_arrive(m->f_done);
-      auto four = [&](int i) { return (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]); };
       float all = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const float4 y = *reinterpret_cast<const float4 *>(&m->frob[par][4 * i]);
         all += (y.x + y.y) + (y.z + y.w);
       }
-      const float xi = four(X_IN), xo = four(X_OUT), moved = fmaf(step, sum + xo, -four(X_ROW)), duv = (sum + x[X_DIAG]) + xo;
-      float suf = xi, pre = moved;  // readers from t on, writers before t (with the pairs)
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float p = __shfl_down_sync(0xffffffffu, suf, o), q = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane + o < 32) suf += p;
-        if (lane >= o) pre += q;
-      }
-      if (lane == 0) m->scan[0][w] = suf;
-      if (lane == 31) m->scan[1][w] = pre;
-      group_or(2, 128, false);
-      pre -= moved;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        if (i > w) suf += m->scan[0][i];
-        if (i < w) pre += m->scan[1][i];
-      }
-      const float da = start == t ? 0.0f : pre + suf + across * all;
-      const float dd = in ? fmaf(a.A[h], da, duv) * sigmoid(raw) : 0.0f;
-      if (in) {
-        if (!isfinite(dd)) bad = 0x7f80u;
-        const size_t i = (size_t)u * a.T + c * L + t;
-        if (a.gates_f32)
-          static_cast<float *>(a.ddt)[i] = dd;
-        else
-          static_cast<__nv_bfloat16 *>(a.ddt)[i] = __float2bfloat16_rn(dd);
-      }
-      const float sA = warp_sum(in ? step * da : 0.0f), sb = warp_sum(dd), sg = warp_sum(x[X_GV]);
-      if (lane == 0) {  // a warp's tokens each
-        const size_t n = (size_t)chunks * 4, i = (size_t)at * 4 + w;
-        sums[i] = sA;
-        sums[n + i] = sb;
-        sums[2 * n + i] = sg;
-      }
+      tc::tmem_ld_wait();
+      tc::fence_before_sync();
+      warp_arrive(m->f_done);
+      auto four = [&](int i) { return (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]); };
+      const float xo = four(X_OUT);
+      last = Steps{four(X_IN), fmaf(step, sum + xo, -four(X_ROW)), (sum + x[X_DIAG]) + xo, x[X_GV], across * all, raw, step, at, start};
     }
+    if (b == 0 && ok && last.at >= 0) steps();
     if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
   } else if (warp == 16) {
     // ---- products ----
@@ -434,8 +451,8 @@ __global__ void __launch_bounds__(576, 1)
       tc::mbar_arrive_expect_tx(bar(m->full2), 2 * V_TILE<P> + REC * 4);
       tc::bulk_g2s(tc::smem_u32(sm + O::R), adjoints + (size_t)at * V_TILE<P>, V_TILE<P>, bar(m->full2));
     };
+    auto fetch_gates = [&](int at) { tc::bulk_g2s(tc::smem_u32(m->rec), records + (size_t)at * REC, REC * 4, bar(m->full2)); };
     auto fetch_state = [&](int at) {
-      tc::bulk_g2s(tc::smem_u32(m->rec), records + (size_t)at * REC, REC * 4, bar(m->full2));
       tc::bulk_g2s(tc::smem_u32(sm + O::S), states + (size_t)at * V_TILE<P>, V_TILE<P>, bar(m->full2));
     };
     auto fetch_v = [&](int at) {
@@ -458,29 +475,36 @@ __global__ void __launch_bounds__(576, 1)
       prefetch_bytes(records + (size_t)at * REC, REC * 4);
     };
     if ((int)blockIdx.x < chunks) {
-      fetch_v(blockIdx.x);
-      fetch_qk(blockIdx.x);
-      fetch_g(blockIdx.x);
-      fetch_adjoint(blockIdx.x);
-      fetch_state(blockIdx.x);
+      const int at = blockIdx.x;
+      fetch_v(at);
+      fetch_qk(at);
+      fetch_g(at);
+      fetch_adjoint(at);
+      fetch_state(at);
+      fetch_gates(at);
       sent1 = sent2 = 1;
     }
-    // (each tile as soon as nothing reads it: R after K R^T, S or W after dQ and dK's products, V's place after the columns'
-    // sums, the others after their gradients have left from there)
+    // (Each as soon as nothing reads it: V after the first products, R after K R^T, S or W after dQ and dK's products,
+    // Q, K and G after the gradients have left from there, the gates after the columns' sums.)
     for (int at = blockIdx.x, it = 0; at < chunks; at += gridDim.x, it++) {
       const uint32_t par = it & 1;
       const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u), next = at + gridDim.x;
       const bool more = next < chunks;
       if (more) prefetch(next);
-      if (!(ok = wait(bar(m->e), par, limit, gave_up))) break;
+      if (!(ok = wait(bar(m->c2), par, limit, gave_up))) break;
+      if (more) {  // (what is announced is sent, whatever happens)
+        fetch_v(next);
+        sent1++;
+      }
+      ok = wait(bar(m->e), par, limit, gave_up);
       if (more) {
         fetch_adjoint(next);
         sent2++;
       }
-      ok = wait(bar(m->fg), par, limit, gave_up);
-      if (more) fetch_state(next);  // (announced: it is sent whatever happened)
-      if (!ok || !(ok = wait(bar(m->qk_staged), par, limit, gave_up))) break;
-      if (!dqp) {
+      ok = ok && wait(bar(m->fg), par, limit, gave_up);
+      if (more) fetch_state(next);
+      ok = ok && wait(bar(m->qk_staged), par, limit, gave_up);
+      if (!dqp && ok) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
           tensor_s2g_3d(&mapDq, tc::smem_u32(sm) + i * HALF, 64 * i, y, uk);
@@ -489,16 +513,16 @@ __global__ void __launch_bounds__(576, 1)
         tc::bulk_commit();
       }
       if (more) {
-        fetch_v(next);
-        sent1++;
         tc::bulk_wait_read();
         fetch_qk(next);
       }
-      ok = wait(bar(m->v_staged), par, limit, gave_up);
+      ok = ok && wait(bar(m->v_staged), par, limit, gave_up);
+      if (more) fetch_gates(next);
+      if (ok) {
 #pragma unroll
-      for (int i = 0; i < P / 64; i++)
-        if (ok) tensor_s2g_3d(&mapDv, tc::smem_u32(sm + O::G) + i * HALF, 64 * i, y, u);
-      tc::bulk_commit();
+        for (int i = 0; i < P / 64; i++) tensor_s2g_3d(&mapDv, tc::smem_u32(sm + O::G) + i * HALF, 64 * i, y, u);
+        tc::bulk_commit();
+      }
       if (more) {
         tc::bulk_wait_read();
         fetch_g(next);

@@ -242,3 +242,30 @@ def test_captured_and_on_another_stream(lib, dtype, d):
     o = call(stream=side)
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [200, 6000])
+def test_waits_that_give_up_are_reported(lib, d, T):
+    """On the tensor cores (whole sequences, and in segments): the status says so, the next call is clean."""
+    s = make(BF16, 1, 2, 1, T, 128, d, seed=41, states=True)
+    out, S = forward(lib, s)
+    args = dict(dt_bias=s["dt_bias"], skip=s["skip"], S0=s["S0"], dS_final=s["dS_final"], gates_dtype=F32)
+    scan = (s["q"], s["k"], s["v"], s["dt"], s["A"])
+    grads = lib.mesa_ssm_backward_chunked(*scan, s["dout"], **args)
+    ws = torch.empty(lib.mesa_ssm_workspace_size(1, 2, 1, T, 128, d, BF16), dtype=torch.uint8, device="cuda")
+    wb = torch.empty(lib.mesa_ssm_backward_workspace_size(1, 2, 1, T, 128, d, BF16), dtype=torch.uint8, device="cuda")
+    try:
+        lib.mesa_debug_set_wait_limit(0)
+        forward(lib, s, workspace=ws)
+        lib.mesa_ssm_backward_chunked(*scan, s["dout"], workspace=wb, **args)
+        torch.cuda.synchronize()
+    finally:
+        lib.mesa_debug_set_wait_limit(-1)
+    assert lib.mesa_forward_status_code(ws)[0] == lib.MESA_ERR_TIMEOUT
+    assert lib.mesa_forward_status_code(wb)[0] == lib.MESA_ERR_TIMEOUT
+    again, S2 = forward(lib, s, workspace=ws)
+    assert torch.equal(out, again) and torch.equal(S, S2)
+    r = lib.mesa_ssm_backward_chunked(*scan, s["dout"], workspace=wb, **args)
+    assert all(torch.equal(x, y) for x, y in zip(grads, r))
+    assert lib.mesa_forward_status_code(ws)[0] == lib.MESA_OK and lib.mesa_forward_status_code(wb)[0] == lib.MESA_OK
