@@ -46,13 +46,6 @@ struct Vec<__nv_bfloat16, 4> {
   __device__ static void unpack(Raw r, u64 (&v)[2]) { v[0] = bf2(r.x), v[1] = bf2(r.y); }
   __device__ static Raw pack(const u64 (&v)[2]) { return make_uint2(to_bf2(v[0]), to_bf2(v[1])); }
 };
-template <>
-struct Vec<__nv_bfloat16, 8> {
-  using Raw = uint4;
-  __device__ static void unpack(Raw r, u64 (&v)[4]) { v[0] = bf2(r.x), v[1] = bf2(r.y), v[2] = bf2(r.z), v[3] = bf2(r.w); }
-  __device__ static Raw pack(const u64 (&v)[4]) { return make_uint4(to_bf2(v[0]), to_bf2(v[1]), to_bf2(v[2]), to_bf2(v[3])); }
-};
-
 // The taps of VEC channels from channel c0 of head h on, and their bias.
 template <int VEC, int W>
 __device__ __forceinline__ void load_taps(const ConvArgs &a, int h, int c0, u64 (&w)[W][VEC / 2], u64 (&bias)[VEC / 2]) {
@@ -220,28 +213,29 @@ __global__ void __launch_bounds__(128) mesa_causal_conv_step_kernel(ConvArgs a) 
 // Block: GX channel groups of four x rows of runs; part p of a head's (batch, run) pairs; sums over a part's tokens stay
 // in registers, those of the parts are added by mesa_causal_conv_cols_kernel, both in a fixed order.
 constexpr int kBwdRun = 64;
-__host__ __device__ inline int bwd_gx(int d) { return d / 4 < 32 ? d / 4 : 32; }
+constexpr int kBwdVec = 4;  // channels a thread (two: half the registers, but 153 us)
+__host__ __device__ inline int bwd_gx(int d) { return d / kBwdVec < 32 ? d / kBwdVec : 32; }
 
 // (Two CTAs per SM: 203 -> 140 us at 8 x 16 x 4096 x 128; runs of 64 tokens instead of 32: 138.)
 template <typename TIO, int W, bool PACKED>
 __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArgs a, int parts, int runs) {
-  using V = Vec<TIO, 4>;
-  constexpr int AHEAD = 4, N = 4 * (W + 1);
+  using V = Vec<TIO, kBwdVec>;
+  constexpr int AHEAD = 4, VEC = kBwdVec, P = VEC / 2, N = VEC * (W + 1);
   extern __shared__ float sm[];
   const int gx = bwd_gx(a.d), rows = kBlock / gx, g = threadIdx.x % gx, row = threadIdx.x / gx;
-  const int h = blockIdx.z, c0 = (blockIdx.y * gx + g) * 4, pairs = a.B * runs;
+  const int h = blockIdx.z, c0 = (blockIdx.y * gx + g) * VEC, pairs = a.B * runs;
   const bool on = row < rows && c0 < a.d;
-  u64 dw[W][2] = {}, db[2] = {};
+  u64 dw[W][P] = {}, db[P] = {};
   if (on) {
-    u64 w[W][2], bias[2];
-    load_taps<4, W>(a, h, c0, w, bias);
+    u64 w[W][P], bias[P];
+    load_taps<VEC, W>(a, h, c0, w, bias);
     for (int pr = blockIdx.x * rows + row; pr < pairs; pr += parts * rows) {
       const int b = pr / runs, u = b * a.H + h, t0 = pr % runs * kBwdRun, t1 = min(t0 + kBwdRun, a.T);
       const size_t base = (size_t)u * a.T * a.d + c0;
       const TIO *src = static_cast<const TIO *>(a.x) + base, *dout = static_cast<const TIO *>(a.dout) + base;
       TIO *dx = static_cast<TIO *>(a.dx) + base;
       const uint8_t *starts = PACKED ? a.starts + (size_t)b * a.T : nullptr;
-      u64 x[W][2], pend[W][2] = {};  // pend[s]: what the tokens so far give dx_{t-s}
+      u64 x[W][P], pend[W][P] = {};  // pend[s]: what the tokens so far give dx_{t-s}
       int age;  // tokens before t of its document, W - 1 at most
       struct Token {
         typename V::Raw x, g;
@@ -257,14 +251,16 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
         if (PACKED && in.cut) {
           age = 0;
 #pragma unroll
-          for (int s = 1; s < W; s++) x[s][0] = x[s][1] = 0;
+          for (int s = 1; s < W; s++)
+#pragma unroll
+            for (int p = 0; p < P; p++) x[s][p] = 0;
         }
-        u64 dy[2];
+        u64 dy[P];
         V::unpack(in.x, x[0]);
         V::unpack(in.g, dy);
         if (a.silu) {
 #pragma unroll
-          for (int p = 0; p < 2; p++) {
+          for (int p = 0; p < P; p++) {
             u64 y = fma2(w[0][p], x[0][p], bias[p]);
 #pragma unroll
             for (int s = 1; s < W; s++) y = fma2(w[s][p], x[s][p], y);
@@ -274,7 +270,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
         }
         if constexpr (decltype(mine)::value) {
 #pragma unroll
-          for (int p = 0; p < 2; p++) {
+          for (int p = 0; p < P; p++) {
             db[p] = add2(db[p], dy[p]);
 #pragma unroll
             for (int s = 0; s < W; s++) dw[s][p] = fma2(dy[p], x[s][p], dw[s][p]);
@@ -282,28 +278,30 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
         }
         if (!PACKED || age >= W - 1) {
 #pragma unroll
-          for (int p = 0; p < 2; p++)
+          for (int p = 0; p < P; p++)
 #pragma unroll
             for (int s = W - 1; s > 0; s--) pend[s][p] = fma2(w[s][p], dy[p], pend[s - 1][p]);
         } else {  // a document's first tokens: nothing of theirs reaches the one before
 #pragma unroll
-          for (int p = 0; p < 2; p++)
+          for (int p = 0; p < P; p++)
 #pragma unroll
             for (int s = W - 1; s > 0; s--) pend[s][p] = age < s ? pend[s - 1][p] : fma2(w[s][p], dy[p], pend[s - 1][p]);
         }
 #pragma unroll
-        for (int p = 0; p < 2; p++) pend[0][p] = mul2(w[0][p], dy[p]);
+        for (int p = 0; p < P; p++) pend[0][p] = mul2(w[0][p], dy[p]);
         if constexpr (decltype(emit)::value)
           *reinterpret_cast<typename V::Raw *>(dx + (size_t)(t - (W - 1)) * a.d) = V::pack(pend[W - 1]);
         if (PACKED) age = min(age + 1, W - 1);
 #pragma unroll
-        for (int s = W - 1; s > 0; s--) x[s][0] = x[s - 1][0], x[s][1] = x[s - 1][1];
+        for (int s = W - 1; s > 0; s--)
+#pragma unroll
+          for (int p = 0; p < P; p++) x[s][p] = x[s - 1][p];
       };
       constexpr std::true_type yes{};
       constexpr std::false_type no{};
       Token in[2][AHEAD];
       int t = t0;
-      age = load_window<TIO, 4, W>(a, u, t0, c0, x);
+      age = load_window<TIO, VEC, W>(a, u, t0, c0, x);
       const int lead = min(t0 + W - 1, t1);
 #pragma unroll 1
       for (; t < lead; t++) {  // nothing of the run's own is complete yet
@@ -347,7 +345,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
   if (!a.partial) return;
   // the rows' sums: [row][value][group]
 #pragma unroll
-  for (int p = 0; p < 2; p++)
+  for (int p = 0; p < P; p++)
 #pragma unroll
     for (int s = 0; s <= W; s++) {
       float lo, hi;
@@ -360,7 +358,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
   __syncthreads();
   float *dst = a.partial + (size_t)blockIdx.x * a.H * a.d * (W + 1);
   for (int i = threadIdx.x; i < N * gx; i += kBlock) {
-    const int gg = i % gx, v = i / gx, c = (blockIdx.y * gx + gg) * 4 + v / (W + 1);
+    const int gg = i % gx, v = i / gx, c = (blockIdx.y * gx + gg) * VEC + v / (W + 1);
     if (c >= a.d) continue;
     float x = 0.0f;
     for (int r = 0; r < rows; r++) x += sm[(r * N + v) * gx + gg];
@@ -425,9 +423,9 @@ int backward(const ConvArgs &a, cudaStream_t st) {
   const int parts = conv_bwd_parts(a.B, a.H, a.T, a.d), gx = bwd_gx(a.d), runs = (a.T + kBwdRun - 1) / kBwdRun;
   return by_width(a.W, [&](auto w) {
     constexpr int W = decltype(w)::value;
-    const size_t smem = a.partial ? (size_t)(kBlock / gx) * gx * 4 * (W + 1) * sizeof(float) : 0;
+    const size_t smem = a.partial ? (size_t)(kBlock / gx) * gx * kBwdVec * (W + 1) * sizeof(float) : 0;
     timing_mark_begin(K_CONV_BWD, st);
-    const dim3 grid(parts, (a.d / 4 + gx - 1) / gx, a.H);
+    const dim3 grid(parts, (a.d / kBwdVec + gx - 1) / gx, a.H);
     if (a.starts)
       mesa_causal_conv_bwd_kernel<TIO, W, true><<<grid, kBlock, smem, st>>>(a, parts, runs);
     else
@@ -459,7 +457,7 @@ int step(const ConvArgs &a, cudaStream_t st) {
 // Two CTAs for each of a GB300's 152 SMs (what their registers allow at once) over all heads and channels, no more than
 // there are runs.  (us of 8 x 16 x 4096 x 128: two 166, three 221, four 189, six 192)
 int conv_bwd_parts(int B, int H, int T, int d) {
-  const int gx = bwd_gx(d), rows = kBlock / gx, slabs = (d / 4 + gx - 1) / gx;
+  const int gx = bwd_gx(d), rows = kBlock / gx, slabs = (d / kBwdVec + gx - 1) / gx;
   const size_t pairs = (size_t)B * ((T + kBwdRun - 1) / kBwdRun), most = (pairs + rows - 1) / rows;
   size_t n = 152 * 2 / ((size_t)H * slabs);
   if (n > most) n = most;

@@ -54,10 +54,10 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, Ss
 
 // Four elements of a unit's state a thread, chunk after chunk: what a chunk adds is replaced by the state before it
 // (from S0 on; what is left after the last goes to S_final), the adjoints' by the adjoint after it, backwards (from
-// dS_final to dS0).  Eight chunks' values are asked for together: their latency is what this takes.
+// dS_final to dS0).  Sixteen chunks' values are asked for together: their latency is what this takes.
 template <bool ADJOINT>
 __global__ void __launch_bounds__(128) mesa_ssm_scan_kernel(SsmArgs a, SsmWorkspace ws, int NC) {
-  constexpr int AHEAD = 8;
+  constexpr int AHEAD = 16;
   const int n4 = a.dv * a.dk / 4, e = blockIdx.x * 128 + threadIdx.x, u = blockIdx.y;
   if (e >= n4) return;
   const float4 *from = reinterpret_cast<const float4 *>(ADJOINT ? a.dS_final : a.S0);

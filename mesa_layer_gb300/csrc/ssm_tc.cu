@@ -16,51 +16,71 @@ using namespace ssm;
 
 namespace {
 
-// grid (NC, U), a thread a token: the chunks' records.  (In the chain's own warps the two scans of sums, the exponentials
-// and the logarithm were on its way: 225 us for 8 x 16 x 4096, against 0000 with this before it.)
-__global__ void __launch_bounds__(L) mesa_ssm_gates_kernel(SsmArgs a, float *records) {
-  __shared__ float thi[4], tlo[4];
-  __shared__ int ts[4];
-  const int u = blockIdx.y, h = u % a.H, c = blockIdx.x, t = threadIdx.x, w = t >> 5, lane = t & 31, at = c * L + t;
-  float *r = records + ((size_t)u * gridDim.x + c) * REC;
-  float raw = -INFINITY;  // (past the end: nothing is forgotten, nothing written)
-  bool start = false;
-  if (at < a.T) {
-    raw = a.dt[(size_t)u * a.T + at] + (a.dt_bias ? a.dt_bias[h] : 0.0f);
-    start = a.starts && a.starts[(size_t)(u / a.H) * a.T + at];
+// grid (half of NC, U), a thread a token of two chunks (one's instructions fill the other's waits): the chunks' records.
+// (In the chain's own warps the scan of sums, the exponentials and the logarithm were on its way: 225 us for
+// 8 x 16 x 4096, against 200 with this before it.)
+__global__ void __launch_bounds__(L) mesa_ssm_gates_kernel(SsmArgs a, float *records, int NC) {
+  __shared__ float thi[2][4], tlo[2][4];
+  __shared__ int ts[2][4];
+  const int u = blockIdx.y, h = u % a.H, t = threadIdx.x, w = t >> 5, lane = t & 31;
+  const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f, A = a.A[h];
+  float step[2];
+  Two l[2];
+  int s[2];
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    const int at = (2 * blockIdx.x + k) * L + t;
+    float raw = -INFINITY;  // (past the end: nothing is forgotten, nothing written)
+    bool start = false;
+    if (at < a.T) {
+      raw = a.dt[(size_t)u * a.T + at] + bias;
+      start = a.starts && a.starts[(size_t)(u / a.H) * a.T + at];
+    }
+    step[k] = softplus(raw);
+    l[k] = start ? Two{0.0f, 0.0f} : log2_decay(step[k], A);
+    s[k] = start ? t : -1;
   }
-  const float step = softplus(raw);
-  Two l = start ? Two{0.0f, 0.0f} : log2_decay(step, a.A[h]);
-  int s = start ? t : -1;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Two p = {__shfl_up_sync(0xffffffffu, l.hi, o), __shfl_up_sync(0xffffffffu, l.lo, o)};
-    const int ps = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) {
-      l = two_add(p, l);
-      s = max(s, ps);
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      const Two p = {__shfl_up_sync(0xffffffffu, l[k].hi, o), __shfl_up_sync(0xffffffffu, l[k].lo, o)};
+      const int ps = __shfl_up_sync(0xffffffffu, s[k], o);
+      if (lane >= o) {
+        l[k] = two_add(p, l[k]);
+        s[k] = max(s[k], ps);
+      }
     }
   }
-  if (lane == 31) thi[w] = l.hi, tlo[w] = l.lo, ts[w] = s;
-  const Two end = {__shfl_sync(0xffffffffu, l.hi, 31), __shfl_sync(0xffffffffu, l.lo, 31)};
-  const int send = __shfl_sync(0xffffffffu, s, 31);
-  r[R_OUT + t] = t >= send ? exp2f(two_sub(end, l)) : 0.0f;
-  r[R_IN + t] = s < 0 ? exp2f(l.hi + l.lo) : 0.0f;
-  r[R_LOG + t] = l.hi + l.lo;
-  r[R_STEP + t] = step;
+#pragma unroll
+  for (int k = 0; k < 2; k++)
+    if (lane == 31) thi[k][w] = l[k].hi, tlo[k][w] = l[k].lo, ts[k][w] = s[k];
   __syncthreads();
-  int before = -1;
-  for (int i = 0; i < w; i++) before = max(before, ts[i]);
-  r[R_START + t] = __int_as_float(max(s, before));
-  if (t < 32) {  // decays over whole warps' tokens, from..to
-    const int from = t < 16 ? t % 4 + 1 : t < 20 ? 0 : t < 24 ? t - 20 + 1 : 0, to = t < 16 ? t / 4 : t < 20 ? t - 16 : 4;
-    Two d = {0.0f, 0.0f};
-    bool cut = false;
-    for (int i = from; i < to; i++) {
-      d = two_add(d, Two{thi[i], tlo[i]});
-      cut |= ts[i] >= 0;
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    const int c = 2 * blockIdx.x + k;
+    if (c >= NC) break;
+    float *r = records + ((size_t)u * NC + c) * REC;
+    const Two end = {__shfl_sync(0xffffffffu, l[k].hi, 31), __shfl_sync(0xffffffffu, l[k].lo, 31)};
+    const int send = __shfl_sync(0xffffffffu, s[k], 31);
+    r[R_OUT + t] = t >= send ? rule::ex2(two_sub(end, l[k])) : 0.0f;
+    r[R_IN + t] = s[k] < 0 ? rule::ex2(l[k].hi + l[k].lo) : 0.0f;
+    r[R_LOG + t] = l[k].hi + l[k].lo;
+    r[R_STEP + t] = step[k];
+    int before = -1;
+    for (int i = 0; i < w; i++) before = max(before, ts[k][i]);
+    r[R_START + t] = __int_as_float(max(s[k], before));
+    if (w == k) {  // decays over whole warps' tokens, from..to
+      const int from = lane < 16 ? lane % 4 + 1 : lane < 20 ? 0 : lane < 24 ? lane - 20 + 1 : 0,
+                to = lane < 16 ? lane / 4 : lane < 20 ? lane - 16 : 4;
+      Two d = {0.0f, 0.0f};
+      bool cut = false;
+      for (int i = from; i < to; i++) {
+        d = two_add(d, Two{thi[k][i], tlo[k][i]});
+        cut |= ts[k][i] >= 0;
+      }
+      r[R_BETWEEN + lane] = cut ? 0.0f : rule::ex2(d.hi + d.lo);
     }
-    r[R_BETWEEN + t] = cut ? 0.0f : exp2f(d.hi + d.lo);
   }
 }
 
@@ -529,23 +549,36 @@ __global__ void __launch_bounds__(448, 1)
 }
 
 // The states before the segments from what each leaves: S_{y+1} = decay_y S_y + left_y, S_0 the call's (copied: the last
-// segment may write its final state over it); the adjoints after them the same way, backwards.  Four elements a thread.
+// segment may write its final state over it); the adjoints after them the same way, backwards.  Four elements a thread;
+// eight segments' are asked for together (one after the other: 27 us for 16 units in nine segments).
 __global__ void __launch_bounds__(128) mesa_ssm_join_kernel(SsmArgs a, SsmSegments sg, bool adjoint) {
-  const int n4 = a.dv * a.dk / 4, e = blockIdx.x * 128 + threadIdx.x, u = blockIdx.y;
+  constexpr int AHEAD = 8;
+  const int n4 = a.dv * a.dk / 4, e = blockIdx.x * 128 + threadIdx.x, u = blockIdx.y, n = sg.n;
   if (e >= n4) return;
   const float4 *from = reinterpret_cast<const float4 *>(adjoint ? a.dS_final : a.S0);
-  float4 *x = reinterpret_cast<float4 *>(adjoint ? sg.R : sg.S) + (size_t)u * sg.n * n4 + e;
+  float4 *x = reinterpret_cast<float4 *>(adjoint ? sg.R : sg.S) + (size_t)u * n * n4 + e;
+  const float *decay = sg.decay + (size_t)u * n;
   float4 s = from ? from[(size_t)u * n4 + e] : make_float4(0, 0, 0, 0);
-  for (int i = 0; i < sg.n; i++) {
-    const int y = adjoint ? sg.n - 1 - i : i;
-    if (i + 1 == sg.n) {
-      x[(size_t)y * n4] = s;
-      break;
+  for (int i0 = 0; i0 < n; i0 += AHEAD) {
+    float4 d[AHEAD];
+    float w[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; j++) {
+      const int y = adjoint ? n - 1 - i0 - j : i0 + j;
+      if (i0 + j + 1 < n) {  // (the last one's is not needed)
+        d[j] = x[(size_t)y * n4];
+        w[j] = decay[y];
+      }
     }
-    const float4 d = x[(size_t)y * n4];
-    const float w = sg.decay[(size_t)u * sg.n + y];
-    x[(size_t)y * n4] = s;
-    s = w == 0.0f ? d : make_float4(fmaf(w, s.x, d.x), fmaf(w, s.y, d.y), fmaf(w, s.z, d.z), fmaf(w, s.w, d.w));
+#pragma unroll
+    for (int j = 0; j < AHEAD; j++) {
+      const int y = adjoint ? n - 1 - i0 - j : i0 + j;
+      if (i0 + j < n) {
+        x[(size_t)y * n4] = s;
+        if (i0 + j + 1 < n)
+          s = w[j] == 0.0f ? d[j] : make_float4(fmaf(w[j], s.x, d[j].x), fmaf(w[j], s.y, d[j].y), fmaf(w[j], s.z, d[j].z), fmaf(w[j], s.w, d[j].w));
+      }
+    }
   }
 }
 
@@ -604,15 +637,16 @@ int chains(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStre
 
 }  // namespace
 
-// Segments: a GB300's 152 SMs hold a CTA each; two segments or more read k and v twice.
+// Segments: a GB300's 152 SMs hold a CTA each.  A segment's chunks are walked twice (before a forward the second time takes
+// half as long), and the two more kernels cost as much as four or five chunks: shorter chains are left whole.  us of one
+// chain, of segments, forward / backward (units x chunks): 1 x 4 21, 20 / 38, 43; 1 x 8 33, 21 / 50, 43; 16 x 16 57, 27 /
+// 86, 64; 24 x 9 (dv = 64) 32, 24 / 57, 53; 48 x 9 37, 33 / 76, 85; 70 x 32 106, 96 / 266, 291; 16 x 512 1496, 297 / 2135, 939.
 SsmSegments ssm_segments(int U, int T, int dv, bool backward, void *workspace, size_t *bytes) {
   const int NC = (T + L - 1) / L;
   SsmSegments sg;
-  int n = U > 0 ? 152 / U : 1;
-  if (n > NC / 4) n = NC / 4;  // four chunks at least
-  if (n < 2) n = 1;
-  sg.per = (NC + n - 1) / n;
-  sg.n = n > 1 ? (NC + sg.per - 1) / sg.per : 1;  // (no empty one)
+  const int most = U > 0 ? 152 / U : 1, n = most < NC ? most : NC;
+  sg.per = n > 1 ? (NC + n - 1) / n : NC;
+  sg.n = n > 1 && (backward ? 2 * sg.per + 5 < NC : 3 * sg.per + 8 < 2 * NC) ? (NC + sg.per - 1) / sg.per : 1;  // (no empty one)
   auto up256 = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t state = sg.n > 1 ? (size_t)U * sg.n * dv * DK * sizeof(float) : 0, decay = up256((size_t)U * sg.n * sizeof(float)),
                recs = up256((size_t)U * NC * REC * sizeof(float));
@@ -628,7 +662,8 @@ SsmSegments ssm_segments(int U, int T, int dv, bool backward, void *workspace, s
 
 int launch_ssm_gates(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
   timing_mark_begin(K_SSM_GATES, st);
-  mesa_ssm_gates_kernel<<<dim3((a.T + L - 1) / L, a.units()), L, 0, st>>>(a, sg.records);
+  const int NC = (a.T + L - 1) / L;
+  mesa_ssm_gates_kernel<<<dim3((NC + 1) / 2, a.units()), L, 0, st>>>(a, sg.records, NC);
   timing_mark_end(K_SSM_GATES, st);
   return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
