@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "mixer_ops.h"
+#include "overlap.cuh"
 #include "packed.cuh"
 
 namespace mesa {
@@ -342,6 +343,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
           *reinterpret_cast<typename V::Raw *>(dx + (size_t)(t - s) * a.d) = V::pack(pend[s - 1]);
     }
   }
+  may_follow();
   if (!a.partial) return;
   // the rows' sums: [row][value][group]
 #pragma unroll
@@ -369,6 +371,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
 // Eight lanes a value over the parts' sums.
 __global__ void __launch_bounds__(kBlock) mesa_causal_conv_cols_kernel(ConvArgs a, int parts) {
   const int n = a.H * a.d * (a.W + 1), i = (blockIdx.x * kBlock + threadIdx.x) / 8, l = threadIdx.x & 7;
+  ahead_done();
   float x = 0.0f;
   if (i < n)
     for (int p = l; p < parts; p += 8) x += a.partial[(size_t)p * n + i];
@@ -433,8 +436,10 @@ int backward(const ConvArgs &a, cudaStream_t st) {
     timing_mark_end(K_CONV_BWD, st);
     if (a.partial) {
       timing_mark_begin(K_CONV_COLS, st);
-      mesa_causal_conv_cols_kernel<<<(unsigned)(((size_t)a.H * a.d * (W + 1) * 8 + kBlock - 1) / kBlock), kBlock, 0, st>>>(a, parts);
+      const bool ok = launch_after(mesa_causal_conv_cols_kernel, (unsigned)(((size_t)a.H * a.d * (W + 1) * 8 + kBlock - 1) / kBlock), kBlock, 0,
+                                   st, a, parts);
       timing_mark_end(K_CONV_COLS, st);
+      if (!ok) return -1;
     }
     return done();
   });

@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "mixer_ops.h"
+#include "overlap.cuh"
 
 namespace mesa {
 
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_qk_norm_rotary_bwd_kernel(Rota
       }
     }
   }
+  may_follow();
   if (!a.partial) return;
 #pragma unroll
   for (int which = 0; which < 2; which++) {
@@ -287,6 +289,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_qk_norm_rotary_bwd_kernel(Rota
 // A warp a channel over the CTAs' sums.
 __global__ void __launch_bounds__(kBlock) mesa_qk_norm_rotary_cols_kernel(RotaryArgs a, int parts) {
   const int i = (blockIdx.x * kBlock + threadIdx.x) / 32, lane = threadIdx.x & 31;
+  ahead_done();
   if (i >= 2 * a.d) return;
   float x = 0.0f;
   for (int p = lane; p < parts; p += 32) x += a.partial[(size_t)p * 2 * a.d + i];
@@ -344,8 +347,9 @@ int backward(const RotaryArgs &a, cudaStream_t st) {
     timing_mark_end(K_ROTARY_BWD, st);
     if (a.partial) {
       timing_mark_begin(K_ROTARY_COLS, st);
-      mesa_qk_norm_rotary_cols_kernel<<<(2 * a.d * 32 + kBlock - 1) / kBlock, kBlock, 0, st>>>(a, parts);
+      const bool ok = launch_after(mesa_qk_norm_rotary_cols_kernel, (2 * a.d * 32 + kBlock - 1) / kBlock, kBlock, 0, st, a, parts);
       timing_mark_end(K_ROTARY_COLS, st);
+      if (!ok) return -1;
     }
     return done();
   });

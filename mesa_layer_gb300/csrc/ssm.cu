@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, Ss
   __shared__ Gates g;
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  may_follow();
   load_rows<DK, C>(k, ADJOINT ? a.q : a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
   load_rows<DV, C>(v, ADJOINT ? a.dout : a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   if (threadIdx.x < 32) gates_load(g, a, u, t0, n, threadIdx.x);
@@ -39,11 +40,12 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, Ss
     const int t = i / DV;
     v[t * (DV + 4) + i % DV] *= ADJOINT ? g.f[t] : g.c[t] * g.step[t];
   }
-  if (!ADJOINT && threadIdx.x == 0) ws.decay[(size_t)u * NC + c] = g.f[C - 1];
   __syncthreads();
   float acc[DV / 16][DK / 16];
   zero(acc);
   mm_tn<C>(acc, v, DV + 4, k, DK + 4, ty, tx);
+  ahead_done();
+  if (!ADJOINT && threadIdx.x == 0) ws.decay[(size_t)u * NC + c] = g.f[C - 1];
   float *dst = (ADJOINT ? ws.R : ws.S) + ((size_t)u * NC + c) * a.dv * a.dk;
 #pragma unroll
   for (int i = 0; i < DV / 16; i++)
@@ -59,6 +61,8 @@ template <bool ADJOINT>
 __global__ void __launch_bounds__(128) mesa_ssm_scan_kernel(SsmArgs a, SsmWorkspace ws, int NC) {
   constexpr int AHEAD = 16;
   const int n4 = a.dv * a.dk / 4, e = blockIdx.x * 128 + threadIdx.x, u = blockIdx.y;
+  may_follow();
+  ahead_done();
   if (e >= n4) return;
   const float4 *from = reinterpret_cast<const float4 *>(ADJOINT ? a.dS_final : a.S0);
   float4 *to = reinterpret_cast<float4 *>(ADJOINT ? a.dS0 : a.S_final);
@@ -97,12 +101,14 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWo
   __shared__ Gates g;
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  may_follow();
   const float *state = NC > 1 ? ws.S + ((size_t)u * NC + c) * a.dv * a.dk : a.S0 ? a.S0 + (size_t)u * a.dv * a.dk : nullptr;
   load_rows<DK, C>(q, a.q, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
   load_rows<DK, C>(k, a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
   load_rows<DV, C>(v, a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
-  if (state) load_rows<DK, DV>(S, state, 0, 0, a.dv, a.dk);
   if (threadIdx.x < 32) gates_load(g, a, u, t0, n, threadIdx.x);
+  ahead_done();  // (the states)
+  if (state) load_rows<DK, DV>(S, state, 0, 0, a.dv, a.dk);
   __syncthreads();
   {
     float acc[2][2];
@@ -144,22 +150,19 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWo
 
 template <int DK, int DV>
 struct States {
-  static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, bool adjoint, cudaStream_t st) {
+  static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, bool adjoint, bool first, cudaStream_t st) {
     const size_t smem = sizeof(float) * C * (DK + DV + 8);
     const dim3 grid(NC, a.units());
     timing_mark_begin(K_SSM_STATES, st);
-    const bool ok = adjoint ? launch(mesa_ssm_states_kernel<DK, DV, true>, grid, smem, st, a, ws)
-                            : launch(mesa_ssm_states_kernel<DK, DV, false>, grid, smem, st, a, ws);
+    const bool ok = adjoint ? launch(mesa_ssm_states_kernel<DK, DV, true>, grid, smem, false, st, a, ws)
+                            : launch(mesa_ssm_states_kernel<DK, DV, false>, grid, smem, first, st, a, ws);
     timing_mark_end(K_SSM_STATES, st);
     if (!ok) return -1;
     const dim3 elements((a.dv * a.dk / 4 + 127) / 128, a.units());
     timing_mark_begin(K_SSM_SCAN, st);
-    if (adjoint)
-      mesa_ssm_scan_kernel<true><<<elements, 128, 0, st>>>(a, ws, NC);
-    else
-      mesa_ssm_scan_kernel<false><<<elements, 128, 0, st>>>(a, ws, NC);
+    const bool done = launch_after(adjoint ? mesa_ssm_scan_kernel<true> : mesa_ssm_scan_kernel<false>, elements, 128, 0, st, a, ws, NC);
     timing_mark_end(K_SSM_SCAN, st);
-    return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    return done && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
   }
 };
 template <int DK, int DV>
@@ -167,7 +170,7 @@ struct Out {
   static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, cudaStream_t st) {
     const size_t smem = sizeof(float) * (C * (2 * DK + DV + 12) + DV * (DK + 4) + C * LDC);
     timing_mark_begin(K_SSM_OUT, st);
-    const bool ok = launch(mesa_ssm_out_kernel<DK, DV>, dim3(NC, a.units()), smem, st, a, ws);
+    const bool ok = launch(mesa_ssm_out_kernel<DK, DV>, dim3(NC, a.units()), smem, NC == 1, st, a, ws);
     timing_mark_end(K_SSM_OUT, st);
     return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
   }
@@ -175,16 +178,16 @@ struct Out {
 
 }  // namespace
 
-// The states before every chunk (adjoint: the adjoints after every chunk).
-int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoint, cudaStream_t st) {
-  return by_size<States>(a.dk, a.dv, a, ws, (a.T + C - 1) / C, adjoint, st);
+// The states before every chunk (adjoint: the adjoints after every chunk); first: the call begins with it.
+int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoint, bool first, cudaStream_t st) {
+  return by_size<States>(a.dk, a.dv, a, ws, (a.T + C - 1) / C, adjoint, first, st);
 }
 
 int launch_ssm_forward(const SsmArgs &a, const SsmWorkspace &ws, cudaStream_t st) {
   const int NC = (a.T + C - 1) / C;
   // outputs of one chunk come before its state where S_final is S0's memory
   if (NC == 1 && by_size<Out>(a.dk, a.dv, a, ws, NC, st) != 0) return -1;
-  if ((NC > 1 || a.S_final) && launch_ssm_states(a, ws, false, st) != 0) return -1;
+  if ((NC > 1 || a.S_final) && launch_ssm_states(a, ws, false, NC > 1, st) != 0) return -1;
   return NC == 1 ? 0 : by_size<Out>(a.dk, a.dv, a, ws, NC, st);
 }
 

@@ -20,7 +20,7 @@ namespace mesa {
 
 using namespace ssm;
 
-int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoint, cudaStream_t st);
+int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoint, bool first, cudaStream_t st);
 
 namespace {
 
@@ -42,12 +42,14 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0), h = u % a.H;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
   const size_t at = ((size_t)u * NC + c) * a.dv * a.dk;
+  may_follow();
   load_rows<DK, C>(q, a.q, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
   load_rows<DK, C>(k, a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
   load_rows<DV, C>(v, a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   load_rows<DV, C>(g, a.dout, a.dtype, (size_t)u * a.T + t0, n, a.dv);
-  load_rows<DK, DV>(S, ws.S + at, 0, 0, a.dv, a.dk);
   if (warp == 0) gates_load(ga, a, u, t0, n, lane);
+  ahead_done();  // (the states and adjoints)
+  load_rows<DK, DV>(S, ws.S + at, 0, 0, a.dv, a.dk);
   __syncthreads();
   {
     float G[2][2], Hm[2][2];
@@ -229,6 +231,7 @@ __global__ void __launch_bounds__(256) mesa_ssm_params_kernel(SsmArgs a, const f
   __shared__ float part[8];
   const int h = blockIdx.x, which = blockIdx.y;
   void *dst = which == 0 ? a.dA : which == 1 ? a.dbias : a.dskip;
+  ahead_done();
   if (!dst) return;
   const size_t U = (size_t)a.units();
   float x = 0.0f;
@@ -252,7 +255,7 @@ struct Grads {
   static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, cudaStream_t st) {
     const size_t smem = sizeof(float) * (2 * C * (DK + 4) + 2 * C * (DV + 4) + DV * (DK + 4) + 2 * C * LDC);
     timing_mark_begin(K_SSM_GRADS, st);
-    const bool ok = launch(mesa_ssm_grads_kernel<DK, DV>, dim3(NC, a.units()), smem, st, a, ws);
+    const bool ok = launch(mesa_ssm_grads_kernel<DK, DV>, dim3(NC, a.units()), smem, false, st, a, ws);
     timing_mark_end(K_SSM_GRADS, st);
     return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
   }
@@ -263,9 +266,9 @@ struct Grads {
 int launch_ssm_param_sums(const SsmArgs &a, const float *sums, int n, cudaStream_t st) {
   if (!a.dA && !a.dbias && !a.dskip) return 0;
   timing_mark_begin(K_SSM_PARAMS, st);
-  mesa_ssm_params_kernel<<<dim3(a.H, 3), 256, 0, st>>>(a, sums, n);
+  const bool ok = launch_after(mesa_ssm_params_kernel, dim3(a.H, 3), 256, 0, st, a, sums, n);
   timing_mark_end(K_SSM_PARAMS, st);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_ssm_group_sum(const SsmArgs &a, const float *dqp, const float *dkp, cudaStream_t st) {
@@ -278,7 +281,7 @@ int launch_ssm_group_sum(const SsmArgs &a, const float *dqp, const float *dkp, c
 
 int launch_ssm_backward(const SsmArgs &a, const SsmWorkspace &ws, cudaStream_t st) {
   const int NC = (a.T + C - 1) / C;
-  if (launch_ssm_states(a, ws, false, st) != 0 || launch_ssm_states(a, ws, true, st) != 0) return -1;
+  if (launch_ssm_states(a, ws, false, true, st) != 0 || launch_ssm_states(a, ws, true, false, st) != 0) return -1;
   if (by_size<Grads>(a.dk, a.dv, a, ws, NC, st) != 0) return -1;
   if (ws.dqp && launch_ssm_group_sum(a, ws.dqp, ws.dkp, st) != 0) return -1;
   return launch_ssm_param_sums(a, ws.sums, NC, st);

@@ -109,7 +109,9 @@ __global__ void __launch_bounds__(576, 1)
   };
   int sent1 = 0, sent2 = 0;  // chunks asked for (warp 17)
 
+  may_follow();
   if (warp < 16) {
+    ahead_done();  // (sums, dqp and dkp may be written)
     const int w = warp & 3, b = warp >> 2, t = 32 * w + lane;  // row t, columns of quarter b
     const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
     uint32_t bad = 0;
@@ -479,6 +481,7 @@ __global__ void __launch_bounds__(576, 1)
       fetch_v(at);
       fetch_qk(at);
       fetch_g(at);
+      ahead_done();  // (the states, adjoints and gates; the rows are the call's inputs)
       fetch_adjoint(at);
       fetch_state(at);
       fetch_gates(at);
@@ -562,10 +565,10 @@ int grads(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStrea
   if (cudaFuncSetAttribute(mesa_ssm_grads_tc_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem<P>) != cudaSuccess)
     return -1;
   timing_mark_begin(K_SSM_GRADS, st);
-  mesa_ssm_grads_tc_kernel<P><<<chunks < sms ? chunks : sms, 576, kGradSmem<P>, st>>>(a, NC, chunks, sg.records, ws.S, ws.R, ws.sums,
-                                                                                     ws.dqp, ws.dkp, q, k, v, g, dq, dk, dv);
+  const bool ok = launch_after(mesa_ssm_grads_tc_kernel<P>, chunks < sms ? chunks : sms, 576, kGradSmem<P>, st, a, NC, chunks, sg.records,
+                               ws.S, ws.R, ws.sums, ws.dqp, ws.dkp, q, k, v, g, dq, dk, dv);
   timing_mark_end(K_SSM_GRADS, st);
-  return cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+  return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
 }
 
 // [segments, records | S | R | sums | per-head dq, dk]

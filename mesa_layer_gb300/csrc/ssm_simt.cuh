@@ -2,6 +2,7 @@
 // shared memory as fp32, and small products by 16 x 16 threads.
 #pragma once
 
+#include "overlap.cuh"
 #include "ssm.h"
 #include "ssm_common.cuh"
 
@@ -145,11 +146,12 @@ int by_size(int dk, int dv, Args &&...args) {
   return k(std::integral_constant<int, 128>());
 }
 
-// Launch with `smem` bytes of dynamic shared memory (48 KB without being asked for, the static part among them).
+// Launch, the call's first kernel or not, with `smem` bytes of dynamic shared memory (48 KB without being asked for, the static part among them).
 template <typename K, typename... Args>
-bool launch(K kernel, dim3 grid, size_t smem, cudaStream_t st, const Args &...args) {
+bool launch(K kernel, dim3 grid, size_t smem, bool first, cudaStream_t st, const Args &...args) {
   if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return false;
+  if (!first) return launch_after(kernel, grid, kThreads, smem, st, args...);
   kernel<<<grid, kThreads, smem, st>>>(args...);
   return true;
 }

@@ -23,6 +23,7 @@ __global__ void __launch_bounds__(L) mesa_ssm_gates_kernel(SsmArgs a, float *rec
   __shared__ float thi[2][4], tlo[2][4];
   __shared__ int ts[2][4];
   const int u = blockIdx.y, h = u % a.H, t = threadIdx.x, w = t >> 5, lane = t & 31;
+  may_follow();
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f, A = a.A[h];
   float step[2];
   Two l[2];
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(576, 1)
   const int t = tid & 127, w = warp & 3;  // token, or lane of the state
   const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
 
+  if (warp < 16) ahead_done();  // (the records, the segments' states; the copies are of the call's inputs)
   if (warp < 4) {
     // ---- M ----
     const float *r = record(records, u, NCT, c0);
@@ -444,6 +446,8 @@ __global__ void __launch_bounds__(448, 1)
   const int t = tid & 127, w = warp & 3;  // token, or lane of the state
   const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
 
+  may_follow();
+  if (warp < 12) ahead_done();  // (the records, the segments' states; the copies are of the call's inputs)
   if (warp < 8) {
     const int hf = warp >> 2;  // two warps for each 32 rows, half of the columns each
     auto weight = [&](int c) {
@@ -554,6 +558,8 @@ __global__ void __launch_bounds__(448, 1)
 __global__ void __launch_bounds__(128) mesa_ssm_join_kernel(SsmArgs a, SsmSegments sg, bool adjoint) {
   constexpr int AHEAD = 8;
   const int n4 = a.dv * a.dk / 4, e = blockIdx.x * 128 + threadIdx.x, u = blockIdx.y, n = sg.n;
+  may_follow();
+  ahead_done();
   if (e >= n4) return;
   const float4 *from = reinterpret_cast<const float4 *>(adjoint ? a.dS_final : a.S0);
   float4 *x = reinterpret_cast<float4 *>(adjoint ? sg.R : sg.S) + (size_t)u * n * n4 + e;
@@ -586,15 +592,16 @@ template <typename K, typename... Args>
 bool launch_tc(int kind, K kernel, dim3 grid, int threads, uint32_t smem, cudaStream_t st, const Args &...args) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
   timing_mark_begin(kind, st);
-  kernel<<<grid, threads, smem, st>>>(args...);
+  const bool ok = launch_after(kernel, grid, threads, smem, st, args...);
   timing_mark_end(kind, st);
-  return cudaPeekAtLastError() == cudaSuccess;
+  return ok && cudaPeekAtLastError() == cudaSuccess;
 }
 
-void launch_join(const SsmArgs &a, const SsmSegments &sg, bool adjoint, cudaStream_t st) {
+bool launch_join(const SsmArgs &a, const SsmSegments &sg, bool adjoint, cudaStream_t st) {
   timing_mark_begin(K_SSM_SCAN, st);
-  mesa_ssm_join_kernel<<<dim3(a.dv * DK / 512, a.units()), 128, 0, st>>>(a, sg, adjoint);
+  const bool ok = launch_after(mesa_ssm_join_kernel, dim3(a.dv * DK / 512, a.units()), 128, 0, st, a, sg, adjoint);
   timing_mark_end(K_SSM_SCAN, st);
+  return ok;
 }
 template <int P, int MODE>
 bool launch_chain(const SsmArgs &a, const SsmSegments &sg, uint8_t *kept, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
@@ -610,8 +617,7 @@ int forward(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&o, a.out, a.units(), a.T, P))
     return -1;
   if (sg.n > 1) {
-    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st)) return -1;
-    launch_join(a, sg, false, st);
+    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st) || !launch_join(a, sg, false, st)) return -1;
   }
   return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<P>, dim3(a.units(), sg.n), 576, kFwdSmem<P>, st, a, sg, sg.records, q, k,
                    v, o)
@@ -627,10 +633,8 @@ int chains(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStre
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&g, a.dout, a.units(), a.T, P))
     return -1;
   if (sg.n > 1) {
-    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st)) return -1;
-    launch_join(a, sg, false, st);
-    if (!launch_chain<P, kAdjointSegment>(a, sg, nullptr, q, g, st)) return -1;
-    launch_join(a, sg, true, st);
+    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st) || !launch_join(a, sg, false, st)) return -1;
+    if (!launch_chain<P, kAdjointSegment>(a, sg, nullptr, q, g, st) || !launch_join(a, sg, true, st)) return -1;
   }
   return launch_chain<P, kKeep>(a, sg, ws.S, k, v, st) && launch_chain<P, kAdjoint>(a, sg, ws.R, q, g, st) ? 0 : -1;
 }

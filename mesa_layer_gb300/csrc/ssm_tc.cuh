@@ -9,6 +9,7 @@
 #pragma once
 
 #include "gated_delta_tc.cuh"
+#include "overlap.cuh"
 #include "ssm.h"
 #include "ssm_common.cuh"
 
