@@ -708,15 +708,16 @@ def mesa_ssm_backward_chunked(q, k, v, dt, A, dout, dt_bias=None, skip=None, sta
         raise MesaError(f"ddt, dA, ddt_bias and dskip must be {dtype} or {torch.float32}, got {gates_dtype}")
     if (ddt_bias is not None and dt_bias is None) or (dskip is not None and skip is None):
         raise MesaError("ddt_bias and dskip need dt_bias and skip")
-    dq = _new(q.shape, dtype, dev, stream) if dq is None else dq
-    dk = _new(q.shape, dtype, dev, stream) if dk is None else dk
-    dv = _new(v.shape, dtype, dev, stream) if dv is None else dv
-    ddt = _new((B, H, T), gates_dtype, dev, stream) if ddt is None else ddt
-    dA = _new((H,), gates_dtype, dev, stream) if dA is None else dA
+    gate = _like if gates_dtype is torch.float32 else lambda t, stream: _new(t.shape, gates_dtype, dev, stream)
+    dq = _like(q, stream) if dq is None else dq
+    dk = _like(q, stream) if dk is None else dk
+    dv = _like(v, stream) if dv is None else dv
+    ddt = gate(dt, stream) if ddt is None else ddt
+    dA = gate(A, stream) if dA is None else dA
     if dt_bias is not None and ddt_bias is None:
-        ddt_bias = _new((H,), gates_dtype, dev, stream)
+        ddt_bias = gate(A, stream)
     if skip is not None and dskip is None:
-        dskip = _new((H,), gates_dtype, dev, stream)
+        dskip = gate(A, stream)
     if gates_dtype is torch.float32:
         code |= MESA_GATE_GRADS_F32
     state, heads = (B, H, dvv, dkk), (H,)

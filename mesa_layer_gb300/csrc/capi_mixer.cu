@@ -87,7 +87,6 @@ int mesa_ssm_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dt
   a.S_final = S_final;
   a.status = (unsigned *)workspace;
   a.wait_limit = mesa::wait_limit();
-  if (bad_memset(workspace, sizeof(unsigned), stream)) return MESA_ERR_CUDA;
   if (scan_tc(dtype, dk, dv))
     return mesa::launch_ssm_forward_tc(a, (char *)workspace + kStatusBytes, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
   mesa::SsmWorkspace ws;
@@ -141,7 +140,6 @@ int mesa_ssm_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int d
   a.dS0 = dS0;
   a.status = (unsigned *)workspace;
   a.wait_limit = mesa::wait_limit();
-  if (bad_memset(workspace, sizeof(unsigned), stream)) return MESA_ERR_CUDA;
   if (scan_tc(dtype, dk, dv))
     return mesa::launch_ssm_backward_tc(a, (char *)workspace + kStatusBytes, stream) == 0 ? MESA_OK : MESA_ERR_CUDA;
   mesa::SsmWorkspace ws;

@@ -22,31 +22,35 @@ using namespace ssm;
 
 namespace {
 
-// grid (NC, U): what chunk c adds to its unit's state, [dv, dk], to ws.S (ADJOINT: what it gives the adjoint of
-// the state before it, sum_i e^{l_i} g_i q_i^T, to ws.R); ws.decay.
-template <int DK, int DV, bool ADJOINT>
+// grid (NC, U, 1 or 2): what chunk c adds to its unit's state, [dv, dk], to ws.S, and ws.decay; z = 1: what it gives the
+// adjoint of the state before it, sum_i e^{l_i} g_i q_i^T, to ws.R.
+template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, SsmWorkspace ws) {
   extern __shared__ float4 smem4[];
   float *k = reinterpret_cast<float *>(smem4), *v = k + C * (DK + 4);
   __shared__ Gates g;
+  const bool adjoint = blockIdx.z == 1;
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   may_follow();
-  load_rows<DK, C>(k, ADJOINT ? a.q : a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
-  load_rows<DV, C>(v, ADJOINT ? a.dout : a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
+  load_rows<DK, C>(k, adjoint ? a.q : a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
+  load_rows<DV, C>(v, adjoint ? a.dout : a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   if (threadIdx.x < 32) gates_load(g, a, u, t0, n, threadIdx.x);
   __syncthreads();
   for (int i = threadIdx.x; i < C * DV; i += kThreads) {
     const int t = i / DV;
-    v[t * (DV + 4) + i % DV] *= ADJOINT ? g.f[t] : g.c[t] * g.step[t];
+    v[t * (DV + 4) + i % DV] *= adjoint ? g.f[t] : g.c[t] * g.step[t];
   }
   __syncthreads();
   float acc[DV / 16][DK / 16];
   zero(acc);
   mm_tn<C>(acc, v, DV + 4, k, DK + 4, ty, tx);
   ahead_done();
-  if (!ADJOINT && threadIdx.x == 0) ws.decay[(size_t)u * NC + c] = g.f[C - 1];
-  float *dst = (ADJOINT ? ws.R : ws.S) + ((size_t)u * NC + c) * a.dv * a.dk;
+  if (threadIdx.x == 0 && !adjoint) {
+    ws.decay[(size_t)u * NC + c] = g.f[C - 1];
+    if (ws.clear && c == 0 && u == 0) *a.status = 0;  // (the kernels after this one report)
+  }
+  float *dst = (adjoint ? ws.R : ws.S) + ((size_t)u * NC + c) * a.dv * a.dk;
 #pragma unroll
   for (int i = 0; i < DV / 16; i++)
 #pragma unroll
@@ -55,18 +59,18 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, Ss
 }
 
 // Four elements of a unit's state a thread, chunk after chunk: what a chunk adds is replaced by the state before it
-// (from S0 on; what is left after the last goes to S_final), the adjoints' by the adjoint after it, backwards (from
+// (from S0 on; what is left after the last goes to S_final), the adjoints' (z = 1) by the adjoint after it, backwards (from
 // dS_final to dS0).  Sixteen chunks' values are asked for together: their latency is what this takes.
-template <bool ADJOINT>
 __global__ void __launch_bounds__(128) mesa_ssm_scan_kernel(SsmArgs a, SsmWorkspace ws, int NC) {
   constexpr int AHEAD = 16;
+  const bool adjoint = blockIdx.z == 1;
   const int n4 = a.dv * a.dk / 4, e = blockIdx.x * 128 + threadIdx.x, u = blockIdx.y;
   may_follow();
   ahead_done();
   if (e >= n4) return;
-  const float4 *from = reinterpret_cast<const float4 *>(ADJOINT ? a.dS_final : a.S0);
-  float4 *to = reinterpret_cast<float4 *>(ADJOINT ? a.dS0 : a.S_final);
-  float4 *x = reinterpret_cast<float4 *>(ADJOINT ? ws.R : ws.S) + (size_t)u * NC * n4 + e;
+  const float4 *from = reinterpret_cast<const float4 *>(adjoint ? a.dS_final : a.S0);
+  float4 *to = reinterpret_cast<float4 *>(adjoint ? a.dS0 : a.S_final);
+  float4 *x = reinterpret_cast<float4 *>(adjoint ? ws.R : ws.S) + (size_t)u * NC * n4 + e;
   const float *decay = ws.decay + (size_t)u * NC;
   float4 s = from ? from[(size_t)u * n4 + e] : make_float4(0, 0, 0, 0);
   for (int c0 = 0; c0 < NC; c0 += AHEAD) {
@@ -74,7 +78,7 @@ __global__ void __launch_bounds__(128) mesa_ssm_scan_kernel(SsmArgs a, SsmWorksp
     float w[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; i++) {
-      const int c = ADJOINT ? NC - 1 - c0 - i : c0 + i;
+      const int c = adjoint ? NC - 1 - c0 - i : c0 + i;
       if (c0 + i < NC) {
         d[i] = x[(size_t)c * n4];
         w[i] = decay[c];
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(128) mesa_ssm_scan_kernel(SsmArgs a, SsmWorksp
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; i++) {
-      const int c = ADJOINT ? NC - 1 - c0 - i : c0 + i;
+      const int c = adjoint ? NC - 1 - c0 - i : c0 + i;
       if (c0 + i < NC) {
         x[(size_t)c * n4] = s;
         s = make_float4(fmaf(w[i], s.x, d[i].x), fmaf(w[i], s.y, d[i].y), fmaf(w[i], s.z, d[i].z), fmaf(w[i], s.w, d[i].w));
@@ -150,19 +154,17 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWo
 
 template <int DK, int DV>
 struct States {
-  static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, bool adjoint, bool first, cudaStream_t st) {
+  static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, bool adjoints, cudaStream_t st) {
     const size_t smem = sizeof(float) * C * (DK + DV + 8);
-    const dim3 grid(NC, a.units());
+    const int n = adjoints ? 2 : 1;
     timing_mark_begin(K_SSM_STATES, st);
-    const bool ok = adjoint ? launch(mesa_ssm_states_kernel<DK, DV, true>, grid, smem, false, st, a, ws)
-                            : launch(mesa_ssm_states_kernel<DK, DV, false>, grid, smem, first, st, a, ws);
+    bool ok = launch(mesa_ssm_states_kernel<DK, DV>, dim3(NC, a.units(), n), smem, ws.clear, st, a, ws);
     timing_mark_end(K_SSM_STATES, st);
     if (!ok) return -1;
-    const dim3 elements((a.dv * a.dk / 4 + 127) / 128, a.units());
     timing_mark_begin(K_SSM_SCAN, st);
-    const bool done = launch_after(adjoint ? mesa_ssm_scan_kernel<true> : mesa_ssm_scan_kernel<false>, elements, 128, 0, st, a, ws, NC);
+    ok = launch_after(mesa_ssm_scan_kernel, dim3((a.dv * a.dk / 4 + 127) / 128, a.units(), n), 128, 0, st, a, ws, NC);
     timing_mark_end(K_SSM_SCAN, st);
-    return done && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
+    return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
   }
 };
 template <int DK, int DV>
@@ -178,17 +180,18 @@ struct Out {
 
 }  // namespace
 
-// The states before every chunk (adjoint: the adjoints after every chunk); first: the call begins with it.
-int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoint, bool first, cudaStream_t st) {
-  return by_size<States>(a.dk, a.dv, a, ws, (a.T + C - 1) / C, adjoint, first, st);
+// The states before every chunk; with adjoints those after every chunk, too.
+int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoints, cudaStream_t st) {
+  return by_size<States>(a.dk, a.dv, a, ws, (a.T + C - 1) / C, adjoints, st);
 }
 
-int launch_ssm_forward(const SsmArgs &a, const SsmWorkspace &ws, cudaStream_t st) {
+int launch_ssm_forward(const SsmArgs &a, SsmWorkspace ws, cudaStream_t st) {
   const int NC = (a.T + C - 1) / C;
-  // outputs of one chunk come before its state where S_final is S0's memory
-  if (NC == 1 && by_size<Out>(a.dk, a.dv, a, ws, NC, st) != 0) return -1;
-  if ((NC > 1 || a.S_final) && launch_ssm_states(a, ws, false, NC > 1, st) != 0) return -1;
-  return NC == 1 ? 0 : by_size<Out>(a.dk, a.dv, a, ws, NC, st);
+  ws.clear = NC > 1;
+  if (NC > 1) return launch_ssm_states(a, ws, false, st) == 0 ? by_size<Out>(a.dk, a.dv, a, ws, NC, st) : -1;
+  // outputs of one chunk come before its state: S_final may be S0's memory
+  if (cudaMemsetAsync(a.status, 0, sizeof(unsigned), st) != cudaSuccess || by_size<Out>(a.dk, a.dv, a, ws, NC, st) != 0) return -1;
+  return a.S_final ? launch_ssm_states(a, ws, false, st) : 0;
 }
 
 // ---- the decode step -------------------------------------------------------------------------------

@@ -39,6 +39,7 @@ struct SsmWorkspace {
   float *decay = nullptr;  // [U, NC] what is left of a state after each chunk
   float *sums = nullptr;   // [3][U, NC] what each chunk adds to dA, dbias, dskip
   float *dqp = nullptr, *dkp = nullptr;  // [U, T, dk] per-unit dq, dk (nullptr when every head has its own q, k)
+  bool clear = false;      // the states' kernel is the call's first: it clears the status word
 };
 
 struct SsmStepArgs {
@@ -51,8 +52,8 @@ struct SsmStepArgs {
 };
 
 // Each returns 0 when every launch was enqueued, -1 otherwise.
-int launch_ssm_forward(const SsmArgs &a, const SsmWorkspace &ws, cudaStream_t st);
-int launch_ssm_backward(const SsmArgs &a, const SsmWorkspace &ws, cudaStream_t st);
+int launch_ssm_forward(const SsmArgs &a, SsmWorkspace ws, cudaStream_t st);
+int launch_ssm_backward(const SsmArgs &a, SsmWorkspace ws, cudaStream_t st);
 int launch_ssm_step(const SsmStepArgs &a, cudaStream_t st);
 // The tensor-core path (bf16, dk = 128, dv 64 or 128).
 size_t ssm_tc_workspace(int U, int T, int dv);

@@ -20,7 +20,7 @@ namespace mesa {
 
 using namespace ssm;
 
-int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoint, bool first, cudaStream_t st);
+int launch_ssm_states(const SsmArgs &a, const SsmWorkspace &ws, bool adjoints, cudaStream_t st);
 
 namespace {
 
@@ -279,10 +279,10 @@ int launch_ssm_group_sum(const SsmArgs &a, const float *dqp, const float *dkp, c
   return launch_rule_group_sum(r, dqp, dkp, st);
 }
 
-int launch_ssm_backward(const SsmArgs &a, const SsmWorkspace &ws, cudaStream_t st) {
+int launch_ssm_backward(const SsmArgs &a, SsmWorkspace ws, cudaStream_t st) {
   const int NC = (a.T + C - 1) / C;
-  if (launch_ssm_states(a, ws, false, true, st) != 0 || launch_ssm_states(a, ws, true, false, st) != 0) return -1;
-  if (by_size<Grads>(a.dk, a.dv, a, ws, NC, st) != 0) return -1;
+  ws.clear = true;
+  if (launch_ssm_states(a, ws, true, st) != 0 || by_size<Grads>(a.dk, a.dv, a, ws, NC, st) != 0) return -1;
   if (ws.dqp && launch_ssm_group_sum(a, ws.dqp, ws.dkp, st) != 0) return -1;
   return launch_ssm_param_sums(a, ws.sums, NC, st);
 }

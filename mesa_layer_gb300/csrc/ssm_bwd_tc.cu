@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(576, 1)
   using O = Grad<P>;
   extern __shared__ __align__(1024) uint8_t sm[];
   if (tc::smem_u32(sm) & 1023) {  // (swizzled tiles need it; the declaration asks for it)
+    ahead_done();
     if (threadIdx.x == 0) atomicOr(a.status, tc::kErrMmaTimeout);
     return;
   }

@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(L) mesa_ssm_gates_kernel(SsmArgs a, float *rec
   __shared__ int ts[2][4];
   const int u = blockIdx.y, h = u % a.H, t = threadIdx.x, w = t >> 5, lane = t & 31;
   may_follow();
+  if (t == 0 && u == 0 && blockIdx.x == 0) *a.status = 0;  // (the call's first kernel; those after it report)
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f, A = a.A[h];
   float step[2];
   Two l[2];
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(576, 1)
                                const __grid_constant__ CUtensorMap mapO) {
   extern __shared__ __align__(1024) uint8_t sm[];
   if (tc::smem_u32(sm) & 1023) {  // (swizzled tiles need it; the declaration asks for it)
+    ahead_done();
     if (threadIdx.x == 0) atomicOr(a.status, tc::kErrMmaTimeout);
     return;
   }
@@ -409,6 +411,7 @@ __global__ void __launch_bounds__(448, 1)
   constexpr bool ADJ = MODE == kAdjoint || MODE == kAdjointSegment, KEEP = MODE == kKeep || MODE == kAdjoint;
   extern __shared__ __align__(1024) uint8_t sm[];
   if (tc::smem_u32(sm) & 1023) {
+    ahead_done();
     if (threadIdx.x == 0) atomicOr(a.status, tc::kErrMmaTimeout);
     return;
   }
