@@ -637,6 +637,15 @@ def mesa_block_norm_backward(x, y, dx_out, dh=None, gate=None, w_post=None, res_
     return dx, dy, dgate, dw_post, dres_scale, dw_pre
 
 
+def _launch_stream(stream, device):
+    """_raw_stream for kernels that are launched on the current device: it has to be the tensors' (the default stream
+    is a handle that every device has)."""
+    index = device.index
+    if torch._C._cuda_getDevice() != index or (stream is not None and stream.device_index != index):
+        raise MesaError(f"the tensors are on {device}: make it the current device, and give a stream of it")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
 def _starts(starts, shape, device):
     """Check the marks of the documents' first tokens (bool or uint8, or None)."""
     if starts is not None:
@@ -681,7 +690,7 @@ def mesa_ssm_forward_chunked(q, k, v, dt, A, dt_bias=None, skip=None, starts=Non
     workspace = _workspace(workspace, int(lib.mesa_ssm_workspace_size(B, H, Hk, T, dk, dv, code)), q.device, stream)
     _check(lib.mesa_ssm_forward_chunked(B, H, Hk, T, dk, dv, code, _at(q), _at(k), _at(v), _at(dt), _at(A), _at(dt_bias),
                                         _at(skip), _at(starts), _at(out), _at(S0), _at(S_final), _at(workspace),
-                                        workspace.numel(), _raw_stream(stream, q.device)), "mesa_ssm_forward_chunked")
+                                        workspace.numel(), _launch_stream(stream, q.device)), "mesa_ssm_forward_chunked")
     return out
 
 
@@ -730,7 +739,7 @@ def mesa_ssm_backward_chunked(q, k, v, dt, A, dout, dt_bias=None, skip=None, sta
     _check(lib.mesa_ssm_backward_chunked(B, H, Hk, T, dkk, dvv, code, _at(q), _at(k), _at(v), _at(dt), _at(A),
                                          _at(dt_bias), _at(skip), _at(starts), _at(dout), _at(S0), _at(dS_final), _at(dq),
                                          _at(dk), _at(dv), _at(ddt), _at(dA), _at(ddt_bias), _at(dskip), _at(dS0),
-                                         _at(workspace), workspace.numel(), _raw_stream(stream, dev)),
+                                         _at(workspace), workspace.numel(), _launch_stream(stream, dev)),
            "mesa_ssm_backward_chunked")
     return dq, dk, dv, ddt, dA, ddt_bias, dskip
 
@@ -751,7 +760,7 @@ def mesa_ssm_step(S_state, q, k, v, dt, A, dt_bias=None, skip=None, out=None, st
                  (A, "A", f32, heads), (dt_bias, "dt_bias", f32, heads), (skip, "skip", f32, heads),
                  (S_state, "S_state", f32, (N, H, dv, dk)), (out, "out", dtype, vshape))
     _check(lib.mesa_ssm_step(N, H, Hk, dk, dv, code, _at(S_state), _at(q), _at(k), _at(v), _at(dt), _at(A), _at(dt_bias),
-                             _at(skip), _at(out), _raw_stream(stream, dev)), "mesa_ssm_step")
+                             _at(skip), _at(out), _launch_stream(stream, dev)), "mesa_ssm_step")
     return out
 
 
@@ -779,7 +788,7 @@ def mesa_causal_conv(x, w, bias=None, silu=True, starts=None, state0=None, state
     _require_all(x.device, (out, "out", x.dtype, x.shape), (state0, "state0", torch.float32, state),
                  (state_final, "state_final", torch.float32, state))
     _check(lib.mesa_causal_conv(B, H, T, d, W, code, bool(silu), _at(x), _at(w), _at(bias), _at(starts), _at(state0),
-                                _at(state_final), _at(out), _raw_stream(stream, x.device)), "mesa_causal_conv")
+                                _at(state_final), _at(out), _launch_stream(stream, x.device)), "mesa_causal_conv")
     return out
 
 
@@ -792,7 +801,7 @@ def mesa_causal_conv_step(x, w, conv_state, bias=None, silu=True, out=None, stre
     out = _like(x, stream) if out is None else out
     _require_all(x.device, (conv_state, "conv_state", torch.float32, (N, H, W - 1, d)), (out, "out", x.dtype, x.shape))
     _check(lib.mesa_causal_conv_step(N, H, d, W, code, bool(silu), _at(x), _at(w), _at(bias), _at(conv_state), _at(out),
-                                     _raw_stream(stream, x.device)), "mesa_causal_conv_step")
+                                     _launch_stream(stream, x.device)), "mesa_causal_conv_step")
     return out
 
 
@@ -818,7 +827,7 @@ def mesa_causal_conv_backward(x, w, dout, bias=None, silu=True, starts=None, dx=
     workspace = _workspace(workspace, int(lib.mesa_causal_conv_backward_workspace_size(B, H, T, d, W)), x.device, stream)
     _check(lib.mesa_causal_conv_backward(B, H, T, d, W, code, bool(silu), _at(x), _at(w), _at(bias), _at(starts), _at(dout),
                                          _at(dx), _at(dw), _at(dbias), _at(workspace), workspace.numel(),
-                                         _raw_stream(stream, x.device)), "mesa_causal_conv_backward")
+                                         _launch_stream(stream, x.device)), "mesa_causal_conv_backward")
     return dx, dw, dbias
 
 
@@ -857,7 +866,7 @@ def mesa_qk_norm_rotary(q, k=None, wq=None, wk=None, inv_freq=None, positions=No
     _require_all(q.device, (q_out, "q_out", q.dtype, q.shape), (k_out, "k_out", q.dtype, (B, Hk, T, d)))
     _check(lib.mesa_qk_norm_rotary(B, H, Hk, T, d, R, code, bool(interleaved), bool(norm), _at(q), _at(k), _at(wq), _at(wk),
                                    _at(inv_freq), _at(positions), int(offset), rot_scale, eps, _at(q_out), _at(k_out),
-                                   _raw_stream(stream, q.device)), "mesa_qk_norm_rotary")
+                                   _launch_stream(stream, q.device)), "mesa_qk_norm_rotary")
     return q_out, k_out
 
 
@@ -891,7 +900,7 @@ def mesa_qk_norm_rotary_backward(q, k, dq_out, dk_out=None, wq=None, wk=None, in
     _check(lib.mesa_qk_norm_rotary_backward(B, H, Hk, T, d, R, code, bool(interleaved), bool(norm), _at(q), _at(k), _at(wq),
                                             _at(wk), _at(inv_freq), _at(positions), int(offset), rot_scale, eps,
                                             _at(dq_out), _at(dk_out), _at(dq), _at(dk), _at(dwq), _at(dwk),
-                                            _at(workspace), workspace.numel(), _raw_stream(stream, dev)),
+                                            _at(workspace), workspace.numel(), _launch_stream(stream, dev)),
            "mesa_qk_norm_rotary_backward")
     return dq, dk, dwq, dwk
 

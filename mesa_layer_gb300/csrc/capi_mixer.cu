@@ -30,8 +30,11 @@ int check_scan(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   return MESA_OK;
 }
 
-// The tensor-core path: bf16, dk = 128, dv 64 or 128.
-bool scan_tc(int dtype, int dk, int dv) { return dtype == MESA_BF16 && dk == 128 && (dv == 64 || dv == 128); }
+// The tensor-core path: bf16, dk = 128 and dv 64 or 128, or both 64.  (us on it, on the CUDA cores, forward / backward:
+// 8 x 16 x 4096, both 64: 92, 700 / 287, 1610.)
+bool scan_tc(int dtype, int dk, int dv) {
+  return dtype == MESA_BF16 && ((dk == 128 && (dv == 64 || dv == 128)) || (dk == 64 && dv == 64));
+}
 
 // Workspace of the CUDA-core path: [status | S | decay], and for the backward [R | sums | per-head dq, dk].
 size_t scan_parts(int B, int H, int Hk, int T, int dk, int dv, bool backward, mesa::SsmWorkspace *ws, char *base) {
@@ -97,7 +100,7 @@ int mesa_ssm_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dt
 size_t mesa_ssm_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   dtype &= ~MESA_GATE_GRADS_F32;  // (the same workspace)
   if (check_scan(B, H, Hk, T, dk, dv, dtype) != MESA_OK) return 0;
-  if (scan_tc(dtype, dk, dv)) return kStatusBytes + mesa::ssm_tc_backward_workspace(B, H, Hk, T, dv);
+  if (scan_tc(dtype, dk, dv)) return kStatusBytes + mesa::ssm_tc_backward_workspace(B, H, Hk, T, dk, dv);
   return scan_parts(B, H, Hk, T, dk, dv, true, nullptr, nullptr);
 }
 

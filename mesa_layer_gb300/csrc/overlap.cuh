@@ -3,7 +3,8 @@
 // A kernel launched with launch_after may start once every CTA of the kernel ahead has called may_follow (or ended): its
 // set-up and its reads of the call's own inputs then run beside that one's tail.  What earlier kernels of the call write
 // may be read, and what they read be written, only after ahead_done, which waits for the end of all of them (at least one
-// thread of every CTA calls it, so that ends come in order).  The first kernel of a call is launched plainly: everything
+// thread of every CTA calls it, so that ends come in order).  A warp with a bounded wait calls it first: the wait's limit
+// counts from there.  The first kernel of a call is launched plainly: everything
 // before the call has ended when it starts.
 #pragma once
 

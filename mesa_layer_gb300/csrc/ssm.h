@@ -55,10 +55,10 @@ struct SsmStepArgs {
 int launch_ssm_forward(const SsmArgs &a, SsmWorkspace ws, cudaStream_t st);
 int launch_ssm_backward(const SsmArgs &a, SsmWorkspace ws, cudaStream_t st);
 int launch_ssm_step(const SsmStepArgs &a, cudaStream_t st);
-// The tensor-core path (bf16, dk = 128, dv 64 or 128).
+// The tensor-core path (bf16, dk = 128 and dv 64 or 128, or both 64).
 size_t ssm_tc_workspace(int U, int T, int dv);
 int launch_ssm_forward_tc(const SsmArgs &a, void *workspace, cudaStream_t st);
-size_t ssm_tc_backward_workspace(int B, int H, int Hk, int T, int dv);
+size_t ssm_tc_backward_workspace(int B, int H, int Hk, int T, int dk, int dv);
 int launch_ssm_backward_tc(const SsmArgs &a, void *workspace, cudaStream_t st);
 // dA, dbias, dskip from n sums a unit, [3][U, n].
 int launch_ssm_param_sums(const SsmArgs &a, const float *sums, int n, cudaStream_t st);

@@ -1,5 +1,5 @@
-// ssm_bwd_tc.cu -- the selective scan's gradients on the tensor cores (bf16, dk = 128, dv 64 or 128; formulas in
-// ssm_bwd.cu, operand formats in ssm_tc.cuh).
+// ssm_bwd_tc.cu -- the selective scan's gradients on the tensor cores (bf16, dk = 128 and dv 64 or 128, or both
+// 64; formulas in ssm_bwd.cu, operand formats in ssm_tc.cuh).
 //
 // Two walks over the chunks (mesa_ssm_chain_tc_kernel) leave the states before and the adjoints after every chunk as
 // bf16 operands S^T, R^T [dk][dv]; then every chunk's gradients come from its rows and these two, chunk by chunk:
@@ -68,7 +68,7 @@ __device__ __forceinline__ void prefetch_bytes(const void *p, uint32_t bytes) {
 
 // A resident CTA per SM over `chunks` chunks of all units, 576 threads: warps 0-15 (lane quarter warp % 4, column
 // quarter warp / 4), 16 products, 17 copies.
-template <int P>
+template <int N, int P>
 __global__ void __launch_bounds__(576, 1)
     mesa_ssm_grads_tc_kernel(SsmArgs a, int NC, int chunks, const float *records, const uint8_t *states, const uint8_t *adjoints,
                              float *sums, float *dqp, float *dkp, const __grid_constant__ CUtensorMap mapQ,
@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(576, 1)
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
+  if (N < DK) clear_halves(sm, 2);
   if (warp == 16) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
   if (tid == 544) {
     for (uint64_t *b : {&m->full1, &m->full2, &m->c1, &m->c2, &m->e, &m->fg, &m->h, &m->drain}) tc::mbar_init(bar(*b), 1);
@@ -111,8 +112,8 @@ __global__ void __launch_bounds__(576, 1)
   int sent1 = 0, sent2 = 0;  // chunks asked for (warp 17)
 
   may_follow();
+  if (warp != 17) ahead_done();
   if (warp < 16) {
-    ahead_done();  // (sums, dqp and dkp may be written)
     const int w = warp & 3, b = warp >> 2, t = 32 * w + lane;  // row t, columns of quarter b
     const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
     uint32_t bad = 0;
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(576, 1)
       auto scaled = [&](uint32_t col, const uint8_t *tile, float s) {  // returns the row's product with the tile's, unscaled
         const u64 s2 = pack2(s, s);
         u64 dot = 0;
+        if (32 * b >= N) return 0.0f;  // (no such channels)
 #pragma unroll
         for (int hh = 0; hh < 2; hh++) {
           float x[16];
@@ -299,13 +301,13 @@ __global__ void __launch_bounds__(576, 1)
       // ---- c (K R^T); the sums so far ----
       need(m->e, par);
       {
-        constexpr int N = P / 4;
-        float x[N];
-        tc::tmem_ld<N>(tl + T_A + N * b, x);
+        constexpr int V = P / 4;
+        float x[V];
+        tc::tmem_ld<V>(tl + T_A + V * b, x);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < N; i++) x[i] *= ct;
-        tc::tmem_st<N>(tl + T_A + N * b, x);
+        for (int i = 0; i < V; i++) x[i] *= ct;
+        tc::tmem_st<V>(tl + T_A + V * b, x);
         if (b <= w) m->rec[w * L + 32 * b + lane] = col;  // (every block is done: the gates have been read)
         tmem_put(tl + T_B + X_ROW + b, row);
         tmem_put(tl + T_B + X_IN + b, x_in);
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(576, 1)
       // ---- dQ, dK ----
       need(m->fg, par);
       auto put = [&](uint32_t col, uint8_t *tile, float *part) {
+        if (32 * b >= N) return;  // (the tiles' second halves stay zero)
         float x[32];
         tc::tmem_ld32(tl + col + 32 * b, x);
         tc::tmem_ld_wait();
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(576, 1)
           if (!part) {
             *reinterpret_cast<uint4 *>(tile + tile_off(t, 4 * b + cc, L)) = o;
           } else if (in) {
-            float4 *dst = reinterpret_cast<float4 *>(part + ((size_t)u * a.T + c * L + t) * DK + 32 * b + 8 * cc);
+            float4 *dst = reinterpret_cast<float4 *>(part + ((size_t)u * a.T + c * L + t) * N + 32 * b + 8 * cc);
             dst[0] = make_float4(x[8 * cc], x[8 * cc + 1], x[8 * cc + 2], x[8 * cc + 3]);
             dst[1] = make_float4(x[8 * cc + 4], x[8 * cc + 5], x[8 * cc + 6], x[8 * cc + 7]);
           }
@@ -348,15 +351,15 @@ __global__ void __launch_bounds__(576, 1)
           if (i >= w) sum += m->rec[i * L + t];
       }
       {
-        constexpr int N = P / 4;
+        constexpr int V = P / 4;
         const float skip = a.skip ? a.skip[h] : 0.0f;
         const u64 step2 = pack2(step, step), skip2 = pack2(skip, skip);
-        float x[N];
-        tc::tmem_ld<N>(tl + T_A + N * b, x);
+        float x[V];
+        tc::tmem_ld<V>(tl + T_A + V * b, x);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int cc = 0; cc < N / 8; cc++) {
-          const uint32_t to = tile_off(t, N / 8 * b + cc, L);
+        for (int cc = 0; cc < V / 8; cc++) {
+          const uint32_t to = tile_off(t, V / 8 * b + cc, L);
           const uint4 g = *reinterpret_cast<const uint4 *>(sm + O::G + to);
           const uint32_t gs[4] = {g.x, g.y, g.z, g.w};
           uint32_t o[4];
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(576, 1)
       if (!need(m->full1, par) || (it > 0 && !need(m->f_done, par ^ 1))) break;
       if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_A, qk + step128(s), kk + step128(s), id, s > 0);
+        for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_A, qk + step128(s), kk + step128(s), id, s > 0);
 #pragma unroll
         for (int s = 0; s < P / 16; s++) tc::mma_f16(tbase + T_B, gk + step128(s), vk + step128(s), id, s > 0);
       }
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(576, 1)
       if (!need(m->a_done, par)) break;
       if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_A, kk + step128(s), rm + step_mn(s), idP, s > 0);
+        for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_A, kk + step128(s), rm + step_mn(s), idP, s > 0);
         tc::mma_commit(bar(m->e));
       }
       if (!need(m->b_done, par)) break;
@@ -459,18 +462,18 @@ __global__ void __launch_bounds__(576, 1)
       tc::bulk_g2s(tc::smem_u32(sm + O::S), states + (size_t)at * V_TILE<P>, V_TILE<P>, bar(m->full2));
     };
     auto fetch_v = [&](int at) {
-      tc::mbar_arrive_expect_tx(bar(m->full1), 2 * QK_TILE + 2 * V_TILE<P>);
+      tc::mbar_arrive_expect_tx(bar(m->full1), 2 * L * N * 2 + 2 * V_TILE<P>);
       tile(O::V, mapV, P, at, m->full1, 0);
     };
     auto fetch_qk = [&](int at) {
-      tile(0, mapQ, DK, at, m->full1, 1);
-      tile(O::K, mapK, DK, at, m->full1, 1);
+      tile(0, mapQ, N, at, m->full1, 1);
+      tile(O::K, mapK, N, at, m->full1, 1);
     };
     auto fetch_g = [&](int at) { tile(O::G, mapG, P, at, m->full1, 0); };
     auto prefetch = [&](int at) {
       const int u = at / NC, y = (at - u * NC) * L, uk = a.qk_unit(u);
 #pragma unroll
-      for (int i = 0; i < 2; i++) prefetch_tile(&mapQ, 64 * i, y, uk), prefetch_tile(&mapK, 64 * i, y, uk);
+      for (int i = 0; i < N / 64; i++) prefetch_tile(&mapQ, 64 * i, y, uk), prefetch_tile(&mapK, 64 * i, y, uk);
 #pragma unroll
       for (int i = 0; i < P / 64; i++) prefetch_tile(&mapV, 64 * i, y, u), prefetch_tile(&mapG, 64 * i, y, u);
       prefetch_bytes(states + (size_t)at * V_TILE<P>, V_TILE<P>);
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(576, 1)
       ok = ok && wait(bar(m->qk_staged), par, limit, gave_up);
       if (!dqp && ok) {
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < N / 64; i++) {
           tensor_s2g_3d(&mapDq, tc::smem_u32(sm) + i * HALF, 64 * i, y, uk);
           tensor_s2g_3d(&mapDk, tc::smem_u32(sm + O::K) + i * HALF, 64 * i, y, uk);
         }
@@ -554,19 +557,19 @@ __global__ void __launch_bounds__(576, 1)
   if (warp == 16) tc::tmem_free(tbase, 512);
 }
 
-template <int P>
+template <int N, int P>
 int grads(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStream_t st) {
   CUtensorMap q{}, k{}, v{}, g{}, dq{}, dk{}, dv{};
   const int shared = a.B * a.Hk, NC = (a.T + L - 1) / L, chunks = a.units() * NC, sms = sm_count();
-  if (!tmap_units_bf16(&q, a.q, shared, a.T, DK) || !tmap_units_bf16(&k, a.k, shared, a.T, DK) ||
+  if (!tmap_units_bf16(&q, a.q, shared, a.T, N) || !tmap_units_bf16(&k, a.k, shared, a.T, N) ||
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&g, a.dout, a.units(), a.T, P) ||
-      !tmap_units_bf16(&dq, a.dq, shared, a.T, DK) || !tmap_units_bf16(&dk, a.dk_out, shared, a.T, DK) ||
+      !tmap_units_bf16(&dq, a.dq, shared, a.T, N) || !tmap_units_bf16(&dk, a.dk_out, shared, a.T, N) ||
       !tmap_units_bf16(&dv, a.dv_out, a.units(), a.T, P) || sms <= 0)
     return -1;
-  if (cudaFuncSetAttribute(mesa_ssm_grads_tc_kernel<P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem<P>) != cudaSuccess)
+  if (cudaFuncSetAttribute(mesa_ssm_grads_tc_kernel<N, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGradSmem<P>) != cudaSuccess)
     return -1;
   timing_mark_begin(K_SSM_GRADS, st);
-  const bool ok = launch_after(mesa_ssm_grads_tc_kernel<P>, chunks < sms ? chunks : sms, 576, kGradSmem<P>, st, a, NC, chunks, sg.records,
+  const bool ok = launch_after(mesa_ssm_grads_tc_kernel<N, P>, chunks < sms ? chunks : sms, 576, kGradSmem<P>, st, a, NC, chunks, sg.records,
                                ws.S, ws.R, ws.sums, ws.dqp, ws.dkp, q, k, v, g, dq, dk, dv);
   timing_mark_end(K_SSM_GRADS, st);
   return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
@@ -575,7 +578,7 @@ int grads(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStrea
 // [segments, records | S | R | sums | per-head dq, dk]
 size_t parts(const SsmArgs &a, void *workspace, SsmSegments *sg, SsmTcBwd *ws) {
   auto up256 = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t U = a.units(), NC = ((size_t)a.T + L - 1) / L, tiles = U * NC * L * a.dv * 2, part = a.Hk != a.H ? U * a.T * DK * 4 : 0;
+  const size_t U = a.units(), NC = ((size_t)a.T + L - 1) / L, tiles = U * NC * L * a.dv * 2, part = a.Hk != a.H ? U * a.T * a.dk * 4 : 0;
   size_t at;
   const SsmSegments s = ssm_segments(a.units(), a.T, a.dv, true, workspace, &at);
   if (sg) *sg = s;
@@ -595,8 +598,8 @@ size_t parts(const SsmArgs &a, void *workspace, SsmSegments *sg, SsmTcBwd *ws) {
 
 }  // namespace
 
-size_t ssm_tc_backward_workspace(int B, int H, int Hk, int T, int dv) {
-  SsmArgs a{B, H, Hk, T, DK, dv, 1};
+size_t ssm_tc_backward_workspace(int B, int H, int Hk, int T, int dk, int dv) {
+  SsmArgs a{B, H, Hk, T, dk, dv, 1};
   return parts(a, nullptr, nullptr, nullptr);
 }
 
@@ -605,7 +608,7 @@ int launch_ssm_backward_tc(const SsmArgs &a, void *workspace, cudaStream_t st) {
   SsmTcBwd ws;
   parts(a, workspace, &sg, &ws);
   if (launch_ssm_gates(a, sg, st) != 0 || launch_ssm_chains_tc(a, sg, ws, st) != 0) return -1;
-  if ((a.dv == 128 ? grads<128>(a, sg, ws, st) : grads<64>(a, sg, ws, st)) != 0) return -1;
+  if ((a.dk == 64 ? grads<64, 64>(a, sg, ws, st) : a.dv == 128 ? grads<128, 128>(a, sg, ws, st) : grads<128, 64>(a, sg, ws, st)) != 0) return -1;
   if (ws.dqp && launch_ssm_group_sum(a, ws.dqp, ws.dkp, st) != 0) return -1;
   return launch_ssm_param_sums(a, ws.sums, 4 * ((a.T + L - 1) / L), st);
 }

@@ -1,5 +1,5 @@
-// ssm_tc.cu -- the selective state space scan's forward on the tensor cores (bf16, dk = 128, dv 64 or 128; the operand
-// formats are in ssm_tc.cuh).
+// ssm_tc.cu -- the selective state space scan's forward on the tensor cores (bf16, dk = 128 and dv 64 or 128, or both 64; the
+// operand formats are in ssm_tc.cuh).
 //
 // In a chunk of 128 tokens, S the state before it, f_i the decay from before the chunk to token i, E_ij from token j to i:
 //     O = f (Q S^T) + M V + skip V,   M = (Q K^T) o E D,     S' = f_end S + (w V)^T K, w_j = E_{end,j} D_j.
@@ -104,7 +104,7 @@ constexpr uint32_t kFwdSmem = Fwd<P>::MISC + sizeof(FwdMisc);
 static_assert(kFwdSmem<128> <= 232448, "shared memory per block");
 
 // grid (U, segments), 576 threads.
-template <int P>
+template <int N, int P>
 __global__ void __launch_bounds__(576, 1)
     mesa_ssm_forward_tc_kernel(SsmArgs a, SsmSegments sg, const float *records, const __grid_constant__ CUtensorMap mapQ,
                                const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(576, 1)
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
+  if (N < DK) clear_halves(sm, 4);
   if (warp == 16) tc::tmem_alloc(tc::smem_u32(&m->tmem), 512);
   if (tid == 544) {
     for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->g_full, &m->y_full, &m->cs_done, &m->drain})
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(576, 1)
   const int t = tid & 127, w = warp & 3;  // token, or lane of the state
   const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
 
-  if (warp < 16) ahead_done();  // (the records, the segments' states; the copies are of the call's inputs)
+  if (warp != 17) ahead_done();  // (the records, the segments' states; the copies are of the call's inputs)
   if (warp < 4) {
     // ---- M ----
     const float *r = record(records, u, NCT, c0);
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(576, 1)
   } else if (warp < 16) {
     // ---- the state, then K's rows weighed: two warps for each 32 lanes (rows), half of the columns each ----
     const int hf = warp < 12 ? 0 : 1, h0 = hf * P / 64, h1 = h0 + P / 64;
-    const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
+    const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * N : a.S0 ? a.S0 + (size_t)u * P * N : nullptr;
     const float *r = record(records, u, NCT, c0);
     float next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w], left = r[R_ALL];
     for (int c = 0; c < NC; c++) {
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(576, 1)
         left = r[R_ALL];
       }
       if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
-      state_step(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0, h0, h1);
+      state_step<N>(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0, h0, h1);
       tc::fence_smem_to_async();
       tc::fence_before_sync();
       warp_arrive(m->s_full);
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->w_full);
     }
     if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && a.S_final && seg == sg.n - 1)
-      state_out(tl + T_S, a.S_final + (size_t)u * P * DK, t, h0, h1);
+      state_out<N>(tl + T_S, a.S_final + (size_t)u * P * N, t, h0, h1);
   } else if (warp == 16) {
     // ---- products ----
     const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(576, 1)
         const uint64_t q = tc::kmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
                        k = tc::kmajor_desc(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), L, 0);
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
+        for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
         tc::mma_commit(bar(m->g_full));
       }
       return true;
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(576, 1)
       if (elect_one()) {
         const uint64_t qd = tc::kmajor_desc(q, L, 0);
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
+        for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
         tc::mma_commit(bar(m->cs_done));
       }
       if (!need(m->m_full, ph)) break;
@@ -336,15 +337,16 @@ __global__ void __launch_bounds__(576, 1)
     auto at = [&](uint32_t where, int c) { return tc::smem_u32(sm + where) + (c & 1) * (where == Fwd<P>::V ? V_TILE<P> : QK_TILE); };
     auto fetch_kv = [&](int c) {
       const uint32_t b = bar(m->full[c & 1]);
-      tc::mbar_arrive_expect_tx(b, 2 * QK_TILE + V_TILE<P>);
-      load_tile<DK>(at(Fwd<P>::K, c), &mapK, (c0 + c) * L, uk, b);
+      tc::mbar_arrive_expect_tx(b, 2 * L * N * 2 + V_TILE<P>);
+      load_tile<N>(at(Fwd<P>::K, c), &mapK, (c0 + c) * L, uk, b);
       load_tile<P>(at(Fwd<P>::V, c), &mapV, (c0 + c) * L, u, b);
     };
-    auto fetch_q = [&](int c) { load_tile<DK>(at(0, c), &mapQ, (c0 + c) * L, uk, bar(m->full[c & 1])); };
+    auto fetch_q = [&](int c) { load_tile<N>(at(0, c), &mapQ, (c0 + c) * L, uk, bar(m->full[c & 1])); };
     for (; sent < min(NC, 2); sent++) {
       fetch_kv(sent);
       fetch_q(sent);
     }
+    ahead_done();
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1, par = (c >> 1) & 1;
       if (!(ok = wait(bar(m->y_staged[ph]), par, limit, gave_up))) break;
@@ -404,7 +406,7 @@ constexpr uint32_t kChainSmem = Chain<P>::MISC + sizeof(ChainMisc);
 
 // grid (U, segments (from 1 on for adjoint segments, all but the last for segments)), 448 threads: warps 0-7 weigh
 // rows, 8-11 the state, 12 products, 13 copies.  kept: [U, NC][V_TILE] operand tiles.
-template <int P, int MODE>
+template <int N, int P, int MODE>
 __global__ void __launch_bounds__(448, 1)
     mesa_ssm_chain_tc_kernel(SsmArgs a, SsmSegments sg, const float *records, uint8_t *kept, const __grid_constant__ CUtensorMap mapK,
                              const __grid_constant__ CUtensorMap mapV) {
@@ -423,6 +425,7 @@ __global__ void __launch_bounds__(448, 1)
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
+  if (N < DK) clear_halves(sm, 4);  // (the rests', too)
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&m->tmem), 128);
   if (tid == 416) {
     for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->kept, &m->drain}) tc::mbar_init(bar(*b), 1);
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(448, 1)
   const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
 
   may_follow();
-  if (warp < 12) ahead_done();  // (the records, the segments' states; the copies are of the call's inputs)
+  if (warp != 13) ahead_done();  // (the records, the segments' states; the copies are of the call's inputs)
   if (warp < 8) {
     const int hf = warp >> 2;  // two warps for each 32 rows, half of the columns each
     auto weight = [&](int c) {
@@ -470,9 +473,9 @@ __global__ void __launch_bounds__(448, 1)
     }
   } else if (warp < 12) {
     const float *from = nullptr;
-    if constexpr (MODE == kKeep) from = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * DK : a.S0 ? a.S0 + (size_t)u * P * DK : nullptr;
+    if constexpr (MODE == kKeep) from = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * N : a.S0 ? a.S0 + (size_t)u * P * N : nullptr;
     if constexpr (MODE == kAdjoint)
-      from = sg.n > 1 ? sg.R + ((size_t)u * sg.n + seg) * P * DK : a.dS_final ? a.dS_final + (size_t)u * P * DK : nullptr;
+      from = sg.n > 1 ? sg.R + ((size_t)u * sg.n + seg) * P * N : a.dS_final ? a.dS_final + (size_t)u * P * N : nullptr;
     float next = record(records, u, NCT, chunk(0))[R_ALL], left = 1.0f;  // (left: of a state, after the segment)
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
@@ -481,16 +484,16 @@ __global__ void __launch_bounds__(448, 1)
       left *= all;
       if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
       if (KEEP && c > 0 && !need(m->kept, (c - 1) & 1)) break;  // (the last tile has left)
-      state_step(tl + T_G, KEEP ? sm + Chain<P>::S : nullptr, t, all, c == 0, from, 0, P / 32);
+      state_step<N>(tl + T_G, KEEP ? sm + Chain<P>::S : nullptr, t, all, c == 0, from, 0, P / 32);
       if (KEEP) tc::fence_smem_to_async();
       tc::fence_before_sync();
       warp_arrive(m->s_full);
     }
     float *to = nullptr;
-    if constexpr (MODE == kSegment) to = sg.S + ((size_t)u * sg.n + seg) * P * DK;
-    if constexpr (MODE == kAdjointSegment) to = sg.R + ((size_t)u * sg.n + seg) * P * DK;
-    if constexpr (MODE == kAdjoint) to = a.dS0 && seg == 0 ? a.dS0 + (size_t)u * P * DK : nullptr;
-    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && to) state_out(tl + T_G, to, t, 0, P / 32);
+    if constexpr (MODE == kSegment) to = sg.S + ((size_t)u * sg.n + seg) * P * N;
+    if constexpr (MODE == kAdjointSegment) to = sg.R + ((size_t)u * sg.n + seg) * P * N;
+    if constexpr (MODE == kAdjoint) to = a.dS0 && seg == 0 ? a.dS0 + (size_t)u * P * N : nullptr;
+    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && to) state_out<N>(tl + T_G, to, t, 0, P / 32);
     if (!KEEP && t == 0) sg.decay[(size_t)u * sg.n + seg] = left;
   } else if (warp == 12) {
     const uint32_t idS = idesc_bf16(128, P, true, true);
@@ -515,12 +518,13 @@ __global__ void __launch_bounds__(448, 1)
     const int uk = a.qk_unit(u);
     auto fetch = [&](int c) {
       const uint32_t ph = c & 1, b = bar(m->full[ph]);
-      tc::mbar_arrive_expect_tx(b, QK_TILE + V_TILE<P>);
-      load_tile<DK>(tc::smem_u32(sm + ph * QK_TILE), &mapK, chunk(c) * L, uk, b);
+      tc::mbar_arrive_expect_tx(b, L * N * 2 + V_TILE<P>);
+      load_tile<N>(tc::smem_u32(sm + ph * QK_TILE), &mapK, chunk(c) * L, uk, b);
       load_tile<P>(tc::smem_u32(sm + Chain<P>::V + ph * V_TILE<P>), &mapV, chunk(c) * L, u, b);
       sent++;
     };
     for (int c = 0; c < min(NC, 2); c++) fetch(c);
+    ahead_done();
     for (int c = 0; c < NC; c++) {
       if (KEEP) {
         if (!(ok = wait(bar(m->s_full), c & 1, limit, gave_up))) break;
@@ -602,44 +606,44 @@ bool launch_tc(int kind, K kernel, dim3 grid, int threads, uint32_t smem, cudaSt
 
 bool launch_join(const SsmArgs &a, const SsmSegments &sg, bool adjoint, cudaStream_t st) {
   timing_mark_begin(K_SSM_SCAN, st);
-  const bool ok = launch_after(mesa_ssm_join_kernel, dim3(a.dv * DK / 512, a.units()), 128, 0, st, a, sg, adjoint);
+  const bool ok = launch_after(mesa_ssm_join_kernel, dim3((a.dv * a.dk / 4 + 127) / 128, a.units()), 128, 0, st, a, sg, adjoint);
   timing_mark_end(K_SSM_SCAN, st);
   return ok;
 }
-template <int P, int MODE>
+template <int N, int P, int MODE>
 bool launch_chain(const SsmArgs &a, const SsmSegments &sg, uint8_t *kept, const CUtensorMap &k, const CUtensorMap &v, cudaStream_t st) {
   const int n = MODE == kSegment || MODE == kAdjointSegment ? sg.n - 1 : sg.n;
-  return launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<P, MODE>, dim3(a.units(), n), 448, kChainSmem<P>, st, a, sg, sg.records, kept, k,
+  return launch_tc(K_SSM_CHAIN, mesa_ssm_chain_tc_kernel<N, P, MODE>, dim3(a.units(), n), 448, kChainSmem<P>, st, a, sg, sg.records, kept, k,
                    v);
 }
 
-template <int P>
+template <int N, int P>
 int forward(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
   CUtensorMap q{}, k{}, v{}, o{};
-  if (!tmap_units_bf16(&q, a.q, a.B * a.Hk, a.T, DK) || !tmap_units_bf16(&k, a.k, a.B * a.Hk, a.T, DK) ||
+  if (!tmap_units_bf16(&q, a.q, a.B * a.Hk, a.T, N) || !tmap_units_bf16(&k, a.k, a.B * a.Hk, a.T, N) ||
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&o, a.out, a.units(), a.T, P))
     return -1;
   if (sg.n > 1) {
-    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st) || !launch_join(a, sg, false, st)) return -1;
+    if (!launch_chain<N, P, kSegment>(a, sg, nullptr, k, v, st) || !launch_join(a, sg, false, st)) return -1;
   }
-  return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<P>, dim3(a.units(), sg.n), 576, kFwdSmem<P>, st, a, sg, sg.records, q, k,
+  return launch_tc(K_SSM_FORWARD, mesa_ssm_forward_tc_kernel<N, P>, dim3(a.units(), sg.n), 576, kFwdSmem<P>, st, a, sg, sg.records, q, k,
                    v, o)
              ? 0
              : -1;
 }
 
 // The states before every chunk and the adjoints after it.
-template <int P>
+template <int N, int P>
 int chains(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStream_t st) {
   CUtensorMap q{}, k{}, v{}, g{};
-  if (!tmap_units_bf16(&q, a.q, a.B * a.Hk, a.T, DK) || !tmap_units_bf16(&k, a.k, a.B * a.Hk, a.T, DK) ||
+  if (!tmap_units_bf16(&q, a.q, a.B * a.Hk, a.T, N) || !tmap_units_bf16(&k, a.k, a.B * a.Hk, a.T, N) ||
       !tmap_units_bf16(&v, a.v, a.units(), a.T, P) || !tmap_units_bf16(&g, a.dout, a.units(), a.T, P))
     return -1;
   if (sg.n > 1) {
-    if (!launch_chain<P, kSegment>(a, sg, nullptr, k, v, st) || !launch_join(a, sg, false, st)) return -1;
-    if (!launch_chain<P, kAdjointSegment>(a, sg, nullptr, q, g, st) || !launch_join(a, sg, true, st)) return -1;
+    if (!launch_chain<N, P, kSegment>(a, sg, nullptr, k, v, st) || !launch_join(a, sg, false, st)) return -1;
+    if (!launch_chain<N, P, kAdjointSegment>(a, sg, nullptr, q, g, st) || !launch_join(a, sg, true, st)) return -1;
   }
-  return launch_chain<P, kKeep>(a, sg, ws.S, k, v, st) && launch_chain<P, kAdjoint>(a, sg, ws.R, q, g, st) ? 0 : -1;
+  return launch_chain<N, P, kKeep>(a, sg, ws.S, k, v, st) && launch_chain<N, P, kAdjoint>(a, sg, ws.R, q, g, st) ? 0 : -1;
 }
 
 }  // namespace
@@ -678,10 +682,10 @@ int launch_ssm_gates(const SsmArgs &a, const SsmSegments &sg, cudaStream_t st) {
 int launch_ssm_forward_tc(const SsmArgs &a, void *workspace, cudaStream_t st) {
   const SsmSegments sg = ssm_segments(a.units(), a.T, a.dv, false, workspace, nullptr);
   if (launch_ssm_gates(a, sg, st) != 0) return -1;
-  return a.dv == 128 ? forward<128>(a, sg, st) : forward<64>(a, sg, st);
+  return a.dk == 64 ? forward<64, 64>(a, sg, st) : a.dv == 128 ? forward<128, 128>(a, sg, st) : forward<128, 64>(a, sg, st);
 }
 int launch_ssm_chains_tc(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStream_t st) {
-  return a.dv == 128 ? chains<128>(a, sg, ws, st) : chains<64>(a, sg, ws, st);
+  return a.dk == 64 ? chains<64, 64>(a, sg, ws, st) : a.dv == 128 ? chains<128, 128>(a, sg, ws, st) : chains<128, 64>(a, sg, ws, st);
 }
 size_t ssm_tc_workspace(int U, int T, int dv) {
   size_t n;

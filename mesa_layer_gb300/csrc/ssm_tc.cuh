@@ -1,11 +1,13 @@
-// ssm_tc.cuh -- what the tensor-core kernels of the selective scan share (bf16, dk = 128, dv = P in {64, 128}, chunks of
-// L = 128 tokens).
+// ssm_tc.cuh -- what the tensor-core kernels of the selective scan share (bf16, dk = N = 128 and dv = P in {64, 128}, or N =
+// P = 64; chunks of L = 128 tokens).
 //
 // Rows of q, k, v (and of the output's gradient) are bf16 operands as they come from memory.  What is formed on the way
 // is rounded to bf16 where only bf16 outputs depend on it (the pairs' weights M, the state as an operand: 2^-9 of a
 // term each, as much as the output's own rounding), and to two bf16 values (2^-17) where it enters a state, which is
 // fp32 in tensor memory from chunk to chunk.  bf16 has fp32's range, so no scales are needed.
-// States lie transposed, S^T [dk lanes][dv columns]: the same 128 lanes for either dv.
+// States lie transposed, S^T [dk lanes][dv columns]: the same 128 lanes for every size.  N = 64 uses tiles of 128 columns
+// whose second half is zero from the start and stays so (a gradient put there is zero, too): half of the products is
+// idle, but the memory's share of a chunk is the longer one.
 #pragma once
 
 #include "gated_delta_tc.cuh"
@@ -26,7 +28,7 @@ using rule::tensor_s2g_3d;
 using rule::tile_off;
 using rule::wait;
 
-constexpr int L = 128, DK = 128;
+constexpr int L = 128, DK = 128;                      // tokens of a chunk; columns of a q or k tile, lanes of the state
 constexpr uint32_t QK_TILE = L * DK * 2;              // 128 rows of 128 bf16: two halves of 64 columns
 constexpr uint32_t HALF = L * 64 * 2;
 template <int P>
@@ -84,6 +86,7 @@ __device__ __forceinline__ void weigh_row(uint8_t *tile, uint8_t *rest, int t, f
 
 // Columns 32 h0 .. 32 h1 - 1 of lane n of the state in tensor memory (from global memory [P][dk], or zero, where `first`)
 // become the operand row n at `op` (nullptr: none), and are multiplied by `all` where they lie.
+template <int N>
 __device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, float all, bool first, const float *S0, int h0, int h1) {
   const u64 all2 = pack2(all, all);
 #pragma unroll 1
@@ -91,7 +94,7 @@ __device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, floa
     float x[32];
     if (first) {
 #pragma unroll
-      for (int i = 0; i < 32; i++) x[i] = S0 ? S0[(size_t)(32 * h + i) * DK + n] : 0.0f;
+      for (int i = 0; i < 32; i++) x[i] = S0 && n < N ? S0[(size_t)(32 * h + i) * N + n] : 0.0f;
     } else {
       tc::tmem_ld32(tS + 32 * h, x);
       tc::tmem_ld_wait();
@@ -109,6 +112,7 @@ __device__ __forceinline__ void state_step(uint32_t tS, uint8_t *op, int n, floa
   }
   tc::tmem_st_wait();
 }
+template <int N>
 __device__ __forceinline__ void state_out(uint32_t tS, float *dst, int n, int h0, int h1) {
 #pragma unroll 1
   for (int h = h0; h < h1; h++) {
@@ -116,8 +120,16 @@ __device__ __forceinline__ void state_out(uint32_t tS, float *dst, int n, int h0
     tc::tmem_ld32(tS + 32 * h, x);
     tc::tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 32; i++) dst[(size_t)(32 * h + i) * DK + n] = x[i];
+    for (int i = 0; i < 32; i++)
+      if (n < N) dst[(size_t)(32 * h + i) * N + n] = x[i];
   }
+}
+
+// Zeros where tiles of 64 channels leave theirs, `n` tiles from `tiles` on, by the whole block.
+__device__ __forceinline__ void clear_halves(uint8_t *tiles, int n) {
+  for (int i = threadIdx.x; i < n * (int)(HALF / 16); i += blockDim.x)
+    *reinterpret_cast<uint4 *>(tiles + (i / (HALF / 16)) * QK_TILE + HALF + (i % (HALF / 16)) * 16) = make_uint4(0, 0, 0, 0);
+  tc::fence_smem_to_async();
 }
 
 // The halves of 64 channels of 128 tokens' rows of unit z, from token y on.

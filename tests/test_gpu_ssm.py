@@ -80,7 +80,8 @@ SIZES = [  # dtype, B, H, Hk, T, dk, dv, packed, states
     (BF16, 2, 2, 1, 47, 64, 64, True, True), (BF16, 1, 2, 2, 31, 32, 128, False, False), (BF16, 1, 1, 1, 1, 128, 128, False, True),
     (BF16, 1, 2, 2, 2, 128, 64, False, False), (BF16, 2, 4, 2, 127, 128, 128, True, True), (BF16, 1, 2, 2, 128, 128, 128, False, True),
     (BF16, 1, 3, 1, 129, 128, 64, False, True), (BF16, 2, 2, 2, 333, 128, 128, True, True), (BF16, 1, 2, 1, 700, 128, 64, True, False),
-    (BF16, 1, 2, 2, 640, 128, 128, False, True), (BF16, 1, 2, 2, 300, 64, 128, False, True), (BF16, 1, 4, 2, 300, 64, 64, True, True),
+    (BF16, 1, 2, 2, 640, 128, 128, False, True), (BF16, 1, 2, 2, 300, 64, 128, False, True), (BF16, 1, 4, 2, 300, 64, 64, True, True), (BF16, 1, 2, 2, 129, 64, 64, False, True),
+    (BF16, 2, 3, 3, 1500, 64, 64, True, True), (BF16, 1, 2, 1, 200, 128, 32, False, True), (BF16, 1, 1, 1, 3000, 128, 128, True, True),
 ]
 
 
@@ -188,7 +189,7 @@ def test_empty_sequences(lib, dtype, d):
     assert torch.equal(dS0, s["dS_final"]) and all(not x.float().abs().sum() for x in r[4:])
 
 
-@pytest.mark.parametrize("dtype,d", [(F32, 64), (BF16, 128)])
+@pytest.mark.parametrize("dtype,d", [(F32, 64), (BF16, 64), (BF16, 128)])
 def test_status_and_units_of_their_own(lib, dtype, d):
     """A NaN is reported and reaches its own unit's later tokens alone."""
     s = make(dtype, 2, 2, 2, 300, d, d, seed=3)
@@ -202,7 +203,24 @@ def test_status_and_units_of_their_own(lib, dtype, d):
     assert out2[1, 0, 200:, 3].isnan().all()
 
 
-@pytest.mark.parametrize("dtype,d", [(F32, 64), (BF16, 128)])
+@pytest.mark.parametrize("dtype,d", [(F32, 32), (BF16, 64), (BF16, 128)])
+def test_gradients_of_units_of_their_own(lib, dtype, d):
+    """A NaN in one unit's value is reported and reaches no other unit's gradients."""
+    B, H, T = 2, 90, 200  # (more chunks than SMs: a CTA takes several units)
+    s = make(dtype, B, H, H, T, d, d, seed=6)
+    args = dict(dt_bias=s["dt_bias"], skip=s["skip"], gates_dtype=F32)
+    ws = torch.empty(lib.mesa_ssm_backward_workspace_size(B, H, H, T, d, d, dtype), dtype=torch.uint8, device="cuda")
+    clean = lib.mesa_ssm_backward_chunked(s["q"], s["k"], s["v"], s["dt"], s["A"], s["dout"], workspace=ws, **args)
+    assert lib.mesa_forward_status_code(ws)[0] == lib.MESA_OK
+    s["v"][0, 3, 17, 5] = torch.nan
+    r = lib.mesa_ssm_backward_chunked(s["q"], s["k"], s["v"], s["dt"], s["A"], s["dout"], workspace=ws, **args)
+    assert lib.mesa_forward_status_code(ws)[0] == lib.MESA_ERR_NONFINITE
+    others = torch.ones(B, H, dtype=torch.bool, device="cuda")
+    others[0, 3] = False
+    assert all(torch.equal(x[others], y[others]) for x, y in zip(clean[:4], r[:4]))
+
+
+@pytest.mark.parametrize("dtype,d", [(F32, 64), (BF16, 64), (BF16, 128)])
 def test_states_in_place_and_nothing_beyond(lib, dtype, d):
     """S_final may be S0's memory; what lies behind each output stays."""
     B, H, T = 1, 3, 261
@@ -244,17 +262,17 @@ def test_captured_and_on_another_stream(lib, dtype, d):
     assert torch.equal(o, want)
 
 
-@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dk,d", [(128, 64), (128, 128), (64, 64)])
 @pytest.mark.parametrize("T", [200, 6000])
-def test_waits_that_give_up_are_reported(lib, d, T):
+def test_waits_that_give_up_are_reported(lib, dk, d, T):
     """On the tensor cores (whole sequences, and in segments): the status says so, the next call is clean."""
-    s = make(BF16, 1, 2, 1, T, 128, d, seed=41, states=True)
+    s = make(BF16, 1, 2, 1, T, dk, d, seed=41, states=True)
     out, S = forward(lib, s)
     args = dict(dt_bias=s["dt_bias"], skip=s["skip"], S0=s["S0"], dS_final=s["dS_final"], gates_dtype=F32)
     scan = (s["q"], s["k"], s["v"], s["dt"], s["A"])
     grads = lib.mesa_ssm_backward_chunked(*scan, s["dout"], **args)
-    ws = torch.empty(lib.mesa_ssm_workspace_size(1, 2, 1, T, 128, d, BF16), dtype=torch.uint8, device="cuda")
-    wb = torch.empty(lib.mesa_ssm_backward_workspace_size(1, 2, 1, T, 128, d, BF16), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(lib.mesa_ssm_workspace_size(1, 2, 1, T, dk, d, BF16), dtype=torch.uint8, device="cuda")
+    wb = torch.empty(lib.mesa_ssm_backward_workspace_size(1, 2, 1, T, dk, d, BF16), dtype=torch.uint8, device="cuda")
     try:
         lib.mesa_debug_set_wait_limit(0)
         forward(lib, s, workspace=ws)

@@ -126,3 +126,19 @@ def test_binding_refuses_host_tensors_and_shapes():
         binding.mesa_causal_conv_step(q, torch.zeros(2, 16, 4), None)
     with pytest.raises(binding.MesaError, match="float32 or bfloat16"):
         binding.mesa_qk_norm_rotary(q.half(), q)
+
+
+def test_another_device_is_refused(monkeypatch):
+    """Kernels go to the current device: tensors (or a stream) of another one are refused before the launch."""
+    class Stream:
+        cuda_stream, device_index = 7, 1
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 5 + i, raising=False)
+    assert binding._launch_stream(None, torch.device("cuda", 0)) == 5
+    with pytest.raises(binding.MesaError, match="current device"):
+        binding._launch_stream(None, torch.device("cuda", 1))
+    with pytest.raises(binding.MesaError, match="current device"):
+        binding._launch_stream(Stream, torch.device("cuda", 0))
+    Stream.device_index = 0
+    assert binding._launch_stream(Stream, torch.device("cuda", 0)) == 7
