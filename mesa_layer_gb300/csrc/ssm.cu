@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, Ss
   __syncthreads();
   float acc[DV / 16][DK / 16];
   zero(acc);
-  mm_tn<C>(acc, v, DV + 4, k, DK + 4, ty, tx);
+  mm_outer<C, DV, DK>(acc, v, DV + 4, k, DK + 4, ty, tx);
   ahead_done();
   if (threadIdx.x == 0 && !adjoint) {
     ws.decay[(size_t)u * NC + c] = g.f[C - 1];
@@ -52,10 +52,19 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, Ss
   }
   float *dst = (adjoint ? ws.R : ws.S) + ((size_t)u * NC + c) * a.dv * a.dk;
 #pragma unroll
-  for (int i = 0; i < DV / 16; i++)
+  for (int i = 0; i < DV / 16; i++) {
+    const int p = frag<DV>(ty, i);
+    if (p >= a.dv) continue;
+    if constexpr (DK >= 64) {  // (dk = DK)
 #pragma unroll
-    for (int j = 0; j < DK / 16; j++)
-      if (ty + 16 * i < a.dv && tx + 16 * j < a.dk) dst[(ty + 16 * i) * a.dk + tx + 16 * j] = acc[i][j];
+      for (int j = 0; j < DK / 16; j += 4)
+        *reinterpret_cast<float4 *>(dst + p * a.dk + frag<DK>(tx, j)) = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < DK / 16; j++)
+        if (frag<DK>(tx, j) < a.dk) dst[p * a.dk + frag<DK>(tx, j)] = acc[i][j];
+    }
+  }
 }
 
 // Four elements of a unit's state a thread, chunk after chunk: what a chunk adds is replaced by the state before it
@@ -101,7 +110,7 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWorkspace ws) {
   extern __shared__ float4 smem4[];
   float *q = reinterpret_cast<float *>(smem4), *k = q + C * (DK + 4), *v = k + C * (DK + 4), *S = v + C * (DV + 4),
-        *M = S + DV * (DK + 4);
+        *M = S + kPart<DV> * (DK + 4);
   __shared__ Gates g;
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -112,7 +121,8 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWo
   load_rows<DV, C>(v, a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   if (threadIdx.x < 32) gates_load(g, a, u, t0, n, threadIdx.x);
   ahead_done();  // (the states)
-  if (state) load_rows<DK, DV>(S, state, 0, 0, a.dv, a.dk);
+  constexpr int PART = kPart<DV>;
+  if (state) load_rows<DK, PART>(S, state, 0, 0, min(a.dv, PART), a.dk);
   __syncthreads();
   {
     float acc[2][2];
@@ -129,12 +139,19 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWo
   }
   float acc[2][DV / 16];
   zero(acc);
-  if (state) mm_nt<DK>(acc, q, DK + 4, S, DK + 4, ty, tx);
+  if (state) mm_nt<DK, 0, PART / 16>(acc, q, DK + 4, S, DK + 4, ty, tx);
+  __syncthreads();
+  if constexpr (PART < DV) {
+    if (state) {
+      load_rows<DK, PART>(S, state, 0, PART, a.dv - PART, a.dk);
+      __syncthreads();
+      mm_nt<DK, PART / 16, PART / 16>(acc, q, DK + 4, S, DK + 4, ty, tx);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 2; i++)
 #pragma unroll
     for (int j = 0; j < DV / 16; j++) acc[i][j] = g.s[ty + 16 * i] < 0 ? acc[i][j] * g.f[ty + 16 * i] : 0.0f;
-  __syncthreads();
   mm_nn<C>(acc, M, LDC, v, DV + 4, ty, tx);
   const float skip = a.skip ? a.skip[u % a.H] : 0.0f;
   bool bad = false;
@@ -170,7 +187,7 @@ struct States {
 template <int DK, int DV>
 struct Out {
   static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (C * (2 * DK + DV + 12) + DV * (DK + 4) + C * LDC);
+    const size_t smem = sizeof(float) * (C * (2 * DK + DV + 12) + kPart<DV> * (DK + 4) + C * LDC);
     timing_mark_begin(K_SSM_OUT, st);
     const bool ok = launch(mesa_ssm_out_kernel<DK, DV>, dim3(NC, a.units()), smem, NC == 1, st, a, ws);
     timing_mark_end(K_SSM_OUT, st);

@@ -33,12 +33,14 @@ __device__ __forceinline__ float sum16(float x) {  // over a row's 16 threads
 // grid (NC, U)
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, SsmWorkspace ws) {
-  constexpr int LK = DK + 4, LV = DV + 4;
+  constexpr int LK = DK + 4, LV = DV + 4, PART = kPart<DV>;
   extern __shared__ float4 smem4[];
   float *q = reinterpret_cast<float *>(smem4), *k = q + C * LK, *v = k + C * LK, *g = v + C * LV, *S = g + C * LV,
-        *M = S + DV * LK, *W = M + C * LDC;
+        *M = S + PART * LK, *W = M + C * LDC;
+  constexpr int LX = C + 1;  // the pairs' terms, in the states' place until these come
+  float *X = S;
   __shared__ Gates ga;
-  __shared__ float X[C][C + 1], x_in[C], x_out[C], duv[C], gv[C], across[kThreads / 32];
+  __shared__ float x_in[C], x_out[C], duv[C], gv[C], pairs[C], across[kThreads / 32];
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0), h = u % a.H;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
   const size_t at = ((size_t)u * NC + c) * a.dv * a.dk;
@@ -48,8 +50,6 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
   load_rows<DV, C>(v, a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   load_rows<DV, C>(g, a.dout, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   if (warp == 0) gates_load(ga, a, u, t0, n, lane);
-  ahead_done();  // (the states and adjoints)
-  load_rows<DK, DV>(S, ws.S + at, 0, 0, a.dv, a.dk);
   __syncthreads();
   {
     float G[2][2], Hm[2][2];
@@ -66,130 +66,116 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
         const float d = ga.decay(r, t), w = on ? Hm[i][j] * d * ga.step[t] : 0.0f;
         M[r * LDC + t] = on ? G[i][j] * d : 0.0f;
         W[r * LDC + t] = w;
-        X[r][t] = on && t < r ? G[i][j] * w : 0.0f;
+        X[r * LX + t] = on && t < r ? G[i][j] * w : 0.0f;
         if (r == t) gv[r] = Hm[i][j];
       }
   }
+  __syncthreads();
+  // X[i][t] <- sum over j < t (a warp: four rows), then for each t the sum over i >= t
+#pragma unroll
+  for (int i = warp; i < C; i += kThreads / 32) {
+    float x = X[i * LX + lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const float before = __shfl_up_sync(0xffffffffu, x, 1);
+    X[i * LX + lane] = lane > 0 ? before : 0.0f;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float x = 0.0f;
+    for (int i = lane; i < C; i++) x += X[i * LX + lane];
+    pairs[lane] = x;
+  }
+  ahead_done();  // (the states and adjoints)
+  __syncthreads();
   const bool own = ws.dqp == nullptr;  // every head has its own q, k
   const size_t krow = (own ? (size_t)a.qk_unit(u) : (size_t)u) * a.T + t0, vrow = (size_t)u * a.T + t0;
   bool bad = false;
-  {
-    float acc[2][DK / 16];
-    zero(acc);
-    mm_nn<DV>(acc, g, LV, S, LK, ty, tx);
+  const float skip = a.skip ? a.skip[h] : 0.0f;
+  float aq[2][DK / 16], ak[2][DK / 16], cross = 0.0f, dots[2] = {0.0f, 0.0f};
+  zero(aq);
+  zero(ak);
+  // the rows of S and R in one or two parts
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int r = ty + 16 * i;
-      const float f = ga.f[r];
-      float x = 0.0f;
-#pragma unroll
-      for (int j = 0; j < DK / 16; j++) {
-        acc[i][j] = ga.s[r] < 0 ? acc[i][j] * f : 0.0f;
-        x = fmaf(acc[i][j], q[r * LK + tx + 16 * j], x);
-      }
-      x = sum16(x);
-      if (tx == 0) x_in[r] = x;
-    }
-    __syncthreads();  // M, W, X
-    mm_nn<C>(acc, W, LDC, k, LK, ty, tx);
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-      for (int j = 0; j < DK / 16; j++)
-        if (ty + 16 * i < n && tx + 16 * j < a.dk) {
-          bad |= !isfinite(acc[i][j]);
-          store(own ? a.dq : ws.dqp, !own || a.dtype == 0, (krow + ty + 16 * i) * a.dk + tx + 16 * j, acc[i][j]);
-        }
-  }
-  {  // R takes S's place
-    constexpr int N4 = DV * DK / 4 / kThreads;
+  for (int p0 = 0; p0 < DV; p0 += PART) {
+    const int rows = min(a.dv - p0, PART);
+    if (p0 > 0) __syncthreads();
+    load_rows<DK, PART>(S, ws.S + at, 0, p0, rows, a.dk);
+    __syncthreads();
+    mm_nn<PART>(aq, g + p0, LV, S, LK, ty, tx);
+    constexpr int N4 = PART * DK / 4 / kThreads;
     float4 r[N4];
-    float x = 0.0f;
 #pragma unroll
     for (int i = 0; i < N4; i++) {
       const int e = tid + i * kThreads, p = e / (DK / 4), cc = 4 * (e % (DK / 4));
-      r[i] = p < a.dv && cc < a.dk ? *reinterpret_cast<const float4 *>(ws.R + at + (size_t)p * a.dk + cc) : make_float4(0, 0, 0, 0);
+      r[i] = p < rows && cc < a.dk ? *reinterpret_cast<const float4 *>(ws.R + at + (size_t)(p0 + p) * a.dk + cc) : make_float4(0, 0, 0, 0);
       const float4 s = *reinterpret_cast<const float4 *>(S + p * LK + cc);
-      x = fmaf(r[i].x, s.x, fmaf(r[i].y, s.y, fmaf(r[i].z, s.z, fmaf(r[i].w, s.w, x))));
+      cross = fmaf(r[i].x, s.x, fmaf(r[i].y, s.y, fmaf(r[i].z, s.z, fmaf(r[i].w, s.w, cross))));
     }
-    x = warp_sum(x);
-    if (lane == 0) across[warp] = x;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N4; i++) {
+    for (int i = 0; i < N4; i++) {  // R takes S's place
       const int e = tid + i * kThreads;
       *reinterpret_cast<float4 *>(S + e / (DK / 4) * LK + 4 * (e % (DK / 4))) = r[i];
     }
-    // X[i][t] <- sum over j < t (a warp: four rows)
-#pragma unroll
-    for (int i = warp; i < C; i += kThreads / 32) {
-      float x = X[i][lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const float before = __shfl_up_sync(0xffffffffu, x, 1);
-      X[i][lane] = lane > 0 ? before : 0.0f;
-    }
     __syncthreads();
-  }
-  const float *R = S;
-  {
-    float acc[2][DK / 16];
+    mm_nn<PART>(ak, v + p0, LV, S, LK, ty, tx);
+    float acc[2][PART / 16];
     zero(acc);
-    mm_nn<DV>(acc, v, LV, R, LK, ty, tx);
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int r = ty + 16 * i;
-      const float w = ga.c[r] * ga.step[r];
-      float x = 0.0f;
-#pragma unroll
-      for (int j = 0; j < DK / 16; j++) {
-        acc[i][j] *= w;
-        x = fmaf(acc[i][j], k[r * LK + tx + 16 * j], x);
-      }
-      x = sum16(x);
-      if (tx == 0) x_out[r] = x;
-    }
-    mm_tn<C>(acc, W, LDC, q, LK, ty, tx);
+    mm_nt<DK>(acc, k, LK, S, LK, ty, tx);
 #pragma unroll
     for (int i = 0; i < 2; i++)
 #pragma unroll
-      for (int j = 0; j < DK / 16; j++)
-        if (ty + 16 * i < n && tx + 16 * j < a.dk) {
-          bad |= !isfinite(acc[i][j]);
-          store(own ? a.dk_out : ws.dkp, !own || a.dtype == 0, (krow + ty + 16 * i) * a.dk + tx + 16 * j, acc[i][j]);
-        }
-  }
-  {
-    const float skip = a.skip ? a.skip[h] : 0.0f;
-    float acc[2][DV / 16];
-    zero(acc);
-    mm_nt<DK>(acc, k, LK, R, LK, ty, tx);
-#pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-      for (int j = 0; j < DV / 16; j++) acc[i][j] *= ga.c[ty + 16 * i];
-    mm_tn<C>(acc, M, LDC, g, LV, ty, tx);
+      for (int j = 0; j < PART / 16; j++) acc[i][j] *= ga.c[ty + 16 * i];
+    mm_tn<C>(acc, M, LDC, g + p0, LV, ty, tx);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const int r = ty + 16 * i;
-      float x = 0.0f;
+      const int row = ty + 16 * i;
 #pragma unroll
-      for (int j = 0; j < DV / 16; j++) {
-        const int p = tx + 16 * j;
-        x = fmaf(acc[i][j], v[r * LV + p], x);
-        if (r < n && p < a.dv) {
-          const float o = ga.step[r] * acc[i][j], y = a.skip ? fmaf(skip, g[r * LV + p], o) : o;
+      for (int j = 0; j < PART / 16; j++) {
+        const int p = p0 + tx + 16 * j;
+        dots[i] = fmaf(acc[i][j], v[row * LV + p], dots[i]);
+        if (row < n && p < a.dv) {
+          const float o = ga.step[row] * acc[i][j], y = a.skip ? fmaf(skip, g[row * LV + p], o) : o;
           bad |= !isfinite(y);
-          store(a.dv_out, a.dtype == 0, (vrow + r) * a.dv + p, y);
+          store(a.dv_out, a.dtype == 0, (vrow + row) * a.dv + p, y);
         }
       }
-      x = sum16(x);
-      if (tx == 0) duv[r] = x;
     }
   }
+  cross = warp_sum(cross);
+  if (lane == 0) across[warp] = cross;
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const int row = ty + 16 * i;
+    const float f = ga.f[row], w = ga.c[row] * ga.step[row], x = sum16(dots[i]);
+    float in = 0.0f, out = 0.0f;
+#pragma unroll
+    for (int j = 0; j < DK / 16; j++) {
+      aq[i][j] = ga.s[row] < 0 ? aq[i][j] * f : 0.0f;
+      ak[i][j] *= w;
+      in = fmaf(aq[i][j], q[row * LK + tx + 16 * j], in);
+      out = fmaf(ak[i][j], k[row * LK + tx + 16 * j], out);
+    }
+    in = sum16(in);
+    out = sum16(out);
+    if (tx == 0) duv[row] = x, x_in[row] = in, x_out[row] = out;
+  }
+  mm_nn<C>(aq, W, LDC, k, LK, ty, tx);
+  mm_tn<C>(ak, W, LDC, q, LK, ty, tx);
+#pragma unroll
+  for (int i = 0; i < 2; i++)
+#pragma unroll
+    for (int j = 0; j < DK / 16; j++)
+      if (ty + 16 * i < n && tx + 16 * j < a.dk) {
+        const size_t to = (krow + ty + 16 * i) * a.dk + tx + 16 * j;
+        bad |= !isfinite(aq[i][j]) || !isfinite(ak[i][j]);
+        store(own ? a.dq : ws.dqp, !own || a.dtype == 0, to, aq[i][j]);
+        store(own ? a.dk_out : ws.dkp, !own || a.dtype == 0, to, ak[i][j]);
+      }
   __syncthreads();
   if (warp == 0) {  // token `lane`
     const int t = lane;
@@ -204,11 +190,9 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
     }
     out = __shfl_up_sync(0xffffffffu, out, 1);
     if (lane == 0) out = 0.0f;
-    float pairs = 0.0f;
-    for (int i = t; i < C; i++) pairs += X[i][t];
     const bool start = ga.s[t] == t;
     const float left = ga.s[C - 1] < 0 ? ga.f[C - 1] * all : 0.0f;
-    const float da = start ? 0.0f : pairs + in + out + left;
+    const float da = start ? 0.0f : pairs[t] + in + out + left;
     const float dstep = fmaf(a.A[h], da, duv[t]);
     const float draw = t < n ? dstep * sigmoid(ga.raw[t]) : 0.0f;
     if (t < n) {
@@ -253,7 +237,7 @@ __global__ void __launch_bounds__(256) mesa_ssm_params_kernel(SsmArgs a, const f
 template <int DK, int DV>
 struct Grads {
   static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, cudaStream_t st) {
-    const size_t smem = sizeof(float) * (2 * C * (DK + 4) + 2 * C * (DV + 4) + DV * (DK + 4) + 2 * C * LDC);
+    const size_t smem = sizeof(float) * (2 * C * (DK + 4) + 2 * C * (DV + 4) + kPart<DV> * (DK + 4) + 2 * C * LDC);
     timing_mark_begin(K_SSM_GRADS, st);
     const bool ok = launch(mesa_ssm_grads_kernel<DK, DV>, dim3(NC, a.units()), smem, false, st, a, ws);
     timing_mark_end(K_SSM_GRADS, st);

@@ -52,17 +52,37 @@ __device__ __forceinline__ void gates_load(Gates &g, const SsmArgs &a, int u, in
   g.c[lane] = lane >= send ? exp2f(two_sub(end, l)) : 0.0f;
 }
 
-// n rows of d channels (fp32 or bf16) to fp32 rows of D channels, stride D + 4, what is missing as zeros.
+// n rows of d channels (fp32 or bf16) to fp32 rows of D channels, stride D + 4, what is missing as zeros.  Eight loads of a
+// thread are in flight together (one after the other, they were most of the time: 543 us of a 2 x 16 x 4096 x 128 fp32
+// forward's outputs, so 000).
 template <int D, int ROWS>
 __device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype, size_t first, int n, int d) {
-  for (int i = threadIdx.x; i < ROWS * (D / 4); i += kThreads) {
-    const int r = i / (D / 4), c = 4 * (i % (D / 4));
-    float4 x = make_float4(0, 0, 0, 0);
-    if (r < n && c < d) {
+  constexpr int PER = ROWS * (D / 4) / kThreads, BATCH = PER < 8 ? PER : 8;
+  static_assert(PER % BATCH == 0 && PER * kThreads == ROWS * (D / 4), "whole batches");
+  const bool bf16 = dtype == 1;
+#pragma unroll
+  for (int i0 = 0; i0 < PER; i0 += BATCH) {
+    uint4 x[BATCH];
+#pragma unroll
+    for (int j = 0; j < BATCH; j++) {
+      const int i = threadIdx.x + (i0 + j) * kThreads, r = i / (D / 4), c = 4 * (i % (D / 4));
       const size_t at = (first + r) * d + c;
-      x = dtype == 1 ? load4(static_cast<const __nv_bfloat16 *>(src), at) : load4(static_cast<const float *>(src), at);
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (r < n && c < d) {
+        if (bf16) {
+          const uint2 y = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(src) + at);
+          x[j].x = y.x, x[j].y = y.y;
+        } else {
+          x[j] = *reinterpret_cast<const uint4 *>(static_cast<const float *>(src) + at);
+        }
+      }
     }
-    *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = x;
+#pragma unroll
+    for (int j = 0; j < BATCH; j++) {
+      const int i = threadIdx.x + (i0 + j) * kThreads, r = i / (D / 4), c = 4 * (i % (D / 4));
+      if (bf16) x[j] = make_uint4(x[j].x << 16, x[j].x & 0xffff0000u, x[j].y << 16, x[j].y & 0xffff0000u);
+      *reinterpret_cast<uint4 *>(dst + r * (D + 4) + c) = x[j];
+    }
   }
 }
 __device__ __forceinline__ void store(void *p, bool f32, size_t i, float x) {
@@ -73,8 +93,8 @@ __device__ __forceinline__ void store(void *p, bool f32, size_t i, float x) {
 }
 
 // Products by 16 x 16 threads (ty, tx): this thread's rows ty + 16 i, columns tx + 16 j.
-// acc += A B^T, A [.][K], B [.][K] (row strides lda, ldb).
-template <int K, int RI, int CJ>
+// acc += A B^T, A [.][K], B [.][K] (row strides lda, ldb); with J0, COLS the columns' share acc[.][J0 ..] of COLS alone.
+template <int K, int J0 = 0, int COLS = 0, int RI, int CJ>
 __device__ __forceinline__ void mm_nt(float (&acc)[RI][CJ], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
 #pragma unroll 4
   for (int k = 0; k < K; k += 4) {
@@ -82,8 +102,8 @@ __device__ __forceinline__ void mm_nt(float (&acc)[RI][CJ], const float *A, int 
 #pragma unroll
     for (int i = 0; i < RI; i++) x[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * lda + k);
 #pragma unroll
-    for (int j = 0; j < CJ; j++) {
-      const float4 y = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * ldb + k);
+    for (int j = J0; j < (COLS ? J0 + COLS : CJ); j++) {
+      const float4 y = *reinterpret_cast<const float4 *>(B + (tx + 16 * (j - J0)) * ldb + k);
 #pragma unroll
       for (int i = 0; i < RI; i++)
         acc[i][j] = fmaf(x[i].w, y.w, fmaf(x[i].z, y.z, fmaf(x[i].y, y.y, fmaf(x[i].x, y.x, acc[i][j]))));
@@ -124,6 +144,38 @@ __device__ __forceinline__ void mm_tn(float (&acc)[RI][CJ], const float *A, int 
       for (int j = 0; j < CJ; j++) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
   }
 }
+// The same where both rows' elements lie side by side: this thread's rows and columns frag<M>(ty, i), frag<N>(tx, j), in
+// groups of four from 64 on (a quarter of the shared-memory instructions).
+template <int D>
+__device__ __forceinline__ int frag(int t, int i) {
+  return D >= 64 ? 64 * (i / 4) + 4 * t + i % 4 : t + 16 * i;
+}
+template <int D>
+__device__ __forceinline__ void load_frag(const float *row, int t, float (&x)[D / 16]) {
+  if constexpr (D >= 64) {
+#pragma unroll
+    for (int g = 0; g < D / 64; g++) {
+      const float4 y = *reinterpret_cast<const float4 *>(row + 64 * g + 4 * t);
+      x[4 * g] = y.x, x[4 * g + 1] = y.y, x[4 * g + 2] = y.z, x[4 * g + 3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 16; i++) x[i] = row[t + 16 * i];
+  }
+}
+template <int K, int M, int N>
+__device__ __forceinline__ void mm_outer(float (&acc)[M / 16][N / 16], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
+#pragma unroll 2
+  for (int k = 0; k < K; k++) {
+    float x[M / 16], y[N / 16];
+    load_frag<M>(A + k * lda, ty, x);
+    load_frag<N>(B + k * ldb, tx, y);
+#pragma unroll
+    for (int i = 0; i < M / 16; i++)
+#pragma unroll
+      for (int j = 0; j < N / 16; j++) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+  }
+}
 template <int RI, int CJ>
 __device__ __forceinline__ void zero(float (&acc)[RI][CJ]) {
 #pragma unroll
@@ -131,6 +183,10 @@ __device__ __forceinline__ void zero(float (&acc)[RI][CJ]) {
 #pragma unroll
     for (int j = 0; j < CJ; j++) acc[i][j] = 0.0f;
 }
+
+// Rows of a state that are in shared memory at a time: two CTAs of the largest size fit an SM then.
+template <int DV>
+constexpr int kPart = DV > 64 ? 64 : DV;
 
 // Sizes are padded to 32, 64 or 128 channels in shared memory (16 to 32).
 template <template <int, int> class F, typename... Args>
