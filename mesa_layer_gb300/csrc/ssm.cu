@@ -33,8 +33,8 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_states_kernel(SsmArgs a, Ss
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   may_follow();
-  load_rows<DK, C>(k, adjoint ? a.q : a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
-  load_rows<DV, C>(v, adjoint ? a.dout : a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
+  load_rows<DK, C, kThreads>(k, adjoint ? a.q : a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
+  load_rows<DV, C, kThreads>(v, adjoint ? a.dout : a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   if (threadIdx.x < 32) gates_load(g, a, u, t0, n, threadIdx.x);
   __syncthreads();
   for (int i = threadIdx.x; i < C * DV; i += kThreads) {
@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(128) mesa_ssm_scan_kernel(SsmArgs a, SsmWorksp
 
 // grid (NC, U): a chunk's outputs from the state before it (of one chunk: S0).
 template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWorkspace ws) {
+__global__ void __launch_bounds__(kFew) mesa_ssm_out_kernel(SsmArgs a, SsmWorkspace ws) {
+  constexpr int TY = kFew / 16;
   extern __shared__ float4 smem4[];
   float *q = reinterpret_cast<float *>(smem4), *k = q + C * (DK + 4), *v = k + C * (DK + 4), *S = v + C * (DV + 4),
         *M = S + kPart<DV> * (DK + 4);
@@ -125,41 +126,41 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_out_kernel(SsmArgs a, SsmWo
   if (state) load_rows<DK, PART>(S, state, 0, 0, min(a.dv, PART), a.dk);
   __syncthreads();
   {
-    float acc[2][2];
+    float acc[4][2];
     zero(acc);
-    mm_nt<DK>(acc, q, DK + 4, k, DK + 4, ty, tx);
+    mm_nt<TY, DK>(acc, q, DK + 4, k, DK + 4, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int j = 0; j < 2; j++) {
-        const int r = ty + 16 * i, t = tx + 16 * j;
+        const int r = ty + TY * i, t = tx + 16 * j;
         const float d = g.decay(r, t);  // (what lies across a start or above the diagonal is dropped, whatever it is)
         M[r * LDC + t] = t <= r && t >= g.s[r] ? acc[i][j] * d * g.step[t] : 0.0f;
       }
   }
-  float acc[2][DV / 16];
+  float acc[4][DV / 16];
   zero(acc);
-  if (state) mm_nt<DK, 0, PART / 16>(acc, q, DK + 4, S, DK + 4, ty, tx);
+  if (state) mm_nt<TY, DK, 0, PART / 16>(acc, q, DK + 4, S, DK + 4, ty, tx);
   __syncthreads();
   if constexpr (PART < DV) {
     if (state) {
       load_rows<DK, PART>(S, state, 0, PART, a.dv - PART, a.dk);
       __syncthreads();
-      mm_nt<DK, PART / 16, PART / 16>(acc, q, DK + 4, S, DK + 4, ty, tx);
+      mm_nt<TY, DK, PART / 16, PART / 16>(acc, q, DK + 4, S, DK + 4, ty, tx);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 2; i++)
+  for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int j = 0; j < DV / 16; j++) acc[i][j] = g.s[ty + 16 * i] < 0 ? acc[i][j] * g.f[ty + 16 * i] : 0.0f;
-  mm_nn<C>(acc, M, LDC, v, DV + 4, ty, tx);
+    for (int j = 0; j < DV / 16; j++) acc[i][j] = g.s[ty + TY * i] < 0 ? acc[i][j] * g.f[ty + TY * i] : 0.0f;
+  mm_nn<TY, C>(acc, M, LDC, v, DV + 4, ty, tx);
   const float skip = a.skip ? a.skip[u % a.H] : 0.0f;
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < 2; i++)
+  for (int i = 0; i < 4; i++)
 #pragma unroll
     for (int j = 0; j < DV / 16; j++) {
-      const int r = ty + 16 * i, p = tx + 16 * j;
+      const int r = ty + TY * i, p = tx + 16 * j;
       if (r < n && p < a.dv) {
         const float o = a.skip ? fmaf(skip, v[r * (DV + 4) + p], acc[i][j]) : acc[i][j];
         store(a.out, a.dtype == 0, ((size_t)u * a.T + t0 + r) * a.dv + p, o);
@@ -175,7 +176,7 @@ struct States {
     const size_t smem = sizeof(float) * C * (DK + DV + 8);
     const int n = adjoints ? 2 : 1;
     timing_mark_begin(K_SSM_STATES, st);
-    bool ok = launch(mesa_ssm_states_kernel<DK, DV>, dim3(NC, a.units(), n), smem, ws.clear, st, a, ws);
+    bool ok = launch(mesa_ssm_states_kernel<DK, DV>, dim3(NC, a.units(), n), kThreads, smem, ws.clear, st, a, ws);
     timing_mark_end(K_SSM_STATES, st);
     if (!ok) return -1;
     timing_mark_begin(K_SSM_SCAN, st);
@@ -189,7 +190,7 @@ struct Out {
   static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, cudaStream_t st) {
     const size_t smem = sizeof(float) * (C * (2 * DK + DV + 12) + kPart<DV> * (DK + 4) + C * LDC);
     timing_mark_begin(K_SSM_OUT, st);
-    const bool ok = launch(mesa_ssm_out_kernel<DK, DV>, dim3(NC, a.units()), smem, NC == 1, st, a, ws);
+    const bool ok = launch(mesa_ssm_out_kernel<DK, DV>, dim3(NC, a.units()), kFew, smem, NC == 1, st, a, ws);
     timing_mark_end(K_SSM_OUT, st);
     return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
   }

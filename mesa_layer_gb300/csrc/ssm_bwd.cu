@@ -30,38 +30,43 @@ __device__ __forceinline__ float sum16(float x) {  // over a row's 16 threads
   return x;
 }
 
+// Threads a chunk: with four rows each of 128 channels their sums leave an SM too few warps (us of 2 x 16 x 4096 fp32, both
+// 128, 128 threads 830, 256 threads 729; both 64 239, 260).
+template <int DK, int DV>
+constexpr int kGradThreads = DK + DV > 192 ? 256 : kFew;
+
 // grid (NC, U)
 template <int DK, int DV>
-__global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, SsmWorkspace ws) {
-  constexpr int LK = DK + 4, LV = DV + 4, PART = kPart<DV>;
+__global__ void __launch_bounds__(kGradThreads<DK, DV>) mesa_ssm_grads_kernel(SsmArgs a, SsmWorkspace ws) {
+  constexpr int LK = DK + 4, LV = DV + 4, PART = kPart<DV>, TH = kGradThreads<DK, DV>, TY = TH / 16, RI = C / TY;
   extern __shared__ float4 smem4[];
   float *q = reinterpret_cast<float *>(smem4), *k = q + C * LK, *v = k + C * LK, *g = v + C * LV, *S = g + C * LV,
         *M = S + PART * LK, *W = M + C * LDC;
   constexpr int LX = C + 1;  // the pairs' terms, in the states' place until these come
   float *X = S;
   __shared__ Gates ga;
-  __shared__ float x_in[C], x_out[C], duv[C], gv[C], pairs[C], across[kThreads / 32];
+  __shared__ float x_in[C], x_out[C], duv[C], gv[C], pairs[C], across[TH / 32];
   const int u = blockIdx.y, c = blockIdx.x, NC = gridDim.x, t0 = c * C, n = min(C, a.T - t0), h = u % a.H;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, lane = tid & 31, warp = tid >> 5;
   const size_t at = ((size_t)u * NC + c) * a.dv * a.dk;
   may_follow();
-  load_rows<DK, C>(q, a.q, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
-  load_rows<DK, C>(k, a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
-  load_rows<DV, C>(v, a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
-  load_rows<DV, C>(g, a.dout, a.dtype, (size_t)u * a.T + t0, n, a.dv);
+  load_rows<DK, C, TH>(q, a.q, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
+  load_rows<DK, C, TH>(k, a.k, a.dtype, (size_t)a.qk_unit(u) * a.T + t0, n, a.dk);
+  load_rows<DV, C, TH>(v, a.v, a.dtype, (size_t)u * a.T + t0, n, a.dv);
+  load_rows<DV, C, TH>(g, a.dout, a.dtype, (size_t)u * a.T + t0, n, a.dv);
   if (warp == 0) gates_load(ga, a, u, t0, n, lane);
   __syncthreads();
   {
-    float G[2][2], Hm[2][2];
+    float G[RI][2], Hm[RI][2];
     zero(G);
     zero(Hm);
-    mm_nt<DK>(G, q, LK, k, LK, ty, tx);
-    mm_nt<DV>(Hm, g, LV, v, LV, ty, tx);
+    mm_nt<TY, DK>(G, q, LK, k, LK, ty, tx);
+    mm_nt<TY, DV>(Hm, g, LV, v, LV, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < RI; i++)
 #pragma unroll
       for (int j = 0; j < 2; j++) {
-        const int r = ty + 16 * i, t = tx + 16 * j;
+        const int r = ty + TY * i, t = tx + 16 * j;
         const bool on = t <= r && t >= ga.s[r];
         const float d = ga.decay(r, t), w = on ? Hm[i][j] * d * ga.step[t] : 0.0f;
         M[r * LDC + t] = on ? G[i][j] * d : 0.0f;
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
   __syncthreads();
   // X[i][t] <- sum over j < t (a warp: four rows), then for each t the sum over i >= t
 #pragma unroll
-  for (int i = warp; i < C; i += kThreads / 32) {
+  for (int i = warp; i < C; i += TH / 32) {
     float x = X[i * LX + lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
   const size_t krow = (own ? (size_t)a.qk_unit(u) : (size_t)u) * a.T + t0, vrow = (size_t)u * a.T + t0;
   bool bad = false;
   const float skip = a.skip ? a.skip[h] : 0.0f;
-  float aq[2][DK / 16], ak[2][DK / 16], cross = 0.0f, dots[2] = {0.0f, 0.0f};
+  float aq[RI][DK / 16], ak[RI][DK / 16], cross = 0.0f, dots[RI] = {};
   zero(aq);
   zero(ak);
   // the rows of S and R in one or two parts
@@ -103,37 +108,31 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
   for (int p0 = 0; p0 < DV; p0 += PART) {
     const int rows = min(a.dv - p0, PART);
     if (p0 > 0) __syncthreads();
-    load_rows<DK, PART>(S, ws.S + at, 0, p0, rows, a.dk);
+    load_rows<DK, PART, TH>(S, ws.S + at, 0, p0, rows, a.dk);
     __syncthreads();
-    mm_nn<PART>(aq, g + p0, LV, S, LK, ty, tx);
-    constexpr int N4 = PART * DK / 4 / kThreads;
-    float4 r[N4];
-#pragma unroll
-    for (int i = 0; i < N4; i++) {
-      const int e = tid + i * kThreads, p = e / (DK / 4), cc = 4 * (e % (DK / 4));
-      r[i] = p < rows && cc < a.dk ? *reinterpret_cast<const float4 *>(ws.R + at + (size_t)(p0 + p) * a.dk + cc) : make_float4(0, 0, 0, 0);
-      const float4 s = *reinterpret_cast<const float4 *>(S + p * LK + cc);
-      cross = fmaf(r[i].x, s.x, fmaf(r[i].y, s.y, fmaf(r[i].z, s.z, fmaf(r[i].w, s.w, cross))));
+    mm_nn<TY, PART>(aq, g + p0, LV, S, LK, ty, tx);
+    __syncthreads();
+#pragma unroll 8
+    for (int i = 0; i < PART * DK / 4 / TH; i++) {  // R takes S's place, an element its own
+      const int e = tid + i * TH, p = e / (DK / 4), cc = 4 * (e % (DK / 4));
+      const float4 r = p < rows && cc < a.dk ? *reinterpret_cast<const float4 *>(ws.R + at + (size_t)(p0 + p) * a.dk + cc) : make_float4(0, 0, 0, 0);
+      float4 *s = reinterpret_cast<float4 *>(S + p * LK + cc);
+      cross = fmaf(r.x, s->x, fmaf(r.y, s->y, fmaf(r.z, s->z, fmaf(r.w, s->w, cross))));
+      *s = r;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N4; i++) {  // R takes S's place
-      const int e = tid + i * kThreads;
-      *reinterpret_cast<float4 *>(S + e / (DK / 4) * LK + 4 * (e % (DK / 4))) = r[i];
-    }
-    __syncthreads();
-    mm_nn<PART>(ak, v + p0, LV, S, LK, ty, tx);
-    float acc[2][PART / 16];
+    mm_nn<TY, PART>(ak, v + p0, LV, S, LK, ty, tx);
+    float acc[RI][PART / 16];
     zero(acc);
-    mm_nt<DK>(acc, k, LK, S, LK, ty, tx);
+    mm_nt<TY, DK>(acc, k, LK, S, LK, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 2; i++)
+    for (int i = 0; i < RI; i++)
 #pragma unroll
-      for (int j = 0; j < PART / 16; j++) acc[i][j] *= ga.c[ty + 16 * i];
-    mm_tn<C>(acc, M, LDC, g + p0, LV, ty, tx);
+      for (int j = 0; j < PART / 16; j++) acc[i][j] *= ga.c[ty + TY * i];
+    mm_tn<TY, C>(acc, M, LDC, g + p0, LV, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int row = ty + 16 * i;
+    for (int i = 0; i < RI; i++) {
+      const int row = ty + TY * i;
 #pragma unroll
       for (int j = 0; j < PART / 16; j++) {
         const int p = p0 + tx + 16 * j;
@@ -149,8 +148,8 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
   cross = warp_sum(cross);
   if (lane == 0) across[warp] = cross;
 #pragma unroll
-  for (int i = 0; i < 2; i++) {
-    const int row = ty + 16 * i;
+  for (int i = 0; i < RI; i++) {
+    const int row = ty + TY * i;
     const float f = ga.f[row], w = ga.c[row] * ga.step[row], x = sum16(dots[i]);
     float in = 0.0f, out = 0.0f;
 #pragma unroll
@@ -164,14 +163,14 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
     out = sum16(out);
     if (tx == 0) duv[row] = x, x_in[row] = in, x_out[row] = out;
   }
-  mm_nn<C>(aq, W, LDC, k, LK, ty, tx);
-  mm_tn<C>(ak, W, LDC, q, LK, ty, tx);
+  mm_nn<TY, C>(aq, W, LDC, k, LK, ty, tx);
+  mm_tn<TY, C>(ak, W, LDC, q, LK, ty, tx);
 #pragma unroll
-  for (int i = 0; i < 2; i++)
+  for (int i = 0; i < RI; i++)
 #pragma unroll
     for (int j = 0; j < DK / 16; j++)
-      if (ty + 16 * i < n && tx + 16 * j < a.dk) {
-        const size_t to = (krow + ty + 16 * i) * a.dk + tx + 16 * j;
+      if (ty + TY * i < n && tx + 16 * j < a.dk) {
+        const size_t to = (krow + ty + TY * i) * a.dk + tx + 16 * j;
         bad |= !isfinite(aq[i][j]) || !isfinite(ak[i][j]);
         store(own ? a.dq : ws.dqp, !own || a.dtype == 0, to, aq[i][j]);
         store(own ? a.dk_out : ws.dkp, !own || a.dtype == 0, to, ak[i][j]);
@@ -181,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) mesa_ssm_grads_kernel(SsmArgs a, Ssm
     const int t = lane;
     float in = x_in[t], out = x_out[t], all = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; i++) all += across[i];
+    for (int i = 0; i < TH / 32; i++) all += across[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {  // readers from t on, writers up to t
       const float y = __shfl_down_sync(0xffffffffu, in, o), z = __shfl_up_sync(0xffffffffu, out, o);
@@ -239,7 +238,7 @@ struct Grads {
   static int run(const SsmArgs &a, const SsmWorkspace &ws, int NC, cudaStream_t st) {
     const size_t smem = sizeof(float) * (2 * C * (DK + 4) + 2 * C * (DV + 4) + kPart<DV> * (DK + 4) + 2 * C * LDC);
     timing_mark_begin(K_SSM_GRADS, st);
-    const bool ok = launch(mesa_ssm_grads_kernel<DK, DV>, dim3(NC, a.units()), smem, false, st, a, ws);
+    const bool ok = launch(mesa_ssm_grads_kernel<DK, DV>, dim3(NC, a.units()), kGradThreads<DK, DV>, smem, false, st, a, ws);
     timing_mark_end(K_SSM_GRADS, st);
     return ok && cudaPeekAtLastError() == cudaSuccess ? 0 : -1;
   }

@@ -10,7 +10,7 @@ namespace mesa {
 namespace ssm {
 
 constexpr int C = kSsmChunk;  // a warp's lanes: one token each
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kFew = 128;  // of the states' kernel; of those whose threads take four rows each
 constexpr int LDC = C + 4;    // row stride of a [C x C] matrix
 
 struct Gates {
@@ -54,18 +54,18 @@ __device__ __forceinline__ void gates_load(Gates &g, const SsmArgs &a, int u, in
 
 // n rows of d channels (fp32 or bf16) to fp32 rows of D channels, stride D + 4, what is missing as zeros.  Eight loads of a
 // thread are in flight together (one after the other, they were most of the time: 543 us of a 2 x 16 x 4096 x 128 fp32
-// forward's outputs, so 000).
-template <int D, int ROWS>
+// forward's outputs, so 345).
+template <int D, int ROWS, int TH = kFew>
 __device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype, size_t first, int n, int d) {
-  constexpr int PER = ROWS * (D / 4) / kThreads, BATCH = PER < 8 ? PER : 8;
-  static_assert(PER % BATCH == 0 && PER * kThreads == ROWS * (D / 4), "whole batches");
+  constexpr int PER = ROWS * (D / 4) / TH, BATCH = PER < 8 ? PER : 8;
+  static_assert(PER % BATCH == 0 && PER * TH == ROWS * (D / 4), "whole batches");
   const bool bf16 = dtype == 1;
 #pragma unroll
   for (int i0 = 0; i0 < PER; i0 += BATCH) {
     uint4 x[BATCH];
 #pragma unroll
     for (int j = 0; j < BATCH; j++) {
-      const int i = threadIdx.x + (i0 + j) * kThreads, r = i / (D / 4), c = 4 * (i % (D / 4));
+      const int i = threadIdx.x + (i0 + j) * TH, r = i / (D / 4), c = 4 * (i % (D / 4));
       const size_t at = (first + r) * d + c;
       x[j] = make_uint4(0, 0, 0, 0);
       if (r < n && c < d) {
@@ -79,7 +79,7 @@ __device__ __forceinline__ void load_rows(float *dst, const void *src, int dtype
     }
 #pragma unroll
     for (int j = 0; j < BATCH; j++) {
-      const int i = threadIdx.x + (i0 + j) * kThreads, r = i / (D / 4), c = 4 * (i % (D / 4));
+      const int i = threadIdx.x + (i0 + j) * TH, r = i / (D / 4), c = 4 * (i % (D / 4));
       if (bf16) x[j] = make_uint4(x[j].x << 16, x[j].x & 0xffff0000u, x[j].y << 16, x[j].y & 0xffff0000u);
       *reinterpret_cast<uint4 *>(dst + r * (D + 4) + c) = x[j];
     }
@@ -92,15 +92,17 @@ __device__ __forceinline__ void store(void *p, bool f32, size_t i, float x) {
     static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
 }
 
-// Products by 16 x 16 threads (ty, tx): this thread's rows ty + 16 i, columns tx + 16 j.
+// Products by TY x 16 threads (ty, tx): this thread's rows ty + TY i, columns tx + 16 j.  A 16-byte load of a warp takes
+// four turns of shared memory whatever its lanes share: with two rows a thread the loads take 2.5 times as long as the
+// products, with four rows (TY = 8) 1.5 times.
 // acc += A B^T, A [.][K], B [.][K] (row strides lda, ldb); with J0, COLS the columns' share acc[.][J0 ..] of COLS alone.
-template <int K, int J0 = 0, int COLS = 0, int RI, int CJ>
+template <int TY, int K, int J0 = 0, int COLS = 0, int RI, int CJ>
 __device__ __forceinline__ void mm_nt(float (&acc)[RI][CJ], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
 #pragma unroll 4
   for (int k = 0; k < K; k += 4) {
     float4 x[RI];
 #pragma unroll
-    for (int i = 0; i < RI; i++) x[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * lda + k);
+    for (int i = 0; i < RI; i++) x[i] = *reinterpret_cast<const float4 *>(A + (ty + TY * i) * lda + k);
 #pragma unroll
     for (int j = J0; j < (COLS ? J0 + COLS : CJ); j++) {
       const float4 y = *reinterpret_cast<const float4 *>(B + (tx + 16 * (j - J0)) * ldb + k);
@@ -111,13 +113,13 @@ __device__ __forceinline__ void mm_nt(float (&acc)[RI][CJ], const float *A, int 
   }
 }
 // acc += A B, A [.][K], B [K][.].
-template <int K, int RI, int CJ>
+template <int TY, int K, int RI, int CJ>
 __device__ __forceinline__ void mm_nn(float (&acc)[RI][CJ], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
 #pragma unroll 2
   for (int k = 0; k < K; k += 4) {
     float4 x[RI];
 #pragma unroll
-    for (int i = 0; i < RI; i++) x[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * lda + k);
+    for (int i = 0; i < RI; i++) x[i] = *reinterpret_cast<const float4 *>(A + (ty + TY * i) * lda + k);
 #pragma unroll
     for (int e = 0; e < 4; e++)
 #pragma unroll
@@ -129,13 +131,13 @@ __device__ __forceinline__ void mm_nn(float (&acc)[RI][CJ], const float *A, int 
   }
 }
 // acc += A^T B, A [K][.], B [K][.].
-template <int K, int RI, int CJ>
+template <int TY, int K, int RI, int CJ>
 __device__ __forceinline__ void mm_tn(float (&acc)[RI][CJ], const float *A, int lda, const float *B, int ldb, int ty, int tx) {
 #pragma unroll 4
   for (int k = 0; k < K; k++) {
     float x[RI], y[CJ];
 #pragma unroll
-    for (int i = 0; i < RI; i++) x[i] = A[k * lda + ty + 16 * i];
+    for (int i = 0; i < RI; i++) x[i] = A[k * lda + ty + TY * i];
 #pragma unroll
     for (int j = 0; j < CJ; j++) y[j] = B[k * ldb + tx + 16 * j];
 #pragma unroll
@@ -144,7 +146,7 @@ __device__ __forceinline__ void mm_tn(float (&acc)[RI][CJ], const float *A, int 
       for (int j = 0; j < CJ; j++) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
   }
 }
-// The same where both rows' elements lie side by side: this thread's rows and columns frag<M>(ty, i), frag<N>(tx, j), in
+// acc += A^T B by 16 x 16 threads, where both rows' elements lie side by side: this thread's rows and columns frag<M>(ty, i), frag<N>(tx, j), in
 // groups of four from 64 on (a quarter of the shared-memory instructions).
 template <int D>
 __device__ __forceinline__ int frag(int t, int i) {
@@ -204,11 +206,11 @@ int by_size(int dk, int dv, Args &&...args) {
 
 // Launch, the call's first kernel or not, with `smem` bytes of dynamic shared memory (48 KB without being asked for, the static part among them).
 template <typename K, typename... Args>
-bool launch(K kernel, dim3 grid, size_t smem, bool first, cudaStream_t st, const Args &...args) {
+bool launch(K kernel, dim3 grid, int threads, size_t smem, bool first, cudaStream_t st, const Args &...args) {
   if (smem > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return false;
-  if (!first) return launch_after(kernel, grid, kThreads, smem, st, args...);
-  kernel<<<grid, kThreads, smem, st>>>(args...);
+  if (!first) return launch_after(kernel, grid, threads, smem, st, args...);
+  kernel<<<grid, threads, smem, st>>>(args...);
   return true;
 }
 
