@@ -326,9 +326,9 @@ template <typename TIO>
 int forward(const RotaryArgs &a, cudaStream_t st) {
   const size_t blocks = ((size_t)a.B * a.T * (a.d / Row<TIO>::VEC) + kFwdBlock - 1) / kFwdBlock;
   if (blocks > 0x7fffffff) return -1;
-  // all heads of a token in one thread where that fills the SMs twice, else fewer
+  // all heads of a token in one thread (its angles serve them all) where that fills the SMs, else fewer
   int heads = a.H + a.Hk;
-  while (heads > 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 32) heads = (heads + 1) / 2;
+  while (heads > 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 8) heads = (heads + 1) / 2;
   if (heads <= 4 && blocks * ((a.H + a.Hk + heads - 1) / heads) < 152 * 8) heads = 1;
   return by_pairs(a, [&](auto d, auto p) {
     timing_mark_begin(K_ROTARY, st);
