@@ -562,6 +562,7 @@ __global__ void __launch_bounds__(448, 1)
 // The states before the segments from what each leaves: S_{y+1} = decay_y S_y + left_y, S_0 the call's (copied: the last
 // segment may write its final state over it); the adjoints after them the same way, backwards.  Four elements a thread;
 // eight segments' are asked for together (one after the other: 27 us for 16 units in nine segments).
+// No decay is too small to carry what is not finite, as in one chain.
 __global__ void __launch_bounds__(128) mesa_ssm_join_kernel(SsmArgs a, SsmSegments sg, bool adjoint) {
   constexpr int AHEAD = 8;
   const int n4 = a.dv * a.dk / 4, e = blockIdx.x * 128 + threadIdx.x, u = blockIdx.y, n = sg.n;
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(128) mesa_ssm_join_kernel(SsmArgs a, SsmSegmen
       if (i0 + j < n) {
         x[(size_t)y * n4] = s;
         if (i0 + j + 1 < n)
-          s = w[j] == 0.0f ? d[j] : make_float4(fmaf(w[j], s.x, d[j].x), fmaf(w[j], s.y, d[j].y), fmaf(w[j], s.z, d[j].z), fmaf(w[j], s.w, d[j].w));
+          s = make_float4(fmaf(w[j], s.x, d[j].x), fmaf(w[j], s.y, d[j].y), fmaf(w[j], s.z, d[j].z), fmaf(w[j], s.w, d[j].w));
       }
     }
   }
