@@ -386,9 +386,11 @@ __global__ void __launch_bounds__(576, 1)
 }
 
 // ---- the states alone ------------------------------------------------------------------------------------
-// A segment's walk without outputs: what it leaves of a zero state (kSegment), or, from the state before it, the states
-// before its chunks as operands (kKeep: 16-bit tiles for the backward); the adjoints after the chunks the same way,
-// backwards, from rows of q and dout (kAdjoint, kAdjointSegment).
+// A segment's walk without outputs: from the state before it the states before its chunks as operands (kKeep: 16-bit tiles
+// for the backward), or what it leaves of a zero state (kSegment); the adjoints after the chunks the same way, backwards,
+// from rows of q and dout (kAdjoint, kAdjointSegment).  What a segment leaves is one sum: its chunks are taken from the end
+// on and their rows weighed by the decay that is still to come, so that the state stays in the accumulator (1 x 16 x 65536
+// forward 298 -> 294 us; rescaled after each chunk, the state went to registers and back).
 enum ChainMode { kSegment, kKeep, kAdjointSegment, kAdjoint };
 
 // shared memory: two row tiles | their rests | two v tiles | the state as an operand (kept) | misc
@@ -397,7 +399,7 @@ struct Chain {
   static constexpr uint32_t R = 2 * QK_TILE, V = 4 * QK_TILE, S = V + 2 * V_TILE<P>, MISC = S + V_TILE<P>;
 };
 struct ChainMisc {
-  uint64_t full[2], w_full[2], st_done[2], s_full, kept, drain;
+  uint64_t full[2], w_full[2], st_done[2], s_full, kept, sum, drain;  // (sum: the last chunk's products)
   uint32_t tmem;
   int gave_up;
 };
@@ -421,14 +423,14 @@ __global__ void __launch_bounds__(448, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int u = blockIdx.x, seg = blockIdx.y + (MODE == kAdjointSegment ? 1 : 0), NCT = (a.T + L - 1) / L;
   const int c0 = seg * sg.per, NC = sg.n > 1 ? min(NCT - c0, sg.per) : NCT;
-  auto chunk = [&](int c) { return ADJ ? c0 + NC - 1 - c : c0 + c; };  // of step c
+  auto chunk = [&](int c) { return ADJ == KEEP ? c0 + NC - 1 - c : c0 + c; };  // of step c
   auto bar = [](uint64_t &b) { return tc::smem_u32(&b); };
   volatile int *gave_up = &m->gave_up;
   const unsigned limit = a.wait_limit;
   if (N < DK) clear_halves(sm, 4);  // (the rests', too)
   if (warp == 12) tc::tmem_alloc(tc::smem_u32(&m->tmem), 128);
   if (tid == 416) {
-    for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->kept, &m->drain}) tc::mbar_init(bar(*b), 1);
+    for (uint64_t *b : {&m->full[0], &m->full[1], &m->st_done[0], &m->st_done[1], &m->kept, &m->sum, &m->drain}) tc::mbar_init(bar(*b), 1);
     for (uint64_t *b : {&m->w_full[0], &m->w_full[1]}) tc::mbar_init(bar(*b), 8);
     tc::mbar_init(bar(m->s_full), 4);
     m->gave_up = 0;
@@ -460,58 +462,64 @@ __global__ void __launch_bounds__(448, 1)
       const float *r = record(records, u, NCT, chunk(c));
       return ADJ ? r[R_IN + t] * r[R_FIRST + w] : r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
     };
-    float next = weight(0);
+    float next = weight(0), coming = 1.0f, all = KEEP ? 1.0f : record(records, u, NCT, chunk(0))[R_ALL];
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
-      const float mine = next;
-      if (c + 1 < NC) next = weight(c + 1);
+      const float mine = next * coming;
+      if constexpr (!KEEP) coming *= all;
+      if (c + 1 < NC) {
+        next = weight(c + 1);
+        if constexpr (!KEEP) all = record(records, u, NCT, chunk(c + 1))[R_ALL];
+      }
       if (c > 1 && !need(m->st_done[ph], ((c - 2) >> 1) & 1)) break;  // (its tiles are free)
       if (!need(m->full[ph], (c >> 1) & 1)) break;
       weigh_row(sm + ph * QK_TILE, sm + Chain<P>::R + ph * QK_TILE, t, mine, 8 * hf, 8 * hf + 8);
       tc::fence_smem_to_async();
       warp_arrive(m->w_full[ph]);
     }
+    if (!KEEP && tid == 0) sg.decay[(size_t)u * sg.n + seg] = coming;  // of a state, after the segment
   } else if (warp < 12) {
-    const float *from = nullptr;
-    if constexpr (MODE == kKeep) from = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * N : a.S0 ? a.S0 + (size_t)u * P * N : nullptr;
-    if constexpr (MODE == kAdjoint)
-      from = sg.n > 1 ? sg.R + ((size_t)u * sg.n + seg) * P * N : a.dS_final ? a.dS_final + (size_t)u * P * N : nullptr;
-    float next = record(records, u, NCT, chunk(0))[R_ALL], left = 1.0f;  // (left: of a state, after the segment)
-    for (int c = 0; c < NC; c++) {
-      const uint32_t ph = c & 1;
-      const float all = next;
-      if (c + 1 < NC) next = record(records, u, NCT, chunk(c + 1))[R_ALL];
-      left *= all;
-      if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
-      if (KEEP && c > 0 && !need(m->kept, (c - 1) & 1)) break;  // (the last tile has left)
-      state_step<N>(tl + T_G, KEEP ? sm + Chain<P>::S : nullptr, t, all, c == 0, from, 0, P / 32);
-      if (KEEP) tc::fence_smem_to_async();
-      tc::fence_before_sync();
-      warp_arrive(m->s_full);
+    if constexpr (KEEP) {
+      const float *from = MODE == kKeep ? (sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * N : a.S0 ? a.S0 + (size_t)u * P * N : nullptr)
+                          : sg.n > 1    ? sg.R + ((size_t)u * sg.n + seg) * P * N
+                          : a.dS_final  ? a.dS_final + (size_t)u * P * N
+                                        : nullptr;
+      float next = record(records, u, NCT, chunk(0))[R_ALL];
+      for (int c = 0; c < NC; c++) {
+        const uint32_t ph = c & 1;
+        const float all = next;
+        if (c + 1 < NC) next = record(records, u, NCT, chunk(c + 1))[R_ALL];
+        if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
+        if (c > 0 && !need(m->kept, (c - 1) & 1)) break;  // (the last tile has left)
+        state_step<N>(tl + T_G, sm + Chain<P>::S, t, all, c == 0, from, 0, P / 32);
+        tc::fence_smem_to_async();
+        tc::fence_before_sync();
+        warp_arrive(m->s_full);
+      }
     }
     float *to = nullptr;
     if constexpr (MODE == kSegment) to = sg.S + ((size_t)u * sg.n + seg) * P * N;
     if constexpr (MODE == kAdjointSegment) to = sg.R + ((size_t)u * sg.n + seg) * P * N;
     if constexpr (MODE == kAdjoint) to = a.dS0 && seg == 0 ? a.dS0 + (size_t)u * P * N : nullptr;
-    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && to) state_out<N>(tl + T_G, to, t, 0, P / 32);
-    if (!KEEP && t == 0) sg.decay[(size_t)u * sg.n + seg] = left;
+    if (ok && need(m->sum, 0) && to) state_out<N>(tl + T_G, to, t, 0, P / 32);
   } else if (warp == 12) {
     const uint32_t idS = idesc_bf16(128, P, true, true);
     for (int c = 0; c < NC; c++) {
       const uint32_t ph = c & 1;
-      ok &= wait(bar(m->s_full), ph, limit, gave_up);
-      ok &= wait(bar(m->w_full[ph]), (c >> 1) & 1, limit, gave_up);
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      tc::fence_after_sync();
+      if constexpr (KEEP) {
+        if (!need(m->s_full, ph)) break;
+      }
+      if (!need(m->w_full[ph], (c >> 1) & 1)) break;
       if (elect_one()) {
         const uint64_t vd = tc::mnmajor_desc(tc::smem_u32(sm + Chain<P>::V + ph * V_TILE<P>), L, 0),
                        kd = tc::mnmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
                        rd = tc::mnmajor_desc(tc::smem_u32(sm + Chain<P>::R + ph * QK_TILE), L, 0);
 #pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, kd + step_mn(s), vd + step_mn(s), idS, true);
+        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, kd + step_mn(s), vd + step_mn(s), idS, KEEP || s > 0 || c > 0);
 #pragma unroll
         for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_G, rd + step_mn(s), vd + step_mn(s), idS, true);
         tc::mma_commit(bar(m->st_done[ph]));
+        if (c + 1 == NC) tc::mma_commit(bar(m->sum));
       }
     }
   } else if (lane == 0) {
@@ -651,14 +659,15 @@ int chains(const SsmArgs &a, const SsmSegments &sg, const SsmTcBwd &ws, cudaStre
 
 // Segments: a GB300's 152 SMs hold a CTA each.  A segment's chunks are walked twice (before a forward the second time takes
 // half as long), and the two more kernels cost as much as four or five chunks: shorter chains are left whole.  us of one
-// chain, of segments, forward / backward (units x chunks): 1 x 4 21, 20 / 38, 43; 1 x 8 33, 21 / 50, 43; 16 x 16 57, 27 /
-// 86, 64; 24 x 9 (dv = 64) 32, 24 / 57, 53; 48 x 9 37, 33 / 76, 85; 70 x 32 106, 96 / 266, 291; 16 x 512 1496, 297 / 2135, 939.
+// chain, of segments, forward / backward, in a graph (units x chunks): 1 x 4 16, 13 / 30, 32 (launched one by one, the two
+// kernels more cost the 3 us); 1 x 8 28, 14 / 43, 33; 16 x 16 52, 22 / 78, 55; 24 x 9 (dv = 64) 27, 18 / 50, 44; 48 x 9
+// 32, 26 / 66, 72; 70 x 16 54, 49 / 135, 154; 70 x 32 101, 86 / 256, 275; 16 x 512 1489, 283 / 2117, 920.
 SsmSegments ssm_segments(int U, int T, int dv, bool backward, void *workspace, size_t *bytes) {
   const int NC = (T + L - 1) / L;
   SsmSegments sg;
   const int most = U > 0 ? 152 / U : 1, n = most < NC ? most : NC;
   sg.per = n > 1 ? (NC + n - 1) / n : NC;
-  sg.n = n > 1 && (backward ? 2 * sg.per + 5 < NC : 3 * sg.per + 8 < 2 * NC) ? (NC + sg.per - 1) / sg.per : 1;  // (no empty one)
+  sg.n = n > 1 && (backward ? 2 * sg.per + 5 <= NC : 3 * sg.per + 8 <= 2 * NC) ? (NC + sg.per - 1) / sg.per : 1;  // (no empty one)
   auto up256 = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t state = sg.n > 1 ? (size_t)U * sg.n * dv * DK * sizeof(float) : 0, decay = up256((size_t)U * sg.n * sizeof(float)),
                recs = up256((size_t)U * NC * REC * sizeof(float));
