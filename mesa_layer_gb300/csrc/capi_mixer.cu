@@ -205,7 +205,7 @@ int mesa_causal_conv_step(int N, int H, int d, int W, int dtype, int silu, const
 
 size_t mesa_causal_conv_backward_workspace_size(int B, int H, int T, int d, int W) {
   if (check_conv(B, H, T, d, W, MESA_F32) != MESA_OK || (size_t)B * H == 0 || T == 0) return 0;
-  return align256((size_t)mesa::conv_bwd_parts(B, H, T, d) * H * d * (W + 1) * sizeof(float));
+  return align256((size_t)mesa::conv_bwd_parts(B, H, T, d, W) * H * d * (W + 1) * sizeof(float));
 }
 
 int mesa_causal_conv_backward(int B, int H, int T, int d, int W, int dtype, int silu, const void *x, const float *w,

@@ -3,7 +3,7 @@
 //     y_t = bias + sum_{s < W} w_s x_{t-s},   o_t = silu(y_t) or y_t,
 // taps that would reach before a document's first token left out.  A thread owns a few channels and walks a run of
 // tokens with the last W - 1 inputs in registers (the run's own W - 1 predecessors are read again), so that every
-// input is read about once and nothing goes through shared memory.  Bound by memory.
+// input is read about once; nothing is shared between threads but the gradients' last sums.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -213,43 +213,105 @@ __global__ void __launch_bounds__(128) mesa_causal_conv_step_kernel(ConvArgs a) 
 // dy_t = do_t silu'(y_t),   dx_t = sum_s w_s dy_{t+s} (inside the document),   dw_s = sum_t dy_t x_{t-s}.
 // Block: GX channel groups of four x rows of runs; part p of a head's (batch, run) pairs; sums over a part's tokens stay
 // in registers, those of the parts are added by mesa_causal_conv_cols_kernel, both in a fixed order.
-constexpr int kBwdRun = 64;
+constexpr int kBwdBlock = 128;
 constexpr int kBwdVec = 4;  // channels a thread (two: half the registers, but 153 us)
 __host__ __device__ inline int bwd_gx(int d) { return d / kBwdVec < 32 ? d / kBwdVec : 32; }
 
-// (Two CTAs per SM: 203 -> 140 us at 8 x 16 x 4096 x 128; runs of 64 tokens instead of 32: 138.)
+// As many CTAs as a GB300's 152 SMs hold at once (bwd_ctas: what keeps taps, windows and sums in registers; four tokens'
+// chains interleave, and more warps with values in local memory lose: W = 4 with three, four, five, six CTAs an SM 95, 93,
+// 116, 136 us at 8 x 16 x 4096 x 128; W = 8 with two, three 172, 212), shared by all heads and channels; and runs of which
+// every row takes as many as the others, as nearly as that goes (in parts of a sequence of 16 tokens at least; a run costs
+// about four tokens more than it has).  us of 8 x 16 x 4001 x 128: runs of 64 tokens, three or four a row, 137; this, the
+// inputs on their way in shared memory instead of registers, and no case distinction while no document starts, 98 (75 % of a copy's rate at W = 2 and in fp32; at W = 4 the packed products' pipe
+// and the exponentials' latency, 45 % of the issue slots).
+struct BwdSplit {
+  int parts, run, runs;  // CTAs that share a head's channels; tokens a run, runs a sequence
+};
+constexpr int bwd_ctas(int W) { return W <= 2 ? 6 : W <= 5 ? 4 : W <= 7 ? 3 : 2; }
+BwdSplit bwd_split(int B, int H, int T, int d, int W) {
+  const int gx = bwd_gx(d), rows = kBwdBlock / gx, slabs = (d / kBwdVec + gx - 1) / gx;
+  const int n = max(152 * bwd_ctas(W) / (H * slabs), 1), slots = n * rows;
+  BwdSplit best{1, T > 0 ? T : 1, 1};
+  double least = 1e30;
+  for (int each = 1; each <= 8; each++) {
+    int runs = max(1, (int)((long long)each * slots / B));
+    const int run = max((T + runs - 1) / runs, 16);
+    runs = max(1, (T + run - 1) / run);
+    const long long all = (long long)B * runs;
+    const double cost = (double)((all + slots - 1) / slots) * (run + 4);
+    if (cost < least) {
+      least = cost;
+      best = {(int)min((all + rows - 1) / rows, (long long)n), run, runs};
+    }
+  }
+  return best;
+}
+
+// 8 or 16 bytes to shared memory, in flight until the wait for their group.
+template <int N>
+__device__ __forceinline__ void copy_ahead(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// A thread's inputs come through shared memory of its own, kRing groups of kGroup tokens: [ring][token][x, dout][thread].
+constexpr int kGroup = 4;
+constexpr int kRing = 2;  // (three or four: the same times)
+template <typename TIO>
+constexpr uint32_t kRingBytes = kRing * kGroup * 2 * kBwdBlock * kBwdVec * sizeof(TIO);
+
 template <typename TIO, int W, bool PACKED>
-__global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArgs a, int parts, int runs) {
+__global__ void __launch_bounds__(kBwdBlock, bwd_ctas(W)) mesa_causal_conv_bwd_kernel(ConvArgs a, int parts, int run, int runs) {
   using V = Vec<TIO, kBwdVec>;
-  constexpr int AHEAD = 4, VEC = kBwdVec, P = VEC / 2, N = VEC * (W + 1);
-  extern __shared__ float sm[];
-  const int gx = bwd_gx(a.d), rows = kBlock / gx, g = threadIdx.x % gx, row = threadIdx.x / gx;
+  using Raw = typename V::Raw;
+  constexpr int VEC = kBwdVec, P = VEC / 2, N = VEC * (W + 1), RING = kRing;
+  extern __shared__ __align__(16) uint8_t ring[];
+  const int gx = bwd_gx(a.d), rows = kBwdBlock / gx, g = threadIdx.x % gx, row = threadIdx.x / gx;
   const int h = blockIdx.z, c0 = (blockIdx.y * gx + g) * VEC, pairs = a.B * runs;
   const bool on = row < rows && c0 < a.d;
   u64 dw[W][P] = {}, db[P] = {};
   if (on) {
     u64 w[W][P], bias[P];
     load_taps<VEC, W>(a, h, c0, w, bias);
+    Raw *const mine_at = reinterpret_cast<Raw *>(ring) + threadIdx.x;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine_at);
+#pragma unroll 1
     for (int pr = blockIdx.x * rows + row; pr < pairs; pr += parts * rows) {
-      const int b = pr / runs, u = b * a.H + h, t0 = pr % runs * kBwdRun, t1 = min(t0 + kBwdRun, a.T);
+      const int b = pr / runs, u = b * a.H + h, t0 = pr % runs * run, t1 = min(t0 + run, a.T), end = min(t1 + W - 1, a.T);
       const size_t base = (size_t)u * a.T * a.d + c0;
       const TIO *src = static_cast<const TIO *>(a.x) + base, *dout = static_cast<const TIO *>(a.dout) + base;
       TIO *dx = static_cast<TIO *>(a.dx) + base;
       const uint8_t *starts = PACKED ? a.starts + (size_t)b * a.T : nullptr;
       u64 x[W][P], pend[W][P] = {};  // pend[s]: what the tokens so far give dx_{t-s}
-      int age;  // tokens before t of its document, W - 1 at most
-      struct Token {
-        typename V::Raw x, g;
-        bool cut;
+      auto fetch = [&](int t, int slot) {
+#pragma unroll
+        for (int j = 0; j < kGroup; j++)
+          if (t + j < end) {
+            const uint32_t at = to + ((slot * kGroup + j) * 2 * kBwdBlock) * (uint32_t)sizeof(Raw);
+            copy_ahead<sizeof(Raw)>(at, src + (size_t)(t + j) * a.d);
+            copy_ahead<sizeof(Raw)>(at + kBwdBlock * (uint32_t)sizeof(Raw), dout + (size_t)(t + j) * a.d);
+          }
+        copies_commit();
       };
-      auto load = [&](int t, Token &in) {
-        in.x = *reinterpret_cast<const typename V::Raw *>(src + (size_t)t * a.d);
-        in.g = *reinterpret_cast<const typename V::Raw *>(dout + (size_t)t * a.d);
-        if (PACKED) in.cut = starts[t];
+      auto any_start = [&](int t) {
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < kGroup; j++)
+          if (PACKED && t + j < end) any |= starts[t + j] != 0;
+        return any;
       };
-      // Token t: dx of token t - (W - 1) is complete (EMIT: it is the run's own); MINE: so is t.
-      auto token = [&](int t, const Token &in, auto mine, auto emit) {
-        if (PACKED && in.cut) {
+#pragma unroll
+      for (int k = 0; k < RING - 1; k++) fetch(t0 + k * kGroup, k);
+      bool later = any_start(t0);
+      int age = load_window<TIO, VEC, W>(a, u, t0, c0, x);  // tokens before t of its document, W - 1 at most
+      // Token t: dx of token t - (W - 1) is complete (emit: it is the run's own); mine: so is t.  fresh: it may be among the
+      // first W - 1 of its document.
+      auto token = [&](int t, const Raw *in, bool fresh, bool mine, bool emit) {
+        if (fresh && starts[t]) {
           age = 0;
 #pragma unroll
           for (int s = 1; s < W; s++)
@@ -257,8 +319,8 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
             for (int p = 0; p < P; p++) x[s][p] = 0;
         }
         u64 dy[P];
-        V::unpack(in.x, x[0]);
-        V::unpack(in.g, dy);
+        V::unpack(in[0], x[0]);
+        V::unpack(in[kBwdBlock], dy);
         if (a.silu) {
 #pragma unroll
           for (int p = 0; p < P; p++) {
@@ -269,7 +331,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
             dy[p] = mul2(dy[p], mul2(g, fma2(y, sub2(one, g), one)));
           }
         }
-        if constexpr (decltype(mine)::value) {
+        if (mine) {
 #pragma unroll
           for (int p = 0; p < P; p++) {
             db[p] = add2(db[p], dy[p]);
@@ -277,7 +339,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
             for (int s = 0; s < W; s++) dw[s][p] = fma2(dy[p], x[s][p], dw[s][p]);
           }
         }
-        if (!PACKED || age >= W - 1) {
+        if (!fresh || age >= W - 1) {
 #pragma unroll
           for (int p = 0; p < P; p++)
 #pragma unroll
@@ -290,62 +352,42 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
         }
 #pragma unroll
         for (int p = 0; p < P; p++) pend[0][p] = mul2(w[0][p], dy[p]);
-        if constexpr (decltype(emit)::value)
-          *reinterpret_cast<typename V::Raw *>(dx + (size_t)(t - (W - 1)) * a.d) = V::pack(pend[W - 1]);
-        if (PACKED) age = min(age + 1, W - 1);
+        if (emit) *reinterpret_cast<Raw *>(dx + (size_t)(t - (W - 1)) * a.d) = V::pack(pend[W - 1]);
+        if (fresh) age = min(age + 1, W - 1);
 #pragma unroll
         for (int s = W - 1; s > 0; s--)
 #pragma unroll
           for (int p = 0; p < P; p++) x[s][p] = x[s - 1][p];
       };
-      constexpr std::true_type yes{};
-      constexpr std::false_type no{};
-      Token in[2][AHEAD];
-      int t = t0;
-      age = load_window<TIO, VEC, W>(a, u, t0, c0, x);
-      const int lead = min(t0 + W - 1, t1);
+      int slot = 0;
 #pragma unroll 1
-      for (; t < lead; t++) {  // nothing of the run's own is complete yet
-        load(t, in[0][0]);
-        token(t, in[0][0], yes, no);
-      }
-      if (t + 2 * AHEAD <= t1) {
+      for (int t = t0; t < end; t += kGroup) {
+        fetch(t + (RING - 1) * kGroup, slot == 0 ? RING - 1 : slot - 1);
+        const bool fresh = PACKED && (later || age < W - 1);
+        later = any_start(t + kGroup);
+        copies_wait<RING - 1>();
+        const Raw *in = mine_at + slot * kGroup * 2 * kBwdBlock;
+        if (t >= t0 + W - 1 && t + kGroup <= t1 && !fresh) {
 #pragma unroll
-        for (int j = 0; j < AHEAD; j++) load(t + j, in[0][j]);
+          for (int j = 0; j < kGroup; j++) token(t + j, in + j * 2 * kBwdBlock, false, true, true);
+        } else {  // (the run's first tokens and the next one's, a document's first ones)
 #pragma unroll 1
-        for (; t + 3 * AHEAD <= t1; t += 2 * AHEAD) {  // (the next tokens are on their way)
-#pragma unroll
-          for (int j = 0; j < AHEAD; j++) load(t + AHEAD + j, in[1][j]);
-#pragma unroll
-          for (int j = 0; j < AHEAD; j++) token(t + j, in[0][j], yes, yes);
-#pragma unroll
-          for (int j = 0; j < AHEAD; j++) load(t + 2 * AHEAD + j, in[0][j]);
-#pragma unroll
-          for (int j = 0; j < AHEAD; j++) token(t + AHEAD + j, in[1][j], yes, yes);
+          for (int j = 0; j < kGroup && t + j < end; j++)
+            token(t + j, in + j * 2 * kBwdBlock, PACKED, t + j < t1, t + j >= t0 + W - 1);
         }
-#pragma unroll
-        for (int j = 0; j < AHEAD; j++) token(t + j, in[0][j], yes, yes);
-        t += AHEAD;
-      }
-#pragma unroll 1
-      for (; t < t1; t++) {
-        load(t, in[0][0]);
-        token(t, in[0][0], yes, yes);
-      }
-#pragma unroll 1
-      for (; t < t1 + W - 1 && t < a.T; t++) {  // the next run's first tokens
-        load(t, in[0][0]);
-        token(t, in[0][0], no, yes);
+        if (++slot == RING) slot = 0;
       }
 #pragma unroll
-      for (int s = W - 1; s >= 1; s--)  // the sequence's end (t = T): token t - s's sum is in pend[s - 1]
-        if (t < t1 + W - 1 && t - s >= t0 && t - s < t1)
-          *reinterpret_cast<typename V::Raw *>(dx + (size_t)(t - s) * a.d) = V::pack(pend[s - 1]);
+      for (int s = W - 1; s >= 1; s--)  // the sequence's end (end = T): token T - s's sum is in pend[s - 1]
+        if (end < t1 + W - 1 && end - s >= t0 && end - s < t1)
+          *reinterpret_cast<Raw *>(dx + (size_t)(end - s) * a.d) = V::pack(pend[s - 1]);
     }
   }
   may_follow();
   if (!a.partial) return;
   // the rows' sums: [row][value][group]
+  float *const sm = reinterpret_cast<float *>(ring);
+  __syncthreads();  // (every row has read its inputs)
 #pragma unroll
   for (int p = 0; p < P; p++)
 #pragma unroll
@@ -359,7 +401,7 @@ __global__ void __launch_bounds__(kBlock, 2) mesa_causal_conv_bwd_kernel(ConvArg
     }
   __syncthreads();
   float *dst = a.partial + (size_t)blockIdx.x * a.H * a.d * (W + 1);
-  for (int i = threadIdx.x; i < N * gx; i += kBlock) {
+  for (int i = threadIdx.x; i < N * gx; i += kBwdBlock) {
     const int gg = i % gx, v = i / gx, c = (blockIdx.y * gx + gg) * VEC + v / (W + 1);
     if (c >= a.d) continue;
     float x = 0.0f;
@@ -423,16 +465,17 @@ int forward(const ConvArgs &a, cudaStream_t st) {
 
 template <typename TIO>
 int backward(const ConvArgs &a, cudaStream_t st) {
-  const int parts = conv_bwd_parts(a.B, a.H, a.T, a.d), gx = bwd_gx(a.d), runs = (a.T + kBwdRun - 1) / kBwdRun;
+  const BwdSplit split = bwd_split(a.B, a.H, a.T, a.d, a.W);
+  const int parts = split.parts, gx = bwd_gx(a.d);
   return by_width(a.W, [&](auto w) {
     constexpr int W = decltype(w)::value;
-    const size_t smem = a.partial ? (size_t)(kBlock / gx) * gx * kBwdVec * (W + 1) * sizeof(float) : 0;
+    const size_t sums = a.partial ? (size_t)(kBwdBlock / gx) * gx * kBwdVec * (W + 1) * sizeof(float) : 0;
+    const size_t smem = sums > kRingBytes<TIO> ? sums : kRingBytes<TIO>;
     timing_mark_begin(K_CONV_BWD, st);
     const dim3 grid(parts, (a.d / kBwdVec + gx - 1) / gx, a.H);
-    if (a.starts)
-      mesa_causal_conv_bwd_kernel<TIO, W, true><<<grid, kBlock, smem, st>>>(a, parts, runs);
-    else
-      mesa_causal_conv_bwd_kernel<TIO, W, false><<<grid, kBlock, smem, st>>>(a, parts, runs);
+    auto kernel = a.starts ? mesa_causal_conv_bwd_kernel<TIO, W, true> : mesa_causal_conv_bwd_kernel<TIO, W, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return -1;
+    kernel<<<grid, kBwdBlock, smem, st>>>(a, parts, split.run, split.runs);
     timing_mark_end(K_CONV_BWD, st);
     if (a.partial) {
       timing_mark_begin(K_CONV_COLS, st);
@@ -459,15 +502,7 @@ int step(const ConvArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Two CTAs for each of a GB300's 152 SMs (what their registers allow at once) over all heads and channels, no more than
-// there are runs.  (us of 8 x 16 x 4096 x 128: two 166, three 221, four 189, six 192)
-int conv_bwd_parts(int B, int H, int T, int d) {
-  const int gx = bwd_gx(d), rows = kBlock / gx, slabs = (d / kBwdVec + gx - 1) / gx;
-  const size_t pairs = (size_t)B * ((T + kBwdRun - 1) / kBwdRun), most = (pairs + rows - 1) / rows;
-  size_t n = 152 * 2 / ((size_t)H * slabs);
-  if (n > most) n = most;
-  return n < 1 ? 1 : (int)n;
-}
+int conv_bwd_parts(int B, int H, int T, int d, int W) { return bwd_split(B, H, T, d, W).parts; }
 
 int launch_causal_conv(const ConvArgs &a, cudaStream_t st) {
   return a.dtype == 1 ? forward<__nv_bfloat16, 4>(a, st) : forward<float, 4>(a, st);

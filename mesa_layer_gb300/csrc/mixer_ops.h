@@ -22,7 +22,7 @@ struct ConvArgs {
   float *dw = nullptr, *dbias = nullptr;
   float *partial = nullptr;  // [parts][H, d, W + 1]
 };
-int conv_bwd_parts(int B, int H, int T, int d);  // CTAs that share a head's channels in the backward
+int conv_bwd_parts(int B, int H, int T, int d, int W);  // CTAs that share a head's channels in the backward
 int launch_causal_conv(const ConvArgs &a, cudaStream_t st);
 int launch_causal_conv_step(const ConvArgs &a, cudaStream_t st);
 int launch_causal_conv_backward(const ConvArgs &a, cudaStream_t st);
