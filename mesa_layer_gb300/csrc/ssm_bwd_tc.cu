@@ -6,8 +6,11 @@
 //     Q K^T, g V^T -> M' = (Q K^T) o E, W = (g V^T) o E D;    dQ = f (g S) + W K,   dK = c D (V R) + W^T Q,
 //     du = c (K R^T) + M'^T g,   dV = D du + skip g.
 // Eight products of 128^3 a chunk (P = 128).  The scales f, c D and c are put on where the products lie in tensor memory,
-// with the sums that the decays' gradients need on the way.  The pairs' terms X = (Q K^T) o W stay fp32, and the sum over
-// readers i >= t and writers j < t runs as F(t + 1) = F(t) - sum_j X_tj + sum_i X_it inside a chunk (2^-24 of the terms).
+// with the sums that the decays' gradients need on the way.  The pairs' terms X = (Q K^T) o W stay fp32.  A token's sum over
+// readers i >= t and writers j < t is put together from terms that belong to it alone, by blocks of 32 tokens: those of its
+// own block (writers' running sums, added over the readers), its block's readers with earlier blocks' writers, its block's
+// writers with later blocks' readers, and whole blocks on either side.  (Run along the chunk as F(t + 1) = F(t) - sum_j X_tj +
+// sum_i X_it, 2^-24 of a loud document stayed in the next one: 0.1 of ddt where the first was 1e6 times as loud.)
 // du . v is the sum of the same terms (X / D over a token's readers) and c (V R) . k, not a product with du: M's rounding
 // to bf16 would be in it (ddt 1.6e-3 off before its own rounding, so 3e-4; the sum of ddt over a head 3.7e-3, so 7e-4).
 #include "launch.h"
@@ -28,7 +31,7 @@ struct Grad {
 struct GradMisc {
   alignas(16) float rec[REC];  // the chunk's gates; once every block is done, by rows' warp and token: its rows' sum of X / D
   float frob[2][16];
-  float scan[2][4];
+  float scan[4][4];  // sums over a warp's tokens: of what it reads from before warp 0, 1, 2; of what it writes past the chunk
   uint64_t full1, full2, c1, c2, e, fg, h, a_done, b_done, c_done, f_done, qk_staged, v_staged, drain;
   uint32_t tmem;
   int gave_up;
@@ -36,8 +39,11 @@ struct GradMisc {
 template <int P>
 constexpr uint32_t kGradSmem = Grad<P>::MISC + sizeof(GradMisc);
 static_assert(kGradSmem<128> <= 232448, "shared memory per block");
-// Tensor memory: Q K^T, then du | g V^T, then sums by token | dQ | dK.  The sums' columns, by quarter of the channels:
+// Tensor memory: Q K^T, then du | g V^T, then the diagonal blocks' pairs and sums by token | dQ | dK.  The sums' columns (T_SUM:
+// of the block beside the token's own), by quarter of the channels (X_ROW: of the chunk's tokens; the token's own quarter holds
+// its own block's share of its sum over readers and writers):
 constexpr uint32_t T_A = 0, T_B = 128, T_DQ = 256, T_DK = 384;
+__device__ __forceinline__ uint32_t T_SUM(int w) { return T_B + 32 * ((w + 1) & 3); }
 constexpr int X_ROW = 0, X_IN = 4, X_OUT = 8, X_GV = 12, X_DIAG = 13;
 
 __device__ __forceinline__ void tmem_put(uint32_t taddr, float x) {
@@ -117,32 +123,38 @@ __global__ void __launch_bounds__(576, 1)
     const int w = warp & 3, b = warp >> 2, t = 32 * w + lane;  // row t, columns of quarter b
     const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
     uint32_t bad = 0;
-    // What the steps' gradients of a chunk need (warps 0-3, token t).  They are put together while the next chunk's products run.
+    // What the steps' gradients of a chunk need (one warp for each 32 tokens: not the diagonal block's, which takes longest).
+    // They are put together while the next chunk's products run.
+    const bool teller = b == ((w + 1) & 3);
     struct Steps {
-      float xi, moved, duv, gv, across, raw, step;
+      float in, from0, from1, from2;  // what the token reads from before the chunk, from the blocks 0, 1, 2 before its own
+      float own, out, past;  // its own block's pairs and what crosses the whole chunk; what it writes for later blocks, past the chunk
+      float duv, gv, raw, step;
       int at, start;
     } last;
     last.at = -1;
     auto steps = [&]() {
       const int u = last.at / NC, c = last.at - u * NC, h = u % a.H;
       const bool in = c * L + t < a.T;
-      float suf = last.xi, pre = last.moved;  // readers from t on, writers before t (with the pairs)
+      const float reads0 = last.in, reads1 = reads0 + last.from0, reads2 = reads1 + last.from1;
+      float suf = reads2 + last.from2, pre = last.out + last.past;  // over the warp: readers from t on, writers before t
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float p = __shfl_down_sync(0xffffffffu, suf, o), q = __shfl_up_sync(0xffffffffu, pre, o);
         if (lane + o < 32) suf += p;
         if (lane >= o) pre += q;
       }
-      if (lane == 0) m->scan[0][w] = suf;
-      if (lane == 31) m->scan[1][w] = pre;
+      pre = __shfl_up_sync(0xffffffffu, pre, 1);
+      if (lane == 0) pre = 0.0f;
+      const float s0 = warp_sum(reads0), s1 = warp_sum(reads1), s2 = warp_sum(reads2), s3 = warp_sum(last.past);
+      if (lane == 0) m->scan[0][w] = s0, m->scan[1][w] = s1, m->scan[2][w] = s2, m->scan[3][w] = s3;
       group_or(2, 128, false);
-      pre -= last.moved;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        if (i > w) suf += m->scan[0][i];
-        if (i < w) pre += m->scan[1][i];
+        if (i > w) suf += m->scan[w < 3 ? w : 0][i];
+        if (i < w) pre += m->scan[3][i];
       }
-      const float da = last.start == t ? 0.0f : pre + suf + last.across;
+      const float da = last.start == t ? 0.0f : (last.own + pre) + suf;
       const float dd = in ? fmaf(a.A[h], da, last.duv) * sigmoid(last.raw) : 0.0f;
       if (in) {
         if (!isfinite(dd)) bad = 0x7f80u;
@@ -189,7 +201,7 @@ __global__ void __launch_bounds__(576, 1)
         break;
       }
       // ---- M', W and the pairs' sums: block (w, b), eight columns at a time ----
-      if (b == 0 && it > 0) steps();
+      if (teller && it > 0) steps();
       float row = 0.0f, gv = 0.0f, diag = 0.0f, col = 0.0f;  // col: column 32 b + lane
       need(m->c1, par);
       if (b <= w) {
@@ -237,8 +249,12 @@ __global__ void __launch_bounds__(576, 1)
           const uint32_t to = tile_off(t, 4 * b + cc, L);
           *reinterpret_cast<uint4 *>(sm + O::M + to) = make_uint4(om[0], om[1], om[2], om[3]);
           *reinterpret_cast<uint4 *>(sm + O::W + to) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-          const float sum = transposed_sum(x, lane);
-          if (lane >> 3 == cc) col = sum;
+          if (b == w) {  // (for later, in g V^T's place, which has been read)
+            tc::tmem_st8(tl + T_B + 32 * b + 8 * cc, x);
+          } else {
+            const float sum = transposed_sum(x, lane);
+            if (lane >> 3 == cc) col = sum;
+          }
         };
 #pragma unroll 1
         for (int cc = 0; cc < 4; cc += 2) {
@@ -298,6 +314,24 @@ __global__ void __launch_bounds__(576, 1)
       tc::tmem_st_wait();
       tc::fence_before_sync();
       warp_arrive(m->b_done);
+      // ---- the diagonal block's sums: its columns', and of the pairs with readers from token 32 w + lane on and writers before
+      // it (off the products' way) ----
+      if (b == w) {
+        float run = 0.0f;  // of this lane's row
+#pragma unroll 1
+        for (int cc = 0; cc < 4; cc++) {
+          float x[8], y[8];  // X / D; its steps' multiples summed along the row so far
+          tc::tmem_ld8(tl + T_B + 32 * b + 8 * cc, x);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            y[j] = lane >= 8 * cc + j ? run : 0.0f;
+            run = fmaf(x[j], __shfl_sync(0xffffffffu, step, 8 * cc + j), run);
+          }
+          const float pairs = transposed_sum(y, lane), sum = transposed_sum(x, lane);
+          if (lane >> 3 == cc) row = pairs, col = sum;
+        }
+      }
       // ---- c (K R^T); the sums so far ----
       need(m->e, par);
       {
@@ -309,10 +343,10 @@ __global__ void __launch_bounds__(576, 1)
         for (int i = 0; i < V; i++) x[i] *= ct;
         tc::tmem_st<V>(tl + T_A + V * b, x);
         if (b <= w) m->rec[w * L + 32 * b + lane] = col;  // (every block is done: the gates have been read)
-        tmem_put(tl + T_B + X_ROW + b, row);
-        tmem_put(tl + T_B + X_IN + b, x_in);
-        tmem_put(tl + T_B + X_OUT + b, x_out);
-        if (b == w) tmem_put(tl + T_B + X_GV, gv), tmem_put(tl + T_B + X_DIAG, diag);
+        tmem_put(tl + T_SUM(w) + X_ROW + b, row);
+        tmem_put(tl + T_SUM(w) + X_IN + b, x_in);
+        tmem_put(tl + T_SUM(w) + X_OUT + b, x_out);
+        if (b == w) tmem_put(tl + T_SUM(w) + X_GV, gv), tmem_put(tl + T_SUM(w) + X_DIAG, diag);
         tc::tmem_st_wait();
         tc::fence_before_sync();
         warp_arrive(m->c_done);
@@ -344,11 +378,12 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->qk_staged);
       // ---- dV ----
       need(m->h, par);
-      float sum = 0.0f;
-      if (b == 0) {  // (all warps' columns are there)
+      float later = 0.0f, mine_col = 0.0f;  // X / D over the readers of later blocks, of its own
+      if (teller) {  // (all warps' columns are there)
+        mine_col = m->rec[w * L + t];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          if (i >= w) sum += m->rec[i * L + t];
+        for (int i = 1; i < 4; i++)
+          if (i > w) later += m->rec[i * L + t];
       }
       {
         constexpr int V = P / 4;
@@ -380,10 +415,10 @@ __global__ void __launch_bounds__(576, 1)
         ok = false;
         break;
       }
-      if (b > 0) continue;
+      if (!teller) continue;
       tc::fence_after_sync();
       float x[16];
-      tc::tmem_ld16(tl + T_B, x);
+      tc::tmem_ld16(tl + T_SUM(w), x);
       float all = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
@@ -395,9 +430,11 @@ __global__ void __launch_bounds__(576, 1)
       warp_arrive(m->f_done);
       auto four = [&](int i) { return (x[i] + x[i + 1]) + (x[i + 2] + x[i + 3]); };
       const float xo = four(X_OUT);
-      last = Steps{four(X_IN), fmaf(step, sum + xo, -four(X_ROW)), (sum + x[X_DIAG]) + xo, x[X_GV], across * all, raw, step, at, start};
+      last = Steps{four(X_IN), w > 0 ? x[X_ROW] : 0.0f, w > 1 ? x[X_ROW + 1] : 0.0f, w > 2 ? x[X_ROW + 2] : 0.0f,
+                   fmaf(across, all, w == 0 ? x[X_ROW] : w == 1 ? x[X_ROW + 1] : w == 2 ? x[X_ROW + 2] : x[X_ROW + 3]), step * later,
+                   step * xo, (later + mine_col + x[X_DIAG]) + xo, x[X_GV], raw, step, at, start};
     }
-    if (b == 0 && ok && last.at >= 0) steps();
+    if (teller && ok && last.at >= 0) steps();
     if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
   } else if (warp == 16) {
     // ---- products ----
