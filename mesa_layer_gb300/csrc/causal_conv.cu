@@ -234,14 +234,14 @@ BwdSplit bwd_split(int B, int H, int T, int d, int W) {
   BwdSplit best{1, T > 0 ? T : 1, 1};
   double least = 1e30;
   for (int each = 1; each <= 8; each++) {
-    int runs = max(1, (int)((long long)each * slots / B));
-    const int run = max((T + runs - 1) / runs, 16);
-    runs = max(1, (T + run - 1) / run);
-    const long long all = (long long)B * runs;
+    long long runs = max(1LL, (long long)each * slots / B);  // (tokens and a run's length together may pass 32 bits)
+    const int run = max((int)((T + runs - 1) / runs), 16);
+    runs = max(1LL, ((long long)T + run - 1) / run);
+    const long long all = B * runs;
     const double cost = (double)((all + slots - 1) / slots) * (run + 4);
     if (cost < least) {
       least = cost;
-      best = {(int)min((all + rows - 1) / rows, (long long)n), run, runs};
+      best = {(int)min((all + rows - 1) / rows, (long long)n), run, (int)runs};
     }
   }
   return best;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kBwdBlock, bwd_ctas(W)) mesa_causal_conv_bwd_k
     const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine_at);
 #pragma unroll 1
     for (int pr = blockIdx.x * rows + row; pr < pairs; pr += parts * rows) {
-      const int b = pr / runs, u = b * a.H + h, t0 = pr % runs * run, t1 = min(t0 + run, a.T), end = min(t1 + W - 1, a.T);
+      const int b = pr / runs, u = b * a.H + h, t0 = pr % runs * run, t1 = t0 + min(run, a.T - t0), end = min(t1 + W - 1, a.T);
       const size_t base = (size_t)u * a.T * a.d + c0;
       const TIO *src = static_cast<const TIO *>(a.x) + base, *dout = static_cast<const TIO *>(a.dout) + base;
       TIO *dx = static_cast<TIO *>(a.dx) + base;
