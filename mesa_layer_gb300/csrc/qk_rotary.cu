@@ -100,7 +100,8 @@ __device__ __forceinline__ void token_angles(const RotaryArgs &a, size_t token, 
   }
 }
 
-// The pairs' values of this lane's channels of one row (raw: the lane's own; row: the row in memory).
+// The pairs' values of this lane's channels of one row (raw: the lane's own; row: the row in memory); 0 for channels that do
+// not turn (their S is 0, but 0 times what is not finite would not be).
 template <typename TIO, int PAIRS>
 __device__ __forceinline__ void pairs_of(const RotaryArgs &a, const TIO *row, uint4 raw, int c0, float (&p)[Row<TIO>::VEC]) {
   constexpr int VEC = Row<TIO>::VEC;
@@ -109,13 +110,14 @@ __device__ __forceinline__ void pairs_of(const RotaryArgs &a, const TIO *row, ui
     float v[VEC];
     Row<TIO>::unpack(raw, v);
 #pragma unroll
-    for (int i = 0; i < VEC; i++) p[i] = v[i ^ 1];
+    for (int i = 0; i < VEC; i++) p[i] = c0 + i < a.R ? v[i ^ 1] : 0.0f;
   } else if constexpr (PAIRS == kHalves) {  // another lane's channels, in the same places
     const int lane = threadIdx.x & 31, from = c0 < half ? lane + half / VEC : c0 < a.R ? lane - half / VEC : lane;
     raw.x = __shfl_sync(0xffffffffu, raw.x, from);
     raw.y = __shfl_sync(0xffffffffu, raw.y, from);
     raw.z = __shfl_sync(0xffffffffu, raw.z, from);
     raw.w = __shfl_sync(0xffffffffu, raw.w, from);
+    if (c0 >= a.R) raw = make_uint4(0, 0, 0, 0);
     Row<TIO>::unpack(raw, p);
   } else {
 #pragma unroll
