@@ -391,6 +391,8 @@ int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void 
  * workspace: at least mesa_ssm_workspace_size() bytes, 256-byte aligned; its first word is the status word read by
  * mesa_forward_status (MESA_ERR_NONFINITE: a non-finite out).
  * The outputs' memory is none of the inputs'.
+ * A NaN or infinity in q_t reaches out_t alone, one in k_t, v_t (its channel) or dt_t the unit's outputs from t on and S_final;
+ * what it reaches is not finite, NaN for most.  (On the tensor cores its unit is walked twice.)
  * Arithmetic: sums, states and gates in fp32, log-decays as sums of two fp32 values.  Decays below 2^-150 count as that.
  * bf16 with dk = 128 and dv in {64, 128}, or both 64, runs on the tensor cores in chunks of 128 tokens: the pairs' weights
  * and the state as an operand are rounded to bf16 (2^-9 of a term each, as much as out's own rounding), what enters the
@@ -415,9 +417,10 @@ int mesa_ssm_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dt
  * dtype | MESA_GATE_GRADS_F32, the last four in fp32 like their parameters.  dS0: NULL or [B, H, dv, dk] fp32 (it may be
  * dS_final's memory).  The states are recomputed; every sum has a fixed order.  S0 as given to the forward.
  * Other arguments, sizes, alignment (dout and the gradients too) and errors as the forward (MESA_ERR_NONFINITE: dq, dk, dv
- * or ddt is not finite).  On the tensor cores states and adjoints are bf16 operands (2^-9) and so are the pairs' weights,
- * dS0 as S_final; the pairs' share of ddt stays fp32, so that ddt is 3e-4 off before its rounding, dA up to 1e-3 of its norm
- * over the heads.
+ * or ddt is not finite).  What is not finite in a token's q, k, v or dout reaches the gradients whose formulas hold it, no others
+ * (of its own document); a dt_t that is not the unit's, those of dq before t excepted.
+ * On the tensor cores states and adjoints are bf16 operands (2^-9) and so are the pairs' weights, dS0 as S_final; the
+ * pairs' share of ddt stays fp32, so that ddt is 3e-4 off before its rounding, dA up to 1e-3 of its norm over the heads.
  */
 size_t mesa_ssm_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 int mesa_ssm_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q, const void *k,

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kFew) mesa_ssm_out_kernel(SsmArgs a, SsmWorksp
   for (int i = 0; i < 4; i++)
 #pragma unroll
     for (int j = 0; j < DV / 16; j++) acc[i][j] = g.s[ty + TY * i] < 0 ? acc[i][j] * g.f[ty + TY * i] : 0.0f;
-  mm_nn<TY, C>(acc, M, LDC, v, DV + 4, ty, tx);
+  mm_lower<TY>(acc, M, LDC, v, DV + 4, ty, tx);
   const float skip = a.skip ? a.skip[u % a.H] : 0.0f;
   bool bad = false;
 #pragma unroll

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kGradThreads<DK, DV>) mesa_ssm_grads_kernel(Ss
     for (int i = 0; i < RI; i++)
 #pragma unroll
       for (int j = 0; j < PART / 16; j++) acc[i][j] *= ga.c[ty + TY * i];
-    mm_tn<TY, C>(acc, M, LDC, g + p0, LV, ty, tx);
+    mm_lower_t<TY>(acc, M, LDC, g + p0, LV, ty, tx);
 #pragma unroll
     for (int i = 0; i < RI; i++) {
       const int row = ty + TY * i;
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kGradThreads<DK, DV>) mesa_ssm_grads_kernel(Ss
     out = sum16(out);
     if (tx == 0) duv[row] = x, x_in[row] = in, x_out[row] = out;
   }
-  mm_nn<TY, C>(aq, W, LDC, k, LK, ty, tx);
-  mm_tn<TY, C>(ak, W, LDC, q, LK, ty, tx);
+  mm_lower<TY>(aq, W, LDC, k, LK, ty, tx);
+  mm_lower_t<TY>(ak, W, LDC, q, LK, ty, tx);
 #pragma unroll
   for (int i = 0; i < RI; i++)
 #pragma unroll

@@ -35,7 +35,12 @@ struct GradMisc {
   uint64_t full1, full2, c1, c2, e, fg, h, a_done, b_done, c_done, f_done, qk_staged, v_staged, drain;
   uint32_t tmem;
   int gave_up;
+  int odd;  // something of a token of the chunk's is not finite
 };
+// Marks of chunks that hold what is not finite, by column, in the gates' place once these have been read: the first such row of
+// K, the last of Q and of G plus one (they reach the gradients from there on, or up to there).
+constexpr int MARK_K = 0, MARK_Q = DK, MARK_G = 2 * DK, MARKS = R_START;
+static_assert(MARK_G + 128 <= (REC - MARKS) * 4, "the gates' part that the columns' sums leave");
 template <int P>
 constexpr uint32_t kGradSmem = Grad<P>::MISC + sizeof(GradMisc);
 static_assert(kGradSmem<128> <= 232448, "shared memory per block");
@@ -63,6 +68,57 @@ __device__ __forceinline__ float transposed_sum(float (&x)[8], int lane) {
   float y = x[0];
   y += __shfl_xor_sync(0xffffffffu, y, 8);
   return y + __shfl_xor_sync(0xffffffffu, y, 16);
+}
+// What is not finite in one token's row meets the zeros of the tokens that it has nothing to do with, in W K, W^T Q and M'^T g
+// (ssm_tc.cuh).  By a whole warp, in chunks that have any: what is not finite in the rows of K, Q and G goes to marks and is
+// taken out of the tiles, and M' and W get their zeros above the diagonal (formed as 0 times what is not finite, they are not).
+template <int P>
+__device__ __noinline__ void take_out(uint8_t *sm, uint8_t *marks, int lane) {
+  using O = Grad<P>;
+  const int c = lane & 15;  // half a warp a tile, a lane eight columns
+#pragma unroll 1
+  for (int i = lane >> 4; i < 3; i += 2) {
+    uint8_t *tile = sm + (i == 0 ? O::K : i == 1 ? 0 : O::G), *to = marks + (i == 0 ? MARK_K : i == 1 ? MARK_Q : MARK_G) + 8 * c;
+    if (i == 2 && 8 * c >= P) break;
+    for (int e = 0; e < 8; e++) to[e] = i == 0 ? kNoRow : 0;
+#pragma unroll 1
+    for (int t = 0; t < L; t++) {
+      uint4 *at = reinterpret_cast<uint4 *>(tile + tile_off(t, c, L));
+      if (!odd_words(*at)) continue;
+      uint16_t *x = reinterpret_cast<uint16_t *>(at);
+      for (int e = 0; e < 8; e++)
+        if (odd_word(x[e])) {
+          x[e] = 0;
+          to[e] = (uint8_t)(i == 0 ? min((int)to[e], t) : t + 1);
+        }
+    }
+  }
+#pragma unroll 1
+  for (int t = lane >> 4; t < L; t += 2)
+#pragma unroll 1
+    for (int e = max(t + 1 - 8 * c, 0); e < 8; e++) *word_at(sm + O::M, t, 8 * c + e) = *word_at(sm + O::W, t, 8 * c + e) = 0;
+  tc::fence_smem_to_async();
+  __syncwarp();
+}
+// NaN in the gradients of row t that marks say (from where they leave, or in the heads' parts in memory); whether there is any.
+// (Calls, so that the usual chunk's code stays as short as without.)
+__device__ __noinline__ bool spoil_qk(uint8_t *q, uint8_t *k, const uint8_t *marks, int t, int n0, float *dq, float *dk) {
+  bool any = false;
+  for (int n = n0; n < n0 + 32; n++) {
+    const bool a = marks[MARK_K + n] <= t, b = marks[MARK_Q + n] > t;
+    any |= a || b;
+    if (a) *word_at(q, t, n) = 0x7fff;
+    if (b) *word_at(k, t, n) = 0x7fff;
+    if (a && dq) dq[n] = NAN;
+    if (b && dk) dk[n] = NAN;
+  }
+  return any;
+}
+__device__ __noinline__ bool spoil_v(uint8_t *v, const uint8_t *marks, int t, int p0, int n) {
+  bool any = false;
+  for (int p = p0; p < p0 + n; p++)
+    if (marks[MARK_G + p] > t) any = true, *word_at(v, t, p) = 0x7fff;
+  return any;
 }
 // L2 prefetches of what the next chunk's copies will read.
 __device__ __forceinline__ void prefetch_tile(const void *map, int x, int y, int z) {
@@ -99,12 +155,14 @@ __global__ void __launch_bounds__(576, 1)
     for (uint64_t *b : {&m->full1, &m->full2, &m->c1, &m->c2, &m->e, &m->fg, &m->h, &m->drain}) tc::mbar_init(bar(*b), 1);
     for (uint64_t *b : {&m->a_done, &m->b_done, &m->c_done, &m->qk_staged, &m->v_staged}) tc::mbar_init(bar(*b), 16);
     tc::mbar_init(bar(m->f_done), 4);
-    m->gave_up = 0;
+    m->gave_up = m->odd = 0;
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = __shfl_sync(0xffffffffu, m->tmem, 0);
+  uint8_t *const marks = reinterpret_cast<uint8_t *>(m->rec + MARKS);
+  auto odd = [&]() { return *static_cast<volatile int *>(&m->odd) != 0; };
   auto warp_arrive = [&](uint64_t &b) {  // one arrival per warp, after what its lanes did
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
@@ -270,6 +328,7 @@ __global__ void __launch_bounds__(576, 1)
           piece(cc + 1, x[1], y[1]);
         }
         row = sum2(row2);
+        if (b == w && !isfinite(diag * step)) m->odd = 1;  // ((q . k) (g . v) D: something of this row's is not)
       } else {
 #pragma unroll
         for (int cc = 0; cc < 4; cc++) {
@@ -325,7 +384,9 @@ __global__ void __launch_bounds__(576, 1)
           tc::tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; j++) {
-            y[j] = lane >= 8 * cc + j ? run : 0.0f;
+            const bool on = lane >= 8 * cc + j;  // (above the diagonal: 0 times what may not be finite)
+            if (!on) x[j] = 0.0f;
+            y[j] = on ? run : 0.0f;
             run = fmaf(x[j], __shfl_sync(0xffffffffu, step, 8 * cc + j), run);
           }
           const float pairs = transposed_sum(y, lane), sum = transposed_sum(x, lane);
@@ -372,8 +433,13 @@ __global__ void __launch_bounds__(576, 1)
           }
         }
       };
+      const bool marked = odd();
       put(T_DQ, sm, dqp);
       put(T_DK, sm + O::K, dkp);
+      if (marked && 32 * b < N) {
+        const size_t row = in ? ((size_t)u * a.T + c * L + t) * N : 0;
+        if (spoil_qk(sm, sm + O::K, marks, t, 32 * b, dqp && in ? dqp + row : nullptr, dqp && in ? dkp + row : nullptr) && in) bad = 0x7fff;
+      }
       tc::fence_smem_to_async();
       warp_arrive(m->qk_staged);
       // ---- dV ----
@@ -407,6 +473,7 @@ __global__ void __launch_bounds__(576, 1)
           *reinterpret_cast<uint4 *>(sm + O::G + to) = y;
           if (in) bad = rule::absmax_words(bad, y);
         }
+        if (marked && spoil_v(sm + O::G, marks, t, V * b, V) && in) bad = 0x7fff;
         tc::fence_before_sync();
         tc::fence_smem_to_async();
         warp_arrive(m->v_staged);
@@ -415,6 +482,7 @@ __global__ void __launch_bounds__(576, 1)
         ok = false;
         break;
       }
+      if (tid == 0) m->odd = 0;
       if (!teller) continue;
       tc::fence_after_sync();
       float x[16];
@@ -469,6 +537,10 @@ __global__ void __launch_bounds__(576, 1)
         tc::mma_commit(bar(m->e));
       }
       if (!need(m->b_done, par)) break;
+      if (odd()) {
+        if (!need(m->e, par)) break;  // (K R^T has read K)
+        take_out<P>(sm, marks, lane);
+      }
       if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_DQ, wk + step128(s), kmn + step_mn(s), idB, true);

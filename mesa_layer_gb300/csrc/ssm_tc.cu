@@ -7,6 +7,10 @@
 // those of a segment of it) with the state in tensor memory; q, k and v are read and o is written once.  Warps: four turn
 // Q K^T into M, four write the outputs, eight turn the state into the next operand and weigh K's rows, one issues the
 // products, one the copies.  Two chains run side by side, Q K^T -> M -> M V and state -> Q S^T -> state.
+// In M V what is not finite in a value meets the zeros of the tokens before it.  A walk whose outputs are not all finite is
+// done over, this time with a look at the values of each chunk before M V (ssm_tc.cuh; in every walk that took 1 to 5 % of its time).
+#include <type_traits>
+
 #include "launch.h"
 #include "ssm_tc.cuh"
 
@@ -95,6 +99,8 @@ struct Fwd {
 };
 struct FwdMisc {
   float cw[2][L], log[L], step[L];  // step and decay from a token to its warp's end; for the diagonal blocks
+  uint8_t marks[2][L];  // (a walk done over) by channel, the first row of the chunk's values that is not finite, kNoRow: none
+  int again;            // an output was not finite: another walk
   uint64_t full[2], y_staged[2], st_done[2], g_full, m_full, y_full, y_free, s_full, w_full, cs_done, drain;
   uint32_t tmem;
   int gave_up;
@@ -129,7 +135,7 @@ __global__ void __launch_bounds__(576, 1)
       tc::mbar_init(bar(*b), 1);
     for (uint64_t *b : {&m->m_full, &m->y_free, &m->y_staged[0], &m->y_staged[1]}) tc::mbar_init(bar(*b), 4);
     for (uint64_t *b : {&m->s_full, &m->w_full}) tc::mbar_init(bar(*b), 8);
-    m->gave_up = 0;
+    m->gave_up = m->again = 0;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -151,220 +157,266 @@ __global__ void __launch_bounds__(576, 1)
   const uint32_t tl = tbase + ((uint32_t)(32 * w) << 16);
 
   if (warp != 17) ahead_done();  // (the records, the segments' states; the copies are of the call's inputs)
-  if (warp < 4) {
-    // ---- M ----
-    const float *r = record(records, u, NCT, c0);
-    float out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
-    for (int c = 0; c < NC; c++) {
-      const uint32_t ph = c & 1;
-      const int s = __float_as_int(start);
-      const float mine = log, from = in;
-      const float *between = r + R_BETWEEN + 4 * w;
-      m->cw[ph][t] = out * step;
-      m->log[t] = log;
-      m->step[t] = step;
-      if (c + 1 < NC) {
-        r += REC;
-        out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
-      }
-      if (group_or(1, 128, !ok)) {  // (also: the others' columns)
-        ok = false;
-        break;
-      }
-      need(m->g_full, ph);
-#pragma unroll 1
-      for (int b = 0; b < w; b++) {  // tokens of an earlier warp: through the end of theirs
-        float x[32], o[16];
-        tc::tmem_ld32(tl + T_G + 32 * b, x);
-        const float f = between[b] * from;
-        const u64 f2 = pack2(f, f);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&m->cw[ph][32 * b + 4 * i]);
-          o[2 * i] = __uint_as_float(bf2(mul2(pack2(x[4 * i], x[4 * i + 1]), mul2(f2, y.x))));
-          o[2 * i + 1] = __uint_as_float(bf2(mul2(pack2(x[4 * i + 2], x[4 * i + 3]), mul2(f2, y.y))));
+  // Step n of the barriers is chunk n - n0: a walk done over goes on with their phases.  (Code of its own: with the same code
+  // for both the first walk is 1 to 5 % slower.)
+  auto walk = [&](auto over) {
+    constexpr bool OVER = decltype(over)::value;
+    const int n0 = OVER ? NC : 0;
+    if (warp < 4) {
+      // ---- M ----
+      const float *r = record(records, u, NCT, c0);
+      float out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
+      for (int c = 0; c < NC; c++) {
+        const int n = n0 + c;
+        const uint32_t ph = n & 1;
+        const int s = __float_as_int(start);
+        const float mine = log, from = in;
+        const float *between = r + R_BETWEEN + 4 * w;
+        m->cw[ph][t] = out * step;
+        m->log[t] = log;
+        m->step[t] = step;
+        if (c + 1 < NC) {
+          r += REC;
+          out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
         }
-        tc::tmem_st16(tl + T_G + 16 * b, o);
-      }
-      {
-        float x[32], o[16];
-        tc::tmem_ld32(tl + T_G + 32 * w, x);
-        const int first = max(s - 32 * w, 0);
-        const uint32_t on = (0xffffffffu >> (31 - lane)) & (0xffffffffu << first);  // the columns that count
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-          const float4 l = *reinterpret_cast<const float4 *>(&m->log[32 * w + 4 * i]);
-          const float4 y = *reinterpret_cast<const float4 *>(&m->step[32 * w + 4 * i]);
-          auto one = [&](int j, float lj, float sj) { return on >> j & 1 ? x[j] * (rule::ex2(mine - lj) * sj) : 0.0f; };
-          o[2 * i] = __uint_as_float(bf2(one(4 * i, l.x, y.x), one(4 * i + 1, l.y, y.y)));
-          o[2 * i + 1] = __uint_as_float(bf2(one(4 * i + 2, l.z, y.z), one(4 * i + 3, l.w, y.w)));
+        if (group_or(1, 128, !ok)) {  // (also: the others' columns)
+          ok = false;
+          break;
         }
-        tc::tmem_st16(tl + T_G + 16 * w, o);
-#pragma unroll
-        for (int i = 0; i < 16; i++) o[i] = 0.0f;
-#pragma unroll 1
-        for (int b = w + 1; b < 4; b++) tc::tmem_st16(tl + T_G + 16 * b, o);
-      }
-      tc::tmem_st_wait();
-      tc::fence_before_sync();
-      warp_arrive(m->m_full);
-    }
-  } else if (warp < 8) {
-    // ---- outputs: from tensor memory to the place of Q, and out from there ----
-    const float skip = a.skip ? a.skip[h] : 0.0f;
-    const u64 skip2 = pack2(skip, skip);
-    const float *r = record(records, u, NCT, c0);
-    float f = r[R_IN + t] * r[R_FIRST + w];
-    uint32_t bad = 0;
-    for (int c = 0; c < NC; c++) {
-      const uint32_t ph = c & 1;
-      uint8_t *X = sm + Fwd<P>::V + ph * V_TILE<P>, *Y = sm + ph * QK_TILE;
-      const u64 f2 = pack2(f, f);
-      const bool in = (c0 + c) * L + t < a.T;
-      if (c + 1 < NC) {
-        r += REC;
-        f = r[R_IN + t] * r[R_FIRST + w];
-      }
-      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->y_full, ph)) break;
-#pragma unroll 1
-      for (int hh = 0; hh < P / 16; hh++) {
-        float p[16], q[16];
-        tc::tmem_ld16(tl + T_Y1 + 16 * hh, p);
-        tc::tmem_ld16(tl + T_Y2 + 16 * hh, q);
-        const uint32_t at[2] = {tile_off(t, 2 * hh, L), tile_off(t, 2 * hh + 1, L)};
-        const uint4 x[2] = {*reinterpret_cast<const uint4 *>(X + at[0]), *reinterpret_cast<const uint4 *>(X + at[1])};
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int e = 8 * k + 2 * i;
-            u64 y = fma2(f2, pack2(p[e], p[e + 1]), pack2(q[e], q[e + 1]));
-            if (a.skip) y = fma2(skip2, of_bf2(xs[i]), y);
-            o[i] = bf2(y);
+        need(m->g_full, ph);
+        if (OVER && t < P) {  // channel t of the values (M V waits for this)
+          // (The marks of two chunks before have been used: these scores follow the last chunk's products, and those the outputs.)
+          need(m->full[ph], (n >> 1) & 1);
+          uint8_t *V = sm + Fwd<P>::V + ph * V_TILE<P>;
+          int first = kNoRow;
+          for (int i = L - 1; i >= 0; i--) {
+            uint16_t *x = word_at(V, i, t);
+            if (odd_word(*x)) *x = 0, first = i;
           }
-          const uint4 y = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4 *>(Y + at[k]) = y;
-          if (in) bad = rule::absmax_words(bad, y);
+          m->marks[ph][t] = (uint8_t)first;
+          tc::fence_smem_to_async();
+        }
+#pragma unroll 1
+        for (int b = 0; b < w; b++) {  // tokens of an earlier warp: through the end of theirs
+          float x[32], o[16];
+          tc::tmem_ld32(tl + T_G + 32 * b, x);
+          const float f = between[b] * from;
+          const u64 f2 = pack2(f, f);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&m->cw[ph][32 * b + 4 * i]);
+            o[2 * i] = __uint_as_float(bf2(mul2(pack2(x[4 * i], x[4 * i + 1]), mul2(f2, y.x))));
+            o[2 * i + 1] = __uint_as_float(bf2(mul2(pack2(x[4 * i + 2], x[4 * i + 3]), mul2(f2, y.y))));
+          }
+          tc::tmem_st16(tl + T_G + 16 * b, o);
+        }
+        {
+          float x[32], o[16];
+          tc::tmem_ld32(tl + T_G + 32 * w, x);
+          const int first = max(s - 32 * w, 0);
+          const uint32_t on = (0xffffffffu >> (31 - lane)) & (0xffffffffu << first);  // the columns that count
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const float4 l = *reinterpret_cast<const float4 *>(&m->log[32 * w + 4 * i]);
+            const float4 y = *reinterpret_cast<const float4 *>(&m->step[32 * w + 4 * i]);
+            auto one = [&](int j, float lj, float sj) { return on >> j & 1 ? x[j] * (rule::ex2(mine - lj) * sj) : 0.0f; };
+            o[2 * i] = __uint_as_float(bf2(one(4 * i, l.x, y.x), one(4 * i + 1, l.y, y.y)));
+            o[2 * i + 1] = __uint_as_float(bf2(one(4 * i + 2, l.z, y.z), one(4 * i + 3, l.w, y.w)));
+          }
+          tc::tmem_st16(tl + T_G + 16 * w, o);
+#pragma unroll
+          for (int i = 0; i < 16; i++) o[i] = 0.0f;
+#pragma unroll 1
+          for (int b = w + 1; b < 4; b++) tc::tmem_st16(tl + T_G + 16 * b, o);
+        }
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        warp_arrive(m->m_full);
+      }
+    } else if (warp < 8) {
+      // ---- outputs: from tensor memory to the place of Q, and out from there ----
+      const float skip = a.skip ? a.skip[h] : 0.0f;
+      const u64 skip2 = pack2(skip, skip);
+      const float *r = record(records, u, NCT, c0);
+      float f = r[R_IN + t] * r[R_FIRST + w];
+      uint32_t bad = 0;
+      for (int c = 0; c < NC; c++) {
+        const int n = n0 + c;
+        const uint32_t ph = n & 1;
+        uint8_t *X = sm + Fwd<P>::V + ph * V_TILE<P>, *Y = sm + ph * QK_TILE;
+        const u64 f2 = pack2(f, f);
+        const bool in = (c0 + c) * L + t < a.T;
+        if (c + 1 < NC) {
+          r += REC;
+          f = r[R_IN + t] * r[R_FIRST + w];
+        }
+        if (!need(m->full[ph], (n >> 1) & 1) || !need(m->y_full, ph)) break;
+#pragma unroll 1
+        for (int hh = 0; hh < P / 16; hh++) {
+          float p[16], q[16];
+          tc::tmem_ld16(tl + T_Y1 + 16 * hh, p);
+          tc::tmem_ld16(tl + T_Y2 + 16 * hh, q);
+          const uint32_t at[2] = {tile_off(t, 2 * hh, L), tile_off(t, 2 * hh + 1, L)};
+          const uint4 x[2] = {*reinterpret_cast<const uint4 *>(X + at[0]), *reinterpret_cast<const uint4 *>(X + at[1])};
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 2; k++) {
+            const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              const int e = 8 * k + 2 * i;
+              u64 y = fma2(f2, pack2(p[e], p[e + 1]), pack2(q[e], q[e + 1]));
+              if (a.skip) y = fma2(skip2, of_bf2(xs[i]), y);
+              o[i] = bf2(y);
+            }
+            const uint4 y = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(Y + at[k]) = y;
+            if (in) bad = rule::absmax_words(bad, y);
+          }
+        }
+        if constexpr (OVER) {
+          for (int p = 0; p < P; p++)
+            if (m->marks[ph][p] <= t) {
+              *word_at(Y, t, p) = 0x7fff;  // NaN
+              if (in) bad = 0x7fff;
+            }
+        }
+        tc::fence_before_sync();
+        warp_arrive(m->y_free);
+        tc::fence_smem_to_async();
+        warp_arrive(m->y_staged[ph]);
+      }
+      if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) {
+        if constexpr (OVER)
+          atomicOr(a.status, tc::kErrNonFinite);
+        else
+          m->again = 1;
+      }
+    } else if (warp < 16) {
+      // ---- the state, then K's rows weighed: two warps for each 32 lanes (rows), half of the columns each ----
+      const int hf = warp < 12 ? 0 : 1, h0 = hf * P / 64, h1 = h0 + P / 64;
+      const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * N : a.S0 ? a.S0 + (size_t)u * P * N : nullptr;
+      const float *r = record(records, u, NCT, c0);
+      float next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w], left = r[R_ALL];
+      for (int c = 0; c < NC; c++) {
+        const int n = n0 + c;
+        const uint32_t ph = n & 1;
+        const float mine = next, all = left;
+        if (c + 1 < NC) {
+          r += REC;
+          next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
+          left = r[R_ALL];
+        }
+        if (n > 0 && !need(m->st_done[ph ^ 1], ((n - 1) >> 1) & 1)) break;
+        state_step<N>(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0, h0, h1);
+        tc::fence_smem_to_async();
+        tc::fence_before_sync();
+        warp_arrive(m->s_full);
+        // (Q K^T has read K, Q S^T the state)
+        if (!need(m->full[ph], (n >> 1) & 1) || !need(m->cs_done, ph)) break;
+        weigh_row(sm + Fwd<P>::K + ph * QK_TILE, sm + Fwd<P>::S, t, mine, 8 * hf, 8 * hf + 8);
+        tc::fence_smem_to_async();
+        warp_arrive(m->w_full);
+      }
+      if (ok) need(m->st_done[(n0 + NC - 1) & 1], ((n0 + NC - 1) >> 1) & 1);
+    } else if (warp == 16) {
+      // ---- products ----
+      const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
+                     idS = idesc_bf16(128, P, true, true);
+      const uint32_t sS = tc::smem_u32(sm + Fwd<P>::S);
+      const uint64_t sd = tc::mnmajor_desc(sS, L, 0);  // (the state, or the rests: the same form)
+      auto scores = [&](int n) -> bool {  // Q K^T of step n
+        const uint32_t ph = n & 1;
+        if (!need(m->full[ph], (n >> 1) & 1)) return false;
+        if (elect_one()) {
+          const uint64_t q = tc::kmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
+                         k = tc::kmajor_desc(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), L, 0);
+#pragma unroll
+          for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
+          tc::mma_commit(bar(m->g_full));
+        }
+        return true;
+      };
+      scores(n0);
+      for (int n = n0; ok && n < n0 + NC; n++) {
+        const uint32_t ph = n & 1, q = tc::smem_u32(sm + ph * QK_TILE), k = tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE),
+                       v = tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>);
+        const uint64_t vd = tc::mnmajor_desc(v, L, 0), kd = tc::mnmajor_desc(k, L, 0);
+        if (!need(m->s_full, ph) || (n > 0 && !need(m->y_free, ph ^ 1))) break;
+        if (elect_one()) {
+          const uint64_t qd = tc::kmajor_desc(q, L, 0);
+#pragma unroll
+          for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
+          tc::mma_commit(bar(m->cs_done));
+        }
+        if (!need(m->m_full, ph)) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16_ts(tbase + T_Y2, tbase + T_G + 8 * s, vd + step_mn(s), idY, s > 0);
+          tc::mma_commit(bar(m->y_full));
+        }
+        if constexpr (OVER) {  // what was taken out of the values belongs in the state: a NaN for each channel that had any
+          if (!need(m->y_full, ph)) break;
+          for (int p = lane; p < P; p += 32)
+            if (m->marks[ph][p] != kNoRow) *word_at(sm + Fwd<P>::V + ph * V_TILE<P>, m->marks[ph][p], p) = 0x7fff;
+          tc::fence_smem_to_async();
+          __syncwarp();
+        }
+        if (!need(m->w_full, ph)) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, kd + step_mn(s), vd + step_mn(s), idS, true);
+#pragma unroll
+          for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, sd + step_mn(s), vd + step_mn(s), idS, true);
+          tc::mma_commit(bar(m->st_done[ph]));
+        }
+        if (n + 1 < n0 + NC && need(m->y_full, ph)) scores(n + 1);  // (M has been read)
+      }
+    } else if (lane == 0) {
+      // ---- copies ----
+      const int uk = a.qk_unit(u);
+      auto at = [&](uint32_t where, int c) { return tc::smem_u32(sm + where) + ((n0 + c) & 1) * (where == Fwd<P>::V ? V_TILE<P> : QK_TILE); };
+      auto fetch_kv = [&](int c) {
+        const uint32_t b = bar(m->full[(n0 + c) & 1]);
+        tc::mbar_arrive_expect_tx(b, 2 * L * N * 2 + V_TILE<P>);
+        load_tile<N>(at(Fwd<P>::K, c), &mapK, (c0 + c) * L, uk, b);
+        load_tile<P>(at(Fwd<P>::V, c), &mapV, (c0 + c) * L, u, b);
+      };
+      auto fetch_q = [&](int c) { load_tile<N>(at(0, c), &mapQ, (c0 + c) * L, uk, bar(m->full[(n0 + c) & 1])); };
+      for (int c = 0; c < min(NC, 2); c++, sent++) {
+        fetch_kv(c);
+        fetch_q(c);
+      }
+      ahead_done();
+      for (int c = 0; c < NC; c++) {
+        const int n = n0 + c;
+        const uint32_t ph = n & 1, par = (n >> 1) & 1;
+        if (!(ok = wait(bar(m->y_staged[ph]), par, limit, gave_up))) break;
+#pragma unroll
+        for (int i = 0; i < P / 64; i++) tensor_s2g_3d(&mapO, at(0, c) + i * HALF, 64 * i, (c0 + c) * L, u);
+        tc::bulk_commit();
+        if (!(ok = wait(bar(m->st_done[ph]), par, limit, gave_up))) break;
+        if (c + 2 < NC) {
+          fetch_kv(c + 2);
+          tc::bulk_wait_read();
+          fetch_q(c + 2);
+          sent++;
         }
       }
-      tc::fence_before_sync();
-      warp_arrive(m->y_free);
-      tc::fence_smem_to_async();
-      warp_arrive(m->y_staged[ph]);
+      tc::bulk_wait_all();
     }
-    if (ok && max(bad & 0xffffu, bad >> 16) >= 0x7f80u) atomicOr(a.status, tc::kErrNonFinite);
-  } else if (warp < 16) {
-    // ---- the state, then K's rows weighed: two warps for each 32 lanes (rows), half of the columns each ----
-    const int hf = warp < 12 ? 0 : 1, h0 = hf * P / 64, h1 = h0 + P / 64;
-    const float *S0 = sg.n > 1 ? sg.S + ((size_t)u * sg.n + seg) * P * N : a.S0 ? a.S0 + (size_t)u * P * N : nullptr;
-    const float *r = record(records, u, NCT, c0);
-    float next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w], left = r[R_ALL];
-    for (int c = 0; c < NC; c++) {
-      const uint32_t ph = c & 1;
-      const float mine = next, all = left;
-      if (c + 1 < NC) {
-        r += REC;
-        next = r[R_OUT + t] * r[R_STEP + t] * r[R_LAST + w];
-        left = r[R_ALL];
-      }
-      if (c > 0 && !need(m->st_done[ph ^ 1], ((c - 1) >> 1) & 1)) break;
-      state_step<N>(tl + T_S, sm + Fwd<P>::S, t, all, c == 0, S0, h0, h1);
-      tc::fence_smem_to_async();
-      tc::fence_before_sync();
-      warp_arrive(m->s_full);
-      // (Q K^T has read K, Q S^T the state)
-      if (!need(m->full[ph], (c >> 1) & 1) || !need(m->cs_done, ph)) break;
-      weigh_row(sm + Fwd<P>::K + ph * QK_TILE, sm + Fwd<P>::S, t, mine, 8 * hf, 8 * hf + 8);
-      tc::fence_smem_to_async();
-      warp_arrive(m->w_full);
-    }
-    if (ok && need(m->st_done[(NC - 1) & 1], ((NC - 1) >> 1) & 1) && a.S_final && seg == sg.n - 1)
-      state_out<N>(tl + T_S, a.S_final + (size_t)u * P * N, t, h0, h1);
-  } else if (warp == 16) {
-    // ---- products ----
-    const uint32_t idG = idesc_bf16(128, 128, false, false), idY = idesc_bf16(128, P, false, true),
-                   idS = idesc_bf16(128, P, true, true);
-    const uint32_t sS = tc::smem_u32(sm + Fwd<P>::S);
-    const uint64_t sd = tc::mnmajor_desc(sS, L, 0);  // (the state, or the rests: the same form)
-    auto scores = [&](int c) -> bool {  // Q K^T of chunk c
-      const uint32_t ph = c & 1;
-      if (!need(m->full[ph], (c >> 1) & 1)) return false;
-      if (elect_one()) {
-        const uint64_t q = tc::kmajor_desc(tc::smem_u32(sm + ph * QK_TILE), L, 0),
-                       k = tc::kmajor_desc(tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE), L, 0);
-#pragma unroll
-        for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_G, q + step128(s), k + step128(s), idG, s > 0);
-        tc::mma_commit(bar(m->g_full));
-      }
-      return true;
-    };
-    scores(0);
-    for (int c = 0; ok && c < NC; c++) {
-      const uint32_t ph = c & 1, q = tc::smem_u32(sm + ph * QK_TILE), k = tc::smem_u32(sm + Fwd<P>::K + ph * QK_TILE),
-                     v = tc::smem_u32(sm + Fwd<P>::V + ph * V_TILE<P>);
-      const uint64_t vd = tc::mnmajor_desc(v, L, 0), kd = tc::mnmajor_desc(k, L, 0);
-      if (!need(m->s_full, ph) || (c > 0 && !need(m->y_free, (c - 1) & 1))) break;
-      if (elect_one()) {
-        const uint64_t qd = tc::kmajor_desc(q, L, 0);
-#pragma unroll
-        for (int s = 0; s < N / 16; s++) tc::mma_f16(tbase + T_Y1, qd + step128(s), sd + step_mn(s), idY, s > 0);
-        tc::mma_commit(bar(m->cs_done));
-      }
-      if (!need(m->m_full, ph)) break;
-      if (elect_one()) {
-#pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16_ts(tbase + T_Y2, tbase + T_G + 8 * s, vd + step_mn(s), idY, s > 0);
-        tc::mma_commit(bar(m->y_full));
-      }
-      if (!need(m->w_full, ph)) break;
-      if (elect_one()) {
-#pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, kd + step_mn(s), vd + step_mn(s), idS, true);
-#pragma unroll
-        for (int s = 0; s < 8; s++) tc::mma_f16(tbase + T_S, sd + step_mn(s), vd + step_mn(s), idS, true);
-        tc::mma_commit(bar(m->st_done[ph]));
-      }
-      if (c + 1 < NC && need(m->y_full, ph)) scores(c + 1);  // (M has been read)
-    }
-  } else if (lane == 0) {
-    // ---- copies ----
-    const int uk = a.qk_unit(u);
-    auto at = [&](uint32_t where, int c) { return tc::smem_u32(sm + where) + (c & 1) * (where == Fwd<P>::V ? V_TILE<P> : QK_TILE); };
-    auto fetch_kv = [&](int c) {
-      const uint32_t b = bar(m->full[c & 1]);
-      tc::mbar_arrive_expect_tx(b, 2 * L * N * 2 + V_TILE<P>);
-      load_tile<N>(at(Fwd<P>::K, c), &mapK, (c0 + c) * L, uk, b);
-      load_tile<P>(at(Fwd<P>::V, c), &mapV, (c0 + c) * L, u, b);
-    };
-    auto fetch_q = [&](int c) { load_tile<N>(at(0, c), &mapQ, (c0 + c) * L, uk, bar(m->full[c & 1])); };
-    for (; sent < min(NC, 2); sent++) {
-      fetch_kv(sent);
-      fetch_q(sent);
-    }
-    ahead_done();
-    for (int c = 0; c < NC; c++) {
-      const uint32_t ph = c & 1, par = (c >> 1) & 1;
-      if (!(ok = wait(bar(m->y_staged[ph]), par, limit, gave_up))) break;
-#pragma unroll
-      for (int i = 0; i < P / 64; i++) tensor_s2g_3d(&mapO, at(0, c) + i * HALF, 64 * i, (c0 + c) * L, u);
-      tc::bulk_commit();
-      if (!(ok = wait(bar(m->st_done[ph]), par, limit, gave_up))) break;
-      if (c + 2 < NC) {
-        fetch_kv(c + 2);
-        tc::bulk_wait_read();
-        fetch_q(c + 2);
-        sent++;
-      }
-    }
-    tc::bulk_wait_all();
+    if (!ok) *gave_up = 1;
+    __syncthreads();
+  };
+  walk(std::false_type());
+  if (!*gave_up && m->again) walk(std::true_type());
+  if (a.S_final && seg == sg.n - 1 && warp >= 8 && warp < 16 && !*gave_up) {
+    const int hf = warp < 12 ? 0 : 1;
+    state_out<N>(tl + T_S, a.S_final + (size_t)u * P * N, t, hf * P / 64, (hf + 1) * P / 64);
   }
-  if (!ok) *gave_up = 1;
-  __syncthreads();
   // a wait gave up: products and copies still in flight finish before the memory is released
   if (*gave_up) {
     if (warp == 16 && elect_one()) tc::mma_commit(bar(m->drain));

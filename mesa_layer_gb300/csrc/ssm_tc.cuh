@@ -84,6 +84,19 @@ __device__ __forceinline__ void weigh_row(uint8_t *tile, uint8_t *rest, int t, f
   }
 }
 
+// What is not finite in a token's row must not reach the outputs (or gradients) of tokens on the other side of it, but a matrix
+// product multiplies it by their zeros.  So the chunks that hold any (rare) have it taken out of the tile (zeros) before the
+// product, with a mark for each column from which row, or up to which, the product's column is not finite: NaN is put there after.
+constexpr int kNoRow = 128;
+__device__ __forceinline__ bool odd_word(uint32_t x) { return (x & 0x7f80u) == 0x7f80u; }  // a bf16 value that is not finite
+__device__ __forceinline__ bool odd_words(uint4 x) {
+  const uint32_t m = rule::absmax_words(0, x);
+  return max(m & 0xffffu, m >> 16) >= 0x7f80u;
+}
+__device__ __forceinline__ uint16_t *word_at(uint8_t *tile, int row, int column) {
+  return reinterpret_cast<uint16_t *>(tile + tile_off(row, column >> 3, L)) + (column & 7);
+}
+
 // Columns 32 h0 .. 32 h1 - 1 of lane n of the state in tensor memory (from global memory [P][dk], or zero, where `first`)
 // become the operand row n at `op` (nullptr: none), and are multiplied by `all` where they lie.
 template <int N>
