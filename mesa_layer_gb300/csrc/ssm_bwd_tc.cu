@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(576, 1)
       need(m->full2, par);  // (a warp that gives up goes on to the next barrier with the others)
       const float *r = m->rec;
       const float r_in = r[R_IN + t], step = r[R_STEP + t], f = r_in * r[R_FIRST + w], ct = r[R_OUT + t] * r[R_LAST + w],
-                  mine = r[R_LOG + t], across = r[R_ALL];
-      const int start = __float_as_int(r[R_START + t]);
+                  mine = r[R_LOG + t], mine_lo = lo_of(r, t), across = r[R_ALL];
+      const int start = start_of(r, t);
       {
         u64 x2 = 0;
 #pragma unroll 2
@@ -268,6 +268,8 @@ __global__ void __launch_bounds__(576, 1)
         u64 row2 = 0;
         const uint32_t on = b < w ? 0xffffffffu : (0xffffffffu >> (31 - lane)) & (0xffffffffu << max(start - 32 * w, 0));  // columns that count
         const float *rj = r + (b < w ? R_OUT : R_LOG) + 32 * b, *sj = r + R_STEP + 32 * b;
+        const uint32_t *lo_pairs = reinterpret_cast<const uint32_t *>(r + R_LO) + 16 * b;
+        const u64 mine2 = pack2(mine, mine), lo2 = pack2(mine_lo, mine_lo);
         float x[2][8], y[2][8];
         tc::tmem_ld8(tl + T_A + 32 * b, x[0]);
         tc::tmem_ld8(tl + T_B + 32 * b, y[0]);
@@ -286,8 +288,8 @@ __global__ void __launch_bounds__(576, 1)
                 e = mul2(fac2, e);
               } else {  // the diagonal block: e = 0 where a column does not count
                 float l0, l1;
-                unpack2(e, l0, l1);
-                e = pack2(on >> (8 * cc + j) & 1 ? rule::ex2(mine - l0) : 0.0f, on >> (8 * cc + j + 1) & 1 ? rule::ex2(mine - l1) : 0.0f);
+                unpack2(add2(sub2(mine2, e), sub2(lo2, of_bf2(lo_pairs[4 * cc + 2 * q + i]))), l0, l1);
+                e = pack2(on >> (8 * cc + j) & 1 ? rule::ex2(l0) : 0.0f, on >> (8 * cc + j + 1) & 1 ? rule::ex2(l1) : 0.0f);
               }
               const u64 m2 = mul2(x2, e);
               u64 z2 = mul2(m2, y2);

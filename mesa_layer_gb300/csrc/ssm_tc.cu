@@ -71,11 +71,12 @@ __global__ void __launch_bounds__(L) mesa_ssm_gates_kernel(SsmArgs a, float *rec
     const int send = __shfl_sync(0xffffffffu, s[k], 31);
     r[R_OUT + t] = t >= send ? rule::ex2(two_sub(end, l[k])) : 0.0f;
     r[R_IN + t] = s[k] < 0 ? rule::ex2(l[k].hi + l[k].lo) : 0.0f;
-    r[R_LOG + t] = l[k].hi + l[k].lo;
+    r[R_LOG + t] = l[k].hi;
+    reinterpret_cast<__nv_bfloat16 *>(r + R_LO)[t] = __float2bfloat16_rn(l[k].lo);
     r[R_STEP + t] = step[k];
     int before = -1;
     for (int i = 0; i < w; i++) before = max(before, ts[k][i]);
-    r[R_START + t] = __int_as_float(max(s[k], before));
+    reinterpret_cast<int8_t *>(r + R_START)[t] = (int8_t)max(s[k], before);
     if (w == k) {  // decays over whole warps' tokens, from..to
       const int from = lane < 16 ? lane % 4 + 1 : lane < 20 ? 0 : lane < 24 ? lane - 20 + 1 : 0,
                 to = lane < 16 ? lane / 4 : lane < 20 ? lane - 16 : 4;
@@ -98,7 +99,7 @@ struct Fwd {
   static constexpr uint32_t K = 2 * QK_TILE, V = 4 * QK_TILE, S = V + 2 * V_TILE<P>, MISC = S + QK_TILE;
 };
 struct FwdMisc {
-  float cw[2][L], log[L], step[L];  // step and decay from a token to its warp's end; for the diagonal blocks
+  float cw[2][L], log[L], lo[L], step[L];  // step and decay from a token to its warp's end; for the diagonal blocks
   uint8_t marks[2][L];  // (a walk done over) by channel, the first row of the chunk's values that is not finite, kNoRow: none
   int again;            // an output was not finite: another walk
   uint64_t full[2], y_staged[2], st_done[2], g_full, m_full, y_full, y_free, s_full, w_full, cs_done, drain;
@@ -165,19 +166,21 @@ __global__ void __launch_bounds__(576, 1)
     if (warp < 4) {
       // ---- M ----
       const float *r = record(records, u, NCT, c0);
-      float out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
+      float out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], lo = lo_of(r, t), step = r[R_STEP + t];
+      int start = start_of(r, t);
       for (int c = 0; c < NC; c++) {
         const int n = n0 + c;
         const uint32_t ph = n & 1;
-        const int s = __float_as_int(start);
-        const float mine = log, from = in;
+        const int s = start;
+        const float mine = log, mine_lo = lo, from = in;
         const float *between = r + R_BETWEEN + 4 * w;
         m->cw[ph][t] = out * step;
         m->log[t] = log;
+        m->lo[t] = lo;
         m->step[t] = step;
         if (c + 1 < NC) {
           r += REC;
-          out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], step = r[R_STEP + t], start = r[R_START + t];
+          out = r[R_OUT + t], in = r[R_IN + t], log = r[R_LOG + t], lo = lo_of(r, t), step = r[R_STEP + t], start = start_of(r, t);
         }
         if (group_or(1, 128, !ok)) {  // (also: the others' columns)
           ok = false;
@@ -216,14 +219,21 @@ __global__ void __launch_bounds__(576, 1)
           tc::tmem_ld32(tl + T_G + 32 * w, x);
           const int first = max(s - 32 * w, 0);
           const uint32_t on = (0xffffffffu >> (31 - lane)) & (0xffffffffu << first);  // the columns that count
+          const u64 mine2 = pack2(mine, mine), lo2 = pack2(mine_lo, mine_lo);
           tc::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            const float4 l = *reinterpret_cast<const float4 *>(&m->log[32 * w + 4 * i]);
-            const float4 y = *reinterpret_cast<const float4 *>(&m->step[32 * w + 4 * i]);
-            auto one = [&](int j, float lj, float sj) { return on >> j & 1 ? x[j] * (rule::ex2(mine - lj) * sj) : 0.0f; };
-            o[2 * i] = __uint_as_float(bf2(one(4 * i, l.x, y.x), one(4 * i + 1, l.y, y.y)));
-            o[2 * i + 1] = __uint_as_float(bf2(one(4 * i + 2, l.z, y.z), one(4 * i + 3, l.w, y.w)));
+            const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&m->log[32 * w + 4 * i]);
+            const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(&m->lo[32 * w + 4 * i]);
+            const ulonglong2 y = *reinterpret_cast<const ulonglong2 *>(&m->step[32 * w + 4 * i]);
+            auto two = [&](int j, u64 lj, u64 kj, u64 sj) {  // columns j and j + 1
+              float d0, d1;
+              unpack2(add2(sub2(mine2, lj), sub2(lo2, kj)), d0, d1);
+              unpack2(mul2(pack2(rule::ex2(d0), rule::ex2(d1)), sj), d0, d1);
+              return __uint_as_float(bf2(on >> j & 1 ? x[j] * d0 : 0.0f, on >> (j + 1) & 1 ? x[j + 1] * d1 : 0.0f));
+            };
+            o[2 * i] = two(4 * i, l.x, k.x, y.x);
+            o[2 * i + 1] = two(4 * i + 2, l.y, k.y, y.y);
           }
           tc::tmem_st16(tl + T_G + 16 * w, o);
 #pragma unroll

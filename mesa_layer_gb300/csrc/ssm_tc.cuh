@@ -50,11 +50,14 @@ __device__ __forceinline__ uint32_t bf2(u64 x) {
 }
 
 // A chunk's gates, one record of floats [U, NC]: for each token the decay from it to the end of its warp's 32 tokens and
-// from before them to it (0 across a start), log2 of the latter, the step's length, the last start up to it inside the
-// chunk (-1: none); then the decays from before warp w to ... [w][b]: from the end of warp b's tokens (b < w), FIRST[w]: from
+// from before them to it (0 across a start), log2 of the latter (R_LO: what its rounding to fp32 left, as bf16: 2^-21 where a
+// warp's tokens forget all that they can), the step's length, the last start up to it inside the chunk (a byte, -1: none); then
+// the decays from before warp w to ... [w][b]: from the end of warp b's tokens (b < w), FIRST[w]: from
 // before the chunk to before warp w, LAST[w]: from the end of warp w to the chunk's end, ALL: across the chunk.
-constexpr int R_OUT = 0, R_IN = L, R_LOG = 2 * L, R_STEP = 3 * L, R_START = 4 * L, R_BETWEEN = 5 * L, R_FIRST = R_BETWEEN + 16,
-              R_LAST = R_FIRST + 4, R_ALL = R_LAST + 4, REC = R_BETWEEN + 32;
+constexpr int R_OUT = 0, R_IN = L, R_LOG = 2 * L, R_STEP = 3 * L, R_START = 4 * L, R_LO = R_START + L / 4, R_BETWEEN = R_LO + L / 2,
+              R_FIRST = R_BETWEEN + 16, R_LAST = R_FIRST + 4, R_ALL = R_LAST + 4, REC = R_BETWEEN + 32;
+__device__ __forceinline__ int start_of(const float *r, int t) { return reinterpret_cast<const int8_t *>(r + R_START)[t]; }
+__device__ __forceinline__ float lo_of(const float *r, int t) { return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(r + R_LO)[t]); }
 __device__ __forceinline__ const float *record(const float *records, int u, int NC, int c) {
   return records + ((size_t)u * NC + c) * REC;
 }
