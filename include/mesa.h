@@ -420,7 +420,9 @@ int mesa_ssm_forward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dt
  * or ddt is not finite).  What is not finite in a token's q, k, v or dout reaches the gradients whose formulas hold it, no others
  * (of its own document); a dt_t that is not the unit's, those of dq before t excepted.
  * On the tensor cores states and adjoints are bf16 operands (2^-9) and so are the pairs' weights, dS0 as S_final; the
- * pairs' share of ddt stays fp32, so that ddt is 3e-4 off before its rounding, dA up to 1e-3 of its norm over the heads.
+ * share of ddt, dA and ddt_bias that stays inside a chunk is fp32, what passes between chunks carries the operands' rounding
+ * (2.4e-3 of it): before its own rounding ddt is 3e-4 off for heads that forget within a few hundred tokens, up to 3e-3 for
+ * those that hardly forget, dA and ddt_bias by 1e-3 to 3e-3 of their chunks' shares.
  */
 size_t mesa_ssm_backward_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 int mesa_ssm_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int dtype, const void *q, const void *k,
