@@ -118,7 +118,10 @@ int mesa_ssm_backward_chunked(int B, int H, int Hk, int T, int dk, int dv, int d
   const size_t U = (size_t)B * H, state = U * dv * dk * sizeof(float);
   const size_t param = (size_t)H * (gates_f32 || dtype == MESA_F32 ? 4 : 2);
   if (!all_aligned16(q, k, v, dout, S0, dS_final, dq, dk_out, dv_out, dS0)) return MESA_ERR_INVALID_ARG;
-  if (U == 0 || T == 0) {  // empty sums; the state's gradient passes through
+  if (U == 0 || T == 0) {  // empty sums (of a key head without value heads, too); the state's gradient passes through
+    const size_t qk = H == 0 ? (size_t)B * Hk * T * dk * (dtype == MESA_F32 ? 4 : 2) : 0;
+    if (qk > 0 && (!dq || !dk_out)) return MESA_ERR_INVALID_ARG;
+    if (qk > 0 && (bad_memset(dq, qk, stream) || bad_memset(dk_out, qk, stream))) return MESA_ERR_CUDA;
     for (void *p : {dA, ddt_bias, dskip})
       if (H > 0 && bad_memset(p, param, stream)) return MESA_ERR_CUDA;
     if (U == 0 || !dS0 || dS0 == dS_final) return MESA_OK;
