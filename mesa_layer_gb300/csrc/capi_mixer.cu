@@ -261,7 +261,7 @@ int mesa_qk_norm_rotary(int B, int H, int Hk, int T, int d, int R, int dtype, in
 
 size_t mesa_qk_norm_rotary_backward_workspace_size(int B, int H, int Hk, int T, int d) {
   if (B < 0 || H < 0 || Hk < 0 || T < 0 || !dim_ok(d)) return 0;
-  return align256((size_t)mesa::rotary_bwd_parts(B, H, Hk, T, d) * 2 * d * sizeof(float));
+  return align256((size_t)mesa::rotary_bwd_parts(B, T, d) * 2 * d * sizeof(float));
 }
 
 int mesa_qk_norm_rotary_backward(int B, int H, int Hk, int T, int d, int R, int dtype, int interleaved, int norm,

@@ -40,7 +40,7 @@ struct RotaryArgs {
   float *dwq = nullptr, *dwk = nullptr;
   float *partial = nullptr;     // [parts][2][d]
 };
-int rotary_bwd_parts(int B, int H, int Hk, int T, int d);
+int rotary_bwd_parts(int B, int T, int d);  // CTAs of the backward at most
 int launch_qk_norm_rotary(const RotaryArgs &a, cudaStream_t st);
 int launch_qk_norm_rotary_backward(const RotaryArgs &a, cudaStream_t st);
 

@@ -340,9 +340,14 @@ int forward(const RotaryArgs &a, cudaStream_t st) {
     return done();
   });
 }
+// Two CTAs for each of a GB300's 152 SMs, no more than there are tokens for (d = 128: a CTA takes 16 of bf16, 8 of fp32).
+int bwd_parts(int B, int T, int d, int vec) {
+  const size_t n = ((size_t)B * T * (d / vec) + kBlock - 1) / kBlock;
+  return n < 1 ? 1 : n < 152 * 2 ? (int)n : 152 * 2;
+}
 template <typename TIO>
 int backward(const RotaryArgs &a, cudaStream_t st) {
-  const int parts = rotary_bwd_parts(a.B, a.H, a.Hk, a.T, a.d);
+  const int parts = bwd_parts(a.B, a.T, a.d, Row<TIO>::VEC);
   return by_pairs(a, [&](auto d, auto p) {
     timing_mark_begin(K_ROTARY_BWD, st);
     mesa_qk_norm_rotary_bwd_kernel<TIO, decltype(d)::value, decltype(p)::value><<<parts, kBlock, 0, st>>>(a);
@@ -359,11 +364,8 @@ int backward(const RotaryArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Two CTAs for each of a GB300's 152 SMs, no more than there are tokens for (16 a CTA at d = 128).
-int rotary_bwd_parts(int B, int, int, int T, int d) {
-  const size_t n = ((size_t)B * T * (d / 4) + kBlock - 1) / kBlock;
-  return n < 1 ? 1 : n < 152 * 2 ? (int)n : 152 * 2;
-}
+// (For the workspace, whose size goes by either type: fp32 has more.)
+int rotary_bwd_parts(int B, int T, int d) { return bwd_parts(B, T, d, Row<float>::VEC); }
 
 int launch_qk_norm_rotary(const RotaryArgs &a, cudaStream_t st) {
   return a.dtype == 1 ? forward<__nv_bfloat16>(a, st) : forward<float>(a, st);
