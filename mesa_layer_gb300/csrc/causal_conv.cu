@@ -102,7 +102,8 @@ __device__ __forceinline__ int load_window(const ConvArgs &a, int u, int t0, int
 
 // Thread (unit, run, channel group) over runs of `run` tokens; the next AHEAD tokens' inputs are on their way while the
 // present ones are worked on.
-// (Seven CTAs per SM where that fits: 60 -> 58 us at 8 x 16 x 4096 x 128.)
+// (Seven CTAs per SM for bf16 and up to four taps without documents, though four taps then leave 36 bytes a thread in local
+// memory: 60 -> 58 us at 8 x 16 x 4096 x 128.)
 template <typename TIO, int VEC, int W, bool PACKED>
 __global__ void __launch_bounds__(kFwdBlock, sizeof(TIO) == 2 && W <= 4 && !PACKED ? 7 : 1) mesa_causal_conv_kernel(ConvArgs a, int run, int runs) {
   using V = Vec<TIO, VEC>;
@@ -217,8 +218,8 @@ constexpr int kBwdBlock = 128;
 constexpr int kBwdVec = 4;  // channels a thread (two: half the registers, but 153 us)
 __host__ __device__ inline int bwd_gx(int d) { return d / kBwdVec < 32 ? d / kBwdVec : 32; }
 
-// As many CTAs as a GB300's 152 SMs hold at once (bwd_ctas: what keeps taps, windows and sums in registers; four tokens'
-// chains interleave, and more warps with values in local memory lose: W = 4 with three, four, five, six CTAs an SM 95, 93,
+// As many CTAs as a GB300's 152 SMs hold at once (bwd_ctas: what keeps taps, windows and sums in registers, but for 4 to 44 bytes a
+// thread with W = 5 and 7 and documents; four tokens' chains interleave, and more warps with values in local memory lose: W = 4 with three, four, five, six CTAs an SM 95, 93,
 // 116, 136 us at 8 x 16 x 4096 x 128; W = 8 with two, three 172, 212), shared by all heads and channels; and runs of which
 // every row takes as many as the others, as nearly as that goes (in parts of a sequence of 16 tokens at least; a run costs
 // about four tokens more than it has).  us of 8 x 16 x 4001 x 128: runs of 64 tokens, three or four a row, 137; this, the
