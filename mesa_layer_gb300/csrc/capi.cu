@@ -226,7 +226,7 @@ const char *mesa_kernel_name(int kind) {
     case mesa::K_SSM_CHAIN: return "mesa_ssm_chain_tc_kernel";
     case mesa::K_SSM_OUT: return "mesa_ssm_out_kernel";
     case mesa::K_SSM_STEP: return "mesa_ssm_step_kernel";
-    case mesa::K_SSM_GRADS: return "mesa_ssm_grads_kernel";
+    case mesa::K_SSM_GRADS: return "mesa_ssm_grads_kernel|mesa_ssm_grads_tc_kernel";
     case mesa::K_SSM_PARAMS: return "mesa_ssm_params_kernel";
     case mesa::K_CONV: return "mesa_causal_conv_kernel";
     case mesa::K_CONV_STEP: return "mesa_causal_conv_step_kernel";
