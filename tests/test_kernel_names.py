@@ -34,4 +34,4 @@ def test_kernels_of_the_scan_the_convolution_and_the_rotation(names):
 def test_no_kernel_is_named_that_is_not_there(names):
     text = "".join(open(p).read() for p in glob.glob(os.path.join(build.CSRC, "*.cu*")))
     there = set(re.findall(r"__global__[^;{]*?\b(\w+)\s*\(", text)) | set(re.findall(r"\b(mesa_\w+_kernel)\s*\(", text))
-    assert {n.split("<")[0] for kind in names for n in kind.split("|")} <= there
+    assert {n.split("<")[0] for kind in names for n in re.split(r"[|+]", kind)} <= there
