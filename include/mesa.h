@@ -450,7 +450,8 @@ int mesa_ssm_step(int N, int H, int Hk, int dk, int dv, int dtype, float *S_stat
  *   state0: NULL (zeros) or [B, H, W-1, d] fp32, the inputs before token 0, [.., s, :] the one s + 1 tokens back;
  *   state_final: NULL or the same of the last token (what a document's start cuts off as zeros), not state0's memory.
  *   d a multiple of 8, at most 65536; 1 <= W <= 8; B * H <= 65535; activations and states 16-byte aligned.
- * Arithmetic is fp32; SiLU from the hardware's exponential and division (2^-21).
+ * Arithmetic is fp32; SiLU from the hardware's exponential and division: 2^-21 in fp32 calls (down to 2^-120, below 0); in bf16
+ * ones, beside the output's 2^-9, 2^-21 and |y| 2^-24.
  */
 int mesa_causal_conv(int B, int H, int T, int d, int W, int dtype, int silu, const void *x, const float *w,
                      const float *bias, const uint8_t *starts, const float *state0, float *state_final, void *out,
