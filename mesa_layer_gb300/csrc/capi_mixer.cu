@@ -31,7 +31,7 @@ int check_scan(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
 }
 
 // The tensor-core path: bf16, dk = 128 and dv 64 or 128, or both 64.  (us on it, on the CUDA cores, forward / backward:
-// 8 x 16 x 4096, both 64: 92, 700 / 287, 1610.)
+// 8 x 16 x 4096, both 64: 87, 700 / 300, 1610.)
 bool scan_tc(int dtype, int dk, int dv) {
   return dtype == MESA_BF16 && ((dk == 128 && (dv == 64 || dv == 128)) || (dk == 64 && dv == 64));
 }
