@@ -67,6 +67,38 @@ def test_forward_with_several_of_them(lib, dtype, dk, dv):  # noqa: F811
     assert torch.equal(E.isnan().all(-1), gone[:, :, -1]) and same(E[~gone[:, :, -1]], S[~gone[:, :, -1]])
 
 
+@pytest.mark.parametrize("dtype,dk,dv", SIZES)
+def test_forward_with_states_in_place(lib, dtype, dk, dv):  # noqa: F811
+    """S_final over S0's memory, captured and replayed: a walk done over begins from the same state."""
+    clean = case(dtype, dk, dv)
+    out, S = forward(lib, clean)
+    v, state, o = clean["v"].clone(), clean["S0"].clone(), torch.empty_like(out)
+    scan = (clean["q"], clean["k"], v, clean["dt"], clean["A"])
+
+    def call():
+        lib.mesa_ssm_forward_chunked(*scan, dt_bias=clean["dt_bias"], skip=clean["skip"], out=o, S0=state, S_final=state)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    others = torch.arange(dv, device="cuda") != 3
+    for bad in (torch.nan, 1.0, -torch.inf):
+        v.copy_(clean["v"])
+        v[0, 1, 140, 3] = bad
+        state.copy_(clean["S0"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(o[:, 1, :, others], out[:, 1, :, others]) and same(o[:, 1, :140], out[:, 1, :140]) and same(state[:, 1, others], S[:, 1, others])
+        assert same(o[:, [0, 2, 3]], out[:, [0, 2, 3]]) and same(state[:, [0, 2, 3]], S[:, [0, 2, 3]])
+        assert bool(o[0, 1, 140:, 3].isfinite().all() if bad == 1.0 else not o[0, 1, 140:, 3].isfinite().any())
+        assert bool(state[0, 1, 3].isfinite().all() if bad == 1.0 else not state[0, 1, 3].isfinite().any())
+
+
 def test_forward_in_segments(lib):  # noqa: F811
     """Few long units: a segment's first walk carries it, the second keeps what came before."""
     for dk, dv in ((128, 128), (128, 64), (64, 64)):
