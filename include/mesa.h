@@ -396,7 +396,8 @@ int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void 
  * Arithmetic: sums, states and gates in fp32, log-decays as sums of two fp32 values.  Decays below 2^-150 count as that.
  * bf16 with dk = 128 and dv in {64, 128}, or both 64, runs on the tensor cores in chunks of 128 tokens: the pairs' weights
  * and the state as an operand are rounded to bf16 (2^-9 of a term each, as much as out's own rounding), what enters the
- * state to two bf16 values (S_final carries 2^-17 of a term).  Everything else runs in fp32 on the CUDA cores in chunks
+ * state to two bf16 values (S_final carries 2^-17 of a term: 2.5e-6 in all; sums on the tensor cores are cut to fp32 rather than
+ * rounded, which adds up where heads hardly forget: 6e-6 after 8192 tokens, 2e-5 after 32768).  Everything else runs in fp32 on the CUDA cores in chunks
  * of 32.  Long sequences of few (batch, head) units are cut into segments that run side by side on the tensor cores.
  * The kernels of a call overlap (programmatic dependent launch); towards everything else in the stream it is one piece.
  */

@@ -6,7 +6,9 @@
 // term each, as much as the output's own rounding), and to two bf16 values (2^-17) where it enters a state, which is
 // fp32 in tensor memory from chunk to chunk.  bf16 has fp32's range, so no scales are needed.  (A third value would take the
 // final state's error from 2.3e-6 to 3e-7, near fp32's own 1.2e-7, but eight more products stand in every chunk's chain: us of
-// 8 x 16 x 4096 forward 113 to 131, 128 x 64 98 to 111, 64 x 64 89 to 105, 1 x 16 x 65536 293 to 325.  The outputs do not change.)
+// 8 x 16 x 4096 forward 113 to 131, 128 x 64 98 to 111, 64 x 64 89 to 105, 1 x 16 x 65536 293 to 325.  The outputs do not change.
+// As a walk of its own over the tokens that a final state still holds: 111 to 127, 175 with heads that hardly forget, 16 x 512
+// 20 to 30.  And where heads hardly forget, it is the tensor cores' sums that count, which cut what does not fit.)
 // States lie transposed, S^T [dk lanes][dv columns]: the same 128 lanes for every size.  N = 64 uses tiles of 128 columns
 // whose second half is zero from the start and stays so (a gradient put there is zero, too): half of the products is
 // idle.  64 x 64 states take 80 % of the time of 128 x 128 for half of the bytes: a chunk's chain has the same steps.
