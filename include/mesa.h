@@ -391,14 +391,15 @@ int mesa_block_norm_backward(int N, int D, int dtype, const void *x, const void 
  * workspace: at least mesa_ssm_workspace_size() bytes, 256-byte aligned; its first word is the status word read by
  * mesa_forward_status (MESA_ERR_NONFINITE: a non-finite out).
  * The outputs' memory is none of the inputs'.
- * A NaN or infinity in q_t reaches out_t alone, one in k_t, v_t (its channel) or dt_t the unit's outputs from t on and S_final;
- * what it reaches is not finite, NaN for most.  (On the tensor cores its unit is walked twice.)
+ * A NaN or infinity in q_t reaches out_t alone, one in k_t, v_t (its channel) or dt_t the unit's outputs from t on and
+ * S_final; what it reaches is not finite, NaN for most.  (On the tensor cores its unit is walked twice.)
  * Arithmetic: sums, states and gates in fp32, log-decays as sums of two fp32 values.  Decays below 2^-150 count as that.
  * bf16 with dk = 128 and dv in {64, 128}, or both 64, runs on the tensor cores in chunks of 128 tokens: the pairs' weights
  * and the state as an operand are rounded to bf16 (2^-9 of a term each, as much as out's own rounding), what enters the
- * state to two bf16 values (S_final carries 2^-17 of a term: 2.5e-6 in all; sums on the tensor cores are cut to fp32 rather than
- * rounded, which adds up where heads hardly forget: 6e-6 after 8192 tokens, 2e-5 after 32768).  Everything else runs in fp32 on the CUDA cores in chunks
- * of 32.  Long sequences of few (batch, head) units are cut into segments that run side by side on the tensor cores.
+ * state to two bf16 values (S_final carries 2^-17 of a term: 2.5e-6 in all; sums on the tensor cores are cut to fp32 rather
+ * than rounded, which adds up where heads hardly forget: 6e-6 after 8192 tokens, 2e-5 after 32768).  Everything else runs in
+ * fp32 on the CUDA cores in chunks of 32.  Long sequences of few (batch, head) units are cut into segments that run side by
+ * side on the tensor cores.
  * The kernels of a call overlap (programmatic dependent launch); towards everything else in the stream it is one piece.
  */
 size_t mesa_ssm_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);

@@ -236,9 +236,9 @@ constexpr int kBwdBlock = 128;
 constexpr int kBwdVec = 4;  // channels a thread (two: half the registers, but 153 us)
 __host__ __device__ inline int bwd_gx(int d) { return d / kBwdVec < 32 ? d / kBwdVec : 32; }
 
-// As many CTAs as a GB300's 152 SMs hold at once (bwd_ctas: what keeps taps, windows and sums in registers, but for 4 to 44 bytes a
-// thread with W = 5 and 7 and documents; four tokens' chains interleave, and more warps with values in local memory lose: W = 4 with three, four, five, six CTAs an SM 95, 93,
-// 116, 136 us at 8 x 16 x 4096 x 128; W = 8 with two, three 172, 212), shared by all heads and channels; and runs of which
+// As many CTAs as a GB300's 152 SMs hold at once (bwd_ctas: what keeps taps, windows and sums in registers, but for 4 to 20
+// bytes a thread with documents and W = 5, 7, or 2 in fp32; four tokens' chains interleave, and more warps with values in local memory lose: W = 4 with
+// three, four, five, six CTAs an SM 95, 93, 116, 136 us at 8 x 16 x 4096 x 128; W = 8 with two, three 172, 212), shared by all heads and channels; and runs of which
 // every row takes as many as the others, as nearly as that goes (in parts of a sequence of 16 tokens at least; a run costs
 // about four tokens more than it has).  us of 8 x 16 x 4001 x 128: runs of 64 tokens, three or four a row, 137; this, the
 // inputs on their way in shared memory instead of registers, and no case distinction while no document starts, 98 (75 % of a copy's rate at W = 2 and in fp32; at W = 4 the packed products' pipe
